@@ -46,6 +46,8 @@ ENTRY_POINTS = (
     "moe_ffn_fp8_workspace_size", "moe_grouped_ffn_fp8", "moe_grouped_ffn_bwd_fp8",
     "moe_decode_fused_workspace_size", "moe_decode_fused",
     "moe_combine_bwd_weights", "moe_ffn_down_bwd_data_gather", "moe_ffn_down_bwd_weight_gather",
+    "moe_few_tokens_workspace_size", "moe_few_tokens", "moe_few_tokens_int8",
+    "moe_linear_int8", "moe_linear_int8_workspace_size", "moe_linear_int8_dynamic",
 )
 
 
@@ -70,6 +72,11 @@ def make_shape(T, H, K, num_experts, F=0, capacity=None, zero_expert_num=0, copy
 class MoeFp8Weight(ctypes.Structure):
     """Mirror of struct moe_fp8_weight (device pointers)."""
     _fields_ = [("codes", ctypes.c_void_p), ("codes_t", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class MoeInt8Weight(ctypes.Structure):
+    """Mirror of struct moe_int8_weight (device pointers)."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -144,6 +151,13 @@ def lib() -> ctypes.CDLL:
         L.moe_ffn_down_fwd_mx.argtypes = [S] + [P] * 7
         L.moe_ffn_down_bwd_data_mx.argtypes = [S] + [P] * 10
         L.moe_ffn_gate_up_bwd_data_mx.argtypes = [S] + [P] * 9
+        Z = ctypes.c_size_t
+        L.moe_few_tokens_workspace_size.argtypes = [S, I64, I32C, ctypes.POINTER(Z)]
+        L.moe_few_tokens.argtypes = [S] + [P] * 7 + [I64] + [P] * 10 + [Z, P]
+        L.moe_few_tokens_int8.argtypes = [S] + [P] * 6 + [I64] + [P] * 8 + [Z, P]
+        L.moe_linear_int8.argtypes = [I64, I64, I64] + [P] * 7
+        L.moe_linear_int8_workspace_size.argtypes = [I64, I64, I64, ctypes.POINTER(Z)]
+        L.moe_linear_int8_dynamic.argtypes = [I64, I64, I64] + [P] * 6 + [Z, P]
         for name in ENTRY_POINTS:
             if name != "moe_status_str":
                 getattr(L, name).restype = ctypes.c_int32
@@ -1279,6 +1293,215 @@ def moe_layer_int8(x, topk_idx, topk_weights, wq_gate, wq_up, wq_down, *, smooth
     out = torch.empty((T, H), dtype=BF16, device=dev)
     moe_combine(shape, y, topk_idx, topk_weights, d.assist_info_for_combine, recv, mask, shared_expert_x, x,
                 const_alpha_1, const_alpha_2, const_v, out, stream)
+    return out
+
+
+# ----------------------------------------------------------------------------- few tokens, int8 product
+
+FEW_TOKENS_MAX = 64
+
+
+def _at(t, dtype, n, name, dev):
+    """The address of a tensor argument (None: a NULL pointer): a contiguous tensor of
+    this dtype on device dev with at least n elements, else MoeError."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise MoeError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype and not (dtype is U8 and t.dtype in U8):
+        raise MoeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise MoeError(f"{name} is on {t.device}, expected {dev}")
+    if not t.is_contiguous():
+        raise MoeError(f"{name} must be contiguous")
+    if t.numel() < n:
+        raise MoeError(f"{name} holds {t.numel()} elements, needs at least {n}")
+    return t.data_ptr()
+
+
+def _device_of(x, name):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise MoeError(f"{name} must be a GPU tensor")
+    return x.device
+
+
+def _launch(entry, dev, stream, *args):
+    """Call a C entry with its stream argument last, on the device its tensors are on."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise MoeError(f"the stream is on {stream.device}, the tensors on {dev}")
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            _check(entry(*args, stream.cuda_stream))
+    else:
+        _check(entry(*args, stream.cuda_stream))
+
+
+def _int8_pair(w):
+    """(codes, scales) of an Int8Weights or of a (codes, scales) pair."""
+    return (w.codes, w.scales) if isinstance(w, Int8Weights) else tuple(w)
+
+
+def moe_few_tokens_workspace_size(shape: MoeShape, shared_F: int = 0, int8: bool = False) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_few_tokens_workspace_size(ctypes.byref(shape), shared_F, int(int8), ctypes.byref(n)))
+    return n.value
+
+
+def _few_common(shape, dev, x, topk_idx, topk_weights, x_active_mask, shared_expert_x, const_alpha_1, const_alpha_2,
+                const_v, out, err_flag):
+    T, H, K = shape.T, shape.H, shape.K
+    QH = shape.const_expert_num * H
+    return ((_at(x, BF16, T * H, "x", dev), _at(topk_idx, I32, T * K, "topk_idx", dev),
+             _at(topk_weights, F32, T * K, "topk_weights", dev),
+             _at(x_active_mask, U8, (0, T, T * K)[shape.mask_ndim], "x_active_mask", dev)),
+            (_at(shared_expert_x, BF16, T * H, "shared_expert_x", dev),
+             _at(const_alpha_1, BF16, QH, "const_alpha_1", dev), _at(const_alpha_2, BF16, QH, "const_alpha_2", dev),
+             _at(const_v, BF16, QH, "const_v", dev), _at(out, BF16, T * H, "out", dev),
+             _at(err_flag, I32, 1, "err_flag", dev)))
+
+
+def _bytes_of(workspace, dev):
+    if workspace is not None and workspace.device != dev:
+        raise MoeError(f"workspace is on {workspace.device}, expected {dev}")
+    return _ptr(workspace, None, "workspace"), 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def moe_few_tokens(shape, x, topk_idx, topk_weights, x_active_mask, w_gate, w_up, w_down, shared_w, shared_expert_x,
+                   const_alpha_1, const_alpha_2, const_v, out, err_flag, workspace, stream=None):
+    """shared_w: None or the shared expert's (gate, up, down) weights."""
+    dev = _device_of(x, "x")
+    n = shape.num_experts * shape.F * shape.H
+    a, b = _few_common(shape, dev, x, topk_idx, topk_weights, x_active_mask, shared_expert_x, const_alpha_1,
+                       const_alpha_2, const_v, out, err_flag)
+    Fs = 0 if shared_w is None else shared_w[0].shape[-2]
+    s = (None, None, None) if shared_w is None else [
+        _at(t, BF16, Fs * shape.H, "shared expert weights", dev) for t in shared_w]
+    _launch(lib().moe_few_tokens, dev, stream, ctypes.byref(shape), *a, _at(w_gate, BF16, n, "w_gate", dev),
+            _at(w_up, BF16, n, "w_up", dev), _at(w_down, BF16, n, "w_down", dev), Fs, *s, *b,
+            *_bytes_of(workspace, dev))
+
+
+def moe_few_tokens_int8(shape, x, topk_idx, topk_weights, x_active_mask, smooth_scales, w, shared_w, shared_expert_x,
+                        const_alpha_1, const_alpha_2, const_v, out, err_flag, workspace, stream=None):
+    """w, shared_w: (gate, up, down), each an Int8Weights or a (codes, scales) pair."""
+    dev = _device_of(x, "x")
+    H = shape.H
+
+    def three(ws, E, F):
+        c = [_int8_pair(v) for v in ws]
+        return (MoeInt8Weight * 3)(*[
+            MoeInt8Weight(_at(q, I8T, E * F * H, "int8 weight codes", dev), _at(s, F32, E * n, "int8 weight scales", dev))
+            for (q, s), n in zip(c, (F, F, H))])
+
+    a, b = _few_common(shape, dev, x, topk_idx, topk_weights, x_active_mask, shared_expert_x, const_alpha_1,
+                       const_alpha_2, const_v, out, err_flag)
+    Fs = 0 if shared_w is None else _int8_pair(shared_w[0])[0].shape[-2]
+    _launch(lib().moe_few_tokens_int8, dev, stream, ctypes.byref(shape), *a,
+            _at(smooth_scales, F32, shape.num_experts * H, "smooth_scales", dev),
+            three(w, shape.num_experts, shape.F), Fs, None if shared_w is None else three(shared_w, 1, Fs), *b,
+            *_bytes_of(workspace, dev))
+
+
+@torch.no_grad()
+def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smooth_scales=None, x_active_mask=None,
+                         shared_expert_x=None, shared_w_gate=None, shared_w_up=None, shared_w_down=None,
+                         const_alpha_1=None, const_alpha_2=None, const_v=None, zero_expert_num=0, copy_expert_num=0,
+                         const_expert_num=0, err_flag=None, stream=None):
+    """Forward of one MoE layer for a decode step of at most FEW_TOKENS_MAX tokens (inference,
+    no autograd), every active expert's weights read once; moe_layer's arguments and meaning.
+
+    Weights (the shared expert's too): bf16 tensors w_gate, w_up (E, F, H) and w_down (E, H, F),
+    or for all of them Int8Weights or (codes, scales) pairs, then optionally with
+    smooth_scales (E, H).  err_flag: an int32 tensor for the routing's MOE_FLAG_* bits."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # its output and workspace then belong to that stream
+            return moe_layer_few_tokens(
+                x, topk_idx, topk_weights, w_gate, w_up, w_down, smooth_scales=smooth_scales,
+                x_active_mask=x_active_mask, shared_expert_x=shared_expert_x, shared_w_gate=shared_w_gate,
+                shared_w_up=shared_w_up, shared_w_down=shared_w_down, const_alpha_1=const_alpha_1,
+                const_alpha_2=const_alpha_2, const_v=const_v, zero_expert_num=zero_expert_num,
+                copy_expert_num=copy_expert_num, const_expert_num=const_expert_num, err_flag=err_flag)
+    T, H = x.shape
+    K = topk_idx.shape[1]
+    int8 = not isinstance(w_gate, torch.Tensor)
+    E, F, _ = (_int8_pair(w_gate)[0] if int8 else w_gate).shape
+    dev = _device_of(x, "x")
+    mask_ndim = 0 if x_active_mask is None else x_active_mask.dim()
+    shape = make_shape(T, H, K, E, F=F, zero_expert_num=zero_expert_num, copy_expert_num=copy_expert_num,
+                       const_expert_num=const_expert_num, mask_ndim=mask_ndim)
+    shared_w = None if shared_w_gate is None else (shared_w_gate, shared_w_up, shared_w_down)
+    for ws, n in ((((w_gate, w_up, w_down), E), (shared_w, 1)) if shared_w else (((w_gate, w_up, w_down), E),)):
+        if int8:
+            ws = [_int8_pair(w)[0] for w in ws]
+        f = ws[0].shape[1]
+        if ws[0].shape != (n, f, H) or ws[1].shape != (n, f, H) or ws[2].shape != (n, H, f):
+            raise MoeError(f"weights {[tuple(w.shape) for w in ws]} do not fit {n} experts of {H} columns")
+    if topk_idx.shape != (T, K) or topk_weights.shape != (T, K):
+        raise MoeError(f"topk_idx {tuple(topk_idx.shape)} and topk_weights {tuple(topk_weights.shape)} for {T} tokens")
+    Fs = 0 if shared_w is None else (_int8_pair(shared_w_gate)[0] if int8 else shared_w_gate).shape[-2]
+    workspace = torch.empty(moe_few_tokens_workspace_size(shape, Fs, int8), dtype=torch.uint8, device=dev)
+    out = torch.empty((T, H), dtype=BF16, device=dev)
+    if err_flag is None:
+        err_flag = torch.empty(1, dtype=I32, device=dev)
+    rest = (shared_w, shared_expert_x, const_alpha_1, const_alpha_2, const_v, out, err_flag, workspace)
+    if int8:
+        moe_few_tokens_int8(shape, x, topk_idx, topk_weights, x_active_mask, smooth_scales, (w_gate, w_up, w_down), *rest)
+    else:
+        if smooth_scales is not None:
+            raise MoeError("smooth_scales go with int8 weights")
+        moe_few_tokens(shape, x, topk_idx, topk_weights, x_active_mask, w_gate, w_up, w_down, *rest)
+    return out
+
+
+def moe_linear_int8(xq, xs, wq, ws, bias, out, stream=None):
+    """xq (M, K), wq (N, K) int8, their scales (M,), (N,) fp32, bias (N,) fp32 or None -> out (M, N) bf16."""
+    dev = _device_of(xq, "xq")
+    (M, K), N = xq.shape, wq.shape[0]
+    _launch(lib().moe_linear_int8, dev, stream, M, N, K, _at(xq, I8T, M * K, "xq", dev), _at(xs, F32, M, "xs", dev),
+            _at(wq, I8T, N * K, "wq", dev), _at(ws, F32, N, "ws", dev), _at(bias, F32, N, "bias", dev),
+            _at(out, BF16, M * N, "out", dev))
+
+
+def moe_linear_int8_workspace_size(M: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_linear_int8_workspace_size(M, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def moe_linear_int8_dynamic(x, wq, ws, bias, out, workspace, stream=None):
+    """moe_linear_int8 of bf16 rows x (M, K), quantised per row in the call."""
+    dev = _device_of(x, "x")
+    (M, K), N = x.shape, wq.shape[0]
+    _launch(lib().moe_linear_int8_dynamic, dev, stream, M, N, K, _at(x, BF16, M * K, "x", dev),
+            _at(wq, I8T, N * K, "wq", dev), _at(ws, F32, N, "ws", dev), _at(bias, F32, N, "bias", dev),
+            _at(out, BF16, M * N, "out", dev), *_bytes_of(workspace, dev))
+
+
+@torch.no_grad()
+def linear_int8(x, w, *, x_scales=None, bias=None, stream=None):
+    """x (..., K) times the transpose of int8 weights (N, K) with one scale per output channel ->
+    (..., N) bf16 (inference, no autograd).  w: an Int8Weights or a (codes, scales) pair.
+    x: bf16 rows, quantised per row in the call, or int8 codes with their x_scales (...);
+    bias: fp32 (N,)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # its output and workspace then belong to that stream
+            return linear_int8(x, w, x_scales=x_scales, bias=bias)
+    wq, ws = _int8_pair(w)
+    if wq.dim() != 2 or x.shape[-1] != wq.shape[1]:
+        raise MoeError(f"x {tuple(x.shape)} and weights {tuple(wq.shape)} do not multiply")
+    dev = _device_of(x, "x")
+    N = wq.shape[0]
+    out = torch.empty((*x.shape[:-1], N), dtype=BF16, device=dev)
+    _at(x, BF16 if x_scales is None else I8T, 0, "x", dev)
+    rows = x.view(-1, x.shape[-1]) if x.dim() != 2 else x
+    if x_scales is not None:
+        moe_linear_int8(rows, x_scales, wq, ws, bias, out)
+    else:
+        workspace = torch.empty(moe_linear_int8_workspace_size(rows.shape[0], N, rows.shape[1]), dtype=torch.uint8,
+                                device=dev)
+        moe_linear_int8_dynamic(rows, wq, ws, bias, out, workspace)
     return out
 
 

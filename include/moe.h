@@ -92,6 +92,13 @@ typedef struct moe_fp8_weight {
   const float* scales;     /* (E, N/128, Kdim/128) */
 } moe_fp8_weight;
 
+/* One weight tensor in int8 with one fp32 scale per output channel, as
+ * moe_quant_rows_int8 writes it over the rows of the (out, in) matrices. */
+typedef struct moe_int8_weight {
+  const int8_t* codes;  /* (E, N, Kdim) */
+  const float* scales;  /* (E, N) */
+} moe_int8_weight;
+
 /* Human-readable name of a status code (static string). */
 const char* moe_status_str(moe_status st);
 
@@ -741,6 +748,90 @@ moe_status moe_decode_fused(const moe_shape* s, const void* x, const int32_t* to
                             const void* w_up, const void* w_down, const void* shared_expert_x, const void* ori_x,
                             const void* const_alpha_1, const void* const_alpha_2, const void* const_v, void* out,
                             int32_t* err_flag, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------- few tokens
+ * A whole MoE layer forward for a decode step of at most 64 tokens.  Each active
+ * expert's weights are read from memory once; there is no routing pass (every
+ * workgroup sorts the T K <= 1024 slots for itself), no expanded rows, and
+ * nothing is rounded between x and out:
+ *   out[t] = bf16(sum over k of topk_weights[t,k] * v(t,k) + shared[t])
+ * with v = Wd_e (silu(Wg_e x_t) * (Wu_e x_t)) for a routed slot, 0 for a zero
+ * expert and for a masked, out-of-range or repeated slot, x_t for a copy expert,
+ * alpha_1[j] * x_t + alpha_2[j] * v[j] for constant expert j (low_latency_combine
+ * page, Function and Parameters; ori_x is x).  h keeps 16 significant bits (two
+ * bf16 parts), every sum is fp32, so out is closer to the exact value than the
+ * chain moe_route .. moe_combine, which rounds G, U, h and y to bf16.
+ * shared[t] is shared_expert_x[t], or the shared expert's FFN of x_t when its
+ * weights are given (shared_F > 0: (1, shared_F, H), (1, shared_F, H),
+ * (1, H, shared_F)), or nothing; giving both is MOE_ERR_BAD_RANGE.
+ * The weights and values of inactive slots are not used, whatever they hold.
+ * Results do not depend on the other tokens' rows or on atomics: the same call
+ * gives the same bits.
+ */
+
+/* Bytes of device workspace of moe_few_tokens (int8 = 0) or moe_few_tokens_int8
+ * (int8 = 1) for this shape; shared_F = 0 without shared expert weights.  Nothing
+ * in it needs clearing.  Calls that share one must not overlap in time. */
+moe_status moe_few_tokens_workspace_size(const moe_shape* s, int64_t shared_F, int32_t int8, size_t* bytes);
+
+/* moe_few_tokens - bf16 weights.  Two kernel launches.
+ *  in   x (T, H) bf16, topk_idx (T, K) int32, topk_weights (T, K) fp32,
+ *       x_active_mask as for moe_dispatch
+ *  in   w_gate, w_up (E, F, H), w_down (E, H, F) bf16; shared_w_* likewise or NULL
+ *  in   shared_expert_x (T, H) bf16 or NULL; const_alpha_1/_2, const_v (Q, H) bf16
+ *  out  out (T, H) bf16; err_flag (1,) int32: moe_dispatch's MOE_FLAG_* bits (with
+ *       T = 0 it is written 0 and nothing else)
+ *  ws   workspace >= moe_few_tokens_workspace_size bytes
+ * s->capacity is checked as everywhere and not used otherwise.
+ * MOE_ERR_UNSUPPORTED: T > 64, comm_quant_mode != 0.  MOE_ERR_BAD_SHAPE: F or
+ * shared_F not a multiple of 32; x, a weight or the workspace not on a 16-byte
+ * boundary. */
+moe_status moe_few_tokens(const moe_shape* s, const void* x, const int32_t* topk_idx, const float* topk_weights,
+                          const uint8_t* x_active_mask, const void* w_gate, const void* w_up, const void* w_down,
+                          int64_t shared_F, const void* shared_w_gate, const void* shared_w_up,
+                          const void* shared_w_down, const void* shared_expert_x, const void* const_alpha_1,
+                          const void* const_alpha_2, const void* const_v, void* out, int32_t* err_flag,
+                          void* workspace, size_t ws_bytes, void* stream);
+
+/* moe_few_tokens_int8 - int8 weights (w8a8, the int8 path's arithmetic without its
+ * bf16 roundings): x_t times smooth_scales[e] (NULL: 1) is quantised per row by
+ * the rule of moe_quant_rows_int8, G and U are exact integer sums times
+ * (row scale x channel scale), h in fp32 is quantised per row by the same rule,
+ * y likewise.  The shared expert takes x_t without smooth scales.
+ *  in   smooth_scales NULL or (E, H) fp32
+ *  in   w[3] gate, up, down; shared_w NULL or three weights
+ *  other arguments as moe_few_tokens.  H a multiple of 16 (MOE_ERR_BAD_SHAPE); H, F
+ *  and shared_F at most 131072 (MOE_ERR_UNSUPPORTED). */
+moe_status moe_few_tokens_int8(const moe_shape* s, const void* x, const int32_t* topk_idx,
+                               const float* topk_weights, const uint8_t* x_active_mask, const float* smooth_scales,
+                               const moe_int8_weight* w, int64_t shared_F, const moe_int8_weight* shared_w,
+                               const void* shared_expert_x, const void* const_alpha_1, const void* const_alpha_2,
+                               const void* const_v, void* out, int32_t* err_flag, void* workspace, size_t ws_bytes,
+                               void* stream);
+
+/* ------------------------------------------------------- int8 matrix product
+ * The dense product of the int8 path (the projections around the layer):
+ *   out[m, n] = bf16((sum over k of xq[m, k] * wq[n, k]) * (xs[m] * ws[n]) + bias[n])
+ * with an exact integer sum, for any M >= 0 and N >= 1 and K a positive multiple
+ * of 16 (MOE_ERR_BAD_SHAPE) up to 131072; M and N at most 2^24 (MOE_ERR_UNSUPPORTED).
+ */
+
+/* moe_linear_int8 - one launch.
+ *  in   xq (M, K) int8, xs (M) fp32; wq (N, K) int8, ws (N) fp32 (moe_quant_rows_int8
+ *       of the bf16 matrices); bias (N) fp32 or NULL
+ *  out  out (M, N) bf16
+ * xq and wq on 16-byte boundaries (MOE_ERR_BAD_SHAPE). */
+moe_status moe_linear_int8(int64_t M, int64_t N, int64_t K, const int8_t* xq, const float* xs, const int8_t* wq,
+                           const float* ws, const float* bias, void* out, void* stream);
+
+/* moe_linear_int8_dynamic - moe_linear_int8 of bf16 rows x (M, K), quantised per
+ * row by the rule of moe_quant_rows_int8 (rows whose largest magnitude is below
+ * 2^-121 keep a finite multiplier).  workspace >= moe_linear_int8_workspace_size
+ * bytes. */
+moe_status moe_linear_int8_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
+moe_status moe_linear_int8_dynamic(int64_t M, int64_t N, int64_t K, const void* x, const int8_t* wq,
+                                   const float* ws, const float* bias, void* out, void* workspace, size_t ws_bytes,
+                                   void* stream);
 
 /* moe_hbm_stream - a reference streaming kernel (not part of the layer): the
  * measured HBM ceiling that the gather-reduce kernels are compared with.
