@@ -1,6 +1,6 @@
-// A whole MoE layer forward for a few tokens (T <= 64) in two kernels: every
-// expert's weights are read from memory once, whatever the number of its rows,
-// and nothing is rounded between x and out.
+// A whole MoE layer forward for a few tokens (T <= 64): every expert's weights are
+// read from memory once, whatever the number of its rows, and nothing is rounded
+// between x and out.
 //
 //   gate/up   for every active slot s = (t, k) of expert e:
 //             h_s = silu(Wg_e x_t) * (Wu_e x_t)
@@ -11,13 +11,15 @@
 // expert in LDS for itself (route_lds).  A shared expert is one more expert that
 // every token goes to with weight 1.
 //
-// Work split.  gate/up: a workgroup per (active expert, 16 columns of F), its
-// waves splitting the contraction over H.  down: a workgroup per 16 columns of H
+// Work split.  gate/up: a workgroup per (active expert, columns of F), its waves
+// splitting the contraction over H.  down, T <= 16: a workgroup per 32 columns of H
 // that goes over all active experts, its waves splitting the (expert, F) steps
-// evenly, so a token's weighted sum stays inside one workgroup: no atomics, and
-// the same order of additions in every call.  Rows are packed per expert (the
-// matrix cores take 16 at a time) and each wave adds its packed rows' weighted
-// results to its own LDS copy of the output tile.
+// evenly, so a token's weighted sum stays inside one workgroup: no third kernel, no
+// atomics, the same order of additions in every call.  Rows are packed per expert
+// (the matrix cores take 16 at a time); each wave adds its packed rows' weighted
+// results to its own LDS copy of the output tile.  down, T > 16: a workgroup per
+// (active expert, 64 columns), which reads each row of h half as often, and a
+// small kernel for the weighted sums.
 //
 // bf16: h leaves as two bf16 planes, hi = bf16(h) and lo = bf16(h - hi), 16
 // significant bits in all; both multiply the same weight registers.  int8: rows
@@ -33,7 +35,24 @@ namespace moe {
 namespace {
 
 constexpr int kMaxTokens = 64, kMaxSlots = 1024, kMaxExperts = 1024;
-constexpr int kUpWaves = 4, kDownWaves = 8;
+
+// Sizes of the work, by the row tiles (16 rows) that T tokens may need, RTM = 1, 2
+// or 4.  Waves split the contraction; CT column tiles of a wave share its
+// activation loads, which cost the vector L1 as much as the weights' (RT = 1 to 4
+// tiles of rows, in bf16 two planes of h); U steps of loads are in flight in a
+// wave.  (UP: gate/up, DN: down that sums over the experts, Y: down by expert.)
+constexpr int kUpWaves = 4, kDownWaves = 8, kYWaves = 4;
+template <int RTM>
+constexpr int kUpCT = RTM == 1 ? 1 : 2;
+template <int RTM>
+constexpr int kDownCT = RTM == 1 ? 2 : 4;
+template <int RTM>
+constexpr int kUpOcc = RTM == 1 ? 4 : 2;  // waves per SIMD the registers have to leave room for
+constexpr int kDownOcc = 3;
+template <int RT>
+constexpr int kUpU = RT == 4 ? 2 : 4;
+template <int RT>
+constexpr int kDownU = RT == 1 ? 4 : (RT == 2 ? 2 : 1);
 
 struct FewArgs {
   const int32_t* idx;
@@ -75,58 +94,94 @@ struct FewArgs {
   int64_t H, F, Fs;  // Fs 0: no shared expert
   int T, K, E, Z, C, Q, mask_ndim;
   int groups;  // most active experts: min(T K, E)
+  float* y;   // rows of slots, then the shared expert's: the expert outputs where down does not join them
 };
 
-// The call's slots sorted by expert, in LDS.
+// The call's slots sorted by expert, in LDS (sized by the call: route_bytes).
 struct Route {
-  int32_t code[kMaxSlots];       // id of a routed slot, MOE_SLOT_NONE, MOE_SLOT_COPY or -(3 + j)
-  int32_t first[kMaxExperts];    // slots of the expert, then the end of its run in `slot`
-  uint16_t expert[kMaxSlots];    // active experts, in id order
-  uint16_t begin[kMaxSlots + 1];  // the active expert's run in `slot`
-  uint16_t slot[kMaxSlots];
-  int32_t active;
-  uint32_t err;
+  int32_t* head;     // active experts, error bits
+  int32_t* code;     // S: id of a routed slot, MOE_SLOT_NONE, MOE_SLOT_COPY or -(3 + j)
+  int32_t* first;    // E: slots of the expert, then the end of its run in `slot`
+  uint16_t* expert;  // active experts, in id order
+  uint16_t* begin;   // the active expert's run in `slot`; one more than experts
+  uint16_t* slot;    // S
 };
 
-// Fills r (every thread of the workgroup; THREADS of them).  A masked, invalid
-// or repeated slot (the later one) is inactive, as in the dispatch.  The order
-// of an expert's slots in `slot` is not fixed; no result depends on it.
-template <int THREADS>
-__device__ void route_lds(const FewArgs& a, Route& r) {
+__host__ __device__ inline int route_bytes(int S, int E, int groups) {
+  const int n = 16 + 4 * (S + E) + 2 * (2 * groups + 1 + S);
+  return (n + 15) / 16 * 16;
+}
+
+__device__ __forceinline__ Route route_at(char* lds, int S, int E, int groups) {
+  Route r;
+  r.head = reinterpret_cast<int32_t*>(lds);
+  r.code = r.head + 4;
+  r.first = r.code + S;
+  r.expert = reinterpret_cast<uint16_t*>(r.first + E);
+  r.begin = r.expert + groups;
+  r.slot = r.begin + groups + 1;
+  return r;
+}
+
+// Class of slot k of token t, `ids` its K ids: a routed expert's id, MOE_SLOT_NONE,
+// MOE_SLOT_COPY or -(3 + j).  A masked, invalid or repeated slot (the later one) is
+// inactive, as in the dispatch.
+__device__ __forceinline__ int slot_code(const FewArgs& a, const int32_t* ids, int t, int k, uint32_t& err) {
+  const int id = ids[k];
+  bool act = true, dup = false;
+  if (a.mask_ndim == 1) {
+    act = a.mask[t] != 0;
+    if (k == 0 && t > 0 && act && a.mask[t - 1] == 0) err |= MOE_FLAG_MASK_NOT_PREFIX;
+  } else if (a.mask_ndim == 2) {
+    act = a.mask[t * a.K + k] != 0;
+  }
+  for (int j = 0; j < k; ++j) dup |= ids[j] == id;
+  if (id < 0 || id >= a.E + a.Z + a.C + a.Q) {
+    err |= MOE_FLAG_ID_RANGE;
+    return MOE_SLOT_NONE;
+  }
+  if (dup) {
+    err |= MOE_FLAG_ID_DUPLICATE;
+    return MOE_SLOT_NONE;
+  }
+  if (!act) return MOE_SLOT_NONE;
+  if (id < a.E) return id;
+  if (id < a.E + a.Z) return MOE_SLOT_NONE;
+  return id < a.E + a.Z + a.C ? MOE_SLOT_COPY : -(3 + (id - a.E - a.Z - a.C));
+}
+
+// Fills r (every thread of the workgroup; THREADS of them, at most SLOTS slots).
+// The order of an expert's slots in `slot` is not fixed; no result depends on it.
+template <int THREADS, int SLOTS>
+__device__ void route_lds(const FewArgs& a, const Route& r) {
+  constexpr int PER = (SLOTS + THREADS - 1) / THREADS;
   const int tid = threadIdx.x, S = a.T * a.K;
+  int id[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) id[i] = tid + i * THREADS < S ? a.idx[tid + i * THREADS] : -1;
   for (int e = tid; e < a.E; e += THREADS) r.first[e] = 0;
-  if (tid == 0) r.err = 0;
-  for (int s = tid; s < S; s += THREADS) r.code[s] = a.idx[s];
+  if (tid == 0) r.head[1] = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (tid + i * THREADS < S) r.code[tid + i * THREADS] = id[i];
   __syncthreads();
-  int cls[(kMaxSlots + THREADS - 1) / THREADS];
   uint32_t err = 0;
 #pragma unroll
-  for (int i = 0; i < (kMaxSlots + THREADS - 1) / THREADS; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int s = tid + i * THREADS;
-    if (s >= S) break;
-    const int t = s / a.K, k = s - t * a.K, id = r.code[s];
-    bool act = true, dup = false;
-    if (a.mask_ndim == 1) {
-      act = a.mask[t] != 0;
-      if (k == 0 && t > 0 && act && a.mask[t - 1] == 0) err |= MOE_FLAG_MASK_NOT_PREFIX;
-    } else if (a.mask_ndim == 2) {
-      act = a.mask[s] != 0;
-    }
-    for (int j = 1; j <= k; ++j) dup |= r.code[s - j] == id;
     int c = MOE_SLOT_NONE;
-    if (id < 0 || id >= a.E + a.Z + a.C + a.Q) err |= MOE_FLAG_ID_RANGE;
-    else if (dup) err |= MOE_FLAG_ID_DUPLICATE;
-    else if (!act) ;
-    else if (id < a.E) c = id;
-    else if (id >= a.E + a.Z) c = id < a.E + a.Z + a.C ? MOE_SLOT_COPY : -(3 + (id - a.E - a.Z - a.C));
-    cls[i] = c;
-    if (c >= 0) atomicAdd(&r.first[c], 1);
+    if (s < S) {
+      const int t = s / a.K;
+      c = slot_code(a, r.code + t * a.K, t, s - t * a.K, err);
+      if (c >= 0) atomicAdd(&r.first[c], 1);
+    }
+    id[i] = c;
   }
-  if (err) atomicOr(&r.err, err);
+  if (err) atomicOr(reinterpret_cast<uint32_t*>(&r.head[1]), err);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < (kMaxSlots + THREADS - 1) / THREADS; ++i)
-    if (tid + i * THREADS < S) r.code[tid + i * THREADS] = cls[i];
+  for (int i = 0; i < PER; ++i)
+    if (tid + i * THREADS < S) r.code[tid + i * THREADS] = id[i];
   if (tid < kWave) {
     // one wave: counts to run starts and the list of active experts
     int row = 0, n = 0;
@@ -149,16 +204,14 @@ __device__ void route_lds(const FewArgs& a, Route& r) {
       n += __popcll(m);
     }
     if (tid == 0) {
-      r.active = n;
+      r.head[0] = n;
       r.begin[n] = (uint16_t)row;
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < (kMaxSlots + THREADS - 1) / THREADS; ++i) {
-    const int s = tid + i * THREADS;
-    if (s < S && cls[i] >= 0) r.slot[atomicAdd(&r.first[cls[i]], 1)] = (uint16_t)s;
-  }
+  for (int i = 0; i < PER; ++i)
+    if (id[i] >= 0) r.slot[atomicAdd(&r.first[id[i]], 1)] = (uint16_t)(tid + i * THREADS);
   __syncthreads();
 }
 
@@ -214,51 +267,67 @@ __global__ __launch_bounds__(256) void k_few_quant_h(FewArgs a) {
   if (threadIdx.x == 0) (sh ? a.shs : a.hs)[row] = s;
 }
 
-// A group's rows r0 .. r0 + 16 RT - 1 through its 16 gate and 16 up columns from
-// f0 on.  `slots`: the group's slots, NULL for the shared expert (row = token).
-template <bool I8, int RT>
-__device__ __forceinline__ void gate_up_rows(const FewArgs& a, const uint16_t* slots, int n, int r0, int e, int64_t f0,
-                                             float4 (*red)[2][4][kWave]) {
-  constexpr int ES = I8 ? 1 : 2;
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+// An expert's rows (at most 16 RT) through its 16 CT gate and 16 CT up columns from
+// f0 on.  `slots`: the expert's slots, NULL for the shared expert (row = token).
+// red: 2 RT KB for each wave.
+template <bool I8, int RT, int CT>
+__device__ __forceinline__ void gate_up_rows(const FewArgs& a, const uint16_t* slots, int n, int e, int64_t f0,
+                                             float4* red) {
+  typedef typename MfmaAcc<I8>::type Acc;
+  constexpr int ES = I8 ? 1 : 2, U = kUpU<RT>;
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const bool sh = slots == nullptr;
   const int64_t F = sh ? a.Fs : a.F, bytes = a.H * ES;
   const int64_t wrow = (sh ? 0 : (int64_t)e * F) + f0;
-  const int64_t woff = (wrow + lane % 16) * bytes + 16 * (lane / 16);
-  const char* w[2] = {static_cast<const char*>(sh ? a.swg : a.wg) + woff, static_cast<const char*>(sh ? a.swu : a.wu) + woff};
-  const char* x[1][RT];
+  const char* w[2 * CT];
+  uint32_t woff[2 * CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    // a column tile past F reads the first one
+    const int64_t at = (wrow + (f0 + 16 * c < F ? 16 * c : 0)) * bytes;
+    w[2 * c] = static_cast<const char*>(sh ? a.swg : a.wg) + at;
+    w[2 * c + 1] = static_cast<const char*>(sh ? a.swu : a.wu) + at;
+    woff[2 * c] = woff[2 * c + 1] = (uint32_t)(lane % 16) * (uint32_t)bytes + 16 * (lane / 16);
+  }
+  const char* x[1] = {I8 ? reinterpret_cast<const char*>(a.xq) : reinterpret_cast<const char*>(a.x)};
+  uint32_t xoff[RT];  // at most 64 rows of 2^21 bytes, or 1088 of 2^17
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    int i = r0 + 16 * r + lane % 16;
+    int i = 16 * r + lane % 16;
     if (i >= n) i = n - 1;
     const int s = sh ? i : slots[i];
-    const int64_t row = sh ? s : (I8 && a.smooth ? a.T + s : s / a.K);
-    x[0][r] = (I8 ? reinterpret_cast<const char*>(a.xq) : reinterpret_cast<const char*>(a.x)) + row * bytes + 16 * (lane / 16);
+    const int row = sh ? s : (I8 && a.smooth ? a.T + s : s / a.K);
+    xoff[r] = (uint32_t)row * (uint32_t)bytes + 16 * (lane / 16);
   }
-  typename MfmaAcc<I8>::type acc[2][RT];
+  Acc acc[2 * CT][RT];
 #pragma unroll
-  for (int g = 0; g < 2; ++g)
+  for (int g = 0; g < 2 * CT; ++g)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[g][r] = typename MfmaAcc<I8>::type{0, 0, 0, 0};
+    for (int r = 0; r < RT; ++r) acc[g][r] = Acc{0, 0, 0, 0};
   const int ns = stream_steps(bytes);
-  stream_mfma<I8, 2, RT, 1, RT == 4 ? 2 : 4>(w, x, bytes, ns * wave / kUpWaves, ns * (wave + 1) / kUpWaves, acc);
+  stream_mfma<I8, 2 * CT, RT, 1, U>(w, woff, x, xoff, bytes, ns * wave / kUpWaves, ns * (wave + 1) / kUpWaves, acc);
 #pragma unroll
-  for (int g = 0; g < 2; ++g)
+  for (int ct = 0; ct < CT; ++ct) {
+    if (ct > 0) __syncthreads();
 #pragma unroll
-    for (int r = 0; r < RT; ++r) red[wave][g][r][lane] = __builtin_bit_cast(float4, acc[g][r]);
-  __syncthreads();
-  const int i = r0 + 16 * wave + lane % 16;
-  if (wave < RT && i < n) {
-    typename MfmaAcc<I8>::type s[2];
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        red[((wave * 2 + g) * RT + r) * kWave + lane] = __builtin_bit_cast(float4, acc[2 * ct + g][r]);
+    __syncthreads();
+    const int r = wave;
+    const int i = 16 * r + lane % 16;
+    if (r >= RT || i >= n || f0 + 16 * ct >= F) continue;
+    Acc s[2];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      s[g] = __builtin_bit_cast(typename MfmaAcc<I8>::type, red[0][g][wave][lane]);
+      s[g] = Acc{0, 0, 0, 0};
 #pragma unroll
-      for (int v = 1; v < kUpWaves; ++v)
-        s[g] += __builtin_bit_cast(typename MfmaAcc<I8>::type, red[v][g][wave][lane]);
+      for (int v = 0; v < kUpWaves; ++v)
+        s[g] += __builtin_bit_cast(Acc, red[((v * 2 + g) * RT + r) * kWave + lane]);
     }
     const int slot = sh ? i : slots[i];
-    const int64_t c = 4 * (lane / 16), at = (int64_t)slot * F + f0 + c;
+    const int64_t c = 16 * ct + 4 * (lane / 16), at = (int64_t)slot * F + f0 + c;
     float h[4];
     float xs = 1.f;
     if constexpr (I8) xs = a.xs[sh ? slot : (a.smooth ? a.T + slot : slot / a.K)];
@@ -286,106 +355,137 @@ __device__ __forceinline__ void gate_up_rows(const FewArgs& a, const uint16_t* s
       *reinterpret_cast<uint2*>((sh ? a.shlo : a.hlo) + at) = make_uint2(pack_bf2(lo[0], lo[1]), pack_bf2(lo[2], lo[3]));
     }
   }
-  __syncthreads();
 }
 
-template <bool I8>
-__global__ __launch_bounds__(kUpWaves* kWave) void k_few_gate_up(FewArgs a) {
-  __shared__ Route route;
-  __shared__ float4 red[kUpWaves][2][4][kWave];
-  route_lds<kUpWaves * kWave>(a, route);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err_flag = (int32_t)route.err;
-  const int tiles = (int)(a.F / 16);
-  const int g = blockIdx.x / tiles;
-  const uint16_t* slots = nullptr;
-  int n = a.T, e = 0;
-  int64_t f0 = (int64_t)(blockIdx.x - a.groups * tiles) * 16;
-  if (g < a.groups) {
-    if (g >= route.active) return;
-    e = route.expert[g];
-    slots = route.slot + route.begin[g];
-    n = route.begin[g + 1] - route.begin[g];
-    f0 = (int64_t)(blockIdx.x % tiles) * 16;
-  } else if (a.Fs == 0) {
-    return;
-  }
-  for (int r0 = 0; r0 < n;) {
-    const int left = (n - r0 + 15) / 16;
-    if (left == 1) gate_up_rows<I8, 1>(a, slots, n, r0, e, f0, red);
-    else if (left == 2) gate_up_rows<I8, 2>(a, slots, n, r0, e, f0, red);
-    else gate_up_rows<I8, 4>(a, slots, n, r0, e, f0, red);
-    r0 += left == 1 ? 16 : (left == 2 ? 32 : 64);
+// RTM: row tiles that T tokens may need (1, 2 or 4)
+template <bool I8, int RTM, int CT>
+__global__ __launch_bounds__(kUpWaves* kWave, kUpOcc<RTM>) void k_few_gate_up(FewArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const Route route = route_at(lds, a.T * a.K, a.E, a.groups);
+  float4* red = reinterpret_cast<float4*>(lds + route_bytes(a.T * a.K, a.E, a.groups));
+  route_lds<kUpWaves * kWave, RTM * 256>(a, route);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err_flag = route.head[1];
+  const int tiles = (int)((a.F + 16 * CT - 1) / (16 * CT));
+  const int routed = uniform(route.head[0]) * tiles, items = routed + (int)((a.Fs + 16 * CT - 1) / (16 * CT));
+  const int it = blockIdx.x;
+  if (it < items) {
+    const bool sh = it >= routed;
+    const int g = sh ? 0 : it / tiles;
+    const int b = sh ? 0 : uniform(route.begin[g]);
+    const uint16_t* slots = sh ? nullptr : route.slot + b;
+    const int n = sh ? a.T : uniform(route.begin[g + 1]) - b, e = sh ? 0 : uniform(route.expert[g]);
+    const int64_t f0 = (int64_t)(sh ? it - routed : it - g * tiles) * (16 * CT);
+    const int rt = (n + 15) / 16;
+    if (RTM > 2 && rt > 2) gate_up_rows<I8, RTM, CT>(a, slots, n, e, f0, red);
+    else if (RTM > 1 && rt > 1) gate_up_rows<I8, RTM < 2 ? 1 : 2, CT>(a, slots, n, e, f0, red);
+    else gate_up_rows<I8, 1, CT>(a, slots, n, e, f0, red);
   }
 }
 
-// One expert's packed rows through this workgroup's 16 columns from c0 on, steps
-// [s0, s1) of F, added to the wave's output tile `o` (T rows of 16 columns).
-template <bool I8, int RT>
-__device__ __forceinline__ void down_rows(const FewArgs& a, const uint16_t* slots, int n, int r0, int e, int64_t c0,
-                                          int s0, int s1, float (*o)[16]) {
+// One expert's packed rows (at most 16 RT) through 16 CT columns of H from c0 on,
+// steps [s0, s1) of F.  slot[r]: the lane's row (slot, or the shared expert's
+// token), -1 past the last.
+template <bool I8, int RT, int CT, int U>
+__device__ __forceinline__ void down_stream(const FewArgs& a, const uint16_t* slots, int n, int e, int64_t c0, int s0,
+                                            int s1, int (&slot)[RT], typename MfmaAcc<I8>::type (&acc)[CT][RT]) {
   constexpr int ES = I8 ? 1 : 2, PX = I8 ? 1 : 2;
   const int lane = threadIdx.x % kWave;
   const bool sh = slots == nullptr;
   const int64_t F = sh ? a.Fs : a.F, bytes = F * ES;
-  const int64_t col = c0 + lane % 16 < a.H ? c0 + lane % 16 : a.H - 1;
   const int64_t wrow = sh ? 0 : (int64_t)e * a.H;
-  const char* w[1] = {static_cast<const char*>(sh ? a.swd : a.wd) + (wrow + col) * bytes + 16 * (lane / 16)};
-  const char* x[PX][RT];
-  int slot[RT];
+  const char* w[CT];
+  uint32_t woff[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    // a column past H reads the last one
+    const int64_t left = a.H - 1 - c0, col = 16 * c + lane % 16;
+    w[c] = static_cast<const char*>(sh ? a.swd : a.wd) + (wrow + c0) * bytes;
+    woff[c] = (uint32_t)(col < left ? col : left) * (uint32_t)bytes + 16 * (lane / 16);
+  }
+  const char* x[PX];
+  x[0] = I8 ? reinterpret_cast<const char*>(sh ? a.shq : a.hq) : reinterpret_cast<const char*>(sh ? a.shhi : a.hhi);
+  if constexpr (!I8) x[1] = reinterpret_cast<const char*>(sh ? a.shlo : a.hlo);
+  uint32_t xoff[RT];  // at most 1024 rows of 2^21 bytes
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    int i = r0 + 16 * r + lane % 16;
+    int i = 16 * r + lane % 16;
     const bool in = i < n;
     if (!in) i = n - 1;
     const int s = sh ? i : slots[i];
     slot[r] = in ? s : -1;
-    const int64_t off = s * bytes + 16 * (lane / 16);
-    if constexpr (I8) {
-      x[0][r] = reinterpret_cast<const char*>(sh ? a.shq : a.hq) + off;
-    } else {
-      x[0][r] = reinterpret_cast<const char*>(sh ? a.shhi : a.hhi) + off;
-      x[1][r] = reinterpret_cast<const char*>(sh ? a.shlo : a.hlo) + off;
-    }
+    xoff[r] = (uint32_t)s * (uint32_t)bytes + 16 * (lane / 16);
   }
-  typename MfmaAcc<I8>::type acc[1][RT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) acc[0][r] = typename MfmaAcc<I8>::type{0, 0, 0, 0};
-  stream_mfma<I8, 1, RT, PX, RT == 1 ? 8 : (RT == 2 ? 4 : 2)>(w, x, bytes, s0, s1, acc);
-  const int64_t c = c0 + 4 * (lane / 16);
-  if (c >= a.H) return;  // H is a multiple of 8: four columns are in or out together
+  for (int c = 0; c < CT; ++c)
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-    if (slot[r] >= 0) {
-      const float wt = sh ? 1.0f : a.w[slot[r]];
-      float4* p = reinterpret_cast<float4*>(&o[sh ? slot[r] : slot[r] / a.K][4 * (lane / 16)]);
+    for (int r = 0; r < RT; ++r) acc[c][r] = typename MfmaAcc<I8>::type{0, 0, 0, 0};
+  stream_mfma<I8, CT, RT, PX, U>(w, woff, x, xoff, bytes, s0, s1, acc);
+}
+
+// down_stream of at most 16 rows, the weighted results added to the wave's output
+// tile `o` (T rows of 16 CT columns).
+template <bool I8, int CT>
+__device__ __forceinline__ void down_rows(const FewArgs& a, const uint16_t* slots, int n, int e, int64_t c0, int s0,
+                                          int s1, float (*o)[16 * CT]) {
+  const int lane = threadIdx.x % kWave;
+  const bool sh = slots == nullptr;
+  const int64_t wrow = sh ? 0 : (int64_t)e * a.H;
+  typename MfmaAcc<I8>::type acc[CT][1];
+  int slot[1];
+  down_stream<I8, 1, CT, kDownU<1>>(a, slots, n, e, c0, s0, s1, slot, acc);
+  if (slot[0] >= 0) {
+    const float wt = sh ? 1.0f : a.w[slot[0]];
+    float* row = o[sh ? slot[0] : slot[0] / a.K];
+    float hs = 1.f;
+    if constexpr (I8) hs = (sh ? a.shs : a.hs)[slot[0]];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const int64_t c = c0 + 16 * ct + 4 * (lane / 16);
+      if (c >= a.H) continue;  // H is a multiple of 8: four columns are in or out together
+      float4* p = reinterpret_cast<float4*>(row + 16 * ct + 4 * (lane / 16));
       float4 v = *p;
       float y[4];
-      float hs = 1.f;
-      if constexpr (I8) hs = (sh ? a.shs : a.hs)[slot[r]];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        y[q] = (float)acc[0][r][q];
+        y[q] = (float)acc[ct][0][q];
         if constexpr (I8) y[q] *= __fmul_rn(hs, (sh ? a.swds : a.wds)[wrow + c + q]);
       }
       v.x += wt * y[0]; v.y += wt * y[1]; v.z += wt * y[2]; v.w += wt * y[3];
       *p = v;
     }
+  }
   // the next expert's rows of the same tokens may sit in other lanes
   __builtin_amdgcn_wave_barrier();
 }
 
-// dynamic LDS: kDownWaves output tiles of T rows x 16 columns
-template <bool I8>
-__global__ __launch_bounds__(kDownWaves* kWave) void k_few_down(FewArgs a) {
-  constexpr int ES = I8 ? 1 : 2;
-  __shared__ Route route;
-  extern __shared__ __attribute__((aligned(16))) float tiles[];
-  const int wave = threadIdx.x / kWave;
-  for (int i = threadIdx.x; i < kDownWaves * a.T * 16; i += kDownWaves * kWave) tiles[i] = 0.f;
-  route_lds<kDownWaves * kWave>(a, route);
-  const int64_t c0 = (int64_t)blockIdx.x * 16;
-  float(*o)[16] = reinterpret_cast<float(*)[16]>(tiles) + wave * a.T;
-  const int per = stream_steps(a.F * ES), routed = route.active * per;
+// out[t, c] from its routed sum: the special experts in k order, the shared term last.
+__device__ __forceinline__ void few_finish(const FewArgs& a, const int32_t* code, int t, int64_t c, float v) {
+  for (int k = 0; k < a.K; ++k) {
+    if (code[k] > MOE_SLOT_COPY) continue;
+    float f = bf2f(a.x[t * a.H + c]);
+    if (code[k] != MOE_SLOT_COPY) {
+      const int64_t j = (int64_t)(-code[k] - 3) * a.H + c;
+      f = bf2f(a.a1[j]) * f + bf2f(a.a2[j]) * bf2f(a.cv[j]);
+    }
+    v += a.w[t * a.K + k] * f;
+  }
+  if (a.shared_x) v += bf2f(a.shared_x[t * a.H + c]);
+  a.out[t * a.H + c] = (bf16_t)f2bf(v);
+}
+
+// dynamic LDS: the routing, then kDownWaves output tiles of T rows x 16 CT columns
+template <bool I8, int CT>
+__global__ __launch_bounds__(kDownWaves* kWave, kDownOcc) void k_few_down(FewArgs a) {
+  constexpr int ES = I8 ? 1 : 2, COLS = 16 * CT;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const Route route = route_at(lds, a.T * a.K, a.E, a.groups);
+  float* tiles = reinterpret_cast<float*>(lds + route_bytes(a.T * a.K, a.E, a.groups));
+  const int wave = uniform(threadIdx.x / kWave);
+  for (int i = threadIdx.x; i < kDownWaves * a.T * COLS; i += kDownWaves * kWave) tiles[i] = 0.f;
+  route_lds<kDownWaves * kWave, 256>(a, route);
+  const int64_t c0 = (int64_t)blockIdx.x * COLS;
+  float(*o)[COLS] = reinterpret_cast<float(*)[COLS]>(tiles) + wave * a.T;
+  const int per = stream_steps(a.F * ES), routed = uniform(route.head[0]) * per;
   const int total = routed + stream_steps(a.Fs * ES);
   int u = (int)((int64_t)total * wave / kDownWaves);
   const int u1 = (int)((int64_t)total * (wave + 1) / kDownWaves);
@@ -394,41 +494,113 @@ __global__ __launch_bounds__(kDownWaves* kWave) void k_few_down(FewArgs a) {
     const int g = u / per, s0 = sh ? u - routed : u - g * per;
     const int len = (sh ? total - routed : per) - s0;
     const int s1 = s0 + (len < u1 - u ? len : u1 - u);
-    const int n = sh ? a.T : route.begin[g + 1] - route.begin[g];
-    const int e = sh ? 0 : route.expert[g];
-    const uint16_t* slots = sh ? nullptr : route.slot + route.begin[g];
-    for (int r0 = 0; r0 < n;) {
-      const int left = (n - r0 + 15) / 16;
-      if (left == 1) down_rows<I8, 1>(a, slots, n, r0, e, c0, s0, s1, o);
-      else if (left == 2) down_rows<I8, 2>(a, slots, n, r0, e, c0, s0, s1, o);
-      else down_rows<I8, 4>(a, slots, n, r0, e, c0, s0, s1, o);
-      r0 += left == 1 ? 16 : (left == 2 ? 32 : 64);
-    }
+    const int b = sh ? 0 : uniform(route.begin[g]);
+    const int n = sh ? a.T : uniform(route.begin[g + 1]) - b;
+    const int e = sh ? 0 : uniform(route.expert[g]);
+    const uint16_t* slots = sh ? nullptr : route.slot + b;
     u += s1 - s0;
+    down_rows<I8, CT>(a, slots, n, e, c0, s0, s1, o);
   }
   __syncthreads();
-  // join the waves' tiles, then the special experts in k order, the shared term last
-  for (int i = threadIdx.x; i < a.T * 16; i += kDownWaves * kWave) {
-    const int t = i / 16;
-    const int64_t c = c0 + i % 16;
+  for (int i = threadIdx.x; i < a.T * COLS; i += kDownWaves * kWave) {
+    const int t = i / COLS;
+    const int64_t c = c0 + i % COLS;
     if (c >= a.H) continue;
     float v = 0.f;
 #pragma unroll
-    for (int p = 0; p < kDownWaves; ++p) v += tiles[p * a.T * 16 + i];
-    for (int k = 0; k < a.K; ++k) {
-      const int code = route.code[t * a.K + k];
-      if (code > MOE_SLOT_COPY) continue;
-      float f = bf2f(a.x[t * a.H + c]);
-      if (code != MOE_SLOT_COPY) {
-        const int64_t j = (int64_t)(-code - 3) * a.H + c;
-        f = bf2f(a.a1[j]) * f + bf2f(a.a2[j]) * bf2f(a.cv[j]);
-      }
-      v += a.w[t * a.K + k] * f;
-    }
-    if (a.shared_x) v += bf2f(a.shared_x[t * a.H + c]);
-    a.out[t * a.H + c] = (bf16_t)f2bf(v);
+    for (int p = 0; p < kDownWaves; ++p) v += tiles[p * a.T * COLS + i];
+    few_finish(a, route.code + t * a.K, t, c, v);
   }
 }
+
+// One expert's rows (at most 16 RT) through 16 CT columns of H from c0 on: rows of y.
+// red: RT KB for each wave.
+template <bool I8, int RT, int CT>
+__device__ __forceinline__ void down_y_rows(const FewArgs& a, const uint16_t* slots, int n, int e, int64_t c0,
+                                            float4* red) {
+  typedef typename MfmaAcc<I8>::type Acc;
+  constexpr int U = kDownU<RT>;
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const bool sh = slots == nullptr;
+  Acc acc[CT][RT];
+  int slot[RT];
+  const int ns = stream_steps((sh ? a.Fs : a.F) * (I8 ? 1 : 2));
+  down_stream<I8, RT, CT, U>(a, slots, n, e, c0, ns * wave / kYWaves, ns * (wave + 1) / kYWaves, slot, acc);
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    if (ct > 0) __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RT; ++r) red[(wave * RT + r) * kWave + lane] = __builtin_bit_cast(float4, acc[ct][r]);
+    __syncthreads();
+    const int i = 16 * wave + lane % 16;
+    const int64_t c = c0 + 16 * ct + 4 * (lane / 16);
+    if (wave >= RT || i >= n || c >= a.H) continue;
+    Acc s = {0, 0, 0, 0};
+#pragma unroll
+    for (int v = 0; v < kYWaves; ++v) s += __builtin_bit_cast(Acc, red[(v * RT + wave) * kWave + lane]);
+    const int64_t row = sh ? i : slots[i];
+    float y[4];
+    float hs = 1.f;
+    if constexpr (I8) hs = (sh ? a.shs : a.hs)[row];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      y[q] = (float)s[q];
+      if constexpr (I8) y[q] *= __fmul_rn(hs, (sh ? a.swds : a.wds + (int64_t)e * a.H)[c + q]);
+    }
+    *reinterpret_cast<float4*>(a.y + (sh ? (int64_t)a.T * a.K + row : row) * a.H + c) = make_float4(y[0], y[1], y[2], y[3]);
+  }
+}
+
+// larger batches: a workgroup per (active expert, 16 CT columns of H)
+template <bool I8, int RTM, int CT>
+__global__ __launch_bounds__(kYWaves* kWave, kDownOcc) void k_few_down_y(FewArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const Route route = route_at(lds, a.T * a.K, a.E, a.groups);
+  float4* red = reinterpret_cast<float4*>(lds + route_bytes(a.T * a.K, a.E, a.groups));
+  route_lds<kYWaves * kWave, RTM * 256>(a, route);
+  const int tiles = (int)((a.H + 16 * CT - 1) / (16 * CT));
+  const int routed = uniform(route.head[0]) * tiles, items = routed + (a.Fs > 0 ? tiles : 0);
+  const int it = blockIdx.x;
+  if (it < items) {
+    const bool sh = it >= routed;
+    const int g = it / tiles;
+    const int64_t c0 = (int64_t)(it - g * tiles) * (16 * CT);
+    const int b = sh ? 0 : uniform(route.begin[g]);
+    const uint16_t* slots = sh ? nullptr : route.slot + b;
+    const int n = sh ? a.T : uniform(route.begin[g + 1]) - b, e = sh ? 0 : uniform(route.expert[g]);
+    const int rt = (n + 15) / 16;
+    if (RTM > 2 && rt > 2) down_y_rows<I8, RTM, CT>(a, slots, n, e, c0, red);
+    else if (RTM > 1 && rt > 1) down_y_rows<I8, RTM < 2 ? 1 : 2, CT>(a, slots, n, e, c0, red);
+    else down_y_rows<I8, 1, CT>(a, slots, n, e, c0, red);
+  }
+}
+
+// four outputs of one token per thread: the weighted sum of y over its slots in k
+// order, the shared expert's row and the shared term
+__global__ __launch_bounds__(256) void k_few_join(FewArgs a) {
+  __shared__ int32_t code[16];
+  const int t = blockIdx.y;
+  if (threadIdx.x < a.K) {
+    uint32_t err = 0;
+    code[threadIdx.x] = slot_code(a, a.idx + t * a.K, t, threadIdx.x, err);
+  }
+  __syncthreads();
+  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (c >= a.H) return;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k <= a.K; ++k) {
+    const bool sh = k == a.K;
+    if (sh ? a.Fs == 0 : code[k] < 0) continue;
+    const float wt = sh ? 1.f : a.w[t * a.K + k];
+    const float4 y = *reinterpret_cast<const float4*>(a.y + (sh ? (int64_t)a.T * a.K + t : (int64_t)t * a.K + k) * a.H + c);
+    v[0] += wt * y.x; v[1] += wt * y.y; v[2] += wt * y.z; v[3] += wt * y.w;
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) few_finish(a, code, t, c + q, v[q]);
+}
+
+// Whether the down kernel sums over the experts itself (two kernels in all).
+bool few_joins(int T) { return T <= 16; }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -456,6 +628,7 @@ size_t few_layout(FewArgs& a, bool i8, char* base) {
     a.shhi = reinterpret_cast<bf16_t*>(take(T * Fs * 2));
     a.shlo = reinterpret_cast<bf16_t*>(take(T * Fs * 2));
   }
+  if (!few_joins(a.T)) a.y = reinterpret_cast<float*>(take((S + T) * H * 4));
   return n < 256 ? 256 : n;
 }
 
@@ -476,6 +649,27 @@ struct FewWeight {
   const void* codes;
   const float* scales;
 };
+
+template <bool I8, int RTM>
+moe_status few_launch(FewArgs& a, hipStream_t strm) {
+  constexpr int UC = kUpCT<RTM>, DC = kDownCT<RTM>;
+  const int S = a.T * a.K, rb = route_bytes(S, a.E, a.groups);
+  auto tiles = [](int64_t n, int ct) { return (n + 16 * ct - 1) / (16 * ct); };
+  const int64_t up = a.groups * tiles(a.F, UC) + tiles(a.Fs, UC);
+  if (up > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL((k_few_gate_up<I8, RTM, UC>), dim3((unsigned)up), dim3(kUpWaves * kWave),
+                     rb + kUpWaves * 2 * RTM * kWave * 16, strm, a);
+  if (I8) hipLaunchKernelGGL(k_few_quant_h, dim3(S + (a.Fs ? a.T : 0)), dim3(256), 0, strm, a);
+  if constexpr (RTM == 1) {
+    hipLaunchKernelGGL((k_few_down<I8, DC>), dim3((unsigned)tiles(a.H, DC)), dim3(kDownWaves * kWave),
+                       rb + kDownWaves * a.T * 16 * DC * 4, strm, a);
+  } else {
+    hipLaunchKernelGGL((k_few_down_y<I8, RTM, DC>), dim3((unsigned)(a.groups + (a.Fs > 0)) * tiles(a.H, DC)),
+                       dim3(kYWaves * kWave), rb + kYWaves * RTM * kWave * 16, strm, a);
+    hipLaunchKernelGGL(k_few_join, dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.T), dim3(256), 0, strm, a);
+  }
+  return launch_status();
+}
 
 // The kernels read and write vectors of up to 16 bytes.
 bool misaligned(std::initializer_list<const void*> ps) {
@@ -526,23 +720,17 @@ moe_status few_impl(const moe_shape* s, bool i8, const void* x, const int32_t* t
   a.groups = S < a.E ? S : a.E;
   const size_t need = few_layout(a, i8, static_cast<char*>(workspace));
   if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
-  // gate/up tiles; one workgroup at least, for the error flag
-  const int64_t nb = a.T == 0 ? 0 : a.groups * (a.F / 16) + Fs / 16;
-  if (nb > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  const dim3 up((unsigned)(nb > 0 ? nb : 1)), down((unsigned)((a.H + 15) / 16));
-  const size_t lds = (size_t)kDownWaves * a.T * 16 * 4;
-  if (i8) {
-    if (S > 0) hipLaunchKernelGGL(k_few_quant_x, dim3(a.T + (smooth ? S : 0)), dim3(256), 0, strm, a);
-    hipLaunchKernelGGL(k_few_gate_up<true>, up, dim3(kUpWaves * kWave), 0, strm, a);
-    if (S == 0) return launch_status();
-    hipLaunchKernelGGL(k_few_quant_h, dim3(S + (Fs ? a.T : 0)), dim3(256), 0, strm, a);
-    hipLaunchKernelGGL(k_few_down<true>, down, dim3(kDownWaves * kWave), lds, strm, a);
-  } else {
-    hipLaunchKernelGGL(k_few_gate_up<false>, up, dim3(kUpWaves * kWave), 0, strm, a);
-    if (S == 0) return launch_status();
-    hipLaunchKernelGGL(k_few_down<false>, down, dim3(kDownWaves * kWave), lds, strm, a);
+  if (S == 0) {
+    // the error flag alone
+    a.Fs = 0;
+    hipLaunchKernelGGL((k_few_gate_up<false, 1, kUpCT<1>>), dim3(1), dim3(kUpWaves * kWave), route_bytes(0, a.E, 0), strm, a);
+    return launch_status();
   }
-  return launch_status();
+  if (i8) {
+    hipLaunchKernelGGL(k_few_quant_x, dim3(a.T + (smooth ? S : 0)), dim3(256), 0, strm, a);
+    return a.T <= 16 ? few_launch<true, 1>(a, strm) : (a.T <= 32 ? few_launch<true, 2>(a, strm) : few_launch<true, 4>(a, strm));
+  }
+  return a.T <= 16 ? few_launch<false, 1>(a, strm) : (a.T <= 32 ? few_launch<false, 2>(a, strm) : few_launch<false, 4>(a, strm));
 }
 
 }  // namespace

@@ -39,21 +39,25 @@ __global__ __launch_bounds__(256) void k_quant_x(const uint4* __restrict__ x, in
 template <int RT>
 __global__ __launch_bounds__(kRowWaves* kWave) void k_linear_rows(LinArgs a) {
   __shared__ i32x4_t red[kRowWaves][RT][kWave];
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (RT * 16);
-  const int64_t n = n0 + lane % 16 < a.N ? n0 + lane % 16 : a.N - 1;
-  const char* w[1] = {reinterpret_cast<const char*>(a.wq) + n * a.K + 16 * (lane / 16)};
-  const char* x[1][RT];
+  // a column or row past the end reads the last one
+  const uint32_t K = (uint32_t)a.K, nl = (uint32_t)(a.N - 1 - n0), ml = (uint32_t)(a.M - 1 - m0);
+  const char* w[1] = {reinterpret_cast<const char*>(a.wq) + n0 * a.K};
+  const char* x[1] = {reinterpret_cast<const char*>(a.xq) + m0 * a.K};
+  const uint32_t row = lane % 16, chunk = 16 * (lane / 16);
+  const uint32_t woff[1] = {(row < nl ? row : nl) * K + chunk};
+  uint32_t xoff[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    const int64_t m = m0 + 16 * r + lane % 16;
-    x[0][r] = reinterpret_cast<const char*>(a.xq) + (m < a.M ? m : a.M - 1) * a.K + 16 * (lane / 16);
+    const uint32_t m = 16 * r + row;
+    xoff[r] = (m < ml ? m : ml) * K + chunk;
   }
   i32x4_t acc[1][RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) acc[0][r] = i32x4_t{0, 0, 0, 0};
   const int ns = stream_steps(a.K);
-  stream_mfma<true, 1, RT, 1, RT == 1 ? 8 : (RT == 2 ? 4 : 2)>(w, x, a.K, ns * wave / kRowWaves,
+  stream_mfma<true, 1, RT, 1, RT == 1 ? 8 : (RT == 2 ? 4 : 2)>(w, woff, x, xoff, a.K, ns * wave / kRowWaves,
                                                               ns * (wave + 1) / kRowWaves, acc);
 #pragma unroll
   for (int r = 0; r < RT; ++r) red[wave][r][lane] = acc[0][r];

@@ -43,12 +43,22 @@ constexpr int kStepBytes = 64;  // bytes of every row in one step
 // Steps of a row of `bytes` bytes (a multiple of 16; the last step may be partial).
 __host__ __device__ inline int stream_steps(int64_t bytes) { return (int)((bytes + kStepBytes - 1) / kStepBytes); }
 
+// A value that every lane of the wave holds, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ i32x4_t ld16(const char* base, uint32_t off) {
+  return *reinterpret_cast<const i32x4_t*>(base + (size_t)off);
+}
+
 // acc[n][r] += (16 weight rows n) x (16 activation rows r) over steps [s0, s1) of
-// rows of `bytes` bytes.  w[n] and x[p][r] point at this lane's row, chunk l / 16
-// of step 0 (PX planes of activations, each multiplied with the same weights).
-// U steps' loads are issued before their products.
+// rows of `bytes` bytes.  A lane's chunk of step s of weight rows n is at
+// w[n] + 64 s + woff[n], of activation rows r, plane p, at x[p] + 64 s + xoff[r]
+// (PX planes, each multiplied with the same weights); w, x, s0 and s1 are the
+// same in every lane, so they stay in scalar registers.  U steps' loads are
+// issued before their products.
 template <bool I8, int NW, int RT, int PX, int U>
-__device__ __forceinline__ void stream_mfma(const char* const (&w)[NW], const char* const (&x)[PX][RT], int64_t bytes,
+__device__ __forceinline__ void stream_mfma(const char* const (&w)[NW], const uint32_t (&woff)[NW],
+                                            const char* const (&x)[PX], const uint32_t (&xoff)[RT], int64_t bytes,
                                             int s0, int s1, typename MfmaAcc<I8>::type (&acc)[NW][RT]) {
   const int full = (int)(bytes / kStepBytes);
   const int e = s1 < full ? s1 : full;
@@ -59,12 +69,13 @@ __device__ __forceinline__ void stream_mfma(const char* const (&w)[NW], const ch
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int n = 0; n < NW; ++n) wv[u][n] = *reinterpret_cast<const i32x4_t*>(w[n] + o + u * kStepBytes);
+      for (int n = 0; n < NW; ++n) wv[u][n] = ld16(w[n] + o + u * kStepBytes, woff[n]);
 #pragma unroll
       for (int p = 0; p < PX; ++p)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) xv[u][p][r] = *reinterpret_cast<const i32x4_t*>(x[p][r] + o + u * kStepBytes);
+        for (int r = 0; r < RT; ++r) xv[u][p][r] = ld16(x[p] + o + u * kStepBytes, xoff[r]);
     }
+    __builtin_amdgcn_sched_barrier(0);  // every load of the U steps before the first product
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -81,11 +92,11 @@ __device__ __forceinline__ void stream_mfma(const char* const (&w)[NW], const ch
     const i32x4_t z = {0, 0, 0, 0};
     i32x4_t wv[NW], xv[PX][RT];
 #pragma unroll
-    for (int n = 0; n < NW; ++n) wv[n] = in ? *reinterpret_cast<const i32x4_t*>(w[n] + o) : z;
+    for (int n = 0; n < NW; ++n) wv[n] = in ? ld16(w[n] + o, woff[n]) : z;
 #pragma unroll
     for (int p = 0; p < PX; ++p)
 #pragma unroll
-      for (int r = 0; r < RT; ++r) xv[p][r] = in ? *reinterpret_cast<const i32x4_t*>(x[p][r] + o) : z;
+      for (int r = 0; r < RT; ++r) xv[p][r] = in ? ld16(x[p] + o, xoff[r]) : z;
 #pragma unroll
     for (int n = 0; n < NW; ++n)
 #pragma unroll

@@ -202,7 +202,7 @@ def test_rows_do_not_depend_on_the_batch():
 @gpu
 @pytest.mark.parametrize("int8", [False, True])
 def test_no_tokens(int8):
-    p = make(1, 128, 32, 4, 2, 19, int8=int8)
+    p = make(1, 128, 32, 4, 2, 19, int8=int8, shared=64)
     p["x"], p["idx"], p["w"] = p["x"][:0], p["idx"][:0], p["w"][:0]
     flag = torch.full((1,), 3, dtype=torch.int32, device=DEV)
     assert call(p, err_flag=flag).shape == (0, 128)
