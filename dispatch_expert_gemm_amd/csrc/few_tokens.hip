@@ -38,21 +38,25 @@ constexpr int kMaxTokens = 64, kMaxSlots = 1024, kMaxExperts = 1024;
 
 // Sizes of the work, by the row tiles (16 rows) that T tokens may need, RTM = 1, 2
 // or 4.  Waves split the contraction; CT column tiles of a wave share its
-// activation loads, which cost the vector L1 as much as the weights' (RT = 1 to 4
-// tiles of rows, in bf16 two planes of h); U steps of loads are in flight in a
-// wave.  (UP: gate/up, DN: down that sums over the experts, Y: down by expert.)
-constexpr int kUpWaves = 4, kDownWaves = 8, kYWaves = 4;
-template <int RTM>
-constexpr int kUpCT = RTM == 1 ? 1 : 2;
-template <int RTM>
-constexpr int kDownCT = RTM == 1 ? 2 : 4;
-template <int RTM>
-constexpr int kUpOcc = RTM == 1 ? 4 : 2;  // waves per SIMD the registers have to leave room for
-constexpr int kDownOcc = 3;
-template <int RT>
-constexpr int kUpU = RT == 4 ? 2 : 4;
-template <int RT>
-constexpr int kDownU = RT == 1 ? 4 : (RT == 2 ? 2 : 1);
+// activation rows; a wave's ring of LDS holds D steps.  (Up: gate/up, Down: down
+// that sums over the experts, Y: down by expert.)
+#ifndef UP_W
+#define UP_W 4
+#define DN_W 8
+#define Y_W 4
+#define UP_KS 16
+#define Y_KS 16
+#define DN_CT 2
+#define Y_CT 4
+#define UP_R 16384
+#define DN_R 16384
+#define Y_R 24576
+#endif
+constexpr int kUpWaves = UP_W, kDownWaves = DN_W, kYWaves = Y_W;
+constexpr int kDownCT = DN_CT, kYCT = Y_CT;
+constexpr int kUpRing = UP_R, kDownRing = DN_R, kYRing = Y_R;  // bytes of a wave's ring
+template <int NW, int RT, int PX, int RING>
+constexpr int kDepth = RING / kSlot<NW, RT, PX> < 1 ? 1 : (RING / kSlot<NW, RT, PX> > 4 ? 4 : RING / kSlot<NW, RT, PX>);
 
 struct FewArgs {
   const int32_t* idx;
@@ -78,6 +82,7 @@ struct FewArgs {
   const bf16_t* cv;
   bf16_t* out;
   int32_t* err_flag;
+  char* table;  // workspace: the route
   // workspace; rows of slots, then the shared expert's rows of tokens
   bf16_t* hhi;
   bf16_t* hlo;
@@ -97,30 +102,40 @@ struct FewArgs {
   float* y;   // rows of slots, then the shared expert's: the expert outputs where down does not join them
 };
 
-// The call's slots sorted by expert, in LDS (sized by the call: route_bytes).
+// The call's slots sorted by expert.
 struct Route {
   int32_t* head;     // active experts, error bits
   int32_t* code;     // S: id of a routed slot, MOE_SLOT_NONE, MOE_SLOT_COPY or -(3 + j)
-  int32_t* first;    // E: slots of the expert, then the end of its run in `slot`
   uint16_t* expert;  // active experts, in id order
   uint16_t* begin;   // the active expert's run in `slot`; one more than experts
   uint16_t* slot;    // S
+  int32_t* first;    // E, while it is built: slots of the expert, then the end of its run
 };
 
-__host__ __device__ inline int route_bytes(int S, int E, int groups) {
-  const int n = 16 + 4 * (S + E) + 2 * (2 * groups + 1 + S);
-  return (n + 15) / 16 * 16;
+// Bytes of a route without `first` (a multiple of 16), and with it.
+__host__ __device__ inline int route_bytes(int S, int groups) {
+  return (16 + 4 * S + 2 * (2 * groups + 1 + S) + 15) / 16 * 16;
+}
+__host__ __device__ inline int route_work_bytes(int S, int E, int groups) {
+  return (route_bytes(S, groups) + 4 * E + 15) / 16 * 16;
 }
 
-__device__ __forceinline__ Route route_at(char* lds, int S, int E, int groups) {
+__device__ __forceinline__ Route route_at(char* p, int S, int groups) {
   Route r;
-  r.head = reinterpret_cast<int32_t*>(lds);
+  r.head = reinterpret_cast<int32_t*>(p);
   r.code = r.head + 4;
-  r.first = r.code + S;
-  r.expert = reinterpret_cast<uint16_t*>(r.first + E);
+  r.expert = reinterpret_cast<uint16_t*>(r.code + S);
   r.begin = r.expert + groups;
   r.slot = r.begin + groups + 1;
+  r.first = reinterpret_cast<int32_t*>(p + route_bytes(S, groups));
   return r;
+}
+
+// A whole route, copied by every thread of the workgroup (THREADS of them).
+template <int THREADS>
+__device__ __forceinline__ void route_copy(char* to, const char* from, int S, int groups) {
+  for (int i = threadIdx.x; i < route_bytes(S, groups) / 16; i += THREADS)
+    reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(from)[i];
 }
 
 // Class of slot k of token t, `ids` its K ids: a routed expert's id, MOE_SLOT_NONE,
@@ -150,7 +165,7 @@ __device__ __forceinline__ int slot_code(const FewArgs& a, const int32_t* ids, i
   return id < a.E + a.Z + a.C ? MOE_SLOT_COPY : -(3 + (id - a.E - a.Z - a.C));
 }
 
-// Fills r (every thread of the workgroup; THREADS of them, at most SLOTS slots).
+// Fills r in LDS (every thread of the workgroup; THREADS of them, at most SLOTS slots).
 // The order of an expert's slots in `slot` is not fixed; no result depends on it.
 template <int THREADS, int SLOTS>
 __device__ void route_lds(const FewArgs& a, const Route& r) {
@@ -215,35 +230,49 @@ __device__ void route_lds(const FewArgs& a, const Route& r) {
   __syncthreads();
 }
 
-// int8: one workgroup per row of codes: the tokens' rows, then (with smooth
-// scales) the slots' rows x_t * smooth[e].  Slots that are not routed to an
-// expert are left out.
-__global__ __launch_bounds__(256) void k_few_quant_x(FewArgs a) {
-  __shared__ float red[4];
-  const int r = blockIdx.x;
-  const float* sm = nullptr;
-  int t = r;
-  if (r >= a.T) {
-    const int s = r - a.T, e = a.idx[s];
-    if (e < 0 || e >= a.E) return;
-    t = s / a.K;
-    sm = a.smooth + (int64_t)e * a.H;
-  } else if (a.smooth && a.Fs == 0) {
-    return;
+// The first workgroup routes the call for the kernels behind it (ROUTE); int8: one
+// more for each row of codes: the tokens' rows, then (with smooth scales) the slots'
+// rows x_t * smooth[e].  Slots that are not routed to an expert are left out.
+template <bool ROUTE, bool I8>
+__global__ __launch_bounds__(256) void k_few_prep(FewArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  if (ROUTE && blockIdx.x == 0) {
+    const Route r = route_at(lds, a.T * a.K, a.groups);
+    route_lds<256, kMaxSlots>(a, r);
+    if (threadIdx.x == 0) *a.err_flag = r.head[1];
+    route_copy<256>(a.table, lds, a.T * a.K, a.groups);
   }
-  const uint4* src = reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H);
-  uint2* dst = reinterpret_cast<uint2*>(a.xq + (int64_t)r * a.H);
-  const float s = quant_row_int8<4>(
-      a.H, red,
-      [&](int64_t i, float* f) {
-        unpack8(src[i], f);
-        if (sm) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) f[q] = __fmul_rn(f[q], sm[8 * i + q]);
-        }
-      },
-      [&](int64_t i, uint2 c) { dst[i] = c; });
-  if (threadIdx.x == 0) a.xs[r] = s;
+  if constexpr (I8) {
+    const int r = (int)blockIdx.x - (ROUTE ? 1 : 0);
+    const float* sm = nullptr;
+    int t = r;
+    if (r < 0) return;
+    if (r >= a.T) {
+      const int s = r - a.T, e = a.idx[s];
+      if (e < 0 || e >= a.E) return;
+      t = s / a.K;
+      sm = a.smooth + (int64_t)e * a.H;
+    } else if (a.smooth && a.Fs == 0) {
+      return;
+    }
+    const uint4* src = reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H);
+    uint2* dst = reinterpret_cast<uint2*>(a.xq + (int64_t)r * a.H);
+    const float s = quant_row_int8<4>(
+        a.H, reinterpret_cast<float*>(lds),
+        [&](int64_t i, float* f) {
+          const uint4 v = src[i];
+          if (sm) {
+            const float4 p = reinterpret_cast<const float4*>(sm)[2 * i], q = reinterpret_cast<const float4*>(sm)[2 * i + 1];
+            unpack8(v, f);
+            f[0] = __fmul_rn(f[0], p.x); f[1] = __fmul_rn(f[1], p.y); f[2] = __fmul_rn(f[2], p.z); f[3] = __fmul_rn(f[3], p.w);
+            f[4] = __fmul_rn(f[4], q.x); f[5] = __fmul_rn(f[5], q.y); f[6] = __fmul_rn(f[6], q.z); f[7] = __fmul_rn(f[7], q.w);
+          } else {
+            unpack8(v, f);
+          }
+        },
+        [&](int64_t i, uint2 c) { dst[i] = c; });
+    if (threadIdx.x == 0) a.xs[r] = s;
+  }
 }
 
 // int8: one workgroup per row of h: the slots' rows, then the shared expert's.
@@ -267,182 +296,197 @@ __global__ __launch_bounds__(256) void k_few_quant_h(FewArgs a) {
   if (threadIdx.x == 0) (sh ? a.shs : a.hs)[row] = s;
 }
 
-// An expert's rows (at most 16 RT) through its 16 CT gate and 16 CT up columns from
-// f0 on.  `slots`: the expert's slots, NULL for the shared expert (row = token).
-// red: 2 RT KB for each wave.
-template <bool I8, int RT, int CT>
+// Offsets of an expert's packed rows in a matrix of `bytes`-byte rows: tile r's row
+// stream_row(j) is row_of(16 r + stream_row(j)); rows past n read zeros.
+template <int RT, int XI, class F>
+__device__ __forceinline__ void row_offsets(int n, int64_t bytes, uint32_t (&xoff)[RT][XI], F row_of) {
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int j = 0; j < XI; ++j) {
+      const int i = 16 * r + stream_row(j);
+      xoff[r][j] = i < n ? (uint32_t)row_of(i) * (uint32_t)bytes : kPastBuffer;
+    }
+}
+
+// G and U of four columns (from f0 on) of one row -> h.
+template <bool I8>
+__device__ __forceinline__ void swiglu_store(const FewArgs& a, bool sh, int slot, int xrow, int64_t wrow, int64_t at,
+                                             const typename MfmaAcc<I8>::type& sg, const typename MfmaAcc<I8>::type& su) {
+  float h[4];
+  float xs = 1.f;
+  if constexpr (I8) xs = a.xs[xrow];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float g = (float)sg[q], u = (float)su[q];
+    if constexpr (I8) {
+      g *= __fmul_rn(xs, (sh ? a.swgs : a.wgs)[wrow + q]);
+      u *= __fmul_rn(xs, (sh ? a.swus : a.wus)[wrow + q]);
+    }
+    h[q] = g / (1.0f + __expf(-g)) * u;
+  }
+  if constexpr (I8) {
+    *reinterpret_cast<float4*>((sh ? a.shf : a.hf) + at) = make_float4(h[0], h[1], h[2], h[3]);
+  } else {
+    float lo[4];
+    uint32_t hi[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      hi[q] = f2bf(h[q]);
+      // nothing below an infinite or NaN high part
+      lo[q] = (hi[q] & 0x7f80u) == 0x7f80u ? 0.f : h[q] - bf2f(hi[q]);
+    }
+    *reinterpret_cast<uint2*>((sh ? a.shhi : a.hhi) + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    *reinterpret_cast<uint2*>((sh ? a.shlo : a.hlo) + at) = make_uint2(pack_bf2(lo[0], lo[1]), pack_bf2(lo[2], lo[3]));
+  }
+}
+
+// An expert's rows (at most 16 RT, XI = 1: 8) through its gate and up columns from f0
+// on, 16 of each for every KS waves, which split the contraction.  `slots`: the
+// expert's slots, NULL for the shared expert (row = token).  lds: the waves' rings.
+template <bool I8, int RT, int XI, int KS>
 __device__ __forceinline__ void gate_up_rows(const FewArgs& a, const uint16_t* slots, int n, int e, int64_t f0,
-                                             float4* red) {
+                                             char* lds) {
   typedef typename MfmaAcc<I8>::type Acc;
-  constexpr int ES = I8 ? 1 : 2, U = kUpU<RT>;
+  constexpr int ES = I8 ? 1 : 2;
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const bool sh = slots == nullptr;
   const int64_t F = sh ? a.Fs : a.F, bytes = a.H * ES;
-  const int64_t wrow = (sh ? 0 : (int64_t)e * F) + f0;
-  const char* w[2 * CT];
-  uint32_t woff[2 * CT];
+  f0 += 16 * (wave / KS);
+  const bool in = f0 < F;  // (KS < waves: the last workgroup's waves may have no columns)
+  const int64_t wrow = (sh ? 0 : (int64_t)e * F) + (in ? f0 : 0);
+  const i32x4_t w[2] = {buffer_of(static_cast<const char*>(sh ? a.swg : a.wg) + wrow * bytes, 16 * bytes),
+                        buffer_of(static_cast<const char*>(sh ? a.swu : a.wu) + wrow * bytes, 16 * bytes)};
+  auto x_row = [&](int s) { return sh ? s : (I8 && a.smooth ? a.T + s : s / a.K); };
+  const i32x4_t x[1] = {I8 ? buffer_of(a.xq, (a.T + (a.smooth ? a.T * a.K : 0)) * bytes) : buffer_of(a.x, a.T * bytes)};
+  uint32_t xoff[RT][XI];
+  row_offsets<RT, XI>(n, bytes, xoff, [&](int i) { return x_row(sh ? i : slots[i]); });
+  Acc acc[2][RT];
 #pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    // a column tile past F reads the first one
-    const int64_t at = (wrow + (f0 + 16 * c < F ? 16 * c : 0)) * bytes;
-    w[2 * c] = static_cast<const char*>(sh ? a.swg : a.wg) + at;
-    w[2 * c + 1] = static_cast<const char*>(sh ? a.swu : a.wu) + at;
-    woff[2 * c] = woff[2 * c + 1] = (uint32_t)(lane % 16) * (uint32_t)bytes + 16 * (lane / 16);
-  }
-  const char* x[1] = {I8 ? reinterpret_cast<const char*>(a.xq) : reinterpret_cast<const char*>(a.x)};
-  uint32_t xoff[RT];  // at most 64 rows of 2^21 bytes, or 1088 of 2^17
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    int i = 16 * r + lane % 16;
-    if (i >= n) i = n - 1;
-    const int s = sh ? i : slots[i];
-    const int row = sh ? s : (I8 && a.smooth ? a.T + s : s / a.K);
-    xoff[r] = (uint32_t)row * (uint32_t)bytes + 16 * (lane / 16);
-  }
-  Acc acc[2 * CT][RT];
-#pragma unroll
-  for (int g = 0; g < 2 * CT; ++g)
+  for (int g = 0; g < 2; ++g)
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[g][r] = Acc{0, 0, 0, 0};
-  const int ns = stream_steps(bytes);
-  stream_mfma<I8, 2 * CT, RT, 1, U>(w, woff, x, xoff, bytes, ns * wave / kUpWaves, ns * (wave + 1) / kUpWaves, acc);
+  const int ns = in ? stream_steps(bytes) : 0, part = wave % KS;
+  stream_mfma<I8, 2, RT, 1, XI, kDepth<2, RT, 1, kUpRing>>(w, x, xoff, bytes, ns * part / KS, ns * (part + 1) / KS,
+                                                          lds + wave * kUpRing, acc);
+  const int64_t c = 4 * (lane / 16);
+  auto finish = [&](int r, const Acc& g, const Acc& u) {
+    const int i = 16 * r + lane % 16;
+    if (!in || i >= n) return;
+    const int slot = sh ? i : slots[i];
+    swiglu_store<I8>(a, sh, slot, x_row(slot), wrow + c, (int64_t)slot * F + f0 + c, g, u);
+  };
+  if constexpr (KS == 1) {
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    if (ct > 0) __syncthreads();
+    for (int r = 0; r < RT; ++r) finish(r, acc[0][r], acc[1][r]);
+  } else {
+    static_assert(KS == kUpWaves && RT <= KS && 2 * RT * 1024 <= kUpRing, "parts");
+    // the waves' parts meet in their rings' place
+    float4* red = reinterpret_cast<float4*>(lds);
 #pragma unroll
     for (int g = 0; g < 2; ++g)
 #pragma unroll
       for (int r = 0; r < RT; ++r)
-        red[((wave * 2 + g) * RT + r) * kWave + lane] = __builtin_bit_cast(float4, acc[2 * ct + g][r]);
+        red[wave * (kUpRing / 16) + (g * RT + r) * kWave + lane] = __builtin_bit_cast(float4, acc[g][r]);
     __syncthreads();
-    const int r = wave;
-    const int i = 16 * r + lane % 16;
-    if (r >= RT || i >= n || f0 + 16 * ct >= F) continue;
-    Acc s[2];
+    if (wave < RT) {
+      Acc s[2];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      s[g] = Acc{0, 0, 0, 0};
+      for (int g = 0; g < 2; ++g) {
+        s[g] = Acc{0, 0, 0, 0};
 #pragma unroll
-      for (int v = 0; v < kUpWaves; ++v)
-        s[g] += __builtin_bit_cast(Acc, red[((v * 2 + g) * RT + r) * kWave + lane]);
-    }
-    const int slot = sh ? i : slots[i];
-    const int64_t c = 16 * ct + 4 * (lane / 16), at = (int64_t)slot * F + f0 + c;
-    float h[4];
-    float xs = 1.f;
-    if constexpr (I8) xs = a.xs[sh ? slot : (a.smooth ? a.T + slot : slot / a.K)];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float g = (float)s[0][q], u = (float)s[1][q];
-      if constexpr (I8) {
-        g *= __fmul_rn(xs, (sh ? a.swgs : a.wgs)[wrow + c + q]);
-        u *= __fmul_rn(xs, (sh ? a.swus : a.wus)[wrow + c + q]);
+        for (int v = 0; v < KS; ++v)
+          s[g] += __builtin_bit_cast(Acc, red[v * (kUpRing / 16) + (g * RT + wave) * kWave + lane]);
       }
-      h[q] = g / (1.0f + __expf(-g)) * u;
-    }
-    if constexpr (I8) {
-      *reinterpret_cast<float4*>((sh ? a.shf : a.hf) + at) = make_float4(h[0], h[1], h[2], h[3]);
-    } else {
-      float lo[4];
-      uint32_t hi[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        hi[q] = f2bf(h[q]);
-        // nothing below an infinite or NaN high part
-        lo[q] = (hi[q] & 0x7f80u) == 0x7f80u ? 0.f : h[q] - bf2f(hi[q]);
-      }
-      *reinterpret_cast<uint2*>((sh ? a.shhi : a.hhi) + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-      *reinterpret_cast<uint2*>((sh ? a.shlo : a.hlo) + at) = make_uint2(pack_bf2(lo[0], lo[1]), pack_bf2(lo[2], lo[3]));
+      finish(wave, s[0], s[1]);
     }
   }
 }
 
-// RTM: row tiles that T tokens may need (1, 2 or 4)
-template <bool I8, int RTM, int CT>
-__global__ __launch_bounds__(kUpWaves* kWave, kUpOcc<RTM>) void k_few_gate_up(FewArgs a) {
+// RTM: row tiles that T tokens may need (1, 2 or 4).  RTM = 1 routes for itself, and
+// the first workgroup for the kernels behind it.
+template <bool I8, int RTM, int KS>
+__global__ __launch_bounds__(kUpWaves* kWave, 2) void k_few_gate_up(FewArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  const Route route = route_at(lds, a.T * a.K, a.E, a.groups);
-  float4* red = reinterpret_cast<float4*>(lds + route_bytes(a.T * a.K, a.E, a.groups));
-  route_lds<kUpWaves * kWave, RTM * 256>(a, route);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err_flag = route.head[1];
-  const int tiles = (int)((a.F + 16 * CT - 1) / (16 * CT));
-  const int routed = uniform(route.head[0]) * tiles, items = routed + (int)((a.Fs + 16 * CT - 1) / (16 * CT));
-  const int it = blockIdx.x;
-  if (it < items) {
-    const bool sh = it >= routed;
-    const int g = sh ? 0 : it / tiles;
-    const int b = sh ? 0 : uniform(route.begin[g]);
-    const uint16_t* slots = sh ? nullptr : route.slot + b;
-    const int n = sh ? a.T : uniform(route.begin[g + 1]) - b, e = sh ? 0 : uniform(route.expert[g]);
-    const int64_t f0 = (int64_t)(sh ? it - routed : it - g * tiles) * (16 * CT);
-    const int rt = (n + 15) / 16;
-    if (RTM > 2 && rt > 2) gate_up_rows<I8, RTM, CT>(a, slots, n, e, f0, red);
-    else if (RTM > 1 && rt > 1) gate_up_rows<I8, RTM < 2 ? 1 : 2, CT>(a, slots, n, e, f0, red);
-    else gate_up_rows<I8, 1, CT>(a, slots, n, e, f0, red);
+  constexpr int COLS = 16 * kUpWaves / KS;
+  const int S = a.T * a.K;
+  const Route route = route_at(RTM == 1 ? lds : a.table, S, a.groups);
+  char* rings = lds + (RTM == 1 ? route_work_bytes(S, a.E, a.groups) : 0);
+  if constexpr (RTM == 1) {
+    route_lds<kUpWaves * kWave, 256>(a, route);
+    if (blockIdx.x == 0) {
+      if (threadIdx.x == 0) *a.err_flag = route.head[1];
+      route_copy<kUpWaves * kWave>(a.table, lds, S, a.groups);
+    }
   }
+  const int tiles = (int)((a.F + COLS - 1) / COLS);
+  const int routed = uniform(route.head[0]) * tiles, items = routed + (int)((a.Fs + COLS - 1) / COLS);
+  const int it = blockIdx.x;
+  if (it >= items) return;
+  const bool sh = it >= routed;
+  const int g = sh ? 0 : it / tiles;
+  const int b = sh ? 0 : uniform(route.begin[g]);
+  const uint16_t* slots = sh ? nullptr : route.slot + b;
+  const int n = sh ? a.T : uniform(route.begin[g + 1]) - b, e = sh ? 0 : uniform(route.expert[g]);
+  const int64_t f0 = (int64_t)(sh ? it - routed : it - g * tiles) * COLS;
+  const int rt = (n + 15) / 16;
+  if (RTM > 2 && rt > 2) gate_up_rows<I8, RTM, 2, KS>(a, slots, n, e, f0, rings);
+  else if (RTM > 1 && rt > 1) gate_up_rows<I8, RTM < 2 ? 1 : 2, 2, KS>(a, slots, n, e, f0, rings);
+  else if (n > 8) gate_up_rows<I8, 1, 2, KS>(a, slots, n, e, f0, rings);
+  else gate_up_rows<I8, 1, 1, KS>(a, slots, n, e, f0, rings);
 }
 
-// One expert's packed rows (at most 16 RT) through 16 CT columns of H from c0 on,
-// steps [s0, s1) of F.  slot[r]: the lane's row (slot, or the shared expert's
-// token), -1 past the last.
-template <bool I8, int RT, int CT, int U>
+// One expert's packed rows (at most 16 RT, XI = 1: 8) through 16 CT columns of H from
+// c0 on, steps [s0, s1) of F.
+template <bool I8, int RT, int XI, int CT, int RING>
 __device__ __forceinline__ void down_stream(const FewArgs& a, const uint16_t* slots, int n, int e, int64_t c0, int s0,
-                                            int s1, int (&slot)[RT], typename MfmaAcc<I8>::type (&acc)[CT][RT]) {
+                                            int s1, char* ring, typename MfmaAcc<I8>::type (&acc)[CT][RT]) {
   constexpr int ES = I8 ? 1 : 2, PX = I8 ? 1 : 2;
-  const int lane = threadIdx.x % kWave;
   const bool sh = slots == nullptr;
-  const int64_t F = sh ? a.Fs : a.F, bytes = F * ES;
-  const int64_t wrow = sh ? 0 : (int64_t)e * a.H;
-  const char* w[CT];
-  uint32_t woff[CT];
+  const int64_t bytes = (sh ? a.Fs : a.F) * ES, rows = sh ? a.T : (int64_t)a.T * a.K;
+  i32x4_t w[CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
-    // a column past H reads the last one
-    const int64_t left = a.H - 1 - c0, col = 16 * c + lane % 16;
-    w[c] = static_cast<const char*>(sh ? a.swd : a.wd) + (wrow + c0) * bytes;
-    woff[c] = (uint32_t)(col < left ? col : left) * (uint32_t)bytes + 16 * (lane / 16);
+    // columns past H lie past the buffer; a column tile past H reads the first one
+    const int64_t col = c0 + (c0 + 16 * c < a.H ? 16 * c : 0), left = a.H - col;
+    w[c] = buffer_of(static_cast<const char*>(sh ? a.swd : a.wd) + ((sh ? 0 : (int64_t)e * a.H) + col) * bytes,
+                     (left < 16 ? left : 16) * bytes);
   }
-  const char* x[PX];
-  x[0] = I8 ? reinterpret_cast<const char*>(sh ? a.shq : a.hq) : reinterpret_cast<const char*>(sh ? a.shhi : a.hhi);
-  if constexpr (!I8) x[1] = reinterpret_cast<const char*>(sh ? a.shlo : a.hlo);
-  uint32_t xoff[RT];  // at most 1024 rows of 2^21 bytes
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    int i = 16 * r + lane % 16;
-    const bool in = i < n;
-    if (!in) i = n - 1;
-    const int s = sh ? i : slots[i];
-    slot[r] = in ? s : -1;
-    xoff[r] = (uint32_t)s * (uint32_t)bytes + 16 * (lane / 16);
-  }
+  i32x4_t x[PX];
+  x[0] = buffer_of(I8 ? static_cast<const void*>(sh ? a.shq : a.hq) : static_cast<const void*>(sh ? a.shhi : a.hhi), rows * bytes);
+  if constexpr (!I8) x[1] = buffer_of(sh ? a.shlo : a.hlo, rows * bytes);
+  uint32_t xoff[RT][XI];
+  row_offsets<RT, XI>(n, bytes, xoff, [&](int i) { return sh ? i : (int)slots[i]; });
 #pragma unroll
   for (int c = 0; c < CT; ++c)
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[c][r] = typename MfmaAcc<I8>::type{0, 0, 0, 0};
-  stream_mfma<I8, CT, RT, PX, U>(w, woff, x, xoff, bytes, s0, s1, acc);
+  stream_mfma<I8, CT, RT, PX, XI, kDepth<CT, RT, PX, RING>>(w, x, xoff, bytes, s0, s1, ring, acc);
 }
 
 // down_stream of at most 16 rows, the weighted results added to the wave's output
 // tile `o` (T rows of 16 CT columns).
-template <bool I8, int CT>
+template <bool I8, int XI, int CT>
 __device__ __forceinline__ void down_rows(const FewArgs& a, const uint16_t* slots, int n, int e, int64_t c0, int s0,
-                                          int s1, float (*o)[16 * CT]) {
+                                          int s1, char* ring, float (*o)[16 * CT]) {
   const int lane = threadIdx.x % kWave;
   const bool sh = slots == nullptr;
   const int64_t wrow = sh ? 0 : (int64_t)e * a.H;
+  const int row = lane % 16 < n ? (sh ? lane % 16 : slots[lane % 16]) : -1;
+  float wt = 1.f, hs = 1.f;
+  if (row >= 0) {
+    if (!sh) wt = a.w[row];
+    if constexpr (I8) hs = (sh ? a.shs : a.hs)[row];
+  }
   typename MfmaAcc<I8>::type acc[CT][1];
-  int slot[1];
-  down_stream<I8, 1, CT, kDownU<1>>(a, slots, n, e, c0, s0, s1, slot, acc);
-  if (slot[0] >= 0) {
-    const float wt = sh ? 1.0f : a.w[slot[0]];
-    float* row = o[sh ? slot[0] : slot[0] / a.K];
-    float hs = 1.f;
-    if constexpr (I8) hs = (sh ? a.shs : a.hs)[slot[0]];
+  down_stream<I8, 1, XI, CT, kDownRing>(a, slots, n, e, c0, s0, s1, ring, acc);
+  if (row >= 0) {
+    float* out = o[sh ? row : row / a.K];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       const int64_t c = c0 + 16 * ct + 4 * (lane / 16);
       if (c >= a.H) continue;  // H is a multiple of 8: four columns are in or out together
-      float4* p = reinterpret_cast<float4*>(row + 16 * ct + 4 * (lane / 16));
+      float4* p = reinterpret_cast<float4*>(out + 16 * ct + 4 * (lane / 16));
       float4 v = *p;
       float y[4];
 #pragma unroll
@@ -475,14 +519,16 @@ __device__ __forceinline__ void few_finish(const FewArgs& a, const int32_t* code
 
 // dynamic LDS: the routing, then kDownWaves output tiles of T rows x 16 CT columns
 template <bool I8, int CT>
-__global__ __launch_bounds__(kDownWaves* kWave, kDownOcc) void k_few_down(FewArgs a) {
+__global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(FewArgs a) {
   constexpr int ES = I8 ? 1 : 2, COLS = 16 * CT;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  const Route route = route_at(lds, a.T * a.K, a.E, a.groups);
-  float* tiles = reinterpret_cast<float*>(lds + route_bytes(a.T * a.K, a.E, a.groups));
+  const Route route = route_at(lds, a.T * a.K, a.groups);
+  char* rings = lds + route_bytes(a.T * a.K, a.groups);
+  float* tiles = reinterpret_cast<float*>(rings + kDownWaves * kDownRing);
   const int wave = uniform(threadIdx.x / kWave);
   for (int i = threadIdx.x; i < kDownWaves * a.T * COLS; i += kDownWaves * kWave) tiles[i] = 0.f;
-  route_lds<kDownWaves * kWave, 256>(a, route);
+  route_copy<kDownWaves * kWave>(lds, a.table, a.T * a.K, a.groups);
+  __syncthreads();
   const int64_t c0 = (int64_t)blockIdx.x * COLS;
   float(*o)[COLS] = reinterpret_cast<float(*)[COLS]>(tiles) + wave * a.T;
   const int per = stream_steps(a.F * ES), routed = uniform(route.head[0]) * per;
@@ -499,7 +545,8 @@ __global__ __launch_bounds__(kDownWaves* kWave, kDownOcc) void k_few_down(FewArg
     const int e = sh ? 0 : uniform(route.expert[g]);
     const uint16_t* slots = sh ? nullptr : route.slot + b;
     u += s1 - s0;
-    down_rows<I8, CT>(a, slots, n, e, c0, s0, s1, o);
+    if (n > 8) down_rows<I8, 2, CT>(a, slots, n, e, c0, s0, s1, rings + wave * kDownRing, o);
+    else down_rows<I8, 1, CT>(a, slots, n, e, c0, s0, s1, rings + wave * kDownRing, o);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < a.T * COLS; i += kDownWaves * kWave) {
@@ -513,31 +560,24 @@ __global__ __launch_bounds__(kDownWaves* kWave, kDownOcc) void k_few_down(FewArg
   }
 }
 
-// One expert's rows (at most 16 RT) through 16 CT columns of H from c0 on: rows of y.
-// red: RT KB for each wave.
-template <bool I8, int RT, int CT>
+// One expert's rows (at most 16 RT) through columns of H from c0 on, 16 CT for every
+// KS waves, which split the contraction: rows of y.  lds: the waves' rings.
+template <bool I8, int RT, int XI, int CT, int KS>
 __device__ __forceinline__ void down_y_rows(const FewArgs& a, const uint16_t* slots, int n, int e, int64_t c0,
-                                            float4* red) {
+                                            char* lds) {
   typedef typename MfmaAcc<I8>::type Acc;
-  constexpr int U = kDownU<RT>;
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const bool sh = slots == nullptr;
+  c0 += 16 * CT * (wave / KS);
+  const bool in = c0 < a.H;
   Acc acc[CT][RT];
-  int slot[RT];
-  const int ns = stream_steps((sh ? a.Fs : a.F) * (I8 ? 1 : 2));
-  down_stream<I8, RT, CT, U>(a, slots, n, e, c0, ns * wave / kYWaves, ns * (wave + 1) / kYWaves, slot, acc);
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    if (ct > 0) __syncthreads();
-#pragma unroll
-    for (int r = 0; r < RT; ++r) red[(wave * RT + r) * kWave + lane] = __builtin_bit_cast(float4, acc[ct][r]);
-    __syncthreads();
-    const int i = 16 * wave + lane % 16;
+  const int ns = in ? stream_steps((sh ? a.Fs : a.F) * (I8 ? 1 : 2)) : 0, part = wave % KS;
+  down_stream<I8, RT, XI, CT, kYRing>(a, slots, n, e, in ? c0 : 0, ns * part / KS, ns * (part + 1) / KS,
+                                      lds + wave * kYRing, acc);
+  auto finish = [&](int ct, int r, const Acc& s) {
+    const int i = 16 * r + lane % 16;
     const int64_t c = c0 + 16 * ct + 4 * (lane / 16);
-    if (wave >= RT || i >= n || c >= a.H) continue;
-    Acc s = {0, 0, 0, 0};
-#pragma unroll
-    for (int v = 0; v < kYWaves; ++v) s += __builtin_bit_cast(Acc, red[(v * RT + wave) * kWave + lane]);
+    if (i >= n || c >= a.H) return;
     const int64_t row = sh ? i : slots[i];
     float y[4];
     float hs = 1.f;
@@ -548,52 +588,72 @@ __device__ __forceinline__ void down_y_rows(const FewArgs& a, const uint16_t* sl
       if constexpr (I8) y[q] *= __fmul_rn(hs, (sh ? a.swds : a.wds + (int64_t)e * a.H)[c + q]);
     }
     *reinterpret_cast<float4*>(a.y + (sh ? (int64_t)a.T * a.K + row : row) * a.H + c) = make_float4(y[0], y[1], y[2], y[3]);
+  };
+  if constexpr (KS == 1) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) finish(ct, r, acc[ct][r]);
+  } else {
+    static_assert(KS == kYWaves && CT * RT * 1024 <= kYRing, "parts");
+    float4* red = reinterpret_cast<float4*>(lds);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        red[wave * (kYRing / 16) + (ct * RT + r) * kWave + lane] = __builtin_bit_cast(float4, acc[ct][r]);
+    __syncthreads();
+    for (int q = wave; q < CT * RT; q += KS) {
+      Acc s = {0, 0, 0, 0};
+#pragma unroll
+      for (int v = 0; v < KS; ++v) s += __builtin_bit_cast(Acc, red[v * (kYRing / 16) + q * kWave + lane]);
+      finish(q / RT, q % RT, s);
+    }
   }
 }
 
-// larger batches: a workgroup per (active expert, 16 CT columns of H)
-template <bool I8, int RTM, int CT>
-__global__ __launch_bounds__(kYWaves* kWave, kDownOcc) void k_few_down_y(FewArgs a) {
+// larger batches: a workgroup per (active expert, columns of H)
+template <bool I8, int RTM, int CT, int KS>
+__global__ __launch_bounds__(kYWaves* kWave, 2) void k_few_down_y(FewArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  const Route route = route_at(lds, a.T * a.K, a.E, a.groups);
-  float4* red = reinterpret_cast<float4*>(lds + route_bytes(a.T * a.K, a.E, a.groups));
-  route_lds<kYWaves * kWave, RTM * 256>(a, route);
-  const int tiles = (int)((a.H + 16 * CT - 1) / (16 * CT));
+  constexpr int COLS = 16 * CT * kYWaves / KS;
+  const Route route = route_at(a.table, a.T * a.K, a.groups);
+  const int tiles = (int)((a.H + COLS - 1) / COLS);
   const int routed = uniform(route.head[0]) * tiles, items = routed + (a.Fs > 0 ? tiles : 0);
   const int it = blockIdx.x;
-  if (it < items) {
-    const bool sh = it >= routed;
-    const int g = it / tiles;
-    const int64_t c0 = (int64_t)(it - g * tiles) * (16 * CT);
-    const int b = sh ? 0 : uniform(route.begin[g]);
-    const uint16_t* slots = sh ? nullptr : route.slot + b;
-    const int n = sh ? a.T : uniform(route.begin[g + 1]) - b, e = sh ? 0 : uniform(route.expert[g]);
-    const int rt = (n + 15) / 16;
-    if (RTM > 2 && rt > 2) down_y_rows<I8, RTM, CT>(a, slots, n, e, c0, red);
-    else if (RTM > 1 && rt > 1) down_y_rows<I8, RTM < 2 ? 1 : 2, CT>(a, slots, n, e, c0, red);
-    else down_y_rows<I8, 1, CT>(a, slots, n, e, c0, red);
-  }
+  if (it >= items) return;
+  const bool sh = it >= routed;
+  const int g = it / tiles;
+  const int64_t c0 = (int64_t)(it - g * tiles) * COLS;
+  const int b = sh ? 0 : uniform(route.begin[g]);
+  const uint16_t* slots = sh ? nullptr : route.slot + b;
+  const int n = sh ? a.T : uniform(route.begin[g + 1]) - b, e = sh ? 0 : uniform(route.expert[g]);
+  const int rt = (n + 15) / 16;
+  if (RTM > 2 && rt > 2) down_y_rows<I8, RTM, 2, CT, KS>(a, slots, n, e, c0, lds);
+  else if (RTM > 1 && rt > 1) down_y_rows<I8, RTM < 2 ? 1 : 2, 2, CT, KS>(a, slots, n, e, c0, lds);
+  else if (n > 8) down_y_rows<I8, 1, 2, CT, KS>(a, slots, n, e, c0, lds);
+  else down_y_rows<I8, 1, 1, CT, KS>(a, slots, n, e, c0, lds);
 }
 
 // four outputs of one token per thread: the weighted sum of y over its slots in k
-// order, the shared expert's row and the shared term
+// order, the shared expert's row, the special experts and the shared term
+template <int KMAX>
 __global__ __launch_bounds__(256) void k_few_join(FewArgs a) {
-  __shared__ int32_t code[16];
   const int t = blockIdx.y;
-  if (threadIdx.x < a.K) {
-    uint32_t err = 0;
-    code[threadIdx.x] = slot_code(a, a.idx + t * a.K, t, threadIdx.x, err);
-  }
-  __syncthreads();
+  const int32_t* code = route_at(a.table, a.T * a.K, a.groups).code + t * a.K;
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (c >= a.H) return;
+  float4 y[KMAX + 1];
+#pragma unroll
+  for (int k = 0; k < KMAX; ++k)
+    if (k < a.K && code[k] >= 0) y[k] = *reinterpret_cast<const float4*>(a.y + ((int64_t)t * a.K + k) * a.H + c);
+  if (a.Fs > 0) y[KMAX] = *reinterpret_cast<const float4*>(a.y + ((int64_t)a.T * a.K + t) * a.H + c);
   float v[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k <= a.K; ++k) {
-    const bool sh = k == a.K;
-    if (sh ? a.Fs == 0 : code[k] < 0) continue;
-    const float wt = sh ? 1.f : a.w[t * a.K + k];
-    const float4 y = *reinterpret_cast<const float4*>(a.y + (sh ? (int64_t)a.T * a.K + t : (int64_t)t * a.K + k) * a.H + c);
-    v[0] += wt * y.x; v[1] += wt * y.y; v[2] += wt * y.z; v[3] += wt * y.w;
+#pragma unroll
+  for (int k = 0; k <= KMAX; ++k) {
+    if (k < KMAX ? k >= a.K || code[k] < 0 : a.Fs == 0) continue;
+    const float wt = k < KMAX ? a.w[t * a.K + k] : 1.f;
+    v[0] += wt * y[k].x; v[1] += wt * y[k].y; v[2] += wt * y[k].z; v[3] += wt * y[k].w;
   }
 #pragma unroll
   for (int q = 0; q < 4; ++q) few_finish(a, code, t, c + q, v[q]);
@@ -613,6 +673,7 @@ size_t few_layout(FewArgs& a, bool i8, char* base) {
     n += up256(bytes);
     return p;
   };
+  a.table = take(route_bytes((int)S, a.groups));
   if (i8) {
     a.xq = reinterpret_cast<int8_t*>(take((T + S) * H));
     a.xs = reinterpret_cast<float*>(take((T + S) * 4));
@@ -641,6 +702,8 @@ moe_status check_few(const moe_shape* s, int64_t shared_F, bool i8) {
   if (i8 && (s->H > 131072 || s->F > 131072 || shared_F > 131072)) return MOE_ERR_UNSUPPORTED;
   if (s->comm_quant_mode != 0) return MOE_ERR_UNSUPPORTED;
   if (s->T > kMaxTokens) return MOE_ERR_UNSUPPORTED;
+  // the rows of h are addressed with 31-bit offsets
+  if (s->T * s->K * s->F * 2 >= 0x7ffffff0) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -650,25 +713,57 @@ struct FewWeight {
   const float* scales;
 };
 
+// More than 64 KB of dynamic LDS has to be asked for.
+template <class F>
+bool lds_allowed(F k, int bytes) {
+  return bytes <= 65536 || hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                               bytes) == hipSuccess;
+}
+
+template <bool I8, int RTM, int KS>
+bool launch_up(const FewArgs& a, hipStream_t strm) {
+  constexpr int COLS = 16 * kUpWaves / KS;
+  const int lds = (RTM == 1 ? route_work_bytes(a.T * a.K, a.E, a.groups) : 0) + kUpWaves * kUpRing;
+  const int64_t n = a.groups * ((a.F + COLS - 1) / COLS) + (a.Fs + COLS - 1) / COLS;
+  if (!lds_allowed(k_few_gate_up<I8, RTM, KS>, lds)) return false;
+  hipLaunchKernelGGL((k_few_gate_up<I8, RTM, KS>), dim3((unsigned)n), dim3(kUpWaves * kWave), lds, strm, a);
+  return true;
+}
+
+template <bool I8, int RTM, int KS>
+bool launch_y(const FewArgs& a, hipStream_t strm) {
+  constexpr int COLS = 16 * kYCT * kYWaves / KS, lds = kYWaves * kYRing;
+  const int64_t n = (a.groups + (a.Fs > 0)) * ((a.H + COLS - 1) / COLS);
+  if (!lds_allowed(k_few_down_y<I8, RTM, kYCT, KS>, lds)) return false;
+  hipLaunchKernelGGL((k_few_down_y<I8, RTM, kYCT, KS>), dim3((unsigned)n), dim3(kYWaves * kWave), lds, strm, a);
+  const dim3 grid((unsigned)((a.H + 1023) / 1024), (unsigned)a.T);
+  if (a.K <= 8) hipLaunchKernelGGL(k_few_join<8>, grid, dim3(256), 0, strm, a);
+  else hipLaunchKernelGGL(k_few_join<16>, grid, dim3(256), 0, strm, a);
+  return true;
+}
+
 template <bool I8, int RTM>
 moe_status few_launch(FewArgs& a, hipStream_t strm) {
-  constexpr int UC = kUpCT<RTM>, DC = kDownCT<RTM>;
-  const int S = a.T * a.K, rb = route_bytes(S, a.E, a.groups);
-  auto tiles = [](int64_t n, int ct) { return (n + 16 * ct - 1) / (16 * ct); };
-  const int64_t up = a.groups * tiles(a.F, UC) + tiles(a.Fs, UC);
-  if (up > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL((k_few_gate_up<I8, RTM, UC>), dim3((unsigned)up), dim3(kUpWaves * kWave),
-                     rb + kUpWaves * 2 * RTM * kWave * 16, strm, a);
+  constexpr int ES = I8 ? 1 : 2;
+  constexpr bool ROUTE = RTM > 1;
+  const int S = a.T * a.K, rb = route_bytes(S, a.groups), rw = route_work_bytes(S, a.E, a.groups);
+  if (ROUTE || I8)
+    hipLaunchKernelGGL((k_few_prep<ROUTE, I8>), dim3((ROUTE ? 1 : 0) + (I8 ? a.T + (a.smooth ? S : 0) : 0)), dim3(256),
+                       ROUTE ? rw : 16, strm, a);
+  // waves split a long contraction; a short one is a wave's own
+  bool ok = stream_steps(a.H * ES) < UP_KS ? launch_up<I8, RTM, 1>(a, strm) : launch_up<I8, RTM, kUpWaves>(a, strm);
   if (I8) hipLaunchKernelGGL(k_few_quant_h, dim3(S + (a.Fs ? a.T : 0)), dim3(256), 0, strm, a);
   if constexpr (RTM == 1) {
-    hipLaunchKernelGGL((k_few_down<I8, DC>), dim3((unsigned)tiles(a.H, DC)), dim3(kDownWaves * kWave),
-                       rb + kDownWaves * a.T * 16 * DC * 4, strm, a);
+    constexpr auto kDown = k_few_down<I8, kDownCT>;
+    const int lds = rb + kDownWaves * (kDownRing + a.T * 16 * kDownCT * 4);
+    ok = ok && lds_allowed(kDown, lds);
+    if (ok)
+      hipLaunchKernelGGL(kDown, dim3((unsigned)((a.H + 16 * kDownCT - 1) / (16 * kDownCT))), dim3(kDownWaves * kWave), lds,
+                         strm, a);
   } else {
-    hipLaunchKernelGGL((k_few_down_y<I8, RTM, DC>), dim3((unsigned)(a.groups + (a.Fs > 0)) * tiles(a.H, DC)),
-                       dim3(kYWaves * kWave), rb + kYWaves * RTM * kWave * 16, strm, a);
-    hipLaunchKernelGGL(k_few_join, dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.T), dim3(256), 0, strm, a);
+    ok = ok && (stream_steps(a.F * ES) < Y_KS ? launch_y<I8, RTM, 1>(a, strm) : launch_y<I8, RTM, kYWaves>(a, strm));
   }
-  return launch_status();
+  return ok ? launch_status() : MOE_ERR_HIP;
 }
 
 // The kernels read and write vectors of up to 16 bytes.
@@ -720,16 +815,15 @@ moe_status few_impl(const moe_shape* s, bool i8, const void* x, const int32_t* t
   a.groups = S < a.E ? S : a.E;
   const size_t need = few_layout(a, i8, static_cast<char*>(workspace));
   if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  // gate/up tiles
+  if ((int64_t)a.groups * (a.F / 16) + Fs / 16 > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   if (S == 0) {
     // the error flag alone
-    a.Fs = 0;
-    hipLaunchKernelGGL((k_few_gate_up<false, 1, kUpCT<1>>), dim3(1), dim3(kUpWaves * kWave), route_bytes(0, a.E, 0), strm, a);
+    hipLaunchKernelGGL((k_few_prep<true, false>), dim3(1), dim3(256), route_work_bytes(0, a.E, 0), strm, a);
     return launch_status();
   }
-  if (i8) {
-    hipLaunchKernelGGL(k_few_quant_x, dim3(a.T + (smooth ? S : 0)), dim3(256), 0, strm, a);
+  if (i8)
     return a.T <= 16 ? few_launch<true, 1>(a, strm) : (a.T <= 32 ? few_launch<true, 2>(a, strm) : few_launch<true, 4>(a, strm));
-  }
   return a.T <= 16 ? few_launch<false, 1>(a, strm) : (a.T <= 32 ? few_launch<false, 2>(a, strm) : few_launch<false, 4>(a, strm));
 }
 
@@ -745,6 +839,7 @@ extern "C" moe_status moe_few_tokens_workspace_size(const moe_shape* s, int64_t 
   if (!bytes) return MOE_ERR_NULL_ARG;
   FewArgs a = {};
   a.T = (int)s->T; a.K = s->K; a.H = s->H; a.F = s->F; a.Fs = shared_F;
+  a.groups = a.T * a.K < s->num_experts ? a.T * a.K : s->num_experts;
   *bytes = few_layout(a, int8 == 1, nullptr);
   return MOE_OK;
 }

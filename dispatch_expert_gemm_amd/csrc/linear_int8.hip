@@ -7,12 +7,12 @@
 // split the contraction, each streaming its part of the 16 weight rows from
 // memory into the matrix cores (stream_mfma.hpp); the int32 partial sums meet in
 // LDS, where their order does not matter.  Bound: HBM, N * K bytes of weights.
+#include <type_traits>
+
 #include "stream_mfma.hpp"
 
 namespace moe {
 namespace {
-
-constexpr int kRowWaves = 8;
 
 struct LinArgs {
   const int8_t* xq;
@@ -36,44 +36,275 @@ __global__ __launch_bounds__(256) void k_quant_x(const uint4* __restrict__ x, in
   if (threadIdx.x == 0) scales[r] = s;
 }
 
-template <int RT>
-__global__ __launch_bounds__(kRowWaves* kWave) void k_linear_rows(LinArgs a) {
-  __shared__ i32x4_t red[kRowWaves][RT][kWave];
+#ifndef R_W
+#define R_W 8
+#define R_CT 1
+#define R_D 2
+#endif
+// One workgroup per (16 CT output columns, 16 RT rows): W waves split the
+// contraction and their int32 sums meet in LDS.
+template <int RT, int CT, int XI, int D, int W>
+__global__ __launch_bounds__(W* kWave, 2) void k_linear_rows(LinArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (RT * 16);
-  // a column or row past the end reads the last one
-  const uint32_t K = (uint32_t)a.K, nl = (uint32_t)(a.N - 1 - n0), ml = (uint32_t)(a.M - 1 - m0);
-  const char* w[1] = {reinterpret_cast<const char*>(a.wq) + n0 * a.K};
-  const char* x[1] = {reinterpret_cast<const char*>(a.xq) + m0 * a.K};
-  const uint32_t row = lane % 16, chunk = 16 * (lane / 16);
-  const uint32_t woff[1] = {(row < nl ? row : nl) * K + chunk};
-  uint32_t xoff[RT];
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * CT), m0 = (int64_t)blockIdx.y * (RT * 16);
+  i32x4_t w[CT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const uint32_t m = 16 * r + row;
-    xoff[r] = (m < ml ? m : ml) * K + chunk;
+  for (int c = 0; c < CT; ++c) {
+    // columns past N lie past the buffer; a column tile past N reads the first one
+    const int64_t col = n0 + (n0 + 16 * c < a.N ? 16 * c : 0), left = a.N - col;
+    w[c] = buffer_of(a.wq + col * a.K, (left < 16 ? left : 16) * a.K);
   }
-  i32x4_t acc[1][RT];
+  const int64_t ml = a.M - m0 < 16 * RT ? a.M - m0 : 16 * RT;
+  const i32x4_t x[1] = {buffer_of(a.xq + m0 * a.K, ml * a.K)};
+  uint32_t xoff[RT][XI];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) acc[0][r] = i32x4_t{0, 0, 0, 0};
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int j = 0; j < XI; ++j) xoff[r][j] = (16 * r + stream_row(j)) * (uint32_t)a.K;
+  i32x4_t acc[CT][RT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[c][r] = i32x4_t{0, 0, 0, 0};
   const int ns = stream_steps(a.K);
-  stream_mfma<true, 1, RT, 1, RT == 1 ? 8 : (RT == 2 ? 4 : 2)>(w, woff, x, xoff, a.K, ns * wave / kRowWaves,
-                                                              ns * (wave + 1) / kRowWaves, acc);
+  constexpr int RING = D * kSlot<CT, RT, 1>;
+  stream_mfma<true, CT, RT, 1, XI, D>(w, x, xoff, a.K, ns * wave / W, ns * (wave + 1) / W, lds + wave * RING, acc);
+  // (the waves' parts take their own rings' place)
+  static_assert(RING >= CT * RT * 1024, "parts");
+  i32x4_t* red = reinterpret_cast<i32x4_t*>(lds);
 #pragma unroll
-  for (int r = 0; r < RT; ++r) red[wave][r][lane] = acc[0][r];
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) red[wave * (RING / 16) + (c * RT + r) * kWave + lane] = acc[c][r];
   __syncthreads();
-  if (wave >= RT) return;
-  i32x4_t s = {0, 0, 0, 0};
+  for (int part = wave; part < CT * RT; part += W) {
+    const int c = part / RT, r = part % RT;
+    i32x4_t s = {0, 0, 0, 0};
 #pragma unroll
-  for (int v = 0; v < kRowWaves; ++v) s += red[v][wave][lane];
-  const int64_t m = m0 + 16 * wave + lane % 16, c0 = n0 + 4 * (lane / 16);
-  if (m >= a.M) return;
-  const float xs = a.xs[m];
-  for (int i = 0; i < 4 && c0 + i < a.N; ++i) {
-    float f = (float)s[i] * __fmul_rn(xs, a.ws[c0 + i]);
-    if (a.bias) f += a.bias[c0 + i];
-    a.out[m * a.N + c0 + i] = (bf16_t)f2bf(f);
+    for (int v = 0; v < W; ++v) s += red[v * (RING / 16) + part * kWave + lane];
+    const int64_t m = m0 + 16 * r + lane % 16, c0 = n0 + 16 * c + 4 * (lane / 16);
+    if (m >= a.M) continue;
+    const float xs = a.xs[m];
+    for (int i = 0; i < 4 && c0 + i < a.N; ++i) {
+      float f = (float)s[i] * __fmul_rn(xs, a.ws[c0 + i]);
+      if (a.bias) f += a.bias[c0 + i];
+      a.out[m * a.N + c0 + i] = (bf16_t)f2bf(f);
+    }
   }
+}
+
+// More than 64 KB of dynamic LDS has to be asked for.
+template <class F>
+moe_status allow_lds(F k, int bytes) {
+  if (bytes > 65536 &&
+      hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+    return MOE_ERR_HIP;
+  return MOE_OK;
+}
+
+template <int RT, int CT, int XI, int D, int W>
+moe_status launch_rows(const LinArgs& a, hipStream_t strm) {
+  constexpr int bytes = W * D * kSlot<CT, RT, 1>;
+  static_assert(bytes <= 160 * 1024, "LDS");
+  const auto k = k_linear_rows<RT, CT, XI, D, W>;
+  if (allow_lds(k, bytes) != MOE_OK) return MOE_ERR_HIP;
+  hipLaunchKernelGGL(k, dim3((unsigned)((a.N + 16 * CT - 1) / (16 * CT)), (unsigned)((a.M + 16 * RT - 1) / (16 * RT))),
+                     dim3(W * kWave), bytes, strm, a);
+  return launch_status();
+}
+
+#ifndef L_BK
+#define L_BK 128
+#define L_S 2
+#define L_GM 8
+#endif
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+template <int BM, int BN, int WM, int WN, int BK, int S>
+__global__ __launch_bounds__(WM* WN* kWave, (BM * BN <= 128 * 128 ? 2 : 1) * WM * WN / 4) void k_linear_tiles(
+    LinArgs a, int mt, int nt) {
+  constexpr int W = WM * WN, TI = BM / WM / 32, TJ = BN / WN / 32;
+  constexpr int RPL = 1024 / BK, CPR = BK / 16;           // rows and chunks of one load
+  constexpr int LA = BM / RPL / W, LB = BN / RPL / W;     // loads of a wave and step
+  constexpr int kStage = (BM + BN) * BK;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  // XCD x (workgroups are dealt round-robin) takes the x-th eighth of the tiles, in
+  // groups of L_GM row tiles, column by column
+  const int tiles = mt * nt;
+  int t = blockIdx.x;
+  {
+    const int x = t & 7, i = t >> 3, q = tiles >> 3, rem = tiles & 7;
+    t = x * q + (x < rem ? x : rem) + i;
+  }
+  const int group = L_GM * nt, g = t / group, in = t - g * group;
+  const int rows = mt - g * L_GM < L_GM ? mt - g * L_GM : L_GM;
+  const int64_t m0 = (int64_t)(g * L_GM + in % rows) * BM, n0 = (int64_t)(in / rows) * BN;
+  const uint32_t K = (uint32_t)a.K;
+  const int64_t ml = a.M - m0 < BM ? a.M - m0 : BM, nl = a.N - n0 < BN ? a.N - n0 : BN;
+  const i32x4_t ra = buffer_of(a.xq + m0 * a.K, ml * a.K), rb = buffer_of(a.wq + n0 * a.K, nl * a.K);
+  uint32_t vo[LA + LB], kc[LA + LB];
+#pragma unroll
+  for (int j = 0; j < LA + LB; ++j) {
+    const bool isA = j < LA;
+    const int r = ((isA ? wave * LA + j : wave * LB + j - LA)) * RPL + lane / CPR;
+    const int64_t lim = (isA ? ml : nl) - 1;
+    kc[j] = 16 * swizzle<BK>(r, lane % CPR);
+    vo[j] = (uint32_t)(r < lim ? r : lim) * K + kc[j];
+  }
+  const int nk = (int)((a.K + BK - 1) / BK);
+#ifndef L_ROT
+#define L_ROT 2
+#endif
+  const int mi = (int)(m0 / BM), ni = (int)(n0 / BN);
+  const int ks = (L_ROT == 0 ? 0 : L_ROT == 1 ? (mi + ni) % 8 : L_ROT == 2 ? 2 * ((mi + ni) % 16) : L_ROT == 3 ? 2 * ((mi * 5 + ni * 3) % 16) : (mi * 7 + ni * 11)) % nk;
+  auto issue = [&](int st, int kt) {
+    kt = kt + ks < nk ? kt + ks : kt + ks - nk;
+    const char* base = lds + st * kStage;
+    const uint32_t k0 = (uint32_t)kt * BK;
+    if (k0 + BK <= K) {
+#pragma unroll
+      for (int j = 0; j < LA; ++j) load_lds(ra, base + (wave * LA + j) * 1024, vo[j], k0);
+#pragma unroll
+      for (int j = 0; j < LB; ++j) load_lds(rb, base + BM * BK + (wave * LB + j) * 1024, vo[LA + j], k0);
+    } else {
+      // the last, partial step: chunks past the row's end read zeros
+#pragma unroll
+      for (int j = 0; j < LA; ++j) load_lds(ra, base + (wave * LA + j) * 1024, k0 + kc[j] < K ? vo[j] : kPastBuffer, k0);
+#pragma unroll
+      for (int j = 0; j < LB; ++j)
+        load_lds(rb, base + BM * BK + (wave * LB + j) * 1024, k0 + kc[LA + j] < K ? vo[LA + j] : kPastBuffer, k0);
+    }
+  };
+  i32x16_t acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
+  const int wm = wave / WN, wn = wave % WN;
+  int ar[TI];
+#pragma unroll
+  for (int i = 0; i < TI; ++i) ar[i] = wm * (BM / WM) + 32 * i + lane % 32;
+  const int br = wn * (BN / WN) + lane % 32;
+  // fragments of sub-step kk (32 of K): lane l takes chunk 2 kk + l / 32 of its rows
+  i32x4_t fa[2][TI], fb[2][TJ];
+  auto read = [&](auto B, const char* stage, int kk) {
+    constexpr int b = decltype(B)::value;
+    const int c = 2 * kk + lane / 32;
+    const char* as = stage + ar[0] * BK + 16 * swizzle<BK>(ar[0], c);  // the same for rows 32 apart
+    const char* bs = stage + BM * BK + br * BK + 16 * swizzle<BK>(br, c);
+#pragma unroll
+    for (int i = 0; i < TI; ++i) fa[b][i] = *reinterpret_cast<const i32x4_t*>(as + 32 * i * BK);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) fb[b][j] = *reinterpret_cast<const i32x4_t*>(bs + 32 * j * BK);
+  };
+  auto products = [&](auto B) {
+    constexpr int b = decltype(B)::value;
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[b][j], fa[b][i], acc[i][j], 0, 0, 0);
+  };
+  constexpr std::integral_constant<int, 0> B0;
+  constexpr std::integral_constant<int, 1> B1;
+  constexpr int L = LA + LB, KK = BK / 32;
+  static_assert(KK % 2 == 0, "fragment buffers alternate");
+  // The pipeline: S - 1 steps of loads beyond the current one.  A sub-step's
+  // fragments are read while the products of the one before it run; before the last
+  // products of a step every wave has its fragments and the next step's tiles have
+  // arrived, so one barrier there frees the step's stage for the loads of step
+  // kt + S and opens the next one.
+#pragma unroll
+  for (int p = 0; p < S; ++p)
+    if (p < nk) issue(p, p);
+  if (S - 1 < nk) __builtin_amdgcn_s_waitcnt(vm_wait(L * (S - 1)));
+  else __builtin_amdgcn_s_waitcnt(vm_wait(0));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  int st = 0;
+  read(B0, lds, 0);
+  for (int kt = 0; kt < nk; ++kt) {
+    const char* stage = lds + st * kStage;
+#pragma unroll
+    for (int kk = 0; kk < KK; kk += 2) {
+      read(B1, stage, kk + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      products(B0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (kk + 2 < KK) {
+        read(B0, stage, kk + 2);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      else {
+        if (kt + S - 1 < nk) __builtin_amdgcn_s_waitcnt(vm_wait(L * (S - 2)));
+        else __builtin_amdgcn_s_waitcnt(vm_wait(0));
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (kt + S < nk) issue(st, kt + S);
+        st = st + 1 < S ? st + 1 : 0;
+        // (past the last step: stale LDS, not used)
+        read(B0, lds + st * kStage, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      products(B1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  __syncthreads();
+  // scales and bias, bf16 rows through LDS, whole row pieces out
+  constexpr int PITCH = BN * 2 + 16;
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const int64_t m = m0 + ar[i];
+    const float xs = m < a.M ? a.xs[m] : 0.f;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = wn * (BN / WN) + 32 * j + 8 * q + 4 * (lane / 32);
+        float f[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int64_t n = n0 + col + v < a.N ? n0 + col + v : a.N - 1;
+          f[v] = (float)acc[i][j][4 * q + v] * __fmul_rn(xs, a.ws[n]);
+          if (a.bias) f[v] += a.bias[n];
+        }
+        *reinterpret_cast<uint2*>(lds + ar[i] * PITCH + col * 2) = make_uint2(pk_bf16(f[0], f[1]), pk_bf16(f[2], f[3]));
+      }
+  }
+  __syncthreads();
+  if (a.N % 8 == 0) {
+    constexpr int VPR = BN / 8;
+    for (int v = threadIdx.x; v < BM * VPR; v += W * kWave) {
+      const int r = v / VPR, c = v % VPR;
+      if (m0 + r < a.M && n0 + c * 8 < a.N)
+        *reinterpret_cast<uint4*>(a.out + (m0 + r) * a.N + n0 + c * 8) = *reinterpret_cast<const uint4*>(lds + r * PITCH + c * 16);
+    }
+  } else {
+    for (int v = threadIdx.x; v < BM * BN; v += W * kWave) {
+      const int r = v / BN, c = v % BN;
+      if (m0 + r < a.M && n0 + c < a.N)
+        a.out[(m0 + r) * a.N + n0 + c] = *reinterpret_cast<const bf16_t*>(lds + r * PITCH + c * 2);
+    }
+  }
+}
+
+template <int BM, int BN, int WM, int WN, int BK, int S>
+moe_status launch_tiles(const LinArgs& a, hipStream_t strm) {
+  const int mt = (int)((a.M + BM - 1) / BM), nt = (int)((a.N + BN - 1) / BN);
+  constexpr int stages = S * (BM + BN) * BK, outs = BM * (BN * 2 + 16);
+  constexpr int bytes = stages > outs ? stages : outs;
+  static_assert(bytes <= 160 * 1024, "LDS");
+  const auto k = k_linear_tiles<BM, BN, WM, WN, BK, S>;
+  if (allow_lds(k, bytes) != MOE_OK) return MOE_ERR_HIP;
+  hipLaunchKernelGGL(k, dim3((unsigned)(mt * nt)), dim3(WM * WN * kWave), bytes, strm, a, mt, nt);
+  return launch_status();
 }
 
 moe_status check_linear(int64_t M, int64_t N, int64_t K) {
@@ -90,13 +321,28 @@ bool misaligned(const void* p, const void* q) {
 }
 
 moe_status linear_impl(const LinArgs& a, hipStream_t strm) {
-  const unsigned nt = (unsigned)((a.N + 15) / 16);
-  const int rt = a.M <= 16 ? 1 : (a.M <= 32 ? 2 : 4);
-  const dim3 grid(nt, (unsigned)((a.M + rt * 16 - 1) / (rt * 16))), block(kRowWaves * kWave);
-  if (rt == 1) hipLaunchKernelGGL(k_linear_rows<1>, grid, block, 0, strm, a);
-  else if (rt == 2) hipLaunchKernelGGL(k_linear_rows<2>, grid, block, 0, strm, a);
-  else hipLaunchKernelGGL(k_linear_rows<4>, grid, block, 0, strm, a);
-  return launch_status();
+#ifdef FORCE
+  if (FORCE == 1) return launch_tiles<256, 256, 2, 4, 128, 2>(a, strm);
+  if (FORCE == 2) return launch_tiles<128, 128, 2, 2, 128, 2>(a, strm);
+  if (FORCE == 3) return launch_tiles<64, 128, 2, 2, 128, 3>(a, strm);
+  if (FORCE == 4) return launch_tiles<64, 128, 2, 2, 128, 6>(a, strm);
+  if (FORCE == 5) return launch_tiles<64, 64, 2, 2, 128, 4>(a, strm);
+  if (FORCE == 6) return launch_tiles<64, 64, 2, 2, 128, 8>(a, strm);
+  if (FORCE == 7) return launch_tiles<64, 32, 2, 1, 128, 6>(a, strm);
+  if (FORCE == 8) return launch_tiles<128, 128, 2, 2, 128, 4>(a, strm);
+  if (FORCE == 9) return launch_tiles<128, 256, 2, 4, 128, 3>(a, strm);
+#endif
+#ifndef FORCE
+  if (a.M > 64) {
+    const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
+    if (big >= 200) return launch_tiles<256, 256, 2, 4, 128, 2>(a, strm);
+    return launch_tiles<128, 128, 2, 2, 128, 2>(a, strm);
+  }
+#endif
+  if (a.M <= 8) return launch_rows<1, R_CT, 1, R_D, R_W>(a, strm);
+  if (a.M <= 16) return launch_rows<1, R_CT, 2, R_D, R_W>(a, strm);
+  if (a.M <= 32) return launch_rows<2, R_CT, 2, R_D, R_W>(a, strm);
+  return launch_rows<4, R_CT, 2, R_D, R_W>(a, strm);
 }
 
 }  // namespace

@@ -1,16 +1,18 @@
 // Products of a few activation rows with weights that are read once: the wave
 // level of the few-token layer and of the int8 matrix product's small-M form.
 //
-// A wave multiplies 16 weight rows (output columns) with up to 16 * RT
-// activation rows over a range of the contraction, in steps of 64 bytes per row
-// (32 bf16 or 64 int8 values): v_mfma_f32_16x16x32_bf16 or
-// v_mfma_i32_16x16x64_i8, the weights the first operand.  Lane l holds 16 bytes
-// of weight row l % 16 and of activation row l % 16, both at chunk l / 16 of the
-// step, so operands go from memory to the matrix cores in the layout they are
-// stored in, with no LDS and no shuffles; the result's lane l holds columns
-// 4 (l / 16) .. + 3 of activation row l % 16.  A product's column depends on its
-// own activation row alone, so a lane without a row of its own may read any
-// valid row: its results are dropped.
+// A wave multiplies NW groups of 16 weight rows (output columns) with up to 16 RT
+// activation rows over a range of the contraction, in steps of 128 bytes per row
+// (64 bf16 or 128 int8 values): v_mfma_f32_16x16x32_bf16 or v_mfma_i32_16x16x64_i8,
+// the weights the first operand.  Both operands go from memory straight into a
+// small LDS ring of the wave's own, eight rows of 128 bytes by each load, so every
+// request is a whole cache line (rows of 64 bytes spread over the lanes as the
+// matrix cores take them reached 37 against 94 bytes per ns and CU), and no
+// barrier is needed: the wave waits for its own loads by count.  Fragments then
+// are read as 16 bytes of row l % 16, chunk 4 kk + l / 16; the result's lane l
+// holds columns 4 (l / 16) .. + 3 of activation row l % 16.  A product's column
+// depends on its own activation row alone, so what a lane without a row holds
+// does not matter.
 #pragma once
 
 #include "common.hpp"
@@ -38,7 +40,7 @@ __device__ __forceinline__ typename MfmaAcc<I8>::type mfma16(const i32x4_t& w, c
                                                    0, 0);
 }
 
-constexpr int kStepBytes = 64;  // bytes of every row in one step
+constexpr int kStepBytes = 128;  // bytes of every row in one step
 
 // Steps of a row of `bytes` bytes (a multiple of 16; the last step may be partial).
 __host__ __device__ inline int stream_steps(int64_t bytes) { return (int)((bytes + kStepBytes - 1) / kStepBytes); }
@@ -46,63 +48,132 @@ __host__ __device__ inline int stream_steps(int64_t bytes) { return (int)((bytes
 // A value that every lane of the wave holds, in a scalar register.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-__device__ __forceinline__ i32x4_t ld16(const char* base, uint32_t off) {
-  return *reinterpret_cast<const i32x4_t*>(base + (size_t)off);
+// s_waitcnt immediate: at most n vector memory operations outstanding (LDS reads:
+// none)
+constexpr int vm_wait(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
+
+// Raw buffer over `bytes` bytes (below 2^31) at p, in scalar registers: accesses
+// past it read zeros.
+__device__ __forceinline__ i32x4_t buffer_of(const void* p, int64_t bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return i32x4_t{uniform((int)(uint32_t)v), uniform((int)(uint32_t)(v >> 32) & 0xffff),
+                 uniform((int)(bytes < 0 ? 0 : bytes)), 0x00020000};
+}
+constexpr uint32_t kPastBuffer = 0x80000000u;
+
+// One 16-byte-per-lane load from buffer offset vo (per lane) + so into LDS at `lds`
+// (+ 16 lane).  It has no register result; the pipelines wait for it by count.
+__device__ __forceinline__ void load_lds(const i32x4_t& r, const char* lds, uint32_t vo, uint32_t so) {
+  const uint32_t m0 = (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char*)(lds));
+  asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" : : "v"(vo), "s"(r), "s"(so), "{m0}"(m0));
 }
 
-// acc[n][r] += (16 weight rows n) x (16 activation rows r) over steps [s0, s1) of
-// rows of `bytes` bytes.  A lane's chunk of step s of weight rows n is at
-// w[n] + 64 s + woff[n], of activation rows r, plane p, at x[p] + 64 s + xoff[r]
-// (PX planes, each multiplied with the same weights); w, x, s0 and s1 are the
-// same in every lane, so they stay in scalar registers.  U steps' loads are
-// issued before their products.
-template <bool I8, int NW, int RT, int PX, int U>
-__device__ __forceinline__ void stream_mfma(const char* const (&w)[NW], const uint32_t (&woff)[NW],
-                                            const char* const (&x)[PX], const uint32_t (&xoff)[RT], int64_t bytes,
-                                            int s0, int s1, typename MfmaAcc<I8>::type (&acc)[NW][RT]) {
-  const int full = (int)(bytes / kStepBytes);
-  const int e = s1 < full ? s1 : full;
-  int s = s0;
-  for (; s + U <= e; s += U) {
-    i32x4_t wv[U][NW], xv[U][PX][RT];
-    const int64_t o = (int64_t)s * kStepBytes;
+// Chunk position of chunk c (16 bytes) of row r in LDS rows of BK bytes: the 16 rows
+// that one read phase takes lie in 16 different slots of a 256-byte window.
+template <int BK>
+__device__ __forceinline__ int swizzle(int r, int c) {
+  return BK == 128 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
+}
+
+// Lane l's row (of 16, its half j) and chunk byte in a row group's loads.
+__device__ __forceinline__ int stream_row(int j) { return 8 * j + (threadIdx.x % kWave) / 8; }
+__device__ __forceinline__ uint32_t stream_chunk(int j) {
+  return 16 * swizzle<128>(stream_row(j), threadIdx.x % 8);
+}
+
+// Bytes of one ring slot; a wave's ring is D of them.
+template <int NW, int RT, int PX>
+constexpr int kSlot = (NW + PX * RT) * 2048;
+
+// acc[n][r] += (weight rows of group n) x (activation rows of tile r) over steps
+// [s0, s1) of rows of `bytes` bytes.  w[n]: a buffer of group n's rows (its end also
+// ends the valid rows); x[p]: a buffer of plane p's activation rows, xoff[r][j] the
+// byte offset of row stream_row(j) of tile r in it, kPastBuffer for none (PX planes,
+// each multiplied with the same weights; XI = 1: tiles of at most 8 rows).  ring: D
+// slots of LDS.  w, x, s0 and s1 are the same in every lane.
+template <bool I8, int NW, int RT, int PX, int XI, int D>
+__device__ __forceinline__ void stream_mfma(const i32x4_t (&w)[NW], const i32x4_t (&x)[PX],
+                                            const uint32_t (&xoff)[RT][XI], int64_t bytes, int s0, int s1, char* ring,
+                                            typename MfmaAcc<I8>::type (&acc)[NW][RT]) {
+  constexpr int I = 2 * NW + PX * RT * XI;  // loads of one slot
+  const int lane = threadIdx.x % kWave;
+  const uint32_t nb = (uint32_t)bytes;
+  uint32_t woff[2], xo[RT][XI];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+  for (int j = 0; j < 2; ++j) woff[j] = stream_row(j) * nb + stream_chunk(j);
 #pragma unroll
-      for (int n = 0; n < NW; ++n) wv[u][n] = ld16(w[n] + o + u * kStepBytes, woff[n]);
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int p = 0; p < PX; ++p)
+    for (int j = 0; j < XI; ++j) xo[r][j] = xoff[r][j] == kPastBuffer ? kPastBuffer : xoff[r][j] + stream_chunk(j);
+  auto issue = [&](char* slot, int s) {
+    const uint32_t o = (uint32_t)s * kStepBytes;
+    uint32_t wo[2] = {woff[0], woff[1]}, xs[RT][XI];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) xv[u][p][r] = ld16(x[p] + o + u * kStepBytes, xoff[r]);
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int j = 0; j < XI; ++j) xs[r][j] = xo[r][j];
+    if (o + kStepBytes > nb) {
+      // the last, partial step: chunks past the row's end read zeros
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (o + stream_chunk(j) >= nb) {
+          wo[j] = kPastBuffer;
+          if (j < XI)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) xs[r][j < XI ? j : 0] = kPastBuffer;
+        }
     }
-    __builtin_amdgcn_sched_barrier(0);  // every load of the U steps before the first product
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int n = 0; n < NW; ++n)
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int p = 0; p < PX; ++p) acc[n][r] = mfma16<I8>(wv[u][n], xv[u][p][r], acc[n][r]);
-  }
-  for (; s < s1; ++s) {
-    const int64_t o = (int64_t)s * kStepBytes;
-    // past the row's end (only in the last, partial step) both operands are zero
-    const bool in = o + 16 * (int)((threadIdx.x % kWave) / 16) < bytes;
-    const i32x4_t z = {0, 0, 0, 0};
-    i32x4_t wv[NW], xv[PX][RT];
-#pragma unroll
-    for (int n = 0; n < NW; ++n) wv[n] = in ? ld16(w[n] + o, woff[n]) : z;
-#pragma unroll
-    for (int p = 0; p < PX; ++p)
-#pragma unroll
-      for (int r = 0; r < RT; ++r) xv[p][r] = in ? ld16(x[p] + o, xoff[r]) : z;
 #pragma unroll
     for (int n = 0; n < NW; ++n)
 #pragma unroll
+      for (int j = 0; j < 2; ++j) load_lds(w[n], slot + n * 2048 + j * 1024, wo[j], o);
+#pragma unroll
+    for (int p = 0; p < PX; ++p)
+#pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int p = 0; p < PX; ++p) acc[n][r] = mfma16<I8>(wv[n], xv[p][r], acc[n][r]);
+        for (int j = 0; j < XI; ++j) load_lds(x[p], slot + (NW + p * RT + r) * 2048 + j * 1024, xs[r][j], o);
+  };
+  const int n = s1 - s0;
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (d < n) issue(ring + d * kSlot<NW, RT, PX>, s0 + d);
+  int at[2];  // this lane's fragments in a row group
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) at[kk] = (lane % 16) * 128 + 16 * swizzle<128>(lane % 16, 4 * kk + lane / 16);
+  auto step = [&](char* slot, int i) {
+    // the slot's loads have arrived: later ones may be outstanding
+    if (i + D - 1 < n) __builtin_amdgcn_s_waitcnt(vm_wait(I * (D - 1)));
+    else __builtin_amdgcn_s_waitcnt(vm_wait(0));
+    asm volatile("" ::: "memory");
+    i32x4_t wv[2][NW], xv[2][PX][RT];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+      for (int g = 0; g < NW; ++g) wv[kk][g] = *reinterpret_cast<const i32x4_t*>(slot + g * 2048 + at[kk]);
+#pragma unroll
+      for (int p = 0; p < PX; ++p)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          xv[kk][p][r] = *reinterpret_cast<const i32x4_t*>(slot + (NW + p * RT + r) * 2048 + at[kk]);
+    }
+    // every fragment is in registers: the slot takes the loads of a later step
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (i + D < n) issue(slot, s0 + i + D);
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int g = 0; g < NW; ++g)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int p = 0; p < PX; ++p) acc[g][r] = mfma16<I8>(wv[kk][g], xv[kk][p][r], acc[g][r]);
+  };
+  for (int i = 0; i < n; i += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (i + d < n) step(ring + d * kSlot<NW, RT, PX>, i + d);
   }
 }
 
