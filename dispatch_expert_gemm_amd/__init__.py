@@ -11,6 +11,7 @@ GPU tensor of the right dtype, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -1300,47 +1301,62 @@ def moe_layer_int8(x, topk_idx, topk_weights, wq_gate, wq_up, wq_down, *, smooth
 
 FEW_TOKENS_MAX = 64
 
+# The calls below are the ones of a decode step, where the host's time for a call counts:
+# sizes are looked up by shape once, the arguments are checked in one expression each.
+
+
+def _refuse(t, dtype, n, name, dev):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise MoeError(f"{name} must be a GPU tensor")
+    if t.get_device() != dev:
+        raise MoeError(f"{name} is on {t.device}, expected device {dev}")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise MoeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise MoeError(f"{name} must be contiguous")
+    raise MoeError(f"{name} holds {t.numel()} elements, needs at least {n}")
+
 
 def _at(t, dtype, n, name, dev):
     """The address of a tensor argument (None: a NULL pointer): a contiguous tensor of
-    this dtype on device dev with at least n elements, else MoeError."""
+    this dtype on GPU number dev with at least n elements, else MoeError."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise MoeError(f"{name} must be a GPU tensor")
-    if t.dtype != dtype and not (dtype is U8 and t.dtype in U8):
-        raise MoeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise MoeError(f"{name} is on {t.device}, expected {dev}")
-    if not t.is_contiguous():
-        raise MoeError(f"{name} must be contiguous")
-    if t.numel() < n:
-        raise MoeError(f"{name} holds {t.numel()} elements, needs at least {n}")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, n, name, dev)
 
 
 def _device_of(x, name):
+    """The number of the GPU that x is on."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise MoeError(f"{name} must be a GPU tensor")
-    return x.device
+    return x.get_device()
 
 
 def _launch(entry, dev, stream, *args):
-    """Call a C entry with its stream argument last, on the device its tensors are on."""
+    """Call a C entry with its stream argument last, on the GPU its tensors are on."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise MoeError(f"the stream is on {stream.device}, the tensors on {dev}")
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            _check(entry(*args, stream.cuda_stream))
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise MoeError(f"the stream is on {stream.device}, the tensors on device {dev}")
     else:
-        _check(entry(*args, stream.cuda_stream))
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            st = entry(*args, raw)
+    else:
+        st = entry(*args, raw)
+    if st != 0:
+        _check(st)
 
 
 def _int8_pair(w):
     """(codes, scales) of an Int8Weights or of a (codes, scales) pair."""
-    return (w.codes, w.scales) if isinstance(w, Int8Weights) else tuple(w)
+    return (w.codes, w.scales) if isinstance(w, Int8Weights) else w
 
 
 def moe_few_tokens_workspace_size(shape: MoeShape, shared_F: int = 0, int8: bool = False) -> int:
@@ -1353,58 +1369,81 @@ def _few_common(shape, dev, x, topk_idx, topk_weights, x_active_mask, shared_exp
                 const_v, out, err_flag):
     T, H, K = shape.T, shape.H, shape.K
     QH = shape.const_expert_num * H
+    if x_active_mask is not None and x_active_mask.dtype is torch.bool:
+        x_active_mask = x_active_mask.view(torch.uint8)
     return ((_at(x, BF16, T * H, "x", dev), _at(topk_idx, I32, T * K, "topk_idx", dev),
              _at(topk_weights, F32, T * K, "topk_weights", dev),
-             _at(x_active_mask, U8, (0, T, T * K)[shape.mask_ndim], "x_active_mask", dev)),
+             _at(x_active_mask, U8T, (0, T, T * K)[shape.mask_ndim], "x_active_mask", dev)),
             (_at(shared_expert_x, BF16, T * H, "shared_expert_x", dev),
              _at(const_alpha_1, BF16, QH, "const_alpha_1", dev), _at(const_alpha_2, BF16, QH, "const_alpha_2", dev),
              _at(const_v, BF16, QH, "const_v", dev), _at(out, BF16, T * H, "out", dev),
              _at(err_flag, I32, 1, "err_flag", dev)))
 
 
-def _bytes_of(workspace, dev):
-    if workspace is not None and workspace.device != dev:
-        raise MoeError(f"workspace is on {workspace.device}, expected {dev}")
-    return _ptr(workspace, None, "workspace"), 0 if workspace is None else workspace.numel() * workspace.element_size()
+def _few_bf16(shape, dev, ins, w_gate, w_up, w_down, shared_w, Fs, rest, ws_at, ws_bytes, stream):
+    n, H = shape.num_experts * shape.F * shape.H, shape.H
+    s = (None, None, None) if shared_w is None else [
+        _at(t, BF16, Fs * H, "shared expert weights", dev) for t in shared_w]
+    _launch(lib().moe_few_tokens, dev, stream, ctypes.byref(shape), *ins, _at(w_gate, BF16, n, "w_gate", dev),
+            _at(w_up, BF16, n, "w_up", dev), _at(w_down, BF16, n, "w_down", dev), Fs, *s, *rest, ws_at, ws_bytes)
+
+
+def _few_int8(shape, dev, ins, smooth_scales, w, shared_w, Fs, rest, ws_at, ws_bytes, stream):
+    E, F, H = shape.num_experts, shape.F, shape.H
+
+    def three(ws, E, F):
+        a = []
+        for v, n in zip(ws, (F, F, H)):
+            q, s = _int8_pair(v)
+            a += (_at(q, I8T, E * F * H, "int8 weight codes", dev), _at(s, F32, E * n, "int8 weight scales", dev))
+        return (MoeInt8Weight * 3)((a[0], a[1]), (a[2], a[3]), (a[4], a[5]))
+
+    _launch(lib().moe_few_tokens_int8, dev, stream, ctypes.byref(shape), *ins,
+            _at(smooth_scales, F32, E * H, "smooth_scales", dev), three(w, E, F), Fs,
+            None if shared_w is None else three(shared_w, 1, Fs), *rest, ws_at, ws_bytes)
+
+
+def _bytes_at(workspace, dev):
+    if workspace is None:
+        return None, 0
+    n = workspace.numel() * workspace.element_size() if isinstance(workspace, torch.Tensor) else 0
+    return _at(workspace, workspace.dtype if n else None, 0, "workspace", dev), n
 
 
 def moe_few_tokens(shape, x, topk_idx, topk_weights, x_active_mask, w_gate, w_up, w_down, shared_w, shared_expert_x,
                    const_alpha_1, const_alpha_2, const_v, out, err_flag, workspace, stream=None):
     """shared_w: None or the shared expert's (gate, up, down) weights."""
     dev = _device_of(x, "x")
-    n = shape.num_experts * shape.F * shape.H
-    a, b = _few_common(shape, dev, x, topk_idx, topk_weights, x_active_mask, shared_expert_x, const_alpha_1,
-                       const_alpha_2, const_v, out, err_flag)
+    ins, rest = _few_common(shape, dev, x, topk_idx, topk_weights, x_active_mask, shared_expert_x, const_alpha_1,
+                            const_alpha_2, const_v, out, err_flag)
     Fs = 0 if shared_w is None else shared_w[0].shape[-2]
-    s = (None, None, None) if shared_w is None else [
-        _at(t, BF16, Fs * shape.H, "shared expert weights", dev) for t in shared_w]
-    _launch(lib().moe_few_tokens, dev, stream, ctypes.byref(shape), *a, _at(w_gate, BF16, n, "w_gate", dev),
-            _at(w_up, BF16, n, "w_up", dev), _at(w_down, BF16, n, "w_down", dev), Fs, *s, *b,
-            *_bytes_of(workspace, dev))
+    _few_bf16(shape, dev, ins, w_gate, w_up, w_down, shared_w, Fs, rest, *_bytes_at(workspace, dev), stream)
 
 
 def moe_few_tokens_int8(shape, x, topk_idx, topk_weights, x_active_mask, smooth_scales, w, shared_w, shared_expert_x,
                         const_alpha_1, const_alpha_2, const_v, out, err_flag, workspace, stream=None):
     """w, shared_w: (gate, up, down), each an Int8Weights or a (codes, scales) pair."""
     dev = _device_of(x, "x")
-    H = shape.H
-
-    def three(ws, E, F):
-        c = [_int8_pair(v) for v in ws]
-        return (MoeInt8Weight * 3)(*[
-            MoeInt8Weight(_at(q, I8T, E * F * H, "int8 weight codes", dev), _at(s, F32, E * n, "int8 weight scales", dev))
-            for (q, s), n in zip(c, (F, F, H))])
-
-    a, b = _few_common(shape, dev, x, topk_idx, topk_weights, x_active_mask, shared_expert_x, const_alpha_1,
-                       const_alpha_2, const_v, out, err_flag)
+    ins, rest = _few_common(shape, dev, x, topk_idx, topk_weights, x_active_mask, shared_expert_x, const_alpha_1,
+                            const_alpha_2, const_v, out, err_flag)
     Fs = 0 if shared_w is None else _int8_pair(shared_w[0])[0].shape[-2]
-    _launch(lib().moe_few_tokens_int8, dev, stream, ctypes.byref(shape), *a,
-            _at(smooth_scales, F32, shape.num_experts * H, "smooth_scales", dev),
-            three(w, shape.num_experts, shape.F), Fs, None if shared_w is None else three(shared_w, 1, Fs), *b,
-            *_bytes_of(workspace, dev))
+    _few_int8(shape, dev, ins, smooth_scales, w, shared_w, Fs, rest, *_bytes_at(workspace, dev), stream)
 
 
-@torch.no_grad()
+@functools.lru_cache(maxsize=256)
+def _few_sizes(T, H, K, E, F, Z, C, Q, mask_ndim, Fs, int8):
+    """(shape, bytes of workspace rounded up to 256)."""
+    shape = make_shape(T, H, K, E, F=F, zero_expert_num=Z, copy_expert_num=C, const_expert_num=Q, mask_ndim=mask_ndim)
+    return shape, (moe_few_tokens_workspace_size(shape, Fs, int8) + 255) // 256 * 256
+
+
+def _fits(ws, n, H):
+    f = ws[0].shape[-2]
+    if ws[0].shape != (n, f, H) or ws[1].shape != (n, f, H) or ws[2].shape != (n, H, f):
+        raise MoeError(f"weights {[tuple(w.shape) for w in ws]} do not fit {n} experts of {H} columns")
+    return f
+
+
 def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smooth_scales=None, x_active_mask=None,
                          shared_expert_x=None, shared_w_gate=None, shared_w_up=None, shared_w_down=None,
                          const_alpha_1=None, const_alpha_2=None, const_v=None, zero_expert_num=0, copy_expert_num=0,
@@ -1423,35 +1462,39 @@ def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smo
                 shared_w_up=shared_w_up, shared_w_down=shared_w_down, const_alpha_1=const_alpha_1,
                 const_alpha_2=const_alpha_2, const_v=const_v, zero_expert_num=zero_expert_num,
                 copy_expert_num=copy_expert_num, const_expert_num=const_expert_num, err_flag=err_flag)
-    T, H = x.shape
-    K = topk_idx.shape[1]
-    int8 = not isinstance(w_gate, torch.Tensor)
-    E, F, _ = (_int8_pair(w_gate)[0] if int8 else w_gate).shape
     dev = _device_of(x, "x")
-    mask_ndim = 0 if x_active_mask is None else x_active_mask.dim()
-    shape = make_shape(T, H, K, E, F=F, zero_expert_num=zero_expert_num, copy_expert_num=copy_expert_num,
-                       const_expert_num=const_expert_num, mask_ndim=mask_ndim)
-    shared_w = None if shared_w_gate is None else (shared_w_gate, shared_w_up, shared_w_down)
-    for ws, n in ((((w_gate, w_up, w_down), E), (shared_w, 1)) if shared_w else (((w_gate, w_up, w_down), E),)):
-        if int8:
-            ws = [_int8_pair(w)[0] for w in ws]
-        f = ws[0].shape[1]
-        if ws[0].shape != (n, f, H) or ws[1].shape != (n, f, H) or ws[2].shape != (n, H, f):
-            raise MoeError(f"weights {[tuple(w.shape) for w in ws]} do not fit {n} experts of {H} columns")
+    T, H = x.shape
+    K = topk_idx.shape[-1]
     if topk_idx.shape != (T, K) or topk_weights.shape != (T, K):
         raise MoeError(f"topk_idx {tuple(topk_idx.shape)} and topk_weights {tuple(topk_weights.shape)} for {T} tokens")
-    Fs = 0 if shared_w is None else (_int8_pair(shared_w_gate)[0] if int8 else shared_w_gate).shape[-2]
-    workspace = torch.empty(moe_few_tokens_workspace_size(shape, Fs, int8), dtype=torch.uint8, device=dev)
-    out = torch.empty((T, H), dtype=BF16, device=dev)
-    if err_flag is None:
-        err_flag = torch.empty(1, dtype=I32, device=dev)
-    rest = (shared_w, shared_expert_x, const_alpha_1, const_alpha_2, const_v, out, err_flag, workspace)
+    int8 = not isinstance(w_gate, torch.Tensor)
+    w = (w_gate, w_up, w_down)
+    shared_w = None if shared_w_gate is None else (shared_w_gate, shared_w_up, shared_w_down)
     if int8:
-        moe_few_tokens_int8(shape, x, topk_idx, topk_weights, x_active_mask, smooth_scales, (w_gate, w_up, w_down), *rest)
+        codes = [_int8_pair(v)[0] for v in w]
+        E = codes[0].shape[0]
+        F = _fits(codes, E, H)
+        Fs = 0 if shared_w is None else _fits([_int8_pair(v)[0] for v in shared_w], 1, H)
     else:
+        E = w_gate.shape[0]
+        F = _fits(w, E, H)
+        Fs = 0 if shared_w is None else _fits(shared_w, 1, H)
         if smooth_scales is not None:
             raise MoeError("smooth_scales go with int8 weights")
-        moe_few_tokens(shape, x, topk_idx, topk_weights, x_active_mask, w_gate, w_up, w_down, *rest)
+    shape, ws_bytes = _few_sizes(T, H, K, E, F, zero_expert_num, copy_expert_num, const_expert_num,
+                                 0 if x_active_mask is None else x_active_mask.dim(), Fs, int8)
+    out = torch.empty((T, H), dtype=BF16, device=x.device)
+    # the error flag, where the caller wants none, behind the workspace
+    workspace = torch.empty(ws_bytes + 4, dtype=U8T, device=x.device)
+    ws_at = workspace.data_ptr()
+    ins, rest = _few_common(shape, dev, x, topk_idx, topk_weights, x_active_mask, shared_expert_x, const_alpha_1,
+                            const_alpha_2, const_v, out, err_flag)
+    if err_flag is None:
+        rest = (*rest[:-1], ws_at + ws_bytes)
+    if int8:
+        _few_int8(shape, dev, ins, smooth_scales, w, shared_w, Fs, rest, ws_at, ws_bytes, None)
+    else:
+        _few_bf16(shape, dev, ins, w_gate, w_up, w_down, shared_w, Fs, rest, ws_at, ws_bytes, None)
     return out
 
 
@@ -1464,6 +1507,7 @@ def moe_linear_int8(xq, xs, wq, ws, bias, out, stream=None):
             _at(out, BF16, M * N, "out", dev))
 
 
+@functools.lru_cache(maxsize=256)
 def moe_linear_int8_workspace_size(M: int, N: int, K: int) -> int:
     n = ctypes.c_size_t()
     _check(lib().moe_linear_int8_workspace_size(M, N, K, ctypes.byref(n)))
@@ -1476,10 +1520,9 @@ def moe_linear_int8_dynamic(x, wq, ws, bias, out, workspace, stream=None):
     (M, K), N = x.shape, wq.shape[0]
     _launch(lib().moe_linear_int8_dynamic, dev, stream, M, N, K, _at(x, BF16, M * K, "x", dev),
             _at(wq, I8T, N * K, "wq", dev), _at(ws, F32, N, "ws", dev), _at(bias, F32, N, "bias", dev),
-            _at(out, BF16, M * N, "out", dev), *_bytes_of(workspace, dev))
+            _at(out, BF16, M * N, "out", dev), *_bytes_at(workspace, dev))
 
 
-@torch.no_grad()
 def linear_int8(x, w, *, x_scales=None, bias=None, stream=None):
     """x (..., K) times the transpose of int8 weights (N, K) with one scale per output channel ->
     (..., N) bf16 (inference, no autograd).  w: an Int8Weights or a (codes, scales) pair.
@@ -1488,20 +1531,23 @@ def linear_int8(x, w, *, x_scales=None, bias=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):  # its output and workspace then belong to that stream
             return linear_int8(x, w, x_scales=x_scales, bias=bias)
-    wq, ws = _int8_pair(w)
-    if wq.dim() != 2 or x.shape[-1] != wq.shape[1]:
-        raise MoeError(f"x {tuple(x.shape)} and weights {tuple(wq.shape)} do not multiply")
     dev = _device_of(x, "x")
+    wq, ws = _int8_pair(w)
+    K = x.shape[-1]
+    if wq.dim() != 2 or wq.shape[1] != K:
+        raise MoeError(f"x {tuple(x.shape)} and weights {tuple(wq.shape)} do not multiply")
     N = wq.shape[0]
-    out = torch.empty((*x.shape[:-1], N), dtype=BF16, device=dev)
-    _at(x, BF16 if x_scales is None else I8T, 0, "x", dev)
-    rows = x.view(-1, x.shape[-1]) if x.dim() != 2 else x
+    M = x.numel() // K if K else 0
+    out = torch.empty((*x.shape[:-1], N), dtype=BF16, device=x.device)
+    args = (_at(wq, I8T, N * K, "wq", dev), _at(ws, F32, N, "ws", dev), _at(bias, F32, N, "bias", dev), out.data_ptr())
     if x_scales is not None:
-        moe_linear_int8(rows, x_scales, wq, ws, bias, out)
+        _launch(lib().moe_linear_int8, dev, None, M, N, K, _at(x, I8T, M * K, "x", dev),
+                _at(x_scales, F32, M, "x_scales", dev), *args)
     else:
-        workspace = torch.empty(moe_linear_int8_workspace_size(rows.shape[0], N, rows.shape[1]), dtype=torch.uint8,
-                                device=dev)
-        moe_linear_int8_dynamic(rows, wq, ws, bias, out, workspace)
+        n = moe_linear_int8_workspace_size(M, N, K)
+        workspace = torch.empty(n, dtype=U8T, device=x.device)
+        _launch(lib().moe_linear_int8_dynamic, dev, None, M, N, K, _at(x, BF16, M * K, "x", dev), *args,
+                workspace.data_ptr(), n)
     return out
 
 

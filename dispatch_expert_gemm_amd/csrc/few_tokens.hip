@@ -713,19 +713,12 @@ struct FewWeight {
   const float* scales;
 };
 
-// More than 64 KB of dynamic LDS has to be asked for.
-template <class F>
-bool lds_allowed(F k, int bytes) {
-  return bytes <= 65536 || hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                               bytes) == hipSuccess;
-}
-
 template <bool I8, int RTM, int KS>
 bool launch_up(const FewArgs& a, hipStream_t strm) {
   constexpr int COLS = 16 * kUpWaves / KS;
   const int lds = (RTM == 1 ? route_work_bytes(a.T * a.K, a.E, a.groups) : 0) + kUpWaves * kUpRing;
   const int64_t n = a.groups * ((a.F + COLS - 1) / COLS) + (a.Fs + COLS - 1) / COLS;
-  if (!lds_allowed(k_few_gate_up<I8, RTM, KS>, lds)) return false;
+  if (!lds_allowed<k_few_gate_up<I8, RTM, KS>>(lds)) return false;
   hipLaunchKernelGGL((k_few_gate_up<I8, RTM, KS>), dim3((unsigned)n), dim3(kUpWaves * kWave), lds, strm, a);
   return true;
 }
@@ -734,7 +727,7 @@ template <bool I8, int RTM, int KS>
 bool launch_y(const FewArgs& a, hipStream_t strm) {
   constexpr int COLS = 16 * kYCT * kYWaves / KS, lds = kYWaves * kYRing;
   const int64_t n = (a.groups + (a.Fs > 0)) * ((a.H + COLS - 1) / COLS);
-  if (!lds_allowed(k_few_down_y<I8, RTM, kYCT, KS>, lds)) return false;
+  if (!lds_allowed<k_few_down_y<I8, RTM, kYCT, KS>>(lds)) return false;
   hipLaunchKernelGGL((k_few_down_y<I8, RTM, kYCT, KS>), dim3((unsigned)n), dim3(kYWaves * kWave), lds, strm, a);
   const dim3 grid((unsigned)((a.H + 1023) / 1024), (unsigned)a.T);
   if (a.K <= 8) hipLaunchKernelGGL(k_few_join<8>, grid, dim3(256), 0, strm, a);
@@ -756,7 +749,7 @@ moe_status few_launch(FewArgs& a, hipStream_t strm) {
   if constexpr (RTM == 1) {
     constexpr auto kDown = k_few_down<I8, kDownCT>;
     const int lds = rb + kDownWaves * (kDownRing + a.T * 16 * kDownCT * 4);
-    ok = ok && lds_allowed(kDown, lds);
+    ok = ok && lds_allowed<kDown>(lds);
     if (ok)
       hipLaunchKernelGGL(kDown, dim3((unsigned)((a.H + 16 * kDownCT - 1) / (16 * kDownCT))), dim3(kDownWaves * kWave), lds,
                          strm, a);

@@ -7,6 +7,7 @@
 // split the contraction, each streaming its part of the 16 weight rows from
 // memory into the matrix cores (stream_mfma.hpp); the int32 partial sums meet in
 // LDS, where their order does not matter.  Bound: HBM, N * K bytes of weights.
+#include <algorithm>
 #include <type_traits>
 
 #include "stream_mfma.hpp"
@@ -36,11 +37,6 @@ __global__ __launch_bounds__(256) void k_quant_x(const uint4* __restrict__ x, in
   if (threadIdx.x == 0) scales[r] = s;
 }
 
-#ifndef R_W
-#define R_W 8
-#define R_CT 1
-#define R_D 2
-#endif
 // One workgroup per (16 CT output columns, 16 RT rows): W waves split the
 // contraction and their int32 sums meet in LDS.
 template <int RT, int CT, int XI, int D, int W>
@@ -94,32 +90,31 @@ __global__ __launch_bounds__(W* kWave, 2) void k_linear_rows(LinArgs a) {
   }
 }
 
-// More than 64 KB of dynamic LDS has to be asked for.
-template <class F>
-moe_status allow_lds(F k, int bytes) {
-  if (bytes > 65536 &&
-      hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
-    return MOE_ERR_HIP;
-  return MOE_OK;
-}
-
 template <int RT, int CT, int XI, int D, int W>
 moe_status launch_rows(const LinArgs& a, hipStream_t strm) {
   constexpr int bytes = W * D * kSlot<CT, RT, 1>;
   static_assert(bytes <= 160 * 1024, "LDS");
-  const auto k = k_linear_rows<RT, CT, XI, D, W>;
-  if (allow_lds(k, bytes) != MOE_OK) return MOE_ERR_HIP;
+  constexpr auto k = k_linear_rows<RT, CT, XI, D, W>;
+  if (!lds_allowed<k>(bytes)) return MOE_ERR_HIP;
   hipLaunchKernelGGL(k, dim3((unsigned)((a.N + 16 * CT - 1) / (16 * CT)), (unsigned)((a.M + 16 * RT - 1) / (16 * RT))),
                      dim3(W * kWave), bytes, strm, a);
   return launch_status();
 }
 
-#ifndef L_BK
-#define L_BK 128
-#define L_S 2
-#define L_GM 8
-#endif
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+// Tile t of mt x nt tiles: XCD x (workgroups are dealt round-robin) takes the x-th
+// eighth of them, in groups of eight row tiles, column by column, so that the tiles in
+// flight on an XCD share operands in its L2.
+__device__ __forceinline__ void tile_of(int t, int mt, int nt, int BM, int BN, int64_t& m0, int64_t& n0) {
+  constexpr int GM = 8;
+  const int tiles = mt * nt, x = t & 7, q = tiles >> 3, rem = tiles & 7;
+  t = x * q + (x < rem ? x : rem) + (t >> 3);
+  const int group = GM * nt, g = t / group, in = t - g * group;
+  const int rows = mt - g * GM < GM ? mt - g * GM : GM;
+  m0 = (int64_t)(g * GM + in % rows) * BM;
+  n0 = (int64_t)(in / rows) * BN;
+}
 
 template <int BM, int BN, int WM, int WN, int BK, int S>
 __global__ __launch_bounds__(WM* WN* kWave, (BM * BN <= 128 * 128 ? 2 : 1) * WM * WN / 4) void k_linear_tiles(
@@ -130,17 +125,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (BM * BN <= 128 * 128 ? 2 : 1) * WM 
   constexpr int kStage = (BM + BN) * BK;
     extern __shared__ __attribute__((aligned(16))) char lds[];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  // XCD x (workgroups are dealt round-robin) takes the x-th eighth of the tiles, in
-  // groups of L_GM row tiles, column by column
-  const int tiles = mt * nt;
-  int t = blockIdx.x;
-  {
-    const int x = t & 7, i = t >> 3, q = tiles >> 3, rem = tiles & 7;
-    t = x * q + (x < rem ? x : rem) + i;
-  }
-  const int group = L_GM * nt, g = t / group, in = t - g * group;
-  const int rows = mt - g * L_GM < L_GM ? mt - g * L_GM : L_GM;
-  const int64_t m0 = (int64_t)(g * L_GM + in % rows) * BM, n0 = (int64_t)(in / rows) * BN;
+  int64_t m0, n0;
+  tile_of(blockIdx.x, mt, nt, BM, BN, m0, n0);
   const uint32_t K = (uint32_t)a.K;
   const int64_t ml = a.M - m0 < BM ? a.M - m0 : BM, nl = a.N - n0 < BN ? a.N - n0 : BN;
   const i32x4_t ra = buffer_of(a.xq + m0 * a.K, ml * a.K), rb = buffer_of(a.wq + n0 * a.K, nl * a.K);
@@ -154,11 +140,9 @@ __global__ __launch_bounds__(WM* WN* kWave, (BM * BN <= 128 * 128 ? 2 : 1) * WM 
     vo[j] = (uint32_t)(r < lim ? r : lim) * K + kc[j];
   }
   const int nk = (int)((a.K + BK - 1) / BK);
-#ifndef L_ROT
-#define L_ROT 2
-#endif
-  const int mi = (int)(m0 / BM), ni = (int)(n0 / BN);
-  const int ks = (L_ROT == 0 ? 0 : L_ROT == 1 ? (mi + ni) % 8 : L_ROT == 2 ? 2 * ((mi + ni) % 16) : L_ROT == 3 ? 2 * ((mi * 5 + ni * 3) % 16) : (mi * 7 + ni * 11)) % nk;
+  // tiles that share rows start at different steps, so that they do not ask the same
+  // L2 channels for the same lines at once
+  const int ks = (int)((2 * (m0 / BM + n0 / BN)) % 32) % nk;
   auto issue = [&](int st, int kt) {
     kt = kt + ks < nk ? kt + ks : kt + ks - nk;
     const char* base = lds + st * kStage;
@@ -301,8 +285,8 @@ moe_status launch_tiles(const LinArgs& a, hipStream_t strm) {
   constexpr int stages = S * (BM + BN) * BK, outs = BM * (BN * 2 + 16);
   constexpr int bytes = stages > outs ? stages : outs;
   static_assert(bytes <= 160 * 1024, "LDS");
-  const auto k = k_linear_tiles<BM, BN, WM, WN, BK, S>;
-  if (allow_lds(k, bytes) != MOE_OK) return MOE_ERR_HIP;
+  constexpr auto k = k_linear_tiles<BM, BN, WM, WN, BK, S>;
+  if (!lds_allowed<k>(bytes)) return MOE_ERR_HIP;
   hipLaunchKernelGGL(k, dim3((unsigned)(mt * nt)), dim3(WM * WN * kWave), bytes, strm, a, mt, nt);
   return launch_status();
 }
@@ -320,29 +304,47 @@ bool misaligned(const void* p, const void* q) {
   return (reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) % 16 != 0;
 }
 
+// The kernel is chosen by its estimated time (us), from what each cost on MI355X with
+// cold weights: the tiled kernels take ceil(tiles / 256) rounds of K / 128 steps of
+// 0.44 (64 x 128), 0.60 (128 x 128), 1.0 (128 x 256) and 1.75 us (256 x 256), the
+// row kernel moves (64 + 16 CT) K bytes for each workgroup at 45 bytes per ns and CU.
+// Measured / estimated: 64 x 7168 x 7168 18.9 / 18.3 (rows, CT 2), 25.6 with CT 4, 32.6
+// on 64 x 128; 200 x 2048 x 2048 6.6 / 7.4 (rows), 10.2 on 64 x 128; 512 x 4096 x 7168
+// 30.5 / 29.6 (64 x 128), 38.6 by rows, 56 on 128 x 256; 1024 x 7168 x 7168 66 / 61
+// (128 x 256), 99 on 256 x 256; 4096 x 4096 x 7168 114 / 103 (256 x 256), 132 on
+// 128 x 256.
 moe_status linear_impl(const LinArgs& a, hipStream_t strm) {
+  // up to 16 rows: two column tiles for each wave, which halves the rows' share of the
+  // loads, where that leaves half a CU's worth of workgroups (16 x 7168 x 7168 12.9
+  // against 14.3 us; 1 x 2048 x 7168 8.9 against 6.5 us)
+  if (a.M <= 8 && a.N < 4096) return launch_rows<1, 1, 1, 2, 8>(a, strm);
+  if (a.M <= 8) return launch_rows<1, 2, 1, 2, 4>(a, strm);
+  if (a.M <= 16 && a.N < 4096) return launch_rows<1, 1, 2, 2, 8>(a, strm);
+  if (a.M <= 16) return launch_rows<1, 2, 2, 2, 4>(a, strm);
+  if (a.M <= 32) return launch_rows<2, 2, 2, 1, 8>(a, strm);
+  auto up = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
+  const double steps = up(a.K, 128);
+  auto tiled = [&](int bm, int bn, double c) { return up((int64_t)(up(a.M, bm) * up(a.N, bn)), 256) * steps * c + 5; };
+  auto rows = [&](int ct) {
+    return std::max(1.0, up(a.M, 64) * up(a.N, 16 * ct) / 256) * (64 + 16 * ct) * (double)a.K / 45e3 + 3;
+  };
+  const double t[6] = {rows(2), rows(4), tiled(64, 128, 0.44), tiled(128, 128, 0.60), tiled(128, 256, 1.0),
+                       tiled(256, 256, 1.75)};
+  int best = 0;
+  // (the row kernel's workgroups: ceil(M / 64) lie along the grid's second axis)
+  for (int i = a.M > 64 * 65535 ? 2 : 1; i < 6; ++i)
+    if (t[i] < t[best] || (best < 2 && a.M > 64 * 65535)) best = i;
 #ifdef FORCE
-  if (FORCE == 1) return launch_tiles<256, 256, 2, 4, 128, 2>(a, strm);
-  if (FORCE == 2) return launch_tiles<128, 128, 2, 2, 128, 2>(a, strm);
-  if (FORCE == 3) return launch_tiles<64, 128, 2, 2, 128, 3>(a, strm);
-  if (FORCE == 4) return launch_tiles<64, 128, 2, 2, 128, 6>(a, strm);
-  if (FORCE == 5) return launch_tiles<64, 64, 2, 2, 128, 4>(a, strm);
-  if (FORCE == 6) return launch_tiles<64, 64, 2, 2, 128, 8>(a, strm);
-  if (FORCE == 7) return launch_tiles<64, 32, 2, 1, 128, 6>(a, strm);
-  if (FORCE == 8) return launch_tiles<128, 128, 2, 2, 128, 4>(a, strm);
-  if (FORCE == 9) return launch_tiles<128, 256, 2, 4, 128, 3>(a, strm);
+  best = FORCE;
 #endif
-#ifndef FORCE
-  if (a.M > 64) {
-    const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-    if (big >= 200) return launch_tiles<256, 256, 2, 4, 128, 2>(a, strm);
-    return launch_tiles<128, 128, 2, 2, 128, 2>(a, strm);
+  switch (best) {
+    case 0: return launch_rows<4, 2, 2, 1, 8>(a, strm);
+    case 1: return launch_rows<4, 4, 2, 2, 4>(a, strm);
+    case 2: return launch_tiles<64, 128, 2, 4, 128, 3>(a, strm);
+    case 3: return launch_tiles<128, 128, 2, 4, 128, 4>(a, strm);
+    case 4: return launch_tiles<128, 256, 2, 4, 128, 3>(a, strm);
+    default: return launch_tiles<256, 256, 2, 4, 128, 2>(a, strm);
   }
-#endif
-  if (a.M <= 8) return launch_rows<1, R_CT, 1, R_D, R_W>(a, strm);
-  if (a.M <= 16) return launch_rows<1, R_CT, 2, R_D, R_W>(a, strm);
-  if (a.M <= 32) return launch_rows<2, R_CT, 2, R_D, R_W>(a, strm);
-  return launch_rows<4, R_CT, 2, R_D, R_W>(a, strm);
 }
 
 }  // namespace

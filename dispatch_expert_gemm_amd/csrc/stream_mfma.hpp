@@ -15,6 +15,8 @@
 // does not matter.
 #pragma once
 
+#include <atomic>
+
 #include "common.hpp"
 
 namespace moe {
@@ -219,6 +221,24 @@ __device__ __forceinline__ float quant_row_int8(int64_t n, float* red, Get get8,
     put2(i, make_uint2(i8x4(f[0], f[1], f[2], f[3], inv), i8x4(f[4], f[5], f[6], f[7], inv)));
   }
   return scale;
+}
+
+// More than 64 KB of dynamic LDS has to be asked for, once for each kernel, size and
+// device (the largest size asked for so far holds for smaller ones).
+template <auto KERNEL>
+bool lds_allowed(int bytes) {
+  if (bytes <= 65536) return true;
+  constexpr int kDevices = 64;
+  static std::atomic<int> asked[kDevices];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return false;
+  if (dev < kDevices && asked[dev].load(std::memory_order_relaxed) >= bytes) return true;
+  // (two threads may ask at once: both for the whole 160 KB, so either order serves)
+  if (hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize,
+                          160 * 1024) != hipSuccess)
+    return false;
+  if (dev < kDevices) asked[dev].store(160 * 1024, std::memory_order_relaxed);
+  return true;
 }
 
 }  // namespace moe
