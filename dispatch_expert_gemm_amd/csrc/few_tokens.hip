@@ -36,27 +36,27 @@ namespace {
 
 constexpr int kMaxTokens = 64, kMaxSlots = 1024, kMaxExperts = 1024;
 
-// Sizes of the work, by the row tiles (16 rows) that T tokens may need, RTM = 1, 2
-// or 4.  Waves split the contraction; CT column tiles of a wave share its
-// activation rows; a wave's ring of LDS holds D steps.  (Up: gate/up, Down: down
-// that sums over the experts, Y: down by expert.)
-#ifndef UP_W
-#define UP_W 4
-#define DN_W 8
-#define Y_W 4
-#define UP_KS 16
-#define Y_KS 16
-#define DN_CT 2
-#define Y_CT 4
-#define UP_R 16384
-#define DN_R 16384
-#define Y_R 24576
-#endif
-constexpr int kUpWaves = UP_W, kDownWaves = DN_W, kYWaves = Y_W;
-constexpr int kDownCT = DN_CT, kYCT = Y_CT;
-constexpr int kUpRing = UP_R, kDownRing = DN_R, kYRing = Y_R;  // bytes of a wave's ring
+// Sizes of the work.  Up: gate/up, Down: down that sums over the experts, Y: down by
+// expert.  A wave's ring of LDS holds D steps of its operands; CT column tiles of a
+// wave share its activation rows.
+constexpr int kUpWaves = 4, kDownWaves = 8, kYWaves = 4;
+template <int RTM>
+constexpr int kUpRing = RTM == 1 ? 12288 : 16384;
+// steps of H below which a wave has its columns to itself, and steps of F likewise (Y)
+constexpr int kUpOwn = 16, kYOwn = 40;
+constexpr int kDownRing = 12288;
+// Y, by the waves KS that split the contraction: a long one wants few reads of h
+// (F = 14336 in bf16, 64 tokens: 180 us, with two column tiles 206 to 227), a short one
+// more workgroups on a CU, whose beginnings and ends overlap (64 experts of F = 480 in
+// int8: 13.4 us, with four column tiles 19)
+template <int KS>
+constexpr int kYCT = KS == 1 ? 2 : 4;
+template <bool I8, int RTM, int KS>
+constexpr int kYRing = KS > 1 ? 24576 : (I8 || RTM < 4 ? 12288 : 20480);
 template <int NW, int RT, int PX, int RING>
 constexpr int kDepth = RING / kSlot<NW, RT, PX> < 1 ? 1 : (RING / kSlot<NW, RT, PX> > 4 ? 4 : RING / kSlot<NW, RT, PX>);
+// int8, one or two tokens: the rows' codes are formed by the kernels that use them
+constexpr int kHeldTokens = 2, kHeldUpDepth = 2, kHeldDownDepth = 3, kHeldBytes = 49152;
 
 struct FewArgs {
   const int32_t* idx;
@@ -230,6 +230,15 @@ __device__ void route_lds(const FewArgs& a, const Route& r) {
   __syncthreads();
 }
 
+// Values 8 i .. 8 i + 7 of a row of x, times its smooth scales (NULL: 1).
+__device__ __forceinline__ void x_times_smooth(const uint4& x, const float* smooth, int64_t i, float* f) {
+  unpack8(x, f);
+  if (!smooth) return;
+  const float4 p = reinterpret_cast<const float4*>(smooth)[2 * i], q = reinterpret_cast<const float4*>(smooth)[2 * i + 1];
+  f[0] = __fmul_rn(f[0], p.x); f[1] = __fmul_rn(f[1], p.y); f[2] = __fmul_rn(f[2], p.z); f[3] = __fmul_rn(f[3], p.w);
+  f[4] = __fmul_rn(f[4], q.x); f[5] = __fmul_rn(f[5], q.y); f[6] = __fmul_rn(f[6], q.z); f[7] = __fmul_rn(f[7], q.w);
+}
+
 // The first workgroup routes the call for the kernels behind it (ROUTE); int8: one
 // more for each row of codes: the tokens' rows, then (with smooth scales) the slots'
 // rows x_t * smooth[e].  Slots that are not routed to an expert are left out.
@@ -260,19 +269,18 @@ __global__ __launch_bounds__(256) void k_few_prep(FewArgs a) {
     const float s = quant_row_int8<4>(
         a.H, reinterpret_cast<float*>(lds),
         [&](int64_t i, float* f) {
-          const uint4 v = src[i];
-          if (sm) {
-            const float4 p = reinterpret_cast<const float4*>(sm)[2 * i], q = reinterpret_cast<const float4*>(sm)[2 * i + 1];
-            unpack8(v, f);
-            f[0] = __fmul_rn(f[0], p.x); f[1] = __fmul_rn(f[1], p.y); f[2] = __fmul_rn(f[2], p.z); f[3] = __fmul_rn(f[3], p.w);
-            f[4] = __fmul_rn(f[4], q.x); f[5] = __fmul_rn(f[5], q.y); f[6] = __fmul_rn(f[6], q.z); f[7] = __fmul_rn(f[7], q.w);
-          } else {
-            unpack8(v, f);
-          }
+          x_times_smooth(src[i], sm, i, f);
         },
         [&](int64_t i, uint2 c) { dst[i] = c; });
     if (threadIdx.x == 0) a.xs[r] = s;
   }
+}
+
+// Values 8 i .. 8 i + 7 of a fp32 row.
+__device__ __forceinline__ void load8(const float4* src, int64_t i, float* f) {
+  const float4 p = src[2 * i], q = src[2 * i + 1];
+  f[0] = p.x; f[1] = p.y; f[2] = p.z; f[3] = p.w;
+  f[4] = q.x; f[5] = q.y; f[6] = q.z; f[7] = q.w;
 }
 
 // int8: one workgroup per row of h: the slots' rows, then the shared expert's.
@@ -288,9 +296,7 @@ __global__ __launch_bounds__(256) void k_few_quant_h(FewArgs a) {
   const float s = quant_row_int8<4>(
       n, red,
       [&](int64_t i, float* f) {
-        const float4 p = src[2 * i], q = src[2 * i + 1];
-        f[0] = p.x; f[1] = p.y; f[2] = p.z; f[3] = p.w;
-        f[4] = q.x; f[5] = q.y; f[6] = q.z; f[7] = q.w;
+        load8(src, i, f);
       },
       [&](int64_t i, uint2 c) { dst[i] = c; });
   if (threadIdx.x == 0) (sh ? a.shs : a.hs)[row] = s;
@@ -309,13 +315,11 @@ __device__ __forceinline__ void row_offsets(int n, int64_t bytes, uint32_t (&xof
     }
 }
 
-// G and U of four columns (from f0 on) of one row -> h.
+// G and U of four columns of one row (int8: of scale xs) -> h at `at`.
 template <bool I8>
-__device__ __forceinline__ void swiglu_store(const FewArgs& a, bool sh, int slot, int xrow, int64_t wrow, int64_t at,
+__device__ __forceinline__ void swiglu_store(const FewArgs& a, bool sh, int slot, float xs, int64_t wrow, int64_t at,
                                              const typename MfmaAcc<I8>::type& sg, const typename MfmaAcc<I8>::type& su) {
   float h[4];
-  float xs = 1.f;
-  if constexpr (I8) xs = a.xs[xrow];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     float g = (float)sg[q], u = (float)su[q];
@@ -344,7 +348,7 @@ __device__ __forceinline__ void swiglu_store(const FewArgs& a, bool sh, int slot
 // An expert's rows (at most 16 RT, XI = 1: 8) through its gate and up columns from f0
 // on, 16 of each for every KS waves, which split the contraction.  `slots`: the
 // expert's slots, NULL for the shared expert (row = token).  lds: the waves' rings.
-template <bool I8, int RT, int XI, int KS>
+template <bool I8, int RT, int XI, int KS, int RING>
 __device__ __forceinline__ void gate_up_rows(const FewArgs& a, const uint16_t* slots, int n, int e, int64_t f0,
                                              char* lds) {
   typedef typename MfmaAcc<I8>::type Acc;
@@ -367,27 +371,28 @@ __device__ __forceinline__ void gate_up_rows(const FewArgs& a, const uint16_t* s
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[g][r] = Acc{0, 0, 0, 0};
   const int ns = in ? stream_steps(bytes) : 0, part = wave % KS;
-  stream_mfma<I8, 2, RT, 1, XI, kDepth<2, RT, 1, kUpRing>>(w, x, xoff, bytes, ns * part / KS, ns * (part + 1) / KS,
-                                                          lds + wave * kUpRing, acc);
+  static_assert(kSlot<2, RT, 1> <= RING, "a ring holds a step");
+  stream_mfma<I8, 2, RT, 1, XI, kDepth<2, RT, 1, RING>>(w, x, xoff, bytes, ns * part / KS, ns * (part + 1) / KS,
+                                                          lds + wave * RING, acc);
   const int64_t c = 4 * (lane / 16);
   auto finish = [&](int r, const Acc& g, const Acc& u) {
     const int i = 16 * r + lane % 16;
     if (!in || i >= n) return;
     const int slot = sh ? i : slots[i];
-    swiglu_store<I8>(a, sh, slot, x_row(slot), wrow + c, (int64_t)slot * F + f0 + c, g, u);
+    swiglu_store<I8>(a, sh, slot, I8 ? a.xs[x_row(slot)] : 1.f, wrow + c, (int64_t)slot * F + f0 + c, g, u);
   };
   if constexpr (KS == 1) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) finish(r, acc[0][r], acc[1][r]);
   } else {
-    static_assert(KS == kUpWaves && RT <= KS && 2 * RT * 1024 <= kUpRing, "parts");
+    static_assert(KS == kUpWaves && RT <= KS && 2 * RT * 1024 <= RING, "parts");
     // the waves' parts meet in their rings' place
     float4* red = reinterpret_cast<float4*>(lds);
 #pragma unroll
     for (int g = 0; g < 2; ++g)
 #pragma unroll
       for (int r = 0; r < RT; ++r)
-        red[wave * (kUpRing / 16) + (g * RT + r) * kWave + lane] = __builtin_bit_cast(float4, acc[g][r]);
+        red[wave * (RING / 16) + (g * RT + r) * kWave + lane] = __builtin_bit_cast(float4, acc[g][r]);
     __syncthreads();
     if (wave < RT) {
       Acc s[2];
@@ -396,16 +401,61 @@ __device__ __forceinline__ void gate_up_rows(const FewArgs& a, const uint16_t* s
         s[g] = Acc{0, 0, 0, 0};
 #pragma unroll
         for (int v = 0; v < KS; ++v)
-          s[g] += __builtin_bit_cast(Acc, red[v * (kUpRing / 16) + (g * RT + wave) * kWave + lane]);
+          s[g] += __builtin_bit_cast(Acc, red[v * (RING / 16) + (g * RT + wave) * kWave + lane]);
       }
       finish(wave, s[0], s[1]);
     }
   }
 }
 
+// gate_up_rows for one or two tokens in int8: the rows are quantised here, behind the
+// first weight loads (every workgroup of an expert does it again: a launch of its own
+// costs about 5 us).  lds: the waves' rings, the codes, scales and maxima.
+__device__ __forceinline__ void gate_up_held(const FewArgs& a, const uint16_t* slots, int n, int e, int64_t f0,
+                                             char* lds) {
+  constexpr int W = kUpWaves, RING = kHeldUpDepth * kSlot<2, 0, 0>;
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, pitch = held_pitch(a.H);
+  const bool sh = slots == nullptr;
+  const int64_t F = sh ? a.Fs : a.F, wrow = (sh ? 0 : (int64_t)e * F) + f0;
+  char* codes = lds + W * RING;
+  float* scales = reinterpret_cast<float*>(codes + a.T * pitch);
+  float* red = scales + kHeldTokens;
+  const i32x4_t w[2] = {buffer_of(static_cast<const char*>(sh ? a.swg : a.wg) + wrow * a.H, 16 * a.H),
+                        buffer_of(static_cast<const char*>(sh ? a.swu : a.wu) + wrow * a.H, 16 * a.H)};
+  i32x4_t acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  const int ns = stream_steps(a.H), mine = lane % 16 < n ? lane % 16 : 0;
+  const float* sm = sh || !a.smooth ? nullptr : a.smooth + (int64_t)e * a.H;
+  stream_held<2, kHeldUpDepth>(w, codes + mine * pitch + 16 * (lane / 16), a.H, ns * wave / W, ns * (wave + 1) / W,
+                               lds + wave * RING, acc, [&] {
+    quant_rows_int8<W, kHeldTokens, 4>(
+        n, a.H, red,
+        [&](int r, int64_t i, float* f) {
+          const int t = sh ? r : slots[r] / a.K;
+          x_times_smooth(reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H)[i], sm, i, f);
+        },
+        [&](int r, int64_t i, uint2 c) { *reinterpret_cast<uint2*>(codes + r * pitch + 8 * i) = c; },
+        [&](int r, float s) { scales[r] = s; });
+    held_pad<W * kWave>(codes, n, a.H, pitch);
+    __syncthreads();
+  });
+  i32x4_t* red2 = reinterpret_cast<i32x4_t*>(lds);
+#pragma unroll
+  for (int g = 0; g < 2; ++g) red2[wave * (RING / 16) + g * kWave + lane] = acc[g];
+  __syncthreads();
+  if (wave > 0 || lane % 16 >= n) return;
+  i32x4_t s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+  for (int g = 0; g < 2; ++g)
+#pragma unroll
+    for (int v = 0; v < W; ++v) s[g] += red2[v * (RING / 16) + g * kWave + lane];
+  const int slot = sh ? mine : slots[mine];
+  const int64_t c = 4 * (lane / 16);
+  swiglu_store<true>(a, sh, slot, scales[mine], wrow + c, (int64_t)slot * F + f0 + c, s[0], s[1]);
+}
+
 // RTM: row tiles that T tokens may need (1, 2 or 4).  RTM = 1 routes for itself, and
 // the first workgroup for the kernels behind it.
-template <bool I8, int RTM, int KS>
+template <bool I8, int RTM, int KS, bool HELD>
 __global__ __launch_bounds__(kUpWaves* kWave, 2) void k_few_gate_up(FewArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   constexpr int COLS = 16 * kUpWaves / KS;
@@ -429,11 +479,24 @@ __global__ __launch_bounds__(kUpWaves* kWave, 2) void k_few_gate_up(FewArgs a) {
   const uint16_t* slots = sh ? nullptr : route.slot + b;
   const int n = sh ? a.T : uniform(route.begin[g + 1]) - b, e = sh ? 0 : uniform(route.expert[g]);
   const int64_t f0 = (int64_t)(sh ? it - routed : it - g * tiles) * COLS;
-  const int rt = (n + 15) / 16;
-  if (RTM > 2 && rt > 2) gate_up_rows<I8, RTM, 2, KS>(a, slots, n, e, f0, rings);
-  else if (RTM > 1 && rt > 1) gate_up_rows<I8, RTM < 2 ? 1 : 2, 2, KS>(a, slots, n, e, f0, rings);
-  else if (n > 8) gate_up_rows<I8, 1, 2, KS>(a, slots, n, e, f0, rings);
-  else gate_up_rows<I8, 1, 1, KS>(a, slots, n, e, f0, rings);
+  if constexpr (HELD) {
+    gate_up_held(a, slots, n, e, f0, rings);
+  } else {
+    constexpr int RING = kUpRing<RTM>;
+    const int rt = (n + 15) / 16;
+    if (RTM > 2 && rt > 2) gate_up_rows<I8, RTM, 2, KS, RING>(a, slots, n, e, f0, rings);
+    else if (RTM > 1 && rt > 1) gate_up_rows<I8, RTM < 2 ? 1 : 2, 2, KS, RING>(a, slots, n, e, f0, rings);
+    else if (n > 8) gate_up_rows<I8, 1, 2, KS, RING>(a, slots, n, e, f0, rings);
+    else gate_up_rows<I8, 1, 1, KS, RING>(a, slots, n, e, f0, rings);
+  }
+}
+
+// Column tile c from c0 on of an expert's W_down: columns past H lie past the buffer, a
+// tile past H reads the first one.
+__device__ __forceinline__ i32x4_t down_weights(const FewArgs& a, bool sh, int e, int64_t c0, int c, int64_t bytes) {
+  const int64_t col = c0 + (c0 + 16 * c < a.H ? 16 * c : 0), left = a.H - col;
+  return buffer_of(static_cast<const char*>(sh ? a.swd : a.wd) + ((sh ? 0 : (int64_t)e * a.H) + col) * bytes,
+                   (left < 16 ? left : 16) * bytes);
 }
 
 // One expert's packed rows (at most 16 RT, XI = 1: 8) through 16 CT columns of H from
@@ -447,10 +510,7 @@ __device__ __forceinline__ void down_stream(const FewArgs& a, const uint16_t* sl
   i32x4_t w[CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
-    // columns past H lie past the buffer; a column tile past H reads the first one
-    const int64_t col = c0 + (c0 + 16 * c < a.H ? 16 * c : 0), left = a.H - col;
-    w[c] = buffer_of(static_cast<const char*>(sh ? a.swd : a.wd) + ((sh ? 0 : (int64_t)e * a.H) + col) * bytes,
-                     (left < 16 ? left : 16) * bytes);
+    w[c] = down_weights(a, sh, e, c0, c, bytes);
   }
   i32x4_t x[PX];
   x[0] = buffer_of(I8 ? static_cast<const void*>(sh ? a.shq : a.hq) : static_cast<const void*>(sh ? a.shhi : a.hhi), rows * bytes);
@@ -461,14 +521,28 @@ __device__ __forceinline__ void down_stream(const FewArgs& a, const uint16_t* sl
   for (int c = 0; c < CT; ++c)
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[c][r] = typename MfmaAcc<I8>::type{0, 0, 0, 0};
+  static_assert(kSlot<CT, RT, PX> <= RING, "a ring holds a step");
   stream_mfma<I8, CT, RT, PX, XI, kDepth<CT, RT, PX, RING>>(w, x, xoff, bytes, s0, s1, ring, acc);
 }
 
+// int8, one or two tokens: the codes of every row of h in LDS (slots, then the shared
+// expert's), and their scales.
+struct HeldRows {
+  char* codes;
+  float* scales;
+};
+__host__ __device__ inline int held_h_bytes(int S, int T, int64_t F, int64_t Fs) {
+  return S * held_pitch(F) + (Fs ? T * held_pitch(Fs) : 0);
+}
+__device__ __forceinline__ int held_h_at(int S, int64_t F, int64_t Fs, bool sh, int row) {
+  return sh ? S * held_pitch(F) + row * held_pitch(Fs) : row * held_pitch(F);
+}
+
 // down_stream of at most 16 rows, the weighted results added to the wave's output
-// tile `o` (T rows of 16 CT columns).
-template <bool I8, int XI, int CT>
+// tile `o` (T rows of 16 CT columns).  XI = 0: the rows are in LDS (held).
+template <bool I8, int XI, int CT, int RING>
 __device__ __forceinline__ void down_rows(const FewArgs& a, const uint16_t* slots, int n, int e, int64_t c0, int s0,
-                                          int s1, char* ring, float (*o)[16 * CT]) {
+                                          int s1, char* ring, float (*o)[16 * CT], const HeldRows& held) {
   const int lane = threadIdx.x % kWave;
   const bool sh = slots == nullptr;
   const int64_t wrow = sh ? 0 : (int64_t)e * a.H;
@@ -476,10 +550,26 @@ __device__ __forceinline__ void down_rows(const FewArgs& a, const uint16_t* slot
   float wt = 1.f, hs = 1.f;
   if (row >= 0) {
     if (!sh) wt = a.w[row];
-    if constexpr (I8) hs = (sh ? a.shs : a.hs)[row];
+    if constexpr (XI == 0) hs = held.scales[sh ? a.T * a.K + row : row];
+    else if constexpr (I8) hs = (sh ? a.shs : a.hs)[row];
   }
   typename MfmaAcc<I8>::type acc[CT][1];
-  down_stream<I8, 1, XI, CT, kDownRing>(a, slots, n, e, c0, s0, s1, ring, acc);
+  if constexpr (XI == 0) {
+    const int64_t bytes = sh ? a.Fs : a.F;
+    const int any = row >= 0 ? row : (sh ? 0 : slots[0]);
+    i32x4_t w[CT], sum[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      w[c] = down_weights(a, sh, e, c0, c, bytes);
+      sum[c] = i32x4_t{0, 0, 0, 0};
+    }
+    stream_held<CT, RING / kSlot<CT, 0, 0>>(w, held.codes + held_h_at(a.T * a.K, a.F, a.Fs, sh, any) + 16 * (lane / 16), bytes, s0,
+                                    s1, ring, sum, [] {});
+#pragma unroll
+    for (int c = 0; c < CT; ++c) acc[c][0] = sum[c];
+  } else {
+    down_stream<I8, 1, XI, CT, RING>(a, slots, n, e, c0, s0, s1, ring, acc);
+  }
   if (row >= 0) {
     float* out = o[sh ? row : row / a.K];
 #pragma unroll
@@ -517,17 +607,41 @@ __device__ __forceinline__ void few_finish(const FewArgs& a, const int32_t* code
   a.out[t * a.H + c] = (bf16_t)f2bf(v);
 }
 
-// dynamic LDS: the routing, then kDownWaves output tiles of T rows x 16 CT columns
-template <bool I8, int CT>
+// dynamic LDS: the routing, the waves' rings and output tiles of T rows x 16 CT columns
+template <bool I8, int CT, bool HELD>
 __global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(FewArgs a) {
   constexpr int ES = I8 ? 1 : 2, COLS = 16 * CT;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const Route route = route_at(lds, a.T * a.K, a.groups);
-  char* rings = lds + route_bytes(a.T * a.K, a.groups);
-  float* tiles = reinterpret_cast<float*>(rings + kDownWaves * kDownRing);
+  constexpr int RING = HELD ? kHeldDownDepth * kSlot<CT, 0, 0> : kDownRing;
+  const int S = a.T * a.K;
+  char* rings = lds + route_bytes(S, a.groups);
+  float* tiles = reinterpret_cast<float*>(rings + kDownWaves * RING);
   const int wave = uniform(threadIdx.x / kWave);
   for (int i = threadIdx.x; i < kDownWaves * a.T * COLS; i += kDownWaves * kWave) tiles[i] = 0.f;
-  route_copy<kDownWaves * kWave>(lds, a.table, a.T * a.K, a.groups);
+  route_copy<kDownWaves * kWave>(lds, a.table, S, a.groups);
+  HeldRows held = {};
+  if constexpr (HELD) {
+    // every row of h to int8, a wave a row
+    held.scales = tiles + kDownWaves * a.T * COLS;
+    held.codes = reinterpret_cast<char*>(held.scales + (S + a.T + 3) / 4 * 4);
+    const Route table = route_at(a.table, S, a.groups);
+    for (int r = wave; r < S + (a.Fs ? a.T : 0); r += kDownWaves) {
+      const bool sh = r >= S;
+      if (!sh && uniform(table.code[r]) < 0) continue;
+      const int row = sh ? r - S : r;
+      const int64_t n = sh ? a.Fs : a.F;
+      const float4* src = reinterpret_cast<const float4*>((sh ? a.shf : a.hf) + row * n);
+      char* dst = held.codes + held_h_at(S, a.F, a.Fs, sh, row);
+      const float sc = quant_row_int8_wave(
+          n, [&](int64_t i, float* f) { load8(src, i, f); },
+          [&](int64_t i, uint2 c) { *reinterpret_cast<uint2*>(dst + 8 * i) = c; });
+      const int lane = threadIdx.x % kWave;
+      if (lane == 0) held.scales[r] = sc;
+      // zeros up to the end of the last step
+      for (int64_t i = n + 8 * lane; i < held_pitch(n) - 64; i += 8 * kWave) *reinterpret_cast<uint2*>(dst + i) = make_uint2(0u, 0u);
+    }
+  }
   __syncthreads();
   const int64_t c0 = (int64_t)blockIdx.x * COLS;
   float(*o)[COLS] = reinterpret_cast<float(*)[COLS]>(tiles) + wave * a.T;
@@ -545,8 +659,9 @@ __global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(FewArgs a) {
     const int e = sh ? 0 : uniform(route.expert[g]);
     const uint16_t* slots = sh ? nullptr : route.slot + b;
     u += s1 - s0;
-    if (n > 8) down_rows<I8, 2, CT>(a, slots, n, e, c0, s0, s1, rings + wave * kDownRing, o);
-    else down_rows<I8, 1, CT>(a, slots, n, e, c0, s0, s1, rings + wave * kDownRing, o);
+    if constexpr (HELD) down_rows<I8, 0, CT, RING>(a, slots, n, e, c0, s0, s1, rings + wave * RING, o, held);
+    else if (n > 8) down_rows<I8, 2, CT, RING>(a, slots, n, e, c0, s0, s1, rings + wave * RING, o, held);
+    else down_rows<I8, 1, CT, RING>(a, slots, n, e, c0, s0, s1, rings + wave * RING, o, held);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < a.T * COLS; i += kDownWaves * kWave) {
@@ -560,20 +675,21 @@ __global__ __launch_bounds__(kDownWaves* kWave, 2) void k_few_down(FewArgs a) {
   }
 }
 
-// One expert's rows (at most 16 RT) through columns of H from c0 on, 16 CT for every
+// One expert's rows (at most 16 RT) through columns of H from c0 on, 16 kYCT for every
 // KS waves, which split the contraction: rows of y.  lds: the waves' rings.
-template <bool I8, int RT, int XI, int CT, int KS>
+template <bool I8, int RTM, int RT, int XI, int KS>
 __device__ __forceinline__ void down_y_rows(const FewArgs& a, const uint16_t* slots, int n, int e, int64_t c0,
                                             char* lds) {
   typedef typename MfmaAcc<I8>::type Acc;
+  constexpr int CT = kYCT<KS>, RING = kYRing<I8, RTM, KS>;
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const bool sh = slots == nullptr;
   c0 += 16 * CT * (wave / KS);
   const bool in = c0 < a.H;
   Acc acc[CT][RT];
   const int ns = in ? stream_steps((sh ? a.Fs : a.F) * (I8 ? 1 : 2)) : 0, part = wave % KS;
-  down_stream<I8, RT, XI, CT, kYRing>(a, slots, n, e, in ? c0 : 0, ns * part / KS, ns * (part + 1) / KS,
-                                      lds + wave * kYRing, acc);
+  down_stream<I8, RT, XI, CT, RING>(a, slots, n, e, in ? c0 : 0, ns * part / KS, ns * (part + 1) / KS,
+                                      lds + wave * RING, acc);
   auto finish = [&](int ct, int r, const Acc& s) {
     const int i = 16 * r + lane % 16;
     const int64_t c = c0 + 16 * ct + 4 * (lane / 16);
@@ -595,28 +711,28 @@ __device__ __forceinline__ void down_y_rows(const FewArgs& a, const uint16_t* sl
 #pragma unroll
       for (int r = 0; r < RT; ++r) finish(ct, r, acc[ct][r]);
   } else {
-    static_assert(KS == kYWaves && CT * RT * 1024 <= kYRing, "parts");
+    static_assert(KS == kYWaves && CT * RT * 1024 <= RING, "parts");
     float4* red = reinterpret_cast<float4*>(lds);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
       for (int r = 0; r < RT; ++r)
-        red[wave * (kYRing / 16) + (ct * RT + r) * kWave + lane] = __builtin_bit_cast(float4, acc[ct][r]);
+        red[wave * (RING / 16) + (ct * RT + r) * kWave + lane] = __builtin_bit_cast(float4, acc[ct][r]);
     __syncthreads();
     for (int q = wave; q < CT * RT; q += KS) {
       Acc s = {0, 0, 0, 0};
 #pragma unroll
-      for (int v = 0; v < KS; ++v) s += __builtin_bit_cast(Acc, red[v * (kYRing / 16) + q * kWave + lane]);
+      for (int v = 0; v < KS; ++v) s += __builtin_bit_cast(Acc, red[v * (RING / 16) + q * kWave + lane]);
       finish(q / RT, q % RT, s);
     }
   }
 }
 
 // larger batches: a workgroup per (active expert, columns of H)
-template <bool I8, int RTM, int CT, int KS>
+template <bool I8, int RTM, int KS>
 __global__ __launch_bounds__(kYWaves* kWave, 2) void k_few_down_y(FewArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  constexpr int COLS = 16 * CT * kYWaves / KS;
+  constexpr int COLS = 16 * kYCT<KS> * kYWaves / KS;
   const Route route = route_at(a.table, a.T * a.K, a.groups);
   const int tiles = (int)((a.H + COLS - 1) / COLS);
   const int routed = uniform(route.head[0]) * tiles, items = routed + (a.Fs > 0 ? tiles : 0);
@@ -629,10 +745,10 @@ __global__ __launch_bounds__(kYWaves* kWave, 2) void k_few_down_y(FewArgs a) {
   const uint16_t* slots = sh ? nullptr : route.slot + b;
   const int n = sh ? a.T : uniform(route.begin[g + 1]) - b, e = sh ? 0 : uniform(route.expert[g]);
   const int rt = (n + 15) / 16;
-  if (RTM > 2 && rt > 2) down_y_rows<I8, RTM, 2, CT, KS>(a, slots, n, e, c0, lds);
-  else if (RTM > 1 && rt > 1) down_y_rows<I8, RTM < 2 ? 1 : 2, 2, CT, KS>(a, slots, n, e, c0, lds);
-  else if (n > 8) down_y_rows<I8, 1, 2, CT, KS>(a, slots, n, e, c0, lds);
-  else down_y_rows<I8, 1, 1, CT, KS>(a, slots, n, e, c0, lds);
+  if (RTM > 2 && rt > 2) down_y_rows<I8, RTM, RTM, 2, KS>(a, slots, n, e, c0, lds);
+  else if (RTM > 1 && rt > 1) down_y_rows<I8, RTM, RTM < 2 ? 1 : 2, 2, KS>(a, slots, n, e, c0, lds);
+  else if (n > 8) down_y_rows<I8, RTM, 1, 2, KS>(a, slots, n, e, c0, lds);
+  else down_y_rows<I8, RTM, 1, 1, KS>(a, slots, n, e, c0, lds);
 }
 
 // four outputs of one token per thread: the weighted sum of y over its slots in k
@@ -643,17 +759,25 @@ __global__ __launch_bounds__(256) void k_few_join(FewArgs a) {
   const int32_t* code = route_at(a.table, a.T * a.K, a.groups).code + t * a.K;
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (c >= a.H) return;
+  // every slot's row is read at once, also those that nothing was written to, and used
+  // or not afterwards
   float4 y[KMAX + 1];
+  int cd[KMAX];
+  float wt[KMAX];
 #pragma unroll
   for (int k = 0; k < KMAX; ++k)
-    if (k < a.K && code[k] >= 0) y[k] = *reinterpret_cast<const float4*>(a.y + ((int64_t)t * a.K + k) * a.H + c);
+    if (k < a.K) {
+      y[k] = *reinterpret_cast<const float4*>(a.y + ((int64_t)t * a.K + k) * a.H + c);
+      cd[k] = code[k];
+      wt[k] = a.w[t * a.K + k];
+    }
   if (a.Fs > 0) y[KMAX] = *reinterpret_cast<const float4*>(a.y + ((int64_t)a.T * a.K + t) * a.H + c);
   float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int k = 0; k <= KMAX; ++k) {
-    if (k < KMAX ? k >= a.K || code[k] < 0 : a.Fs == 0) continue;
-    const float wt = k < KMAX ? a.w[t * a.K + k] : 1.f;
-    v[0] += wt * y[k].x; v[1] += wt * y[k].y; v[2] += wt * y[k].z; v[3] += wt * y[k].w;
+    if (k < KMAX ? k >= a.K || cd[k < KMAX ? k : 0] < 0 : a.Fs == 0) continue;
+    const float w = k < KMAX ? wt[k < KMAX ? k : 0] : 1.f;
+    v[0] += w * y[k].x; v[1] += w * y[k].y; v[2] += w * y[k].z; v[3] += w * y[k].w;
   }
 #pragma unroll
   for (int q = 0; q < 4; ++q) few_finish(a, code, t, c + q, v[q]);
@@ -713,22 +837,46 @@ struct FewWeight {
   const float* scales;
 };
 
-template <bool I8, int RTM, int KS>
+template <bool I8, int RTM, int KS, bool HELD>
 bool launch_up(const FewArgs& a, hipStream_t strm) {
   constexpr int COLS = 16 * kUpWaves / KS;
-  const int lds = (RTM == 1 ? route_work_bytes(a.T * a.K, a.E, a.groups) : 0) + kUpWaves * kUpRing;
+  constexpr auto k = k_few_gate_up<I8, RTM, KS, HELD>;
+  const int lds = (RTM == 1 ? route_work_bytes(a.T * a.K, a.E, a.groups) : 0) +
+                  (HELD ? kUpWaves * kHeldUpDepth * kSlot<2, 0, 0> + a.T * held_pitch(a.H) + kHeldTokens * (4 + 4 * kUpWaves)
+                        : kUpWaves * kUpRing<RTM>);
   const int64_t n = a.groups * ((a.F + COLS - 1) / COLS) + (a.Fs + COLS - 1) / COLS;
-  if (!lds_allowed<k_few_gate_up<I8, RTM, KS>>(lds)) return false;
-  hipLaunchKernelGGL((k_few_gate_up<I8, RTM, KS>), dim3((unsigned)n), dim3(kUpWaves * kWave), lds, strm, a);
+  if (!lds_allowed<k>(lds)) return false;
+  hipLaunchKernelGGL(k, dim3((unsigned)n), dim3(kUpWaves * kWave), lds, strm, a);
   return true;
+}
+
+template <bool I8, int CT, bool HELD>
+bool launch_down_as(const FewArgs& a, hipStream_t strm) {
+  constexpr auto k = k_few_down<I8, CT, HELD>;
+  const int S = a.T * a.K, ring = HELD ? kHeldDownDepth * kSlot<CT, 0, 0> : kDownRing;
+  const int lds = route_bytes(S, a.groups) + kDownWaves * (ring + a.T * 16 * CT * 4) +
+                  (HELD ? (S + a.T + 3) / 4 * 16 + held_h_bytes(S, a.T, a.F, a.Fs) : 0);
+  if (!lds_allowed<k>(lds)) return false;
+  hipLaunchKernelGGL(k, dim3((unsigned)((a.H + 16 * CT - 1) / (16 * CT))), dim3(kDownWaves * kWave), lds, strm, a);
+  return true;
+}
+
+// 16 columns for a workgroup while those workgroups do not exceed the 256 CUs, else 32:
+// H = 1536 with 16 tokens 57.9 against 74.8 us for the layer, H = 4096 240 against 267;
+// H = 5120 with 4 tokens 134.9 against 128.2, H = 7168 equal (int8 4 us slower with 16).
+// Sixteen or four waves: within 2% of eight, H = 1536 more than 10% slower.
+template <bool I8, bool HELD>
+bool launch_down(const FewArgs& a, hipStream_t strm) {
+  return a.H <= 16 * 256 ? launch_down_as<I8, 1, HELD>(a, strm) : launch_down_as<I8, 2, HELD>(a, strm);
 }
 
 template <bool I8, int RTM, int KS>
 bool launch_y(const FewArgs& a, hipStream_t strm) {
-  constexpr int COLS = 16 * kYCT * kYWaves / KS, lds = kYWaves * kYRing;
+  constexpr int COLS = 16 * kYCT<KS> * kYWaves / KS, lds = kYWaves * kYRing<I8, RTM, KS>;
+  constexpr auto k = k_few_down_y<I8, RTM, KS>;
   const int64_t n = (a.groups + (a.Fs > 0)) * ((a.H + COLS - 1) / COLS);
-  if (!lds_allowed<k_few_down_y<I8, RTM, kYCT, KS>>(lds)) return false;
-  hipLaunchKernelGGL((k_few_down_y<I8, RTM, kYCT, KS>), dim3((unsigned)n), dim3(kYWaves * kWave), lds, strm, a);
+  if (!lds_allowed<k>(lds)) return false;
+  hipLaunchKernelGGL(k, dim3((unsigned)n), dim3(kYWaves * kWave), lds, strm, a);
   const dim3 grid((unsigned)((a.H + 1023) / 1024), (unsigned)a.T);
   if (a.K <= 8) hipLaunchKernelGGL(k_few_join<8>, grid, dim3(256), 0, strm, a);
   else hipLaunchKernelGGL(k_few_join<16>, grid, dim3(256), 0, strm, a);
@@ -739,23 +887,22 @@ template <bool I8, int RTM>
 moe_status few_launch(FewArgs& a, hipStream_t strm) {
   constexpr int ES = I8 ? 1 : 2;
   constexpr bool ROUTE = RTM > 1;
-  const int S = a.T * a.K, rb = route_bytes(S, a.groups), rw = route_work_bytes(S, a.E, a.groups);
+  const int S = a.T * a.K;
+  if constexpr (I8 && RTM == 1) {
+    if (a.T <= kHeldTokens && a.H <= 4 * 8 * kUpWaves * kWave && held_h_bytes(S, a.T, a.F, a.Fs) <= kHeldBytes)
+      return launch_up<true, 1, kUpWaves, true>(a, strm) && launch_down<true, true>(a, strm) ? launch_status() : MOE_ERR_HIP;
+  }
   if (ROUTE || I8)
     hipLaunchKernelGGL((k_few_prep<ROUTE, I8>), dim3((ROUTE ? 1 : 0) + (I8 ? a.T + (a.smooth ? S : 0) : 0)), dim3(256),
-                       ROUTE ? rw : 16, strm, a);
+                       ROUTE ? route_work_bytes(S, a.E, a.groups) : 16, strm, a);
   // waves split a long contraction; a short one is a wave's own
-  bool ok = stream_steps(a.H * ES) < UP_KS ? launch_up<I8, RTM, 1>(a, strm) : launch_up<I8, RTM, kUpWaves>(a, strm);
+  bool ok = stream_steps(a.H * ES) < kUpOwn ? launch_up<I8, RTM, 1, false>(a, strm)
+                                           : launch_up<I8, RTM, kUpWaves, false>(a, strm);
   if (I8) hipLaunchKernelGGL(k_few_quant_h, dim3(S + (a.Fs ? a.T : 0)), dim3(256), 0, strm, a);
-  if constexpr (RTM == 1) {
-    constexpr auto kDown = k_few_down<I8, kDownCT>;
-    const int lds = rb + kDownWaves * (kDownRing + a.T * 16 * kDownCT * 4);
-    ok = ok && lds_allowed<kDown>(lds);
-    if (ok)
-      hipLaunchKernelGGL(kDown, dim3((unsigned)((a.H + 16 * kDownCT - 1) / (16 * kDownCT))), dim3(kDownWaves * kWave), lds,
-                         strm, a);
-  } else {
-    ok = ok && (stream_steps(a.F * ES) < Y_KS ? launch_y<I8, RTM, 1>(a, strm) : launch_y<I8, RTM, kYWaves>(a, strm));
-  }
+  if constexpr (RTM == 1)
+    ok = ok && launch_down<I8, false>(a, strm);
+  else
+    ok = ok && (stream_steps(a.F * ES) < kYOwn ? launch_y<I8, RTM, 1>(a, strm) : launch_y<I8, RTM, kYWaves>(a, strm));
   return ok ? launch_status() : MOE_ERR_HIP;
 }
 

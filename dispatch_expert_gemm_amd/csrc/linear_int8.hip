@@ -90,6 +90,66 @@ __global__ __launch_bounds__(W* kWave, 2) void k_linear_rows(LinArgs a) {
   }
 }
 
+// The dynamic product of one or two rows in one launch: every workgroup quantises the
+// rows for itself, into LDS, behind its first weight loads.  1 x 7168 x 7168 12.9 us
+// against 16.5 with a launch for the codes, two rows 14.9 against 17.1; with four rows
+// the workgroups' work on the rows costs more than the launch (18.5 against 17.1).
+constexpr int kHeldWaves = 8, kHeldPer = 2;
+template <int ROWS, int CT, int D>
+__global__ __launch_bounds__(kHeldWaves* kWave, 2) void k_linear_held(LinArgs a, const uint4* x) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  constexpr int W = kHeldWaves, RING = D * kSlot<CT, 0, 0>;
+  // dynamic LDS: the rings, the rows' codes, their scales and the quantiser's maxima
+  const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, M = (int)a.M, pitch = held_pitch(a.K);
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * CT);
+  char* codes = lds + W * RING;
+  float* scales = reinterpret_cast<float*>(codes + M * pitch);
+  float* red = scales + ROWS;
+  i32x4_t w[CT], acc[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    const int64_t col = n0 + (n0 + 16 * c < a.N ? 16 * c : 0), left = a.N - col;
+    w[c] = buffer_of(a.wq + col * a.K, (left < 16 ? left : 16) * a.K);
+    acc[c] = i32x4_t{0, 0, 0, 0};
+  }
+  const int ns = stream_steps(a.K), row = lane % 16 < M ? lane % 16 : 0;
+  stream_held<CT, D>(w, codes + row * pitch + 16 * (lane / 16), a.K, ns * wave / W, ns * (wave + 1) / W,
+                              lds + wave * RING, acc, [&] {
+    quant_rows_int8<W, ROWS, kHeldPer>(
+        M, a.K, red, [&](int r, int64_t i, float* f) { unpack8(x[r * (a.K / 8) + i], f); },
+        [&](int r, int64_t i, uint2 c) { *reinterpret_cast<uint2*>(codes + r * pitch + 8 * i) = c; },
+        [&](int r, float s) { scales[r] = s; });
+    held_pad<W * kWave>(codes, M, a.K, pitch);
+    __syncthreads();
+  });
+  // the waves' parts in their rings' place
+  i32x4_t* part = reinterpret_cast<i32x4_t*>(lds);
+#pragma unroll
+  for (int c = 0; c < CT; ++c) part[wave * (RING / 16) + c * kWave + lane] = acc[c];
+  __syncthreads();
+  if (wave >= CT || lane % 16 >= M) return;
+  i32x4_t s = {0, 0, 0, 0};
+#pragma unroll
+  for (int v = 0; v < W; ++v) s += part[v * (RING / 16) + wave * kWave + lane];
+  const int64_t m = lane % 16, c0 = n0 + 16 * wave + 4 * (lane / 16);
+  const float xs = scales[m];
+  for (int i = 0; i < 4 && c0 + i < a.N; ++i) {
+    float f = (float)s[i] * __fmul_rn(xs, a.ws[c0 + i]);
+    if (a.bias) f += a.bias[c0 + i];
+    a.out[m * a.N + c0 + i] = (bf16_t)f2bf(f);
+  }
+}
+
+template <int ROWS, int CT, int D>
+moe_status launch_held(const LinArgs& a, const void* x, hipStream_t strm) {
+  const int bytes = kHeldWaves * D * kSlot<CT, 0, 0> + (int)a.M * held_pitch(a.K) + ROWS * (1 + kHeldWaves) * 4;
+  constexpr auto k = k_linear_held<ROWS, CT, D>;
+  if (!lds_allowed<k>(bytes)) return MOE_ERR_HIP;
+  hipLaunchKernelGGL(k, dim3((unsigned)((a.N + 16 * CT - 1) / (16 * CT))), dim3(kHeldWaves * kWave), bytes, strm, a,
+                     static_cast<const uint4*>(x));
+  return launch_status();
+}
+
 template <int RT, int CT, int XI, int D, int W>
 moe_status launch_rows(const LinArgs& a, hipStream_t strm) {
   constexpr int bytes = W * D * kSlot<CT, RT, 1>;
@@ -334,9 +394,6 @@ moe_status linear_impl(const LinArgs& a, hipStream_t strm) {
   // (the row kernel's workgroups: ceil(M / 64) lie along the grid's second axis)
   for (int i = a.M > 64 * 65535 ? 2 : 1; i < 6; ++i)
     if (t[i] < t[best] || (best < 2 && a.M > 64 * 65535)) best = i;
-#ifdef FORCE
-  best = FORCE;
-#endif
   switch (best) {
     case 0: return launch_rows<4, 2, 2, 1, 8>(a, strm);
     case 1: return launch_rows<4, 4, 2, 2, 4>(a, strm);
@@ -381,6 +438,12 @@ extern "C" moe_status moe_linear_int8_dynamic(int64_t M, int64_t N, int64_t K, c
   if (!x || !wq || !ws || !out) return MOE_ERR_NULL_ARG;
   if (misaligned(x, wq) || misaligned(workspace, nullptr)) return MOE_ERR_BAD_SHAPE;
   if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  const LinArgs h = {nullptr, nullptr, wq, ws, bias, static_cast<bf16_t*>(out), M, N, K};
+  if (M <= 2 && K <= kHeldPer * 8 * kHeldWaves * kWave) {
+    if (M == 2) return launch_held<2, 1, 2>(h, x, as_stream(stream));
+    // wide: two column tiles, which halves the workgroups (14336 x 4096 14.6 against 16.3 us)
+    return N < 8192 ? launch_held<1, 1, 3>(h, x, as_stream(stream)) : launch_held<1, 2, 2>(h, x, as_stream(stream));
+  }
   int8_t* xq = static_cast<int8_t*>(workspace);
   float* xs = reinterpret_cast<float*>(xq + (M * K + 255) / 256 * 256);
   hipLaunchKernelGGL(k_quant_x, dim3((unsigned)M), dim3(256), 0, as_stream(stream), static_cast<const uint4*>(x), K,

@@ -83,9 +83,14 @@ __device__ __forceinline__ uint32_t stream_chunk(int j) {
   return 16 * swizzle<128>(stream_row(j), threadIdx.x % 8);
 }
 
-// Bytes of one ring slot; a wave's ring is D of them.
+// Bytes of one ring slot; a wave's ring is D of them.  RT = 0: the weights alone.
 template <int NW, int RT, int PX>
 constexpr int kSlot = (NW + PX * RT) * 2048;
+
+// Rows of int8 codes that a workgroup holds in LDS whole: bytes of one (a multiple of
+// 128, so the last step reads zeros past the end, and 64 more, so that neighbouring
+// rows lie in different banks).
+__host__ __device__ inline int held_pitch(int64_t len) { return (int)((len + 127) / 128 * 128 + 64); }
 
 // acc[n][r] += (weight rows of group n) x (activation rows of tile r) over steps
 // [s0, s1) of rows of `bytes` bytes.  w[n]: a buffer of group n's rows (its end also
@@ -179,6 +184,64 @@ __device__ __forceinline__ void stream_mfma(const i32x4_t (&w)[NW], const i32x4_
   }
 }
 
+// The same for one tile of int8 rows that the workgroup holds in LDS: `held` is this
+// lane's row (any row, for a lane without one), chunk l / 16.
+template <int NW, int D, class Between>
+__device__ __forceinline__ void stream_held(const i32x4_t (&w)[NW], const char* held, int64_t bytes, int s0, int s1,
+                                            char* ring, i32x4_t (&acc)[NW], Between between) {
+  constexpr int I = 2 * NW;
+  const int lane = threadIdx.x % kWave;
+  const uint32_t nb = (uint32_t)bytes;
+  uint32_t woff[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) woff[j] = stream_row(j) * nb + stream_chunk(j);
+  auto issue = [&](char* slot, int s) {
+    const uint32_t o = (uint32_t)s * kStepBytes;
+    uint32_t wo[2] = {woff[0], woff[1]};
+    if (o + kStepBytes > nb) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (o + stream_chunk(j) >= nb) wo[j] = kPastBuffer;
+    }
+#pragma unroll
+    for (int n = 0; n < NW; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_lds(w[n], slot + n * 2048 + j * 1024, wo[j], o);
+  };
+  const int n = s1 - s0;
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (d < n) issue(ring + d * kSlot<NW, 0, 0>, s0 + d);
+  between();
+  int at[2];
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) at[kk] = (lane % 16) * 128 + 16 * swizzle<128>(lane % 16, 4 * kk + lane / 16);
+  auto step = [&](char* slot, int i) {
+    if (i + D - 1 < n) __builtin_amdgcn_s_waitcnt(vm_wait(I * (D - 1)));
+    else __builtin_amdgcn_s_waitcnt(vm_wait(0));
+    asm volatile("" ::: "memory");
+    i32x4_t wv[2][NW], xv[2];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+      for (int g = 0; g < NW; ++g) wv[kk][g] = *reinterpret_cast<const i32x4_t*>(slot + g * 2048 + at[kk]);
+      xv[kk] = *reinterpret_cast<const i32x4_t*>(held + (s0 + i) * kStepBytes + 64 * kk);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (i + D < n) issue(slot, s0 + i + D);
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int g = 0; g < NW; ++g) acc[g] = mfma16<true>(wv[kk][g], xv[kk], acc[g]);
+  };
+  for (int i = 0; i < n; i += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (i + d < n) step(ring + d * kSlot<NW, 0, 0>, i + d);
+  }
+}
+
 // amax over the workgroup's values (red: one float per wave; every thread gets it).
 template <int WAVES>
 __device__ __forceinline__ float block_max(float m, float* red) {
@@ -200,12 +263,65 @@ __device__ __forceinline__ void int8_scale(float m, float& inv, float& scale) {
   scale = m > 0.f ? __fdiv_rn(m, 127.0f) : 1.0f;
 }
 
-// One row of n values (n a multiple of 8) to int8 by a workgroup of 64 * WAVES
-// threads: codes clamp(rint(v * (127 / amax)), -127, 127), scale amax / 127 (an
-// all-zero row: codes 0, scale 1).  get8(i, f) gives values 8 i .. 8 i + 7; it is
-// called in an amax pass and again for the codes, which go to put2(i, codes).
+// ROWS rows of n values (n a multiple of 8, at most 8 PER values for every thread) to
+// int8 by a workgroup of 64 WAVES threads: codes clamp(rint(v * (127 / amax)), -127,
+// 127), scale amax / 127 (an all-zero row: codes 0, scale 1).  get8(r, i, f) gives values
+// 8 i .. 8 i + 7 of row r < rows, put2(r, i, codes) takes them, scale(r, s) the scales.
+// red: ROWS * WAVES floats of LDS.
+template <int WAVES, int ROWS, int PER, class Get, class Put, class Scale>
+__device__ __forceinline__ void quant_rows_int8(int rows, int64_t n, float* red, Get get8, Put put2, Scale scale) {
+  float f[ROWS][PER][8], m[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      const int i = threadIdx.x + p * WAVES * kWave;
+      if (r < rows && i < n / 8) {
+        get8(r, i, f[r][p]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[r][p][q] = 0.f;
+      }
+    }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    m[r] = 0.f;
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m[r] = fmaxf(m[r], fabsf(f[r][p][q]));
+    m[r] = wave_max64(m[r]);
+    if (threadIdx.x % kWave == 0) red[r * WAVES + threadIdx.x / kWave] = m[r];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    if (r >= rows) break;
+    float a = red[r * WAVES];
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v) a = fmaxf(a, red[r * WAVES + v]);
+    float inv, s;
+    int8_scale(a, inv, s);
+    if (threadIdx.x == 0) scale(r, s);
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      const int i = threadIdx.x + p * WAVES * kWave;
+      const float* v = f[r][p];
+      if (i < n / 8) put2(r, i, make_uint2(i8x4(v[0], v[1], v[2], v[3], inv), i8x4(v[4], v[5], v[6], v[7], inv)));
+    }
+  }
+}
+
+// One row of any length: the row in registers if it fits, else read twice.
 template <int WAVES, class Get, class Put>
 __device__ __forceinline__ float quant_row_int8(int64_t n, float* red, Get get8, Put put2) {
+  float sc = 0.f;
+  if (n <= 4 * 8 * WAVES * kWave) {
+    quant_rows_int8<WAVES, 1, 4>(
+        1, n, red, [&](int, int64_t i, float* f) { get8(i, f); }, [&](int, int64_t i, uint2 c) { put2(i, c); },
+        [&](int, float s) { sc = s; });
+    return sc;
+  }
   float m = 0.f;
   for (int64_t i = threadIdx.x; i < n / 8; i += WAVES * kWave) {
     float f[8];
@@ -213,31 +329,85 @@ __device__ __forceinline__ float quant_row_int8(int64_t n, float* red, Get get8,
 #pragma unroll
     for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(f[q]));
   }
-  float inv, scale;
-  int8_scale(block_max<WAVES>(m, red), inv, scale);
+  float inv;
+  int8_scale(block_max<WAVES>(m, red), inv, sc);
   for (int64_t i = threadIdx.x; i < n / 8; i += WAVES * kWave) {
     float f[8];
     get8(i, f);
     put2(i, make_uint2(i8x4(f[0], f[1], f[2], f[3], inv), i8x4(f[4], f[5], f[6], f[7], inv)));
   }
-  return scale;
+  return sc;
 }
 
-// More than 64 KB of dynamic LDS has to be asked for, once for each kernel, size and
-// device (the largest size asked for so far holds for smaller ones).
+// One row of any length by one wave, the values in registers up to 4096 of them.
+template <class Get, class Put>
+__device__ __forceinline__ float quant_row_int8_wave(int64_t n, Get get8, Put put2) {
+  constexpr int PER = 8;
+  const int lane = threadIdx.x % kWave;
+  const bool held = n <= PER * 8 * kWave;
+  float f[PER][8], m = 0.f, inv, sc;
+  if (held) {
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      if (lane + p * kWave < n / 8) {
+        get8(lane + p * kWave, f[p]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[p][q] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(f[p][q]));
+  } else {
+    for (int64_t i = lane; i < n / 8; i += kWave) {
+      get8(i, f[0]);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(f[0][q]));
+    }
+  }
+  int8_scale(wave_max64(m), inv, sc);
+  auto codes = [&](const float* v) {
+    return make_uint2(i8x4(v[0], v[1], v[2], v[3], inv), i8x4(v[4], v[5], v[6], v[7], inv));
+  };
+  if (held) {
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+      if (lane + p * kWave < n / 8) put2(lane + p * kWave, codes(f[p]));
+  } else {
+    for (int64_t i = lane; i < n / 8; i += kWave) {
+      get8(i, f[0]);
+      put2(i, codes(f[0]));
+    }
+  }
+  return sc;
+}
+
+// Zeros behind rows of codes held in LDS, up to the end of the last step.
+template <int THREADS>
+__device__ __forceinline__ void held_pad(char* codes, int rows, int64_t n, int pitch) {
+  const int pad = pitch - 64 - (int)n;  // a multiple of 8
+  for (int i = threadIdx.x; i < rows * pad / 8; i += THREADS) {
+    const int r = i / (pad / 8);
+    *reinterpret_cast<uint2*>(codes + r * pitch + n + 8 * (i - r * (pad / 8))) = make_uint2(0u, 0u);
+  }
+}
+
+// More than 64 KB of dynamic LDS has to be asked for, once for each kernel and device.
 template <auto KERNEL>
 bool lds_allowed(int bytes) {
   if (bytes <= 65536) return true;
   constexpr int kDevices = 64;
-  static std::atomic<int> asked[kDevices];
+  static std::atomic<bool> asked[kDevices];
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return false;
-  if (dev < kDevices && asked[dev].load(std::memory_order_relaxed) >= bytes) return true;
-  // (two threads may ask at once: both for the whole 160 KB, so either order serves)
+  if (dev < kDevices && asked[dev].load(std::memory_order_relaxed)) return true;
+  // (two threads may ask at once, both for all of it)
   if (hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize,
                           160 * 1024) != hipSuccess)
     return false;
-  if (dev < kDevices) asked[dev].store(160 * 1024, std::memory_order_relaxed);
+  if (dev < kDevices) asked[dev].store(true, std::memory_order_relaxed);
   return true;
 }
 
