@@ -826,7 +826,7 @@ moe_status check_few(const moe_shape* s, int64_t shared_F, bool i8) {
   if (i8 && (s->H > 131072 || s->F > 131072 || shared_F > 131072)) return MOE_ERR_UNSUPPORTED;
   if (s->comm_quant_mode != 0) return MOE_ERR_UNSUPPORTED;
   if (s->T > kMaxTokens) return MOE_ERR_UNSUPPORTED;
-  // the rows of h are addressed with 31-bit offsets
+  // the rows of h are addressed with 31-bit offsets (those of x end below 2^27)
   if (s->T * s->K * s->F * 2 >= 0x7ffffff0) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -933,7 +933,8 @@ moe_status few_impl(const moe_shape* s, bool i8, const void* x, const int32_t* t
   if (Fs > 0 && shared_x) return MOE_ERR_BAD_RANGE;
   const moe_status sp = check_special(s, s->T ? x : (const void*)s, a1, a2, cv);
   if (sp != MOE_OK) return sp;
-  if (misaligned({x, w[0].codes, w[1].codes, w[2].codes, sw[0].codes, sw[1].codes, sw[2].codes, workspace}))
+  if (misaligned({x, w[0].codes, w[1].codes, w[2].codes, sw[0].codes, sw[1].codes, sw[2].codes, smooth,
+                  workspace}))
     return MOE_ERR_BAD_SHAPE;
   FewArgs a = {};
   a.idx = topk_idx; a.w = topk_weights; a.mask = mask;

@@ -323,7 +323,7 @@ __global__ __launch_bounds__(WM* WN* kWave, (BM * BN <= 128 * 128 ? 2 : 1) * WM 
       }
   }
   __syncthreads();
-  if (a.N % 8 == 0) {
+  if (a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0) {
     constexpr int VPR = BN / 8;
     for (int v = threadIdx.x; v < BM * VPR; v += W * kWave) {
       const int r = v / VPR, c = v % VPR;
@@ -355,7 +355,8 @@ moe_status check_linear(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N <= 0 || K <= 0 || K % 16 != 0) return MOE_ERR_BAD_SHAPE;
   // |sum| <= 127 * 127 * K stays below 2^31
   if (K > 131072) return MOE_ERR_UNSUPPORTED;
-  if (M > (int64_t)1 << 24 || N > (int64_t)1 << 24) return MOE_ERR_UNSUPPORTED;
+  // a grid's size stays below 2^31
+  if (M > (int64_t)1 << 24 || N > (int64_t)1 << 24 || M * N > (int64_t)1 << 42) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

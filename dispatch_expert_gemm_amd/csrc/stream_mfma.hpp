@@ -255,11 +255,13 @@ __device__ __forceinline__ float block_max(float m, float* red) {
   return r;
 }
 
-// The int8 rule's multiplier and scale of a row of maximum magnitude m.  The
-// multiplier stays finite, so a zero in a row of tiny values (m < 2^-121) keeps
-// code 0.
+// The int8 rule's multiplier and scale of a row of maximum magnitude m.  127 / m is
+// 127 times the rounded reciprocal, as a program of tensor operations forms it: a value
+// on a border between two codes (half the maximum is one: 63.5) then goes the way it
+// goes there.  The multiplier stays finite, so a zero in a row of tiny values
+// (m < 2^-121) keeps code 0.
 __device__ __forceinline__ void int8_scale(float m, float& inv, float& scale) {
-  inv = m > 0.f ? fminf(__fdiv_rn(127.0f, m), 3.402823466e38f) : 0.f;
+  inv = m > 0.f ? fminf(__fmul_rn(127.0f, __fdiv_rn(1.0f, m)), 3.402823466e38f) : 0.f;
   scale = m > 0.f ? __fdiv_rn(m, 127.0f) : 1.0f;
 }
 

@@ -751,8 +751,7 @@ moe_status moe_decode_fused(const moe_shape* s, const void* x, const int32_t* to
 
 /* ------------------------------------------------------------- few tokens
  * A whole MoE layer forward for a decode step of at most 64 tokens.  Each active
- * expert's weights are read from memory once; there is no routing pass (every
- * workgroup sorts the T K <= 1024 slots for itself), no expanded rows, and
+ * expert's weights are read from memory once, there are no expanded rows, and
  * nothing is rounded between x and out:
  *   out[t] = bf16(sum over k of topk_weights[t,k] * v(t,k) + shared[t])
  * with v = Wd_e (silu(Wg_e x_t) * (Wu_e x_t)) for a routed slot, 0 for a zero
@@ -774,7 +773,8 @@ moe_status moe_decode_fused(const moe_shape* s, const void* x, const int32_t* to
  * in it needs clearing.  Calls that share one must not overlap in time. */
 moe_status moe_few_tokens_workspace_size(const moe_shape* s, int64_t shared_F, int32_t int8, size_t* bytes);
 
-/* moe_few_tokens - bf16 weights.  Two kernel launches.
+/* moe_few_tokens - bf16 weights.  Two kernel launches for T <= 16 (gate/up, which sorts
+ * the slots by expert, and down), four above (sort, gate/up, down, weighted sums).
  *  in   x (T, H) bf16, topk_idx (T, K) int32, topk_weights (T, K) fp32,
  *       x_active_mask as for moe_dispatch
  *  in   w_gate, w_up (E, F, H), w_down (E, H, F) bf16; shared_w_* likewise or NULL
@@ -783,9 +783,9 @@ moe_status moe_few_tokens_workspace_size(const moe_shape* s, int64_t shared_F, i
  *       T = 0 it is written 0 and nothing else)
  *  ws   workspace >= moe_few_tokens_workspace_size bytes
  * s->capacity is checked as everywhere and not used otherwise.
- * MOE_ERR_UNSUPPORTED: T > 64, comm_quant_mode != 0.  MOE_ERR_BAD_SHAPE: F or
- * shared_F not a multiple of 32; x, a weight or the workspace not on a 16-byte
- * boundary. */
+ * MOE_ERR_UNSUPPORTED: T > 64, comm_quant_mode != 0, T*K*F*2 not below 2^31
+ * bytes.  MOE_ERR_BAD_SHAPE: F or shared_F not a multiple of 32; x, a weight or the
+ * workspace not on a 16-byte boundary. */
 moe_status moe_few_tokens(const moe_shape* s, const void* x, const int32_t* topk_idx, const float* topk_weights,
                           const uint8_t* x_active_mask, const void* w_gate, const void* w_up, const void* w_down,
                           int64_t shared_F, const void* shared_w_gate, const void* shared_w_up,
@@ -794,11 +794,17 @@ moe_status moe_few_tokens(const moe_shape* s, const void* x, const int32_t* topk
                           void* workspace, size_t ws_bytes, void* stream);
 
 /* moe_few_tokens_int8 - int8 weights (w8a8, the int8 path's arithmetic without its
- * bf16 roundings): x_t times smooth_scales[e] (NULL: 1) is quantised per row by
- * the rule of moe_quant_rows_int8, G and U are exact integer sums times
- * (row scale x channel scale), h in fp32 is quantised per row by the same rule,
- * y likewise.  The shared expert takes x_t without smooth scales.
- *  in   smooth_scales NULL or (E, H) fp32
+ * bf16 roundings): x_t times smooth_scales[e] (NULL: 1) is quantised per row, G and U
+ * are exact integer sums times (row scale x channel scale), h in fp32 is quantised
+ * per row, y likewise.  The shared expert takes x_t without smooth scales.
+ * Rows become codes clamp(rint(v * (127 * (1/amax))), -127, 127), every operation
+ * rounded to fp32 (the factor at most the largest finite number), and a scale
+ * amax/127 (all-zero row: codes 0, scale 1): the rule of moe_quant_rows_int8 with
+ * 127/amax formed from the reciprocal, as programs of tensor operations form it.  A
+ * value on the border between two codes (exactly amax/2, say) may get the other one.
+ * One or two tokens: two launches where a row of H <= 8192 and all rows of h (48 KiB)
+ * fit a workgroup; else, and up to 16 tokens, four; above five.
+ *  in   smooth_scales NULL or (E, H) fp32, on a 16-byte boundary
  *  in   w[3] gate, up, down; shared_w NULL or three weights
  *  other arguments as moe_few_tokens.  H a multiple of 16 (MOE_ERR_BAD_SHAPE); H, F
  *  and shared_F at most 131072 (MOE_ERR_UNSUPPORTED). */
@@ -813,7 +819,8 @@ moe_status moe_few_tokens_int8(const moe_shape* s, const void* x, const int32_t*
  * The dense product of the int8 path (the projections around the layer):
  *   out[m, n] = bf16((sum over k of xq[m, k] * wq[n, k]) * (xs[m] * ws[n]) + bias[n])
  * with an exact integer sum, for any M >= 0 and N >= 1 and K a positive multiple
- * of 16 (MOE_ERR_BAD_SHAPE) up to 131072; M and N at most 2^24 (MOE_ERR_UNSUPPORTED).
+ * of 16 (MOE_ERR_BAD_SHAPE) up to 131072; M and N at most 2^24, M*N at most 2^42
+ * (MOE_ERR_UNSUPPORTED).
  */
 
 /* moe_linear_int8 - one launch.
@@ -825,9 +832,9 @@ moe_status moe_linear_int8(int64_t M, int64_t N, int64_t K, const int8_t* xq, co
                            const float* ws, const float* bias, void* out, void* stream);
 
 /* moe_linear_int8_dynamic - moe_linear_int8 of bf16 rows x (M, K), quantised per
- * row by the rule of moe_quant_rows_int8 (rows whose largest magnitude is below
- * 2^-121 keep a finite multiplier).  workspace >= moe_linear_int8_workspace_size
- * bytes. */
+ * row by the rule of moe_few_tokens_int8.  workspace >= moe_linear_int8_workspace_size
+ * bytes.  Calls that share one must not overlap in time.  One launch for M <= 2 and
+ * K <= 8192, else two. */
 moe_status moe_linear_int8_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
 moe_status moe_linear_int8_dynamic(int64_t M, int64_t N, int64_t K, const void* x, const int8_t* wq,
                                    const float* ws, const float* bias, void* out, void* workspace, size_t ws_bytes,

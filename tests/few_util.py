@@ -13,10 +13,11 @@ U = 2.0 ** -23
 
 
 def to_int8(v):
-    """Rows of fp32 values -> (codes, scales) in double; the codes by the rule's fp32 products."""
+    """Rows of fp32 values -> (codes, scales) in double; the codes by the rule's fp32 operations:
+    127 / amax is 127 times the rounded reciprocal."""
     assert v.dtype == torch.float32
     amax = v.abs().amax(-1, keepdim=True)
-    inv = torch.where(amax > 0, (torch.full_like(amax, 127.0) / amax).clamp(max=torch.finfo(torch.float32).max),
+    inv = torch.where(amax > 0, (127.0 * (torch.ones_like(amax) / amax)).clamp(max=torch.finfo(torch.float32).max),
                       torch.zeros_like(amax))
     q = (v * inv).round().clamp(-127, 127)
     return q.double(), torch.where(amax > 0, amax.double() / 127, torch.ones_like(amax, dtype=torch.float64))

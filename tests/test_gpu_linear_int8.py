@@ -23,7 +23,8 @@ def make(M, N, K, seed, bias=True):
 SIZES = [(1, 1, 16), (1, 7168, 2048), (2, 17, 48), (3, 16, 64), (5, 100, 1040), (15, 33, 512), (16, 64, 528), (17, 63, 80),
          (31, 250, 16), (33, 1, 4096), (47, 128, 272), (64, 512, 128), (65, 96, 144), (127, 129, 1040), (128, 256, 512),
          (129, 255, 400), (200, 1000, 96), (255, 384, 2048), (256, 256, 256), (300, 777, 336), (513, 512, 1024),
-         (1000, 130, 64), (1, 40, 131072), (70, 300, 16400)]
+         (1000, 130, 64), (1, 40, 131072), (70, 300, 16400), (1, 8200, 96), (2, 300, 8192), (1, 64, 8208), (4, 4100, 64),
+         (12, 4100, 272), (500, 7100, 1040), (1001, 7160, 1040), (2041, 8190, 1040), (2048, 8192, 528)]
 
 
 @gpu
@@ -84,7 +85,7 @@ def test_leading_dimensions_and_no_rows():
 @pytest.mark.parametrize("M,N,K", [(1, 200, 512), (40, 130, 80), (300, 260, 1040)])
 def test_nothing_is_written_past_the_output(M, N, K):
     x, w, b = make(M, N, K, 34)
-    q, s = dm.quant_rows_int8(x)
+    q, s = quant_weight(x)     # rows by the same rule
     out = torch.full((M * N + 512,), 3.0, dtype=torch.bfloat16, device=DEV)
     dm.moe_linear_int8(q, s, *w, b, out)
     torch.cuda.synchronize()
@@ -97,6 +98,18 @@ def test_nothing_is_written_past_the_output(M, N, K):
     torch.cuda.synchronize()
     assert torch.equal(out[:M * N].view(M, N), dm.linear_int8(q, w, x_scales=s, bias=b))
     assert (out[M * N:] == 3.0).all() and (ws[n:] == 0xff).all()
+
+
+@gpu
+@pytest.mark.parametrize("M", [2, 40, 300])
+def test_an_output_off_the_vector_boundary(M):
+    x, w, b = make(M, 264, 512, 40)
+    flat = torch.full((M * 264 + 9,), 3.0, dtype=torch.bfloat16, device=DEV)
+    out = flat[1:1 + M * 264]
+    q, s = quant_weight(x)
+    dm.moe_linear_int8(q, s, *w, b, out)
+    assert torch.equal(out.view(M, 264), dm.linear_int8(x, w, bias=b))
+    assert flat[0] == 3.0 and (flat[1 + M * 264:] == 3.0).all()
 
 
 @gpu
