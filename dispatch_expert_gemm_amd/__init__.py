@@ -1263,18 +1263,38 @@ class Int8Weights:
         return Int8Weights(c, s)
 
 
+def _shared_int8(x, gate, up, down, stream):
+    """The shared expert of moe_layer_int8: every token, one expert."""
+    T, H = x.shape
+    Fs = _fits((gate.codes, up.codes, down.codes), 1, H)
+    shape = make_shape(T, H, 1, 1, F=Fs)
+    with torch.cuda.stream(stream):
+        counts = torch.full((1,), T, dtype=I32, device=x.device)
+        gus = torch.empty((T, 2 * Fs), dtype=BF16, device=x.device)
+        h = torch.empty((T, Fs), dtype=BF16, device=x.device)
+        moe_ffn_gate_up_fwd_int8(shape, *quant_rows_int8(x), gate.codes, gate.scales, up.codes, up.scales, counts, gus, h)
+        return linear_int8(h, (down.codes[0], down.scales[0]))
+
+
 @torch.no_grad()
 def moe_layer_int8(x, topk_idx, topk_weights, wq_gate, wq_up, wq_down, *, smooth_scales=None,
                    x_active_mask=None, shared_expert_x=None, const_alpha_1=None, const_alpha_2=None,
-                   const_v=None, zero_expert_num=0, copy_expert_num=0, const_expert_num=0, stream=None):
+                   const_v=None, zero_expert_num=0, copy_expert_num=0, const_expert_num=0, stream=None,
+                   shared_wq_gate=None, shared_wq_up=None, shared_wq_down=None):
     """Forward of one MoE layer on the decode regime's int8 path (inference, no autograd):
     int8 dispatch (optionally smooth-scaled per expert), w8a8 gate/up GEMM with the SwiGLU
     epilogue, per-row int8 requantisation of h, w8a8 down GEMM, bf16 combine.
-    wq_*: Int8Weights of w_gate, w_up (E, F, H) and w_down (E, H, F)."""
+    wq_*: Int8Weights of w_gate, w_up (E, F, H) and w_down (E, H, F); shared_wq_*: a shared
+    expert's, (1, Fs, H) and (1, H, Fs), run on x without smooth scales in shared_expert_x's place."""
     T, H = x.shape
     K = topk_idx.shape[1]
     E, F, _ = wq_gate.codes.shape
     dev = x.device
+    shared_wq = _shared_weights(shared_wq_gate, shared_wq_up, shared_wq_down)
+    if shared_wq is not None:
+        if shared_expert_x is not None:
+            raise MoeError("shared expert weights and shared_expert_x exclude each other")
+        shared_expert_x = _shared_int8(x, *shared_wq, stream)
     mask_ndim = 0 if x_active_mask is None else x_active_mask.dim()
     shape = make_shape(T, H, K, E, F=F, zero_expert_num=zero_expert_num, copy_expert_num=copy_expert_num,
                        const_expert_num=const_expert_num, mask_ndim=mask_ndim)
@@ -1444,6 +1464,14 @@ def _fits(ws, n, H):
     return f
 
 
+def _shared_weights(gate, up, down):
+    if gate is None and up is None and down is None:
+        return None
+    if gate is None or up is None or down is None:
+        raise MoeError("the shared expert has all three weights or none")
+    return gate, up, down
+
+
 def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smooth_scales=None, x_active_mask=None,
                          shared_expert_x=None, shared_w_gate=None, shared_w_up=None, shared_w_down=None,
                          const_alpha_1=None, const_alpha_2=None, const_v=None, zero_expert_num=0, copy_expert_num=0,
@@ -1469,7 +1497,7 @@ def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smo
         raise MoeError(f"topk_idx {tuple(topk_idx.shape)} and topk_weights {tuple(topk_weights.shape)} for {T} tokens")
     int8 = not isinstance(w_gate, torch.Tensor)
     w = (w_gate, w_up, w_down)
-    shared_w = None if shared_w_gate is None else (shared_w_gate, shared_w_up, shared_w_down)
+    shared_w = _shared_weights(shared_w_gate, shared_w_up, shared_w_down)
     if int8:
         codes = [_int8_pair(v)[0] for v in w]
         E = codes[0].shape[0]

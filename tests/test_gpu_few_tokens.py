@@ -76,6 +76,15 @@ CASES = {
     "largest batch": dict(T=64, H=1024, F=512, E=32, K=8, shared=512),
     "many experts": dict(T=50, H=128, F=32, E=1024, K=16, Z=3, Q=1, mask="2d"),
     "three tiles": dict(T=47, H=160, F=64, E=2, K=2, shared=96),
+    "two tokens": dict(T=2, H=512, F=160, E=6, K=3, shared=96, mask="2d", C=1),
+    "longest held row": dict(T=2, H=8192, F=96, E=3, K=2),
+    "a row too long to hold": dict(T=1, H=8208, F=64, E=2, K=2, shared=64),
+    "too many rows of h to hold": dict(T=2, H=256, F=4096, E=8, K=8),
+    "more columns than 16 for each CU": dict(T=7, H=4112, F=64, E=4, K=2, shared=32),
+    "one token, wide": dict(T=1, H=4112, F=352, E=4, K=2, shared=32),
+    "short contractions": dict(T=40, H=64, F=32, E=3, K=2, shared=32),
+    "long contractions": dict(T=20, H=2064, F=5152, E=2, K=1),
+    "long contractions, four tiles": dict(T=64, H=2064, F=5152, E=3, K=2, one_expert=False, shared=2592),
 }
 
 
@@ -248,6 +257,31 @@ def test_two_streams_at_once():
 
 
 @gpu
+@pytest.mark.parametrize("int8", [False, True])
+def test_two_graphs_at_once(int8):
+    """Each captured call has a workspace of its own."""
+    ps = [make(T, 512, 256, 8, 2, s, int8=int8, smooth=int8) for T, s in ((2, 28), (24, 29))]
+    want = [call(p) for p in ps]
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in ps]
+    for p in ps:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(p))
+        graphs.append(g)
+    for _ in range(4):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+
+
+@gpu
 def test_refusals_of_tensors():
     p = make(4, 128, 64, 4, 2, 26)
 
@@ -273,6 +307,13 @@ def test_refusals_of_tensors():
     refused(x=buf[1:].view(4, 128))                           # not on a 16-byte boundary
     sw = make(1, 128, 64, 4, 2, 27, shared=32)["sw"]
     refused(sw=sw, shared_x=p["x"])                           # both forms of the shared term
+    refused(sw=[sw[0], None, sw[2]])
+    refused(sw=[None, sw[1], sw[2]])
+    q = make(4, 128, 64, 4, 2, 26, int8=True)
+    flat = torch.ones(4 * 128 + 1, device=DEV)
+    q["smooth"] = flat[1:].view(4, 128)                       # not on a 16-byte boundary
+    with pytest.raises(dm.MoeError):
+        call(q)
 
 
 def test_refusals_of_the_entries():
