@@ -1357,13 +1357,17 @@ def _device_of(x, name):
     return x.get_device()
 
 
+def _same_device(stream, dev):
+    if stream.device.index != dev:
+        raise MoeError(f"the stream is on {stream.device}, the tensors on device {dev}")
+
+
 def _launch(entry, dev, stream, *args):
     """Call a C entry with its stream argument last, on the GPU its tensors are on."""
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(dev)
-    elif stream.device.index != dev:
-        raise MoeError(f"the stream is on {stream.device}, the tensors on device {dev}")
     else:
+        _same_device(stream, dev)
         raw = stream.cuda_stream
     if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
@@ -1482,7 +1486,9 @@ def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smo
     Weights (the shared expert's too): bf16 tensors w_gate, w_up (E, F, H) and w_down (E, H, F),
     or for all of them Int8Weights or (codes, scales) pairs, then optionally with
     smooth_scales (E, H).  err_flag: an int32 tensor for the routing's MOE_FLAG_* bits."""
+    dev = _device_of(x, "x")
     if stream is not None:
+        _same_device(stream, dev)
         with torch.cuda.stream(stream):  # its output and workspace then belong to that stream
             return moe_layer_few_tokens(
                 x, topk_idx, topk_weights, w_gate, w_up, w_down, smooth_scales=smooth_scales,
@@ -1490,7 +1496,6 @@ def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smo
                 shared_w_up=shared_w_up, shared_w_down=shared_w_down, const_alpha_1=const_alpha_1,
                 const_alpha_2=const_alpha_2, const_v=const_v, zero_expert_num=zero_expert_num,
                 copy_expert_num=copy_expert_num, const_expert_num=const_expert_num, err_flag=err_flag)
-    dev = _device_of(x, "x")
     T, H = x.shape
     K = topk_idx.shape[-1]
     if topk_idx.shape != (T, K) or topk_weights.shape != (T, K):
@@ -1556,10 +1561,11 @@ def linear_int8(x, w, *, x_scales=None, bias=None, stream=None):
     (..., N) bf16 (inference, no autograd).  w: an Int8Weights or a (codes, scales) pair.
     x: bf16 rows, quantised per row in the call, or int8 codes with their x_scales (...);
     bias: fp32 (N,)."""
+    dev = _device_of(x, "x")
     if stream is not None:
+        _same_device(stream, dev)
         with torch.cuda.stream(stream):  # its output and workspace then belong to that stream
             return linear_int8(x, w, x_scales=x_scales, bias=bias)
-    dev = _device_of(x, "x")
     wq, ws = _int8_pair(w)
     K = x.shape[-1]
     if wq.dim() != 2 or wq.shape[1] != K:

@@ -7,25 +7,40 @@
 //   down      out_t = bf16(sum_k w_tk v_tk + shared_t), v_tk = Wd_e h_s for a
 //             routed slot, the special experts' values as in the combine
 //
-// There is no routing pass: each workgroup sorts the call's T K <= 1024 slots by
-// expert in LDS for itself (route_lds).  A shared expert is one more expert that
-// every token goes to with weight 1.
+// A shared expert is one more expert that every token goes to with weight 1.
 //
-// Work split.  gate/up: a workgroup per (active expert, columns of F), its waves
-// splitting the contraction over H.  down, T <= 16: a workgroup per 32 columns of H
-// that goes over all active experts, its waves splitting the (expert, F) steps
-// evenly, so a token's weighted sum stays inside one workgroup: no third kernel, no
-// atomics, the same order of additions in every call.  Rows are packed per expert
-// (the matrix cores take 16 at a time); each wave adds its packed rows' weighted
-// results to its own LDS copy of the output tile.  down, T > 16: a workgroup per
-// (active expert, 64 columns), which reads each row of h half as often, and a
-// small kernel for the weighted sums.
+// Kernels.  T <= 16: k_few_gate_up, k_few_down.  T > 16: k_few_prep, k_few_gate_up,
+// k_few_down_y, k_few_join.  int8 has its rows quantised by k_few_prep (x, times the
+// expert's smooth scales) and k_few_quant_h (h); one or two tokens (HELD) form the
+// codes inside the two kernels that use them.
+//
+// Route.  The T K <= 1024 slots sorted by expert: with T <= 16 every workgroup of
+// gate/up sorts them in LDS for itself (no launch), and the first leaves the table for
+// the kernels behind; with more k_few_prep does it once.
+//
+// Split.  gate/up: a workgroup per (active expert, columns of F); a long contraction over
+// H is split over its four waves, a short one is one wave's own.  down, T <= 16: a
+// workgroup per 16 or 32 columns of H that goes over all active experts, its eight waves
+// splitting the (expert, F) steps evenly, so a token's weighted sum stays inside one
+// workgroup: no third kernel, no atomics, the same order of additions in every call.
+// Rows are packed per expert (the matrix cores take 16 at a time); each wave adds its
+// packed rows' weighted results to its own LDS copy of the output tile.  down, T > 16: a
+// workgroup per (active expert, columns of H), which reads each row of h less often, and
+// a small kernel for the weighted sums, again in a fixed order.
+//
+// Every operand of a product goes straight into LDS, in whole cache lines, by loads that
+// have no register result; each wave has a ring of a few steps for itself and waits by
+// count, so the main loops have no barrier (stream_mfma.hpp).
 //
 // bf16: h leaves as two bf16 planes, hi = bf16(h) and lo = bf16(h - hi), 16
-// significant bits in all; both multiply the same weight registers.  int8: rows
-// of x (times the expert's smooth scales) are quantised by a kernel before
-// gate/up, rows of fp32 h by a kernel before down; sums are exact integers.
-// Bound: HBM, the active experts' weights.
+// significant bits in all; both multiply the same weight registers.  int8: sums are
+// exact integers.
+//
+// Bound: HBM, the active experts' weights (reads reach 6.0 TB/s here).  Layers on
+// MI355X with cold weights: one token, 8 of 32 experts and a shared one, H = 7168,
+// F = 2048: 146 us, 5.4 TB/s (int8 84 us, 4.7); 13 tokens 440 to 470 us, 5.7 to 6.0 TB/s
+// (9 in int8 231 us, 5.5); 64 tokens on 8 experts of 14336 x 4096 515 us, 5.5 TB/s; 64 tokens
+// in int8 308 us, 4.7.  One token of 64 experts of 1536 x 480: 15.6 us, of which the bytes are 6.
 #include <initializer_list>
 
 #include "combine_token.hpp"
@@ -38,12 +53,18 @@ constexpr int kMaxTokens = 64, kMaxSlots = 1024, kMaxExperts = 1024;
 
 // Sizes of the work.  Up: gate/up, Down: down that sums over the experts, Y: down by
 // expert.  A wave's ring of LDS holds D steps of its operands; CT column tiles of a
-// wave share its activation rows.
+// wave share its activation rows.  Up's ring, up to 16 rows for an expert: 8 KB takes one
+// token with a shared expert from 146 to 154 us, 24 KB 9 tokens in int8 from 228 to 263
+// (fewer workgroups on a CU); more rows: 12 KB takes 64 tokens in int8 from 308 to 315, 24 KB
+// to 334.
 constexpr int kUpWaves = 4, kDownWaves = 8, kYWaves = 4;
 template <int RTM>
 constexpr int kUpRing = RTM == 1 ? 12288 : 16384;
-// steps of H below which a wave has its columns to itself, and steps of F likewise (Y)
+// 128-byte steps of H below which a wave has its columns to itself, and steps of F likewise
+// (Y).  Split at every length: 48 tokens on 64 experts of 1536 x 480 in int8 47 -> 64 us;
+// split at none: 64 tokens on 8 experts of 4096 x 14336 509 -> 564 us, one token 15 -> 18.
 constexpr int kUpOwn = 16, kYOwn = 40;
+// (8 KB: 16 tokens of 64 experts of 1536 x 512 in bf16 57.7 -> 69.9 us; 16 KB equal to 2%)
 constexpr int kDownRing = 12288;
 // Y, by the waves KS that split the contraction: a long one wants few reads of h
 // (F = 14336 in bf16, 64 tokens: 180 us, with two column tiles 206 to 227), a short one
@@ -55,7 +76,11 @@ template <bool I8, int RTM, int KS>
 constexpr int kYRing = KS > 1 ? 24576 : (I8 || RTM < 4 ? 12288 : 20480);
 template <int NW, int RT, int PX, int RING>
 constexpr int kDepth = RING / kSlot<NW, RT, PX> < 1 ? 1 : (RING / kSlot<NW, RT, PX> > 4 ? 4 : RING / kSlot<NW, RT, PX>);
-// int8, one or two tokens: the rows' codes are formed by the kernels that use them
+// int8, one or two tokens: the rows' codes are formed by the kernels that use them, which
+// saves two launches (one token of 64 experts of 1536 x 512 20.6 -> 15.8 us, two of 5120 x
+// 1536 48 -> 43.6; two of 7168 x 2048 with a shared expert 134.7 -> 136.7).  Four tokens: 27.7
+// against 26.0 us with the launches.  A ring of three steps in gate/up leaves a workgroup
+// less on a CU: 87 -> 92.6 us.
 constexpr int kHeldTokens = 2, kHeldUpDepth = 2, kHeldDownDepth = 3, kHeldBytes = 49152;
 
 struct FewArgs {

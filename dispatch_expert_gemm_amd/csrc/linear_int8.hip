@@ -1,12 +1,22 @@
 // The matrix product on 8-bit integers with a scale for each token and each
 // output channel, moe_linear_int8: out[m, n] = bf16((sum_k xq[m, k] wq[n, k]) *
 // (xs[m] * ws[n]) + bias[n]), the sum exact in int32; and its dynamic form, which
-// first quantises bf16 rows by the rule of moe_quant_rows_int8.
+// first quantises bf16 rows (int8_scale in stream_mfma.hpp).
 //
-// k_linear_rows: one workgroup per (16 output columns, up to 64 rows).  Its waves
-// split the contraction, each streaming its part of the 16 weight rows from
+// k_linear_rows: one workgroup per (16 CT output columns, up to 64 rows).  Its waves
+// split the contraction, each streaming its part of the weight rows from
 // memory into the matrix cores (stream_mfma.hpp); the int32 partial sums meet in
-// LDS, where their order does not matter.  Bound: HBM, N * K bytes of weights.
+// LDS, where their order does not matter.  k_linear_held: the same for one or two bf16
+// rows, quantised inside.  Bound: HBM, N * K bytes of weights, and for small ones the
+// launch: one row of 7168 x 7168 10.5 us (4.9 TB/s), 37 rows of 7168 x 2048 7.1 us.
+//
+// k_linear_tiles: tiles of 64 x 128 to 256 x 256, both operands in LDS.  Bound: with 256
+// tiles or fewer the operands' way from L2 into LDS (512 x 4096 x 7168: 27.8 us, 1.08 POP/s,
+// 13 TB/s into the CUs); for large products power: 8192 x 14336 x 4096 takes 463 us, of
+// which 376 grow with K (2.55 POP/s there), the matrix cores busy 63% of the time at a clock
+// of 1.82 GHz.  Four waves of 128 x 128, with two thirds of the LDS reads and every load
+// and read between two products, keep them busy 75% of the loop, the clock falls to 1.63
+// GHz and the loop takes the same time; two workgroups of 128 x 256 on a CU 550 us.
 #include <algorithm>
 #include <type_traits>
 
