@@ -292,7 +292,7 @@ __global__ __launch_bounds__(256) void k_few_prep(FewArgs a) {
     const uint4* src = reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H);
     uint2* dst = reinterpret_cast<uint2*>(a.xq + (int64_t)r * a.H);
     const float s = quant_row_int8<4>(
-        a.H, reinterpret_cast<float*>(lds),
+        a.H, reinterpret_cast<uint32_t*>(lds),
         [&](int64_t i, float* f) {
           x_times_smooth(src[i], sm, i, f);
         },
@@ -311,7 +311,7 @@ __device__ __forceinline__ void load8(const float4* src, int64_t i, float* f) {
 // int8: one workgroup per row of h: the slots' rows, then the shared expert's.
 // Rows of slots that are not routed are unwritten, and never read.
 __global__ __launch_bounds__(256) void k_few_quant_h(FewArgs a) {
-  __shared__ float red[4];
+  __shared__ uint32_t red[4];
   const int r = blockIdx.x, S = a.T * a.K;
   if (r < S && (a.idx[r] < 0 || a.idx[r] >= a.E)) return;
   const bool sh = r >= S;
@@ -444,7 +444,7 @@ __device__ __forceinline__ void gate_up_held(const FewArgs& a, const uint16_t* s
   const int64_t F = sh ? a.Fs : a.F, wrow = (sh ? 0 : (int64_t)e * F) + f0;
   char* codes = lds + W * RING;
   float* scales = reinterpret_cast<float*>(codes + a.T * pitch);
-  float* red = scales + kHeldTokens;
+  uint32_t* red = reinterpret_cast<uint32_t*>(scales + kHeldTokens);
   const i32x4_t w[2] = {buffer_of(static_cast<const char*>(sh ? a.swg : a.wg) + wrow * a.H, 16 * a.H),
                         buffer_of(static_cast<const char*>(sh ? a.swu : a.wu) + wrow * a.H, 16 * a.H)};
   i32x4_t acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};

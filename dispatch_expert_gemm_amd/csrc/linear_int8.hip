@@ -38,7 +38,7 @@ struct LinArgs {
 // one workgroup per row
 __global__ __launch_bounds__(256) void k_quant_x(const uint4* __restrict__ x, int64_t K, uint2* __restrict__ codes,
                                                  float* __restrict__ scales) {
-  __shared__ float red[4];
+  __shared__ uint32_t red[4];
   const int64_t r = blockIdx.x;
   const uint4* src = x + r * (K / 8);
   uint2* dst = codes + r * (K / 8);
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kHeldWaves* kWave, 2) void k_linear_held(LinArgs a,
   const int64_t n0 = (int64_t)blockIdx.x * (16 * CT);
   char* codes = lds + W * RING;
   float* scales = reinterpret_cast<float*>(codes + M * pitch);
-  float* red = scales + ROWS;
+  uint32_t* red = reinterpret_cast<uint32_t*>(scales + ROWS);
   i32x4_t w[CT], acc[CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c) {

@@ -242,37 +242,48 @@ __device__ __forceinline__ void stream_held(const i32x4_t (&w)[NW], const char* 
   }
 }
 
-// amax over the workgroup's values (red: one float per wave; every thread gets it).
-template <int WAVES>
-__device__ __forceinline__ float block_max(float m, float* red) {
-  m = wave_max64(m);
-  if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = m;
-  __syncthreads();
-  float r = red[0];
+// A row's largest magnitude is found on the bits of |v|, which order as the values do,
+// with infinity and then NaN above them: a row that holds a NaN gets a scale of NaN and
+// does not pass for a finite one.
+__device__ __forceinline__ void peak_of(uint32_t& m, float v) {
+  const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+  m = b > m ? b : m;
+}
+__device__ __forceinline__ uint32_t wave_peak(uint32_t m) {
 #pragma unroll
-  for (int i = 1; i < WAVES; ++i) r = fmaxf(r, red[i]);
-  __syncthreads();
-  return r;
+  for (int o = 32; o >= 1; o >>= 1) {
+    const uint32_t v = (uint32_t)__shfl_xor((int)m, o, kWave);
+    m = v > m ? v : m;
+  }
+  return m;
+}
+// The largest of the waves' peaks.
+template <int WAVES>
+__device__ __forceinline__ float peak_in(const uint32_t* red) {
+  uint32_t m = red[0];
+#pragma unroll
+  for (int i = 1; i < WAVES; ++i) m = red[i] > m ? red[i] : m;
+  return __uint_as_float(m);
 }
 
 // The int8 rule's multiplier and scale of a row of maximum magnitude m.  127 / m is
 // 127 times the rounded reciprocal, as a program of tensor operations forms it: a value
 // on a border between two codes (half the maximum is one: 63.5) then goes the way it
 // goes there.  The multiplier stays finite, so a zero in a row of tiny values
-// (m < 2^-121) keeps code 0.
+// (m < 2^-121) keeps code 0; infinity and NaN go into the scale.
 __device__ __forceinline__ void int8_scale(float m, float& inv, float& scale) {
-  inv = m > 0.f ? fminf(__fmul_rn(127.0f, __fdiv_rn(1.0f, m)), 3.402823466e38f) : 0.f;
-  scale = m > 0.f ? __fdiv_rn(m, 127.0f) : 1.0f;
+  inv = m == 0.f ? 0.f : fminf(__fmul_rn(127.0f, __fdiv_rn(1.0f, m)), 3.402823466e38f);
+  scale = m == 0.f ? 1.0f : __fdiv_rn(m, 127.0f);
 }
 
 // ROWS rows of n values (n a multiple of 8, at most 8 PER values for every thread) to
 // int8 by a workgroup of 64 WAVES threads: codes clamp(rint(v * (127 / amax)), -127,
 // 127), scale amax / 127 (an all-zero row: codes 0, scale 1).  get8(r, i, f) gives values
 // 8 i .. 8 i + 7 of row r < rows, put2(r, i, codes) takes them, scale(r, s) the scales.
-// red: ROWS * WAVES floats of LDS.
+// red: ROWS * WAVES words of LDS.
 template <int WAVES, int ROWS, int PER, class Get, class Put, class Scale>
-__device__ __forceinline__ void quant_rows_int8(int rows, int64_t n, float* red, Get get8, Put put2, Scale scale) {
-  float f[ROWS][PER][8], m[ROWS];
+__device__ __forceinline__ void quant_rows_int8(int rows, int64_t n, uint32_t* red, Get get8, Put put2, Scale scale) {
+  float f[ROWS][PER][8];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r)
 #pragma unroll
@@ -287,23 +298,20 @@ __device__ __forceinline__ void quant_rows_int8(int rows, int64_t n, float* red,
     }
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
-    m[r] = 0.f;
+    uint32_t m = 0;
 #pragma unroll
     for (int p = 0; p < PER; ++p)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) m[r] = fmaxf(m[r], fabsf(f[r][p][q]));
-    m[r] = wave_max64(m[r]);
-    if (threadIdx.x % kWave == 0) red[r * WAVES + threadIdx.x / kWave] = m[r];
+      for (int q = 0; q < 8; ++q) peak_of(m, f[r][p][q]);
+    m = wave_peak(m);
+    if (threadIdx.x % kWave == 0) red[r * WAVES + threadIdx.x / kWave] = m;
   }
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     if (r >= rows) break;
-    float a = red[r * WAVES];
-#pragma unroll
-    for (int v = 1; v < WAVES; ++v) a = fmaxf(a, red[r * WAVES + v]);
     float inv, s;
-    int8_scale(a, inv, s);
+    int8_scale(peak_in<WAVES>(red + r * WAVES), inv, s);
     if (threadIdx.x == 0) scale(r, s);
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
@@ -316,7 +324,7 @@ __device__ __forceinline__ void quant_rows_int8(int rows, int64_t n, float* red,
 
 // One row of any length: the row in registers if it fits, else read twice.
 template <int WAVES, class Get, class Put>
-__device__ __forceinline__ float quant_row_int8(int64_t n, float* red, Get get8, Put put2) {
+__device__ __forceinline__ float quant_row_int8(int64_t n, uint32_t* red, Get get8, Put put2) {
   float sc = 0.f;
   if (n <= 4 * 8 * WAVES * kWave) {
     quant_rows_int8<WAVES, 1, 4>(
@@ -324,15 +332,18 @@ __device__ __forceinline__ float quant_row_int8(int64_t n, float* red, Get get8,
         [&](int, float s) { sc = s; });
     return sc;
   }
-  float m = 0.f;
+  uint32_t m = 0;
   for (int64_t i = threadIdx.x; i < n / 8; i += WAVES * kWave) {
     float f[8];
     get8(i, f);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(f[q]));
+    for (int q = 0; q < 8; ++q) peak_of(m, f[q]);
   }
+  m = wave_peak(m);
+  if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = m;
+  __syncthreads();
   float inv;
-  int8_scale(block_max<WAVES>(m, red), inv, sc);
+  int8_scale(peak_in<WAVES>(red), inv, sc);
   for (int64_t i = threadIdx.x; i < n / 8; i += WAVES * kWave) {
     float f[8];
     get8(i, f);
@@ -347,7 +358,8 @@ __device__ __forceinline__ float quant_row_int8_wave(int64_t n, Get get8, Put pu
   constexpr int PER = 8;
   const int lane = threadIdx.x % kWave;
   const bool held = n <= PER * 8 * kWave;
-  float f[PER][8], m = 0.f, inv, sc;
+  float f[PER][8], inv, sc;
+  uint32_t m = 0;
   if (held) {
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
@@ -361,15 +373,15 @@ __device__ __forceinline__ float quant_row_int8_wave(int64_t n, Get get8, Put pu
 #pragma unroll
     for (int p = 0; p < PER; ++p)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(f[p][q]));
+      for (int q = 0; q < 8; ++q) peak_of(m, f[p][q]);
   } else {
     for (int64_t i = lane; i < n / 8; i += kWave) {
       get8(i, f[0]);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(f[0][q]));
+      for (int q = 0; q < 8; ++q) peak_of(m, f[0][q]);
     }
   }
-  int8_scale(wave_max64(m), inv, sc);
+  int8_scale(__uint_as_float(wave_peak(m)), inv, sc);
   auto codes = [&](const float* v) {
     return make_uint2(i8x4(v[0], v[1], v[2], v[3], inv), i8x4(v[4], v[5], v[6], v[7], inv));
   };

@@ -802,6 +802,7 @@ moe_status moe_few_tokens(const moe_shape* s, const void* x, const int32_t* topk
  * amax/127 (all-zero row: codes 0, scale 1): the rule of moe_quant_rows_int8 with
  * 127/amax formed from the reciprocal, as programs of tensor operations form it.  A
  * value on the border between two codes (exactly amax/2, say) may get the other one.
+ * A row that holds an infinity or a NaN gives results that are not finite.
  * One or two tokens: two launches where a row of H <= 8192 and all rows of h (48 KiB)
  * fit a workgroup; else, and up to 16 tokens, four; above five.
  *  in   smooth_scales NULL or (E, H) fp32, on a 16-byte boundary

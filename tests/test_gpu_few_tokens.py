@@ -163,14 +163,17 @@ def test_what_no_active_slot_uses_does_not_matter(int8, bad):
 
 
 @gpu
-def test_a_token_with_infinities_does_not_reach_the_others():
-    p = make(8, 256, 64, 4, 2, 16)
+@pytest.mark.parametrize("T", [2, 8, 40])
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_token_that_is_not_finite_does_not_reach_the_others(bad, int8, T):
+    p = make(T, 256, 64, 4, 2, 16, int8=int8, smooth=int8)
     clean = call(p)
-    p["x"][3] = float("inf")
+    p["x"][1, 77] = bad
     out = call(p)
-    keep = [t for t in range(8) if t != 3]
+    keep = [t for t in range(T) if t != 1]
     assert torch.equal(out[keep], clean[keep])
-    assert not torch.isfinite(out[3]).all()
+    assert not torch.isfinite(out[1]).any()
 
 
 @gpu

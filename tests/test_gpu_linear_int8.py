@@ -72,6 +72,20 @@ def test_rows_of_zeros_tiny_and_large_values(M):
 
 
 @gpu
+@pytest.mark.parametrize("K", [256, 16400])
+@pytest.mark.parametrize("M", [2, 40, 300])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_row_that_is_not_finite_does_not_reach_the_others(bad, M, K):
+    x, w, b = make(M, 96, K, 41)
+    clean = dm.linear_int8(x, w, bias=b)
+    x[1, 17] = bad
+    out = dm.linear_int8(x, w, bias=b)
+    keep = [m for m in range(M) if m != 1]
+    assert torch.equal(out[keep], clean[keep])
+    assert not torch.isfinite(out[1]).any()
+
+
+@gpu
 def test_leading_dimensions_and_no_rows():
     x, w, b = make(24, 80, 96, 33)
     want = dm.linear_int8(x, w, bias=b)
