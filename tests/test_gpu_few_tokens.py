@@ -103,6 +103,25 @@ def test_layer_against_64_bits(name, form):
 
 
 @gpu
+@pytest.mark.parametrize("T", [2, 20])
+@pytest.mark.parametrize("int8", [False, True])
+def test_weights_past_32_bits(int8, T):
+    """Weight tensors of more than 2^32 bytes; the first and the last experts are used."""
+    H, F, E = 8192, 4096, 68 if not int8 else 132
+    p = make(T, H, F, 4, 2, 44, int8=int8)
+
+    def spread(w):
+        big = torch.zeros(E, *w.shape[1:], dtype=w.dtype, device=DEV)
+        big[:2], big[-2:] = w[:2], w[2:]
+        return big
+
+    p["ws"] = [(spread(w[0]), spread(w[1])) if int8 else spread(w) for w in p["ws"]]
+    p["idx"] = torch.where(p["idx"] < 2, p["idx"], p["idx"] + E - 4)
+    v, bound, _ = ref(p)
+    check("large weights", call(p), v, bound)
+
+
+@gpu
 @pytest.mark.parametrize("int8", [False, True])
 def test_given_shared_term(int8):
     p = make(7, 256, 96, 5, 2, 12, int8=int8, C=1)

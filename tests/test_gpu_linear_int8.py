@@ -86,6 +86,22 @@ def test_a_row_that_is_not_finite_does_not_reach_the_others(bad, M, K):
 
 
 @gpu
+@pytest.mark.parametrize("M,N,K", [(3, 140000, 16384), (40, 140000, 16384), (300000, 16, 8192), (70000, 32768, 32)])
+def test_offsets_past_32_bits(M, N, K):
+    """Weights, rows and outputs of more than 2^31 bytes or elements: the last rows and columns."""
+    g = torch.Generator(device=DEV).manual_seed(42)
+    wq = torch.zeros(N, K, dtype=torch.int8, device=DEV)
+    wq[-200:] = torch.randint(-127, 128, (min(200, N), K), generator=g, device=DEV, dtype=torch.int8)
+    xq = torch.zeros(M, K, dtype=torch.int8, device=DEV)
+    xq[-200:] = torch.randint(-127, 128, (min(200, M), K), generator=g, device=DEV, dtype=torch.int8)
+    xs, ws = torch.rand(M, generator=g, device=DEV), torch.rand(N, generator=g, device=DEV)
+    out = dm.linear_int8(xq, (wq, ws), x_scales=xs)
+    v, bound = linear64((xq[-200:], xs[-200:]), (wq[-200:], ws[-200:]))
+    check("last", out[-200:, -200:], v, bound)
+    assert (out[:-200, :200] == 0).all() and (out[:200, :-200] == 0).all()
+
+
+@gpu
 def test_leading_dimensions_and_no_rows():
     x, w, b = make(24, 80, 96, 33)
     want = dm.linear_int8(x, w, bias=b)
