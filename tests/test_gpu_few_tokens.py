@@ -103,6 +103,16 @@ def test_layer_against_64_bits(name, form):
 
 
 @gpu
+@pytest.mark.parametrize("T,H,F,int8", [(1, 1 << 20, 32, False), (50, 1 << 20, 32, False), (1, 8, 1 << 20, False),
+                                        (50, 8, 1 << 20, False), (2, 131072, 32, True), (50, 131072, 32, True),
+                                        (2, 16, 131072, True), (50, 16, 131072, True)])
+def test_longest_rows(T, H, F, int8):
+    p = make(T, H, F, 3, 2, 45, int8=int8, smooth=int8, shared=32)
+    v, bound, _ = ref(p)
+    check("longest rows", call(p), v, bound)
+
+
+@gpu
 @pytest.mark.parametrize("T", [2, 20])
 @pytest.mark.parametrize("int8", [False, True])
 def test_weights_past_32_bits(int8, T):
