@@ -8,7 +8,7 @@
 // memory into the matrix cores (stream_mfma.hpp); the int32 partial sums meet in
 // LDS, where their order does not matter.  k_linear_held: the same for one or two bf16
 // rows, quantised inside.  Bound: HBM, N * K bytes of weights, and for small ones the
-// launch: one row of 7168 x 7168 10.5 us (4.9 TB/s), 37 rows of 7168 x 2048 7.1 us.
+// launch: one row of 7168 x 7168 10.5 us (4.9 TB/s), 37 rows of 7168 x 2048 6.4 us.
 //
 // k_linear_tiles: tiles of 64 x 128 to 256 x 256, both operands in LDS.  Bound: with 256
 // tiles or fewer the operands' way from L2 into LDS (512 x 4096 x 7168: 27.8 us, 1.08 POP/s,
@@ -375,8 +375,8 @@ bool misaligned(const void* p, const void* q) {
   return (reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) % 16 != 0;
 }
 
-// The kernel is chosen by its estimated time (us), from what each cost on MI355X with
-// cold weights: the tiled kernels take ceil(tiles / 256) rounds of K / 128 steps of
+// Up to 48 rows the row kernel, beyond the kernel with the least estimated time (us), from
+// what each cost on MI355X with cold weights: the tiled kernels take ceil(tiles / 256) rounds of K / 128 steps of
 // 0.44 (64 x 128), 0.60 (128 x 128), 1.0 (128 x 256) and 1.75 us (256 x 256), the
 // row kernel moves (64 + 16 CT) K bytes for each workgroup at 45 bytes per ns and CU.
 // Measured / estimated: 64 x 7168 x 7168 18.9 / 18.3 (rows, CT 2), 25.6 with CT 4, 32.6
@@ -392,8 +392,17 @@ moe_status linear_impl(const LinArgs& a, hipStream_t strm) {
   if (a.M <= 8) return launch_rows<1, 2, 1, 2, 4>(a, strm);
   if (a.M <= 16 && a.N < 4096) return launch_rows<1, 1, 2, 2, 8>(a, strm);
   if (a.M <= 16) return launch_rows<1, 2, 2, 2, 4>(a, strm);
-  if (a.M <= 32) return launch_rows<2, 2, 2, 1, 8>(a, strm);
+  // more rows: one column tile while those workgroups do not exceed the 256 CUs (20 x 2048
+  // x 7168 6.8 against 7.8 us, 37 x 4096 x 4096 6.9 against 7.5; 32 x 7168 x 7168 19 against
+  // 14), else two; row tiles as needed (37 x 7168 x 7168 on three 15.3, on four 16.4)
+  if (a.M <= 32 && a.N <= 4096) return launch_rows<2, 1, 2, 2, 8>(a, strm);
+  if (a.M <= 32) return launch_rows<2, 2, 2, 2, 4>(a, strm);
+  if (a.M <= 48 && a.N <= 4096) return launch_rows<3, 1, 2, 2, 8>(a, strm);
+  if (a.M <= 48) return launch_rows<3, 2, 2, 1, 8>(a, strm);
   auto up = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
+  // (the same with rows past 64, if there are no more row tiles than column tiles: 56 x 2048
+  // x 7168 9.3 against 10.9 us, 200 x 1024 x 7168 9.6 against 10.9; 2000 x 128 x 7168 19 against 13)
+  if (up(a.M, 64) * up(a.N, 16) <= 256 && up(a.M, 64) <= up(a.N, 16)) return launch_rows<4, 1, 2, 2, 8>(a, strm);
   const double steps = up(a.K, 128);
   auto tiled = [&](int bm, int bn, double c) { return up((int64_t)(up(a.M, bm) * up(a.N, bn)), 256) * steps * c + 5; };
   auto rows = [&](int ct) {

@@ -24,7 +24,8 @@ SIZES = [(1, 1, 16), (1, 7168, 2048), (2, 17, 48), (3, 16, 64), (5, 100, 1040), 
          (31, 250, 16), (33, 1, 4096), (47, 128, 272), (64, 512, 128), (65, 96, 144), (127, 129, 1040), (128, 256, 512),
          (129, 255, 400), (200, 1000, 96), (255, 384, 2048), (256, 256, 256), (300, 777, 336), (513, 512, 1024),
          (1000, 130, 64), (1, 40, 131072), (70, 300, 16400), (1, 8200, 96), (2, 300, 8192), (1, 64, 8208), (4, 4100, 64),
-         (12, 4100, 272), (500, 7100, 1040), (1001, 7160, 1040), (2041, 8190, 1040), (2048, 8192, 528)]
+         (12, 4100, 272), (20, 4096, 144), (25, 4112, 272), (40, 4080, 400), (48, 4100, 144), (60, 4090, 272), (64, 4112, 272),
+         (250, 510, 272), (2000, 128, 144), (500, 7100, 1040), (1001, 7160, 1040), (2041, 8190, 1040), (2048, 8192, 528)]
 
 
 @gpu
