@@ -310,15 +310,16 @@ __device__ __forceinline__ void load8(const float4* src, int64_t i, float* f) {
 
 // int8: one workgroup per row of h: the slots' rows, then the shared expert's.
 // Rows of slots that are not routed are unwritten, and never read.
-__global__ __launch_bounds__(256) void k_few_quant_h(FewArgs a) {
-  __shared__ uint32_t red[4];
+template <int WAVES>
+__global__ __launch_bounds__(WAVES* kWave) void k_few_quant_h(FewArgs a) {
+  __shared__ uint32_t red[WAVES];
   const int r = blockIdx.x, S = a.T * a.K;
   if (r < S && (a.idx[r] < 0 || a.idx[r] >= a.E)) return;
   const bool sh = r >= S;
   const int64_t n = sh ? a.Fs : a.F, row = sh ? r - S : r;
   const float4* src = reinterpret_cast<const float4*>((sh ? a.shf : a.hf) + row * n);
   uint2* dst = reinterpret_cast<uint2*>((sh ? a.shq : a.hq) + row * n);
-  const float s = quant_row_int8<4>(
+  const float s = quant_row_int8<WAVES>(
       n, red,
       [&](int64_t i, float* f) {
         load8(src, i, f);
@@ -923,7 +924,12 @@ moe_status few_launch(FewArgs& a, hipStream_t strm) {
   // waves split a long contraction; a short one is a wave's own
   bool ok = stream_steps(a.H * ES) < kUpOwn ? launch_up<I8, RTM, 1, false>(a, strm)
                                            : launch_up<I8, RTM, kUpWaves, false>(a, strm);
-  if (I8) hipLaunchKernelGGL(k_few_quant_h, dim3(S + (a.Fs ? a.T : 0)), dim3(256), 0, strm, a);
+  if constexpr (I8) {
+    // waves for a row to fit their registers (F = 14336: 3 us less of 165 to 278)
+    const dim3 rows(S + (a.Fs ? a.T : 0));
+    if (a.F > 8192 || a.Fs > 8192) hipLaunchKernelGGL(k_few_quant_h<8>, rows, dim3(8 * kWave), 0, strm, a);
+    else hipLaunchKernelGGL(k_few_quant_h<4>, rows, dim3(4 * kWave), 0, strm, a);
+  }
   if constexpr (RTM == 1)
     ok = ok && launch_down<I8, false>(a, strm);
   else

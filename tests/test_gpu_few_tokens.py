@@ -82,6 +82,8 @@ CASES = {
     "too many rows of h to hold": dict(T=2, H=256, F=4096, E=8, K=8),
     "more columns than 16 for each CU": dict(T=7, H=4112, F=64, E=4, K=2, shared=32),
     "one token, wide": dict(T=1, H=4112, F=352, E=4, K=2, shared=32),
+    "h rows past 8192": dict(T=3, H=160, F=8224, E=2, K=1, shared=32),
+    "shared h rows past 8192": dict(T=18, H=160, F=64, E=4, K=2, shared=8224),
     "short contractions": dict(T=40, H=64, F=32, E=3, K=2, shared=32),
     "long contractions": dict(T=20, H=2064, F=5152, E=2, K=1),
     "long contractions, four tiles": dict(T=64, H=2064, F=5152, E=3, K=2, one_expert=False, shared=2592),
