@@ -377,14 +377,15 @@ bool misaligned(const void* p, const void* q) {
 }
 
 // Up to 48 rows the row kernel, beyond the kernel with the least estimated time (us), from
-// what each cost on MI355X with cold weights: the tiled kernels take ceil(tiles / 256) rounds of K / 128 steps of
-// 0.44 (64 x 128), 0.60 (128 x 128), 1.0 (128 x 256) and 1.75 us (256 x 256), the
-// row kernel moves (64 + 16 CT) K bytes for each workgroup at 45 bytes per ns and CU.
-// Measured / estimated: 64 x 7168 x 7168 18.9 / 18.3 (rows, CT 2), 25.6 with CT 4, 32.6
-// on 64 x 128; 200 x 2048 x 2048 6.6 / 7.4 (rows), 10.2 on 64 x 128; 512 x 4096 x 7168
-// 30.5 / 29.6 (64 x 128), 38.6 by rows, 56 on 128 x 256; 1024 x 7168 x 7168 66 / 61
-// (128 x 256), 99 on 256 x 256; 4096 x 4096 x 7168 114 / 103 (256 x 256), 132 on
-// 128 x 256.
+// what each cost on MI355X with cold weights: a call costs 3 to 3.5, each round of 256
+// workgroups its beginning and end and its part of the contraction, K / 128 steps of the
+// tiled kernels, (64 + 16 CT) K bytes of the row kernel at about 95 bytes per ns and CU.
+// Measured / estimated: 518 x 2000 x 160 6.2 / 6.4 (64 x 128), 10.2 / 10.1 by rows with CT 2,
+// 12.6 / 13.4 with CT 4; 256 x 4096 x 4096 14.1 / 13.2 (rows, CT 4), 16.0 / 16.6 on 64 x 128;
+// 512 x 4096 x 7168 25.5 / 24.7 (64 x 128), 56 on 128 x 256; 1024 x 7168 x 7168 66 / 66
+// (128 x 256), 99 on 256 x 256; 2000 x 4000 x 512 14.6 / 14 (128 x 256), 15.8 on 64 x 128, 18.8 on
+// 256 x 256; 4000 x 8000 x 4096 139 / 140 (256 x 256), 160 on 128 x 256; 4096 x 4096 x 7168
+// 114 / 114 (256 x 256), 132 on 128 x 256.
 moe_status linear_impl(const LinArgs& a, hipStream_t strm) {
   // up to 16 rows: two column tiles for each wave, which halves the rows' share of the
   // loads, where that leaves half a CU's worth of workgroups (16 x 7168 x 7168 12.9
@@ -405,12 +406,10 @@ moe_status linear_impl(const LinArgs& a, hipStream_t strm) {
   // x 7168 9.3 against 10.9 us, 200 x 1024 x 7168 9.6 against 10.9; 2000 x 128 x 7168 19 against 13)
   if (up(a.M, 64) * up(a.N, 16) <= 256 && up(a.M, 64) <= up(a.N, 16)) return launch_rows<4, 1, 2, 2, 8>(a, strm);
   const double steps = up(a.K, 128);
-  auto tiled = [&](int bm, int bn, double c) { return up((int64_t)(up(a.M, bm) * up(a.N, bn)), 256) * steps * c + 5; };
-  auto rows = [&](int ct) {
-    return std::max(1.0, up(a.M, 64) * up(a.N, 16 * ct) / 256) * (64 + 16 * ct) * (double)a.K / 45e3 + 3;
-  };
-  const double t[6] = {rows(2), rows(4), tiled(64, 128, 0.44), tiled(128, 128, 0.60), tiled(128, 256, 1.0),
-                       tiled(256, 256, 1.75)};
+  auto rounds = [&](int bm, int bn) { return up((int64_t)(up(a.M, bm) * up(a.N, bn)), 256); };
+  const double t[6] = {3 + rounds(64, 32) * (2.2 + a.K / 980.0),         3 + rounds(64, 64) * (5 + a.K / 780.0),
+                       3.5 + rounds(64, 128) * (2.2 + 0.34 * steps),     3.5 + rounds(128, 128) * (4.5 + 0.6 * steps),
+                       3.5 + rounds(128, 256) * (6.5 + steps),           3.5 + rounds(256, 256) * (12 + 1.75 * steps)};
   int best = 0;
   // (the row kernel's workgroups: ceil(M / 64) lie along the grid's second axis)
   for (int i = a.M > 64 * 65535 ? 2 : 1; i < 6; ++i)
