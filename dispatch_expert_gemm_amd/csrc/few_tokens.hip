@@ -9,7 +9,8 @@
 //
 // A shared expert is one more expert that every token goes to with weight 1.
 //
-// Kernels.  T <= 16: k_few_gate_up, k_few_down.  T > 16: k_few_prep, k_few_gate_up,
+// Kernels.  T <= 16: k_few_gate_up, k_few_down, or for narrow layers k_few_down_y and
+// k_few_join in the latter's place (few_joins).  T > 16: k_few_prep, k_few_gate_up,
 // k_few_down_y, k_few_join.  int8 has its rows quantised by k_few_prep (x, times the
 // expert's smooth scales) and k_few_quant_h (h); one or two tokens (HELD) form the
 // codes inside the two kernels that use them.
@@ -41,6 +42,7 @@
 // F = 2048: 146 us, 5.4 TB/s (int8 84 us, 4.7); 13 tokens 440 to 470 us, 5.7 to 6.0 TB/s
 // (9 in int8 231 us, 5.5); 64 tokens on 8 experts of 14336 x 4096 515 us, 5.5 TB/s; 64 tokens
 // in int8 308 us, 4.7.  One token of 64 experts of 1536 x 480: 15.6 us, of which the bytes are 6.
+#include <cmath>
 #include <initializer_list>
 
 #include "combine_token.hpp"
@@ -809,8 +811,28 @@ __global__ __launch_bounds__(256) void k_few_join(FewArgs a) {
   for (int q = 0; q < 4; ++q) few_finish(a, code, t, c + q, v[q]);
 }
 
-// Whether the down kernel sums over the experts itself (two kernels in all).
-bool few_joins(int T) { return T <= 16; }
+// int8: whether the rows are quantised inside the two kernels.
+bool few_held(const FewArgs& a, bool i8) {
+  return i8 && a.T <= kHeldTokens && a.H <= 4 * 8 * kUpWaves * kWave &&
+         held_h_bytes(a.T * a.K, a.T, a.F, a.Fs) <= kHeldBytes;
+}
+
+// Whether the down kernel sums over the experts itself: its H / 16 workgroups, each over
+// all active experts, against workgroups by expert and a launch for the sums.  A narrow
+// layer has too few of the former.  Both are estimated (us) for slots spread evenly over
+// the experts.  Itself / by expert, measured, the whole layer in bf16: 1 token of 64 experts
+// of 1536 x 480 15.2 / 20.2 us, 6 tokens 42.2 / 39.0, 16 tokens 59.9 / 52.5; 1 token of 38
+// experts of 672 x 3744 36.7 / 37.4, 6 tokens 129 / 70; 16 tokens of 16 experts of 3584 x 2048
+// 136.6 / 143.5.
+bool few_joins(const FewArgs& a, bool i8) {
+  if (a.T > 16) return false;
+  if (a.H > 16 * 256 || few_held(a, i8)) return true;
+  const double es = i8 ? 1 : 2, active = a.E * (1 - std::exp(-(double)a.T * a.K / a.E));
+  const double bytes = (active * (double)a.F + a.Fs) * es;  // of one column
+  const double itself = bytes * 16 / 38e3 + 0.15 * active;
+  const int columns = stream_steps((int64_t)(a.F * es)) < kYOwn ? 128 : 64;
+  return itself <= std::fmax(columns * a.F * es / 60e3, bytes * a.H / 5e6) + 5;
+}
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -839,7 +861,7 @@ size_t few_layout(FewArgs& a, bool i8, char* base) {
     a.shhi = reinterpret_cast<bf16_t*>(take(T * Fs * 2));
     a.shlo = reinterpret_cast<bf16_t*>(take(T * Fs * 2));
   }
-  if (!few_joins(a.T)) a.y = reinterpret_cast<float*>(take((S + T) * H * 4));
+  if (!few_joins(a, i8)) a.y = reinterpret_cast<float*>(take((S + T) * H * 4));
   return n < 256 ? 256 : n;
 }
 
@@ -888,7 +910,7 @@ bool launch_down_as(const FewArgs& a, hipStream_t strm) {
 }
 
 // 16 columns for a workgroup while those workgroups do not exceed the 256 CUs, else 32:
-// H = 1536 with 16 tokens 57.9 against 74.8 us for the layer, H = 4096 240 against 267;
+// H = 1536 with 2 tokens 20.2 against 23.0 us for the layer, H = 4096 with 16 240 against 267;
 // H = 5120 with 4 tokens 134.9 against 128.2, H = 7168 equal (int8 4 us slower with 16).
 // Sixteen or four waves: within 2% of eight, H = 1536 more than 10% slower.
 template <bool I8, bool HELD>
@@ -915,7 +937,7 @@ moe_status few_launch(FewArgs& a, hipStream_t strm) {
   constexpr bool ROUTE = RTM > 1;
   const int S = a.T * a.K;
   if constexpr (I8 && RTM == 1) {
-    if (a.T <= kHeldTokens && a.H <= 4 * 8 * kUpWaves * kWave && held_h_bytes(S, a.T, a.F, a.Fs) <= kHeldBytes)
+    if (few_held(a, true))
       return launch_up<true, 1, kUpWaves, true>(a, strm) && launch_down<true, true>(a, strm) ? launch_status() : MOE_ERR_HIP;
   }
   if (ROUTE || I8)
@@ -930,7 +952,7 @@ moe_status few_launch(FewArgs& a, hipStream_t strm) {
     if (a.F > 8192 || a.Fs > 8192) hipLaunchKernelGGL(k_few_quant_h<8>, rows, dim3(8 * kWave), 0, strm, a);
     else hipLaunchKernelGGL(k_few_quant_h<4>, rows, dim3(4 * kWave), 0, strm, a);
   }
-  if constexpr (RTM == 1)
+  if (RTM == 1 && few_joins(a, I8))
     ok = ok && launch_down<I8, false>(a, strm);
   else
     ok = ok && (stream_steps(a.F * ES) < kYOwn ? launch_y<I8, RTM, 1>(a, strm) : launch_y<I8, RTM, kYWaves>(a, strm));
@@ -1010,7 +1032,7 @@ extern "C" moe_status moe_few_tokens_workspace_size(const moe_shape* s, int64_t 
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_NULL_ARG;
   FewArgs a = {};
-  a.T = (int)s->T; a.K = s->K; a.H = s->H; a.F = s->F; a.Fs = shared_F;
+  a.T = (int)s->T; a.K = s->K; a.E = s->num_experts; a.H = s->H; a.F = s->F; a.Fs = shared_F;
   a.groups = a.T * a.K < s->num_experts ? a.T * a.K : s->num_experts;
   *bytes = few_layout(a, int8 == 1, nullptr);
   return MOE_OK;

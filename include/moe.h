@@ -773,8 +773,9 @@ moe_status moe_decode_fused(const moe_shape* s, const void* x, const int32_t* to
  * in it needs clearing.  Calls that share one must not overlap in time. */
 moe_status moe_few_tokens_workspace_size(const moe_shape* s, int64_t shared_F, int32_t int8, size_t* bytes);
 
-/* moe_few_tokens - bf16 weights.  Two kernel launches for T <= 16 (gate/up, which sorts
- * the slots by expert, and down), four above (sort, gate/up, down, weighted sums).
+/* moe_few_tokens - bf16 weights.  Two or, for narrow layers, three kernel launches for
+ * T <= 16 (gate/up, which sorts the slots by expert, down, weighted sums), four above
+ * (sort, gate/up, down, weighted sums).
  *  in   x (T, H) bf16, topk_idx (T, K) int32, topk_weights (T, K) fp32,
  *       x_active_mask as for moe_dispatch
  *  in   w_gate, w_up (E, F, H), w_down (E, H, F) bf16; shared_w_* likewise or NULL
@@ -804,7 +805,7 @@ moe_status moe_few_tokens(const moe_shape* s, const void* x, const int32_t* topk
  * value on the border between two codes (exactly amax/2, say) may get the other one.
  * A row that holds an infinity or a NaN gives results that are not finite.
  * One or two tokens: two launches where a row of H <= 8192 and all rows of h (48 KiB)
- * fit a workgroup; else, and up to 16 tokens, four; above five.
+ * fit a workgroup; else, and up to 16 tokens, four or five; above five.
  *  in   smooth_scales NULL or (E, H) fp32, on a 16-byte boundary
  *  in   w[3] gate, up, down; shared_w NULL or three weights
  *  other arguments as moe_few_tokens.  H a multiple of 16 (MOE_ERR_BAD_SHAPE); H, F

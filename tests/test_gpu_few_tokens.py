@@ -84,6 +84,9 @@ CASES = {
     "one token, wide": dict(T=1, H=4112, F=352, E=4, K=2, shared=32),
     "h rows past 8192": dict(T=3, H=160, F=8224, E=2, K=1, shared=32),
     "shared h rows past 8192": dict(T=18, H=160, F=64, E=4, K=2, shared=8224),
+    "narrow, by expert": dict(T=12, H=592, F=1120, E=33, K=6, shared=64, mask="2d", Z=1, C=1, Q=1),
+    "narrow, long": dict(T=6, H=208, F=5184, E=12, K=4),
+    "narrow, full tile": dict(T=16, H=272, F=2624, E=5, K=3, one_expert=False, mask="1d"),
     "short contractions": dict(T=40, H=64, F=32, E=3, K=2, shared=32),
     "long contractions": dict(T=20, H=2064, F=5152, E=2, K=1),
     "long contractions, four tiles": dict(T=64, H=2064, F=5152, E=3, K=2, one_expert=False, shared=2592),
