@@ -830,8 +830,10 @@ bool few_joins(const FewArgs& a, bool i8) {
   const double es = i8 ? 1 : 2, active = a.E * (1 - std::exp(-(double)a.T * a.K / a.E));
   const double bytes = (active * (double)a.F + a.Fs) * es;  // of one column
   const double itself = bytes * 16 / 38e3 + 0.15 * active;
-  const int columns = stream_steps((int64_t)(a.F * es)) < kYOwn ? 128 : 64;
-  return itself <= std::fmax(columns * a.F * es / 60e3, bytes * a.H / 5e6) + 5;
+  // one workgroup by expert: 128 columns with a step or two of loads under way, or 64 with more
+  const bool own = stream_steps((int64_t)(a.F * es)) < kYOwn;
+  const double one = a.F * es * (own ? 128 / (i8 ? 45e3 : 25e3) : 64 / 60e3);
+  return itself <= std::fmax(one, bytes * a.H / 5e6) + 5;
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
