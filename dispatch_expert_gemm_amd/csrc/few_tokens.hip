@@ -1,6 +1,6 @@
 // A whole MoE layer forward for a few tokens (T <= 64): every expert's weights are
 // read from memory once, whatever the number of its rows, and nothing is rounded
-// between x and out.
+// below fp32 between x and out (int8: but to the codes).
 //
 //   gate/up   for every active slot s = (t, k) of expert e:
 //             h_s = silu(Wg_e x_t) * (Wu_e x_t)
@@ -33,9 +33,8 @@
 // have no register result; each wave has a ring of a few steps for itself and waits by
 // count, so the main loops have no barrier (stream_mfma.hpp).
 //
-// bf16: h leaves as two bf16 planes, hi = bf16(h) and lo = bf16(h - hi), 16
-// significant bits in all; both multiply the same weight registers.  int8: sums are
-// exact integers.
+// bf16: h leaves in fp32, and its three bf16 parts, every bit of it, multiply the same
+// weight registers.  int8: sums are exact integers.
 //
 // Bound: HBM, the active experts' weights (reads reach 6.0 TB/s here).  Layers on
 // MI355X with cold weights: one token, 8 of 32 experts and a shared one, H = 7168,
@@ -111,10 +110,8 @@ struct FewArgs {
   int32_t* err_flag;
   char* table;  // workspace: the route
   // workspace; rows of slots, then the shared expert's rows of tokens
-  bf16_t* hhi;
-  bf16_t* hlo;
-  bf16_t* shhi;
-  bf16_t* shlo;
+  float* h[2];   // bf16: fp32 rows in two planes
+  float* sh[2];
   int8_t* xq;  // T rows of x, then T K rows of x * smooth
   float* xs;
   float* hf;
@@ -343,10 +340,11 @@ __device__ __forceinline__ void row_offsets(int n, int64_t bytes, uint32_t (&xof
     }
 }
 
-// G and U of four columns of one row (int8: of scale xs) -> h at `at`.
+// G and U of four columns of one row (int8: of scale xs) -> h from column c on.
 template <bool I8>
-__device__ __forceinline__ void swiglu_store(const FewArgs& a, bool sh, int slot, float xs, int64_t wrow, int64_t at,
+__device__ __forceinline__ void swiglu_store(const FewArgs& a, bool sh, int slot, float xs, int64_t wrow, int64_t c,
                                              const typename MfmaAcc<I8>::type& sg, const typename MfmaAcc<I8>::type& su) {
+  const int64_t F = sh ? a.Fs : a.F;
   float h[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -357,20 +355,8 @@ __device__ __forceinline__ void swiglu_store(const FewArgs& a, bool sh, int slot
     }
     h[q] = g / (1.0f + __expf(-g)) * u;
   }
-  if constexpr (I8) {
-    *reinterpret_cast<float4*>((sh ? a.shf : a.hf) + at) = make_float4(h[0], h[1], h[2], h[3]);
-  } else {
-    float lo[4];
-    uint32_t hi[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      hi[q] = f2bf(h[q]);
-      // nothing below an infinite or NaN high part
-      lo[q] = (hi[q] & 0x7f80u) == 0x7f80u ? 0.f : h[q] - bf2f(hi[q]);
-    }
-    *reinterpret_cast<uint2*>((sh ? a.shhi : a.hhi) + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-    *reinterpret_cast<uint2*>((sh ? a.shlo : a.hlo) + at) = make_uint2(pack_bf2(lo[0], lo[1]), pack_bf2(lo[2], lo[3]));
-  }
+  float* at = I8 ? (sh ? a.shf : a.hf) + (int64_t)slot * F + c : plane_at(sh ? a.sh : a.h, F, slot, c);
+  *reinterpret_cast<float4*>(at) = make_float4(h[0], h[1], h[2], h[3]);
 }
 
 // An expert's rows (at most 16 RT, XI = 1: 8) through its gate and up columns from f0
@@ -407,7 +393,7 @@ __device__ __forceinline__ void gate_up_rows(const FewArgs& a, const uint16_t* s
     const int i = 16 * r + lane % 16;
     if (!in || i >= n) return;
     const int slot = sh ? i : slots[i];
-    swiglu_store<I8>(a, sh, slot, I8 ? a.xs[x_row(slot)] : 1.f, wrow + c, (int64_t)slot * F + f0 + c, g, u);
+    swiglu_store<I8>(a, sh, slot, I8 ? a.xs[x_row(slot)] : 1.f, wrow + c, f0 + c, g, u);
   };
   if constexpr (KS == 1) {
 #pragma unroll
@@ -478,7 +464,7 @@ __device__ __forceinline__ void gate_up_held(const FewArgs& a, const uint16_t* s
     for (int v = 0; v < W; ++v) s[g] += red2[v * (RING / 16) + g * kWave + lane];
   const int slot = sh ? mine : slots[mine];
   const int64_t c = 4 * (lane / 16);
-  swiglu_store<true>(a, sh, slot, scales[mine], wrow + c, (int64_t)slot * F + f0 + c, s[0], s[1]);
+  swiglu_store<true>(a, sh, slot, scales[mine], wrow + c, f0 + c, s[0], s[1]);
 }
 
 // RTM: row tiles that T tokens may need (1, 2 or 4).  RTM = 1 routes for itself, and
@@ -534,17 +520,22 @@ __device__ __forceinline__ void down_stream(const FewArgs& a, const uint16_t* sl
                                             int s1, char* ring, typename MfmaAcc<I8>::type (&acc)[CT][RT]) {
   constexpr int ES = I8 ? 1 : 2, PX = I8 ? 1 : 2;
   const bool sh = slots == nullptr;
-  const int64_t bytes = (sh ? a.Fs : a.F) * ES, rows = sh ? a.T : (int64_t)a.T * a.K;
+  const int64_t F = sh ? a.Fs : a.F, bytes = F * ES, pitch = I8 ? F : plane_pitch(F);
+  const int64_t rows = sh ? a.T : (int64_t)a.T * a.K;
   i32x4_t w[CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     w[c] = down_weights(a, sh, e, c0, c, bytes);
   }
   i32x4_t x[PX];
-  x[0] = buffer_of(I8 ? static_cast<const void*>(sh ? a.shq : a.hq) : static_cast<const void*>(sh ? a.shhi : a.hhi), rows * bytes);
-  if constexpr (!I8) x[1] = buffer_of(sh ? a.shlo : a.hlo, rows * bytes);
+  if constexpr (I8) {
+    x[0] = buffer_of(sh ? a.shq : a.hq, rows * pitch);
+  } else {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) x[p] = buffer_of(sh ? a.sh[p] : a.h[p], rows * pitch);
+  }
   uint32_t xoff[RT][XI];
-  row_offsets<RT, XI>(n, bytes, xoff, [&](int i) { return sh ? i : (int)slots[i]; });
+  row_offsets<RT, XI>(n, pitch, xoff, [&](int i) { return sh ? i : (int)slots[i]; });
 #pragma unroll
   for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -858,10 +849,8 @@ size_t few_layout(FewArgs& a, bool i8, char* base) {
     a.shq = reinterpret_cast<int8_t*>(take(T * Fs));
     a.shs = reinterpret_cast<float*>(take(T * 4));
   } else {
-    a.hhi = reinterpret_cast<bf16_t*>(take(S * F * 2));
-    a.hlo = reinterpret_cast<bf16_t*>(take(S * F * 2));
-    a.shhi = reinterpret_cast<bf16_t*>(take(T * Fs * 2));
-    a.shlo = reinterpret_cast<bf16_t*>(take(T * Fs * 2));
+    for (float*& p : a.h) p = reinterpret_cast<float*>(take(S * plane_pitch(F)));
+    for (float*& p : a.sh) p = reinterpret_cast<float*>(take(T * plane_pitch(Fs)));
   }
   if (!few_joins(a, i8)) a.y = reinterpret_cast<float*>(take((S + T) * H * 4));
   return n < 256 ? 256 : n;
@@ -876,7 +865,8 @@ moe_status check_few(const moe_shape* s, int64_t shared_F, bool i8) {
   if (i8 && (s->H > 131072 || s->F > 131072 || shared_F > 131072)) return MOE_ERR_UNSUPPORTED;
   if (s->comm_quant_mode != 0) return MOE_ERR_UNSUPPORTED;
   if (s->T > kMaxTokens) return MOE_ERR_UNSUPPORTED;
-  // the rows of h are addressed with 31-bit offsets (those of x end below 2^27)
+  // the rows of h (of a plane, F * 2 bytes and at most 64 more, or of codes) are addressed
+  // with 31-bit offsets: 1024 of them of F <= 2^20 - 32 end at 2^31 (those of x below 2^27)
   if (s->T * s->K * s->F * 2 >= 0x7ffffff0) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -752,14 +752,14 @@ moe_status moe_decode_fused(const moe_shape* s, const void* x, const int32_t* to
 /* ------------------------------------------------------------- few tokens
  * A whole MoE layer forward for a decode step of at most 64 tokens.  Each active
  * expert's weights are read from memory once, there are no expanded rows, and
- * nothing is rounded between x and out:
+ * nothing is rounded below fp32 between x and out (int8: but to the codes):
  *   out[t] = bf16(sum over k of topk_weights[t,k] * v(t,k) + shared[t])
  * with v = Wd_e (silu(Wg_e x_t) * (Wu_e x_t)) for a routed slot, 0 for a zero
  * expert and for a masked, out-of-range or repeated slot, x_t for a copy expert,
  * alpha_1[j] * x_t + alpha_2[j] * v[j] for constant expert j (low_latency_combine
- * page, Function and Parameters; ori_x is x).  h keeps 16 significant bits (two
- * bf16 parts), every sum is fp32, so out is closer to the exact value than the
- * chain moe_route .. moe_combine, which rounds G, U, h and y to bf16.
+ * page, Function and Parameters; ori_x is x).  h and every sum are held in fp32, so
+ * out is closer to the exact value than the chain moe_route .. moe_combine, which
+ * rounds G, U, h and y to bf16.
  * shared[t] is shared_expert_x[t], or the shared expert's FFN of x_t when its
  * weights are given (shared_F > 0: (1, shared_F, H), (1, shared_F, H),
  * (1, H, shared_F)), or nothing; giving both is MOE_ERR_BAD_RANGE.
