@@ -35,12 +35,15 @@ struct LinArgs {
   int64_t M, N, K;
 };
 
-// one workgroup of WAVES waves per row
+// One workgroup of WAVES waves per row, kQuantRows of them along the grid's first axis: an
+// axis holds fewer than 2^32 threads.
+constexpr int64_t kQuantRows = 1 << 20;
 template <int WAVES>
-__global__ __launch_bounds__(WAVES* kWave) void k_quant_x(const uint4* __restrict__ x, int64_t K, uint2* __restrict__ codes,
-                                                 float* __restrict__ scales) {
+__global__ __launch_bounds__(WAVES* kWave) void k_quant_x(const uint4* __restrict__ x, int64_t M, int64_t K,
+                                                          uint2* __restrict__ codes, float* __restrict__ scales) {
   __shared__ uint32_t red[WAVES];
-  const int64_t r = blockIdx.x;
+  const int64_t r = blockIdx.y * kQuantRows + blockIdx.x;
+  if (r >= M) return;
   const uint4* src = x + r * (K / 8);
   uint2* dst = codes + r * (K / 8);
   const float s = quant_row_int8<WAVES>(
@@ -366,8 +369,9 @@ moe_status check_linear(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N <= 0 || K <= 0 || K % 16 != 0) return MOE_ERR_BAD_SHAPE;
   // |sum| <= 127 * 127 * K stays below 2^31
   if (K > 131072) return MOE_ERR_UNSUPPORTED;
-  // a grid's size stays below 2^31
-  if (M > (int64_t)1 << 24 || N > (int64_t)1 << 24 || M * N > (int64_t)1 << 42) return MOE_ERR_UNSUPPORTED;
+  // An axis of a grid holds fewer than 2^32 threads: 512 for each 16 to 64 columns or, on
+  // large outputs, each 256 x 256 tile (2^31 for 2^38 outputs, 512 GiB)
+  if (M > (int64_t)1 << 24 || N > (int64_t)1 << 24 || M * N > (int64_t)1 << 38) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -471,11 +475,14 @@ extern "C" moe_status moe_linear_int8_dynamic(int64_t M, int64_t N, int64_t K, c
   // few rows (8 rows of 7168: 15.8 against 16.3 us; 8192 of 2048: 44.5 against 39.4)
   auto quant = [&](auto waves) {
     constexpr int W = decltype(waves)::value;
-    hipLaunchKernelGGL((k_quant_x<W>), dim3((unsigned)M), dim3(W * kWave), 0, as_stream(stream),
-                       static_cast<const uint4*>(x), K, reinterpret_cast<uint2*>(xq), xs);
+    const dim3 grid((unsigned)std::min(M, kQuantRows), (unsigned)((M + kQuantRows - 1) / kQuantRows));
+    hipLaunchKernelGGL((k_quant_x<W>), grid, dim3(W * kWave), 0, as_stream(stream), static_cast<const uint4*>(x), M, K,
+                       reinterpret_cast<uint2*>(xq), xs);
+    return launch_status();
   };
-  if (K > 16384) quant(std::integral_constant<int, 16>());
-  else if (K > 8192 || (K > 4096 && M <= 256)) quant(std::integral_constant<int, 8>());
-  else quant(std::integral_constant<int, 4>());
+  const moe_status qs = K > 16384 ? quant(std::integral_constant<int, 16>())
+                        : K > 8192 || (K > 4096 && M <= 256) ? quant(std::integral_constant<int, 8>())
+                                                             : quant(std::integral_constant<int, 4>());
+  if (qs != MOE_OK) return qs;
   return linear_impl({xq, xs, wq, ws, bias, static_cast<bf16_t*>(out), M, N, K}, as_stream(stream));
 }

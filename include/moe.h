@@ -821,7 +821,7 @@ moe_status moe_few_tokens_int8(const moe_shape* s, const void* x, const int32_t*
  * The dense product of the int8 path (the projections around the layer):
  *   out[m, n] = bf16((sum over k of xq[m, k] * wq[n, k]) * (xs[m] * ws[n]) + bias[n])
  * with an exact integer sum, for any M >= 0 and N >= 1 and K a positive multiple
- * of 16 (MOE_ERR_BAD_SHAPE) up to 131072; M and N at most 2^24, M*N at most 2^42
+ * of 16 (MOE_ERR_BAD_SHAPE) up to 131072; M and N at most 2^24, M*N at most 2^38
  * (MOE_ERR_UNSUPPORTED).
  */
 
