@@ -877,6 +877,12 @@ struct FewWeight {
   const float* scales;
 };
 
+// Waves that split gate/up's contraction: all for a long one, a short one is a wave's own.
+int up_split(const FewArgs& a, bool i8) { return stream_steps(a.H * (i8 ? 1 : 2)) < kUpOwn ? 1 : kUpWaves; }
+
+// Workgroups of gate/up, each with COLS columns of F.
+int64_t up_groups(const FewArgs& a, int COLS) { return a.groups * ((a.F + COLS - 1) / COLS) + (a.Fs + COLS - 1) / COLS; }
+
 template <bool I8, int RTM, int KS, bool HELD>
 bool launch_up(const FewArgs& a, hipStream_t strm) {
   constexpr int COLS = 16 * kUpWaves / KS;
@@ -884,10 +890,9 @@ bool launch_up(const FewArgs& a, hipStream_t strm) {
   const int lds = (RTM == 1 ? route_work_bytes(a.T * a.K, a.E, a.groups) : 0) +
                   (HELD ? kUpWaves * kHeldUpDepth * kSlot<2, 0, 0> + a.T * held_pitch(a.H) + kHeldTokens * (4 + 4 * kUpWaves)
                         : kUpWaves * kUpRing<RTM>);
-  const int64_t n = a.groups * ((a.F + COLS - 1) / COLS) + (a.Fs + COLS - 1) / COLS;
   if (!lds_allowed<k>(lds)) return false;
-  hipLaunchKernelGGL(k, dim3((unsigned)n), dim3(kUpWaves * kWave), lds, strm, a);
-  return true;
+  hipLaunchKernelGGL(k, dim3((unsigned)up_groups(a, COLS)), dim3(kUpWaves * kWave), lds, strm, a);
+  return launch_status() == MOE_OK;
 }
 
 template <bool I8, int CT, bool HELD>
@@ -898,7 +903,7 @@ bool launch_down_as(const FewArgs& a, hipStream_t strm) {
                   (HELD ? (S + a.T + 3) / 4 * 16 + held_h_bytes(S, a.T, a.F, a.Fs) : 0);
   if (!lds_allowed<k>(lds)) return false;
   hipLaunchKernelGGL(k, dim3((unsigned)((a.H + 16 * CT - 1) / (16 * CT))), dim3(kDownWaves * kWave), lds, strm, a);
-  return true;
+  return launch_status() == MOE_OK;
 }
 
 // 16 columns for a workgroup while those workgroups do not exceed the 256 CUs, else 32:
@@ -917,12 +922,14 @@ bool launch_y(const FewArgs& a, hipStream_t strm) {
   const int64_t n = (a.groups + (a.Fs > 0)) * ((a.H + COLS - 1) / COLS);
   if (!lds_allowed<k>(lds)) return false;
   hipLaunchKernelGGL(k, dim3((unsigned)n), dim3(kYWaves * kWave), lds, strm, a);
+  if (launch_status() != MOE_OK) return false;
   const dim3 grid((unsigned)((a.H + 1023) / 1024), (unsigned)a.T);
   if (a.K <= 8) hipLaunchKernelGGL(k_few_join<8>, grid, dim3(256), 0, strm, a);
   else hipLaunchKernelGGL(k_few_join<16>, grid, dim3(256), 0, strm, a);
-  return true;
+  return launch_status() == MOE_OK;
 }
 
+// (no kernel is launched behind one that was not)
 template <bool I8, int RTM>
 moe_status few_launch(FewArgs& a, hipStream_t strm) {
   constexpr int ES = I8 ? 1 : 2;
@@ -930,25 +937,28 @@ moe_status few_launch(FewArgs& a, hipStream_t strm) {
   const int S = a.T * a.K;
   if constexpr (I8 && RTM == 1) {
     if (few_held(a, true))
-      return launch_up<true, 1, kUpWaves, true>(a, strm) && launch_down<true, true>(a, strm) ? launch_status() : MOE_ERR_HIP;
+      return launch_up<true, 1, kUpWaves, true>(a, strm) && launch_down<true, true>(a, strm) ? MOE_OK : MOE_ERR_HIP;
   }
-  if (ROUTE || I8)
+  if (ROUTE || I8) {
     hipLaunchKernelGGL((k_few_prep<ROUTE, I8>), dim3((ROUTE ? 1 : 0) + (I8 ? a.T + (a.smooth ? S : 0) : 0)), dim3(256),
                        ROUTE ? route_work_bytes(S, a.E, a.groups) : 16, strm, a);
-  // waves split a long contraction; a short one is a wave's own
-  bool ok = stream_steps(a.H * ES) < kUpOwn ? launch_up<I8, RTM, 1, false>(a, strm)
-                                           : launch_up<I8, RTM, kUpWaves, false>(a, strm);
+    if (launch_status() != MOE_OK) return MOE_ERR_HIP;
+  }
+  if (!(up_split(a, I8) == 1 ? launch_up<I8, RTM, 1, false>(a, strm) : launch_up<I8, RTM, kUpWaves, false>(a, strm)))
+    return MOE_ERR_HIP;
   if constexpr (I8) {
     // waves for a row to fit their registers (F = 14336: 3 us less of 165 to 278)
     const dim3 rows(S + (a.Fs ? a.T : 0));
     if (a.F > 8192 || a.Fs > 8192) hipLaunchKernelGGL(k_few_quant_h<8>, rows, dim3(8 * kWave), 0, strm, a);
     else hipLaunchKernelGGL(k_few_quant_h<4>, rows, dim3(4 * kWave), 0, strm, a);
+    if (launch_status() != MOE_OK) return MOE_ERR_HIP;
   }
+  bool ok;
   if (RTM == 1 && few_joins(a, I8))
-    ok = ok && launch_down<I8, false>(a, strm);
+    ok = launch_down<I8, false>(a, strm);
   else
-    ok = ok && (stream_steps(a.F * ES) < kYOwn ? launch_y<I8, RTM, 1>(a, strm) : launch_y<I8, RTM, kYWaves>(a, strm));
-  return ok ? launch_status() : MOE_ERR_HIP;
+    ok = stream_steps(a.F * ES) < kYOwn ? launch_y<I8, RTM, 1>(a, strm) : launch_y<I8, RTM, kYWaves>(a, strm);
+  return ok ? MOE_OK : MOE_ERR_HIP;
 }
 
 // The kernels read and write vectors of up to 16 bytes.
@@ -1001,8 +1011,8 @@ moe_status few_impl(const moe_shape* s, bool i8, const void* x, const int32_t* t
   a.groups = S < a.E ? S : a.E;
   const size_t need = few_layout(a, i8, static_cast<char*>(workspace));
   if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
-  // gate/up tiles
-  if ((int64_t)a.groups * (a.F / 16) + Fs / 16 > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  // gate/up's grid holds fewer than 2^32 threads on its axis (the others are smaller)
+  if (up_groups(a, 16 * kUpWaves / up_split(a, i8)) * (kUpWaves * kWave) >= (int64_t)1 << 32) return MOE_ERR_UNSUPPORTED;
   if (S == 0) {
     // the error flag alone
     hipLaunchKernelGGL((k_few_prep<true, false>), dim3(1), dim3(256), route_work_bytes(0, a.E, 0), strm, a);

@@ -785,7 +785,8 @@ moe_status moe_few_tokens_workspace_size(const moe_shape* s, int64_t shared_F, i
  *  ws   workspace >= moe_few_tokens_workspace_size bytes
  * s->capacity is checked as everywhere and not used otherwise.
  * MOE_ERR_UNSUPPORTED: T > 64, comm_quant_mode != 0, T*K*F*2 not below 2^31
- * bytes.  MOE_ERR_BAD_SHAPE: F or shared_F not a multiple of 32; x, a weight or the
+ * bytes, a gate/up grid of 2^32 threads (256 for each active expert and 64 columns
+ * of F, 16 where H * 2 bytes (int8: H) are over 1920).  MOE_ERR_BAD_SHAPE: F or shared_F not a multiple of 32; x, a weight or the
  * workspace not on a 16-byte boundary. */
 moe_status moe_few_tokens(const moe_shape* s, const void* x, const int32_t* topk_idx, const float* topk_weights,
                           const uint8_t* x_active_mask, const void* w_gate, const void* w_up, const void* w_down,
