@@ -1350,6 +1350,12 @@ def _at(t, dtype, n, name, dev):
     _refuse(t, dtype, n, name, dev)
 
 
+def _shaped(t, shape, name):
+    """Raise unless t (when given) has this shape: a larger tensor would be read with another row length."""
+    if t is not None and getattr(t, "shape", None) != shape:
+        raise MoeError(f"{name} must be a tensor of shape {shape}, got {getattr(t, 'shape', t)}")
+
+
 def _device_of(x, name):
     """The number of the GPU that x is on."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
@@ -1462,7 +1468,7 @@ def _few_sizes(T, H, K, E, F, Z, C, Q, mask_ndim, Fs, int8):
 
 
 def _fits(ws, n, H):
-    f = ws[0].shape[-2]
+    f = ws[0].shape[-2] if ws[0].dim() > 1 else 0
     if ws[0].shape != (n, f, H) or ws[1].shape != (n, f, H) or ws[2].shape != (n, H, f):
         raise MoeError(f"weights {[tuple(w.shape) for w in ws]} do not fit {n} experts of {H} columns")
     return f
@@ -1485,7 +1491,8 @@ def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smo
 
     Weights (the shared expert's too): bf16 tensors w_gate, w_up (E, F, H) and w_down (E, H, F),
     or for all of them Int8Weights or (codes, scales) pairs, then optionally with
-    smooth_scales (E, H).  err_flag: an int32 tensor for the routing's MOE_FLAG_* bits."""
+    smooth_scales (E, H).  x_active_mask (T,) or (T, K), shared_expert_x (T, H), const_* (Q, H):
+    tensors of these shapes.  err_flag: an int32 tensor for the routing's MOE_FLAG_* bits."""
     dev = _device_of(x, "x")
     if stream is not None:
         _same_device(stream, dev)
@@ -1496,10 +1503,19 @@ def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smo
                 shared_w_up=shared_w_up, shared_w_down=shared_w_down, const_alpha_1=const_alpha_1,
                 const_alpha_2=const_alpha_2, const_v=const_v, zero_expert_num=zero_expert_num,
                 copy_expert_num=copy_expert_num, const_expert_num=const_expert_num, err_flag=err_flag)
+    if x.dim() != 2 or topk_idx.dim() != 2:
+        raise MoeError(f"x {tuple(x.shape)} and topk_idx {tuple(topk_idx.shape)} must be matrices")
     T, H = x.shape
     K = topk_idx.shape[-1]
     if topk_idx.shape != (T, K) or topk_weights.shape != (T, K):
         raise MoeError(f"topk_idx {tuple(topk_idx.shape)} and topk_weights {tuple(topk_weights.shape)} for {T} tokens")
+    if x_active_mask is not None and x_active_mask.shape not in ((T,), (T, K)):
+        raise MoeError(f"x_active_mask must be of shape {(T,)} or {(T, K)}, got {tuple(x_active_mask.shape)}")
+    _shaped(shared_expert_x, (T, H), "shared_expert_x")
+    if const_expert_num > 0:
+        _shaped(const_alpha_1, (const_expert_num, H), "const_alpha_1")
+        _shaped(const_alpha_2, (const_expert_num, H), "const_alpha_2")
+        _shaped(const_v, (const_expert_num, H), "const_v")
     int8 = not isinstance(w_gate, torch.Tensor)
     w = (w_gate, w_up, w_down)
     shared_w = _shared_weights(shared_w_gate, shared_w_up, shared_w_down)
@@ -1508,12 +1524,16 @@ def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smo
         E = codes[0].shape[0]
         F = _fits(codes, E, H)
         Fs = 0 if shared_w is None else _fits([_int8_pair(v)[0] for v in shared_w], 1, H)
+        for v in w if shared_w is None else (*w, *shared_w):
+            q, s = _int8_pair(v)
+            _shaped(s, q.shape[:-1], "int8 weight scales")
     else:
         E = w_gate.shape[0]
         F = _fits(w, E, H)
         Fs = 0 if shared_w is None else _fits(shared_w, 1, H)
         if smooth_scales is not None:
             raise MoeError("smooth_scales go with int8 weights")
+    _shaped(smooth_scales, (E, H), "smooth_scales")
     shape, ws_bytes = _few_sizes(T, H, K, E, F, zero_expert_num, copy_expert_num, const_expert_num,
                                  0 if x_active_mask is None else x_active_mask.dim(), Fs, int8)
     out = torch.empty((T, H), dtype=BF16, device=x.device)

@@ -1,0 +1,74 @@
+"""Arguments that the few-token layer's and the int8 product's Python calls refuse: tensors that
+are large enough and of another shape."""
+import pytest
+import torch
+
+import dispatch_expert_gemm_amd as dm
+from few_util import quant_weight
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+T, H, F, E, K, Q, FS = 4, 128, 64, 5, 2, 2, 32
+
+
+def layer(int8=False, **kw):
+    g = torch.Generator(device=DEV).manual_seed(91)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)   # noqa: E731
+    form = quant_weight if int8 else (lambda w: w)
+    args = dict(x=r(T, H), topk_idx=torch.tensor([[0, 1], [2, E], [E + 1, 3], [4, 0]], dtype=torch.int32, device=DEV),
+                topk_weights=torch.rand(T, K, generator=g, device=DEV), w_gate=form(r(E, F, H)), w_up=form(r(E, F, H)),
+                w_down=form(r(E, H, F)), const_alpha_1=r(Q, H), const_alpha_2=r(Q, H), const_v=r(Q, H), const_expert_num=Q)
+    args.update(kw)
+    return dm.moe_layer_few_tokens(**args)
+
+
+def bf(*shape):
+    return torch.ones(*shape, dtype=torch.bfloat16, device=DEV)
+
+
+def ones(*shape):
+    return torch.ones(*shape, dtype=torch.uint8, device=DEV)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x_active_mask=ones(T, K + 1)), dict(x_active_mask=ones(K, T)), dict(x_active_mask=ones(T + 1)),
+    dict(x_active_mask=ones(T, 1)), dict(x_active_mask=ones(T, K, 1)), dict(x_active_mask=ones(1)[0]),
+    dict(shared_expert_x=bf(T + 1, H)), dict(shared_expert_x=bf(H, T)), dict(shared_expert_x=bf(T * H)),
+    dict(const_alpha_1=bf(Q + 1, H)), dict(const_alpha_2=bf(H, Q)), dict(const_v=bf(Q, 2 * H)),
+    dict(x=bf(1, T, H)), dict(topk_idx=torch.zeros(T * K, dtype=torch.int32, device=DEV)), dict(w_gate=bf(E * F * H))],
+    ids=lambda kw: next(f"{k} {tuple(v.shape)}" for k, v in kw.items()))
+@pytest.mark.parametrize("int8", [False, True])
+def test_another_shape_is_refused(kw, int8):
+    if int8 and "w_gate" in kw:
+        kw = dict(w_gate=(torch.zeros(E * F * H, dtype=torch.int8, device=DEV), torch.ones(E * F, device=DEV)))
+    layer(int8=int8)
+    with pytest.raises(dm.MoeError):
+        layer(int8=int8, **kw)
+
+
+@pytest.mark.parametrize("shape", [(E, 2 * H), (H, E), (E + 1, H), (E * H,)])
+def test_smooth_scales_of_another_shape_are_refused(shape):
+    layer(int8=True, smooth_scales=torch.ones(E, H, device=DEV))
+    with pytest.raises(dm.MoeError):
+        layer(int8=True, smooth_scales=torch.ones(*shape, device=DEV))
+
+
+def test_weight_scales_of_another_shape_are_refused():
+    q, s = quant_weight(bf(E, F, H))
+    for bad in (torch.ones(E, 2 * F, device=DEV), torch.ones(E * F, device=DEV), torch.ones(F, E, device=DEV)):
+        with pytest.raises(dm.MoeError):
+            layer(int8=True, w_gate=(q, bad))
+    sw = [quant_weight(bf(*shape)) for shape in ((1, FS, H), (1, FS, H), (1, H, FS))]
+    layer(int8=True, shared_w_gate=sw[0], shared_w_up=sw[1], shared_w_down=sw[2])
+    with pytest.raises(dm.MoeError):
+        layer(int8=True, shared_w_gate=sw[0], shared_w_up=sw[1], shared_w_down=(sw[2][0], torch.ones(H, device=DEV)))
+
+
+def test_masks_of_the_documented_shapes_are_taken():
+    """A mask of ones, of either shape and type, changes nothing; constants are not looked at without
+    constant experts."""
+    want = layer()
+    for m in (ones(T), ones(T, K), ones(T).bool(), ones(T, K).bool()):
+        assert torch.equal(layer(x_active_mask=m), want)
+    idx = torch.tensor([[0, 1], [2, 3], [4, 1], [4, 0]], dtype=torch.int32, device=DEV)
+    layer(topk_idx=idx, const_expert_num=0, const_v=bf(1))
