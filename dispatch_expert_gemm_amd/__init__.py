@@ -1474,6 +1474,21 @@ def _fits(ws, n, H):
     return f
 
 
+def _weight_kind(ws):
+    """Whether these weights are int8: all of them pairs, or all tensors."""
+    n = sum(isinstance(w, torch.Tensor) for w in ws)
+    if n == len(ws):
+        return False
+    if n or not all(_is_pair(w) for w in ws):
+        raise MoeError("the weights are all tensors or all Int8Weights or (codes, scales) pairs")
+    return True
+
+
+def _is_pair(w):
+    w = _int8_pair(w)
+    return isinstance(w, (tuple, list)) and len(w) == 2 and all(isinstance(t, torch.Tensor) for t in w)
+
+
 def _shared_weights(gate, up, down):
     if gate is None and up is None and down is None:
         return None
@@ -1516,9 +1531,9 @@ def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smo
         _shaped(const_alpha_1, (const_expert_num, H), "const_alpha_1")
         _shaped(const_alpha_2, (const_expert_num, H), "const_alpha_2")
         _shaped(const_v, (const_expert_num, H), "const_v")
-    int8 = not isinstance(w_gate, torch.Tensor)
     w = (w_gate, w_up, w_down)
     shared_w = _shared_weights(shared_w_gate, shared_w_up, shared_w_down)
+    int8 = _weight_kind(w if shared_w is None else (*w, *shared_w))
     if int8:
         codes = [_int8_pair(v)[0] for v in w]
         E = codes[0].shape[0]

@@ -72,3 +72,18 @@ def test_masks_of_the_documented_shapes_are_taken():
         assert torch.equal(layer(x_active_mask=m), want)
     idx = torch.tensor([[0, 1], [2, 3], [4, 1], [4, 0]], dtype=torch.int32, device=DEV)
     layer(topk_idx=idx, const_expert_num=0, const_v=bf(1))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_weights_of_two_kinds_are_refused(int8):
+    """A bf16 weight among int8 ones and the other way round, also the shared expert's; what is neither."""
+    form = (lambda w: w) if int8 else quant_weight
+    own = quant_weight if int8 else (lambda w: w)
+    sw = [bf(1, FS, H), bf(1, FS, H), bf(1, H, FS)]
+    names = ("shared_w_gate", "shared_w_up", "shared_w_down")
+    layer(int8=int8, **{n: own(w) for n, w in zip(names, sw)})
+    for kw in (dict(w_up=form(bf(E, F, H))), dict(w_gate=form(bf(E, F, H))), dict(w_down=form(bf(E, H, F))),
+               {n: form(w) for n, w in zip(names, sw)}, dict(w_up=None), dict(w_down=(1, 2)),
+               dict(w_gate=quant_weight(bf(E, F, H))[:1])):
+        with pytest.raises(dm.MoeError):
+            layer(int8=int8, **kw)
