@@ -1566,10 +1566,17 @@ def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smo
     return out
 
 
+def _multiplies(x, wq, dim=None):
+    """(N, K) of weights wq (N, K) for rows x (..., K), of `dim` dimensions where it is given."""
+    if not isinstance(wq, torch.Tensor) or wq.dim() != 2 or x.shape[-1:] != wq.shape[1:] or dim not in (None, x.dim()):
+        raise MoeError(f"x {tuple(x.shape)} and weights {tuple(getattr(wq, 'shape', ()))} do not multiply")
+    return wq.shape
+
+
 def moe_linear_int8(xq, xs, wq, ws, bias, out, stream=None):
     """xq (M, K), wq (N, K) int8, their scales (M,), (N,) fp32, bias (N,) fp32 or None -> out (M, N) bf16."""
     dev = _device_of(xq, "xq")
-    (M, K), N = xq.shape, wq.shape[0]
+    (N, K), M = _multiplies(xq, wq, 2), xq.shape[0]
     _launch(lib().moe_linear_int8, dev, stream, M, N, K, _at(xq, I8T, M * K, "xq", dev), _at(xs, F32, M, "xs", dev),
             _at(wq, I8T, N * K, "wq", dev), _at(ws, F32, N, "ws", dev), _at(bias, F32, N, "bias", dev),
             _at(out, BF16, M * N, "out", dev))
@@ -1585,7 +1592,7 @@ def moe_linear_int8_workspace_size(M: int, N: int, K: int) -> int:
 def moe_linear_int8_dynamic(x, wq, ws, bias, out, workspace, stream=None):
     """moe_linear_int8 of bf16 rows x (M, K), quantised per row in the call."""
     dev = _device_of(x, "x")
-    (M, K), N = x.shape, wq.shape[0]
+    (N, K), M = _multiplies(x, wq, 2), x.shape[0]
     _launch(lib().moe_linear_int8_dynamic, dev, stream, M, N, K, _at(x, BF16, M * K, "x", dev),
             _at(wq, I8T, N * K, "wq", dev), _at(ws, F32, N, "ws", dev), _at(bias, F32, N, "bias", dev),
             _at(out, BF16, M * N, "out", dev), *_bytes_at(workspace, dev))
@@ -1594,18 +1601,20 @@ def moe_linear_int8_dynamic(x, wq, ws, bias, out, workspace, stream=None):
 def linear_int8(x, w, *, x_scales=None, bias=None, stream=None):
     """x (..., K) times the transpose of int8 weights (N, K) with one scale per output channel ->
     (..., N) bf16 (inference, no autograd).  w: an Int8Weights or a (codes, scales) pair.
-    x: bf16 rows, quantised per row in the call, or int8 codes with their x_scales (...);
-    bias: fp32 (N,)."""
+    x: bf16 rows, quantised per row in the call, or int8 codes with their x_scales (...); the
+    weights' scales and bias: fp32 (N,); tensors of these shapes."""
     dev = _device_of(x, "x")
     if stream is not None:
         _same_device(stream, dev)
         with torch.cuda.stream(stream):  # its output and workspace then belong to that stream
             return linear_int8(x, w, x_scales=x_scales, bias=bias)
+    if not _is_pair(w):
+        raise MoeError("the weights are an Int8Weights or a (codes, scales) pair")
     wq, ws = _int8_pair(w)
-    K = x.shape[-1]
-    if wq.dim() != 2 or wq.shape[1] != K:
-        raise MoeError(f"x {tuple(x.shape)} and weights {tuple(wq.shape)} do not multiply")
-    N = wq.shape[0]
+    N, K = _multiplies(x, wq)
+    _shaped(ws, (N,), "the weights' scales")
+    _shaped(x_scales, x.shape[:-1], "x_scales")
+    _shaped(bias, (N,), "bias")
     M = x.numel() // K if K else 0
     out = torch.empty((*x.shape[:-1], N), dtype=BF16, device=x.device)
     args = (_at(wq, I8T, N * K, "wq", dev), _at(ws, F32, N, "ws", dev), _at(bias, F32, N, "bias", dev), out.data_ptr())

@@ -87,3 +87,38 @@ def test_weights_of_two_kinds_are_refused(int8):
                dict(w_gate=quant_weight(bf(E, F, H))[:1])):
         with pytest.raises(dm.MoeError):
             layer(int8=int8, **kw)
+
+
+def test_product_arguments_of_another_shape_are_refused():
+    """linear_int8: scales and bias that are large enough; moe_linear_int8 and its dynamic form: weights
+    with more columns than the rows, which were read with the rows' length."""
+    x = bf(2, 3, 64)
+    q, s = quant_weight(x)
+    w, b = quant_weight(bf(40, 64)), torch.ones(40, device=DEV)
+    want = dm.linear_int8(x, w, bias=b)
+    assert torch.equal(dm.linear_int8(q, w, x_scales=s, bias=b), want)
+    for kw in (dict(x_scales=s.view(3, 2)), dict(x_scales=s.view(6)), dict(x_scales=torch.ones(2, 4, device=DEV)),
+               dict(x_scales=s.view(2, 3, 1)), dict(x_scales=s, bias=torch.ones(41, device=DEV)),
+               dict(x_scales=s, bias=b.view(1, 40))):
+        with pytest.raises(dm.MoeError):
+            dm.linear_int8(q, w, **kw)
+    for pair in ((w[0], torch.ones(41, device=DEV)), (w[0], w[1].view(40, 1)), w[0], (w[0], None)):
+        with pytest.raises(dm.MoeError):
+            dm.linear_int8(x, pair)
+    with pytest.raises(dm.MoeError):
+        dm.linear_int8(x[0, 0, 0], w)
+    wide = quant_weight(bf(40, 128))
+    out = bf(6, 40)
+    ws = torch.empty(dm.moe_linear_int8_workspace_size(6, 40, 64), dtype=torch.uint8, device=DEV)
+    rows, (rq, rs) = x.view(6, 64), quant_weight(x.view(6, 64))
+    dm.moe_linear_int8_dynamic(rows, *w, b, out, ws)
+    assert torch.equal(out.view(2, 3, 40), want)
+    for c, sc in (wide, (w[0].view(20, 128), w[1]), (w[0].view(-1), w[1])):
+        with pytest.raises(dm.MoeError):
+            dm.moe_linear_int8_dynamic(rows, c, sc, b, out, ws)
+        with pytest.raises(dm.MoeError):
+            dm.moe_linear_int8(rq, rs, c, sc, b, out)
+    with pytest.raises(dm.MoeError):
+        dm.moe_linear_int8(q, s, *w, b, out)              # three dimensions
+    with pytest.raises(dm.MoeError):
+        dm.moe_linear_int8_dynamic(x, *w, b, out, ws)
