@@ -48,7 +48,7 @@ ENTRY_POINTS = (
     "moe_decode_fused_workspace_size", "moe_decode_fused",
     "moe_combine_bwd_weights", "moe_ffn_down_bwd_data_gather", "moe_ffn_down_bwd_weight_gather",
     "moe_few_tokens_workspace_size", "moe_few_tokens", "moe_few_tokens_int8",
-    "moe_linear_int8", "moe_linear_int8_workspace_size", "moe_linear_int8_dynamic",
+    "moe_linear_int8", "moe_linear_int8_kernel", "moe_linear_int8_workspace_size", "moe_linear_int8_dynamic",
 )
 
 
@@ -157,6 +157,7 @@ def lib() -> ctypes.CDLL:
         L.moe_few_tokens.argtypes = [S] + [P] * 7 + [I64] + [P] * 10 + [Z, P]
         L.moe_few_tokens_int8.argtypes = [S] + [P] * 6 + [I64] + [P] * 8 + [Z, P]
         L.moe_linear_int8.argtypes = [I64, I64, I64] + [P] * 7
+        L.moe_linear_int8_kernel.argtypes = [I64, I64, I64, ctypes.POINTER(ctypes.c_char_p)]
         L.moe_linear_int8_workspace_size.argtypes = [I64, I64, I64, ctypes.POINTER(Z)]
         L.moe_linear_int8_dynamic.argtypes = [I64, I64, I64] + [P] * 6 + [Z, P]
         for name in ENTRY_POINTS:
@@ -1580,6 +1581,13 @@ def moe_linear_int8(xq, xs, wq, ws, bias, out, stream=None):
     _launch(lib().moe_linear_int8, dev, stream, M, N, K, _at(xq, I8T, M * K, "xq", dev), _at(xs, F32, M, "xs", dev),
             _at(wq, I8T, N * K, "wq", dev), _at(ws, F32, N, "ws", dev), _at(bias, F32, N, "bias", dev),
             _at(out, BF16, M * N, "out", dev))
+
+
+def moe_linear_int8_kernel(M: int, N: int, K: int) -> str:
+    """The name of the kernel that a product of int8 codes of this size is launched on."""
+    name = ctypes.c_char_p()
+    _check(lib().moe_linear_int8_kernel(M, N, K, ctypes.byref(name)))
+    return name.value.decode()
 
 
 @functools.lru_cache(maxsize=256)

@@ -380,6 +380,14 @@ bool misaligned(const void* p, const void* q) {
   return (reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) % 16 != 0;
 }
 
+// A kernel for codes: its name, as a trace shows it, and its launch.
+struct LinKernel {
+  const char* name;
+  moe_status (*launch)(const LinArgs&, hipStream_t);
+};
+#define MOE_LIN_KERNEL(kind, ...) \
+  LinKernel { "k_linear_" #kind "<" #__VA_ARGS__ ">", launch_##kind<__VA_ARGS__> }
+
 // Up to 48 rows the row kernel, beyond the kernel with the least estimated time (us), from
 // what each cost on MI355X with cold weights: a call costs 3 to 3.5, each round of 256
 // workgroups its beginning and end and its part of the contraction, K / 128 steps of the
@@ -390,43 +398,45 @@ bool misaligned(const void* p, const void* q) {
 // (128 x 256), 99 on 256 x 256; 2000 x 4000 x 512 14.6 / 14 (128 x 256), 15.8 on 64 x 128, 18.8 on
 // 256 x 256; 4000 x 8000 x 4096 139 / 140 (256 x 256), 160 on 128 x 256; 4096 x 4096 x 7168
 // 114 / 114 (256 x 256), 132 on 128 x 256.
-moe_status linear_impl(const LinArgs& a, hipStream_t strm) {
+LinKernel linear_kernel(int64_t M, int64_t N, int64_t K) {
   // up to 16 rows: two column tiles for each wave, which halves the rows' share of the
   // loads, where that leaves half a CU's worth of workgroups (16 x 7168 x 7168 12.9
   // against 14.3 us; 1 x 2048 x 7168 8.9 against 6.5 us)
-  if (a.M <= 8 && a.N < 4096) return launch_rows<1, 1, 1, 2, 8>(a, strm);
-  if (a.M <= 8) return launch_rows<1, 2, 1, 2, 4>(a, strm);
-  if (a.M <= 16 && a.N < 4096) return launch_rows<1, 1, 2, 2, 8>(a, strm);
-  if (a.M <= 16) return launch_rows<1, 2, 2, 2, 4>(a, strm);
+  if (M <= 8 && N < 4096) return MOE_LIN_KERNEL(rows, 1, 1, 1, 2, 8);
+  if (M <= 8) return MOE_LIN_KERNEL(rows, 1, 2, 1, 2, 4);
+  if (M <= 16 && N < 4096) return MOE_LIN_KERNEL(rows, 1, 1, 2, 2, 8);
+  if (M <= 16) return MOE_LIN_KERNEL(rows, 1, 2, 2, 2, 4);
   // more rows: one column tile while those workgroups do not exceed the 256 CUs (20 x 2048
   // x 7168 6.8 against 7.8 us, 37 x 4096 x 4096 6.9 against 7.5; 32 x 7168 x 7168 19 against
   // 14), else two; row tiles as needed (37 x 7168 x 7168 on three 15.3, on four 16.4)
-  if (a.M <= 32 && a.N <= 4096) return launch_rows<2, 1, 2, 2, 8>(a, strm);
-  if (a.M <= 32) return launch_rows<2, 2, 2, 2, 4>(a, strm);
-  if (a.M <= 48 && a.N <= 4096) return launch_rows<3, 1, 2, 2, 8>(a, strm);
-  if (a.M <= 48) return launch_rows<3, 2, 2, 1, 8>(a, strm);
+  if (M <= 32 && N <= 4096) return MOE_LIN_KERNEL(rows, 2, 1, 2, 2, 8);
+  if (M <= 32) return MOE_LIN_KERNEL(rows, 2, 2, 2, 2, 4);
+  if (M <= 48 && N <= 4096) return MOE_LIN_KERNEL(rows, 3, 1, 2, 2, 8);
+  if (M <= 48) return MOE_LIN_KERNEL(rows, 3, 2, 2, 1, 8);
   auto up = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
   // (the same with rows past 64, if there are no more row tiles than column tiles: 56 x 2048
   // x 7168 9.3 against 10.9 us, 200 x 1024 x 7168 9.6 against 10.9; 2000 x 128 x 7168 19 against 13)
-  if (up(a.M, 64) * up(a.N, 16) <= 256 && up(a.M, 64) <= up(a.N, 16)) return launch_rows<4, 1, 2, 2, 8>(a, strm);
-  const double steps = up(a.K, 128);
-  auto rounds = [&](int bm, int bn) { return up((int64_t)(up(a.M, bm) * up(a.N, bn)), 256); };
-  const double t[6] = {3 + rounds(64, 32) * (2.2 + a.K / 980.0),         3 + rounds(64, 64) * (5 + a.K / 780.0),
+  if (up(M, 64) * up(N, 16) <= 256 && up(M, 64) <= up(N, 16)) return MOE_LIN_KERNEL(rows, 4, 1, 2, 2, 8);
+  const double steps = up(K, 128);
+  auto rounds = [&](int bm, int bn) { return up((int64_t)(up(M, bm) * up(N, bn)), 256); };
+  const double t[6] = {3 + rounds(64, 32) * (2.2 + K / 980.0),           3 + rounds(64, 64) * (5 + K / 780.0),
                        3.5 + rounds(64, 128) * (2.2 + 0.34 * steps),     3.5 + rounds(128, 128) * (4.5 + 0.6 * steps),
                        3.5 + rounds(128, 256) * (6.5 + steps),           3.5 + rounds(256, 256) * (12 + 1.75 * steps)};
   int best = 0;
   // (the row kernel's workgroups: ceil(M / 64) lie along the grid's second axis)
-  for (int i = a.M > 64 * 65535 ? 2 : 1; i < 6; ++i)
-    if (t[i] < t[best] || (best < 2 && a.M > 64 * 65535)) best = i;
+  for (int i = M > 64 * 65535 ? 2 : 1; i < 6; ++i)
+    if (t[i] < t[best] || (best < 2 && M > 64 * 65535)) best = i;
   switch (best) {
-    case 0: return launch_rows<4, 2, 2, 1, 8>(a, strm);
-    case 1: return launch_rows<4, 4, 2, 2, 4>(a, strm);
-    case 2: return launch_tiles<64, 128, 2, 4, 128, 3>(a, strm);
-    case 3: return launch_tiles<128, 128, 2, 4, 128, 4>(a, strm);
-    case 4: return launch_tiles<128, 256, 2, 4, 128, 3>(a, strm);
-    default: return launch_tiles<256, 256, 2, 4, 128, 2>(a, strm);
+    case 0: return MOE_LIN_KERNEL(rows, 4, 2, 2, 1, 8);
+    case 1: return MOE_LIN_KERNEL(rows, 4, 4, 2, 2, 4);
+    case 2: return MOE_LIN_KERNEL(tiles, 64, 128, 2, 4, 128, 3);
+    case 3: return MOE_LIN_KERNEL(tiles, 128, 128, 2, 4, 128, 4);
+    case 4: return MOE_LIN_KERNEL(tiles, 128, 256, 2, 4, 128, 3);
+    default: return MOE_LIN_KERNEL(tiles, 256, 256, 2, 4, 128, 2);
   }
 }
+
+moe_status linear_impl(const LinArgs& a, hipStream_t strm) { return linear_kernel(a.M, a.N, a.K).launch(a, strm); }
 
 }  // namespace
 }  // namespace moe
@@ -441,6 +451,14 @@ extern "C" moe_status moe_linear_int8(int64_t M, int64_t N, int64_t K, const int
   if (!xq || !xs || !wq || !ws || !out) return MOE_ERR_NULL_ARG;
   if (misaligned(xq, wq)) return MOE_ERR_BAD_SHAPE;
   return linear_impl({xq, xs, wq, ws, bias, static_cast<bf16_t*>(out), M, N, K}, as_stream(stream));
+}
+
+extern "C" moe_status moe_linear_int8_kernel(int64_t M, int64_t N, int64_t K, const char** name) {
+  const moe_status st = check_linear(M, N, K);
+  if (st != MOE_OK) return st;
+  if (!name) return MOE_ERR_NULL_ARG;
+  *name = M == 0 ? "" : linear_kernel(M, N, K).name;
+  return MOE_OK;
 }
 
 extern "C" moe_status moe_linear_int8_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {

@@ -834,6 +834,10 @@ moe_status moe_few_tokens_int8(const moe_shape* s, const void* x, const int32_t*
 moe_status moe_linear_int8(int64_t M, int64_t N, int64_t K, const int8_t* xq, const float* xs, const int8_t* wq,
                            const float* ws, const float* bias, void* out, void* stream);
 
+/* moe_linear_int8_kernel - the kernel that moe_linear_int8 launches for a product of
+ * this size, by the name that a trace shows (a static string, empty for M = 0). */
+moe_status moe_linear_int8_kernel(int64_t M, int64_t N, int64_t K, const char** name);
+
 /* moe_linear_int8_dynamic - moe_linear_int8 of bf16 rows x (M, K), quantised per
  * row by the rule of moe_few_tokens_int8.  workspace >= moe_linear_int8_workspace_size
  * bytes.  Calls that share one must not overlap in time.  One launch for M <= 2 and
