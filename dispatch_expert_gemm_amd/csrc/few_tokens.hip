@@ -23,7 +23,9 @@
 // H is split over its four waves, a short one is one wave's own.  down, T <= 16: a
 // workgroup per 16 or 32 columns of H that goes over all active experts, its eight waves
 // splitting the (expert, F) steps evenly, so a token's weighted sum stays inside one
-// workgroup: no third kernel, no atomics, the same order of additions in every call.
+// workgroup: no third kernel, no atomics, the same order of additions in every call (where
+// a wave's steps begin follows from the number of active experts, so the other tokens'
+// ids may change the order, their values do not).
 // Rows are packed per expert (the matrix cores take 16 at a time); each wave adds its
 // packed rows' weighted results to its own LDS copy of the output tile.  down, T > 16: a
 // workgroup per (active expert, columns of H), which reads each row of h less often, and
@@ -34,7 +36,8 @@
 // count, so the main loops have no barrier (stream_mfma.hpp).
 //
 // bf16: h leaves in fp32, and its three bf16 parts, every bit of it, multiply the same
-// weight registers.  int8: sums are exact integers.
+// weight registers.  int8: sums are exact integers,
+// those of k_few_down over a wave's part of F, and the parts join in fp32.
 //
 // Bound: HBM, the active experts' weights (reads reach 6.0 TB/s here).  Layers on
 // MI355X with cold weights: one token, 8 of 32 experts and a shared one, H = 7168,

@@ -764,8 +764,10 @@ moe_status moe_decode_fused(const moe_shape* s, const void* x, const int32_t* to
  * weights are given (shared_F > 0: (1, shared_F, H), (1, shared_F, H),
  * (1, H, shared_F)), or nothing; giving both is MOE_ERR_BAD_RANGE.
  * The weights and values of inactive slots are not used, whatever they hold.
- * Results do not depend on the other tokens' rows or on atomics: the same call
- * gives the same bits.
+ * The same call gives the same bits, and a token's bits do not depend on what the
+ * other tokens' rows and weights hold.  Which experts the other tokens go to and how
+ * many tokens there are decide where a sum over experts and F is cut into parts, and
+ * so the order in which fp32 sums join: they may change an output's last bit.
  */
 
 /* Bytes of device workspace of moe_few_tokens (int8 = 0) or moe_few_tokens_int8
@@ -798,7 +800,8 @@ moe_status moe_few_tokens(const moe_shape* s, const void* x, const int32_t* topk
 /* moe_few_tokens_int8 - int8 weights (w8a8, the int8 path's arithmetic without its
  * bf16 roundings): x_t times smooth_scales[e] (NULL: 1) is quantised per row, G and U
  * are exact integer sums times (row scale x channel scale), h in fp32 is quantised
- * per row, y likewise.  The shared expert takes x_t without smooth scales.
+ * per row, y is exact integer sums over parts of F (a wave's), each times (row scale x
+ * channel scale), joined in fp32.  The shared expert takes x_t without smooth scales.
  * Rows become codes clamp(rint(v * (127 * (1/amax))), -127, 127), every operation
  * rounded to fp32 (the factor at most the largest finite number), and a scale
  * amax/127 (all-zero row: codes 0, scale 1): the rule of moe_quant_rows_int8 with
