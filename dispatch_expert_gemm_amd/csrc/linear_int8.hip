@@ -367,7 +367,7 @@ moe_status launch_tiles(const LinArgs& a, hipStream_t strm) {
 
 moe_status check_linear(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N <= 0 || K <= 0 || K % 16 != 0) return MOE_ERR_BAD_SHAPE;
-  // |sum| <= 127 * 127 * K stays below 2^31
+  // |sum| <= 127 * 127 * K stays below 2^31 (128 * 128 * K up to K = 131056)
   if (K > 131072) return MOE_ERR_UNSUPPORTED;
   // An axis of a grid holds fewer than 2^32 threads: 512 for each 16 to 64 columns or, on
   // large outputs, each 256 x 256 tile (2^31 for 2^38 outputs, 512 GiB)

@@ -808,8 +808,10 @@ moe_status moe_few_tokens(const moe_shape* s, const void* x, const int32_t* topk
  * 127/amax formed from the reciprocal, as programs of tensor operations form it.  A
  * value on the border between two codes (exactly amax/2, say) may get the other one.
  * A row that holds an infinity or a NaN gives results that are not finite.
- * One or two tokens: two launches where a row of H <= 8192 and all rows of h (48 KiB)
- * fit a workgroup; else, and up to 16 tokens, four or five; above five.
+ * Launches: two for one or two tokens where a row of H <= 8192 and all rows of h (48
+ * KiB) fit a workgroup; else up to 16 tokens four (codes of x, gate/up, codes of h, down)
+ * or, for narrow layers, five (the weighted sums); above 16 tokens five (the first one
+ * sorts too).
  *  in   smooth_scales NULL or (E, H) fp32, on a 16-byte boundary
  *  in   w[3] gate, up, down; shared_w NULL or three weights
  *  other arguments as moe_few_tokens.  H a multiple of 16 (MOE_ERR_BAD_SHAPE); H, F
@@ -824,7 +826,8 @@ moe_status moe_few_tokens_int8(const moe_shape* s, const void* x, const int32_t*
 /* ------------------------------------------------------- int8 matrix product
  * The dense product of the int8 path (the projections around the layer):
  *   out[m, n] = bf16((sum over k of xq[m, k] * wq[n, k]) * (xs[m] * ws[n]) + bias[n])
- * with an exact integer sum, for any M >= 0 and N >= 1 and K a positive multiple
+ * with an exact integer sum and the rest in fp32, for codes from -127 to 127 (-128 too
+ * while 2^14 K < 2^31, K < 131072), any M >= 0 and N >= 1 and K a positive multiple
  * of 16 (MOE_ERR_BAD_SHAPE) up to 131072; M and N at most 2^24, M*N at most 2^38
  * (MOE_ERR_UNSUPPORTED).
  */

@@ -31,3 +31,17 @@ def test_sizes_that_are_refused():
     assert size(1 << 24, 1 << 14, 131072) == 0
     assert size(1 << 24, (1 << 14) + 1, 16) == -5
     assert size((1 << 14) + 1, 1 << 24, 16) == -5
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 20, 70])
+def test_codes_at_minus_128(M):
+    """Both operands, at the longest rows whose sums stay below 2^31."""
+    N, K = 19, 131056
+    xq = torch.full((M, K), -128, dtype=torch.int8, device=DEV)
+    wq = torch.full((N, K), -128, dtype=torch.int8, device=DEV)
+    wq[1::2] = 127
+    wq[4, ::3] = 126
+    xs, ws = torch.full((M,), 2.0 ** -12, device=DEV), torch.full((N,), 2.0 ** -9, device=DEV)
+    v, bound = linear64((xq, xs), (wq, ws))
+    check("-128", dm.linear_int8(xq, (wq, ws), x_scales=xs), v, bound)
