@@ -53,7 +53,7 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxTokens = 64, kMaxSlots = 1024, kMaxExperts = 1024;
+constexpr int kMaxTokens = 64, kMaxSlots = 1024;
 
 // Sizes of the work.  Up: gate/up, Down: down that sums over the experts, Y: down by
 // expert.  A wave's ring of LDS holds D steps of its operands; CT column tiles of a

@@ -197,7 +197,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (BM * BN <= 128 * 128 ? 2 : 1) * WM 
   constexpr int RPL = 1024 / BK, CPR = BK / 16;           // rows and chunks of one load
   constexpr int LA = BM / RPL / W, LB = BN / RPL / W;     // loads of a wave and step
   constexpr int kStage = (BM + BN) * BK;
-    extern __shared__ __attribute__((aligned(16))) char lds[];
+  static_assert(BK == 128, "the swizzle's rows");
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   int64_t m0, n0;
   tile_of(blockIdx.x, mt, nt, BM, BN, m0, n0);
@@ -210,7 +211,7 @@ __global__ __launch_bounds__(WM* WN* kWave, (BM * BN <= 128 * 128 ? 2 : 1) * WM 
     const bool isA = j < LA;
     const int r = ((isA ? wave * LA + j : wave * LB + j - LA)) * RPL + lane / CPR;
     const int64_t lim = (isA ? ml : nl) - 1;
-    kc[j] = 16 * swizzle<BK>(r, lane % CPR);
+    kc[j] = 16 * swizzle(r, lane % CPR);
     vo[j] = (uint32_t)(r < lim ? r : lim) * K + kc[j];
   }
   const int nk = (int)((a.K + BK - 1) / BK);
@@ -252,8 +253,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (BM * BN <= 128 * 128 ? 2 : 1) * WM 
   auto read = [&](auto B, const char* stage, int kk) {
     constexpr int b = decltype(B)::value;
     const int c = 2 * kk + lane / 32;
-    const char* as = stage + ar[0] * BK + 16 * swizzle<BK>(ar[0], c);  // the same for rows 32 apart
-    const char* bs = stage + BM * BK + br * BK + 16 * swizzle<BK>(br, c);
+    const char* as = stage + ar[0] * BK + 16 * swizzle(ar[0], c);  // the same for rows 32 apart
+    const char* bs = stage + BM * BK + br * BK + 16 * swizzle(br, c);
 #pragma unroll
     for (int i = 0; i < TI; ++i) fa[b][i] = *reinterpret_cast<const i32x4_t*>(as + 32 * i * BK);
 #pragma unroll

@@ -70,17 +70,14 @@ __device__ __forceinline__ void load_lds(const i32x4_t& r, const char* lds, uint
   asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" : : "v"(vo), "s"(r), "s"(so), "{m0}"(m0));
 }
 
-// Chunk position of chunk c (16 bytes) of row r in LDS rows of BK bytes: the 16 rows
+// Chunk position of chunk c (16 bytes) of row r in LDS rows of 128 bytes: the 16 rows
 // that one read phase takes lie in 16 different slots of a 256-byte window.
-template <int BK>
-__device__ __forceinline__ int swizzle(int r, int c) {
-  return BK == 128 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
-}
+__device__ __forceinline__ int swizzle(int r, int c) { return c ^ ((r >> 1) & 7); }
 
 // Lane l's row (of 16, its half j) and chunk byte in a row group's loads.
 __device__ __forceinline__ int stream_row(int j) { return 8 * j + (threadIdx.x % kWave) / 8; }
 __device__ __forceinline__ uint32_t stream_chunk(int j) {
-  return 16 * swizzle<128>(stream_row(j), threadIdx.x % 8);
+  return 16 * swizzle(stream_row(j), threadIdx.x % 8);
 }
 
 // Bytes of one ring slot; a wave's ring is D of them.  RT = 0: the weights alone.
@@ -193,10 +190,10 @@ __device__ __forceinline__ void stream_mfma(const i32x4_t (&w)[NW], const i32x4_
     if (d < n) issue(ring + d * kSlot<NW, RT, PX>, s0 + d);
   int at[2];  // this lane's fragments in a row group
 #pragma unroll
-  for (int kk = 0; kk < 2; ++kk) at[kk] = (lane % 16) * 128 + 16 * swizzle<128>(lane % 16, 4 * kk + lane / 16);
+  for (int kk = 0; kk < 2; ++kk) at[kk] = (lane % 16) * 128 + 16 * swizzle(lane % 16, 4 * kk + lane / 16);
   int atf[2];  // and in a plane's: eight fp32 values
 #pragma unroll
-  for (int h = 0; h < 2; ++h) atf[h] = (lane % 16) * 128 + 16 * swizzle<128>(lane % 16, 2 * (lane / 16) + h);
+  for (int h = 0; h < 2; ++h) atf[h] = (lane % 16) * 128 + 16 * swizzle(lane % 16, 2 * (lane / 16) + h);
   auto step = [&](char* slot, int i) {
     // the slot's loads have arrived: later ones may be outstanding
     if (i + D - 1 < n) __builtin_amdgcn_s_waitcnt(vm_wait(I * (D - 1)));
@@ -274,7 +271,7 @@ __device__ __forceinline__ void stream_held(const i32x4_t (&w)[NW], const char* 
   between();
   int at[2];
 #pragma unroll
-  for (int kk = 0; kk < 2; ++kk) at[kk] = (lane % 16) * 128 + 16 * swizzle<128>(lane % 16, 4 * kk + lane / 16);
+  for (int kk = 0; kk < 2; ++kk) at[kk] = (lane % 16) * 128 + 16 * swizzle(lane % 16, 4 * kk + lane / 16);
   auto step = [&](char* slot, int i) {
     if (i + D - 1 < n) __builtin_amdgcn_s_waitcnt(vm_wait(I * (D - 1)));
     else __builtin_amdgcn_s_waitcnt(vm_wait(0));
