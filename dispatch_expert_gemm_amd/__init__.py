@@ -1387,7 +1387,11 @@ def _launch(entry, dev, stream, *args):
 
 def _int8_pair(w):
     """(codes, scales) of an Int8Weights or of a (codes, scales) pair."""
-    return (w.codes, w.scales) if isinstance(w, Int8Weights) else w
+    if isinstance(w, Int8Weights):
+        w = (w.codes, w.scales)
+    if isinstance(w, (tuple, list)) and len(w) == 2 and isinstance(w[0], torch.Tensor) and isinstance(w[1], torch.Tensor):
+        return w
+    raise MoeError("int8 weights are an Int8Weights or a (codes, scales) pair")
 
 
 def moe_few_tokens_workspace_size(shape: MoeShape, shared_F: int = 0, int8: bool = False) -> int:
@@ -1424,8 +1428,7 @@ def _few_int8(shape, dev, ins, smooth_scales, w, shared_w, Fs, rest, ws_at, ws_b
 
     def three(ws, E, F):
         a = []
-        for v, n in zip(ws, (F, F, H)):
-            q, s = _int8_pair(v)
+        for (q, s), n in zip(ws, (F, F, H)):
             a += (_at(q, I8T, E * F * H, "int8 weight codes", dev), _at(s, F32, E * n, "int8 weight scales", dev))
         return (MoeInt8Weight * 3)((a[0], a[1]), (a[2], a[3]), (a[4], a[5]))
 
@@ -1457,7 +1460,9 @@ def moe_few_tokens_int8(shape, x, topk_idx, topk_weights, x_active_mask, smooth_
     dev = _device_of(x, "x")
     ins, rest = _few_common(shape, dev, x, topk_idx, topk_weights, x_active_mask, shared_expert_x, const_alpha_1,
                             const_alpha_2, const_v, out, err_flag)
-    Fs = 0 if shared_w is None else _int8_pair(shared_w[0])[0].shape[-2]
+    w = [_int8_pair(v) for v in w]
+    shared_w = None if shared_w is None else [_int8_pair(v) for v in shared_w]
+    Fs = 0 if shared_w is None else shared_w[0][0].shape[-2]
     _few_int8(shape, dev, ins, smooth_scales, w, shared_w, Fs, rest, *_bytes_at(workspace, dev), stream)
 
 
@@ -1469,25 +1474,25 @@ def _few_sizes(T, H, K, E, F, Z, C, Q, mask_ndim, Fs, int8):
 
 
 def _fits(ws, n, H):
-    f = ws[0].shape[-2] if ws[0].dim() > 1 else 0
-    if ws[0].shape != (n, f, H) or ws[1].shape != (n, f, H) or ws[2].shape != (n, H, f):
-        raise MoeError(f"weights {[tuple(w.shape) for w in ws]} do not fit {n} experts of {H} columns")
+    try:
+        g, u, d = ws[0].shape, ws[1].shape, ws[2].shape
+    except AttributeError:
+        raise MoeError("the weights are all tensors or all Int8Weights or (codes, scales) pairs") from None
+    f = g[1] if len(g) == 3 else 0
+    if g != (n, f, H) or u != g or d != (n, H, f):
+        raise MoeError(f"weights {[tuple(s) for s in (g, u, d)]} do not fit {n} experts of {H} columns")
     return f
 
 
-def _weight_kind(ws):
-    """Whether these weights are int8: all of them pairs, or all tensors."""
-    n = sum(isinstance(w, torch.Tensor) for w in ws)
-    if n == len(ws):
-        return False
-    if n or not all(_is_pair(w) for w in ws):
-        raise MoeError("the weights are all tensors or all Int8Weights or (codes, scales) pairs")
-    return True
-
-
-def _is_pair(w):
-    w = _int8_pair(w)
-    return isinstance(w, (tuple, list)) and len(w) == 2 and all(isinstance(t, torch.Tensor) for t in w)
+def _fits_int8(ws, n, H):
+    """_fits of int8 weights (n None: as many experts as the first has): (n, f, the pairs)."""
+    ws = [_int8_pair(w) for w in ws]
+    if n is None:
+        n = len(ws[0][0]) if ws[0][0].dim() else 0
+    f = _fits([q for q, _ in ws], n, H)
+    if ws[0][1].shape != (n, f) or ws[1][1].shape != (n, f) or ws[2][1].shape != (n, H):
+        raise MoeError(f"int8 weight scales {[tuple(s.shape) for _, s in ws]} of {n} experts of {f} and {H} rows")
+    return n, f, ws
 
 
 def _shared_weights(gate, up, down):
@@ -1519,37 +1524,37 @@ def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smo
                 shared_w_up=shared_w_up, shared_w_down=shared_w_down, const_alpha_1=const_alpha_1,
                 const_alpha_2=const_alpha_2, const_v=const_v, zero_expert_num=zero_expert_num,
                 copy_expert_num=copy_expert_num, const_expert_num=const_expert_num, err_flag=err_flag)
-    if x.dim() != 2 or topk_idx.dim() != 2:
-        raise MoeError(f"x {tuple(x.shape)} and topk_idx {tuple(topk_idx.shape)} must be matrices")
+    if x.dim() != 2:
+        raise MoeError(f"x must be a matrix, got {tuple(x.shape)}")
     T, H = x.shape
-    K = topk_idx.shape[-1]
-    if topk_idx.shape != (T, K) or topk_weights.shape != (T, K):
-        raise MoeError(f"topk_idx {tuple(topk_idx.shape)} and topk_weights {tuple(topk_weights.shape)} for {T} tokens")
+    slots = topk_idx.shape
+    if len(slots) != 2 or slots[0] != T or topk_weights.shape != slots:
+        raise MoeError(f"topk_idx {tuple(slots)} and topk_weights {tuple(topk_weights.shape)} for {T} tokens")
+    K = slots[1]
     if x_active_mask is not None and x_active_mask.shape not in ((T,), (T, K)):
         raise MoeError(f"x_active_mask must be of shape {(T,)} or {(T, K)}, got {tuple(x_active_mask.shape)}")
-    _shaped(shared_expert_x, (T, H), "shared_expert_x")
+    if shared_expert_x is not None:
+        _shaped(shared_expert_x, (T, H), "shared_expert_x")
     if const_expert_num > 0:
         _shaped(const_alpha_1, (const_expert_num, H), "const_alpha_1")
         _shaped(const_alpha_2, (const_expert_num, H), "const_alpha_2")
         _shaped(const_v, (const_expert_num, H), "const_v")
+    int8 = not isinstance(w_gate, torch.Tensor)
     w = (w_gate, w_up, w_down)
     shared_w = _shared_weights(shared_w_gate, shared_w_up, shared_w_down)
-    int8 = _weight_kind(w if shared_w is None else (*w, *shared_w))
+    Fs = 0
     if int8:
-        codes = [_int8_pair(v)[0] for v in w]
-        E = codes[0].shape[0]
-        F = _fits(codes, E, H)
-        Fs = 0 if shared_w is None else _fits([_int8_pair(v)[0] for v in shared_w], 1, H)
-        for v in w if shared_w is None else (*w, *shared_w):
-            q, s = _int8_pair(v)
-            _shaped(s, q.shape[:-1], "int8 weight scales")
+        E, F, w = _fits_int8(w, None, H)
+        if shared_w is not None:
+            _, Fs, shared_w = _fits_int8(shared_w, 1, H)
     else:
-        E = w_gate.shape[0]
+        E = len(w_gate) if w_gate.dim() else 0
         F = _fits(w, E, H)
         Fs = 0 if shared_w is None else _fits(shared_w, 1, H)
         if smooth_scales is not None:
             raise MoeError("smooth_scales go with int8 weights")
-    _shaped(smooth_scales, (E, H), "smooth_scales")
+    if smooth_scales is not None:
+        _shaped(smooth_scales, (E, H), "smooth_scales")
     shape, ws_bytes = _few_sizes(T, H, K, E, F, zero_expert_num, copy_expert_num, const_expert_num,
                                  0 if x_active_mask is None else x_active_mask.dim(), Fs, int8)
     out = torch.empty((T, H), dtype=BF16, device=x.device)
@@ -1569,9 +1574,10 @@ def moe_layer_few_tokens(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, smo
 
 def _multiplies(x, wq, dim=None):
     """(N, K) of weights wq (N, K) for rows x (..., K), of `dim` dimensions where it is given."""
-    if not isinstance(wq, torch.Tensor) or wq.dim() != 2 or x.shape[-1:] != wq.shape[1:] or dim not in (None, x.dim()):
-        raise MoeError(f"x {tuple(x.shape)} and weights {tuple(getattr(wq, 'shape', ()))} do not multiply")
-    return wq.shape
+    shape = getattr(wq, "shape", ())
+    if len(shape) != 2 or not x.dim() or x.size(-1) != shape[1] or (dim and x.dim() != dim):
+        raise MoeError(f"x {tuple(x.shape)} and weights {tuple(shape)} do not multiply")
+    return shape
 
 
 def moe_linear_int8(xq, xs, wq, ws, bias, out, stream=None):
@@ -1616,17 +1622,18 @@ def linear_int8(x, w, *, x_scales=None, bias=None, stream=None):
         _same_device(stream, dev)
         with torch.cuda.stream(stream):  # its output and workspace then belong to that stream
             return linear_int8(x, w, x_scales=x_scales, bias=bias)
-    if not _is_pair(w):
-        raise MoeError("the weights are an Int8Weights or a (codes, scales) pair")
     wq, ws = _int8_pair(w)
-    N, K = _multiplies(x, wq)
-    _shaped(ws, (N,), "the weights' scales")
-    _shaped(x_scales, x.shape[:-1], "x_scales")
-    _shaped(bias, (N,), "bias")
+    *lead, K = x.shape or (0,)
+    N = _multiplies(x, wq)[0]
+    if ws.dim() != 1 or ws.numel() != N:
+        _shaped(ws, (N,), "the weights' scales")
+    if bias is not None:
+        _shaped(bias, (N,), "bias")
     M = x.numel() // K if K else 0
-    out = torch.empty((*x.shape[:-1], N), dtype=BF16, device=x.device)
+    out = torch.empty((*lead, N), dtype=BF16, device=x.device)
     args = (_at(wq, I8T, N * K, "wq", dev), _at(ws, F32, N, "ws", dev), _at(bias, F32, N, "bias", dev), out.data_ptr())
     if x_scales is not None:
+        _shaped(x_scales, x.shape[:-1], "x_scales")
         _launch(lib().moe_linear_int8, dev, None, M, N, K, _at(x, I8T, M * K, "x", dev),
                 _at(x_scales, F32, M, "x_scales", dev), *args)
     else:
