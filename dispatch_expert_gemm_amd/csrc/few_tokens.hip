@@ -41,9 +41,10 @@
 //
 // Bound: HBM, the active experts' weights (reads reach 6.0 TB/s here).  Layers on
 // MI355X with cold weights: one token, 8 of 32 experts and a shared one, H = 7168,
-// F = 2048: 146 us, 5.4 TB/s (int8 84 us, 4.7); 13 tokens 440 to 470 us, 5.7 to 6.0 TB/s
-// (9 in int8 231 us, 5.5); 64 tokens on 8 experts of 14336 x 4096 515 us, 5.5 TB/s; 64 tokens
-// in int8 308 us, 4.7.  One token of 64 experts of 1536 x 480: 15.6 us, of which the bytes are 6.
+// F = 2048: 147 us, 5.4 TB/s (int8 85 us, 4.7); 13 tokens 461 us, 5.8 TB/s (9 in int8 224 us,
+// 5.6); 64 tokens on 8 experts of 14336 x 4096 498 us, 5.7 TB/s (each expert's rows 64
+// of them, top 8: 714 us); 64 tokens in int8 309 us, 4.7.  One token of 64 experts of 1536 x
+// 480: 16.6 us, of which the bytes are 6.
 #include <cmath>
 #include <initializer_list>
 
@@ -66,14 +67,16 @@ template <int RTM>
 constexpr int kUpRing = RTM == 1 ? 12288 : 16384;
 // 128-byte steps of H below which a wave has its columns to itself, and steps of F likewise
 // (Y).  Split at every length: 48 tokens on 64 experts of 1536 x 480 in int8 47 -> 64 us;
-// split at none: 64 tokens on 8 experts of 4096 x 14336 509 -> 564 us, one token 15 -> 18.
+// split at none: 64 tokens on 8 experts of 4096 x 14336 501 -> 562 us, one token 17 -> 19.
 constexpr int kUpOwn = 16, kYOwn = 40;
-// (8 KB: 16 tokens of 64 experts of 1536 x 512 in bf16 57.7 -> 69.9 us; 16 KB equal to 2%)
+// (8 KB: 2 tokens of 64 experts of 1536 x 512 in bf16 25.5 -> 27.0 us; 16 KB: 13 tokens of 32
+// experts of 7168 x 2048 458 -> 463 us, others equal)
 constexpr int kDownRing = 12288;
 // Y, by the waves KS that split the contraction: a long one wants few reads of h
-// (F = 14336 in bf16, 64 tokens: 180 us, with two column tiles 206 to 227), a short one
-// more workgroups on a CU, whose beginnings and ends overlap (64 experts of F = 480 in
-// int8: 13.4 us, with four column tiles 19)
+// (64 tokens of 8 experts of F = 14336 in bf16: the layer 505 us, with two column tiles 534;
+// with top 8 714 against 813), a short one more workgroups on a CU, whose beginnings and
+// ends overlap (48 tokens of 64 experts of F = 480 in int8: 47.4 us, with four column
+// tiles 53.8)
 template <int KS>
 constexpr int kYCT = KS == 1 ? 2 : 4;
 template <bool I8, int RTM, int KS>
@@ -814,10 +817,19 @@ bool few_held(const FewArgs& a, bool i8) {
 // Whether the down kernel sums over the experts itself: its H / 16 workgroups, each over
 // all active experts, against workgroups by expert and a launch for the sums.  A narrow
 // layer has too few of the former.  Both are estimated (us) for slots spread evenly over
-// the experts.  Itself / by expert, measured, the whole layer in bf16: 1 token of 64 experts
-// of 1536 x 480 15.2 / 20.2 us, 6 tokens 42.2 / 39.0, 16 tokens 59.9 / 52.5; 1 token of 38
-// experts of 672 x 3744 36.7 / 37.4, 6 tokens 129 / 70; 16 tokens of 16 experts of 3584 x 2048
-// 136.6 / 143.5.
+// the experts, with rates fitted to what they measure: itself, 38 bytes per ns of 16 columns
+// and 0.15 us for each expert's beginning; by expert, the longest workgroup or 5 TB/s in
+// all, and 5 us for the launch.  Itself / by expert, measured, the whole layer (us):
+//   64 experts of 1536 x 480, top 8   bf16  1 token 17.2 / 20.5, 4 39.6 / 36.2, 16 76.7 / 60.9
+//                                     int8  4 tokens 28.9 / 29.5, 6 38.6 / 36.0, 16 53.6 / 43.8
+//   38 of 672 x 3744, top 4           bf16  3 tokens 73 / 49.5, 6 118 / 66
+//                                     int8  3 tokens 47.0 / 45.3, 6 74.7 / 57.9
+//   3584 x 2048, 16 tokens of 16, top 8     bf16 139.9 / 142.6, int8 82.8 / 84.7
+//                8 tokens of 8, top 2       bf16 60.3 / 71.7, int8 44.2 / 45.7
+//   128 of 2048 x 768, top 8          bf16  16 tokens 168 / 148, 4 67.1 / 60.8
+//                                     int8  16 tokens 111 / 101, 4 49.9 / 46.7
+// The estimate takes the lesser but for the 4 tokens of 128 experts (10 and 7% more) and 4 int8
+// tokens of 64 (2%).
 bool few_joins(const FewArgs& a, bool i8) {
   if (a.T > 16) return false;
   if (a.H > 16 * 256 || few_held(a, i8)) return true;
@@ -910,8 +922,8 @@ bool launch_down_as(const FewArgs& a, hipStream_t strm) {
 }
 
 // 16 columns for a workgroup while those workgroups do not exceed the 256 CUs, else 32:
-// H = 1536 with 2 tokens 20.2 against 23.0 us for the layer, H = 4096 with 16 240 against 267;
-// H = 5120 with 4 tokens 134.9 against 128.2, H = 7168 equal (int8 4 us slower with 16).
+// H = 1536 with 2 tokens 26.5 against 30.1 us for the layer, H = 4096 with 16 158 against 174;
+// H = 5120 with 4 tokens 201 against 186, H = 7168 with 13 equal (int8 3 us slower with 16).
 // Sixteen or four waves: within 2% of eight, H = 1536 more than 10% slower.
 template <bool I8, bool HELD>
 bool launch_down(const FewArgs& a, hipStream_t strm) {

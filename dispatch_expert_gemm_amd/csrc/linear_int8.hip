@@ -8,15 +8,17 @@
 // memory into the matrix cores (stream_mfma.hpp); the int32 partial sums meet in
 // LDS, where their order does not matter.  k_linear_held: the same for one or two bf16
 // rows, quantised inside.  Bound: HBM, N * K bytes of weights, and for small ones the
-// launch: one row of 7168 x 7168 10.5 us (4.9 TB/s), 37 rows of 7168 x 2048 6.4 us.
+// launch: one row of 7168 x 7168 11.0 us (4.7 TB/s; 10.7 for a call among others, which
+// overlap), 37 rows of 7168 x 2048 6.6 us.
 //
-// k_linear_tiles: tiles of 64 x 128 to 256 x 256, both operands in LDS.  Bound: with 256
-// tiles or fewer the operands' way from L2 into LDS (512 x 4096 x 7168: 27.8 us, 1.08 POP/s,
-// 13 TB/s into the CUs); for large products power: 8192 x 14336 x 4096 takes 463 us, of
-// which 376 grow with K (2.55 POP/s there), the matrix cores busy 63% of the time at a clock
-// of 1.82 GHz.  Four waves of 128 x 128, with two thirds of the LDS reads and every load
-// and read between two products, keep them busy 75% of the loop, the clock falls to 1.63
-// GHz and the loop takes the same time; two workgroups of 128 x 256 on a CU 550 us.
+// k_linear_tiles: tiles of 64 x 128 to 256 x 256, both operands in LDS.  512 x 4096 x 7168
+// takes 26.1 us (1.15 POP/s), on 256 tiles: about 7 are a workgroup's beginning and end, and
+// the loop takes its operands at 72 bytes per ns and CU, where the row kernel reaches
+// about 95.  Bound, for large products: power.  8192 x 14336 x 4096 takes 463 us where the
+// clock stays at 1.93 GHz and up to 545 where it falls to 1.62; 382 of the 463 grow with K
+// (2.52 POP/s there).  The matrix cores are busy for 51% of its cycles, 70% of those that
+// grow with K.  On 128 x 256 tiles 530 us; four waves of 128 x 128, with two thirds of the LDS
+// reads, take the same time.
 #include <algorithm>
 #include <type_traits>
 
@@ -105,9 +107,9 @@ __global__ __launch_bounds__(W* kWave, 2) void k_linear_rows(LinArgs a) {
 }
 
 // The dynamic product of one or two rows in one launch: every workgroup quantises the
-// rows for itself, into LDS, behind its first weight loads.  1 x 7168 x 7168 12.9 us
-// against 16.5 with a launch for the codes, two rows 14.9 against 17.1; with four rows
-// the workgroups' work on the rows costs more than the launch (18.5 against 17.1).
+// rows for itself, into LDS, behind its first weight loads.  1 x 7168 x 7168 11.3 us
+// against 13.4 with a launch for the codes, two rows 12.5 against 13.9; with four rows
+// the workgroups' work on the rows costs more than the launch (15.4 against 14.2).
 constexpr int kHeldWaves = 8, kHeldPer = 2;
 template <int ROWS, int CT, int D>
 __global__ __launch_bounds__(kHeldWaves* kWave, 2) void k_linear_held(LinArgs a, const uint4* x) {
@@ -484,7 +486,7 @@ extern "C" moe_status moe_linear_int8_dynamic(int64_t M, int64_t N, int64_t K, c
   const LinArgs h = {nullptr, nullptr, wq, ws, bias, static_cast<bf16_t*>(out), M, N, K};
   if (M <= 2 && K <= kHeldPer * 8 * kHeldWaves * kWave) {
     if (M == 2) return launch_held<2, 1, 2>(h, x, as_stream(stream));
-    // wide: two column tiles, which halves the workgroups (14336 x 4096 14.6 against 16.3 us)
+    // wide: two column tiles, which halves the workgroups (14336 x 4096 11.8 against 14.0 us)
     return N < 8192 ? launch_held<1, 1, 3>(h, x, as_stream(stream)) : launch_held<1, 2, 2>(h, x, as_stream(stream));
   }
   int8_t* xq = static_cast<int8_t*>(workspace);
