@@ -393,8 +393,9 @@ struct LinKernel {
 
 // Up to 48 rows the row kernel, beyond the kernel with the least estimated time (us), from
 // what each cost on MI355X with cold weights: a call costs 3 to 3.5, each round of 256
-// workgroups its beginning and end and its part of the contraction, K / 128 steps of the
-// tiled kernels, (64 + 16 CT) K bytes of the row kernel at about 95 bytes per ns and CU.
+// workgroups (of 64 x 128 tiles too, two of which fit a CU: the fit is by rounds of 256)
+// its beginning and end and its part of the contraction, K / 128 steps of the tiled
+// kernels, (64 + 16 CT) K bytes of the row kernel at about 95 bytes per ns and CU.
 // Measured / estimated: 518 x 2000 x 160 6.2 / 6.4 (64 x 128), 10.2 / 10.1 by rows with CT 2,
 // 12.6 / 13.4 with CT 4; 256 x 4096 x 4096 14.1 / 13.2 (rows, CT 4), 16.0 / 16.6 on 64 x 128;
 // 512 x 4096 x 7168 25.5 / 24.7 (64 x 128), 56 on 128 x 256; 1024 x 7168 x 7168 66 / 66

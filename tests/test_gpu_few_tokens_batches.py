@@ -48,3 +48,25 @@ def test_other_tokens_values_do_not_change_a_token(T, H, F, int8):
         y, v = make(T, H, F, 6, 3, 120 + t, int8)[0] * 7, torch.rand(T, 3, device=DEV)
         y[t], v[t] = x[t], w[t]
         assert torch.equal(call(y, idx, v, ws, sw)[t], out[t])
+
+
+def test_most_rows_of_the_longest_h():
+    """1024 slots of F = 2^20 - 32 columns: a plane of h ends at offset 2^31.  All but eight columns
+    of each expert are 0, the last among the eight, and what is 0 adds nothing to a sum: the value
+    and its bound are those of a layer of 16 columns, the eight (each of them three additions, a
+    product's parts) and eight of the others."""
+    T, H, F, E, K = 64, 8, 2 ** 20 - 32, 17, 16
+    print(f"[few tokens] T={T} F={F}", flush=True)
+    x, idx, w, ws, _ = make(T, H, F, E, K, 130, False)
+    keep = torch.zeros(E, F, dtype=torch.bool, device=DEV)
+    for e in range(E):
+        keep[e, [0, 31 + e, 64 * e + 32, F // 2, F // 2 + 977 * e + 1, F - 65, F - 33, F - 1]] = True
+    ws[1].masked_fill_(~keep[:, :, None], 0)
+    ws[2].mul_(keep[:, None, :] * 1000)
+    small = []
+    for e in range(E):
+        c = torch.cat([keep[e].nonzero()[:, 0], torch.arange(2, 10, device=DEV)])
+        small.append((ws[0][e, c], ws[1][e, c], ws[2][e][:, c]))
+    v, bound, _ = layer64(x, idx, w, [torch.stack(t) for t in zip(*small)])
+    assert bound.mean() < 0.02 * v.abs().mean()
+    check("longest h", call(x, idx, w, ws, None), v, bound)
