@@ -49,6 +49,9 @@ ENTRY_POINTS = (
     "moe_combine_bwd_weights", "moe_ffn_down_bwd_data_gather", "moe_ffn_down_bwd_weight_gather",
     "moe_few_tokens_workspace_size", "moe_few_tokens", "moe_few_tokens_int8",
     "moe_linear_int8", "moe_linear_int8_kernel", "moe_linear_int8_workspace_size", "moe_linear_int8_dynamic",
+    "moe_balance_workspace_size", "moe_balance_fwd", "moe_balance_bwd",
+    "moe_swiglu_checkpoint_fwd", "moe_swiglu_checkpoint_bwd", "moe_swiglu_checkpoint_restore",
+    "moe_combine_checkpoint", "moe_combine_bwd_weights_checkpoint",
 )
 
 
@@ -160,6 +163,14 @@ def lib() -> ctypes.CDLL:
         L.moe_linear_int8_kernel.argtypes = [I64, I64, I64, ctypes.POINTER(ctypes.c_char_p)]
         L.moe_linear_int8_workspace_size.argtypes = [I64, I64, I64, ctypes.POINTER(Z)]
         L.moe_linear_int8_dynamic.argtypes = [I64, I64, I64] + [P] * 6 + [Z, P]
+        L.moe_balance_workspace_size.argtypes = [I64, I64, I64, ctypes.POINTER(Z)]
+        L.moe_balance_fwd.argtypes = [I64, I64, I32C, I64, I32C, I32C] + [P] * 9 + [Z, P]
+        L.moe_balance_bwd.argtypes = [I64, I64, I32C, I64, I32C, I32C] + [P] * 9
+        L.moe_swiglu_checkpoint_fwd.argtypes = [I64, I64] + [P] * 6
+        L.moe_swiglu_checkpoint_bwd.argtypes = [I64, I64] + [P] * 7
+        L.moe_swiglu_checkpoint_restore.argtypes = [I64, I64] + [P] * 6
+        L.moe_combine_checkpoint.argtypes = [S] + [P] * 15
+        L.moe_combine_bwd_weights_checkpoint.argtypes = [S] + [P] * 15
         for name in ENTRY_POINTS:
             if name != "moe_status_str":
                 getattr(L, name).restype = ctypes.c_int32
@@ -1642,6 +1653,238 @@ def linear_int8(x, w, *, x_scales=None, bias=None, stream=None):
         _launch(lib().moe_linear_int8_dynamic, dev, None, M, N, K, _at(x, BF16, M * K, "x", dev), *args,
                 workspace.data_ptr(), n)
     return out
+
+
+# ------------------------------------------------- balance loss, checkpoints in 8 bits
+
+DTYPE_CODE = {torch.bfloat16: 0, torch.float32: 1}  # MOE_DTYPE_*
+
+
+@functools.lru_cache(maxsize=256)
+def moe_balance_workspace_size(T: int, n_ids: int, num_seqs: int = 0) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_balance_workspace_size(T, n_ids, num_seqs, ctypes.byref(n)))
+    return n.value
+
+
+def _balance_sizes(logits, K, x_active_mask, seq_offsets):
+    """(T, n, K, num_seqs, mask_ndim, dtype) of a balance call, its tensors' shapes checked."""
+    if getattr(logits, "dim", lambda: 0)() != 2:
+        raise MoeError(f"logits must be a tensor of shape (T, n_ids), got {getattr(logits, 'shape', logits)}")
+    T, n = logits.shape
+    if logits.dtype not in DTYPE_CODE:
+        raise MoeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    ndim = 0
+    if x_active_mask is not None:
+        ndim = x_active_mask.dim()
+        _shaped(x_active_mask, (T, K) if ndim == 2 else (T,), "x_active_mask")
+    S = 0
+    if seq_offsets is not None:
+        S = seq_offsets.numel() - 1
+        if seq_offsets.dim() != 1 or S < 1:
+            raise MoeError(f"seq_offsets must hold the num_seqs + 1 ends of at least one sequence, got "
+                           f"{tuple(seq_offsets.shape)}")
+    return T, n, K, S, ndim, DTYPE_CODE[logits.dtype]
+
+
+def _u8(mask):
+    return mask.view(torch.uint8) if mask is not None and mask.dtype is torch.bool else mask
+
+
+def moe_balance_fwd(logits, topk_idx, x_active_mask, seq_offsets, loss, z_loss, counts, seq_tokens, workspace,
+                    stream=None):
+    """logits (T, n) fp32 or bf16, topk_idx (T, K) int32, x_active_mask (T,) or (T, K) or None, seq_offsets
+    (S + 1) int32 or None -> loss, z_loss (fp32, one element), counts (S or 1, n), seq_tokens (S or 1, + 1) int32."""
+    dev = _device_of(logits, "logits")
+    sizes = T, n, K, S, ndim, _ = _balance_sizes(logits, topk_idx.shape[-1], x_active_mask, seq_offsets)
+    _shaped(topk_idx, (T, K), "topk_idx")
+    rows = max(S, 1)
+    _launch(lib().moe_balance_fwd, dev, stream, *sizes, _at(logits, logits.dtype, T * n, "logits", dev),
+            _at(topk_idx, I32, T * K, "topk_idx", dev),
+            _at(_u8(x_active_mask), torch.uint8, T * (K if ndim == 2 else 1), "x_active_mask", dev),
+            _at(seq_offsets, I32, S + 1, "seq_offsets", dev), _at(loss, F32, 1, "loss", dev),
+            _at(z_loss, F32, 1, "z_loss", dev), _at(counts, I32, rows * n, "counts", dev),
+            _at(seq_tokens, I32, rows + 1, "seq_tokens", dev), *_bytes_at(workspace, dev))
+
+
+def moe_balance_bwd(logits, K, x_active_mask, seq_offsets, counts, seq_tokens, grad_loss, grad_z_loss, grad_logits,
+                    stream=None):
+    """Gradient of grad_loss * loss + grad_z_loss * z_loss (fp32 on the device, one element, or None) -> grad_logits."""
+    dev = _device_of(logits, "logits")
+    sizes = T, n, K, S, ndim, _ = _balance_sizes(logits, int(K), x_active_mask, seq_offsets)
+    rows = max(S, 1)
+    _launch(lib().moe_balance_bwd, dev, stream, *sizes, _at(logits, logits.dtype, T * n, "logits", dev),
+            _at(_u8(x_active_mask), torch.uint8, T * (K if ndim == 2 else 1), "x_active_mask", dev),
+            _at(seq_offsets, I32, S + 1, "seq_offsets", dev), _at(counts, I32, rows * n, "counts", dev),
+            _at(seq_tokens, I32, rows + 1, "seq_tokens", dev), _at(grad_loss, F32, 1, "grad_loss", dev),
+            _at(grad_z_loss, F32, 1, "grad_z_loss", dev), _at(grad_logits, logits.dtype, T * n, "grad_logits", dev))
+
+
+class _BalanceFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, topk_idx, x_active_mask, seq_offsets):
+        logits = logits.contiguous()
+        dev = logits.device
+        T, n, K, S, _, _ = _balance_sizes(logits, topk_idx.shape[-1], x_active_mask, seq_offsets)
+        loss, z_loss = torch.empty((), dtype=F32, device=dev), torch.empty((), dtype=F32, device=dev)
+        counts = torch.empty((S, n) if S else (n,), dtype=I32, device=dev)
+        seq_tokens = torch.empty(max(S, 1) + 1, dtype=I32, device=dev)
+        workspace = torch.empty(moe_balance_workspace_size(T, n, S), dtype=torch.uint8, device=dev)
+        moe_balance_fwd(logits, topk_idx, x_active_mask, seq_offsets, loss, z_loss, counts, seq_tokens, workspace)
+        ctx.save_for_backward(logits, x_active_mask, seq_offsets, counts, seq_tokens)
+        ctx.K = K
+        ctx.mark_non_differentiable(counts)
+        ctx.set_materialize_grads(False)
+        return loss, z_loss, counts
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_loss, g_z, _):
+        logits, mask, offsets, counts, seq_tokens = ctx.saved_tensors
+        if g_loss is None and g_z is None:
+            return None, None, None, None
+        grad = torch.empty_like(logits)
+        moe_balance_bwd(logits, ctx.K, mask, offsets, counts, seq_tokens, g_loss, g_z, grad)
+        return grad, None, None, None
+
+
+def balance_loss(logits, topk_idx, *, x_active_mask=None, seq_offsets=None):
+    """The router's balance loss, its z loss and the experts' counts: logits (T, n_ids) fp32 or bf16 and the
+    choices topk_idx (T, K) int32 (router's) -> (loss, z_loss, counts), the losses fp32 scalars, differentiable
+    in the logits (once), the counts int32 (n_ids,).
+
+    Over the active tokens (x_active_mask as moe_layer's, (T,) or (T, K)): loss = n_ids * sum_e f_e P_e with f_e the
+    share of the choices that go to e and P_e the mean of softmax(logits)_e, 1 for an even load; z_loss = mean of
+    logsumexp(logits)^2.  seq_offsets (num_seqs + 1) int32, ascending: the loss of each packed sequence by
+    itself, averaged over tokens, and counts (num_seqs, n_ids); tokens outside the sequences take no part."""
+    _device_of(logits, "logits")
+    if getattr(topk_idx, "dim", lambda: 0)() != 2:
+        raise MoeError(f"topk_idx must be a tensor of shape (T, K), got {getattr(topk_idx, 'shape', topk_idx)}")
+    return _BalanceFn.apply(logits, topk_idx, x_active_mask, seq_offsets)
+
+
+def checkpoint_buffers(rows, width, device, halves=1):
+    """Uninitialised (codes, scales) for `rows` rows of `width` values kept in 8 bits; halves=2: rows [G | U] of
+    two times `width`."""
+    codes = torch.empty((rows, halves * width), dtype=I8T, device=device)
+    return codes, torch.empty((rows, halves * (-(-width // 32))), dtype=BF16, device=device)
+
+
+def _gate_up_sizes(t, name):
+    if getattr(t, "dim", lambda: 0)() != 2 or t.shape[1] % 2 or not t.shape[1]:
+        raise MoeError(f"{name} must be a tensor of shape (R, 2F), got {getattr(t, 'shape', t)}")
+    return t.shape[0], t.shape[1] // 2
+
+
+def _kept_at(codes, scales, R, F, dev):
+    return _at(codes, I8T, R * 2 * F, "codes", dev), _at(scales, BF16, R * 2 * (-(-F // 32)), "scales", dev)
+
+
+def moe_swiglu_checkpoint_fwd(gate_up, h, codes, scales, nrows=None, stream=None):
+    """gate_up (R, 2F) bf16 -> h (R, F) bf16 or None, codes (R, 2F) int8, scales (R, 2 ceil(F / 32)) bf16."""
+    dev = _device_of(gate_up, "gate_up")
+    R, F = _gate_up_sizes(gate_up, "gate_up")
+    _launch(lib().moe_swiglu_checkpoint_fwd, dev, stream, R, F, _at(gate_up, BF16, R * 2 * F, "gate_up", dev),
+            _at(nrows, I32, 1, "nrows", dev), _at(h, BF16, R * F, "h", dev), *_kept_at(codes, scales, R, F, dev))
+
+
+def moe_swiglu_checkpoint_bwd(codes, scales, grad_h, grad_gate_up, h=None, nrows=None, stream=None):
+    """Kept [G | U] and grad_h (R, F) bf16 -> grad_gate_up (R, 2F) bf16, h (R, F) bf16 of the kept values or None."""
+    dev = _device_of(codes, "codes")
+    R, F = _gate_up_sizes(codes, "codes")
+    _launch(lib().moe_swiglu_checkpoint_bwd, dev, stream, R, F, *_kept_at(codes, scales, R, F, dev),
+            _at(nrows, I32, 1, "nrows", dev), _at(grad_h, BF16, R * F, "grad_h", dev),
+            _at(grad_gate_up, BF16, R * 2 * F, "grad_gate_up", dev), _at(h, BF16, R * F, "h", dev))
+
+
+def moe_swiglu_checkpoint_restore(codes, scales, gate_up, h=None, nrows=None, stream=None):
+    """Kept [G | U] -> gate_up (R, 2F) bf16, h (R, F) bf16 of the kept values or None."""
+    dev = _device_of(codes, "codes")
+    R, F = _gate_up_sizes(codes, "codes")
+    _launch(lib().moe_swiglu_checkpoint_restore, dev, stream, R, F, *_kept_at(codes, scales, R, F, dev),
+            _at(nrows, I32, 1, "nrows", dev), _at(gate_up, BF16, R * 2 * F, "gate_up", dev),
+            _at(h, BF16, R * F, "h", dev))
+
+
+class _SwigluCheckpointFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate_up):
+        gate_up = gate_up.contiguous()
+        R, F = _gate_up_sizes(gate_up, "gate_up")
+        h = torch.empty((R, F), dtype=BF16, device=gate_up.device)
+        codes, scales = checkpoint_buffers(R, F, gate_up.device, halves=2)
+        moe_swiglu_checkpoint_fwd(gate_up, h, codes, scales)
+        ctx.save_for_backward(codes, scales)
+        return h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_h):
+        codes, scales = ctx.saved_tensors
+        grad = torch.empty(codes.shape, dtype=BF16, device=codes.device)
+        moe_swiglu_checkpoint_bwd(codes, scales, grad_h.contiguous(), grad)
+        return grad
+
+
+def swiglu_checkpoint(gate_up):
+    """h = silu(G) * U of rows gate_up = [G | U] (..., 2F) bf16 -> (..., F) bf16, keeping gate_up in 8 bits
+    (1.0625 bytes a value) for the backward instead of in bf16: differentiable (once); the forward's h is that of
+    the bf16 values, the gradient that of the kept ones."""
+    _device_of(gate_up, "gate_up")
+    if gate_up.dtype is not BF16:
+        raise MoeError(f"gate_up must be {BF16}, got {gate_up.dtype}")
+    if not gate_up.dim() or gate_up.shape[-1] % 2 or not gate_up.shape[-1]:
+        raise MoeError(f"gate_up must be a tensor of shape (..., 2F), got {tuple(gate_up.shape)}")
+    h = _SwigluCheckpointFn.apply(gate_up if gate_up.dim() == 2 else gate_up.reshape(-1, gate_up.shape[-1]))
+    return h if gate_up.dim() == 2 else h.reshape(*gate_up.shape[:-1], -1)
+
+
+def _kept_rows_at(shape, codes, scales, dev):
+    n = shape.capacity
+    return (_at(codes, I8T, n * shape.H, "y_codes", dev),
+            _at(scales, BF16, n * (-(-shape.H // 32)), "y_scales", dev))
+
+
+def _combine_args(shape, topk_idx, topk_weights, assist_info_for_combine, ep_send_counts, x_active_mask, dev):
+    n = _shape_sizes(shape)
+    return (_at(topk_idx, I32, n["topk_idx"], "topk_idx", dev),
+            _at(topk_weights, F32, n["topk_weights"], "topk_weights", dev),
+            _at(assist_info_for_combine, I32, n["assist_info_for_combine"], "assist_info_for_combine", dev),
+            _at(ep_send_counts, I32, n["ep_send_counts"], "ep_send_counts", dev),
+            _at(_u8(x_active_mask), torch.uint8, n["x_active_mask"], "x_active_mask", dev))
+
+
+def _special_at(shape, ori_x, const_alpha_1, const_alpha_2, const_v, dev):
+    QH = shape.const_expert_num * shape.H
+    return (_at(ori_x, BF16, shape.T * shape.H, "ori_x", dev), _at(const_alpha_1, BF16, QH, "const_alpha_1", dev),
+            _at(const_alpha_2, BF16, QH, "const_alpha_2", dev), _at(const_v, BF16, QH, "const_v", dev))
+
+
+def moe_combine_checkpoint(shape, y, topk_idx, topk_weights, assist_info_for_combine, ep_send_counts, x_active_mask,
+                           shared_expert_x, ori_x, const_alpha_1, const_alpha_2, const_v, out, y_codes, y_scales,
+                           stream=None):
+    """moe_combine that keeps y's routed rows in 8 bits: y_codes (capacity, H) int8, y_scales (capacity,
+    ceil(H / 32)) bf16 (checkpoint_buffers)."""
+    dev = _device_of(y, "y")
+    _launch(lib().moe_combine_checkpoint, dev, stream, ctypes.byref(shape),
+            _at(y, BF16, shape.capacity * shape.H, "y", dev),
+            *_combine_args(shape, topk_idx, topk_weights, assist_info_for_combine, ep_send_counts, x_active_mask, dev),
+            _at(shared_expert_x, BF16, shape.T * shape.H, "shared_expert_x", dev),
+            *_special_at(shape, ori_x, const_alpha_1, const_alpha_2, const_v, dev),
+            _at(out, BF16, shape.T * shape.H, "out", dev), *_kept_rows_at(shape, y_codes, y_scales, dev))
+
+
+def moe_combine_bwd_weights_checkpoint(shape, grad_out, y_codes, y_scales, topk_idx, topk_weights,
+                                       assist_info_for_combine, ep_send_counts, x_active_mask, ori_x, const_alpha_1,
+                                       const_alpha_2, const_v, grad_topk_weights, row_weights=None, stream=None):
+    """moe_combine_bwd_weights on the kept rows of moe_combine_checkpoint."""
+    dev = _device_of(grad_out, "grad_out")
+    _launch(lib().moe_combine_bwd_weights_checkpoint, dev, stream, ctypes.byref(shape),
+            _at(grad_out, BF16, shape.T * shape.H, "grad_out", dev), *_kept_rows_at(shape, y_codes, y_scales, dev),
+            *_combine_args(shape, topk_idx, topk_weights, assist_info_for_combine, ep_send_counts, x_active_mask, dev),
+            *_special_at(shape, ori_x, const_alpha_1, const_alpha_2, const_v, dev),
+            _at(grad_topk_weights, F32, shape.T * shape.K, "grad_topk_weights", dev),
+            _at(row_weights, F32, shape.capacity, "row_weights", dev))
 
 
 def moe_layer(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, x_active_mask=None,

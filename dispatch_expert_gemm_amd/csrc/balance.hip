@@ -1,0 +1,627 @@
+// Balance loss and z loss of the router, per-expert counts, and their gradient to
+// the logits (formulas at moe_balance_fwd in moe.h).
+//
+// Forward: the tokens of a sequence are cut into items of C tokens; a workgroup
+// takes an item, reads each logit once, and leaves the item's column sums of
+// softmax(logits), its histogram of the choices (LDS integer atomics), its sum of
+// lse^2 and its number of active tokens in the workspace.  A second kernel sums
+// the items of every sequence 64 columns at a time in 64 bits, and the last of
+// its workgroups (a ticket that the first kernel clears) joins the sequences.
+// No floating-point atomics; every sum has a fixed order.
+//
+// A token is held by GW lanes with Q runs of four consecutive logits each, so a
+// wave holds 64/GW tokens and a row is read with 16-byte loads; sequence
+// s owns item slots from off[s]/C + s, a bound that the host knows without the
+// offsets: T/C + S slots.
+//
+// Backward: a workgroup takes a run of tokens, recomputes the softmax from the
+// logits (read once) and writes each gradient once; the counts of a token's
+// sequence stay in registers while the sequence stays the same.
+#include "common.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / kWave;
+constexpr int64_t kMaxIds = 4096, kMaxSeqs = 1 << 20;
+
+// Lane permutations within 16 lanes: xor 1, xor 2, then mirrors of 8 and of 16
+// lanes, which reach the other half once the halves hold one value each.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+template <int GW, typename Op>
+__device__ __forceinline__ float group_all(float v, Op op) {
+  if constexpr (GW >= 2) v = op(v, dpp<0xB1>(v));
+  if constexpr (GW >= 4) v = op(v, dpp<0x4E>(v));
+  if constexpr (GW >= 8) v = op(v, dpp<0x141>(v));
+  if constexpr (GW >= 16) v = op(v, dpp<0x140>(v));
+  if constexpr (GW >= 32) v = op(v, __shfl_xor(v, 16, kWave));
+  if constexpr (GW >= 64) v = op(v, __shfl_xor(v, 32, kWave));
+  return v;
+}
+template <int GW>
+__device__ __forceinline__ float group_max(float v) {
+  return group_all<GW>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int GW>
+__device__ __forceinline__ float group_sum(float v) {
+  return group_all<GW>(v, [](float a, float b) { return a + b; });
+}
+
+struct BalanceArgs {
+  const void* logits;
+  const int32_t* idx;
+  const uint8_t* mask;
+  const int32_t* off;  // S + 1, or NULL: one sequence of all tokens
+  int64_t T, slots;    // tokens; item slots
+  int n, K, S, mask_ndim, C;
+  // forward: per item
+  float* psum;     // slots x n
+  int32_t* hist;   // slots x n
+  float* zsum;     // slots
+  int32_t* ntok;   // slots
+  double* dots;    // S x column blocks
+  double* zseq;    // S
+  uint32_t* ticket;
+  float* loss;
+  float* z_loss;
+  int32_t* counts;      // S x n
+  int32_t* seq_tokens;  // S, then their sum
+  // backward
+  const float* g_loss;
+  const float* g_z;
+  void* grad;
+};
+
+// Offsets are data: clamped to [0, T], so whatever they hold stays in bounds.
+__device__ __forceinline__ int64_t off_at(const BalanceArgs& a, int s) {
+  if (!a.off) return s ? a.T : 0;
+  const int64_t o = a.off[s];
+  return o < 0 ? 0 : (o > a.T ? a.T : o);
+}
+
+// The largest s of [0, S) with key(s) <= x, or 0: 64 probes of the range at a time.
+template <typename Key>
+__device__ __forceinline__ int find_last(int S, int64_t x, Key key) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, len = S;
+  while (len > 1) {
+    const int step = (len + 63) >> 6;
+    const int s = lo + lane * step;
+    const uint64_t m = __ballot(lane * step < len && key(s) <= x);
+    const int last = m ? 63 - __clzll(m) : 0;
+    const int left = len - last * step;
+    lo += last * step;
+    len = left < step ? left : step;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float logit(float v) { return v != v ? -INFINITY : v; }
+
+// The four logits of row t from column c on (-inf past n or where NaN).
+template <typename In, bool VEC>
+__device__ __forceinline__ void load4(const BalanceArgs& a, int64_t t, int c, float* v) {
+  const In* p = static_cast<const In*>(a.logits) + t * a.n + c;
+  if constexpr (VEC) {  // n a multiple of 4, aligned rows
+    if (c < a.n) {
+      if constexpr (sizeof(In) == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(p);
+        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        v[0] = bf2f(u.x & 0xffffu); v[1] = bf2f(u.x >> 16);
+        v[2] = bf2f(u.y & 0xffffu); v[3] = bf2f(u.y >> 16);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = logit(v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = -INFINITY;
+      if (c + j < a.n) {
+        if constexpr (sizeof(In) == 4) v[j] = logit(p[j]);
+        else v[j] = logit(bf2f(reinterpret_cast<const bf16_t*>(p)[j]));
+      }
+    }
+  }
+}
+
+// exp(v - m) in place of the row's logits; m the row's largest, total the sum.  A
+// row that holds nothing above -inf gives zeros and total 0.
+template <int GW, int Q>
+__device__ __forceinline__ void row_exp(float (&v)[Q][4], float& m, float& total) {
+  m = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = fmaxf(m, v[q][j]);
+  m = group_max<GW>(m);
+  const bool some = m != -INFINITY;
+  float s = 0.f;
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[q][j] = some ? __expf(v[q][j] - m) : 0.f;
+      s += v[q][j];
+    }
+  total = group_sum<GW>(s);
+}
+
+// Whether token t counts (its lanes pass the same t), and with HIST its choices
+// into the histogram.
+template <int GW, bool HIST>
+__device__ __forceinline__ bool token_on(const BalanceArgs& a, int64_t t, bool in, int* hist) {
+  const int lane = threadIdx.x & 63, l = lane & (GW - 1);
+  if (!HIST && a.mask_ndim != 2) return in && (a.mask_ndim == 0 || a.mask[t]);
+  bool any = false;
+  if (in && (a.mask_ndim != 1 || a.mask[t]))
+    for (int k = l; k < a.K; k += GW) {
+      if (a.mask_ndim == 2 && !a.mask[t * a.K + k]) continue;
+      any = true;
+      if constexpr (HIST) {
+        const int32_t e = a.idx[t * a.K + k];
+        if ((uint32_t)e < (uint32_t)a.n) atomicAdd(&hist[e], 1);
+      }
+    }
+  const uint64_t b = __ballot(any);
+  if constexpr (GW == 64) return b != 0;
+  else return ((b >> (lane & ~(GW - 1))) & ((1ull << GW) - 1)) != 0;
+}
+
+template <typename In, bool VEC, int GW, int Q>
+__global__ __launch_bounds__(kThreads) void k_balance_items(BalanceArgs a) {
+  extern __shared__ float smem[];
+  float* row = smem;                               // n column sums
+  int* hist = reinterpret_cast<int*>(smem + a.n);  // n
+  __shared__ float zs[kWaves];
+  __shared__ int ns[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (GW - 1);
+  constexpr int G = kWave / GW;
+  const int64_t item = blockIdx.x;
+  if (item == 0 && tid == 0) *a.ticket = 0;
+  int s = 0;
+  if (a.off) s = find_last(a.S, item, [&](int i) { return off_at(a, i) / a.C + i; });
+  const int64_t lo = off_at(a, s), hi = off_at(a, s + 1);
+  const int64_t t0 = lo + (item - (lo / a.C + s)) * a.C;
+  const int64_t t1 = t0 + a.C < hi ? t0 + a.C : hi;
+  if (t0 < lo || t0 >= t1) return;  // a slot that no sequence fills: never read
+  for (int i = tid; i < a.n; i += kThreads) hist[i] = 0;
+  __syncthreads();
+  float p[Q][4];
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[q][j] = 0.f;
+  float z = 0.f;
+  int nt = 0;
+  for (int64_t b = t0 + wave * G; b < t1; b += kWaves * G) {
+    const int64_t t = b + lane / GW;
+    const bool in = t < t1;
+    float v[Q][4];
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (in) load4<In, VEC>(a, t, (q * GW + l) * 4, v[q]);
+      else v[q][0] = v[q][1] = v[q][2] = v[q][3] = -INFINITY;
+    const bool on = token_on<GW, true>(a, t, in, hist);
+    float m, total;
+    row_exp<GW, Q>(v, m, total);
+    const float inv = on && total != 0.f ? 1.0f / total : 0.f;
+    if (on) {  // (a token that is off adds nothing, not even a NaN)
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[q][j] += v[q][j] * inv;
+      const float lse = total != 0.f ? m + __logf(total) : 0.f;
+      z += lse * lse;
+      ++nt;
+    }
+  }
+  // the wave's tokens, then the workgroup's waves in order
+#pragma unroll
+  for (int o = GW; o < kWave; o <<= 1) {
+    z += __shfl_xor(z, o, kWave);
+    nt += __shfl_xor(nt, o, kWave);
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[q][j] += __shfl_xor(p[q][j], o, kWave);
+  }
+  if (lane == 0) {
+    zs[wave] = z;
+    ns[wave] = nt;
+  }
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (wave == w && lane < GW)
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = (q * GW + l) * 4 + j;
+          if (c < a.n) row[c] = w ? row[c] + p[q][j] : p[q][j];
+        }
+    __syncthreads();
+  }
+  for (int c = tid; c < a.n; c += kThreads) {
+    a.psum[item * a.n + c] = row[c];
+    a.hist[item * a.n + c] = hist[c];
+  }
+  if (tid == 0) {
+    float v = 0.f;
+    int k = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      v += zs[w];
+      k += ns[w];
+    }
+    a.zsum[item] = v;
+    a.ntok[item] = k;
+  }
+}
+
+__device__ __forceinline__ double block_sum(double v, double* red) {
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
+  __syncthreads();
+  if ((tid & 63) == 0) red[tid >> 6] = v;
+  __syncthreads();
+  double r = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) r += red[w];
+  return r;
+}
+
+// One workgroup for a sequence and 64 columns: four rows of threads share the
+// sequence's items.
+__global__ __launch_bounds__(kThreads) void k_balance_join(BalanceArgs a) {
+  __shared__ double dsum[kWaves][kWave];
+  __shared__ int csum[kWaves][kWave];
+  __shared__ double red[kWaves];
+  __shared__ bool last;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int blocks = (a.n + 63) / 64;
+  const int s = blockIdx.x / blocks, cb = blockIdx.x % blocks, c = cb * 64 + lane;
+  const int64_t lo = off_at(a, s), hi = off_at(a, s + 1);
+  const int64_t i0 = lo / a.C + s;
+  int64_t i1 = hi > lo ? i0 + (hi - lo + a.C - 1) / a.C : i0;
+  if (i1 > a.slots) i1 = a.slots;
+  double p = 0;
+  int k = 0;
+  if (c < a.n)
+#pragma unroll 4
+    for (int64_t i = i0 + wave; i < i1; i += kWaves) {
+      p += a.psum[i * a.n + c];
+      k += a.hist[i * a.n + c];
+    }
+  dsum[wave][lane] = p;
+  csum[wave][lane] = k;
+  double z = 0, nt = 0;
+  if (cb == 0)
+    for (int64_t i = i0 + tid; i < i1; i += kThreads) {
+      z += a.zsum[i];
+      nt += a.ntok[i];
+    }
+  __syncthreads();
+  double dot = 0;
+  if (wave == 0) {
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+      p += dsum[w][lane];
+      k += csum[w][lane];
+    }
+    if (c < a.n) a.counts[(int64_t)s * a.n + c] = k;
+    dot = p * k;
+  }
+  dot = block_sum(dot, red);
+  if (cb == 0) {
+    z = block_sum(z, red);
+    nt = block_sum(nt, red);
+  }
+  if (tid == 0) {
+    a.dots[blockIdx.x] = dot;
+    if (cb == 0) {
+      a.zseq[s] = z;
+      a.seq_tokens[s] = (int32_t)nt;
+    }
+    __threadfence();
+    last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double N = 0, loss = 0;
+  z = 0;
+  for (int i = tid; i < a.S; i += kThreads) {
+    const int m = a.seq_tokens[i];
+    double d = 0;
+    for (int b = 0; b < blocks; ++b) d += a.dots[(int64_t)i * blocks + b];
+    if (m > 0) loss += d / m;
+    N += m;
+    z += a.zseq[i];
+  }
+  N = block_sum(N, red);
+  loss = block_sum(loss, red);
+  z = block_sum(z, red);
+  if (tid == 0) {
+    a.seq_tokens[a.S] = (int32_t)N;
+    *a.loss = N > 0 ? (float)(loss * a.n / (a.K * N)) : 0.f;
+    *a.z_loss = N > 0 ? (float)(z / N) : 0.f;
+  }
+}
+
+template <typename In, bool VEC>
+__device__ __forceinline__ void store4(const BalanceArgs& a, int64_t t, int c, const float* v) {
+  In* p = static_cast<In*>(a.grad) + t * a.n + c;
+  if constexpr (VEC) {
+    if (c >= a.n) return;
+    if constexpr (sizeof(In) == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < a.n) {
+        if constexpr (sizeof(In) == 4) p[j] = v[j];
+        else reinterpret_cast<bf16_t*>(p)[j] = (bf16_t)f2bf(v[j]);
+      }
+  }
+}
+
+template <typename In, bool VEC, int GW, int Q>
+__global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (GW - 1);
+  constexpr int G = kWave / GW;
+  const int64_t t0 = (int64_t)blockIdx.x * a.C;
+  const int64_t t1 = t0 + a.C < a.T ? t0 + a.C : a.T;
+  const double N = a.seq_tokens[a.S];
+  const float gb = a.g_loss ? (float)(*a.g_loss * (double)a.n / (a.K * N)) : 0.f;
+  const float gz = a.g_z ? (float)(*a.g_z * 2.0 / N) : 0.f;
+  // the last sequence that begins at or before the run's first token
+  int s = a.off ? find_last(a.S, t0, [&](int i) { return off_at(a, i); }) : 0;
+  int64_t s0 = off_at(a, s), s1 = off_at(a, s + 1);
+  float f[Q][4], share = 0.f;
+  int held = -1;
+  for (int64_t b = t0 + wave * G; b < t1; b += kWaves * G) {
+    const int64_t t = b + lane / GW;
+    const bool in = t < t1;
+    float v[Q][4];
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (in) load4<In, VEC>(a, t, (q * GW + l) * 4, v[q]);
+      else v[q][0] = v[q][1] = v[q][2] = v[q][3] = -INFINITY;
+    while (t >= s1 && s + 1 < a.S) {
+      ++s;
+      s0 = off_at(a, s);
+      s1 = off_at(a, s + 1);
+    }
+    const bool inside = in && t >= s0 && t < s1;
+    const bool on = token_on<GW, false>(a, t, inside, nullptr);
+    if (on && held != s) {
+      held = s;
+      const int m = a.seq_tokens[s];
+      share = m > 0 ? gb / (float)m : 0.f;
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = (q * GW + l) * 4 + j;
+          f[q][j] = c < a.n ? (float)a.counts[(int64_t)s * a.n + c] : 0.f;
+        }
+    }
+    float m, total;
+    row_exp<GW, Q>(v, m, total);
+    const bool some = on && total != 0.f;
+    const float inv = some ? 1.0f / total : 0.f;
+    float d = 0.f;
+    if (some)
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[q][j] *= inv;
+          d += v[q][j] * f[q][j];
+        }
+    d = group_sum<GW>(d);
+    const float zt = some ? gz * (m + __logf(total)) : 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      float r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[j] = some ? v[q][j] * (share * (f[q][j] - d) + zt) : 0.f;
+      if (in) store4<In, VEC>(a, t, (q * GW + l) * 4, r);
+    }
+  }
+}
+
+// Tokens that a workgroup takes at a time: kWaves waves of 64/GW tokens.
+inline int group_lanes(int64_t n) { return n <= 16 ? 4 : (n <= 64 ? 16 : (n <= 128 ? 32 : 64)); }
+inline int step_tokens(int64_t n) { return kWaves * kWave / group_lanes(n); }
+
+// Tokens of an item: whole steps, about kItems items of a batch.
+constexpr int64_t kItems = 512;
+inline int64_t item_tokens(int64_t T, int64_t n) {
+  const int64_t step = step_tokens(n);
+  const int64_t per = (T + kItems - 1) / kItems;
+  return (per + step - 1) / step * step + (per == 0 ? step : 0);
+}
+
+struct Layout {
+  int64_t slots, psum, hist, zsum, ntok, dots, zseq, ticket, bytes;
+};
+Layout layout_of(int64_t T, int64_t n, int64_t S) {
+  Layout w;
+  w.slots = T / item_tokens(T, n) + S;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t p = at;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  w.psum = take(w.slots * n * 4);
+  w.hist = take(w.slots * n * 4);
+  w.zsum = take(w.slots * 4);
+  w.ntok = take(w.slots * 4);
+  w.dots = take(S * ((n + 63) / 64) * 8);
+  w.zseq = take(S * 8);
+  w.ticket = take(4);
+  w.bytes = at;
+  return w;
+}
+
+moe_status check_balance(int64_t T, int64_t n, int32_t K, int64_t S, int32_t mask_ndim, int32_t dtype) {
+  if (T < 0 || T > 0x7fffffff || n < 1 || n > kMaxIds || K < 1 || K > 16 || K > n) return MOE_ERR_BAD_SHAPE;
+  if (T * K > 0x7fffffff) return MOE_ERR_BAD_SHAPE;  // counts are int32
+  if (S < 0 || S > kMaxSeqs) return MOE_ERR_BAD_SHAPE;
+  if (mask_ndim < 0 || mask_ndim > 2) return MOE_ERR_BAD_RANGE;
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP32) return MOE_ERR_BAD_RANGE;
+  return MOE_OK;
+}
+
+// Calls f(In type tag, VEC, GW, Q) for n columns.
+template <typename In, bool VEC, typename Fn>
+void launch_gq(int64_t n, Fn f) {
+  if (n <= 16) f.template operator()<In, VEC, 4, 1>();
+  else if (n <= 64) f.template operator()<In, VEC, 16, 1>();
+  else if (n <= 128) f.template operator()<In, VEC, 32, 1>();
+  else if (n <= 256) f.template operator()<In, VEC, 64, 1>();
+  else if (n <= 512) f.template operator()<In, VEC, 64, 2>();
+  else if (n <= 1024) f.template operator()<In, VEC, 64, 4>();
+  else if (n <= 2048) f.template operator()<In, VEC, 64, 8>();
+  else f.template operator()<In, VEC, 64, 16>();
+}
+
+struct LaunchItems {
+  const BalanceArgs& a;
+  hipStream_t strm;
+  template <typename In, bool VEC, int GW, int Q>
+  void operator()() const {
+    hipLaunchKernelGGL((k_balance_items<In, VEC, GW, Q>), dim3((unsigned)a.slots), dim3(kThreads),
+                       2 * a.n * 4, strm, a);
+  }
+};
+struct LaunchBwd {
+  const BalanceArgs& a;
+  hipStream_t strm;
+  template <typename In, bool VEC, int GW, int Q>
+  void operator()() const {
+    hipLaunchKernelGGL((k_balance_bwd<In, VEC, GW, Q>), dim3((unsigned)((a.T + a.C - 1) / a.C)), dim3(kThreads), 0,
+                       strm, a);
+  }
+};
+
+template <typename Launch>
+void launch_any(const BalanceArgs& a, int32_t dtype, bool vec, const Launch& f) {
+  if (dtype == MOE_DTYPE_FP32) {
+    if (vec) launch_gq<float, true>(a.n, f);
+    else launch_gq<float, false>(a.n, f);
+  } else {
+    if (vec) launch_gq<bf16_t, true>(a.n, f);
+    else launch_gq<bf16_t, false>(a.n, f);
+  }
+}
+
+inline bool rows_aligned(const void* p, int64_t n, int32_t dtype) {
+  return n % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (dtype == MOE_DTYPE_FP32 ? 16 : 8) == 0;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_balance_workspace_size(int64_t T, int64_t n_ids, int64_t num_seqs, size_t* bytes) {
+  if (!bytes) return MOE_ERR_NULL_ARG;
+  const moe_status st = check_balance(T, n_ids, 1, num_seqs, 0, MOE_DTYPE_FP32);
+  if (st != MOE_OK) return st;
+  *bytes = (size_t)layout_of(T, n_ids, num_seqs ? num_seqs : 1).bytes;
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_balance_fwd(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs, int32_t mask_ndim,
+                                      int32_t dtype, const void* logits, const int32_t* topk_idx,
+                                      const uint8_t* x_active_mask, const int32_t* seq_offsets, float* loss,
+                                      float* z_loss, int32_t* counts, int32_t* seq_tokens, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+  const moe_status st = check_balance(T, n_ids, K, num_seqs, mask_ndim, dtype);
+  if (st != MOE_OK) return st;
+  MOE_NEED(logits, T);
+  MOE_NEED(topk_idx, T);
+  if (mask_ndim) MOE_NEED(x_active_mask, T);
+  if ((num_seqs && !seq_offsets) || !loss || !z_loss || !counts || !seq_tokens) return MOE_ERR_NULL_ARG;
+  const int64_t S = num_seqs ? num_seqs : 1;
+  const Layout w = layout_of(T, n_ids, S);
+  if (!workspace || ws_bytes < (size_t)w.bytes) return MOE_ERR_WORKSPACE;
+  const int64_t blocks = S * ((n_ids + 63) / 64);
+  if (w.slots > 0xffffff || blocks > 0xffffff) return MOE_ERR_BAD_SHAPE;  // 2^32 threads of a launch
+  char* ws = static_cast<char*>(workspace);
+  BalanceArgs a{};
+  a.logits = logits;
+  a.idx = topk_idx;
+  a.mask = x_active_mask;
+  a.off = num_seqs ? seq_offsets : nullptr;
+  a.T = T;
+  a.slots = w.slots;
+  a.n = (int)n_ids;
+  a.K = K;
+  a.S = (int)S;
+  a.mask_ndim = mask_ndim;
+  a.C = (int)item_tokens(T, n_ids);
+  a.psum = reinterpret_cast<float*>(ws + w.psum);
+  a.hist = reinterpret_cast<int32_t*>(ws + w.hist);
+  a.zsum = reinterpret_cast<float*>(ws + w.zsum);
+  a.ntok = reinterpret_cast<int32_t*>(ws + w.ntok);
+  a.dots = reinterpret_cast<double*>(ws + w.dots);
+  a.zseq = reinterpret_cast<double*>(ws + w.zseq);
+  a.ticket = reinterpret_cast<uint32_t*>(ws + w.ticket);
+  a.loss = loss;
+  a.z_loss = z_loss;
+  a.counts = counts;
+  a.seq_tokens = seq_tokens;
+  launch_any(a, dtype, rows_aligned(logits, n_ids, dtype), LaunchItems{a, as_stream(stream)});
+  const moe_status first = launch_status();
+  if (first != MOE_OK) return first;
+  hipLaunchKernelGGL(k_balance_join, dim3((unsigned)blocks), dim3(kThreads), 0, as_stream(stream), a);
+  return launch_status();
+}
+
+extern "C" moe_status moe_balance_bwd(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs, int32_t mask_ndim,
+                                      int32_t dtype, const void* logits, const uint8_t* x_active_mask,
+                                      const int32_t* seq_offsets, const int32_t* counts, const int32_t* seq_tokens,
+                                      const float* grad_loss, const float* grad_z_loss, void* grad_logits,
+                                      void* stream) {
+  const moe_status st = check_balance(T, n_ids, K, num_seqs, mask_ndim, dtype);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!logits || !counts || !seq_tokens || !grad_logits || (num_seqs && !seq_offsets) ||
+      (mask_ndim && !x_active_mask))
+    return MOE_ERR_NULL_ARG;
+  BalanceArgs a{};
+  a.logits = logits;
+  a.mask = x_active_mask;
+  a.off = num_seqs ? seq_offsets : nullptr;
+  a.T = T;
+  a.n = (int)n_ids;
+  a.K = K;
+  a.S = num_seqs ? (int)num_seqs : 1;
+  a.mask_ndim = mask_ndim;
+  // runs of tokens: enough workgroups for every CU, whole steps each
+  const int64_t step = step_tokens(n_ids), per = (T + 2047) / 2048;
+  a.C = (int)((per + step - 1) / step * step);
+  a.counts = const_cast<int32_t*>(counts);
+  a.seq_tokens = const_cast<int32_t*>(seq_tokens);
+  a.g_loss = grad_loss;
+  a.g_z = grad_z_loss;
+  a.grad = grad_logits;
+  launch_any(a, dtype, rows_aligned(logits, n_ids, dtype) && rows_aligned(grad_logits, n_ids, dtype),
+             LaunchBwd{a, as_stream(stream)});
+  return launch_status();
+}

@@ -1,0 +1,606 @@
+// Activation checkpoints in 8 bits: SwiGLU whose [G | U] input is kept as int8
+// codes for the backward, and the combine whose expert rows are.
+//
+// Kept rows: blocks of 32 consecutive columns (a row's last block may be shorter),
+// one bf16 scale each, s = bf16(amax / 127), code = rint(v * fp32(1 / s)); a kept
+// value is code * s, at most half a step from v.  A block whose scale would be
+// below 2^-126 keeps zeros (scale 0); one that holds an infinity or a NaN keeps
+// NaN (scale NaN, codes 0).  G and U are cut into blocks apart.
+//
+// All of it is bound by memory: each input is read once with 16-byte loads and
+// each output written once; the four lanes that hold a block's 32 columns find its
+// amax with two lane permutations on the values' bits, where an infinity and a NaN
+// order above every number.
+#include <type_traits>
+
+#include "combine_token.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kCols = 32;  // columns of a block
+constexpr int kThreads = 256;
+
+// Scale bits and the multiplier of a block from the largest bf16 magnitude's bits.
+// The product with fp32(1/127) rounds to the same bf16 as amax / 127: that quotient
+// of an 8-bit mantissa by 127 is over 2^-17 of its value away from any midpoint of
+// two bf16 numbers.  One Newton step makes v_rcp_f32's result the rounded
+// reciprocal (tested for every scale).
+__device__ __forceinline__ uint32_t kept_scale(uint32_t amax16, float& inv) {
+  inv = 0.f;
+  if (amax16 >= 0x7f80u) return 0x7fc0u;
+  const uint32_t s = f2bf(__fmul_rn(bf2f(amax16), 1.0f / 127.0f));
+  if (s < 0x0080u) return 0u;
+  const float sf = bf2f(s), r = __builtin_amdgcn_rcpf(sf);
+  inv = __fmaf_rn(__fmaf_rn(-sf, r, 1.0f), r, r);
+  return s;
+}
+
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                __builtin_bit_cast(u16x2, b)));
+}
+
+// Largest magnitude (bf16 bits) of the 32 values that four neighbouring lanes hold.
+__device__ __forceinline__ uint32_t block_amax(const uint4& v) {
+  constexpr uint32_t k = 0x7fff7fffu;
+  uint32_t m = max16x2(max16x2(v.x & k, v.y & k), max16x2(v.z & k, v.w & k));
+  m = max16x2(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, true));
+  m = max16x2(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, true));
+  const uint32_t hi = m >> 16, lo = m & 0xffffu;
+  return hi > lo ? hi : lo;
+}
+
+// The code of v in the low byte.  |v * inv| <= 127 (1 + 2^-8), so adding 1.5 * 2^23 to
+// the rounded product (no contraction: the rule rounds it to fp32 first) leaves rint
+// of it, ties to even, in the sum's low bits.
+__device__ __forceinline__ uint32_t code(float v, float inv) {
+#pragma clang fp contract(off)
+  const float p = v * inv;
+  return __float_as_uint(p + 12582912.0f);
+}
+
+// Four codes in a word.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
+  const uint32_t lo = __builtin_amdgcn_perm(code(b, inv), code(a, inv), 0x0c0c0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(code(d, inv), code(c, inv), 0x04000c0cu);
+  return lo | hi;
+}
+
+__device__ __forceinline__ uint2 codes8(const uint4& v, float inv) {
+  float f[8];
+  unpack8(v, f);
+  if (inv == 0.f) return make_uint2(0u, 0u);  // zeros, or an infinity or a NaN among them
+  return make_uint2(codes4(f[0], f[1], f[2], f[3], inv), codes4(f[4], f[5], f[6], f[7], inv));
+}
+
+// Eight kept values: code * s, exact in fp32.
+__device__ __forceinline__ void kept8(const uint2& q, float s, float* f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __fmul_rn((float)(int8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3))), s);
+}
+
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+enum Pass : int { KEEP, GRAD, RESTORE };
+
+struct SwigluArgs {
+  const void* gate_up;   // KEEP: R x 2F
+  const void* grad_h;    // GRAD: R x F
+  const int32_t* nrows;  // rows in use, or NULL
+  int8_t* codes;         // R x 2F
+  uint16_t* scales;      // R x 2 x nb
+  void* out;             // GRAD: dG|dU, RESTORE: G|U (R x 2F)
+  void* h;               // R x F, or NULL
+  int64_t R, F, nb;
+  // vector passes: units of eight columns, `cols` = F / 8 units a row
+  uint32_t cols, step_rows, step_cols;  // kThreads units on: rows and columns
+};
+
+__device__ __forceinline__ int64_t rows_of(const SwigluArgs& a) {
+  int64_t rows = a.R;
+  if (a.nrows) {
+    const int64_t n = *a.nrows;
+    rows = n < 0 ? 0 : (n < rows ? n : rows);
+  }
+  return rows;
+}
+
+__device__ __forceinline__ uint4 pack8h(const float* f) {
+  return make_uint4(pk_bf16(f[0], f[1]), pk_bf16(f[2], f[3]), pk_bf16(f[4], f[5]), pk_bf16(f[6], f[7]));
+}
+
+__device__ __forceinline__ void swiglu_grad(float g, float u, float d, float& dg, float& du, float& h) {
+  const float sg = sigmoid(g), si = g * sg;
+  dg = d * u * __fmaf_rn(si, 1.0f - sg, sg);
+  du = d * si;
+  h = si * u;
+}
+
+// F a multiple of 32 and 16-byte aligned rows: a lane takes eight columns of G and
+// the same eight of U.  kUnits units a thread, kThreads apart, loads first.
+template <int PASS, bool H>
+__global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
+  constexpr int kUnits = 2;
+  const int64_t rows = rows_of(a);
+  const int64_t u0 = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+  int64_t row[kUnits];
+  uint32_t col[kUnits];
+  row[0] = u0 / a.cols;
+  col[0] = (uint32_t)(u0 - row[0] * a.cols);
+#pragma unroll
+  for (int i = 1; i < kUnits; ++i) {
+    row[i] = row[i - 1] + a.step_rows;
+    col[i] = col[i - 1] + a.step_cols;
+    if (col[i] >= a.cols) {
+      col[i] -= a.cols;
+      ++row[i];
+    }
+  }
+  const uint32_t cols = a.cols;
+  if constexpr (PASS == KEEP) {
+    const uint4* gu = static_cast<const uint4*>(a.gate_up);
+    uint4 g[kUnits], u[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+      if (row[i] < rows) {
+        g[i] = gu[row[i] * 2 * cols + col[i]];
+        u[i] = gu[row[i] * 2 * cols + cols + col[i]];
+      }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      if (row[i] >= rows) continue;  // the four lanes of a block leave together
+      float ig, iu;
+      const uint32_t sg = kept_scale(block_amax(g[i]), ig), su = kept_scale(block_amax(u[i]), iu);
+      uint2* codes = reinterpret_cast<uint2*>(a.codes) + row[i] * 2 * cols + col[i];
+      codes[0] = codes8(g[i], ig);
+      codes[cols] = codes8(u[i], iu);
+      if ((col[i] & 3) == 0) {
+        uint16_t* sc = a.scales + row[i] * 2 * a.nb + col[i] / 4;
+        sc[0] = (uint16_t)sg;
+        sc[a.nb] = (uint16_t)su;
+      }
+      if constexpr (H) {
+        float gf[8], uf[8];
+        unpack8(g[i], gf);
+        unpack8(u[i], uf);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gf[j] = gf[j] * sigmoid(gf[j]) * uf[j];
+        static_cast<uint4*>(a.h)[row[i] * cols + col[i]] = pack8h(gf);
+      }
+    }
+  } else {
+    uint2 qg[kUnits], qu[kUnits];
+    uint32_t sg[kUnits], su[kUnits];
+    uint4 dh[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+      if (row[i] < rows) {
+        const uint2* codes = reinterpret_cast<const uint2*>(a.codes) + row[i] * 2 * cols + col[i];
+        const uint16_t* sc = a.scales + row[i] * 2 * a.nb + col[i] / 4;
+        qg[i] = codes[0];
+        qu[i] = codes[cols];
+        sg[i] = sc[0];
+        su[i] = sc[a.nb];
+        if constexpr (PASS == GRAD) dh[i] = static_cast<const uint4*>(a.grad_h)[row[i] * cols + col[i]];
+      }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      if (row[i] >= rows) continue;
+      float g[8], u[8], h[8];
+      kept8(qg[i], bf2f(sg[i]), g);
+      kept8(qu[i], bf2f(su[i]), u);
+      uint4* out = static_cast<uint4*>(a.out) + row[i] * 2 * cols + col[i];
+      if constexpr (PASS == GRAD) {
+        float d[8];
+        unpack8(dh[i], d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) swiglu_grad(g[j], u[j], d[j], g[j], u[j], h[j]);
+      } else if constexpr (H) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = g[j] * sigmoid(g[j]) * u[j];
+      }
+      out[0] = pack8h(g);
+      out[cols] = pack8h(u);
+      if constexpr (H) static_cast<uint4*>(a.h)[row[i] * cols + col[i]] = pack8h(h);
+    }
+  }
+}
+
+// Any F and any alignment: 32 lanes take a block of G and the same block of U, a
+// column each.
+template <int PASS>
+__global__ __launch_bounds__(kThreads) void k_swiglu_any(SwigluArgs a) {
+  const int64_t rows = rows_of(a);
+  const int64_t b = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kCols;
+  const int64_t row = b / a.nb, blk = b - row * a.nb;
+  if (row >= rows) return;  // 32 lanes leave together
+  const int64_t c = blk * kCols + (threadIdx.x & (kCols - 1));
+  const bool in = c < a.F;
+  const int64_t at = row * 2 * a.F + c, ah = row * a.F + c;
+  uint16_t* sc = a.scales + row * 2 * a.nb + blk;
+  uint16_t* h = static_cast<uint16_t*>(a.h);
+  if constexpr (PASS == KEEP) {
+    const uint16_t* gu = static_cast<const uint16_t*>(a.gate_up);
+    const uint32_t g = in ? gu[at] : 0u, u = in ? gu[at + a.F] : 0u;
+    uint32_t m = (g & 0x7fffu) | (u & 0x7fffu) << 16;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = max16x2(m, (uint32_t)__shfl_xor((int)m, o, kCols));
+    float ig, iu;
+    const uint32_t sg = kept_scale(m & 0xffffu, ig), su = kept_scale(m >> 16, iu);
+    if (c == blk * kCols) {
+      sc[0] = (uint16_t)sg;
+      sc[a.nb] = (uint16_t)su;
+    }
+    if (!in) return;
+    const float gf = bf2f(g), uf = bf2f(u);
+    a.codes[at] = ig == 0.f ? (int8_t)0 : (int8_t)code(gf, ig);
+    a.codes[at + a.F] = iu == 0.f ? (int8_t)0 : (int8_t)code(uf, iu);
+    if (h) h[ah] = (uint16_t)f2bf(gf * sigmoid(gf) * uf);
+  } else {
+    if (!in) return;
+    const float g = __fmul_rn((float)a.codes[at], bf2f(sc[0]));
+    const float u = __fmul_rn((float)a.codes[at + a.F], bf2f(sc[a.nb]));
+    uint16_t* out = static_cast<uint16_t*>(a.out);
+    float dg = g, du = u, hv;
+    if constexpr (PASS == GRAD) swiglu_grad(g, u, bf2f(static_cast<const uint16_t*>(a.grad_h)[ah]), dg, du, hv);
+    else hv = g * sigmoid(g) * u;
+    out[at] = (uint16_t)f2bf(dg);
+    out[at + a.F] = (uint16_t)f2bf(du);
+    if (h) h[ah] = (uint16_t)f2bf(hv);
+  }
+}
+
+// ----------------------------------------------------------------------------- combine
+
+struct KeptArgs {
+  uint2* codes;      // capacity x Hv, eight columns each
+  uint16_t* scales;  // capacity x nb
+  int64_t nb;
+};
+
+// Combine that keeps its rows: one wave per token and column part, as k_combine;
+// out is bit for bit k_combine's.
+template <int KMAX>
+__global__ __launch_bounds__(kThreads) void k_combine_keep(CombineArgs a, KeptArgs q) {
+#pragma clang fp contract(off)
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int64_t gw = (int64_t)blockIdx.x * (kThreads / kWave) + wave;
+  const int64_t t = gw / a.split;
+  const int part = (int)(gw - t * a.split);
+  if (t >= a.T) return;
+  SlotInfo<KMAX> si;
+  load_slots(a.slot2row, a.w, t, a.K, lane, si);
+  const int64_t Hv = a.Hv;
+  constexpr int U = kChunk<KMAX>;
+  const int64_t vs = (int64_t)a.split * kWave;
+  for (int64_t b0 = part * kWave; b0 < Hv; b0 += U * vs) {  // (the whole wave: blocks span lanes)
+    uint4 raw[U][KMAX], sh[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t v = b0 + u * vs + lane;
+#pragma unroll
+      for (int k = 0; k < KMAX; ++k)
+        if (si.code[k] >= 0) {
+          raw[u][k] = make_uint4(0u, 0u, 0u, 0u);
+          if (v < Hv) raw[u][k] = ld_row(&a.y[(int64_t)si.code[k] * Hv + v]);
+        }
+      if (a.shared && v < Hv) sh[u] = a.shared[t * Hv + v];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t v = b0 + u * vs + lane;
+      float ox[8], acc[8];
+      if (si.any_ori && v < Hv) unpack8(a.ori[t * Hv + v], ox);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KMAX; ++k) {
+        const int c = si.code[k];
+        if (c == MOE_SLOT_NONE) continue;
+        float f[8];
+        if (c >= 0) {
+          float inv;
+          const uint32_t s = kept_scale(block_amax(raw[u][k]), inv);
+          if (v < Hv) {
+            q.codes[(int64_t)c * Hv + v] = codes8(raw[u][k], inv);
+            if ((lane & 3) == 0) q.scales[(int64_t)c * q.nb + v / 4] = (uint16_t)s;
+          }
+          unpack8(raw[u][k], f);
+        } else if (v < Hv) {
+          special_value(c, ox, a.a1, a.a2, a.cv, Hv, v, f);
+        }
+        const float wk = si.w[k];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = acc[i] + wk * f[i];
+      }
+      if (v < Hv) {
+        if (a.shared) {
+          float sv[8];
+          unpack8(sh[u], sv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = acc[i] + sv[i];
+        }
+        a.out[t * Hv + v] = pack8(acc);
+      }
+    }
+  }
+}
+
+struct KeptBwdArgs {
+  const uint4* dout;
+  const uint2* codes;
+  const uint16_t* scales;
+  const float* w;
+  const int32_t* slot2row;
+  const uint4* ori;
+  const uint4* a1;
+  const uint4* a2;
+  const uint4* cv;
+  float* dw;
+  float* roww;
+  int64_t T, Hv, nb;
+  int K;
+};
+
+// The routing weights' gradient from kept rows: one wave per token.
+template <int KMAX>
+__global__ __launch_bounds__(kThreads) void k_combine_kept_bwd(KeptBwdArgs a) {
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / kWave) + wave;
+  if (t >= a.T) return;
+  SlotInfo<KMAX> si;
+  load_slots(a.slot2row, a.w, t, a.K, lane, si);
+  if (a.roww)
+#pragma unroll
+    for (int k = 0; k < KMAX; ++k)
+      if (lane == k && si.code[k] >= 0) a.roww[si.code[k]] = si.w[k];
+  const int64_t Hv = a.Hv;
+  constexpr int U = kChunk<KMAX>;
+  float dot[KMAX];
+#pragma unroll
+  for (int k = 0; k < KMAX; ++k) dot[k] = 0.f;
+  for (int64_t v0 = lane; v0 < Hv; v0 += U * kWave) {
+    uint2 raw[U][KMAX];
+    uint32_t sc[U][KMAX];
+    uint4 dr[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t v = v0 + u * kWave;
+      if (v < Hv) {
+        dr[u] = a.dout[t * Hv + v];
+#pragma unroll
+        for (int k = 0; k < KMAX; ++k)
+          if (si.code[k] >= 0) {
+            raw[u][k] = a.codes[(int64_t)si.code[k] * Hv + v];
+            sc[u][k] = a.scales[(int64_t)si.code[k] * a.nb + v / 4];
+          }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t v = v0 + u * kWave;
+      if (v < Hv) {
+        float d[8], ox[8];
+        unpack8(dr[u], d);
+        if (si.any_ori) unpack8(a.ori[t * Hv + v], ox);
+#pragma unroll
+        for (int k = 0; k < KMAX; ++k) {
+          const int c = si.code[k];
+          if (c == MOE_SLOT_NONE) continue;
+          float f[8];
+          if (c >= 0) kept8(raw[u][k], bf2f(sc[u][k]), f);
+          else special_value(c, ox, a.a1, a.a2, a.cv, Hv, v, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[k] = __fmaf_rn(f[i], d[i], dot[k]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < KMAX; ++k)
+    if (k < a.K) {
+      float p = dot[k];
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) p += __shfl_xor(p, o, kWave);
+      if (lane == 0) a.dw[t * a.K + k] = si.code[k] == MOE_SLOT_NONE ? 0.f : p;
+    }
+}
+
+template <typename Fn>
+inline void launch_k(int K, Fn f) {
+  if (K <= 2) f(std::integral_constant<int, 2>{});
+  else if (K <= 4) f(std::integral_constant<int, 4>{});
+  else if (K <= 8) f(std::integral_constant<int, 8>{});
+  else f(std::integral_constant<int, 16>{});
+}
+
+inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+moe_status check_swiglu(int64_t R, int64_t F) {
+  if (R < 0 || R > (int64_t)1 << 40 || F < 1 || F > (int64_t)1 << 20) return MOE_ERR_BAD_SHAPE;
+  return MOE_OK;
+}
+
+// HIP refuses a launch of 2^32 threads or more.
+constexpr int64_t kMaxThreads = 0xffffff00;
+
+template <int PASS>
+moe_status launch_swiglu(SwigluArgs a, void* stream) {
+  a.nb = (a.F + kCols - 1) / kCols;
+  const void* io = PASS == KEEP ? a.gate_up : a.out;
+  const bool vec = a.F % kCols == 0 && aligned16(io) && aligned16(a.h) && aligned16(a.grad_h) &&
+                   reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
+  if (vec) {
+    a.cols = (uint32_t)(a.F / 8);
+    a.step_rows = kThreads / a.cols;
+    a.step_cols = kThreads % a.cols;
+    const int64_t units = a.R * (int64_t)a.cols;
+    if (units / 2 > kMaxThreads) return MOE_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)((units + 2 * kThreads - 1) / (2 * kThreads)));
+    if (a.h) hipLaunchKernelGGL((k_swiglu_rows<PASS, true>), grid, dim3(kThreads), 0, as_stream(stream), a);
+    else hipLaunchKernelGGL((k_swiglu_rows<PASS, false>), grid, dim3(kThreads), 0, as_stream(stream), a);
+  } else {
+    const int64_t threads = a.R * a.nb * kCols;
+    if (threads > kMaxThreads) return MOE_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL(k_swiglu_any<PASS>, dim3((unsigned)((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                       as_stream(stream), a);
+  }
+  return launch_status();
+}
+
+// Waves per token: as the plain combine's (combine.hip), for equal results in
+// equal time; sums run over k, so the split changes no bit.
+inline int keep_split(int64_t Hv, int K) {
+  if (K >= 4 && Hv % kWave == 0) {
+    const int km = K <= 4 ? 4 : (K <= 8 ? 8 : 16);
+    const int64_t u = km >= 16 ? 1 : 16 / km;
+    const int64_t blocks = Hv / kWave;
+    if (blocks % u == 0 && blocks / u >= 4 && blocks / u <= 16) return (int)(blocks / u);
+  }
+  return token_split(Hv, K);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_swiglu_checkpoint_fwd(int64_t R, int64_t F, const void* gate_up, const int32_t* nrows,
+                                                void* h, int8_t* codes, void* scales, void* stream) {
+  const moe_status st = check_swiglu(R, F);
+  if (st != MOE_OK) return st;
+  if (R == 0) return MOE_OK;
+  if (!gate_up || !codes || !scales) return MOE_ERR_NULL_ARG;
+  SwigluArgs a{};
+  a.gate_up = gate_up;
+  a.nrows = nrows;
+  a.codes = codes;
+  a.scales = static_cast<uint16_t*>(scales);
+  a.h = h;
+  a.R = R;
+  a.F = F;
+  return launch_swiglu<KEEP>(a, stream);
+}
+
+extern "C" moe_status moe_swiglu_checkpoint_bwd(int64_t R, int64_t F, const int8_t* codes, const void* scales,
+                                                const int32_t* nrows, const void* grad_h, void* grad_gate_up,
+                                                void* h, void* stream) {
+  const moe_status st = check_swiglu(R, F);
+  if (st != MOE_OK) return st;
+  if (R == 0) return MOE_OK;
+  if (!codes || !scales || !grad_h || !grad_gate_up) return MOE_ERR_NULL_ARG;
+  SwigluArgs a{};
+  a.grad_h = grad_h;
+  a.nrows = nrows;
+  a.codes = const_cast<int8_t*>(codes);
+  a.scales = static_cast<uint16_t*>(const_cast<void*>(scales));
+  a.out = grad_gate_up;
+  a.h = h;
+  a.R = R;
+  a.F = F;
+  return launch_swiglu<GRAD>(a, stream);
+}
+
+extern "C" moe_status moe_swiglu_checkpoint_restore(int64_t R, int64_t F, const int8_t* codes, const void* scales,
+                                                    const int32_t* nrows, void* gate_up, void* h, void* stream) {
+  const moe_status st = check_swiglu(R, F);
+  if (st != MOE_OK) return st;
+  if (R == 0) return MOE_OK;
+  if (!codes || !scales || !gate_up) return MOE_ERR_NULL_ARG;
+  SwigluArgs a{};
+  a.nrows = nrows;
+  a.codes = const_cast<int8_t*>(codes);
+  a.scales = static_cast<uint16_t*>(const_cast<void*>(scales));
+  a.out = gate_up;
+  a.h = h;
+  a.R = R;
+  a.F = F;
+  return launch_swiglu<RESTORE>(a, stream);
+}
+
+extern "C" moe_status moe_combine_checkpoint(const moe_shape* s, const void* y, const int32_t* topk_idx,
+                                             const float* topk_weights, const int32_t* assist,
+                                             const int32_t* ep_send_counts, const uint8_t* x_active_mask,
+                                             const void* shared_expert_x, const void* ori_x,
+                                             const void* const_alpha_1, const void* const_alpha_2,
+                                             const void* const_v, void* out, int8_t* y_codes, void* y_scales,
+                                             void* stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (s->comm_quant_mode != 0) return MOE_ERR_UNSUPPORTED;
+  if (s->T == 0) return MOE_OK;
+  MOE_NEED(y, s->capacity * s->H);
+  MOE_NEED(y_codes, s->capacity * s->H);
+  MOE_NEED(y_scales, s->capacity * s->H);
+  if (!topk_idx || !topk_weights || !assist || !ep_send_counts || !out) return MOE_ERR_NULL_ARG;
+  if (s->mask_ndim > 0 && !x_active_mask) return MOE_ERR_NULL_ARG;
+  st = check_special(s, ori_x, const_alpha_1, const_alpha_2, const_v);
+  if (st != MOE_OK) return st;
+  for (const void* p : {y, shared_expert_x, ori_x, const_alpha_1, const_alpha_2, const_v, (const void*)out})
+    if (!aligned16(p)) return MOE_ERR_BAD_SHAPE;
+  if (reinterpret_cast<uintptr_t>(y_codes) % 8) return MOE_ERR_BAD_SHAPE;
+  const CombineArgs a{static_cast<const uint4*>(y),
+                      topk_weights,
+                      assist,
+                      static_cast<const uint4*>(shared_expert_x),
+                      static_cast<const uint4*>(ori_x),
+                      static_cast<const uint4*>(const_alpha_1),
+                      static_cast<const uint4*>(const_alpha_2),
+                      static_cast<const uint4*>(const_v),
+                      static_cast<uint4*>(out),
+                      s->T,
+                      s->K,
+                      s->H / 8,
+                      0,
+                      keep_split(s->H / 8, s->K)};
+  const KeptArgs q{reinterpret_cast<uint2*>(y_codes), static_cast<uint16_t*>(y_scales), (s->H + kCols - 1) / kCols};
+  const int64_t waves = s->T * a.split;
+  launch_k(s->K, [&](auto km) {
+    hipLaunchKernelGGL(k_combine_keep<decltype(km)::value>, dim3((unsigned)((waves + 3) / 4)), dim3(kThreads), 0,
+                       as_stream(stream), a, q);
+  });
+  return launch_status();
+}
+
+extern "C" moe_status moe_combine_bwd_weights_checkpoint(
+    const moe_shape* s, const void* grad_out, const int8_t* y_codes, const void* y_scales, const int32_t* topk_idx,
+    const float* topk_weights, const int32_t* assist, const int32_t* ep_send_counts, const uint8_t* x_active_mask,
+    const void* ori_x, const void* const_alpha_1, const void* const_alpha_2, const void* const_v,
+    float* grad_topk_weights, float* row_weights, void* stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (s->comm_quant_mode != 0) return MOE_ERR_UNSUPPORTED;
+  if (s->T == 0) return MOE_OK;
+  MOE_NEED(y_codes, s->capacity * s->H);
+  MOE_NEED(y_scales, s->capacity * s->H);
+  if (!grad_out || !topk_idx || !topk_weights || !assist || !ep_send_counts || !grad_topk_weights)
+    return MOE_ERR_NULL_ARG;
+  if (s->mask_ndim > 0 && !x_active_mask) return MOE_ERR_NULL_ARG;
+  st = check_special(s, ori_x, const_alpha_1, const_alpha_2, const_v);
+  if (st != MOE_OK) return st;
+  for (const void* p : {grad_out, ori_x, const_alpha_1, const_alpha_2, const_v})
+    if (!aligned16(p)) return MOE_ERR_BAD_SHAPE;
+  if (reinterpret_cast<uintptr_t>(y_codes) % 8) return MOE_ERR_BAD_SHAPE;
+  const KeptBwdArgs a{static_cast<const uint4*>(grad_out),
+                      reinterpret_cast<const uint2*>(y_codes),
+                      static_cast<const uint16_t*>(y_scales),
+                      topk_weights,
+                      assist,
+                      static_cast<const uint4*>(ori_x),
+                      static_cast<const uint4*>(const_alpha_1),
+                      static_cast<const uint4*>(const_alpha_2),
+                      static_cast<const uint4*>(const_v),
+                      grad_topk_weights,
+                      row_weights,
+                      s->T,
+                      s->H / 8,
+                      (s->H + kCols - 1) / kCols,
+                      s->K};
+  launch_k(s->K, [&](auto km) {
+    hipLaunchKernelGGL(k_combine_kept_bwd<decltype(km)::value>, dim3((unsigned)((s->T + 3) / 4)), dim3(kThreads), 0,
+                       as_stream(stream), a);
+  });
+  return launch_status();
+}

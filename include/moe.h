@@ -61,6 +61,7 @@ typedef int32_t moe_status;
                                         result timed out; the output is not valid */
 
 #define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_FP32 1 /* logits of moe_balance_* */
 
 /* Codes stored in the slot-to-row part of assist_info_for_combine. */
 #define MOE_SLOT_NONE (-1)  /* inactive slot, zero expert or invalid slot */
@@ -852,6 +853,116 @@ moe_status moe_linear_int8_workspace_size(int64_t M, int64_t N, int64_t K, size_
 moe_status moe_linear_int8_dynamic(int64_t M, int64_t N, int64_t K, const void* x, const int8_t* wq,
                                    const float* ws, const float* bias, void* out, void* workspace, size_t ws_bytes,
                                    void* stream);
+
+/* ------------------------------------------------------------- balance loss
+ * What spreads the router's load while it trains, and the per-expert counts.  Over
+ * the tokens t of sequence s (all tokens are one sequence without seq_offsets; with
+ * them s holds tokens seq_offsets[s] .. seq_offsets[s + 1] - 1, and tokens outside
+ * every sequence take no part):
+ *   p[t, :] = softmax(logits[t, :])
+ *   c[s, e] = the active slots (t, k) of s with topk_idx[t, k] = e
+ *   n_s     = the active tokens of s, N = their sum over s
+ *   loss    = n_ids / (K N) * sum_s (1 / n_s) sum_e c[s, e] sum_{t active in s} p[t, e]
+ *   z_loss  = (1 / N) sum_{t active} logsumexp(logits[t, :])^2
+ * so loss is the mean over tokens of their sequence's n_ids sum_e f_e P_e, 1 for an
+ * even load.  A slot is active when its mask (T, K) is set, or its token's (T,); a
+ * token is when any of its slots is.  Ids outside [0, n_ids) are not counted.
+ * Without an active token both losses are 0.  A NaN logit counts as -inf, as in the router; a row
+ * that holds nothing above -inf adds nothing to either sum and has gradient 0; a
+ * +inf logit makes the losses NaN.
+ * Sizes: 0 <= T < 2^31, 1 <= n_ids <= 4096, 0 < K <= min(16, n_ids), T K < 2^31, num_seqs 0 (no
+ * seq_offsets) to 2^20, num_seqs * ceil(n_ids / 64) < 2^24 (else MOE_ERR_BAD_SHAPE); dtype of the
+ * logits and their gradient MOE_DTYPE_FP32 or MOE_DTYPE_BF16, mask_ndim 0, 1, 2
+ * (else MOE_ERR_BAD_RANGE).  seq_offsets are data: they are clamped to [0, T], and
+ * where they decrease the results are unspecified, with every access in bounds.
+ * Sums of more than one workgroup's tokens are held in fp64, in a fixed order.
+ */
+moe_status moe_balance_workspace_size(int64_t T, int64_t n_ids, int64_t num_seqs, size_t* bytes);
+
+/* moe_balance_fwd - two launches.
+ *  in   logits (T, n_ids); topk_idx (T, K) int32; x_active_mask (T,) or (T, K) or
+ *       NULL with mask_ndim 0; seq_offsets (num_seqs + 1) int32 or NULL with num_seqs 0
+ *  out  loss, z_loss: one fp32 each; counts (max(num_seqs, 1), n_ids) int32: c;
+ *       seq_tokens (max(num_seqs, 1) + 1) int32: n_s, then N (the backward's)
+ *  workspace >= moe_balance_workspace_size bytes, else MOE_ERR_WORKSPACE.  Calls that
+ *  share one must not overlap in time. */
+moe_status moe_balance_fwd(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs, int32_t mask_ndim, int32_t dtype,
+                           const void* logits, const int32_t* topk_idx, const uint8_t* x_active_mask,
+                           const int32_t* seq_offsets, float* loss, float* z_loss, int32_t* counts,
+                           int32_t* seq_tokens, void* workspace, size_t ws_bytes, void* stream);
+
+/* moe_balance_bwd - the gradient of grad_loss * loss + grad_z_loss * z_loss to the
+ * logits (the counts are held fixed):
+ *   g[t, e] = grad_loss n_ids / (K N n_s) p[t, e] (c[s, e] - sum_j p[t, j] c[s, j])
+ *             + grad_z_loss (2 / N) logsumexp(logits[t, :]) p[t, e]
+ *  in   logits, x_active_mask, seq_offsets, counts, seq_tokens as in the forward;
+ *       grad_loss, grad_z_loss: one fp32 each on the device, or NULL (0)
+ *  out  grad_logits (T, n_ids) in the logits' type, every element written (0 for
+ *       tokens that take no part).  One launch. */
+moe_status moe_balance_bwd(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs, int32_t mask_ndim, int32_t dtype,
+                           const void* logits, const uint8_t* x_active_mask, const int32_t* seq_offsets,
+                           const int32_t* counts, const int32_t* seq_tokens, const float* grad_loss,
+                           const float* grad_z_loss, void* grad_logits, void* stream);
+
+/* ----------------------------------------------------- checkpoints in 8 bits
+ * Activations that only the backward reads, kept as int8 codes with a bf16 scale for
+ * every 32 consecutive columns of a row (the last block of a row may be shorter):
+ * 1.0625 bytes a value.  scale s = bf16(amax / 127), code = rint(v * fp32(1 / s)),
+ * in [-127, 127], ties to even; the kept value is code * s, within s / 2 of v.  A block
+ * whose s would be below 2^-126 keeps zeros; one that holds an infinity or a NaN
+ * keeps NaN.  Rows of width W: codes (rows, W) int8, scales (rows, ceil(W / 32))
+ * bf16; rows [G | U] of width 2F are cut into blocks as two rows of width F: scales
+ * (rows, 2, ceil(F / 32)).  R >= 0 rows, 1 <= F <= 2^20 (else MOE_ERR_BAD_SHAPE);
+ * up to 2^32 columns of G, 2^36 where F is a multiple of 32 and every matrix
+ * begins on a 16-byte boundary (else MOE_ERR_UNSUPPORTED).  nrows: the rows in use,
+ * one int32 on the device (e.g. the last of ep_recv_counts), or NULL: all R; rows past
+ * them are neither read nor written.  One launch each.
+ */
+
+/* moe_swiglu_checkpoint_fwd - h = silu(G) * U and the kept [G | U].
+ *  in   gate_up (R, 2F) bf16
+ *  out  h (R, F) bf16 or NULL; codes (R, 2F) int8, scales (R, 2, ceil(F / 32)) bf16 */
+moe_status moe_swiglu_checkpoint_fwd(int64_t R, int64_t F, const void* gate_up, const int32_t* nrows, void* h,
+                                     int8_t* codes, void* scales, void* stream);
+
+/* moe_swiglu_checkpoint_bwd - SwiGLU's backward from the kept G, U:
+ *   dU = grad_h silu(G), dG = grad_h U sigmoid(G) (1 + G (1 - sigmoid(G)))
+ *  in   grad_h (R, F) bf16
+ *  out  grad_gate_up (R, 2F) bf16: [dG | dU]; h (R, F) bf16 of the kept values, or NULL */
+moe_status moe_swiglu_checkpoint_bwd(int64_t R, int64_t F, const int8_t* codes, const void* scales,
+                                     const int32_t* nrows, const void* grad_h, void* grad_gate_up, void* h,
+                                     void* stream);
+
+/* moe_swiglu_checkpoint_restore - the kept rows in bf16, for the GEMMs that read
+ * gate_up_save and h_act.
+ *  out  gate_up (R, 2F) bf16; h (R, F) bf16 of the kept values, or NULL */
+moe_status moe_swiglu_checkpoint_restore(int64_t R, int64_t F, const int8_t* codes, const void* scales,
+                                         const int32_t* nrows, void* gate_up, void* h, void* stream);
+
+/* moe_combine_checkpoint - moe_combine (out bit for bit) that keeps every routed
+ * row of y in 8 bits on its way, so y need not outlive the call.
+ *  out  y_codes (capacity, H) int8, y_scales (capacity, ceil(H / 32)) bf16: the rows
+ *       that a slot refers to; others are not written
+ *  other arguments as moe_combine.  comm_quant_mode must be 0 (MOE_ERR_UNSUPPORTED);
+ *  bf16 matrices on 16-byte boundaries, codes on 8 (MOE_ERR_BAD_SHAPE). */
+moe_status moe_combine_checkpoint(const moe_shape* s, const void* y, const int32_t* topk_idx,
+                                  const float* topk_weights, const int32_t* assist_info_for_combine,
+                                  const int32_t* ep_send_counts, const uint8_t* x_active_mask,
+                                  const void* shared_expert_x, const void* ori_x, const void* const_alpha_1,
+                                  const void* const_alpha_2, const void* const_v, void* out, int8_t* y_codes,
+                                  void* y_scales, void* stream);
+
+/* moe_combine_bwd_weights_checkpoint - moe_combine_bwd_weights on kept rows:
+ *  in   y_codes, y_scales of moe_combine_checkpoint
+ *  out  grad_topk_weights (T, K) fp32; row_weights (capacity,) fp32 or NULL
+ *  other arguments as moe_combine_bwd_weights, checks as moe_combine_checkpoint. */
+moe_status moe_combine_bwd_weights_checkpoint(const moe_shape* s, const void* grad_out, const int8_t* y_codes,
+                                              const void* y_scales, const int32_t* topk_idx,
+                                              const float* topk_weights, const int32_t* assist_info_for_combine,
+                                              const int32_t* ep_send_counts, const uint8_t* x_active_mask,
+                                              const void* ori_x, const void* const_alpha_1,
+                                              const void* const_alpha_2, const void* const_v,
+                                              float* grad_topk_weights, float* row_weights, void* stream);
 
 /* moe_hbm_stream - a reference streaming kernel (not part of the layer): the
  * measured HBM ceiling that the gather-reduce kernels are compared with.

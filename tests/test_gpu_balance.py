@@ -1,0 +1,280 @@
+"""GPU tests of the router's balance loss, z loss and counts with their gradient, against the 64-bit form."""
+import pytest
+import torch
+
+import dispatch_expert_gemm_amd as dm
+from balance_util import compare, reference
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _inputs(T, n, K, seed, std=1.0, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    l = torch.randn(T, n, generator=g) * std + torch.randn(n, generator=g)
+    idx = l.topk(K, 1)[1].to(torch.int32) if T else torch.zeros(0, K, dtype=torch.int32)
+    return l.to(dtype).to(DEV), idx.to(DEV)
+
+
+def _mask(kind, T, K, seed):
+    g = torch.Generator().manual_seed(seed + 100)
+    if kind == 0:
+        return None
+    if kind == 1:
+        return (torch.arange(T) < T - T // 3).to(DEV)
+    m = torch.rand(T, K, generator=g) >= 0.3
+    m[::5] = False  # whole tokens without a slot
+    return m.to(torch.uint8).to(DEV)
+
+
+def _offsets(S, T, seed, lead=0, tail=0):
+    g = torch.Generator().manual_seed(seed + 200)
+    cuts = (torch.rand(S - 1, generator=g) * max(T - lead - tail, 0)).long().sort()[0] + lead
+    return torch.cat([torch.tensor([min(lead, T)]), cuts.clamp(max=T),
+                      torch.tensor([max(min(lead, T), T - tail)])]).to(torch.int32).to(DEV)
+
+
+def _run(l, idx, mask=None, offsets=None, g=0.7, gz=0.3):
+    l = l.detach().requires_grad_()
+    loss, z, counts = dm.balance_loss(l, idx, x_active_mask=mask, seq_offsets=offsets)
+    assert loss.shape == () and z.shape == () and loss.dtype == torch.float32
+    ups = [v if isinstance(v, torch.Tensor) else torch.tensor(v, device=DEV) for v in (g, gz)]
+    grad, = torch.autograd.grad((loss, z), l, ups)
+    assert grad.dtype == l.dtype and grad.shape == l.shape
+    return loss.detach(), z.detach(), counts, grad
+
+
+def _check(name, l, idx, mask=None, offsets=None, g=0.7, gz=0.3):
+    got = _run(l, idx, mask, offsets, g, gz)
+    g, gz = float(torch.tensor(g)), float(torch.tensor(gz))
+    compare(name, got, reference(l, idx, mask, offsets, g, gz, l.dtype))
+    return got
+
+
+# every number of columns that changes the lanes or runs of a token, odd ones among them
+COLUMNS = [1, 2, 3, 4, 5, 16, 17, 63, 64, 65, 100, 128, 129, 256, 257, 260, 512, 513, 1024, 1025, 2048, 2051, 4096]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("n", COLUMNS)
+def test_columns(n, dtype):
+    T, K = 97, min(n, 8)
+    l, idx = _inputs(T, n, K, n, dtype=dtype)
+    _check(f"n={n}", l, idx, _mask(2, T, K, n))
+
+
+@pytest.mark.parametrize("T", [0, 1, 2, 15, 16, 17, 64, 255, 1000, 4099, 16384])
+def test_tokens(T):
+    l, idx = _inputs(T, 64, 8, T + 1)
+    _check(f"T={T}", l, idx)
+    _check(f"T={T} bf16", l.bfloat16(), idx, _mask(1, T, 8, T))
+
+
+@pytest.mark.parametrize("mask", [0, 1, 2])
+@pytest.mark.parametrize("T,n,K,S,lead,tail", [
+    (1, 64, 8, 1, 0, 0), (1, 8, 2, 5, 0, 0), (300, 64, 8, 1, 7, 11), (300, 64, 8, 300, 0, 0), (513, 100, 3, 64, 0, 40),
+    (513, 100, 3, 65, 3, 0), (2000, 260, 8, 37, 0, 61), (4096, 16, 1, 1000, 100, 100), (4000, 64, 16, 2, 3999, 0),
+    (70, 1024, 16, 9, 0, 3), (16, 64, 8, 5000, 0, 0)])
+def test_sequences(T, n, K, S, lead, tail, mask):
+    """Ragged, empty and one-token sequences, tokens before the first and behind the last."""
+    l, idx = _inputs(T, n, K, S)
+    got = _check(f"S={S}", l, idx, _mask(mask, T, K, S), _offsets(S, T, S, lead, tail))
+    assert got[2].shape == (S, n)
+
+
+def test_sequences_are_each_by_themselves():
+    """Two sequences give the token-weighted mean of their own losses, and the gradient of a token does not see the
+    other sequence's logits."""
+    l, idx = _inputs(200, 64, 8, 5)
+    off = torch.tensor([0, 60, 200], dtype=torch.int32, device=DEV)
+    loss, z, counts, grad = _run(l, idx, None, off)
+    a, b = _run(l[:60], idx[:60]), _run(l[60:], idx[60:])
+    assert abs(float(loss) - (0.3 * float(a[0]) + 0.7 * float(b[0]))) < 1e-6 * float(loss)
+    assert torch.equal(counts, torch.stack([a[2], b[2]]))
+    other = l.clone()
+    other[60:] = other[60:].flip(0)
+    assert torch.equal(_run(other, idx, None, off)[3][:60], grad[:60])
+
+
+def test_even_load_is_one():
+    l = torch.zeros(64, 32, device=DEV)
+    idx = ((torch.arange(64)[:, None] * 4 + torch.arange(4)) % 32).to(torch.int32).to(DEV)
+    loss, _, counts, _ = _run(l, idx)
+    assert float(loss) == 1.0 and (counts == 8).all()
+
+
+@pytest.mark.parametrize("mask", [1, 2])
+def test_masks_that_leave_nothing(mask):
+    l, idx = _inputs(50, 64, 8, 3)
+    m = torch.zeros((50,) if mask == 1 else (50, 8), dtype=torch.bool, device=DEV)
+    loss, z, counts, grad = _run(l, idx, m)
+    assert float(loss) == 0 and float(z) == 0 and not counts.any() and not grad.any()
+
+
+def test_masked_tokens_hold_anything():
+    """NaN and infinities in tokens that take no part change nothing and get gradient 0."""
+    l, idx = _inputs(120, 64, 8, 9)
+    m = torch.rand(120, 8, generator=torch.Generator().manual_seed(1)).to(DEV) >= 0.5
+    m[40:80] = False
+    want = _run(l, idx, m)
+    bad = l.clone()
+    bad[40:60] = float("nan")
+    bad[60:70] = float("inf")
+    bad[70:80] = -float("inf")
+    got = _run(bad, idx, m)
+    for a, b in zip(want[:3], got[:3]):
+        assert torch.equal(a, b)
+    assert torch.equal(want[3][:40], got[3][:40]) and torch.equal(want[3][80:], got[3][80:])
+    assert not got[3][40:80].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_impossible_and_extreme_logits(dtype):
+    l, idx = _inputs(90, 72, 6, 4, dtype=dtype)
+    l[:, 7] = -float("inf")                       # an id that no token may take
+    l[3, :71] = -float("inf")                     # one id left
+    l[4] = -float("inf")                          # nothing left: adds nothing
+    l[5, 10] = float("nan")                       # read as -inf
+    l[6] = torch.finfo(dtype).min                 # the type's lowest value everywhere
+    l[7, 3] = torch.finfo(dtype).min
+    l[8] = l[8] * 30
+    gz = 0.0                                      # lse^2 of the lowest value is an infinity: the z loss by itself below
+    loss, z, counts, grad = _run(l, idx, gz=gz)
+    ref = reference(l, idx, None, None, float(torch.tensor(0.7)), gz, dtype)
+    assert torch.equal(counts.cpu().long(), ref["counts"])
+    assert abs(float(loss) - ref["loss"]) <= ref["loss_bound"]
+    keep = torch.ones(90, dtype=torch.bool)
+    keep[6] = False                               # 0 * lse is 0 * -3e38: finite, but its bound is not
+    err = (grad.cpu().double() - ref["grad"]).abs()
+    assert (err[keep] <= ref["bound"][keep]).all()
+    assert not grad[4].any() and not grad[keep.to(DEV), 7].any() and float(grad[5, 10]) == 0  # (row 6 has an id 7)
+    l[6] = 0
+    _check("extreme", l, idx)
+
+
+def test_plus_infinity_is_seen():
+    l, idx = _inputs(33, 16, 2, 4)
+    l[3, 5] = float("inf")
+    loss, z, _, grad = _run(l, idx)
+    assert not torch.isfinite(loss) and not torch.isfinite(z) and not torch.isfinite(grad[3]).any()
+
+
+def test_ids_outside_are_not_counted_and_repeated_ids_are():
+    l, idx = _inputs(64, 32, 4, 6)
+    idx[3] = torch.tensor([-1, 32, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    idx[4] = 5
+    _check("ids", l, idx)
+
+
+@pytest.mark.parametrize("offsets", [[0, -5, 40, 64], [50, 20, 10, 64], [-9, 10, 5000, 70], [64, 64, 0, 0], [2 ** 31 - 1, -2 ** 31, 3, 9]])
+def test_offsets_that_decrease_or_leave_the_batch_stay_in_bounds(offsets):
+    l, idx = _inputs(64, 32, 4, 6)
+    room = torch.full((64 + 2, 32), 7.0, device=DEV)
+    grad = room[1:-1]
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    loss, z = torch.empty(1, device=DEV), torch.empty(1, device=DEV)
+    counts, tokens = torch.empty(3 * 32, dtype=torch.int32, device=DEV), torch.empty(4, dtype=torch.int32, device=DEV)
+    ws = torch.zeros(dm.moe_balance_workspace_size(64, 32, 3), dtype=torch.uint8, device=DEV)
+    dm.moe_balance_fwd(l, idx, None, off, loss, z, counts, tokens, ws)
+    dm.moe_balance_bwd(l, 4, None, off, counts, tokens, loss, z, grad)
+    torch.cuda.synchronize()
+    assert (room[0] == 7).all() and (room[-1] == 7).all()
+
+
+def test_views_and_misaligned_rows():
+    big, idx = _inputs(50, 80, 4, 8)
+    idx = idx.clamp(max=63)
+    view = big[:, 5:69]                                  # strides: laid out by the call
+    want = _run(view.contiguous(), idx)
+    for a, b in zip(want, _run(view, idx)):
+        assert torch.equal(a, b)
+    flat = torch.empty(50 * 64 + 1, device=DEV)[1:].view(50, 64)  # rows that begin on 4 bytes
+    flat.copy_(view)
+    got = _run(flat, idx)
+    for a, b in zip(want[:3], got[:3]):
+        assert torch.equal(a, b)
+    assert torch.equal(want[3], got[3])
+
+
+def test_one_upstream_gradient_alone():
+    l, idx = _inputs(70, 48, 4, 2)
+    x = l.clone().requires_grad_()
+    loss, z, _ = dm.balance_loss(x, idx)
+    ga, = torch.autograd.grad(loss, x, retain_graph=True)
+    gb, = torch.autograd.grad(z, x)
+    ra, rb = reference(l, idx, g=1.0, gz=0.0), reference(l, idx, g=0.0, gz=1.0)
+    for got, ref in ((ga, ra), (gb, rb)):
+        assert ((got.cpu().double() - ref["grad"]).abs() <= ref["bound"]).all()
+
+
+def test_gradient_against_differences():
+    l, idx = _inputs(12, 10, 3, 7)
+    m = _mask(2, 12, 3, 7)
+    off = torch.tensor([0, 5, 5, 11], dtype=torch.int32, device=DEV)
+    grad = _run(l, idx, m, off, 1.0, 0.5)[3].cpu().double()
+    h = 1e-4
+
+    def value(x):
+        r = reference(x, idx, m, off)
+        return r["loss"] + 0.5 * r["z"]
+
+    base = l.cpu().double()
+    for t, e in [(0, 0), (1, 3), (4, 9), (6, 2), (10, 5), (11, 1)]:
+        a, b = base.clone(), base.clone()
+        a[t, e] += h
+        b[t, e] -= h
+        # the difference quotient's own error is h^2 / 6 of a third derivative (the terms are of the order of 10 / N)
+        assert abs((value(a) - value(b)) / (2 * h) - float(grad[t, e])) < 1e-6 + 10 * h * h
+
+
+def test_bitwise_repeatable_and_whole_workspace_uninitialised():
+    l, idx = _inputs(3000, 160, 8, 1)
+    off = _offsets(11, 3000, 2)
+    a = _run(l, idx, None, off)
+    torch.empty(1 << 24, dtype=torch.uint8, device=DEV).fill_(255)  # what the allocator hands out next
+    b = _run(l, idx, None, off)
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+
+
+def test_other_stream_and_captured_calls():
+    T, n, K = 2000, 64, 8
+    l, idx = _inputs(T, n, K, 1)
+    want = _run(l, idx)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = _run(l, idx)
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    # two captured calls with workspaces of their own, replayed with new inputs and eager work between
+    static = l.clone()
+    ups = [torch.tensor(0.7, device=DEV), torch.tensor(0.3, device=DEV)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [_run(static, idx, None, None, *ups), _run(static * 1.0, idx, None, None, *ups)]
+    for seed in (2, 3, 4):
+        new, _ = _inputs(T, n, K, seed)
+        static.copy_(new)
+        graph.replay()
+        eager = _run(new, idx)
+        torch.cuda.synchronize()
+        for o in outs:
+            for a, b in zip(o, eager):
+                assert torch.equal(a, b)
+
+
+def test_large_batch():
+    """Offsets past 2^31 bytes, many items and the most columns."""
+    T, n, K = 140000, 4096, 4
+    l = torch.randn(1000, n, generator=torch.Generator().manual_seed(1)).to(DEV).repeat(140, 1)
+    idx = l[:1000].topk(K, 1)[1].to(torch.int32).repeat(140, 1)
+    loss, z, counts, grad = _run(l, idx)
+    small = _run(l[:1000], idx[:1000])
+    assert torch.equal(counts, small[2] * 140)
+    # every copy is the same batch: the losses agree to their rounding, the gradients to 1/140
+    assert abs(float(loss) - float(small[0])) < 1e-4 * float(loss)
+    assert abs(float(z) - float(small[1])) < 1e-4 * float(z)
+    part = grad[-1000:] * 140
+    assert float((part - small[3]).abs().max()) < 1e-4 * float(small[3].abs().max())
