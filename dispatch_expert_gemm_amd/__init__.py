@@ -12,6 +12,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -20,6 +22,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libmoe.so")
+NODES_PATH = os.path.join(_PKG, "lib", "moe_torch.so")
 
 MOE_FLAG_ID_RANGE = 1
 MOE_FLAG_ID_DUPLICATE = 2
@@ -176,6 +179,18 @@ def lib() -> ctypes.CDLL:
                 getattr(L, name).restype = ctypes.c_int32
         _lib_handle = L
     return _lib_handle
+
+
+@functools.lru_cache(maxsize=None)
+def _nodes():
+    """The autograd nodes of csrc/torch_nodes.cpp (built by dispatch_expert_gemm_amd.build), loaded once."""
+    if not os.path.exists(NODES_PATH):
+        raise MoeError(f"{NODES_PATH} is missing: run `python -m dispatch_expert_gemm_amd.build`")
+    loader = importlib.machinery.ExtensionFileLoader("moe_torch", NODES_PATH)
+    nodes = importlib.util.module_from_spec(importlib.machinery.ModuleSpec("moe_torch", loader, origin=NODES_PATH))
+    loader.exec_module(nodes)
+    nodes.raise_as(MoeError)
+    return nodes
 
 
 def _check(st: int):
@@ -1720,34 +1735,6 @@ def moe_balance_bwd(logits, K, x_active_mask, seq_offsets, counts, seq_tokens, g
             _at(grad_z_loss, F32, 1, "grad_z_loss", dev), _at(grad_logits, logits.dtype, T * n, "grad_logits", dev))
 
 
-class _BalanceFn(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, topk_idx, x_active_mask, seq_offsets):
-        logits = logits.contiguous()
-        dev = logits.device
-        T, n, K, S, _, _ = _balance_sizes(logits, topk_idx.shape[-1], x_active_mask, seq_offsets)
-        loss, z_loss = torch.empty((), dtype=F32, device=dev), torch.empty((), dtype=F32, device=dev)
-        counts = torch.empty((S, n) if S else (n,), dtype=I32, device=dev)
-        seq_tokens = torch.empty(max(S, 1) + 1, dtype=I32, device=dev)
-        workspace = torch.empty(moe_balance_workspace_size(T, n, S), dtype=torch.uint8, device=dev)
-        moe_balance_fwd(logits, topk_idx, x_active_mask, seq_offsets, loss, z_loss, counts, seq_tokens, workspace)
-        ctx.save_for_backward(logits, x_active_mask, seq_offsets, counts, seq_tokens)
-        ctx.K = K
-        ctx.mark_non_differentiable(counts)
-        ctx.set_materialize_grads(False)
-        return loss, z_loss, counts
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, g_loss, g_z, _):
-        logits, mask, offsets, counts, seq_tokens = ctx.saved_tensors
-        if g_loss is None and g_z is None:
-            return None, None, None, None
-        grad = torch.empty_like(logits)
-        moe_balance_bwd(logits, ctx.K, mask, offsets, counts, seq_tokens, g_loss, g_z, grad)
-        return grad, None, None, None
-
-
 def balance_loss(logits, topk_idx, *, x_active_mask=None, seq_offsets=None):
     """The router's balance loss, its z loss and the experts' counts: logits (T, n_ids) fp32 or bf16 and the
     choices topk_idx (T, K) int32 (router's) -> (loss, z_loss, counts), the losses fp32 scalars, differentiable
@@ -1757,10 +1744,7 @@ def balance_loss(logits, topk_idx, *, x_active_mask=None, seq_offsets=None):
     share of the choices that go to e and P_e the mean of softmax(logits)_e, 1 for an even load; z_loss = mean of
     logsumexp(logits)^2.  seq_offsets (num_seqs + 1) int32, ascending: the loss of each packed sequence by
     itself, averaged over tokens, and counts (num_seqs, n_ids); tokens outside the sequences take no part."""
-    _device_of(logits, "logits")
-    if getattr(topk_idx, "dim", lambda: 0)() != 2:
-        raise MoeError(f"topk_idx must be a tensor of shape (T, K), got {getattr(topk_idx, 'shape', topk_idx)}")
-    return _BalanceFn.apply(logits, topk_idx, x_active_mask, seq_offsets)
+    return _nodes().balance_loss(logits, topk_idx, x_active_mask, seq_offsets)
 
 
 def checkpoint_buffers(rows, width, device, halves=1):
@@ -1806,37 +1790,11 @@ def moe_swiglu_checkpoint_restore(codes, scales, gate_up, h=None, nrows=None, st
             _at(h, BF16, R * F, "h", dev))
 
 
-class _SwigluCheckpointFn(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, gate_up):
-        gate_up = gate_up.contiguous()
-        R, F = _gate_up_sizes(gate_up, "gate_up")
-        h = torch.empty((R, F), dtype=BF16, device=gate_up.device)
-        codes, scales = checkpoint_buffers(R, F, gate_up.device, halves=2)
-        moe_swiglu_checkpoint_fwd(gate_up, h, codes, scales)
-        ctx.save_for_backward(codes, scales)
-        return h
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, grad_h):
-        codes, scales = ctx.saved_tensors
-        grad = torch.empty(codes.shape, dtype=BF16, device=codes.device)
-        moe_swiglu_checkpoint_bwd(codes, scales, grad_h.contiguous(), grad)
-        return grad
-
-
 def swiglu_checkpoint(gate_up):
     """h = silu(G) * U of rows gate_up = [G | U] (..., 2F) bf16 -> (..., F) bf16, keeping gate_up in 8 bits
     (1.0625 bytes a value) for the backward instead of in bf16: differentiable (once); the forward's h is that of
     the bf16 values, the gradient that of the kept ones."""
-    _device_of(gate_up, "gate_up")
-    if gate_up.dtype is not BF16:
-        raise MoeError(f"gate_up must be {BF16}, got {gate_up.dtype}")
-    if not gate_up.dim() or gate_up.shape[-1] % 2 or not gate_up.shape[-1]:
-        raise MoeError(f"gate_up must be a tensor of shape (..., 2F), got {tuple(gate_up.shape)}")
-    h = _SwigluCheckpointFn.apply(gate_up if gate_up.dim() == 2 else gate_up.reshape(-1, gate_up.shape[-1]))
-    return h if gate_up.dim() == 2 else h.reshape(*gate_up.shape[:-1], -1)
+    return _nodes().swiglu_checkpoint(gate_up)
 
 
 def _kept_rows_at(shape, codes, scales, dev):
@@ -1846,12 +1804,11 @@ def _kept_rows_at(shape, codes, scales, dev):
 
 
 def _combine_args(shape, topk_idx, topk_weights, assist_info_for_combine, ep_send_counts, x_active_mask, dev):
-    n = _shape_sizes(shape)
-    return (_at(topk_idx, I32, n["topk_idx"], "topk_idx", dev),
-            _at(topk_weights, F32, n["topk_weights"], "topk_weights", dev),
-            _at(assist_info_for_combine, I32, n["assist_info_for_combine"], "assist_info_for_combine", dev),
-            _at(ep_send_counts, I32, n["ep_send_counts"], "ep_send_counts", dev),
-            _at(_u8(x_active_mask), torch.uint8, n["x_active_mask"], "x_active_mask", dev))
+    TK = shape.T * shape.K
+    return (_at(topk_idx, I32, TK, "topk_idx", dev), _at(topk_weights, F32, TK, "topk_weights", dev),
+            _at(assist_info_for_combine, I32, TK + shape.capacity, "assist_info_for_combine", dev),
+            _at(ep_send_counts, I32, shape.num_experts, "ep_send_counts", dev),
+            _at(_u8(x_active_mask), torch.uint8, (0, shape.T, TK)[shape.mask_ndim], "x_active_mask", dev))
 
 
 def _special_at(shape, ori_x, const_alpha_1, const_alpha_2, const_v, dev):

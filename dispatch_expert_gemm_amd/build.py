@@ -2,13 +2,15 @@
 
     python -m dispatch_expert_gemm_amd.build
 
-compiles every csrc/*.hip with hipcc into lib/libmoe.so.  It always recompiles.
+compiles every csrc/*.hip with hipcc into lib/libmoe.so, and csrc/torch_nodes.cpp
+(autograd nodes that call it) into lib/moe_torch.so.  It always recompiles.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmoe.so")
+TORCH_NODES = os.path.join(LIBDIR, "moe_torch.so")
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep the compiler from forming packed fp32 adds/muls/fmas.
@@ -48,6 +51,29 @@ def _run(cmd):
     return p.returncode, out
 
 
+def nodes_command():
+    """The compiler call of the autograd nodes' object file (host code only)."""
+    from torch.utils import cpp_extension
+    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], "/opt/rocm/include"]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+            "-DTORCH_API_INCLUDE_EXTENSION_H", "-DTORCH_EXTENSION_NAME=moe_torch", "-I", INCLUDE,
+            *[a for i in includes for a in ("-isystem", i)],
+            "-c", os.path.join(CSRC, "torch_nodes.cpp"), "-o", os.path.join(LIBDIR, "obj", "torch_nodes.o")]
+
+
+def link_nodes():
+    from torch.utils import cpp_extension
+    libs = cpp_extension.library_paths()
+    tmp = TORCH_NODES + ".tmp"
+    cmd = ["g++", "-shared", os.path.join(LIBDIR, "obj", "torch_nodes.o"), "-L" + LIBDIR, "-l:libmoe.so",
+           "-Wl,-rpath,$ORIGIN", *["-L" + p for p in libs], "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch",
+           "-ltorch_python", "-o", tmp]
+    rc, out = _run(cmd)
+    if rc != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{out}")
+    os.replace(tmp, TORCH_NODES)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(os.path.join(LIBDIR, "obj"), exist_ok=True)
     cc = hipcc()
@@ -56,19 +82,22 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(LIBDIR, "obj", src.replace(".hip", ".o"))
         cmd = [cc, *COMMON, *EXTRA.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
         jobs.append((src, obj, cmd))
+    kernels = list(jobs)
+    jobs.append(("torch_nodes.cpp", None, nodes_command()))
     with ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
         results = list(ex.map(lambda j: (j, _run(j[2])), jobs))
     for (src, _, cmd), (rc, out) in results:
         if verbose and out.strip():
             print(out)
         if rc != 0:
-            raise RuntimeError(f"hipcc failed on {src}:\n{' '.join(cmd)}\n{out}")
+            raise RuntimeError(f"the compiler failed on {src}:\n{' '.join(cmd)}\n{out}")
     tmp = LIB + ".tmp"
-    cmd = [cc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *[o for _, o, _ in jobs], "-o", tmp]
+    cmd = [cc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *[o for _, o, _ in kernels], "-o", tmp]
     rc, out = _run(cmd)
     if rc != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{out}")
     os.replace(tmp, LIB)
+    link_nodes()
     return LIB
 
 

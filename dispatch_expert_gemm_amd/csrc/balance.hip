@@ -58,9 +58,10 @@ struct BalanceArgs {
   const int32_t* off;  // S + 1, or NULL: one sequence of all tokens
   int64_t T, slots;    // tokens; item slots
   int n, K, S, mask_ndim, C;
+  int pitch;  // of psum's and hist's rows: n up to a multiple of 4
   // forward: per item
-  float* psum;     // slots x n
-  int32_t* hist;   // slots x n
+  float* psum;     // slots x pitch
+  int32_t* hist;   // slots x pitch
   float* zsum;     // slots
   int32_t* ntok;   // slots
   double* dots;    // S x column blocks
@@ -100,12 +101,12 @@ __device__ __forceinline__ int find_last(int S, int64_t x, Key key) {
   return lo;
 }
 
-__device__ __forceinline__ float logit(float v) { return v != v ? -INFINITY : v; }
-
-// The four logits of row t from column c on (-inf past n or where NaN).
+// The four logits of row t from column c on; -inf past n.
 template <typename In, bool VEC>
 __device__ __forceinline__ void load4(const BalanceArgs& a, int64_t t, int c, float* v) {
   const In* p = static_cast<const In*>(a.logits) + t * a.n + c;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = -INFINITY;
   if constexpr (VEC) {  // n a multiple of 4, aligned rows
     if (c < a.n) {
       if constexpr (sizeof(In) == 4) {
@@ -116,22 +117,39 @@ __device__ __forceinline__ void load4(const BalanceArgs& a, int64_t t, int c, fl
         v[0] = bf2f(u.x & 0xffffu); v[1] = bf2f(u.x >> 16);
         v[2] = bf2f(u.y & 0xffffu); v[3] = bf2f(u.y >> 16);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = logit(v[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = -INFINITY;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = -INFINITY;
+    for (int j = 0; j < 4; ++j)
       if (c + j < a.n) {
-        if constexpr (sizeof(In) == 4) v[j] = logit(p[j]);
-        else v[j] = logit(bf2f(reinterpret_cast<const bf16_t*>(p)[j]));
+        if constexpr (sizeof(In) == 4) v[j] = p[j];
+        else v[j] = bf2f(reinterpret_cast<const bf16_t*>(p)[j]);
       }
-    }
   }
+}
+
+// A lane's part of row t (-inf where t >= t1): issued a step ahead of its use.
+template <typename In, bool VEC, int GW, int Q>
+__device__ __forceinline__ void load_row(const BalanceArgs& a, int64_t t, int64_t t1, float (&v)[Q][4]) {
+  const int l = threadIdx.x & (GW - 1);
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    if (t < t1) load4<In, VEC>(a, t, (q * GW + l) * 4, v[q]);
+    else v[q][0] = v[q][1] = v[q][2] = v[q][3] = -INFINITY;
+}
+
+// Rows of up to 1024 columns are loaded a step ahead; longer ones keep 32 or 64 values
+// in flight for each lane anyway, and a second row would leave one wave on a SIMD.
+template <int Q>
+constexpr bool kAhead = Q <= 4;
+
+// The row loaded a step ahead, a NaN read as -inf.
+template <int Q>
+__device__ __forceinline__ void take_row(const float (&next)[Q][4], float (&v)[Q][4]) {
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[q][j] = fmaxf(next[q][j], -INFINITY);  // (fmaxf drops a NaN)
 }
 
 // exp(v - m) in place of the row's logits; m the row's largest, total the sum.  A
@@ -144,58 +162,90 @@ __device__ __forceinline__ void row_exp(float (&v)[Q][4], float& m, float& total
 #pragma unroll
     for (int j = 0; j < 4; ++j) m = fmaxf(m, v[q][j]);
   m = group_max<GW>(m);
-  const bool some = m != -INFINITY;
+  const float base = m != -INFINITY ? m : 0.f;
   float s = 0.f;
 #pragma unroll
   for (int q = 0; q < Q; ++q)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[q][j] = some ? __expf(v[q][j] - m) : 0.f;
+      v[q][j] = __expf(v[q][j] - base);
       s += v[q][j];
     }
   total = group_sum<GW>(s);
 }
 
-// Whether token t counts (its lanes pass the same t), and with HIST its choices
-// into the histogram.
-template <int GW, bool HIST>
-__device__ __forceinline__ bool token_on(const BalanceArgs& a, int64_t t, bool in, int* hist) {
+// Whether token t counts (its lanes pass the same t).
+template <int GW>
+__device__ __forceinline__ bool token_on(const BalanceArgs& a, int64_t t, bool in) {
   const int lane = threadIdx.x & 63, l = lane & (GW - 1);
-  if (!HIST && a.mask_ndim != 2) return in && (a.mask_ndim == 0 || a.mask[t]);
+  if (a.mask_ndim != 2) return in && (a.mask_ndim == 0 || a.mask[t]);
   bool any = false;
-  if (in && (a.mask_ndim != 1 || a.mask[t]))
-    for (int k = l; k < a.K; k += GW) {
-      if (a.mask_ndim == 2 && !a.mask[t * a.K + k]) continue;
-      any = true;
-      if constexpr (HIST) {
-        const int32_t e = a.idx[t * a.K + k];
-        if ((uint32_t)e < (uint32_t)a.n) atomicAdd(&hist[e], 1);
-      }
-    }
+  if (in)
+    for (int k = l; k < a.K; k += GW) any |= a.mask[t * a.K + k] != 0;
   const uint64_t b = __ballot(any);
   if constexpr (GW == 64) return b != 0;
   else return ((b >> (lane & ~(GW - 1))) & ((1ull << GW) - 1)) != 0;
 }
 
-template <typename In, bool VEC, int GW, int Q>
-__global__ __launch_bounds__(kThreads) void k_balance_items(BalanceArgs a) {
-  extern __shared__ float smem[];
-  float* row = smem;                               // n column sums
-  int* hist = reinterpret_cast<int*>(smem + a.n);  // n
-  __shared__ float zs[kWaves];
-  __shared__ int ns[kWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (GW - 1);
-  constexpr int G = kWave / GW;
-  const int64_t item = blockIdx.x;
-  if (item == 0 && tid == 0) *a.ticket = 0;
-  int s = 0;
-  if (a.off) s = find_last(a.S, item, [&](int i) { return off_at(a, i) / a.C + i; });
-  const int64_t lo = off_at(a, s), hi = off_at(a, s + 1);
-  const int64_t t0 = lo + (item - (lo / a.C + s)) * a.C;
-  const int64_t t1 = t0 + a.C < hi ? t0 + a.C : hi;
-  if (t0 < lo || t0 >= t1) return;  // a slot that no sequence fills: never read
-  for (int i = tid; i < a.n; i += kThreads) hist[i] = 0;
+template <int W>
+__device__ __forceinline__ double block_sum(double v, double* red) {
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
   __syncthreads();
+  if ((tid & 63) == 0) red[tid >> 6] = v;
+  __syncthreads();
+  double r = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) r += red[w];
+  return r;
+}
+
+// Waves of a workgroup of items: a wave waits for its tokens' rows, so eight where the
+// registers of Q runs allow it (32768 tokens of 1024 columns, 512 items: 4 waves 67 us,
+// 8 waves and rows loaded ahead 43).
+template <int Q>
+constexpr int kItemWaves = Q <= 4 ? 8 : 4;
+// Rows of column sums in LDS that the waves are added into.
+template <int Q>
+constexpr int kSumRows = Q <= 8 ? 4 : 2;
+
+// ALONE: the batch is one item, so this workgroup finishes it.
+template <typename In, bool VEC, int GW, int Q, bool ALONE>
+__global__ __launch_bounds__(kWave * kItemWaves<Q>, Q <= 4 ? 6 : 1) void k_balance_items(BalanceArgs a) {
+  constexpr int W = kItemWaves<Q>, RW = kSumRows<Q>, G = kWave / GW;
+  extern __shared__ float smem[];
+  float* rows = smem;                                   // RW x n column sums
+  int* hist = reinterpret_cast<int*>(smem + RW * a.n);  // n
+  __shared__ float zs[W];
+  __shared__ int ns[W];
+  __shared__ double red[W];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (GW - 1);
+  const int64_t item = blockIdx.x;
+  if (!ALONE && item == 0 && tid == 0) *a.ticket = 0;
+  int64_t t0 = 0, t1 = a.T;
+  if constexpr (!ALONE) {
+    int s = 0;
+    if (a.off) s = find_last(a.S, item, [&](int i) { return off_at(a, i) / a.C + i; });
+    const int64_t lo = off_at(a, s), hi = off_at(a, s + 1);
+    t0 = lo + (item - (lo / a.C + s)) * a.C;
+    t1 = t0 + a.C < hi ? t0 + a.C : hi;
+    if (t0 < lo || t0 >= t1) return;  // a slot that no sequence fills: never read
+  }
+  for (int i = tid; i < a.n; i += kWave * W) hist[i] = 0;
+  float v[Q][4], next[Q][4];
+  if constexpr (kAhead<Q>) load_row<In, VEC, GW, Q>(a, t0 + wave * G + lane / GW, t1, next);
+  __syncthreads();
+  // the choices by themselves, a thread each: with each token's among its logits the
+  // wave would wait for them too
+  const int slots = (int)(t1 - t0) * a.K;
+  for (int i = tid; i < slots; i += kWave * W) {
+    const int64_t at = t0 * a.K + i;
+    const int32_t e = a.idx[at];
+    bool on = (uint32_t)e < (uint32_t)a.n;
+    if (a.mask_ndim) on = on && a.mask[a.mask_ndim == 2 ? at : t0 + (uint32_t)i / (uint32_t)a.K];
+    if (on) atomicAdd(&hist[e], 1);
+  }
   float p[Q][4];
 #pragma unroll
   for (int q = 0; q < Q; ++q)
@@ -203,15 +253,13 @@ __global__ __launch_bounds__(kThreads) void k_balance_items(BalanceArgs a) {
     for (int j = 0; j < 4; ++j) p[q][j] = 0.f;
   float z = 0.f;
   int nt = 0;
-  for (int64_t b = t0 + wave * G; b < t1; b += kWaves * G) {
+  for (int64_t b = t0 + wave * G; b < t1; b += W * G) {
     const int64_t t = b + lane / GW;
     const bool in = t < t1;
-    float v[Q][4];
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-      if (in) load4<In, VEC>(a, t, (q * GW + l) * 4, v[q]);
-      else v[q][0] = v[q][1] = v[q][2] = v[q][3] = -INFINITY;
-    const bool on = token_on<GW, true>(a, t, in, hist);
+    if constexpr (!kAhead<Q>) load_row<In, VEC, GW, Q>(a, t, t1, next);
+    take_row<Q>(next, v);
+    if constexpr (kAhead<Q>) load_row<In, VEC, GW, Q>(a, t + W * G, t1, next);
+    const bool on = token_on<GW>(a, t, in);
     float m, total;
     row_exp<GW, Q>(v, m, total);
     const float inv = on && total != 0.f ? 1.0f / total : 0.f;
@@ -240,8 +288,9 @@ __global__ __launch_bounds__(kThreads) void k_balance_items(BalanceArgs a) {
     ns[wave] = nt;
   }
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (wave == w && lane < GW)
+  for (int w = 0; w < W / RW; ++w) {
+    if (wave / RW == w && lane < GW) {
+      float* row = rows + (wave % RW) * a.n;
 #pragma unroll
       for (int q = 0; q < Q; ++q)
 #pragma unroll
@@ -249,109 +298,169 @@ __global__ __launch_bounds__(kThreads) void k_balance_items(BalanceArgs a) {
           const int c = (q * GW + l) * 4 + j;
           if (c < a.n) row[c] = w ? row[c] + p[q][j] : p[q][j];
         }
+    }
     __syncthreads();
   }
-  for (int c = tid; c < a.n; c += kThreads) {
-    a.psum[item * a.n + c] = row[c];
-    a.hist[item * a.n + c] = hist[c];
+  double dot = 0;
+  for (int c = tid; c < a.n; c += kWave * W) {
+    float v = rows[c];
+#pragma unroll
+    for (int r = 1; r < RW; ++r) v += rows[r * a.n + c];
+    if constexpr (ALONE) {
+      a.counts[c] = hist[c];
+      dot += (double)v * hist[c];
+    } else {
+      a.psum[item * a.pitch + c] = v;
+      a.hist[item * a.pitch + c] = hist[c];
+    }
   }
+  if constexpr (ALONE) dot = block_sum<W>(dot, red);
   if (tid == 0) {
-    float v = 0.f;
+    double v = 0;
     int k = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < W; ++w) {
       v += zs[w];
       k += ns[w];
     }
-    a.zsum[item] = v;
-    a.ntok[item] = k;
+    if constexpr (ALONE) {
+      a.seq_tokens[0] = a.seq_tokens[1] = k;
+      *a.loss = k ? (float)(dot * a.n / ((double)a.K * k * k)) : 0.f;
+      *a.z_loss = k ? (float)(v / k) : 0.f;
+    } else {
+      a.zsum[item] = (float)v;
+      a.ntok[item] = k;
+    }
   }
 }
 
-__device__ __forceinline__ double block_sum(double v, double* red) {
-  const int tid = threadIdx.x;
+// Sums of three values over a workgroup's waves, in every lane of the first.
+template <int W>
+__device__ __forceinline__ void block_sum3(double& x, double& y, double& z, double (*red)[3]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
+  for (int o = 32; o >= 1; o >>= 1) {
+    x += __shfl_xor(x, o, kWave);
+    y += __shfl_xor(y, o, kWave);
+    z += __shfl_xor(z, o, kWave);
+  }
+  if (lane == 0) {
+    red[wave][0] = x;
+    red[wave][1] = y;
+    red[wave][2] = z;
+  }
   __syncthreads();
-  if ((tid & 63) == 0) red[tid >> 6] = v;
-  __syncthreads();
-  double r = 0;
+  x = y = z = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) r += red[w];
-  return r;
+  for (int w = 0; w < W; ++w) {
+    x += red[w][0];
+    y += red[w][1];
+    z += red[w][2];
+  }
 }
 
-// One workgroup for a sequence and 64 columns: four rows of threads share the
-// sequence's items.
-__global__ __launch_bounds__(kThreads) void k_balance_join(BalanceArgs a) {
-  __shared__ double dsum[kWaves][kWave];
-  __shared__ int csum[kWaves][kWave];
-  __shared__ double red[kWaves];
+template <typename T>
+__device__ __forceinline__ void put(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ __forceinline__ T get(T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// One workgroup for a sequence and 64 columns: 16 lanes hold four columns each, and
+// the 64 groups of them share the sequence's items, eight loads in flight.
+constexpr int kJoinWaves = 16;
+__global__ __launch_bounds__(kWave * kJoinWaves) void k_balance_join(BalanceArgs a) {
+  constexpr int W = kJoinWaves, kRows = W * 4;
+  __shared__ double dsum[W][kWave];
+  __shared__ int csum[W][kWave];
+  __shared__ double red[W][3];
   __shared__ bool last;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int blocks = (a.n + 63) / 64;
-  const int s = blockIdx.x / blocks, cb = blockIdx.x % blocks, c = cb * 64 + lane;
+  const int s = blockIdx.x / blocks, cb = blockIdx.x % blocks;
   const int64_t lo = off_at(a, s), hi = off_at(a, s + 1);
   const int64_t i0 = lo / a.C + s;
   int64_t i1 = hi > lo ? i0 + (hi - lo + a.C - 1) / a.C : i0;
   if (i1 > a.slots) i1 = a.slots;
-  double p = 0;
-  int k = 0;
-  if (c < a.n)
+  double p[4] = {0, 0, 0, 0}, z = 0, nt = 0;
+  int k[4] = {0, 0, 0, 0};
+  const int c4 = cb * 64 + (lane & 15) * 4;
+  if (c4 < a.n)
 #pragma unroll 4
-    for (int64_t i = i0 + wave; i < i1; i += kWaves) {
-      p += a.psum[i * a.n + c];
-      k += a.hist[i * a.n + c];
+    for (int64_t i = i0 + wave * 4 + (lane >> 4); i < i1; i += kRows) {
+      const float4 f = *reinterpret_cast<const float4*>(a.psum + i * a.pitch + c4);
+      const int4 h = *reinterpret_cast<const int4*>(a.hist + i * a.pitch + c4);
+      p[0] += f.x; p[1] += f.y; p[2] += f.z; p[3] += f.w;
+      k[0] += h.x; k[1] += h.y; k[2] += h.z; k[3] += h.w;
     }
-  dsum[wave][lane] = p;
-  csum[wave][lane] = k;
-  double z = 0, nt = 0;
   if (cb == 0)
-    for (int64_t i = i0 + tid; i < i1; i += kThreads) {
+    for (int64_t i = i0 + tid; i < i1; i += kWave * W) {
       z += a.zsum[i];
       nt += a.ntok[i];
     }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+#pragma unroll
+    for (int o = 16; o < kWave; o <<= 1) {
+      p[j] += __shfl_xor(p[j], o, kWave);
+      k[j] += __shfl_xor(k[j], o, kWave);
+    }
+    if (lane < 16) {
+      dsum[wave][lane * 4 + j] = p[j];
+      csum[wave][lane * 4 + j] = k[j];
+    }
+  }
   __syncthreads();
   double dot = 0;
-  if (wave == 0) {
+  const int c = cb * 64 + lane;
+  if (wave == 0 && c < a.n) {
+    double ps = 0;
+    int ks = 0;
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
-      p += dsum[w][lane];
-      k += csum[w][lane];
+    for (int w = 0; w < W; ++w) {
+      ps += dsum[w][lane];
+      ks += csum[w][lane];
     }
-    if (c < a.n) a.counts[(int64_t)s * a.n + c] = k;
-    dot = p * k;
+    a.counts[(int64_t)s * a.n + c] = ks;
+    dot = ps * ks;
   }
-  dot = block_sum(dot, red);
-  if (cb == 0) {
-    z = block_sum(z, red);
-    nt = block_sum(nt, red);
+  block_sum3<W>(dot, z, nt, red);
+  if (gridDim.x == 1) {
+    if (tid == 0) {
+      a.seq_tokens[0] = a.seq_tokens[1] = (int32_t)nt;
+      *a.loss = nt > 0 ? (float)(dot * a.n / (a.K * nt * nt)) : 0.f;
+      *a.z_loss = nt > 0 ? (float)(z / nt) : 0.f;
+    }
+    return;
   }
+  // What the last workgroup reads goes to memory and back as device-scope atomics,
+  // which no L2 holds back, waited for before the ticket: a fence would write back and
+  // drop whole L2s (13 us for this kernel in place of 8).
   if (tid == 0) {
-    a.dots[blockIdx.x] = dot;
+    put(&a.dots[blockIdx.x], dot);
     if (cb == 0) {
-      a.zseq[s] = z;
-      a.seq_tokens[s] = (int32_t)nt;
+      put(&a.zseq[s], z);
+      put(&a.seq_tokens[s], (int32_t)nt);
     }
-    __threadfence();
-    last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
-  __threadfence();
   double N = 0, loss = 0;
   z = 0;
-  for (int i = tid; i < a.S; i += kThreads) {
-    const int m = a.seq_tokens[i];
+  for (int i = tid; i < a.S; i += kWave * W) {
+    const int m = get(&a.seq_tokens[i]);
     double d = 0;
-    for (int b = 0; b < blocks; ++b) d += a.dots[(int64_t)i * blocks + b];
+#pragma unroll 4
+    for (int b = 0; b < blocks; ++b) d += get(&a.dots[(int64_t)i * blocks + b]);
     if (m > 0) loss += d / m;
     N += m;
-    z += a.zseq[i];
+    z += get(&a.zseq[i]);
   }
-  N = block_sum(N, red);
-  loss = block_sum(loss, red);
-  z = block_sum(z, red);
+  block_sum3<W>(N, loss, z, red);
   if (tid == 0) {
     a.seq_tokens[a.S] = (int32_t)N;
     *a.loss = N > 0 ? (float)(loss * a.n / (a.K * N)) : 0.f;
@@ -389,33 +498,37 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
   int s = a.off ? find_last(a.S, t0, [&](int i) { return off_at(a, i); }) : 0;
   int64_t s0 = off_at(a, s), s1 = off_at(a, s + 1);
   float f[Q][4], share = 0.f;
-  int held = -1;
+  auto hold = [&]() {
+    const int m = a.seq_tokens[s];
+    share = m > 0 ? gb / (float)m : 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = (q * GW + l) * 4 + j;
+        f[q][j] = c < a.n ? (float)a.counts[(int64_t)s * a.n + c] : 0.f;
+      }
+  };
+  hold();
+  int held = s;
+  float v[Q][4], next[Q][4];
+  if constexpr (kAhead<Q>) load_row<In, VEC, GW, Q>(a, t0 + wave * G + lane / GW, t1, next);
   for (int64_t b = t0 + wave * G; b < t1; b += kWaves * G) {
     const int64_t t = b + lane / GW;
     const bool in = t < t1;
-    float v[Q][4];
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-      if (in) load4<In, VEC>(a, t, (q * GW + l) * 4, v[q]);
-      else v[q][0] = v[q][1] = v[q][2] = v[q][3] = -INFINITY;
+    if constexpr (!kAhead<Q>) load_row<In, VEC, GW, Q>(a, t, t1, next);
+    take_row<Q>(next, v);
+    if constexpr (kAhead<Q>) load_row<In, VEC, GW, Q>(a, t + kWaves * G, t1, next);
     while (t >= s1 && s + 1 < a.S) {
       ++s;
       s0 = off_at(a, s);
       s1 = off_at(a, s + 1);
     }
     const bool inside = in && t >= s0 && t < s1;
-    const bool on = token_on<GW, false>(a, t, inside, nullptr);
+    const bool on = token_on<GW>(a, t, inside);
     if (on && held != s) {
       held = s;
-      const int m = a.seq_tokens[s];
-      share = m > 0 ? gb / (float)m : 0.f;
-#pragma unroll
-      for (int q = 0; q < Q; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = (q * GW + l) * 4 + j;
-          f[q][j] = c < a.n ? (float)a.counts[(int64_t)s * a.n + c] : 0.f;
-        }
+      hold();
     }
     float m, total;
     row_exp<GW, Q>(v, m, total);
@@ -442,17 +555,22 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
   }
 }
 
-// Tokens that a workgroup takes at a time: kWaves waves of 64/GW tokens.
+// Tokens that a workgroup of `waves` takes at a time.
 inline int group_lanes(int64_t n) { return n <= 16 ? 4 : (n <= 64 ? 16 : (n <= 128 ? 32 : 64)); }
-inline int step_tokens(int64_t n) { return kWaves * kWave / group_lanes(n); }
+inline int step_tokens(int64_t n, int waves) { return waves * kWave / group_lanes(n); }
 
-// Tokens of an item: whole steps, about kItems items of a batch.
-constexpr int64_t kItems = 512;
+// Tokens of an item: whole steps, at most kItems items of a batch, so that with some
+// sequences' last items all of them (three workgroups of eight waves on a CU, 768)
+// are resident at once.
+constexpr int64_t kItems = 700;
 inline int64_t item_tokens(int64_t T, int64_t n) {
-  const int64_t step = step_tokens(n);
+  const int64_t step = step_tokens(n, n <= 1024 ? kItemWaves<4> : kItemWaves<8>);
   const int64_t per = (T + kItems - 1) / kItems;
-  return (per + step - 1) / step * step + (per == 0 ? step : 0);
+  return per ? (per + step - 1) / step * step : step;
 }
+
+// One workgroup does a small batch without sequences in one launch.
+inline bool alone(int64_t T, int64_t n, int64_t num_seqs) { return num_seqs == 0 && T * n <= 32768; }
 
 struct Layout {
   int64_t slots, psum, hist, zsum, ntok, dots, zseq, ticket, bytes;
@@ -466,8 +584,9 @@ Layout layout_of(int64_t T, int64_t n, int64_t S) {
     at += (bytes + 255) / 256 * 256;
     return p;
   };
-  w.psum = take(w.slots * n * 4);
-  w.hist = take(w.slots * n * 4);
+  const int64_t pitch = (n + 3) / 4 * 4;
+  w.psum = take(w.slots * pitch * 4);
+  w.hist = take(w.slots * pitch * 4);
   w.zsum = take(w.slots * 4);
   w.ntok = take(w.slots * 4);
   w.dots = take(S * ((n + 63) / 64) * 8);
@@ -502,10 +621,13 @@ void launch_gq(int64_t n, Fn f) {
 struct LaunchItems {
   const BalanceArgs& a;
   hipStream_t strm;
+  bool one;
   template <typename In, bool VEC, int GW, int Q>
   void operator()() const {
-    hipLaunchKernelGGL((k_balance_items<In, VEC, GW, Q>), dim3((unsigned)a.slots), dim3(kThreads),
-                       2 * a.n * 4, strm, a);
+    const dim3 block(kWave * kItemWaves<Q>);
+    const unsigned lds = (kSumRows<Q> + 1) * a.n * 4;
+    if (one) hipLaunchKernelGGL((k_balance_items<In, VEC, GW, Q, true>), dim3(1), block, lds, strm, a);
+    else hipLaunchKernelGGL((k_balance_items<In, VEC, GW, Q, false>), dim3((unsigned)a.slots), block, lds, strm, a);
   }
 };
 struct LaunchBwd {
@@ -561,7 +683,8 @@ extern "C" moe_status moe_balance_fwd(int64_t T, int64_t n_ids, int32_t K, int64
   const Layout w = layout_of(T, n_ids, S);
   if (!workspace || ws_bytes < (size_t)w.bytes) return MOE_ERR_WORKSPACE;
   const int64_t blocks = S * ((n_ids + 63) / 64);
-  if (w.slots > 0xffffff || blocks > 0xffffff) return MOE_ERR_BAD_SHAPE;  // 2^32 threads of a launch
+  if (w.slots > 0x3fffff || blocks > 0x3fffff) return MOE_ERR_BAD_SHAPE;  // 2^32 threads of a launch
+  const bool one = alone(T, n_ids, num_seqs);
   char* ws = static_cast<char*>(workspace);
   BalanceArgs a{};
   a.logits = logits;
@@ -575,6 +698,7 @@ extern "C" moe_status moe_balance_fwd(int64_t T, int64_t n_ids, int32_t K, int64
   a.S = (int)S;
   a.mask_ndim = mask_ndim;
   a.C = (int)item_tokens(T, n_ids);
+  a.pitch = (int)((n_ids + 3) / 4 * 4);
   a.psum = reinterpret_cast<float*>(ws + w.psum);
   a.hist = reinterpret_cast<int32_t*>(ws + w.hist);
   a.zsum = reinterpret_cast<float*>(ws + w.zsum);
@@ -586,10 +710,10 @@ extern "C" moe_status moe_balance_fwd(int64_t T, int64_t n_ids, int32_t K, int64
   a.z_loss = z_loss;
   a.counts = counts;
   a.seq_tokens = seq_tokens;
-  launch_any(a, dtype, rows_aligned(logits, n_ids, dtype), LaunchItems{a, as_stream(stream)});
+  launch_any(a, dtype, rows_aligned(logits, n_ids, dtype), LaunchItems{a, as_stream(stream), one});
   const moe_status first = launch_status();
-  if (first != MOE_OK) return first;
-  hipLaunchKernelGGL(k_balance_join, dim3((unsigned)blocks), dim3(kThreads), 0, as_stream(stream), a);
+  if (first != MOE_OK || one) return first;
+  hipLaunchKernelGGL(k_balance_join, dim3((unsigned)blocks), dim3(kWave * kJoinWaves), 0, as_stream(stream), a);
   return launch_status();
 }
 
@@ -614,7 +738,7 @@ extern "C" moe_status moe_balance_bwd(int64_t T, int64_t n_ids, int32_t K, int64
   a.S = num_seqs ? (int)num_seqs : 1;
   a.mask_ndim = mask_ndim;
   // runs of tokens: enough workgroups for every CU, whole steps each
-  const int64_t step = step_tokens(n_ids), per = (T + 2047) / 2048;
+  const int64_t step = step_tokens(n_ids, kWaves), per = (T + 2047) / 2048;
   a.C = (int)((per + step - 1) / step * step);
   a.counts = const_cast<int32_t*>(counts);
   a.seq_tokens = const_cast<int32_t*>(seq_tokens);

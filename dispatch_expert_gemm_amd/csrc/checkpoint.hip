@@ -27,13 +27,11 @@ constexpr int kThreads = 256;
 // two bf16 numbers.  One Newton step makes v_rcp_f32's result the rounded
 // reciprocal (tested for every scale).
 __device__ __forceinline__ uint32_t kept_scale(uint32_t amax16, float& inv) {
-  inv = 0.f;
-  if (amax16 >= 0x7f80u) return 0x7fc0u;
-  const uint32_t s = f2bf(__fmul_rn(bf2f(amax16), 1.0f / 127.0f));
-  if (s < 0x0080u) return 0u;
+  const uint32_t s = pk_bf16(__fmul_rn(bf2f(amax16), 1.0f / 127.0f), 0.f);
   const float sf = bf2f(s), r = __builtin_amdgcn_rcpf(sf);
-  inv = __fmaf_rn(__fmaf_rn(-sf, r, 1.0f), r, r);
-  return s;
+  const bool some = s >= 0x0080u && amax16 < 0x7f80u;
+  inv = some ? __fmaf_rn(__fmaf_rn(-sf, r, 1.0f), r, r) : 0.f;
+  return amax16 >= 0x7f80u ? 0x7fc0u : (some ? s : 0u);
 }
 
 __device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
@@ -71,8 +69,9 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
 __device__ __forceinline__ uint2 codes8(const uint4& v, float inv) {
   float f[8];
   unpack8(v, f);
-  if (inv == 0.f) return make_uint2(0u, 0u);  // zeros, or an infinity or a NaN among them
-  return make_uint2(codes4(f[0], f[1], f[2], f[3], inv), codes4(f[4], f[5], f[6], f[7], inv));
+  const uint32_t lo = codes4(f[0], f[1], f[2], f[3], inv), hi = codes4(f[4], f[5], f[6], f[7], inv);
+  // inv 0: zeros, or an infinity or a NaN among them (whose products are none)
+  return inv == 0.f ? make_uint2(0u, 0u) : make_uint2(lo, hi);
 }
 
 // Eight kept values: code * s, exact in fp32.
@@ -260,9 +259,10 @@ struct KeptArgs {
   int64_t nb;
 };
 
-// Combine that keeps its rows: one wave per token and column part, as k_combine;
-// out is bit for bit k_combine's.
-template <int KMAX>
+// Combine that keeps its rows: one wave for a token and a 64-vector column block
+// (every split-th block), its routed rows' loads issued together; out is bit for
+// bit k_combine's.  SPECIAL: copy or constant experts may be among the slots.
+template <int KMAX, bool SPECIAL>
 __global__ __launch_bounds__(kThreads) void k_combine_keep(CombineArgs a, KeptArgs q) {
 #pragma clang fp contract(off)
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
@@ -273,57 +273,49 @@ __global__ __launch_bounds__(kThreads) void k_combine_keep(CombineArgs a, KeptAr
   SlotInfo<KMAX> si;
   load_slots(a.slot2row, a.w, t, a.K, lane, si);
   const int64_t Hv = a.Hv;
-  constexpr int U = kChunk<KMAX>;
-  const int64_t vs = (int64_t)a.split * kWave;
-  for (int64_t b0 = part * kWave; b0 < Hv; b0 += U * vs) {  // (the whole wave: blocks span lanes)
-    uint4 raw[U][KMAX], sh[U];
+  for (int64_t b = part * kWave; b < Hv; b += (int64_t)a.split * kWave) {  // (the whole wave: blocks span lanes)
+    const int64_t v = b + lane;
+    const bool in = v < Hv;
+    uint4 raw[KMAX], sh = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t v = b0 + u * vs + lane;
-#pragma unroll
-      for (int k = 0; k < KMAX; ++k)
-        if (si.code[k] >= 0) {
-          raw[u][k] = make_uint4(0u, 0u, 0u, 0u);
-          if (v < Hv) raw[u][k] = ld_row(&a.y[(int64_t)si.code[k] * Hv + v]);
-        }
-      if (a.shared && v < Hv) sh[u] = a.shared[t * Hv + v];
+    for (int k = 0; k < KMAX; ++k) {
+      raw[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (si.code[k] >= 0 && in) raw[k] = ld_row(&a.y[(int64_t)si.code[k] * Hv + v]);
     }
+    if (a.shared && in) sh = a.shared[t * Hv + v];
+    float ox[8], acc[8];
+    if (SPECIAL && si.any_ori && in) unpack8(a.ori[t * Hv + v], ox);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t v = b0 + u * vs + lane;
-      float ox[8], acc[8];
-      if (si.any_ori && v < Hv) unpack8(a.ori[t * Hv + v], ox);
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KMAX; ++k) {
-        const int c = si.code[k];
-        if (c == MOE_SLOT_NONE) continue;
-        float f[8];
-        if (c >= 0) {
-          float inv;
-          const uint32_t s = kept_scale(block_amax(raw[u][k]), inv);
-          if (v < Hv) {
-            q.codes[(int64_t)c * Hv + v] = codes8(raw[u][k], inv);
-            if ((lane & 3) == 0) q.scales[(int64_t)c * q.nb + v / 4] = (uint16_t)s;
-          }
-          unpack8(raw[u][k], f);
-        } else if (v < Hv) {
-          special_value(c, ox, a.a1, a.a2, a.cv, Hv, v, f);
+    for (int k = 0; k < KMAX; ++k) {
+      const int c = si.code[k];
+      if (SPECIAL ? c == MOE_SLOT_NONE : c < 0) continue;
+      float f[8];
+      if (!SPECIAL || c >= 0) {
+        float inv;
+        const uint32_t s = kept_scale(block_amax(raw[k]), inv);
+        const uint2 codes = codes8(raw[k], inv);
+        if (in) {
+          q.codes[(int64_t)c * Hv + v] = codes;
+          if ((lane & 3) == 0) q.scales[(int64_t)c * q.nb + v / 4] = (uint16_t)s;
         }
-        const float wk = si.w[k];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = acc[i] + wk * f[i];
+        unpack8(raw[k], f);
+      } else if (in) {
+        special_value(c, ox, a.a1, a.a2, a.cv, Hv, v, f);
       }
-      if (v < Hv) {
-        if (a.shared) {
-          float sv[8];
-          unpack8(sh[u], sv);
+      const float wk = si.w[k];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] = acc[i] + sv[i];
-        }
-        a.out[t * Hv + v] = pack8(acc);
+      for (int i = 0; i < 8; ++i) acc[i] = acc[i] + wk * f[i];
+    }
+    if (in) {
+      if (a.shared) {
+        float sv[8];
+        unpack8(sh, sv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = acc[i] + sv[i];
       }
+      a.out[t * Hv + v] = pack8(acc);
     }
   }
 }
@@ -344,68 +336,86 @@ struct KeptBwdArgs {
   int K;
 };
 
-// The routing weights' gradient from kept rows: one wave per token.
-template <int KMAX>
+// The routing weights' gradient from kept rows: W waves per token (1 or 4), each
+// every W-th 64-vector column block, their sums joined in order.
+template <int KMAX, bool SPECIAL, int W>
 __global__ __launch_bounds__(kThreads) void k_combine_kept_bwd(KeptBwdArgs a) {
+  constexpr int kTokens = kThreads / kWave / W;
+  __shared__ float sums[kThreads / kWave][KMAX];
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / kWave) + wave;
-  if (t >= a.T) return;
+  const int part = W == 1 ? 0 : wave;
+  const int64_t t = (int64_t)blockIdx.x * kTokens + (W == 1 ? wave : 0);
+  if (t >= a.T) return;  // (with W = 4 the whole workgroup)
   SlotInfo<KMAX> si;
   load_slots(a.slot2row, a.w, t, a.K, lane, si);
-  if (a.roww)
+  if (a.roww && part == 0)
 #pragma unroll
     for (int k = 0; k < KMAX; ++k)
       if (lane == k && si.code[k] >= 0) a.roww[si.code[k]] = si.w[k];
   const int64_t Hv = a.Hv;
-  constexpr int U = kChunk<KMAX>;
   float dot[KMAX];
 #pragma unroll
   for (int k = 0; k < KMAX; ++k) dot[k] = 0.f;
-  for (int64_t v0 = lane; v0 < Hv; v0 += U * kWave) {
-    uint2 raw[U][KMAX];
-    uint32_t sc[U][KMAX];
-    uint4 dr[U];
+  for (int64_t v = part * kWave + lane; v < Hv; v += W * kWave) {
+    uint2 raw[KMAX];
+    uint32_t sc[KMAX];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t v = v0 + u * kWave;
-      if (v < Hv) {
-        dr[u] = a.dout[t * Hv + v];
-#pragma unroll
-        for (int k = 0; k < KMAX; ++k)
-          if (si.code[k] >= 0) {
-            raw[u][k] = a.codes[(int64_t)si.code[k] * Hv + v];
-            sc[u][k] = a.scales[(int64_t)si.code[k] * a.nb + v / 4];
-          }
+    for (int k = 0; k < KMAX; ++k)
+      if (si.code[k] >= 0) {
+        raw[k] = a.codes[(int64_t)si.code[k] * Hv + v];
+        sc[k] = a.scales[(int64_t)si.code[k] * a.nb + v / 4];
       }
-    }
+    float d[8];
+    unpack8(a.dout[t * Hv + v], d);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t v = v0 + u * kWave;
-      if (v < Hv) {
-        float d[8], ox[8];
-        unpack8(dr[u], d);
-        if (si.any_ori) unpack8(a.ori[t * Hv + v], ox);
+    for (int k = 0; k < KMAX; ++k) {
+      if (si.code[k] < 0) continue;
+      // sum of code * d, then the scale: the eight codes share one
+      float p = 0.f;
 #pragma unroll
-        for (int k = 0; k < KMAX; ++k) {
-          const int c = si.code[k];
-          if (c == MOE_SLOT_NONE) continue;
-          float f[8];
-          if (c >= 0) kept8(raw[u][k], bf2f(sc[u][k]), f);
-          else special_value(c, ox, a.a1, a.a2, a.cv, Hv, v, f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dot[k] = __fmaf_rn(f[i], d[i], dot[k]);
-        }
-      }
+      for (int i = 0; i < 8; ++i)
+        p = __fmaf_rn((float)(int8_t)((i < 4 ? raw[k].x : raw[k].y) >> (8 * (i & 3))), d[i], p);
+      dot[k] = __fmaf_rn(p, bf2f(sc[k]), dot[k]);
     }
   }
+  auto leave = [&](int k, float p) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) p += __shfl_xor(p, o, kWave);
+    if (lane == 0) {
+      if constexpr (W == 1) a.dw[t * a.K + k] = p;
+      else sums[wave][k] = p;
+    }
+  };
 #pragma unroll
   for (int k = 0; k < KMAX; ++k)
-    if (k < a.K) {
-      float p = dot[k];
+    if (k < a.K && (!SPECIAL || si.code[k] > MOE_SLOT_COPY)) leave(k, dot[k]);
+  // copy and constant slots one after the other: among the routed ones they would
+  // double the registers of the loop above (wide rows 68 -> 88 us)
+  if (SPECIAL && si.any_ori)
+    for (int k = 0; k < a.K; ++k) {
+      const int c = __builtin_amdgcn_readfirstlane(a.slot2row[t * a.K + k]);
+      if (c > MOE_SLOT_COPY) continue;
+      float p = 0.f;
+      for (int64_t v = part * kWave + lane; v < Hv; v += W * kWave) {
+        float d[8], ox[8], f[8];
+        unpack8(a.dout[t * Hv + v], d);
+        unpack8(a.ori[t * Hv + v], ox);
+        special_value(c, ox, a.a1, a.a2, a.cv, Hv, v, f);
 #pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) p += __shfl_xor(p, o, kWave);
-      if (lane == 0) a.dw[t * a.K + k] = si.code[k] == MOE_SLOT_NONE ? 0.f : p;
+        for (int i = 0; i < 8; ++i) p = __fmaf_rn(f[i], d[i], p);
+      }
+      leave(k, p);
     }
+  if constexpr (W > 1) {
+    __syncthreads();
+    const int k = threadIdx.x;
+    if (k < a.K) {
+      float p = sums[0][k];
+#pragma unroll
+      for (int w = 1; w < W; ++w) p += sums[w][k];
+      a.dw[t * a.K + k] = p;
+    }
+  }
 }
 
 template <typename Fn>
@@ -450,16 +460,10 @@ moe_status launch_swiglu(SwigluArgs a, void* stream) {
   return launch_status();
 }
 
-// Waves per token: as the plain combine's (combine.hip), for equal results in
-// equal time; sums run over k, so the split changes no bit.
-inline int keep_split(int64_t Hv, int K) {
-  if (K >= 4 && Hv % kWave == 0) {
-    const int km = K <= 4 ? 4 : (K <= 8 ? 8 : 16);
-    const int64_t u = km >= 16 ? 1 : 16 / km;
-    const int64_t blocks = Hv / kWave;
-    if (blocks % u == 0 && blocks / u >= 4 && blocks / u <= 16) return (int)(blocks / u);
-  }
-  return token_split(Hv, K);
+// Waves per token: one for each 64-vector column block, up to 16.
+inline int keep_split(int64_t Hv) {
+  const int64_t blocks = (Hv + kWave - 1) / kWave;
+  return (int)(blocks < 16 ? blocks : 16);
 }
 
 }  // namespace
@@ -554,12 +558,16 @@ extern "C" moe_status moe_combine_checkpoint(const moe_shape* s, const void* y, 
                       s->K,
                       s->H / 8,
                       0,
-                      keep_split(s->H / 8, s->K)};
+                      keep_split(s->H / 8)};
   const KeptArgs q{reinterpret_cast<uint2*>(y_codes), static_cast<uint16_t*>(y_scales), (s->H + kCols - 1) / kCols};
   const int64_t waves = s->T * a.split;
   launch_k(s->K, [&](auto km) {
-    hipLaunchKernelGGL(k_combine_keep<decltype(km)::value>, dim3((unsigned)((waves + 3) / 4)), dim3(kThreads), 0,
-                       as_stream(stream), a, q);
+    constexpr int KM = decltype(km)::value;
+    const dim3 grid((unsigned)((waves + 3) / 4));
+    if (s->copy_expert_num + s->const_expert_num > 0)
+      hipLaunchKernelGGL((k_combine_keep<KM, true>), grid, dim3(kThreads), 0, as_stream(stream), a, q);
+    else
+      hipLaunchKernelGGL((k_combine_keep<KM, false>), grid, dim3(kThreads), 0, as_stream(stream), a, q);
   });
   return launch_status();
 }
@@ -599,8 +607,20 @@ extern "C" moe_status moe_combine_bwd_weights_checkpoint(
                       (s->H + kCols - 1) / kCols,
                       s->K};
   launch_k(s->K, [&](auto km) {
-    hipLaunchKernelGGL(k_combine_kept_bwd<decltype(km)::value>, dim3((unsigned)((s->T + 3) / 4)), dim3(kThreads), 0,
-                       as_stream(stream), a);
+    constexpr int KM = decltype(km)::value;
+    auto go = [&](auto kernel, int64_t blocks) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, as_stream(stream), a);
+    };
+    const bool special = s->copy_expert_num + s->const_expert_num > 0;
+    // four waves for a row of four 64-vector blocks or more: 4096 tokens of 7168
+    // columns 69 us against 75 with two (and 92 with one)
+    if (a.Hv >= 256) {
+      if (special) go(k_combine_kept_bwd<KM, true, 4>, s->T);
+      else go(k_combine_kept_bwd<KM, false, 4>, s->T);
+    } else {
+      if (special) go(k_combine_kept_bwd<KM, true, 1>, (s->T + 3) / 4);
+      else go(k_combine_kept_bwd<KM, false, 1>, (s->T + 3) / 4);
+    }
   });
   return launch_status();
 }

@@ -871,7 +871,7 @@ moe_status moe_linear_int8_dynamic(int64_t M, int64_t N, int64_t K, const void* 
  * that holds nothing above -inf adds nothing to either sum and has gradient 0; a
  * +inf logit makes the losses NaN.
  * Sizes: 0 <= T < 2^31, 1 <= n_ids <= 4096, 0 < K <= min(16, n_ids), T K < 2^31, num_seqs 0 (no
- * seq_offsets) to 2^20, num_seqs * ceil(n_ids / 64) < 2^24 (else MOE_ERR_BAD_SHAPE); dtype of the
+ * seq_offsets) to 2^20, num_seqs * ceil(n_ids / 64) < 2^22 (else MOE_ERR_BAD_SHAPE); dtype of the
  * logits and their gradient MOE_DTYPE_FP32 or MOE_DTYPE_BF16, mask_ndim 0, 1, 2
  * (else MOE_ERR_BAD_RANGE).  seq_offsets are data: they are clamped to [0, T], and
  * where they decrease the results are unspecified, with every access in bounds.
@@ -879,7 +879,7 @@ moe_status moe_linear_int8_dynamic(int64_t M, int64_t N, int64_t K, const void* 
  */
 moe_status moe_balance_workspace_size(int64_t T, int64_t n_ids, int64_t num_seqs, size_t* bytes);
 
-/* moe_balance_fwd - two launches.
+/* moe_balance_fwd - two launches, one for up to 32768 logits without seq_offsets.
  *  in   logits (T, n_ids); topk_idx (T, K) int32; x_active_mask (T,) or (T, K) or
  *       NULL with mask_ndim 0; seq_offsets (num_seqs + 1) int32 or NULL with num_seqs 0
  *  out  loss, z_loss: one fp32 each; counts (max(num_seqs, 1), n_ids) int32: c;

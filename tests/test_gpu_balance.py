@@ -278,3 +278,62 @@ def test_large_batch():
     assert abs(float(z) - float(small[1])) < 1e-4 * float(z)
     part = grad[-1000:] * 140
     assert float((part - small[3]).abs().max()) < 1e-4 * float(small[3].abs().max())
+
+
+def test_differentiable_once():
+    """A second derivative raises; a step that merely builds the graph of its first does not."""
+    l, idx = _inputs(20, 16, 2, 1)
+    x = l.clone().requires_grad_()
+    loss, z, _ = dm.balance_loss(x, idx)
+    g, = torch.autograd.grad(loss + z, x, create_graph=True)
+    assert torch.equal(g.detach(), _run(l, idx, g=1.0, gz=1.0)[3])
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        g.square().sum().backward()
+
+
+def test_without_gradients():
+    l, idx = _inputs(20, 16, 2, 1)
+    loss, z, counts = dm.balance_loss(l, idx)
+    assert not loss.requires_grad and not z.requires_grad
+    with torch.no_grad():
+        assert not dm.balance_loss(l.clone().requires_grad_(), idx)[0].requires_grad
+    x = l.clone().requires_grad_()
+    loss, z, counts = dm.balance_loss(x, idx)
+    assert loss.requires_grad and z.requires_grad and not counts.requires_grad
+    main = x.sum()
+    main += 0.01 * loss + 1e-3 * z  # as a training loop adds them
+    main.backward()
+    assert x.grad.shape == x.shape
+
+
+@pytest.mark.parametrize("change,match", [
+    (dict(logits=lambda l: l.half()), "logits must be float32 or bfloat16"), (dict(logits=lambda l: l[0]), "logits must be"),
+    (dict(idx=lambda i: i.long()), "topk_idx must be torch.int32"), (dict(idx=lambda i: i[:5]), "topk_idx must be a tensor"),
+    (dict(idx=lambda i: i.cpu()), "topk_idx must be a GPU tensor"), (dict(idx=lambda i: i.t().contiguous().t()), "contiguous"),
+    (dict(idx=lambda i: i.repeat(1, 9)), "status -2"), (dict(mask=torch.ones(19)), "x_active_mask must be a tensor"),
+    (dict(mask=torch.ones(20, 3)), "x_active_mask must be a tensor"), (dict(mask=torch.ones(20)), "uint8 or torch.bool"),
+    (dict(off=torch.zeros(1, dtype=torch.int32)), "seq_offsets must hold"), (dict(off=torch.zeros(3)), "seq_offsets must be"),
+    (dict(off=torch.zeros(2, 2, dtype=torch.int32)), "seq_offsets must hold")])
+def test_refusals(change, match):
+    l, idx = _inputs(20, 16, 2, 1)
+    l, idx = change.get("logits", lambda t: t)(l), change.get("idx", lambda t: t)(idx)
+    mask, off = (None if change.get(k) is None else change[k].to(DEV) for k in ("mask", "off"))
+    with pytest.raises(dm.MoeError, match=match):
+        dm.balance_loss(l, idx, x_active_mask=mask, seq_offsets=off)
+
+
+def test_entry_refusals():
+    """The C entries' Python forms: short buffers and other types."""
+    l, idx = _inputs(20, 16, 2, 1)
+    f = torch.empty(1, device=DEV)
+    i = torch.empty(64, dtype=torch.int32, device=DEV)
+    ws = torch.empty(dm.moe_balance_workspace_size(20, 16), dtype=torch.uint8, device=DEV)
+    for bad in (dict(counts=i[:15]), dict(seq_tokens=i[:1]), dict(workspace=ws[:100]), dict(loss=f.double()),
+                dict(topk_idx=idx[:10])):
+        a = dict(logits=l, topk_idx=idx, x_active_mask=None, seq_offsets=None, loss=f, z_loss=f, counts=i, seq_tokens=i,
+                 workspace=ws)
+        a.update(bad)
+        with pytest.raises(dm.MoeError):
+            dm.moe_balance_fwd(**a)
+    with pytest.raises(dm.MoeError, match="grad_logits"):
+        dm.moe_balance_bwd(l, 2, None, None, i, i, f, f, l[:10])

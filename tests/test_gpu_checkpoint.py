@@ -268,12 +268,12 @@ def test_swiglu_gradient_against_differences():
 
 
 def test_kept_memory_of_swiglu():
+    """1.0625 bytes a value of [G | U], and nothing else."""
     gu = gate_up(4096, 480, 1).to(DEV).requires_grad_()
-    torch.cuda.synchronize()
-    before = torch.cuda.memory_allocated()
-    h = dm.swiglu_checkpoint(gu)
-    held = torch.cuda.memory_allocated() - before - h.numel() * 2
-    assert held <= 4096 * 960 * 1.0625 + 4096
+    held = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: held.append(t.numel() * t.element_size()) or t, lambda t: t):
+        h = dm.swiglu_checkpoint(gu)
+    assert sum(held) == 4096 * 960 * 17 // 16
     del h
 
 
@@ -306,6 +306,34 @@ def test_swiglu_streams_and_captured():
         torch.cuda.synchronize()
         for a, b in zip(outs, eager):
             same(a, b)
+
+
+def test_swiglu_differentiable_once():
+    x = gate_up(6, 32, 1).to(DEV).requires_grad_()
+    g, = torch.autograd.grad(dm.swiglu_checkpoint(x).float().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        g.float().square().sum().backward()
+    with torch.no_grad():
+        assert not dm.swiglu_checkpoint(x).requires_grad
+
+
+def test_swiglu_refusals():
+    x = gate_up(6, 32, 1).to(DEV)
+    for bad, match in ((x.float(), "gate_up must be torch.bfloat16"), (x[:, :63], "shape"), (x[:, :0], "shape"),
+                       (x[0, 0], "shape")):
+        with pytest.raises(dm.MoeError, match=match):
+            dm.swiglu_checkpoint(bad)
+    codes, scales = dm.checkpoint_buffers(6, 32, DEV, halves=2)
+    for f in (lambda: dm.moe_swiglu_checkpoint_fwd(x, None, codes[:5], scales),
+              lambda: dm.moe_swiglu_checkpoint_fwd(x, None, codes, scales[:5]),
+              lambda: dm.moe_swiglu_checkpoint_fwd(x, None, codes, scales.float()),
+              lambda: dm.moe_swiglu_checkpoint_fwd(x.t(), None, codes, scales),
+              lambda: dm.moe_swiglu_checkpoint_bwd(codes, scales, x[:, :32], x),
+              lambda: dm.moe_swiglu_checkpoint_bwd(codes, scales, x[:3, :32].contiguous(), x),
+              lambda: dm.moe_swiglu_checkpoint_restore(codes, scales, x[:5]),
+              lambda: dm.moe_swiglu_checkpoint_restore(codes, scales, x, nrows=torch.ones(1, device=DEV))):
+        with pytest.raises(dm.MoeError):
+            f()
 
 
 # ----------------------------------------------------------------------------- combine
