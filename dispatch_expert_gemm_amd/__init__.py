@@ -1042,6 +1042,22 @@ def shared_expert_shape(T, H, F) -> MoeShape:
     return make_shape(T, H, 1, 1, F=F, capacity=T)
 
 
+def _keep_gate_up(gate_up, nrows):
+    """(codes, scales) that stand for gate_up_save and h_act until the backward."""
+    kept = checkpoint_buffers(gate_up.shape[0], gate_up.shape[1] // 2, gate_up.device, halves=2)
+    moe_swiglu_checkpoint_fwd(gate_up, None, *kept, nrows=nrows)
+    return kept
+
+
+def _restore_gate_up(codes, scales, nrows):
+    """gate_up_save and h_act of kept rows."""
+    R, F2 = codes.shape
+    gate_up = torch.empty((R, F2), dtype=BF16, device=codes.device)
+    h = torch.empty((R, F2 // 2), dtype=BF16, device=codes.device)
+    moe_swiglu_checkpoint_restore(codes, scales, gate_up, h, nrows=nrows)
+    return gate_up, h
+
+
 class _MoELayerFn(torch.autograd.Function):
     """Forward: dispatch -> grouped SwiGLU FFN -> combine; backward: the reverse chain.
     In bf16 the dispatch permute is folded into the two GEMMs that read the
@@ -1057,13 +1073,17 @@ class _MoELayerFn(torch.autograd.Function):
     operands (weights quantised in 128 x 128 blocks at every forward,
     activations per (row, 128 columns)), the weight gradients in bf16, or with
     fp8_wgrad on e4m3 operands with one scale per (128 tokens of an expert,
-    column); the shared expert stays bf16.  comm_quant_mode 2: the int8 combine payload."""
+    column); the shared expert stays bf16.  comm_quant_mode 2: the int8 combine payload.
+
+    keep8 (bf16 path): gate_up_save is kept in 8 bits, h not at all (the backward
+    restores both) and the combine keeps y's rows in 8 bits, for the routing weights'
+    gradient alone."""
 
     @staticmethod
     def forward(ctx, x, topk_weights, w_gate, w_up, w_down, shared_expert_x, shared_w_gate,
                 shared_w_up, shared_w_down, topk_idx, x_active_mask, const_alpha_1, const_alpha_2,
                 const_v, zero_expert_num, copy_expert_num, const_expert_num, fp8, comm_quant_mode,
-                fp8_wgrad, mx):
+                fp8_wgrad, mx, keep8):
         T, H = x.shape
         K = topk_idx.shape[1]
         E, F, _ = w_gate.shape
@@ -1145,15 +1165,28 @@ class _MoELayerFn(torch.autograd.Function):
             moe_grouped_ffn(ss, x, shared_w_gate, shared_w_up, shared_w_down, s_counts, s_gus, s_h,
                             shared_expert_x)
             ctx.s_shape = ss
+            if keep8:
+                s_gus, s_h = _keep_gate_up(s_gus, None)
             s_saved = (shared_w_gate, shared_w_up, shared_w_down, s_counts, s_gus, s_h)
         out = torch.empty((T, H), dtype=BF16, device=dev)
-        moe_combine(shape, y, topk_idx, topk_weights, d.assist_info_for_combine, d.ep_recv_counts,
-                    mask, shared_expert_x, x, const_alpha_1, const_alpha_2, const_v, out)
+        combined = (shape, y, topk_idx, topk_weights, d.assist_info_for_combine, d.ep_recv_counts, mask,
+                    shared_expert_x, x, const_alpha_1, const_alpha_2, const_v, out)
+        y_scales = None
+        if keep8:
+            # from here on gus and h are the codes and scales of [G | U], y and y_scales y's
+            gus, h = _keep_gate_up(gus, d.ep_recv_counts[-1:])
+            y = None
+            if ctx.needs_input_grad[1]:
+                y, y_scales = checkpoint_buffers(cap, H, dev)
+                moe_combine_checkpoint(*combined, y, y_scales)
+        if y_scales is None:
+            moe_combine(*combined)
+        ctx.keep8 = bool(keep8)
         ctx.shape = shape
         ctx.has_shared_x = shared_expert_x is not None and not ctx.shared_ffn
         ctx.save_for_backward(x, topk_weights, w_gate, w_up, w_down, topk_idx, mask, const_alpha_1,
                               const_alpha_2, const_v, d.expand_x if fp8 else None, d.assist_info_for_combine,
-                              d.ep_recv_counts, gus, h, y, *s_saved)
+                              d.ep_recv_counts, gus, h, y, y_scales, *s_saved)
         # the transposed weight codes of the data-gradient GEMMs (not tensors
         # of the graph, so kept on ctx)
         ctx.wq = tuple((q.codes_t, q.scales_t) if ctx.mx else (q.codes_t, q.scales) for q in wq)
@@ -1163,8 +1196,10 @@ class _MoELayerFn(torch.autograd.Function):
     def backward(ctx, grad_out):
         saved = ctx.saved_tensors
         (x, topk_weights, w_gate, w_up, w_down, topk_idx, mask, a1, a2, cv, expand_x, assist,
-         recv, gus, h, y) = saved[:16]
+         recv, gus, h, y, y_scales) = saved[:17]
         shape = ctx.shape
+        if ctx.keep8:
+            gus, h = _restore_gate_up(gus, h, recv[-1:])
         grad_out = grad_out.contiguous()
         cap, H, F, T, K = shape.capacity, shape.H, shape.F, shape.T, shape.K
         dev = x.device
@@ -1175,21 +1210,26 @@ class _MoELayerFn(torch.autograd.Function):
         # and writes only grad_y or the row weights (the fp8 variant always writes both)
         need_gw = ctx.needs_input_grad[1] or ctx.fused8
         gw = torch.empty((T, K), dtype=F32, device=dev) if need_gw else None
+        routed = (topk_idx, topk_weights, assist, recv, mask, x, a1, a2, cv)
         if ctx.fused8:
             gyq = torch.empty((cap, H), dtype=U8T, device=dev)
             gys = torch.empty((H // 128, cap), dtype=F32T, device=dev)
-            moe_combine_bwd_fp8(shape, grad_out, y, topk_idx, topk_weights, assist, recv, mask, x, a1, a2, cv,
-                                gy, gyq, gys, gw)
+            moe_combine_bwd_fp8(shape, grad_out, y, *routed, gy, gyq, gys, gw)
         elif not ctx.fp8 and fold_combine_bwd(F):
             # bf16, narrow FFN: the combine backward folded into the down GEMMs
             # (grad_out rows read through the map, each row's routing weight
             # applied in the GEMM)
             roww = torch.empty((cap,), dtype=F32, device=dev)
-            moe_combine_bwd_weights(shape, grad_out, y if need_gw else None, topk_idx, topk_weights, assist, recv,
-                                    mask, x, a1, a2, cv, gw, roww)
+            if ctx.keep8 and need_gw:
+                moe_combine_bwd_weights_checkpoint(shape, grad_out, y, y_scales, *routed, gw, roww)
+            else:
+                moe_combine_bwd_weights(shape, grad_out, y if need_gw else None, *routed, gw, roww)
+        elif ctx.keep8:
+            moe_combine_bwd(shape, grad_out, None, *routed, gy, None)
+            if need_gw:
+                moe_combine_bwd_weights_checkpoint(shape, grad_out, y, y_scales, *routed, gw)
         else:
-            moe_combine_bwd(shape, grad_out, y, topk_idx, topk_weights, assist, recv, mask, x, a1, a2, cv,
-                            gy, gw)
+            moe_combine_bwd(shape, grad_out, y, *routed, gy, gw)
         # the fp8 weight gradients need no bf16 dG/dU (its codes come out of the
         # down data gradient)
         ggu = None if ctx.fp8_wgrad else torch.empty((cap, 2 * F), dtype=BF16, device=dev)
@@ -1249,7 +1289,9 @@ class _MoELayerFn(torch.autograd.Function):
         accum = None
         s_grads = (None, None, None)
         if ctx.shared_ffn:
-            swg, swu, swd, s_counts, s_gus, s_h = saved[16:]
+            swg, swu, swd, s_counts, s_gus, s_h = saved[17:]
+            if ctx.keep8:
+                s_gus, s_h = _restore_gate_up(s_gus, s_h, None)
             ss = ctx.s_shape
             Fs = ss.F
             s_ggu = torch.empty((T, 2 * Fs), dtype=BF16, device=dev)
@@ -1275,7 +1317,7 @@ class _MoELayerFn(torch.autograd.Function):
             moe_ffn_gate_up_bwd_weight_gather(shape, ggu, x, assist, recv, gwg, gwu)
         g_shared = grad_out if ctx.has_shared_x else None
         return (gx, gw, gwg.to(w_gate.dtype), gwu.to(w_up.dtype), gwd.to(w_down.dtype), g_shared,
-                *s_grads, None, None, None, None, None, None, None, None, None, None, None, None)
+                *s_grads, None, None, None, None, None, None, None, None, None, None, None, None, None)
 
 
 @dataclass
@@ -1848,7 +1890,7 @@ def moe_layer(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, x_active_mask=
               shared_expert_x=None, shared_w_gate=None, shared_w_up=None, shared_w_down=None,
               const_alpha_1=None, const_alpha_2=None, const_v=None,
               zero_expert_num=0, copy_expert_num=0, const_expert_num=0, fp8=False,
-              comm_quant_mode=0, fp8_wgrad=False, mx=False):
+              comm_quant_mode=0, fp8_wgrad=False, mx=False, checkpoint_8bit=False):
     """One MoE layer (ori_x is x itself).
 
     The shared-expert term of combine is either given (shared_expert_x) or
@@ -1864,8 +1906,18 @@ def moe_layer(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, x_active_mask=
     tokens of each expert; mx=True (with fp8=True) uses microscaled e4m3 (E8M0
     scale per 32 values, applied by the block-scaled MFMA) instead of fp32 block
     scales for the forward and data-gradient GEMMs; comm_quant_mode=2 sends the
-    expert outputs through the int8 combine payload."""
+    expert outputs through the int8 combine payload.
+
+    checkpoint_8bit=True (bf16 only) keeps what the backward needs of every routed
+    row in 8 bits, 2.125 F + 1.0625 H bytes in place of 6 F + 2 H (2.125 F where
+    topk_weights need no gradient): the forward's results are the same bits, the
+    gradients those of the kept G, U and y."""
+    if checkpoint_8bit and (fp8 or comm_quant_mode):
+        raise MoeError("checkpoint_8bit keeps the bf16 path's activations (not with fp8 or comm_quant_mode)")
+    if checkpoint_8bit and torch.is_grad_enabled():
+        _nodes().refuse_foreign_leaves([x, topk_weights, w_gate, w_up, w_down, shared_expert_x, shared_w_gate,
+                                        shared_w_up, shared_w_down])
     return _MoELayerFn.apply(x, topk_weights, w_gate, w_up, w_down, shared_expert_x, shared_w_gate,
                              shared_w_up, shared_w_down, topk_idx, x_active_mask, const_alpha_1,
                              const_alpha_2, const_v, zero_expert_num, copy_expert_num,
-                             const_expert_num, fp8, comm_quant_mode, fp8_wgrad, mx)
+                             const_expert_num, fp8, comm_quant_mode, fp8_wgrad, mx, checkpoint_8bit)

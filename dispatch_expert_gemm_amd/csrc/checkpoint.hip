@@ -542,8 +542,10 @@ extern "C" moe_status moe_combine_checkpoint(const moe_shape* s, const void* y, 
   if (s->mask_ndim > 0 && !x_active_mask) return MOE_ERR_NULL_ARG;
   st = check_special(s, ori_x, const_alpha_1, const_alpha_2, const_v);
   if (st != MOE_OK) return st;
-  for (const void* p : {y, shared_expert_x, ori_x, const_alpha_1, const_alpha_2, const_v, (const void*)out})
+  const bool special = s->copy_expert_num + s->const_expert_num > 0;
+  for (const void* p : {y, shared_expert_x, const_alpha_1, const_alpha_2, const_v, (const void*)out})
     if (!aligned16(p)) return MOE_ERR_BAD_SHAPE;
+  if (special && !aligned16(ori_x)) return MOE_ERR_BAD_SHAPE;
   if (reinterpret_cast<uintptr_t>(y_codes) % 8) return MOE_ERR_BAD_SHAPE;
   const CombineArgs a{static_cast<const uint4*>(y),
                       topk_weights,
@@ -564,7 +566,7 @@ extern "C" moe_status moe_combine_checkpoint(const moe_shape* s, const void* y, 
   launch_k(s->K, [&](auto km) {
     constexpr int KM = decltype(km)::value;
     const dim3 grid((unsigned)((waves + 3) / 4));
-    if (s->copy_expert_num + s->const_expert_num > 0)
+    if (special)
       hipLaunchKernelGGL((k_combine_keep<KM, true>), grid, dim3(kThreads), 0, as_stream(stream), a, q);
     else
       hipLaunchKernelGGL((k_combine_keep<KM, false>), grid, dim3(kThreads), 0, as_stream(stream), a, q);
@@ -588,8 +590,10 @@ extern "C" moe_status moe_combine_bwd_weights_checkpoint(
   if (s->mask_ndim > 0 && !x_active_mask) return MOE_ERR_NULL_ARG;
   st = check_special(s, ori_x, const_alpha_1, const_alpha_2, const_v);
   if (st != MOE_OK) return st;
-  for (const void* p : {grad_out, ori_x, const_alpha_1, const_alpha_2, const_v})
+  const bool special = s->copy_expert_num + s->const_expert_num > 0;
+  for (const void* p : {grad_out, const_alpha_1, const_alpha_2, const_v})
     if (!aligned16(p)) return MOE_ERR_BAD_SHAPE;
+  if (special && !aligned16(ori_x)) return MOE_ERR_BAD_SHAPE;
   if (reinterpret_cast<uintptr_t>(y_codes) % 8) return MOE_ERR_BAD_SHAPE;
   const KeptBwdArgs a{static_cast<const uint4*>(grad_out),
                       reinterpret_cast<const uint2*>(y_codes),
@@ -611,7 +615,6 @@ extern "C" moe_status moe_combine_bwd_weights_checkpoint(
     auto go = [&](auto kernel, int64_t blocks) {
       hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, as_stream(stream), a);
     };
-    const bool special = s->copy_expert_num + s->const_expert_num > 0;
     // four waves for a row of four 64-vector blocks or more: 4096 tokens of 7168
     // columns 69 us against 75 with two (and 92 with one)
     if (a.Hv >= 256) {

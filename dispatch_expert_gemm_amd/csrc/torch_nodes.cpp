@@ -6,8 +6,10 @@
 // where torch's own x * 2 takes 44.  The nodes call the C entries themselves; the
 // arguments' checks and errors are the Python binding's.
 #include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/variable.h>
 #include <torch/extension.h>
 
 #include "moe.h"
@@ -63,6 +65,27 @@ void* stream_of(const Tensor& t) { return c10::hip::getCurrentHIPStream(t.get_de
 template <typename T>
 T* at_or_null(const Tensor& t) {
   return t.defined() ? static_cast<T*>(t.data_ptr()) : nullptr;
+}
+
+// A leaf whose gradient accumulator belongs to another stream's graph that still lives:
+// the engine would make that stream wait inside a capture, which ends the process.
+void refuse_foreign_leaf(const Tensor& t, const char* name) {
+  if (!at::GradMode::is_enabled() || !t.requires_grad() || !t.is_leaf()) return;
+  const auto accumulator = torch::autograd::impl::try_get_grad_accumulator(t);
+  if (!accumulator) return;
+  const auto home = accumulator->stream();
+  const auto here = c10::hip::getCurrentHIPStream(t.get_device());
+  if (home && home->id() != here.id())
+    refuse(name, " is a leaf of a graph that another stream built and that still lives: a captured backward needs leaves "
+           "of its own (detach() them in the capture, or free that graph)");
+}
+
+bool capturing() { return c10::hip::currentStreamCaptureStatusMayInitCtx() != c10::hip::CaptureStatus::None; }
+
+void refuse_foreign_leaves(const std::vector<std::optional<Tensor>>& tensors) {
+  if (!capturing()) return;
+  for (const auto& t : tensors)
+    if (t && t->is_cuda()) refuse_foreign_leaf(*t, "an input");
 }
 
 // Gradients that cannot be differentiated again: a second derivative raises.
@@ -164,6 +187,7 @@ std::tuple<Tensor, Tensor, Tensor> balance_loss(const Tensor& logits, const Tens
     z.S = off->numel() - 1;
   }
   const c10::DeviceGuard guard(logits.device());
+  if (capturing()) refuse_foreign_leaf(logits, "logits");
   const variable_list r = BalanceNode::apply(logits, c, z);
   return {r[0], r[1], r[2]};
 }
@@ -208,6 +232,7 @@ Tensor swiglu_checkpoint(const Tensor& gate_up) {
   if (!gate_up.dim() || gate_up.size(-1) % 2 || !gate_up.size(-1))
     refuse("gate_up must be a tensor of shape (..., 2F), got ", gate_up.sizes());
   const c10::DeviceGuard guard(gate_up.device());
+  if (capturing()) refuse_foreign_leaf(gate_up, "gate_up");
   return SwigluNode::apply(gate_up);
 }
 
@@ -226,4 +251,5 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
   });
   m.def("balance_loss", &balance_loss);
   m.def("swiglu_checkpoint", &swiglu_checkpoint);
+  m.def("refuse_foreign_leaves", &refuse_foreign_leaves);
 }

@@ -100,8 +100,9 @@ def test_combine_entries_refuse(L):
         assert f(dm.make_shape(8, 64, 2, 4, capacity=15)) == -4
         assert f(ok, c=P(0x10004)) == BAD_SHAPE
         assert f(dm.make_shape(0, 64, 2, 4), **{n: N for n in names}) == OK
-    for name in ("y", "sx", "ox", "out"):
+    for name in ("y", "sx", "out"):
         assert fwd(ok, **{name: P(0x10002)}) == BAD_SHAPE, name
+    assert fwd(dm.make_shape(8, 64, 2, 4, copy_expert_num=1), ox=P(0x10002)) == BAD_SHAPE
     assert bwd(ok, d=P(0x10008)) == BAD_SHAPE
 
 
