@@ -468,12 +468,17 @@ __global__ __launch_bounds__(kWave * kJoinWaves) void k_balance_join(BalanceArgs
   }
 }
 
-template <typename In, bool VEC>
+template <typename In, bool VEC, bool PAST>
 __device__ __forceinline__ void store4(const BalanceArgs& a, int64_t t, int c, const float* v) {
   In* p = static_cast<In*>(a.grad) + t * a.n + c;
   if constexpr (VEC) {
     if (c >= a.n) return;
-    if constexpr (sizeof(In) == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    if constexpr (sizeof(In) == 4) {
+      typedef float f32x4_t __attribute__((ext_vector_type(4)));
+      const f32x4_t r = {v[0], v[1], v[2], v[3]};
+      if constexpr (PAST) __builtin_nontemporal_store(r, reinterpret_cast<f32x4_t*>(p));
+      else *reinterpret_cast<f32x4_t*>(p) = r;
+    }
     else *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
   } else {
 #pragma unroll
@@ -485,7 +490,8 @@ __device__ __forceinline__ void store4(const BalanceArgs& a, int64_t t, int c, c
   }
 }
 
-template <typename In, bool VEC, int GW, int Q>
+// PAST: the gradient does not fit the caches and is written around them.
+template <typename In, bool VEC, int GW, int Q, bool PAST>
 __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (GW - 1);
   constexpr int G = kWave / GW;
@@ -550,7 +556,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
       float r[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) r[j] = some ? v[q][j] * (share * (f[q][j] - d) + zt) : 0.f;
-      if (in) store4<In, VEC>(a, t, (q * GW + l) * 4, r);
+      if (in) store4<In, VEC, PAST>(a, t, (q * GW + l) * 4, r);
     }
   }
 }
@@ -635,8 +641,14 @@ struct LaunchBwd {
   hipStream_t strm;
   template <typename In, bool VEC, int GW, int Q>
   void operator()() const {
-    hipLaunchKernelGGL((k_balance_bwd<In, VEC, GW, Q>), dim3((unsigned)((a.T + a.C - 1) / a.C)), dim3(kThreads), 0,
-                       strm, a);
+    const dim3 grid((unsigned)((a.T + a.C - 1) / a.C));
+    // a gradient past the L2s' 32 MB that stayed in the caches would go to memory while
+    // the next kernel reads (32768 x 1024 fp32, forward and backward 107 us, so 101)
+    constexpr bool kWide = VEC && sizeof(In) == 4;
+    if (kWide && a.T * a.n * 4 > (32 << 20))
+      hipLaunchKernelGGL((k_balance_bwd<In, VEC, GW, Q, kWide>), grid, dim3(kThreads), 0, strm, a);
+    else
+      hipLaunchKernelGGL((k_balance_bwd<In, VEC, GW, Q, false>), grid, dim3(kThreads), 0, strm, a);
   }
 };
 
