@@ -101,41 +101,45 @@ __device__ __forceinline__ int find_last(int S, int64_t x, Key key) {
   return lo;
 }
 
-// The four logits of row t from column c on; -inf past n.
+// Four logits as they lie in memory: converted when they are used, so that a load a
+// step ahead is not waited for.
+template <typename In>
+struct Raw4 {
+  uint32_t w[sizeof(In)];  // four of fp32, or two of two bf16
+};
+
+// The four logits of row t from column c on; -inf past n.  VEC: n is a multiple of 4
+// and the rows are aligned; otherwise the four begin anywhere, and a row's last ones
+// are read one by one.
 template <typename In, bool VEC>
-__device__ __forceinline__ void load4(const BalanceArgs& a, int64_t t, int c, float* v) {
+__device__ __forceinline__ void load4(const BalanceArgs& a, int64_t t, int c, Raw4<In>& v) {
   const In* p = static_cast<const In*>(a.logits) + t * a.n + c;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = -INFINITY;
-  if constexpr (VEC) {  // n a multiple of 4, aligned rows
-    if (c < a.n) {
-      if constexpr (sizeof(In) == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(p);
-        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-        v[0] = bf2f(u.x & 0xffffu); v[1] = bf2f(u.x >> 16);
-        v[2] = bf2f(u.y & 0xffffu); v[3] = bf2f(u.y >> 16);
-      }
+  for (int j = 0; j < (int)sizeof(In); ++j) v.w[j] = sizeof(In) == 4 ? 0xff800000u : 0xff80ff80u;
+  if (VEC ? c < a.n : c + 4 <= a.n) {
+    if constexpr (!VEC) __builtin_memcpy(v.w, p, sizeof(v.w));
+    else if constexpr (sizeof(In) == 4) *reinterpret_cast<uint4*>(v.w) = *reinterpret_cast<const uint4*>(p);
+    else *reinterpret_cast<uint2*>(v.w) = *reinterpret_cast<const uint2*>(p);
+  } else if (!VEC && c < a.n) {
+    const int left = a.n - c;  // 1 to 3
+    if constexpr (sizeof(In) == 4) {
+      v.w[0] = reinterpret_cast<const uint32_t*>(p)[0];
+      if (left > 1) v.w[1] = reinterpret_cast<const uint32_t*>(p)[1];
+      if (left > 2) v.w[2] = reinterpret_cast<const uint32_t*>(p)[2];
+    } else {
+      const bf16_t* q = reinterpret_cast<const bf16_t*>(p);
+      v.w[0] = q[0] | (left > 1 ? (uint32_t)q[1] : 0xff80u) << 16;
+      if (left > 2) v.w[1] = q[2] | 0xff800000u;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (c + j < a.n) {
-        if constexpr (sizeof(In) == 4) v[j] = p[j];
-        else v[j] = bf2f(reinterpret_cast<const bf16_t*>(p)[j]);
-      }
   }
 }
 
 // A lane's part of row t (-inf where t >= t1): issued a step ahead of its use.
 template <typename In, bool VEC, int GW, int Q>
-__device__ __forceinline__ void load_row(const BalanceArgs& a, int64_t t, int64_t t1, float (&v)[Q][4]) {
+__device__ __forceinline__ void load_row(const BalanceArgs& a, int64_t t, int64_t t1, Raw4<In> (&v)[Q]) {
   const int l = threadIdx.x & (GW - 1);
 #pragma unroll
-  for (int q = 0; q < Q; ++q)
-    if (t < t1) load4<In, VEC>(a, t, (q * GW + l) * 4, v[q]);
-    else v[q][0] = v[q][1] = v[q][2] = v[q][3] = -INFINITY;
+  for (int q = 0; q < Q; ++q) load4<In, VEC>(a, t, t < t1 ? (q * GW + l) * 4 : a.n, v[q]);
 }
 
 // Rows of up to 1024 columns are loaded a step ahead; longer ones keep 32 or 64 values
@@ -143,13 +147,18 @@ __device__ __forceinline__ void load_row(const BalanceArgs& a, int64_t t, int64_
 template <int Q>
 constexpr bool kAhead = Q <= 4;
 
-// The row loaded a step ahead, a NaN read as -inf.
-template <int Q>
-__device__ __forceinline__ void take_row(const float (&next)[Q][4], float (&v)[Q][4]) {
+// The values of a row, a NaN read as -inf (fmaxf drops it).
+template <typename In, int Q>
+__device__ __forceinline__ void take_row(const Raw4<In> (&raw)[Q], float (&v)[Q][4]) {
 #pragma unroll
   for (int q = 0; q < Q; ++q)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[q][j] = fmaxf(next[q][j], -INFINITY);  // (fmaxf drops a NaN)
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t b = sizeof(In) == 4 ? raw[q].w[j % sizeof(In)]
+                                         : (j & 1 ? raw[q].w[j / 2 % sizeof(In)] & 0xffff0000u
+                                                  : raw[q].w[j / 2 % sizeof(In)] << 16);
+      v[q][j] = fmaxf(__uint_as_float(b), -INFINITY);
+    }
 }
 
 // exp(v - m) in place of the row's logits; m the row's largest, total the sum.  A
@@ -233,7 +242,8 @@ __global__ __launch_bounds__(kWave * kItemWaves<Q>, Q <= 4 ? 6 : 1) void k_balan
     if (t0 < lo || t0 >= t1) return;  // a slot that no sequence fills: never read
   }
   for (int i = tid; i < a.n; i += kWave * W) hist[i] = 0;
-  float v[Q][4], next[Q][4];
+  float v[Q][4];
+  Raw4<In> next[Q];
   if constexpr (kAhead<Q>) load_row<In, VEC, GW, Q>(a, t0 + wave * G + lane / GW, t1, next);
   __syncthreads();
   // the choices by themselves, a thread each: with each token's among its logits the
@@ -257,7 +267,7 @@ __global__ __launch_bounds__(kWave * kItemWaves<Q>, Q <= 4 ? 6 : 1) void k_balan
     const int64_t t = b + lane / GW;
     const bool in = t < t1;
     if constexpr (!kAhead<Q>) load_row<In, VEC, GW, Q>(a, t, t1, next);
-    take_row<Q>(next, v);
+    take_row<In, Q>(next, v);
     if constexpr (kAhead<Q>) load_row<In, VEC, GW, Q>(a, t + W * G, t1, next);
     const bool on = token_on<GW>(a, t, in);
     float m, total;
@@ -471,18 +481,21 @@ __global__ __launch_bounds__(kWave * kJoinWaves) void k_balance_join(BalanceArgs
 template <typename In, bool VEC, bool PAST>
 __device__ __forceinline__ void store4(const BalanceArgs& a, int64_t t, int c, const float* v) {
   In* p = static_cast<In*>(a.grad) + t * a.n + c;
-  if constexpr (VEC) {
-    if (c >= a.n) return;
+  if (VEC ? c < a.n : c + 4 <= a.n) {
     if constexpr (sizeof(In) == 4) {
       typedef float f32x4_t __attribute__((ext_vector_type(4)));
       const f32x4_t r = {v[0], v[1], v[2], v[3]};
       if constexpr (PAST) __builtin_nontemporal_store(r, reinterpret_cast<f32x4_t*>(p));
-      else *reinterpret_cast<f32x4_t*>(p) = r;
+      else if constexpr (VEC) *reinterpret_cast<f32x4_t*>(p) = r;
+      else __builtin_memcpy(p, &r, 16);
+    } else {
+      const uint2 r = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
+      if constexpr (VEC) *reinterpret_cast<uint2*>(p) = r;
+      else __builtin_memcpy(p, &r, 8);
     }
-    else *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
-  } else {
+  } else if (!VEC && c < a.n) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 3; ++j)
       if (c + j < a.n) {
         if constexpr (sizeof(In) == 4) p[j] = v[j];
         else reinterpret_cast<bf16_t*>(p)[j] = (bf16_t)f2bf(v[j]);
@@ -517,13 +530,14 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
   };
   hold();
   int held = s;
-  float v[Q][4], next[Q][4];
+  float v[Q][4];
+  Raw4<In> next[Q];
   if constexpr (kAhead<Q>) load_row<In, VEC, GW, Q>(a, t0 + wave * G + lane / GW, t1, next);
   for (int64_t b = t0 + wave * G; b < t1; b += kWaves * G) {
     const int64_t t = b + lane / GW;
     const bool in = t < t1;
     if constexpr (!kAhead<Q>) load_row<In, VEC, GW, Q>(a, t, t1, next);
-    take_row<Q>(next, v);
+    take_row<In, Q>(next, v);
     if constexpr (kAhead<Q>) load_row<In, VEC, GW, Q>(a, t + kWaves * G, t1, next);
     while (t >= s1 && s + 1 < a.S) {
       ++s;

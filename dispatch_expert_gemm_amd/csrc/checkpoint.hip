@@ -93,7 +93,7 @@ struct SwigluArgs {
   void* out;             // GRAD: dG|dU, RESTORE: G|U (R x 2F)
   void* h;               // R x F, or NULL
   int64_t R, F, nb;
-  // vector passes: units of eight columns, `cols` = F / 8 units a row
+  // units of eight columns, `cols` of them a row of whole blocks
   uint32_t cols, step_rows, step_cols;  // kThreads units on: rows and columns
 };
 
@@ -117,12 +117,86 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float& dg
   h = si * u;
 }
 
-// F a multiple of 32 and 16-byte aligned rows: a lane takes eight columns of G and
-// the same eight of U.  kUnits units a thread, kThreads apart, loads first.
-template <int PASS, bool H>
+// n of the eight bf16 at p (any address; zeros behind them), and their stores.  A
+// row's last eight columns may be fewer: 4, 2 and 1 of them at a time.
+template <bool WHOLE>
+__device__ __forceinline__ uint4 load8(const uint16_t* p, int n) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (WHOLE) return *reinterpret_cast<const uint4*>(p);
+  if (n >= 8) {
+    __builtin_memcpy(&v, p, 16);
+    return v;
+  }
+  if (n & 4) __builtin_memcpy(&v, p, 8);
+  if (n & 2) {
+    uint32_t w;
+    __builtin_memcpy(&w, p + (n & 4), 4);
+    (n & 4 ? v.z : v.x) = w;
+  }
+  if (n & 1) {
+    const uint32_t w = p[n & 6];
+    (n & 4 ? (n & 2 ? v.w : v.z) : (n & 2 ? v.y : v.x)) = w;
+  }
+  return v;
+}
+template <bool WHOLE>
+__device__ __forceinline__ void store8(uint16_t* p, const uint4& v, int n) {
+  if (WHOLE) {
+    *reinterpret_cast<uint4*>(p) = v;
+    return;
+  }
+  if (n >= 8) {
+    __builtin_memcpy(p, &v, 16);
+    return;
+  }
+  if (n & 4) __builtin_memcpy(p, &v, 8);
+  if (n & 2) {
+    const uint32_t w = n & 4 ? v.z : v.x;
+    __builtin_memcpy(p + (n & 4), &w, 4);
+  }
+  if (n & 1) p[n & 6] = (uint16_t)(n & 4 ? (n & 2 ? v.w : v.z) : (n & 2 ? v.y : v.x));
+}
+// The same of eight codes.
+template <bool WHOLE>
+__device__ __forceinline__ uint2 load8(const int8_t* p, int n) {
+  uint2 v = make_uint2(0u, 0u);
+  if (WHOLE) return *reinterpret_cast<const uint2*>(p);
+  if (n >= 8) {
+    __builtin_memcpy(&v, p, 8);
+    return v;
+  }
+  if (n & 4) __builtin_memcpy(&v, p, 4);
+  uint32_t w = 0;
+  if (n & 2) __builtin_memcpy(&w, p + (n & 4), 2);
+  if (n & 1) w |= (uint32_t)(uint8_t)p[n & 6] << (n & 2 ? 16 : 0);
+  if (n & 3) (n & 4 ? v.y : v.x) = w;
+  return v;
+}
+template <bool WHOLE>
+__device__ __forceinline__ void store8(int8_t* p, const uint2& v, int n) {
+  if (WHOLE) {
+    *reinterpret_cast<uint2*>(p) = v;
+    return;
+  }
+  if (n >= 8) {
+    __builtin_memcpy(p, &v, 8);
+    return;
+  }
+  if (n & 4) __builtin_memcpy(p, &v, 4);
+  const uint32_t w = n & 4 ? v.y : v.x;
+  if (n & 2) __builtin_memcpy(p + (n & 4), &w, 2);
+  if (n & 1) p[n & 6] = (int8_t)(n & 2 ? w >> 16 : w);
+}
+
+// A lane takes eight columns of G and the same eight of U: a unit.  kUnits units a
+// thread, kThreads apart, loads first.  WHOLE: F is a multiple of 32 and every
+// matrix 16-byte aligned; otherwise a row is rounded up to whole blocks (units past
+// F hold zeros) and accesses may begin anywhere: 32768 rows of 1001 columns 69 us,
+// with a lane for each column 158.
+template <int PASS, bool H, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
   constexpr int kUnits = 2;
-  const int64_t rows = rows_of(a);
+  const int64_t rows = rows_of(a), F = a.F;
   const int64_t u0 = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
   int64_t row[kUnits];
   uint32_t col[kUnits];
@@ -137,24 +211,30 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
       ++row[i];
     }
   }
-  const uint32_t cols = a.cols;
+  // columns of unit i that there are (8 where WHOLE), its place in a row of F
+  auto count = [&](int i) {
+    const int left = (int)F - 8 * (int)col[i];
+    return WHOLE ? 8 : (left < 0 ? 0 : (left < 8 ? left : 8));
+  };
+  auto gate = [&](int i) { return row[i] * 2 * F + 8 * (int64_t)col[i]; };
+  auto hcol = [&](int i) { return row[i] * F + 8 * (int64_t)col[i]; };
   if constexpr (PASS == KEEP) {
-    const uint4* gu = static_cast<const uint4*>(a.gate_up);
+    const uint16_t* gu = static_cast<const uint16_t*>(a.gate_up);
     uint4 g[kUnits], u[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
       if (row[i] < rows) {
-        g[i] = gu[row[i] * 2 * cols + col[i]];
-        u[i] = gu[row[i] * 2 * cols + cols + col[i]];
+        g[i] = load8<WHOLE>(gu + gate(i), count(i));
+        u[i] = load8<WHOLE>(gu + gate(i) + F, count(i));
       }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       if (row[i] >= rows) continue;  // the four lanes of a block leave together
       float ig, iu;
       const uint32_t sg = kept_scale(block_amax(g[i]), ig), su = kept_scale(block_amax(u[i]), iu);
-      uint2* codes = reinterpret_cast<uint2*>(a.codes) + row[i] * 2 * cols + col[i];
-      codes[0] = codes8(g[i], ig);
-      codes[cols] = codes8(u[i], iu);
+      const int n = count(i);
+      store8<WHOLE>(a.codes + gate(i), codes8(g[i], ig), n);
+      store8<WHOLE>(a.codes + gate(i) + F, codes8(u[i], iu), n);
       if ((col[i] & 3) == 0) {
         uint16_t* sc = a.scales + row[i] * 2 * a.nb + col[i] / 4;
         sc[0] = (uint16_t)sg;
@@ -166,7 +246,7 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
         unpack8(u[i], uf);
 #pragma unroll
         for (int j = 0; j < 8; ++j) gf[j] = gf[j] * sigmoid(gf[j]) * uf[j];
-        static_cast<uint4*>(a.h)[row[i] * cols + col[i]] = pack8h(gf);
+        store8<WHOLE>(static_cast<uint16_t*>(a.h) + hcol(i), pack8h(gf), n);
       }
     }
   } else {
@@ -176,13 +256,13 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
       if (row[i] < rows) {
-        const uint2* codes = reinterpret_cast<const uint2*>(a.codes) + row[i] * 2 * cols + col[i];
         const uint16_t* sc = a.scales + row[i] * 2 * a.nb + col[i] / 4;
-        qg[i] = codes[0];
-        qu[i] = codes[cols];
+        qg[i] = load8<WHOLE>(a.codes + gate(i), count(i));
+        qu[i] = load8<WHOLE>(a.codes + gate(i) + F, count(i));
         sg[i] = sc[0];
         su[i] = sc[a.nb];
-        if constexpr (PASS == GRAD) dh[i] = static_cast<const uint4*>(a.grad_h)[row[i] * cols + col[i]];
+        if constexpr (PASS == GRAD)
+          dh[i] = load8<WHOLE>(static_cast<const uint16_t*>(a.grad_h) + hcol(i), count(i));
       }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
@@ -190,7 +270,6 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
       float g[8], u[8], h[8];
       kept8(qg[i], bf2f(sg[i]), g);
       kept8(qu[i], bf2f(su[i]), u);
-      uint4* out = static_cast<uint4*>(a.out) + row[i] * 2 * cols + col[i];
       if constexpr (PASS == GRAD) {
         float d[8];
         unpack8(dh[i], d);
@@ -200,54 +279,12 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[j] = g[j] * sigmoid(g[j]) * u[j];
       }
-      out[0] = pack8h(g);
-      out[cols] = pack8h(u);
-      if constexpr (H) static_cast<uint4*>(a.h)[row[i] * cols + col[i]] = pack8h(h);
+      const int n = count(i);
+      uint16_t* out = static_cast<uint16_t*>(a.out) + gate(i);
+      store8<WHOLE>(out, pack8h(g), n);
+      store8<WHOLE>(out + F, pack8h(u), n);
+      if constexpr (H) store8<WHOLE>(static_cast<uint16_t*>(a.h) + hcol(i), pack8h(h), n);
     }
-  }
-}
-
-// Any F and any alignment: 32 lanes take a block of G and the same block of U, a
-// column each.
-template <int PASS>
-__global__ __launch_bounds__(kThreads) void k_swiglu_any(SwigluArgs a) {
-  const int64_t rows = rows_of(a);
-  const int64_t b = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kCols;
-  const int64_t row = b / a.nb, blk = b - row * a.nb;
-  if (row >= rows) return;  // 32 lanes leave together
-  const int64_t c = blk * kCols + (threadIdx.x & (kCols - 1));
-  const bool in = c < a.F;
-  const int64_t at = row * 2 * a.F + c, ah = row * a.F + c;
-  uint16_t* sc = a.scales + row * 2 * a.nb + blk;
-  uint16_t* h = static_cast<uint16_t*>(a.h);
-  if constexpr (PASS == KEEP) {
-    const uint16_t* gu = static_cast<const uint16_t*>(a.gate_up);
-    const uint32_t g = in ? gu[at] : 0u, u = in ? gu[at + a.F] : 0u;
-    uint32_t m = (g & 0x7fffu) | (u & 0x7fffu) << 16;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = max16x2(m, (uint32_t)__shfl_xor((int)m, o, kCols));
-    float ig, iu;
-    const uint32_t sg = kept_scale(m & 0xffffu, ig), su = kept_scale(m >> 16, iu);
-    if (c == blk * kCols) {
-      sc[0] = (uint16_t)sg;
-      sc[a.nb] = (uint16_t)su;
-    }
-    if (!in) return;
-    const float gf = bf2f(g), uf = bf2f(u);
-    a.codes[at] = ig == 0.f ? (int8_t)0 : (int8_t)code(gf, ig);
-    a.codes[at + a.F] = iu == 0.f ? (int8_t)0 : (int8_t)code(uf, iu);
-    if (h) h[ah] = (uint16_t)f2bf(gf * sigmoid(gf) * uf);
-  } else {
-    if (!in) return;
-    const float g = __fmul_rn((float)a.codes[at], bf2f(sc[0]));
-    const float u = __fmul_rn((float)a.codes[at + a.F], bf2f(sc[a.nb]));
-    uint16_t* out = static_cast<uint16_t*>(a.out);
-    float dg = g, du = u, hv;
-    if constexpr (PASS == GRAD) swiglu_grad(g, u, bf2f(static_cast<const uint16_t*>(a.grad_h)[ah]), dg, du, hv);
-    else hv = g * sigmoid(g) * u;
-    out[at] = (uint16_t)f2bf(dg);
-    out[at + a.F] = (uint16_t)f2bf(du);
-    if (h) h[ah] = (uint16_t)f2bf(hv);
   }
 }
 
@@ -440,22 +477,21 @@ template <int PASS>
 moe_status launch_swiglu(SwigluArgs a, void* stream) {
   a.nb = (a.F + kCols - 1) / kCols;
   const void* io = PASS == KEEP ? a.gate_up : a.out;
-  const bool vec = a.F % kCols == 0 && aligned16(io) && aligned16(a.h) && aligned16(a.grad_h) &&
-                   reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
-  if (vec) {
-    a.cols = (uint32_t)(a.F / 8);
-    a.step_rows = kThreads / a.cols;
-    a.step_cols = kThreads % a.cols;
-    const int64_t units = a.R * (int64_t)a.cols;
-    if (units / 2 > kMaxThreads) return MOE_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)((units + 2 * kThreads - 1) / (2 * kThreads)));
-    if (a.h) hipLaunchKernelGGL((k_swiglu_rows<PASS, true>), grid, dim3(kThreads), 0, as_stream(stream), a);
-    else hipLaunchKernelGGL((k_swiglu_rows<PASS, false>), grid, dim3(kThreads), 0, as_stream(stream), a);
+  const bool whole = a.F % kCols == 0 && aligned16(io) && aligned16(a.h) && aligned16(a.grad_h) &&
+                     reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
+  a.cols = (uint32_t)(a.nb * (kCols / 8));
+  a.step_rows = kThreads / a.cols;
+  a.step_cols = kThreads % a.cols;
+  const int64_t units = a.R * (int64_t)a.cols;
+  if (units / 2 > kMaxThreads) return MOE_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)((units + 2 * kThreads - 1) / (2 * kThreads)));
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, as_stream(stream), a); };
+  if (whole) {
+    if (a.h) go(k_swiglu_rows<PASS, true, true>);
+    else go(k_swiglu_rows<PASS, false, true>);
   } else {
-    const int64_t threads = a.R * a.nb * kCols;
-    if (threads > kMaxThreads) return MOE_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL(k_swiglu_any<PASS>, dim3((unsigned)((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                       as_stream(stream), a);
+    if (a.h) go(k_swiglu_rows<PASS, true, false>);
+    else go(k_swiglu_rows<PASS, false, false>);
   }
   return launch_status();
 }

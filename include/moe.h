@@ -912,9 +912,9 @@ moe_status moe_balance_bwd(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs
  * whose s would be below 2^-126 keeps zeros; one that holds an infinity or a NaN
  * keeps NaN.  Rows of width W: codes (rows, W) int8, scales (rows, ceil(W / 32))
  * bf16; rows [G | U] of width 2F are cut into blocks as two rows of width F: scales
- * (rows, 2, ceil(F / 32)).  R >= 0 rows, 1 <= F <= 2^20 (else MOE_ERR_BAD_SHAPE);
- * up to 2^32 columns of G, 2^36 where F is a multiple of 32 and every matrix
- * begins on a 16-byte boundary (else MOE_ERR_UNSUPPORTED).  nrows: the rows in use,
+ * (rows, 2, ceil(F / 32)).  R >= 0 rows, 1 <= F <= 2^20 (else MOE_ERR_BAD_SHAPE), up to
+ * 2^31 blocks of G (else MOE_ERR_UNSUPPORTED); any alignment (fastest with F a multiple of 32
+ * and matrices on 16-byte boundaries).  nrows: the rows in use,
  * one int32 on the device (e.g. the last of ep_recv_counts), or NULL: all R; rows past
  * them are neither read nor written.  One launch each.
  */
