@@ -53,7 +53,8 @@ ENTRY_POINTS = (
     "moe_few_tokens_workspace_size", "moe_few_tokens", "moe_few_tokens_int8",
     "moe_linear_int8", "moe_linear_int8_kernel", "moe_linear_int8_workspace_size", "moe_linear_int8_dynamic",
     "moe_balance_workspace_size", "moe_balance_fwd", "moe_balance_bwd",
-    "moe_swiglu_checkpoint_fwd", "moe_swiglu_checkpoint_bwd", "moe_swiglu_checkpoint_restore",
+    "moe_swiglu_checkpoint_fwd", "moe_swiglu_checkpoint_bwd",
+    "moe_ffn_gate_up_fwd_checkpoint", "moe_ffn_down_bwd_data_checkpoint",
     "moe_combine_checkpoint", "moe_combine_bwd_weights_checkpoint",
 )
 
@@ -170,8 +171,9 @@ def lib() -> ctypes.CDLL:
         L.moe_balance_fwd.argtypes = [I64, I64, I32C, I64, I32C, I32C] + [P] * 9 + [Z, P]
         L.moe_balance_bwd.argtypes = [I64, I64, I32C, I64, I32C, I32C] + [P] * 9
         L.moe_swiglu_checkpoint_fwd.argtypes = [I64, I64] + [P] * 6
-        L.moe_swiglu_checkpoint_bwd.argtypes = [I64, I64] + [P] * 7
-        L.moe_swiglu_checkpoint_restore.argtypes = [I64, I64] + [P] * 6
+        L.moe_swiglu_checkpoint_bwd.argtypes = [I64, I64] + [P] * 6
+        L.moe_ffn_gate_up_fwd_checkpoint.argtypes = [S] + [P] * 9
+        L.moe_ffn_down_bwd_data_checkpoint.argtypes = [S] + [P] * 10
         L.moe_combine_checkpoint.argtypes = [S] + [P] * 15
         L.moe_combine_bwd_weights_checkpoint.argtypes = [S] + [P] * 15
         for name in ENTRY_POINTS:
@@ -1042,22 +1044,6 @@ def shared_expert_shape(T, H, F) -> MoeShape:
     return make_shape(T, H, 1, 1, F=F, capacity=T)
 
 
-def _keep_gate_up(gate_up, nrows):
-    """(codes, scales) that stand for gate_up_save and h_act until the backward."""
-    kept = checkpoint_buffers(gate_up.shape[0], gate_up.shape[1] // 2, gate_up.device, halves=2)
-    moe_swiglu_checkpoint_fwd(gate_up, None, *kept, nrows=nrows)
-    return kept
-
-
-def _restore_gate_up(codes, scales, nrows):
-    """gate_up_save and h_act of kept rows."""
-    R, F2 = codes.shape
-    gate_up = torch.empty((R, F2), dtype=BF16, device=codes.device)
-    h = torch.empty((R, F2 // 2), dtype=BF16, device=codes.device)
-    moe_swiglu_checkpoint_restore(codes, scales, gate_up, h, nrows=nrows)
-    return gate_up, h
-
-
 class _MoELayerFn(torch.autograd.Function):
     """Forward: dispatch -> grouped SwiGLU FFN -> combine; backward: the reverse chain.
     In bf16 the dispatch permute is folded into the two GEMMs that read the
@@ -1075,9 +1061,10 @@ class _MoELayerFn(torch.autograd.Function):
     fp8_wgrad on e4m3 operands with one scale per (128 tokens of an expert,
     column); the shared expert stays bf16.  comm_quant_mode 2: the int8 combine payload.
 
-    keep8 (bf16 path): gate_up_save is kept in 8 bits, h not at all (the backward
-    restores both) and the combine keeps y's rows in 8 bits, for the routing weights'
-    gradient alone."""
+    keep8 (bf16 path): [G | U] leave the gate/up GEMM in 8 bits (saved in the places of
+    gate_up_save and h: their codes and scales), the down data gradient reads them so and
+    writes h again, and the combine keeps y's rows in 8 bits for the routing weights'
+    gradient."""
 
     @staticmethod
     def forward(ctx, x, topk_weights, w_gate, w_up, w_down, shared_expert_x, shared_w_gate,
@@ -1104,7 +1091,9 @@ class _MoELayerFn(torch.autograd.Function):
         else:
             d = dispatch(shape, x, topk_idx, mask) if fp8 else route(shape, topk_idx, mask)
         cap = shape.capacity
-        gus = torch.empty((cap, 2 * F), dtype=BF16, device=dev)
+        # (with keep8 gus holds the codes of [G | U], gus_scales their scales)
+        gus, gus_scales = (checkpoint_buffers(cap, F, dev, halves=2) if keep8 else
+                           (torch.empty((cap, 2 * F), dtype=BF16, device=dev), None))
         h = torch.empty((cap, F), dtype=BF16, device=dev)
         y = torch.empty((cap, H), dtype=BF16, device=dev)
         ctx.fp8 = bool(fp8)
@@ -1149,7 +1138,11 @@ class _MoELayerFn(torch.autograd.Function):
             moe_ffn_down_fwd_fp8(shape, hq, hs, wq[2].codes, wq[2].scales, d.ep_recv_counts, y)
             del xq, xs, hq, hs
         else:
-            moe_ffn_gate_up_fwd_gather(shape, x, d.assist_info_for_combine, w_gate, w_up, d.ep_recv_counts, gus, h)
+            gate_up = (shape, x, d.assist_info_for_combine, w_gate, w_up, d.ep_recv_counts)
+            if keep8:
+                moe_ffn_gate_up_fwd_checkpoint(*gate_up, gus, gus_scales, h)
+            else:
+                moe_ffn_gate_up_fwd_gather(*gate_up, gus, h)
             moe_ffn_down_fwd(shape, h, w_down, d.ep_recv_counts, y)
         ctx.shared_ffn = shared_w_gate is not None
         s_saved = ()
@@ -1159,23 +1152,25 @@ class _MoELayerFn(torch.autograd.Function):
             Fs = shared_w_gate.shape[1]
             ss = shared_expert_shape(T, H, Fs)
             s_counts = torch.full((1,), T, dtype=I32, device=dev)
-            s_gus = torch.empty((T, 2 * Fs), dtype=BF16, device=dev)
             s_h = torch.empty((T, Fs), dtype=BF16, device=dev)
             shared_expert_x = torch.empty((T, H), dtype=BF16, device=dev)
-            moe_grouped_ffn(ss, x, shared_w_gate, shared_w_up, shared_w_down, s_counts, s_gus, s_h,
-                            shared_expert_x)
-            ctx.s_shape = ss
             if keep8:
-                s_gus, s_h = _keep_gate_up(s_gus, None)
+                s_gus, s_scales = checkpoint_buffers(T, Fs, dev, halves=2)
+                moe_ffn_gate_up_fwd_checkpoint(ss, x, None, shared_w_gate, shared_w_up, s_counts, s_gus, s_scales, s_h)
+                moe_ffn_down_fwd(ss, s_h, shared_w_down, s_counts, shared_expert_x)
+                s_h = s_scales
+            else:
+                s_gus = torch.empty((T, 2 * Fs), dtype=BF16, device=dev)
+                moe_grouped_ffn(ss, x, shared_w_gate, shared_w_up, shared_w_down, s_counts, s_gus, s_h,
+                                shared_expert_x)
+            ctx.s_shape = ss
             s_saved = (shared_w_gate, shared_w_up, shared_w_down, s_counts, s_gus, s_h)
         out = torch.empty((T, H), dtype=BF16, device=dev)
         combined = (shape, y, topk_idx, topk_weights, d.assist_info_for_combine, d.ep_recv_counts, mask,
                     shared_expert_x, x, const_alpha_1, const_alpha_2, const_v, out)
         y_scales = None
         if keep8:
-            # from here on gus and h are the codes and scales of [G | U], y and y_scales y's
-            gus, h = _keep_gate_up(gus, d.ep_recv_counts[-1:])
-            y = None
+            h = y = None
             if ctx.needs_input_grad[1]:
                 y, y_scales = checkpoint_buffers(cap, H, dev)
                 moe_combine_checkpoint(*combined, y, y_scales)
@@ -1186,7 +1181,7 @@ class _MoELayerFn(torch.autograd.Function):
         ctx.has_shared_x = shared_expert_x is not None and not ctx.shared_ffn
         ctx.save_for_backward(x, topk_weights, w_gate, w_up, w_down, topk_idx, mask, const_alpha_1,
                               const_alpha_2, const_v, d.expand_x if fp8 else None, d.assist_info_for_combine,
-                              d.ep_recv_counts, gus, h, y, y_scales, *s_saved)
+                              d.ep_recv_counts, gus, gus_scales if keep8 else h, y, y_scales, *s_saved)
         # the transposed weight codes of the data-gradient GEMMs (not tensors
         # of the graph, so kept on ctx)
         ctx.wq = tuple((q.codes_t, q.scales_t) if ctx.mx else (q.codes_t, q.scales) for q in wq)
@@ -1199,7 +1194,7 @@ class _MoELayerFn(torch.autograd.Function):
          recv, gus, h, y, y_scales) = saved[:17]
         shape = ctx.shape
         if ctx.keep8:
-            gus, h = _restore_gate_up(gus, h, recv[-1:])
+            gus, h = (gus, h), torch.empty((shape.capacity, shape.F), dtype=BF16, device=x.device)
         grad_out = grad_out.contiguous()
         cap, H, F, T, K = shape.capacity, shape.H, shape.F, shape.T, shape.K
         dev = x.device
@@ -1279,19 +1274,23 @@ class _MoELayerFn(torch.autograd.Function):
             moe_ffn_gate_up_bwd_data_fp8(shape, dgq, dgs, wgt, wgs, wut, wus, recv, gx_exp)
             del dgq, dgs
         elif fold_combine_bwd(F):
-            moe_ffn_down_bwd_data_gather(shape, grad_out, assist, roww, w_down, gus, recv, ggu)
+            if ctx.keep8:
+                moe_ffn_down_bwd_data_checkpoint(shape, grad_out, assist, roww, w_down, *gus, recv, ggu, h)
+            else:
+                moe_ffn_down_bwd_data_gather(shape, grad_out, assist, roww, w_down, gus, recv, ggu)
             moe_ffn_down_bwd_weight_gather(shape, grad_out, assist, roww, h, recv, gwd)
             moe_ffn_gate_up_bwd_data(shape, ggu, w_gate, w_up, recv, gx_exp)
         else:
-            moe_ffn_down_bwd_data(shape, gy, w_down, gus, recv, ggu)
+            if ctx.keep8:
+                moe_ffn_down_bwd_data_checkpoint(shape, gy, None, None, w_down, *gus, recv, ggu, h)
+            else:
+                moe_ffn_down_bwd_data(shape, gy, w_down, gus, recv, ggu)
             moe_ffn_down_bwd_weight(shape, gy, h, recv, gwd)
             moe_ffn_gate_up_bwd_data(shape, ggu, w_gate, w_up, recv, gx_exp)
         accum = None
         s_grads = (None, None, None)
         if ctx.shared_ffn:
             swg, swu, swd, s_counts, s_gus, s_h = saved[17:]
-            if ctx.keep8:
-                s_gus, s_h = _restore_gate_up(s_gus, s_h, None)
             ss = ctx.s_shape
             Fs = ss.F
             s_ggu = torch.empty((T, 2 * Fs), dtype=BF16, device=dev)
@@ -1300,8 +1299,15 @@ class _MoELayerFn(torch.autograd.Function):
             s_gwu = torch.empty(swu.shape, dtype=F32, device=dev)
             s_gwd = torch.empty(swd.shape, dtype=F32, device=dev)
             # the shared expert's output gradient is grad_out itself
-            moe_grouped_ffn_bwd(ss, grad_out, x, s_gus, s_h, swg, swu, swd, s_counts, s_ggu, accum,
-                                s_gwg, s_gwu, s_gwd)
+            if ctx.keep8:
+                s_kept, s_h = (s_gus, s_h), torch.empty((T, Fs), dtype=BF16, device=dev)
+                moe_ffn_down_bwd_data_checkpoint(ss, grad_out, None, None, swd, *s_kept, s_counts, s_ggu, s_h)
+                moe_ffn_down_bwd_weight(ss, grad_out, s_h, s_counts, s_gwd)
+                moe_ffn_gate_up_bwd_data(ss, s_ggu, swg, swu, s_counts, accum)
+                moe_ffn_gate_up_bwd_weight(ss, s_ggu, x, s_counts, s_gwg, s_gwu)
+            else:
+                moe_grouped_ffn_bwd(ss, grad_out, x, s_gus, s_h, swg, swu, swd, s_counts, s_ggu, accum,
+                                    s_gwg, s_gwu, s_gwd)
             s_grads = (s_gwg.to(swg.dtype), s_gwu.to(swu.dtype), s_gwd.to(swd.dtype))
         gx = torch.empty((T, H), dtype=BF16, device=dev)
         moe_dispatch_bwd(shape, gx_exp, assist, topk_idx, topk_weights, mask, grad_out, a1, accum, gx)
@@ -1807,29 +1813,48 @@ def _kept_at(codes, scales, R, F, dev):
 
 
 def moe_swiglu_checkpoint_fwd(gate_up, h, codes, scales, nrows=None, stream=None):
-    """gate_up (R, 2F) bf16 -> h (R, F) bf16 or None, codes (R, 2F) int8, scales (R, 2 ceil(F / 32)) bf16."""
+    """gate_up (R, 2F) bf16 -> h (R, F) bf16, codes (R, 2F) int8, scales (R, 2 ceil(F / 32)) bf16."""
     dev = _device_of(gate_up, "gate_up")
     R, F = _gate_up_sizes(gate_up, "gate_up")
     _launch(lib().moe_swiglu_checkpoint_fwd, dev, stream, R, F, _at(gate_up, BF16, R * 2 * F, "gate_up", dev),
             _at(nrows, I32, 1, "nrows", dev), _at(h, BF16, R * F, "h", dev), *_kept_at(codes, scales, R, F, dev))
 
 
-def moe_swiglu_checkpoint_bwd(codes, scales, grad_h, grad_gate_up, h=None, nrows=None, stream=None):
-    """Kept [G | U] and grad_h (R, F) bf16 -> grad_gate_up (R, 2F) bf16, h (R, F) bf16 of the kept values or None."""
+def moe_swiglu_checkpoint_bwd(codes, scales, grad_h, grad_gate_up, nrows=None, stream=None):
+    """Kept [G | U] and grad_h (R, F) bf16 -> grad_gate_up (R, 2F) bf16."""
     dev = _device_of(codes, "codes")
     R, F = _gate_up_sizes(codes, "codes")
     _launch(lib().moe_swiglu_checkpoint_bwd, dev, stream, R, F, *_kept_at(codes, scales, R, F, dev),
             _at(nrows, I32, 1, "nrows", dev), _at(grad_h, BF16, R * F, "grad_h", dev),
-            _at(grad_gate_up, BF16, R * 2 * F, "grad_gate_up", dev), _at(h, BF16, R * F, "h", dev))
+            _at(grad_gate_up, BF16, R * 2 * F, "grad_gate_up", dev))
 
 
-def moe_swiglu_checkpoint_restore(codes, scales, gate_up, h=None, nrows=None, stream=None):
-    """Kept [G | U] -> gate_up (R, 2F) bf16, h (R, F) bf16 of the kept values or None."""
-    dev = _device_of(codes, "codes")
-    R, F = _gate_up_sizes(codes, "codes")
-    _launch(lib().moe_swiglu_checkpoint_restore, dev, stream, R, F, *_kept_at(codes, scales, R, F, dev),
-            _at(nrows, I32, 1, "nrows", dev), _at(gate_up, BF16, R * 2 * F, "gate_up", dev),
-            _at(h, BF16, R * F, "h", dev))
+def moe_ffn_gate_up_fwd_checkpoint(shape, x, assist_info_for_combine, w_gate, w_up, ep_recv_counts, codes, scales, h_act,
+                                   stream=None):
+    """moe_ffn_gate_up_fwd_gather (without assist info moe_ffn_gate_up_fwd on expanded rows x) whose [G | U] are
+    kept in 8 bits: codes (capacity, 2F) int8, scales (capacity, 2F / 32) bf16 (checkpoint_buffers, halves=2)."""
+    dev, n, cap, F = _device_of(x, "x"), _shape_sizes(shape), shape.capacity, shape.F
+    gathered = assist_info_for_combine is not None
+    _launch(lib().moe_ffn_gate_up_fwd_checkpoint, dev, stream, ctypes.byref(shape),
+            _at(x, BF16, n["x" if gathered else "expand_x"], "x", dev),
+            _at(assist_info_for_combine, I32, n["assist_info_for_combine"], "assist_info_for_combine", dev),
+            _at(w_gate, BF16, n["w_gate"], "w_gate", dev), _at(w_up, BF16, n["w_up"], "w_up", dev),
+            _at(ep_recv_counts, I32, shape.num_experts, "ep_recv_counts", dev), *_kept_at(codes, scales, cap, F, dev),
+            _at(h_act, BF16, cap * F, "h_act", dev))
+
+
+def moe_ffn_down_bwd_data_checkpoint(shape, grad, assist_info_for_combine, row_weights, w_down, codes, scales,
+                                     ep_recv_counts, grad_gate_up, h_act, stream=None):
+    """moe_ffn_down_bwd_data_gather (without assist info and row weights moe_ffn_down_bwd_data on grad_y rows) from
+    kept [G | U], which also writes their h."""
+    dev, n, cap, F = _device_of(grad, "grad"), _shape_sizes(shape), shape.capacity, shape.F
+    gathered = assist_info_for_combine is not None
+    _launch(lib().moe_ffn_down_bwd_data_checkpoint, dev, stream, ctypes.byref(shape),
+            _at(grad, BF16, n["grad_out" if gathered else "grad_y"], "grad", dev),
+            _at(assist_info_for_combine, I32, n["assist_info_for_combine"], "assist_info_for_combine", dev),
+            _at(row_weights, F32, cap, "row_weights", dev), _at(w_down, BF16, n["w_down"], "w_down", dev),
+            *_kept_at(codes, scales, cap, F, dev), _at(ep_recv_counts, I32, shape.num_experts, "ep_recv_counts", dev),
+            _at(grad_gate_up, BF16, cap * 2 * F, "grad_gate_up", dev), _at(h_act, BF16, cap * F, "h_act", dev))
 
 
 def swiglu_checkpoint(gate_up):

@@ -1,88 +1,25 @@
-// Activation checkpoints in 8 bits: SwiGLU whose [G | U] input is kept as int8
-// codes for the backward, and the combine whose expert rows are.
-//
-// Kept rows: blocks of 32 consecutive columns (a row's last block may be shorter),
-// one bf16 scale each, s = bf16(amax / 127), code = rint(v * fp32(1 / s)); a kept
-// value is code * s, at most half a step from v.  A block whose scale would be
-// below 2^-126 keeps zeros (scale 0); one that holds an infinity or a NaN keeps
-// NaN (scale NaN, codes 0).  G and U are cut into blocks apart.
+// Activation checkpoints in 8 bits (the rule in kept.hpp): SwiGLU whose [G | U] input
+// is kept as int8 codes for the backward, and the combine whose expert rows are.
 //
 // All of it is bound by memory: each input is read once with 16-byte loads and
-// each output written once; the four lanes that hold a block's 32 columns find its
-// amax with two lane permutations on the values' bits, where an infinity and a NaN
-// order above every number.
+// each output written once.  On MI355X (a large copy moves 5.4 TB/s): SwiGLU of
+// 65536 rows, F = 480, 45 us forward and 41 backward, 32768 rows, F = 2048, 97 and 97
+// (5.6 TB/s); the combine of 8192 tokens, H = 1536, K = 8, 64 us (358 MB) and its
+// weights' gradient 24 (132 MB).
 #include <type_traits>
 
 #include "combine_token.hpp"
+#include "kept.hpp"
 
 namespace moe {
 namespace {
 
-constexpr int kCols = 32;  // columns of a block
+constexpr int kCols = kKeptCols;
 constexpr int kThreads = 256;
-
-// Scale bits and the multiplier of a block from the largest bf16 magnitude's bits.
-// The product with fp32(1/127) rounds to the same bf16 as amax / 127: that quotient
-// of an 8-bit mantissa by 127 is over 2^-17 of its value away from any midpoint of
-// two bf16 numbers.  One Newton step makes v_rcp_f32's result the rounded
-// reciprocal (tested for every scale).
-__device__ __forceinline__ uint32_t kept_scale(uint32_t amax16, float& inv) {
-  const uint32_t s = pk_bf16(__fmul_rn(bf2f(amax16), 1.0f / 127.0f), 0.f);
-  const float sf = bf2f(s), r = __builtin_amdgcn_rcpf(sf);
-  const bool some = s >= 0x0080u && amax16 < 0x7f80u;
-  inv = some ? __fmaf_rn(__fmaf_rn(-sf, r, 1.0f), r, r) : 0.f;
-  return amax16 >= 0x7f80u ? 0x7fc0u : (some ? s : 0u);
-}
-
-__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
-  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
-                                                                __builtin_bit_cast(u16x2, b)));
-}
-
-// Largest magnitude (bf16 bits) of the 32 values that four neighbouring lanes hold.
-__device__ __forceinline__ uint32_t block_amax(const uint4& v) {
-  constexpr uint32_t k = 0x7fff7fffu;
-  uint32_t m = max16x2(max16x2(v.x & k, v.y & k), max16x2(v.z & k, v.w & k));
-  m = max16x2(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, true));
-  m = max16x2(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, true));
-  const uint32_t hi = m >> 16, lo = m & 0xffffu;
-  return hi > lo ? hi : lo;
-}
-
-// The code of v in the low byte.  |v * inv| <= 127 (1 + 2^-8), so adding 1.5 * 2^23 to
-// the rounded product (no contraction: the rule rounds it to fp32 first) leaves rint
-// of it, ties to even, in the sum's low bits.
-__device__ __forceinline__ uint32_t code(float v, float inv) {
-#pragma clang fp contract(off)
-  const float p = v * inv;
-  return __float_as_uint(p + 12582912.0f);
-}
-
-// Four codes in a word.
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
-  const uint32_t lo = __builtin_amdgcn_perm(code(b, inv), code(a, inv), 0x0c0c0400u);
-  const uint32_t hi = __builtin_amdgcn_perm(code(d, inv), code(c, inv), 0x04000c0cu);
-  return lo | hi;
-}
-
-__device__ __forceinline__ uint2 codes8(const uint4& v, float inv) {
-  float f[8];
-  unpack8(v, f);
-  const uint32_t lo = codes4(f[0], f[1], f[2], f[3], inv), hi = codes4(f[4], f[5], f[6], f[7], inv);
-  // inv 0: zeros, or an infinity or a NaN among them (whose products are none)
-  return inv == 0.f ? make_uint2(0u, 0u) : make_uint2(lo, hi);
-}
-
-// Eight kept values: code * s, exact in fp32.
-__device__ __forceinline__ void kept8(const uint2& q, float s, float* f) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __fmul_rn((float)(int8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3))), s);
-}
 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
-enum Pass : int { KEEP, GRAD, RESTORE };
+enum Pass : int { KEEP, GRAD };
 
 struct SwigluArgs {
   const void* gate_up;   // KEEP: R x 2F
@@ -90,8 +27,7 @@ struct SwigluArgs {
   const int32_t* nrows;  // rows in use, or NULL
   int8_t* codes;         // R x 2F
   uint16_t* scales;      // R x 2 x nb
-  void* out;             // GRAD: dG|dU, RESTORE: G|U (R x 2F)
-  void* h;               // R x F, or NULL
+  void* out;             // KEEP: h (R x F), GRAD: dG|dU (R x 2F)
   int64_t R, F, nb;
   // units of eight columns, `cols` of them a row of whole blocks
   uint32_t cols, step_rows, step_cols;  // kThreads units on: rows and columns
@@ -110,11 +46,10 @@ __device__ __forceinline__ uint4 pack8h(const float* f) {
   return make_uint4(pk_bf16(f[0], f[1]), pk_bf16(f[2], f[3]), pk_bf16(f[4], f[5]), pk_bf16(f[6], f[7]));
 }
 
-__device__ __forceinline__ void swiglu_grad(float g, float u, float d, float& dg, float& du, float& h) {
+__device__ __forceinline__ void swiglu_grad(float g, float u, float d, float& dg, float& du) {
   const float sg = sigmoid(g), si = g * sg;
   dg = d * u * __fmaf_rn(si, 1.0f - sg, sg);
   du = d * si;
-  h = si * u;
 }
 
 // n of the eight bf16 at p (any address; zeros behind them), and their stores.  A
@@ -193,7 +128,7 @@ __device__ __forceinline__ void store8(int8_t* p, const uint2& v, int n) {
 // matrix 16-byte aligned; otherwise a row is rounded up to whole blocks (units past
 // F hold zeros) and accesses may begin anywhere: 32768 rows of 1001 columns 69 us,
 // with a lane for each column 158.
-template <int PASS, bool H, bool WHOLE>
+template <int PASS, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
   constexpr int kUnits = 2;
   const int64_t rows = rows_of(a), F = a.F;
@@ -240,14 +175,12 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
         sc[0] = (uint16_t)sg;
         sc[a.nb] = (uint16_t)su;
       }
-      if constexpr (H) {
-        float gf[8], uf[8];
-        unpack8(g[i], gf);
-        unpack8(u[i], uf);
+      float gf[8], uf[8];
+      unpack8(g[i], gf);
+      unpack8(u[i], uf);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) gf[j] = gf[j] * sigmoid(gf[j]) * uf[j];
-        store8<WHOLE>(static_cast<uint16_t*>(a.h) + hcol(i), pack8h(gf), n);
-      }
+      for (int j = 0; j < 8; ++j) gf[j] = gf[j] * sigmoid(gf[j]) * uf[j];
+      store8<WHOLE>(static_cast<uint16_t*>(a.out) + hcol(i), pack8h(gf), n);
     }
   } else {
     uint2 qg[kUnits], qu[kUnits];
@@ -261,29 +194,21 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
         qu[i] = load8<WHOLE>(a.codes + gate(i) + F, count(i));
         sg[i] = sc[0];
         su[i] = sc[a.nb];
-        if constexpr (PASS == GRAD)
-          dh[i] = load8<WHOLE>(static_cast<const uint16_t*>(a.grad_h) + hcol(i), count(i));
+        dh[i] = load8<WHOLE>(static_cast<const uint16_t*>(a.grad_h) + hcol(i), count(i));
       }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       if (row[i] >= rows) continue;
-      float g[8], u[8], h[8];
+      float g[8], u[8], d[8];
       kept8(qg[i], bf2f(sg[i]), g);
       kept8(qu[i], bf2f(su[i]), u);
-      if constexpr (PASS == GRAD) {
-        float d[8];
-        unpack8(dh[i], d);
+      unpack8(dh[i], d);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) swiglu_grad(g[j], u[j], d[j], g[j], u[j], h[j]);
-      } else if constexpr (H) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = g[j] * sigmoid(g[j]) * u[j];
-      }
+      for (int j = 0; j < 8; ++j) swiglu_grad(g[j], u[j], d[j], g[j], u[j]);
       const int n = count(i);
       uint16_t* out = static_cast<uint16_t*>(a.out) + gate(i);
       store8<WHOLE>(out, pack8h(g), n);
       store8<WHOLE>(out + F, pack8h(u), n);
-      if constexpr (H) store8<WHOLE>(static_cast<uint16_t*>(a.h) + hcol(i), pack8h(h), n);
     }
   }
 }
@@ -476,8 +401,7 @@ constexpr int64_t kMaxThreads = 0xffffff00;
 template <int PASS>
 moe_status launch_swiglu(SwigluArgs a, void* stream) {
   a.nb = (a.F + kCols - 1) / kCols;
-  const void* io = PASS == KEEP ? a.gate_up : a.out;
-  const bool whole = a.F % kCols == 0 && aligned16(io) && aligned16(a.h) && aligned16(a.grad_h) &&
+  const bool whole = a.F % kCols == 0 && aligned16(a.gate_up) && aligned16(a.grad_h) && aligned16(a.out) &&
                      reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
   a.cols = (uint32_t)(a.nb * (kCols / 8));
   a.step_rows = kThreads / a.cols;
@@ -485,14 +409,8 @@ moe_status launch_swiglu(SwigluArgs a, void* stream) {
   const int64_t units = a.R * (int64_t)a.cols;
   if (units / 2 > kMaxThreads) return MOE_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)((units + 2 * kThreads - 1) / (2 * kThreads)));
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, as_stream(stream), a); };
-  if (whole) {
-    if (a.h) go(k_swiglu_rows<PASS, true, true>);
-    else go(k_swiglu_rows<PASS, false, true>);
-  } else {
-    if (a.h) go(k_swiglu_rows<PASS, true, false>);
-    else go(k_swiglu_rows<PASS, false, false>);
-  }
+  if (whole) hipLaunchKernelGGL((k_swiglu_rows<PASS, true>), grid, dim3(kThreads), 0, as_stream(stream), a);
+  else hipLaunchKernelGGL((k_swiglu_rows<PASS, false>), grid, dim3(kThreads), 0, as_stream(stream), a);
   return launch_status();
 }
 
@@ -512,13 +430,13 @@ extern "C" moe_status moe_swiglu_checkpoint_fwd(int64_t R, int64_t F, const void
   const moe_status st = check_swiglu(R, F);
   if (st != MOE_OK) return st;
   if (R == 0) return MOE_OK;
-  if (!gate_up || !codes || !scales) return MOE_ERR_NULL_ARG;
+  if (!gate_up || !h || !codes || !scales) return MOE_ERR_NULL_ARG;
   SwigluArgs a{};
   a.gate_up = gate_up;
   a.nrows = nrows;
   a.codes = codes;
   a.scales = static_cast<uint16_t*>(scales);
-  a.h = h;
+  a.out = h;
   a.R = R;
   a.F = F;
   return launch_swiglu<KEEP>(a, stream);
@@ -526,7 +444,7 @@ extern "C" moe_status moe_swiglu_checkpoint_fwd(int64_t R, int64_t F, const void
 
 extern "C" moe_status moe_swiglu_checkpoint_bwd(int64_t R, int64_t F, const int8_t* codes, const void* scales,
                                                 const int32_t* nrows, const void* grad_h, void* grad_gate_up,
-                                                void* h, void* stream) {
+                                                void* stream) {
   const moe_status st = check_swiglu(R, F);
   if (st != MOE_OK) return st;
   if (R == 0) return MOE_OK;
@@ -537,27 +455,9 @@ extern "C" moe_status moe_swiglu_checkpoint_bwd(int64_t R, int64_t F, const int8
   a.codes = const_cast<int8_t*>(codes);
   a.scales = static_cast<uint16_t*>(const_cast<void*>(scales));
   a.out = grad_gate_up;
-  a.h = h;
   a.R = R;
   a.F = F;
   return launch_swiglu<GRAD>(a, stream);
-}
-
-extern "C" moe_status moe_swiglu_checkpoint_restore(int64_t R, int64_t F, const int8_t* codes, const void* scales,
-                                                    const int32_t* nrows, void* gate_up, void* h, void* stream) {
-  const moe_status st = check_swiglu(R, F);
-  if (st != MOE_OK) return st;
-  if (R == 0) return MOE_OK;
-  if (!codes || !scales || !gate_up) return MOE_ERR_NULL_ARG;
-  SwigluArgs a{};
-  a.nrows = nrows;
-  a.codes = const_cast<int8_t*>(codes);
-  a.scales = static_cast<uint16_t*>(const_cast<void*>(scales));
-  a.out = gate_up;
-  a.h = h;
-  a.R = R;
-  a.F = F;
-  return launch_swiglu<RESTORE>(a, stream);
 }
 
 extern "C" moe_status moe_combine_checkpoint(const moe_shape* s, const void* y, const int32_t* topk_idx,

@@ -46,6 +46,7 @@
 // groups of row tiles when the output is wide) and every XCD gets a block of
 // every expert (weight gradients).
 #include "common.hpp"
+#include "kept.hpp"
 
 namespace moe {
 namespace {
@@ -109,6 +110,11 @@ struct GemmArgs {
   bf16_t* C0;
   bf16_t* C1;
   const bf16_t* aux;
+  // KEEP: [G | U] as 8-bit checkpoints (codes rows x 2F, scales rows x 2 x F/32) in
+  // place of C1 and aux, and the backward's h (rows x F)
+  int8_t* kq;
+  uint16_t* ks;
+  bf16_t* kh;
   float* W0;
   float* W1;
   // fp8 operands: e4m3 codes, A scales per (row, 128 of K) stored K-block major
@@ -226,12 +232,17 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // whole K, the scales applied once after the loop.
 // MX (with FP8 set): e4m3 codes with E8M0 scales per 32 codes along K, applied by
 // the MFMA itself (no per-step rescale).
-template <int MODE, int BM, int BN, bool FP8, int BK, int S_, int WM_, int WN_, bool I8, bool MX>
+// KEEP (bf16): the gate/up forward leaves [G | U] in 8 bits, and the down data
+// gradient reads them so and writes the kept values' h beside dG | dU.
+template <int MODE, int BM, int BN, bool FP8, int BK, int S_, int WM_, int WN_, bool I8, bool MX, bool KEEP>
 __global__ __launch_bounds__((Cfg<MODE, BM, BN, FP8, BK, S_, WM_, WN_>::kThreads),
                              (Cfg<MODE, BM, BN, FP8, BK, S_, WM_, WN_>::kMinBlocks)) void k_gemm(GemmArgs g) {
   using C = Cfg<MODE, BM, BN, FP8, BK, S_, WM_, WN_>;
   static_assert(!I8 || (FP8 && (MODE == GATE_UP_FWD || MODE == DOWN_FWD)), "int8: forward GEMMs on the 8-bit path");
   static_assert(!MX || (FP8 && !I8 && MODE <= GATE_UP_BWD_DATA), "MX: row-grouped GEMMs on the 8-bit path");
+  static_assert(!KEEP || (!FP8 && (MODE == GATE_UP_FWD ? C::kEpiOnePass || C::kEpiGU2
+                                                       : MODE == DOWN_BWD_DATA && !C::kEpiOnePass)),
+                "8-bit checkpoints: the bf16 gate/up forward and down data gradient");
   auto swz = [](int r) { return swzw<BK>(r); };
   auto lds_off = [](int r, int c) { return lds_offw<BK>(r, c); };
   constexpr bool KGROUP = C::KGROUP, B_KC = C::B_KC;
@@ -1135,6 +1146,24 @@ __global__ __launch_bounds__((Cfg<MODE, BM, BN, FP8, BK, S_, WM_, WN_>::kThreads
   auto store_tile_nt = [&](const bf16_t* t, bf16_t* dst, int64_t ldd, int64_t ncols) {
     store_tile_w(t, CW, CP, dst, ldd, ncols, std::true_type());
   };
+  // the staged G (half 0) or U (half 1) tile as 8-bit checkpoints: eight columns a
+  // thread, four threads a block (F is a multiple of 32: whole blocks)
+  auto keep_tile = [&](const bf16_t* t, int half) {
+    const int64_t nb = g.F / kKeptCols;
+    for (int v = tid; v < BM * (CW / 8); v += kThreads) {
+      const int row = v / (CW / 8), c8 = (v % (CW / 8)) * 8;
+      const uint4 val = *reinterpret_cast<const uint4*>(t + row * CP + c8);
+      float inv;
+      const uint32_t s = kept_scale(block_amax(val), inv);
+      if (row >= rows_valid || n0 + c8 >= g.F) continue;
+      const uint2 q = codes8(val, inv);
+      typedef unsigned int u32x2s __attribute__((ext_vector_type(2)));
+      __builtin_nontemporal_store(u32x2s{q.x, q.y}, reinterpret_cast<u32x2s*>(
+          g.kq + (row0 + row) * 2 * g.F + half * g.F + n0 + c8));
+      if ((c8 & (kKeptCols - 1)) == 0)
+        g.ks[(row0 + row) * 2 * nb + half * nb + (n0 + c8) / kKeptCols] = (uint16_t)s;
+    }
+  };
   // SwiGLU backward: the saved G and U columns [c0, c0 + W) of the tile's rows
   // into LDS (G at smem, U at smem + BM * P, row pitch P).  A thread's 16-byte
   // loads go out in batches of eight before the batch's first LDS write, so
@@ -1147,6 +1176,32 @@ __global__ __launch_bounds__((Cfg<MODE, BM, BN, FP8, BK, S_, WM_, WN_>::kThreads
     static_assert(kChunks % (kBatch * kThreads) == 0, "whole batches of eight chunks per thread");
 #pragma unroll 1
     for (int b0 = 0; b0 < kChunks; b0 += kBatch * kThreads) {
+      if constexpr (KEEP) {
+        // the kept values, rounded to bf16
+        uint2 v[kBatch];
+        uint32_t sc[kBatch];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const int idx = b0 + q * kThreads + tid;
+          const int t = idx / (BM * (W / 8)), w = idx % (BM * (W / 8));
+          const int row = w / (W / 8), c8 = (w % (W / 8)) * 8;
+          const int rr = row < rows_valid ? row : rows_valid - 1;
+          const int64_t col = (t ? g.F : 0) + (c0 + c8 < g.N ? c0 + c8 : g.N - 8);
+          v[q] = *reinterpret_cast<const uint2*>(g.kq + (row0 + rr) * 2 * g.F + col);
+          sc[q] = g.ks[(row0 + rr) * 2 * (g.F / kKeptCols) + col / kKeptCols];
+        }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const int idx = b0 + q * kThreads + tid;
+          const int t = idx / (BM * (W / 8)), w = idx % (BM * (W / 8));
+          const int row = w / (W / 8), c8 = (w % (W / 8)) * 8;
+          float f[8];
+          kept8(v[q], bf2f(sc[q]), f);
+          *reinterpret_cast<uint4*>(smem + t * BM * P + row * P + c8) =
+              make_uint4(pk_bf16(f[0], f[1]), pk_bf16(f[2], f[3]), pk_bf16(f[4], f[5]), pk_bf16(f[6], f[7]));
+        }
+        continue;
+      }
       uint4 v[kBatch];
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
@@ -1220,7 +1275,8 @@ __global__ __launch_bounds__((Cfg<MODE, BM, BN, FP8, BK, S_, WM_, WN_>::kThreads
         }
     __syncthreads();
     store_tile(th, g.C0 + n0, g.F, g.F - n0);
-    store_tile_nt(tg, g.C1 + n0, 2 * g.F, g.F - n0);
+    if constexpr (KEEP) keep_tile(tg, 0);
+    else store_tile_nt(tg, g.C1 + n0, 2 * g.F, g.F - n0);
     // (the per-token fp8 codes of h, qc, come from the 128 x 128 fp8 tiles only)
     if constexpr (MX)
       if (g.qmx) mx_h(th);
@@ -1236,7 +1292,8 @@ __global__ __launch_bounds__((Cfg<MODE, BM, BN, FP8, BK, S_, WM_, WN_>::kThreads
                                                      acc[i][j + TJ / 2][4 * t + 2], acc[i][j + TJ / 2][4 * t + 3]);
         }
     __syncthreads();
-    store_tile_nt(th, g.C1 + g.F + n0, 2 * g.F, g.F - n0);
+    if constexpr (KEEP) keep_tile(th, 1);
+    else store_tile_nt(th, g.C1 + g.F + n0, 2 * g.F, g.F - n0);
   } else if constexpr (MODE == GATE_UP_FWD && !C::kEpiOnePass) {
     // h, then G, then U through one staging tile
     bf16_t* ct = smem;
@@ -1284,19 +1341,39 @@ __global__ __launch_bounds__((Cfg<MODE, BM, BN, FP8, BK, S_, WM_, WN_>::kThreads
               const uint2 up = *reinterpret_cast<const uint2*>(tu + o);
               const float gv[4] = {bf2f(gp.x & 0xffffu), bf2f(gp.x >> 16), bf2f(gp.y & 0xffffu), bf2f(gp.y >> 16)};
               const float uv[4] = {bf2f(up.x & 0xffffu), bf2f(up.x >> 16), bf2f(up.y & 0xffffu), bf2f(up.y >> 16)};
-              float dg[4], du[4];
+              float dg[4], du[4], hk[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const float c = acc[i][j][4 * t + q];
                 const float sg = 1.0f / (1.0f + __expf(-gv[q]));
                 dg[q] = c * uv[q] * sg * (1.0f + gv[q] * (1.0f - sg));
                 du[q] = c * (gv[q] * sg);
+                if constexpr (KEEP) {
+                  hk[q] = gv[q] * sg * uv[q];
+                  acc[i][j][4 * t + q] = du[q];
+                }
               }
               *reinterpret_cast<uint2*>(tg + o) = pack4(dg[0], dg[1], dg[2], dg[3]);
-              *reinterpret_cast<uint2*>(tu + o) = pack4(du[0], du[1], du[2], du[3]);
+              *reinterpret_cast<uint2*>(tu + o) = KEEP ? pack4(hk[0], hk[1], hk[2], hk[3])
+                                                       : pack4(du[0], du[1], du[2], du[3]);
             }
       }
       __syncthreads();
+      if constexpr (KEEP) {
+        // h leaves through U's tile first; dU waits in the accumulators
+        store_tile_w(tu, WC, CPH, g.kh + c0, g.F, g.N - c0, std::false_type());
+        __syncthreads();
+        if (wn == pc)
+#pragma unroll
+          for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                *reinterpret_cast<uint2*>(tu + tm(i) * CPH + tn(j, t) - pc * WC) = pack4(
+                    acc[i][j][4 * t], acc[i][j][4 * t + 1], acc[i][j][4 * t + 2], acc[i][j][4 * t + 3]);
+        __syncthreads();
+      }
       store_tile_w(tg, WC, CPH, g.C0 + c0, 2 * g.F, g.N - c0, std::false_type());
       store_tile_w(tu, WC, CPH, g.C0 + g.F + c0, 2 * g.F, g.N - c0, std::false_type());
       __syncthreads();
@@ -1326,8 +1403,13 @@ __global__ __launch_bounds__((Cfg<MODE, BM, BN, FP8, BK, S_, WM_, WN_>::kThreads
         }
     __syncthreads();
     store_tile(th, g.C0 + n0, g.F, g.F - n0);
-    store_tile_nt(tg, g.C1 + n0, 2 * g.F, g.F - n0);
-    store_tile_nt(tu, g.C1 + g.F + n0, 2 * g.F, g.F - n0);
+    if constexpr (KEEP) {
+      keep_tile(tg, 0);
+      keep_tile(tu, 1);
+    } else {
+      store_tile_nt(tg, g.C1 + n0, 2 * g.F, g.F - n0);
+      store_tile_nt(tu, g.C1 + g.F + n0, 2 * g.F, g.F - n0);
+    }
     if constexpr (FP8) {
       if (g.qmx) mx_h(th);
       if (g.qc) {
@@ -1577,7 +1659,7 @@ __global__ __launch_bounds__((Cfg<MODE, BM, BN, FP8, BK, S_, WM_, WN_>::kThreads
 }
 
 template <int MODE, int BM, int BN, bool FP8, int BK = 64, int S = 2, int WM = 2, int WN = 2, bool I8 = false,
-          bool MX = false>
+          bool MX = false, bool KEEP = false>
 moe_status launch_cfg(GemmArgs g, const moe_shape* s, hipStream_t strm) {
   const int64_t ncols = MODE == GATE_UP_FWD ? g.F : g.N;
   const int64_t bn_cols = MODE == GATE_UP_FWD ? BN / 2 : BN;
@@ -1612,12 +1694,12 @@ moe_status launch_cfg(GemmArgs g, const moe_shape* s, hipStream_t strm) {
   if (g.tiles == 0) return MOE_OK;
   const int64_t grid = (g.tiles + 7) / 8 * 8;  // weight gradients: already 8 * E * block
   if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
-  hipLaunchKernelGGL((k_gemm<MODE, BM, BN, FP8, BK, S, WM, WN, I8, MX>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((k_gemm<MODE, BM, BN, FP8, BK, S, WM, WN, I8, MX, KEEP>), dim3((unsigned)grid),
                      dim3(Cfg<MODE, BM, BN, FP8, BK, S, WM, WN>::kThreads), 0, strm, g);
   return launch_status();
 }
 
-template <int MODE, bool FP8 = false, bool I8 = false, bool MX = false>
+template <int MODE, bool FP8 = false, bool I8 = false, bool MX = false, bool KEEP = false>
 moe_status launch(GemmArgs& g, const moe_shape* s, hipStream_t strm) {
   // Tile shapes per GEMM kind, chosen by measurement on MI355X (MoE layers at
   // H = 1536 / F = 480 and H = 7168 / F = 2048): 128 x 256 tiles (wave tiles
@@ -1666,8 +1748,8 @@ moe_status launch(GemmArgs& g, const moe_shape* s, hipStream_t strm) {
   } else if constexpr (MODE == GATE_UP_BWD_DATA || MODE == DOWN_BWD_W) {
     return launch_cfg<MODE, 128, 256, false, 32, 3>(g, s, strm);
   } else if constexpr (MODE == DOWN_BWD_DATA) {
-    if (g.N >= 1024) return launch_cfg<MODE, 128, 256, false, 32, 3>(g, s, strm);
-    return launch_cfg<MODE, 128, 128, false, 32, 3>(g, s, strm);
+    if (g.N >= 1024) return launch_cfg<MODE, 128, 256, false, 32, 3, 2, 2, false, false, KEEP>(g, s, strm);
+    return launch_cfg<MODE, 128, 128, false, 32, 3, 2, 2, false, false, KEEP>(g, s, strm);
   } else {
     // forward: 256 x 256 tiles of eight waves (wave tiles 128 x 64, one
     // workgroup of 128 KB LDS per CU) do a fifth more work per memory latency
@@ -1679,14 +1761,14 @@ moe_status launch(GemmArgs& g, const moe_shape* s, hipStream_t strm) {
     const int64_t t128 = (s->capacity / 128 + s->num_experts) * ((ncols + cols128 - 1) / cols128);
     const int64_t t256 = (s->capacity / 256 + s->num_experts) * ((ncols + cols256 - 1) / cols256);
     const int64_t r128 = (t128 + 2 * kCUs - 1) / (2 * kCUs), r256 = (t256 + kCUs - 1) / kCUs;
-    if (17 * r256 < 10 * r128) return launch_cfg<MODE, 256, 256, false, 64, 2, 2, 4>(g, s, strm);
+    if (17 * r256 < 10 * r128) return launch_cfg<MODE, 256, 256, false, 64, 2, 2, 4, false, false, KEEP>(g, s, strm);
     // a decode-sized batch (at most 256 routed rows per expert on average)
     // streams each expert's gate/up weights once when its rows fit one 256-row
     // tile: 7-8% faster at T = 512, H = 7168, F = 2048, E = 32, K = 8 (the down
     // forward there was 4% slower on them and keeps the 128 x 128 tiles)
     if (MODE == GATE_UP_FWD && s->T * s->K <= 256 * (int64_t)s->num_experts)
-      return launch_cfg<MODE, 256, 256, false, 64, 2, 2, 4>(g, s, strm);
-    return launch_cfg<MODE, 128, 128, false>(g, s, strm);
+      return launch_cfg<MODE, 256, 256, false, 64, 2, 2, 4, false, false, KEEP>(g, s, strm);
+    return launch_cfg<MODE, 128, 128, false, 64, 2, 2, 2, false, false, KEEP>(g, s, strm);
   }
 }
 
@@ -2003,6 +2085,79 @@ extern "C" moe_status moe_grouped_ffn_bwd(const moe_shape* s, const void* grad_y
   if (st != MOE_OK) return st;
   return moe_ffn_gate_up_bwd_weight(s, grad_gate_up, expand_x, ep_recv_counts, grad_w_gate,
                                     grad_w_up, stream);
+}
+
+// --------------------------------------------------------- checkpoints in 8 bits
+
+namespace {
+// What the entries below need of their kept rows, beside the shape.
+moe_status check_kept(const moe_shape* s, const void* gathered, const void* codes, const void* scales) {
+  if (gathered && (s->T + 1) * s->H * 2 > 0x7ffffff0LL) return MOE_ERR_UNSUPPORTED;
+  if (s->capacity > 0 && (!codes || !scales)) return MOE_ERR_NULL_ARG;
+  return reinterpret_cast<uintptr_t>(codes) % 8 ? MOE_ERR_BAD_SHAPE : MOE_OK;
+}
+}  // namespace
+
+extern "C" moe_status moe_ffn_gate_up_fwd_checkpoint(const moe_shape* s, const void* x, const int32_t* assist,
+                                                     const void* w_gate, const void* w_up,
+                                                     const int32_t* ep_recv_counts, int8_t* codes, void* scales,
+                                                     void* h_act, void* stream) {
+  moe_status st = check_ffn_shape(s);
+  if (st != MOE_OK) return st;
+  if (!w_gate || !w_up || !ep_recv_counts) return MOE_ERR_NULL_ARG;
+  st = check_kept(s, assist, codes, scales);
+  if (st != MOE_OK || s->capacity == 0) return st;
+  if (!x || !h_act) return MOE_ERR_NULL_ARG;
+  GemmArgs g = base_args(s, ep_recv_counts);
+  g.A = static_cast<const bf16_t*>(x);
+  if (assist) {
+    g.gather = assist + s->T * s->K;  // row -> slot
+    g.gK = s->K;
+    g.gbytes = s->T * s->H * 2;
+  }
+  g.lda = s->H;
+  g.B0 = static_cast<const bf16_t*>(w_gate);
+  g.B1 = static_cast<const bf16_t*>(w_up);
+  g.ldb = s->H;
+  g.bstride = s->F * s->H;
+  g.N = s->F;
+  g.Kd = s->H;
+  g.C0 = static_cast<bf16_t*>(h_act);
+  g.kq = codes;
+  g.ks = static_cast<uint16_t*>(scales);
+  return launch<GATE_UP_FWD, false, false, false, true>(g, s, as_stream(stream));
+}
+
+extern "C" moe_status moe_ffn_down_bwd_data_checkpoint(const moe_shape* s, const void* grad, const int32_t* assist,
+                                                       const float* row_weights, const void* w_down,
+                                                       const int8_t* codes, const void* scales,
+                                                       const int32_t* ep_recv_counts, void* grad_gate_up,
+                                                       void* h_act, void* stream) {
+  moe_status st = check_ffn_shape(s);
+  if (st != MOE_OK) return st;
+  if (!w_down || !ep_recv_counts) return MOE_ERR_NULL_ARG;
+  st = check_kept(s, assist, codes, scales);
+  if (st != MOE_OK || s->capacity == 0) return st;
+  if (!grad || !grad_gate_up || !h_act || (assist && !row_weights)) return MOE_ERR_NULL_ARG;
+  GemmArgs g = base_args(s, ep_recv_counts);
+  g.A = static_cast<const bf16_t*>(grad);
+  if (assist) {
+    g.gather = assist + s->T * s->K;
+    g.gK = s->K;
+    g.gbytes = s->T * s->H * 2;
+    g.rowsc = row_weights;
+  }
+  g.lda = s->H;
+  g.B0 = static_cast<const bf16_t*>(w_down);
+  g.ldb = s->F;
+  g.bstride = s->H * s->F;
+  g.N = s->F;
+  g.Kd = s->H;
+  g.kq = const_cast<int8_t*>(codes);
+  g.ks = static_cast<uint16_t*>(const_cast<void*>(scales));
+  g.C0 = static_cast<bf16_t*>(grad_gate_up);
+  g.kh = static_cast<bf16_t*>(h_act);
+  return launch<DOWN_BWD_DATA, false, false, false, true>(g, s, as_stream(stream));
 }
 
 // ----------------------------------------------------------------------------- fp8 entries

@@ -220,7 +220,7 @@ struct SwigluNode : torch::autograd::Function<SwigluNode> {
       const Tensor grad_h = grads[0].contiguous();
       grad = at::empty(ctx->saved_data["sizes"].toIntVector(), grad_h.options());
       check(moe_swiglu_checkpoint_bwd(codes.size(0), codes.size(1) / 2, codes.data_ptr<int8_t>(), scales.data_ptr(),
-                                      nullptr, grad_h.data_ptr(), grad.data_ptr(), nullptr, stream_of(codes)));
+                                      nullptr, grad_h.data_ptr(), grad.data_ptr(), stream_of(codes)));
     }
     return once({grad});
   }

@@ -921,23 +921,34 @@ moe_status moe_balance_bwd(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs
 
 /* moe_swiglu_checkpoint_fwd - h = silu(G) * U and the kept [G | U].
  *  in   gate_up (R, 2F) bf16
- *  out  h (R, F) bf16 or NULL; codes (R, 2F) int8, scales (R, 2, ceil(F / 32)) bf16 */
+ *  out  h (R, F) bf16; codes (R, 2F) int8, scales (R, 2, ceil(F / 32)) bf16 */
 moe_status moe_swiglu_checkpoint_fwd(int64_t R, int64_t F, const void* gate_up, const int32_t* nrows, void* h,
                                      int8_t* codes, void* scales, void* stream);
 
 /* moe_swiglu_checkpoint_bwd - SwiGLU's backward from the kept G, U:
  *   dU = grad_h silu(G), dG = grad_h U sigmoid(G) (1 + G (1 - sigmoid(G)))
  *  in   grad_h (R, F) bf16
- *  out  grad_gate_up (R, 2F) bf16: [dG | dU]; h (R, F) bf16 of the kept values, or NULL */
+ *  out  grad_gate_up (R, 2F) bf16: [dG | dU] */
 moe_status moe_swiglu_checkpoint_bwd(int64_t R, int64_t F, const int8_t* codes, const void* scales,
-                                     const int32_t* nrows, const void* grad_h, void* grad_gate_up, void* h,
-                                     void* stream);
+                                     const int32_t* nrows, const void* grad_h, void* grad_gate_up, void* stream);
 
-/* moe_swiglu_checkpoint_restore - the kept rows in bf16, for the GEMMs that read
- * gate_up_save and h_act.
- *  out  gate_up (R, 2F) bf16; h (R, F) bf16 of the kept values, or NULL */
-moe_status moe_swiglu_checkpoint_restore(int64_t R, int64_t F, const int8_t* codes, const void* scales,
-                                         const int32_t* nrows, void* gate_up, void* h, void* stream);
+/* moe_ffn_gate_up_fwd_checkpoint - moe_ffn_gate_up_fwd_gather, or without assist
+ * moe_ffn_gate_up_fwd on expanded rows x, whose [G | U] leave the GEMM in 8 bits: the
+ * codes and scales of the bf16 gate_up_save that those write (codes (capacity, 2F) on
+ * an 8-byte boundary, else MOE_ERR_BAD_SHAPE; scales (capacity, 2, F / 32)).
+ *  out  codes, scales, h_act (capacity, F) bf16.  One launch. */
+moe_status moe_ffn_gate_up_fwd_checkpoint(const moe_shape* s, const void* x, const int32_t* assist,
+                                          const void* w_gate, const void* w_up, const int32_t* ep_recv_counts,
+                                          int8_t* codes, void* scales, void* h_act, void* stream);
+
+/* moe_ffn_down_bwd_data_checkpoint - moe_ffn_down_bwd_data_gather on grad_out rows, or
+ * without assist and row_weights moe_ffn_down_bwd_data on grad_y rows, from kept
+ * [G | U] (rounded to bf16), which also writes their h for the down weight gradient.
+ *  out  grad_gate_up (capacity, 2F), h_act (capacity, F) bf16.  One launch. */
+moe_status moe_ffn_down_bwd_data_checkpoint(const moe_shape* s, const void* grad, const int32_t* assist,
+                                            const float* row_weights, const void* w_down, const int8_t* codes,
+                                            const void* scales, const int32_t* ep_recv_counts, void* grad_gate_up,
+                                            void* h_act, void* stream);
 
 /* moe_combine_checkpoint - moe_combine (out bit for bit) that keeps every routed
  * row of y in 8 bits on its way, so y need not outlive the call.

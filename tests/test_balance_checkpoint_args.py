@@ -63,17 +63,36 @@ def test_balance_workspace(L):
 
 @pytest.mark.parametrize("kw,expect", [
     (dict(R=-1), BAD_SHAPE), (dict(R=(1 << 40) + 1), BAD_SHAPE), (dict(F=0), BAD_SHAPE), (dict(F=(1 << 20) + 1), BAD_SHAPE),
-    (dict(R=0, a=N, b=N, c=N), OK), (dict(a=N), NULL_ARG), (dict(b=N), NULL_ARG), (dict(c=N), NULL_ARG),
+    (dict(R=0, a=N, b=N, c=N, d=N), OK), (dict(a=N), NULL_ARG), (dict(b=N), NULL_ARG), (dict(c=N), NULL_ARG),
+    (dict(d=N), NULL_ARG),
     (dict(R=1 << 38, F=32), UNSUPPORTED), (dict(R=1 << 33, F=7), UNSUPPORTED)])
 def test_swiglu_entries_refuse(L, kw, expect):
-    a = dict(R=8, F=64, a=P(), b=P(), c=P())
+    a = dict(R=8, F=64, a=P(), b=P(), c=P(), d=P())
     a.update(kw)
     R, F = a["R"], a["F"]
-    assert L.moe_swiglu_checkpoint_fwd(R, F, a["a"], N, P(), a["b"], a["c"], N) == expect
-    assert L.moe_swiglu_checkpoint_bwd(R, F, a["a"], a["b"], N, a["c"], P(), P(), N) == expect
-    assert L.moe_swiglu_checkpoint_restore(R, F, a["a"], a["b"], N, a["c"], P(), N) == expect
-    if expect == NULL_ARG:
-        assert L.moe_swiglu_checkpoint_bwd(R, F, P(), P(), N, P(), N, P(), N) == NULL_ARG
+    assert L.moe_swiglu_checkpoint_fwd(R, F, a["a"], N, a["d"], a["b"], a["c"], N) == expect
+    assert L.moe_swiglu_checkpoint_bwd(R, F, a["a"], a["b"], N, a["c"], a["d"], N) == expect
+
+
+def test_gemm_entries_refuse(L):
+    def fwd(shape, **kw):
+        a = dict(x=P(), assist=P(), wg=P(), wu=P(), recv=P(), c=P(), s=P(), h=P())
+        a.update(kw)
+        return L.moe_ffn_gate_up_fwd_checkpoint(ctypes.byref(shape), *a.values(), N)
+
+    def bwd(shape, **kw):
+        a = dict(x=P(), assist=P(), rw=P(), wd=P(), c=P(), s=P(), recv=P(), ggu=P(), h=P())
+        a.update(kw)
+        return L.moe_ffn_down_bwd_data_checkpoint(ctypes.byref(shape), *a.values(), N)
+
+    ok = dm.make_shape(8, 64, 2, 4, F=64)
+    for f, names in ((fwd, ("x", "wg", "wu", "recv", "c", "s", "h")),
+                     (bwd, ("x", "rw", "wd", "c", "s", "recv", "ggu", "h"))):
+        for name in names:
+            assert f(ok, **{name: N}) == NULL_ARG, name
+        assert f(dm.make_shape(8, 64, 2, 4, F=48)) == BAD_SHAPE
+        assert f(ok, c=P(0x10004)) == BAD_SHAPE
+        assert f(dm.make_shape(1 << 20, 1024, 2, 4, F=64)) == UNSUPPORTED  # 31-bit offsets into gathered rows
 
 
 def test_combine_entries_refuse(L):

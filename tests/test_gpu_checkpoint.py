@@ -83,22 +83,9 @@ def check_swiglu(gu, seed=0):
     same(scales, qs)
     near("h", h, *swiglu64(gu[:, :F].double(), gu[:, F:].double()))
     v = kept(qc[:, :F], qs[:, :qs.shape[1] // 2]), kept(qc[:, F:], qs[:, qs.shape[1] // 2:])
-    grad, hk = torch.empty_like(x), torch.empty_like(h)
-    dm.moe_swiglu_checkpoint_bwd(codes, scales, d.to(DEV), grad, hk)
+    grad = torch.empty_like(x)
+    dm.moe_swiglu_checkpoint_bwd(codes, scales, d.to(DEV), grad)
     near("grad", grad, *swiglu64(*v, d.double()))
-    near("kept h", hk, *swiglu64(*v))
-    back, hr = torch.empty_like(x), torch.empty_like(h)
-    dm.moe_swiglu_checkpoint_restore(codes, scales, back, hr)
-    same(back, torch.cat(v, 1).bfloat16())
-    same(hr, hk)
-    # without the optional outputs: the same bits
-    c2, s2 = dm.checkpoint_buffers(R, F, DEV, halves=2)
-    dm.moe_swiglu_checkpoint_fwd(x, None, c2, s2)
-    g2, b2 = torch.empty_like(x), torch.empty_like(x)
-    dm.moe_swiglu_checkpoint_bwd(c2, s2, d.to(DEV), g2)
-    dm.moe_swiglu_checkpoint_restore(c2, s2, b2)
-    for a, b in ((c2, codes), (s2, scales), (g2, grad), (b2, back)):
-        same(a, b)
     # and through autograd
     leaf = x.clone().requires_grad_()
     out = dm.swiglu_checkpoint(leaf)
@@ -127,7 +114,7 @@ def test_every_scale_and_every_tie():
     v[:, 0] = top
     v[:, 37] = -top
     codes, scales = dm.checkpoint_buffers(R, 32, DEV, halves=2)
-    dm.moe_swiglu_checkpoint_fwd(v.to(DEV), None, codes, scales)
+    dm.moe_swiglu_checkpoint_fwd(v.to(DEV), torch.empty(R, 32, dtype=torch.bfloat16, device=DEV), codes, scales)
     qc, qs = halves(v)
     same(scales, qs)
     same(codes, qc)
@@ -155,10 +142,8 @@ def test_infinities_and_nans_mark_their_block_only(F):
     same(codes, qc)
     same(scales, qs)
     assert int(torch.isnan(scales.float()).sum()) == 4
-    back, grad = torch.empty_like(x), torch.empty_like(x)
-    dm.moe_swiglu_checkpoint_restore(codes, scales, back)
+    grad = torch.empty_like(x)
     bad = torch.isnan(scales.float()).cpu().view(6, 2, -1).repeat_interleave(32, 2)[:, :, :F].reshape(6, 2 * F)
-    assert torch.equal(torch.isnan(back.float()).cpu(), bad)
     dm.moe_swiglu_checkpoint_bwd(codes, scales, torch.ones(6, F, dtype=torch.bfloat16, device=DEV), grad)
     either = bad[:, :F] | bad[:, F:]
     assert torch.equal(torch.isnan(grad[:, :F].float()).cpu(), either)      # dG takes both
@@ -188,20 +173,17 @@ def test_rows_behind_the_last_are_left(F, n):
     gu, nrows = gate_up(R, F, n).to(DEV), torch.tensor([n], dtype=torch.int32, device=DEV)
     used = min(n, R)
     codes, scales = dm.checkpoint_buffers(R, F, DEV, halves=2)
-    h, grad, back, hk = (torch.empty(R, w, dtype=torch.bfloat16, device=DEV) for w in (F, 2 * F, 2 * F, F))
-    for t in (codes, scales, h, grad, back, hk):
+    h, grad = (torch.empty(R, w, dtype=torch.bfloat16, device=DEV) for w in (F, 2 * F))
+    for t in (codes, scales, h, grad):
         t.fill_(9)
     dm.moe_swiglu_checkpoint_fwd(gu, h, codes, scales, nrows=nrows)
-    dm.moe_swiglu_checkpoint_bwd(codes, scales, gu[:, :F].contiguous(), grad, hk, nrows=nrows)
-    dm.moe_swiglu_checkpoint_restore(codes, scales, back, nrows=nrows)
-    for t in (codes, scales, h, grad, back, hk):
+    dm.moe_swiglu_checkpoint_bwd(codes, scales, gu[:, :F].contiguous(), grad, nrows=nrows)
+    for t in (codes, scales, h, grad):
         assert (t[used:] == 9).all()
     if used:
         qc, qs = halves(gu[:used])
         same(codes[:used], qc)
         same(scales[:used], qs)
-        same(back[:used], torch.cat([kept(qc[:, :F], qs[:, :qs.shape[1] // 2]), kept(qc[:, F:], qs[:, qs.shape[1] // 2:])],
-                                    1).bfloat16())
 
 
 def test_misaligned_rows():
@@ -324,14 +306,17 @@ def test_swiglu_refusals():
         with pytest.raises(dm.MoeError, match=match):
             dm.swiglu_checkpoint(bad)
     codes, scales = dm.checkpoint_buffers(6, 32, DEV, halves=2)
-    for f in (lambda: dm.moe_swiglu_checkpoint_fwd(x, None, codes[:5], scales),
-              lambda: dm.moe_swiglu_checkpoint_fwd(x, None, codes, scales[:5]),
-              lambda: dm.moe_swiglu_checkpoint_fwd(x, None, codes, scales.float()),
-              lambda: dm.moe_swiglu_checkpoint_fwd(x.t(), None, codes, scales),
+    h = torch.empty(6, 32, dtype=torch.bfloat16, device=DEV)
+    for f in (lambda: dm.moe_swiglu_checkpoint_fwd(x, h, codes[:5], scales),
+              lambda: dm.moe_swiglu_checkpoint_fwd(x, h, codes, scales[:5]),
+              lambda: dm.moe_swiglu_checkpoint_fwd(x, h, codes, scales.float()),
+              lambda: dm.moe_swiglu_checkpoint_fwd(x, None, codes, scales),
+              lambda: dm.moe_swiglu_checkpoint_fwd(x, h[:5], codes, scales),
+              lambda: dm.moe_swiglu_checkpoint_fwd(x.t(), h, codes, scales),
               lambda: dm.moe_swiglu_checkpoint_bwd(codes, scales, x[:, :32], x),
               lambda: dm.moe_swiglu_checkpoint_bwd(codes, scales, x[:3, :32].contiguous(), x),
-              lambda: dm.moe_swiglu_checkpoint_restore(codes, scales, x[:5]),
-              lambda: dm.moe_swiglu_checkpoint_restore(codes, scales, x, nrows=torch.ones(1, device=DEV))):
+              lambda: dm.moe_swiglu_checkpoint_bwd(codes, scales, h, x[:5]),
+              lambda: dm.moe_swiglu_checkpoint_bwd(codes, scales, h, x, nrows=torch.ones(1, device=DEV))):
         with pytest.raises(dm.MoeError):
             f()
 
