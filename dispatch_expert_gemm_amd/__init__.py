@@ -195,6 +195,13 @@ def _nodes():
     return nodes
 
 
+def _node(name, *args):
+    try:
+        return getattr(_nodes(), name)(*args)
+    except TypeError as e:  # not a tensor
+        raise MoeError(f"{name} takes GPU tensors") from e
+
+
 def _check(st: int):
     if st != 0:
         raise MoeError(f"libmoe status {st}: {lib().moe_status_str(st).decode()}")
@@ -1792,7 +1799,7 @@ def balance_loss(logits, topk_idx, *, x_active_mask=None, seq_offsets=None):
     share of the choices that go to e and P_e the mean of softmax(logits)_e, 1 for an even load; z_loss = mean of
     logsumexp(logits)^2.  seq_offsets (num_seqs + 1) int32, ascending: the loss of each packed sequence by
     itself, averaged over tokens, and counts (num_seqs, n_ids); tokens outside the sequences take no part."""
-    return _nodes().balance_loss(logits, topk_idx, x_active_mask, seq_offsets)
+    return _node("balance_loss", logits, topk_idx, x_active_mask, seq_offsets)
 
 
 def checkpoint_buffers(rows, width, device, halves=1):
@@ -1861,7 +1868,7 @@ def swiglu_checkpoint(gate_up):
     """h = silu(G) * U of rows gate_up = [G | U] (..., 2F) bf16 -> (..., F) bf16, keeping gate_up in 8 bits
     (1.0625 bytes a value) for the backward instead of in bf16: differentiable (once); the forward's h is that of
     the bf16 values, the gradient that of the kept ones."""
-    return _nodes().swiglu_checkpoint(gate_up)
+    return _node("swiglu_checkpoint", gate_up)
 
 
 def _kept_rows_at(shape, codes, scales, dev):

@@ -130,6 +130,11 @@ def test_python_calls_refuse_cpu_tensors():
         dm.balance_loss(torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32))
     with pytest.raises(dm.MoeError, match="GPU tensor"):
         dm.swiglu_checkpoint(torch.zeros(4, 64, dtype=torch.bfloat16))
+    for bad in (None, [1.0], 3):
+        with pytest.raises(dm.MoeError, match="GPU tensors"):
+            dm.balance_loss(bad, torch.zeros(4, 2, dtype=torch.int32))
+        with pytest.raises(dm.MoeError, match="GPU tensors"):
+            dm.swiglu_checkpoint(bad)
     with pytest.raises(dm.MoeError, match="GPU tensor"):
         dm.moe_swiglu_checkpoint_bwd(torch.zeros(4, 64, dtype=torch.int8), N, N, N)
 

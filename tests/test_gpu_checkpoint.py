@@ -417,3 +417,49 @@ def test_combine_rows_that_are_not_finite():
     dm.moe_combine_bwd_weights_checkpoint(shape, torch.ones_like(out), codes, scales, *args, None, None, None, None, gw)
     slots = route.assist_info_for_combine[:T * K].view(T, K)
     assert torch.equal(torch.isnan(gw), (slots == 3) | (slots == 5))
+
+
+# ----------------------------------------------------------------------------- large
+
+
+def test_swiglu_past_32_bit_offsets():
+    """2.3e9 codes, 4.6 GB of gate_up: the first and the last rows."""
+    R, F = 1_120_000, 1024
+    part = gate_up(1000, F, 1).to(DEV)
+    gu = part.repeat(R // 1000, 1)
+    h = torch.empty(R, F, dtype=torch.bfloat16, device=DEV)
+    codes, scales = dm.checkpoint_buffers(R, F, DEV, halves=2)
+    dm.moe_swiglu_checkpoint_fwd(gu, h, codes, scales)
+    d = h  # (any gradient: its last rows repeat as well)
+    grad = torch.empty_like(gu)
+    dm.moe_swiglu_checkpoint_bwd(codes, scales, d, grad)
+    for t in (h, codes, scales, grad):
+        same(t[-1000:], t[:1000])
+    qc, qs = halves(part.cpu())
+    same(codes[-1000:], qc)
+    same(scales[-1000:], qs)
+
+
+def test_combine_past_32_bit_offsets():
+    T, H, E, K = 40000, 7168, 8, 8
+    shape = dm.make_shape(T, H, K, E)
+    y = torch.randn(2000, H, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV).repeat(T * K // 2000, 1)
+    idx = torch.arange(K, dtype=torch.int32, device=DEV).repeat(T, 1)
+    w = torch.rand(T, K, generator=torch.Generator().manual_seed(2)).to(DEV)
+    route = dm.route(shape, idx)
+    args = (idx, w, route.assist_info_for_combine, route.ep_recv_counts, None)
+    out, want = (torch.empty(T, H, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    codes, scales = dm.checkpoint_buffers(T * K, H, DEV)
+    dm.moe_combine_checkpoint(shape, y, *args, None, None, None, None, None, out, codes, scales)
+    dm.moe_combine(shape, y, *args, None, None, None, None, None, want)
+    assert torch.equal(out, want)
+    same(codes[-2000:], codes[:2000])
+    same(scales[-2000:], scales[:2000])
+    qc, qs = rule(y[-50:])
+    same(codes[-50:], qc)
+    same(scales[-50:], qs)
+    gw = torch.empty_like(w)
+    dm.moe_combine_bwd_weights_checkpoint(shape, out, codes, scales, *args, None, None, None, None, gw)
+    c = int(route.assist_info_for_combine[T * K - 1])
+    p = kept(codes[c:c + 1].cpu(), scales[c:c + 1].cpu())[0] * out[T - 1].cpu().double()
+    assert abs(float(gw[T - 1, K - 1]) - float(p.sum())) <= (H / 64 + 12) * 2.0 ** -23 * float(p.abs().sum())
