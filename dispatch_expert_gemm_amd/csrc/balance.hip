@@ -183,15 +183,26 @@ __device__ __forceinline__ void row_exp(float (&v)[Q][4], float& m, float& total
   total = group_sum<GW>(s);
 }
 
-// Whether token t counts (its lanes pass the same t).
+// A lane's part of token t's mask (0 where t is not in [lo, hi)), as it lies in
+// memory: loaded with the token's row, looked at with it.  Four lanes hold up to 16
+// slots, more lanes one each.
 template <int GW>
-__device__ __forceinline__ bool token_on(const BalanceArgs& a, int64_t t, bool in) {
-  const int lane = threadIdx.x & 63, l = lane & (GW - 1);
-  if (a.mask_ndim != 2) return in && (a.mask_ndim == 0 || a.mask[t]);
-  bool any = false;
-  if (in)
-    for (int k = l; k < a.K; k += GW) any |= a.mask[t * a.K + k] != 0;
-  const uint64_t b = __ballot(any);
+__device__ __forceinline__ uint32_t load_mask(const BalanceArgs& a, int64_t t, int64_t lo, int64_t hi) {
+  if (t < lo || t >= hi) return 0u;
+  if (a.mask_ndim == 0) return 1u;
+  if (a.mask_ndim == 1) return a.mask[t];
+  const int l = threadIdx.x & (GW - 1);
+  uint32_t m = l < a.K ? a.mask[t * a.K + l] : 0u;
+  if constexpr (GW < 16)
+    for (int k = l + GW; k < a.K; k += GW) m |= a.mask[t * a.K + k];
+  return m;
+}
+
+// Whether the token whose lanes hold these parts counts.
+template <int GW>
+__device__ __forceinline__ bool token_on(uint32_t mask) {
+  const int lane = threadIdx.x & 63;
+  const uint64_t b = __ballot(mask != 0);
   if constexpr (GW == 64) return b != 0;
   else return ((b >> (lane & ~(GW - 1))) & ((1ull << GW) - 1)) != 0;
 }
@@ -213,16 +224,17 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
 // Waves of a workgroup of items: a wave waits for its tokens' rows, so eight where the
 // registers of Q runs allow it (32768 tokens of 1024 columns, 512 items: 4 waves 67 us,
 // 8 waves and rows loaded ahead 43).
-template <int Q>
-constexpr int kItemWaves = Q <= 4 ? 8 : 4;
+// The only workgroup of a small batch takes 16.
+template <int Q, bool ALONE>
+constexpr int kItemWaves = Q <= 4 ? (ALONE ? 16 : 8) : 4;
 // Rows of column sums in LDS that the waves are added into.
 template <int Q>
 constexpr int kSumRows = Q <= 8 ? 4 : 2;
 
 // ALONE: the batch is one item, so this workgroup finishes it.
 template <typename In, bool VEC, int GW, int Q, bool ALONE>
-__global__ __launch_bounds__(kWave * kItemWaves<Q>, Q <= 4 ? 6 : 1) void k_balance_items(BalanceArgs a) {
-  constexpr int W = kItemWaves<Q>, RW = kSumRows<Q>, G = kWave / GW;
+__global__ __launch_bounds__((kWave * kItemWaves<Q, ALONE>), Q <= 4 && !ALONE ? 6 : 1) void k_balance_items(BalanceArgs a) {
+  constexpr int W = kItemWaves<Q, ALONE>, RW = kSumRows<Q>, G = kWave / GW;
   extern __shared__ float smem[];
   float* rows = smem;                                   // RW x n column sums
   int* hist = reinterpret_cast<int*>(smem + RW * a.n);  // n
@@ -244,7 +256,11 @@ __global__ __launch_bounds__(kWave * kItemWaves<Q>, Q <= 4 ? 6 : 1) void k_balan
   for (int i = tid; i < a.n; i += kWave * W) hist[i] = 0;
   float v[Q][4];
   Raw4<In> next[Q];
-  if constexpr (kAhead<Q>) load_row<In, VEC, GW, Q>(a, t0 + wave * G + lane / GW, t1, next);
+  uint32_t mask_next = 0u;
+  if constexpr (kAhead<Q>) {
+    load_row<In, VEC, GW, Q>(a, t0 + wave * G + lane / GW, t1, next);
+    mask_next = load_mask<GW>(a, t0 + wave * G + lane / GW, t0, t1);
+  }
   __syncthreads();
   // the choices by themselves, a thread each: with each token's among its logits the
   // wave would wait for them too
@@ -265,11 +281,16 @@ __global__ __launch_bounds__(kWave * kItemWaves<Q>, Q <= 4 ? 6 : 1) void k_balan
   int nt = 0;
   for (int64_t b = t0 + wave * G; b < t1; b += W * G) {
     const int64_t t = b + lane / GW;
-    const bool in = t < t1;
-    if constexpr (!kAhead<Q>) load_row<In, VEC, GW, Q>(a, t, t1, next);
+    if constexpr (!kAhead<Q>) {
+      load_row<In, VEC, GW, Q>(a, t, t1, next);
+      mask_next = load_mask<GW>(a, t, t0, t1);
+    }
     take_row<In, Q>(next, v);
-    if constexpr (kAhead<Q>) load_row<In, VEC, GW, Q>(a, t + W * G, t1, next);
-    const bool on = token_on<GW>(a, t, in);
+    const bool on = token_on<GW>(mask_next);
+    if constexpr (kAhead<Q>) {
+      load_row<In, VEC, GW, Q>(a, t + W * G, t1, next);
+      mask_next = load_mask<GW>(a, t + W * G, t0, t1);
+    }
     float m, total;
     row_exp<GW, Q>(v, m, total);
     const float inv = on && total != 0.f ? 1.0f / total : 0.f;
@@ -405,8 +426,9 @@ __global__ __launch_bounds__(kWave * kJoinWaves) void k_balance_join(BalanceArgs
       p[0] += f.x; p[1] += f.y; p[2] += f.z; p[3] += f.w;
       k[0] += h.x; k[1] += h.y; k[2] += h.z; k[3] += h.w;
     }
-  if (cb == 0)
-    for (int64_t i = i0 + tid; i < i1; i += kWave * W) {
+  if (cb == 0 && wave == 0)
+#pragma unroll 4
+    for (int64_t i = i0 + lane; i < i1; i += kWave) {
       z += a.zsum[i];
       nt += a.ntok[i];
     }
@@ -424,19 +446,26 @@ __global__ __launch_bounds__(kWave * kJoinWaves) void k_balance_join(BalanceArgs
   }
   __syncthreads();
   double dot = 0;
-  const int c = cb * 64 + lane;
-  if (wave == 0 && c < a.n) {
-    double ps = 0;
-    int ks = 0;
+  if (wave == 0) {
+    const int c = cb * 64 + lane;
+    if (c < a.n) {
+      double ps = 0;
+      int ks = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      ps += dsum[w][lane];
-      ks += csum[w][lane];
+      for (int w = 0; w < W; ++w) {
+        ps += dsum[w][lane];
+        ks += csum[w][lane];
+      }
+      a.counts[(int64_t)s * a.n + c] = ks;
+      dot = ps * ks;
     }
-    a.counts[(int64_t)s * a.n + c] = ks;
-    dot = ps * ks;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+      dot += __shfl_xor(dot, o, kWave);
+      z += __shfl_xor(z, o, kWave);
+      nt += __shfl_xor(nt, o, kWave);
+    }
   }
-  block_sum3<W>(dot, z, nt, red);
   if (gridDim.x == 1) {
     if (tid == 0) {
       a.seq_tokens[0] = a.seq_tokens[1] = (int32_t)nt;
@@ -510,42 +539,51 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
   constexpr int G = kWave / GW;
   const int64_t t0 = (int64_t)blockIdx.x * a.C;
   const int64_t t1 = t0 + a.C < a.T ? t0 + a.C : a.T;
-  const double N = a.seq_tokens[a.S];
-  const float gb = a.g_loss ? (float)(*a.g_loss * (double)a.n / (a.K * N)) : 0.f;
-  const float gz = a.g_z ? (float)(*a.g_z * 2.0 / N) : 0.f;
+  // (every load before the first use of one: a small batch waits for memory once)
+  float v[Q][4];
+  Raw4<In> next[Q];
+  uint32_t mask_next = 0u;
+  if constexpr (kAhead<Q>) {
+    load_row<In, VEC, GW, Q>(a, t0 + wave * G + lane / GW, t1, next);
+    mask_next = load_mask<GW>(a, t0 + wave * G + lane / GW, t0, t1);
+  }
   // the last sequence that begins at or before the run's first token
   int s = a.off ? find_last(a.S, t0, [&](int i) { return off_at(a, i); }) : 0;
   int64_t s0 = off_at(a, s), s1 = off_at(a, s + 1);
-  float f[Q][4], share = 0.f;
+  int held = s, tokens, c[Q][4];
   auto hold = [&]() {
-    const int m = a.seq_tokens[s];
-    share = m > 0 ? gb / (float)m : 0.f;
+    tokens = a.seq_tokens[s];
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int c = (q * GW + l) * 4 + j;
-        f[q][j] = c < a.n ? (float)a.counts[(int64_t)s * a.n + c] : 0.f;
+        const int e = (q * GW + l) * 4 + j;
+        c[q][j] = e < a.n ? a.counts[(int64_t)s * a.n + e] : 0;
       }
   };
   hold();
-  int held = s;
-  float v[Q][4];
-  Raw4<In> next[Q];
-  if constexpr (kAhead<Q>) load_row<In, VEC, GW, Q>(a, t0 + wave * G + lane / GW, t1, next);
+  const int all = a.seq_tokens[a.S];
+  const float g_loss = a.g_loss ? *a.g_loss : 0.f, g_z = a.g_z ? *a.g_z : 0.f;
+  const float gb = (float)((double)g_loss * a.n / ((double)a.K * all)), gz = (float)(g_z * 2.0 / all);
   for (int64_t b = t0 + wave * G; b < t1; b += kWaves * G) {
     const int64_t t = b + lane / GW;
     const bool in = t < t1;
-    if constexpr (!kAhead<Q>) load_row<In, VEC, GW, Q>(a, t, t1, next);
+    if constexpr (!kAhead<Q>) {
+      load_row<In, VEC, GW, Q>(a, t, t1, next);
+      mask_next = load_mask<GW>(a, t, t0, t1);
+    }
     take_row<In, Q>(next, v);
-    if constexpr (kAhead<Q>) load_row<In, VEC, GW, Q>(a, t + kWaves * G, t1, next);
+    const bool unmasked = token_on<GW>(mask_next);
+    if constexpr (kAhead<Q>) {
+      load_row<In, VEC, GW, Q>(a, t + kWaves * G, t1, next);
+      mask_next = load_mask<GW>(a, t + kWaves * G, t0, t1);
+    }
     while (t >= s1 && s + 1 < a.S) {
       ++s;
       s0 = off_at(a, s);
       s1 = off_at(a, s + 1);
     }
-    const bool inside = in && t >= s0 && t < s1;
-    const bool on = token_on<GW>(a, t, inside);
+    const bool on = unmasked && in && t >= s0 && t < s1;
     if (on && held != s) {
       held = s;
       hold();
@@ -554,6 +592,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
     row_exp<GW, Q>(v, m, total);
     const bool some = on && total != 0.f;
     const float inv = some ? 1.0f / total : 0.f;
+    const float share = some ? gb / (float)tokens : 0.f;
     float d = 0.f;
     if (some)
 #pragma unroll
@@ -561,7 +600,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           v[q][j] *= inv;
-          d += v[q][j] * f[q][j];
+          d += v[q][j] * (float)c[q][j];
         }
     d = group_sum<GW>(d);
     const float zt = some ? gz * (m + __logf(total)) : 0.f;
@@ -569,7 +608,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
     for (int q = 0; q < Q; ++q) {
       float r[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) r[j] = some ? v[q][j] * (share * (f[q][j] - d) + zt) : 0.f;
+      for (int j = 0; j < 4; ++j) r[j] = some ? v[q][j] * (share * ((float)c[q][j] - d) + zt) : 0.f;
       if (in) store4<In, VEC, PAST>(a, t, (q * GW + l) * 4, r);
     }
   }
@@ -584,7 +623,7 @@ inline int step_tokens(int64_t n, int waves) { return waves * kWave / group_lane
 // are resident at once.
 constexpr int64_t kItems = 700;
 inline int64_t item_tokens(int64_t T, int64_t n) {
-  const int64_t step = step_tokens(n, n <= 1024 ? kItemWaves<4> : kItemWaves<8>);
+  const int64_t step = step_tokens(n, n <= 1024 ? kItemWaves<4, false> : kItemWaves<8, false>);
   const int64_t per = (T + kItems - 1) / kItems;
   return per ? (per + step - 1) / step * step : step;
 }
@@ -644,10 +683,11 @@ struct LaunchItems {
   bool one;
   template <typename In, bool VEC, int GW, int Q>
   void operator()() const {
-    const dim3 block(kWave * kItemWaves<Q>);
     const unsigned lds = (kSumRows<Q> + 1) * a.n * 4;
-    if (one) hipLaunchKernelGGL((k_balance_items<In, VEC, GW, Q, true>), dim3(1), block, lds, strm, a);
-    else hipLaunchKernelGGL((k_balance_items<In, VEC, GW, Q, false>), dim3((unsigned)a.slots), block, lds, strm, a);
+    if (one) hipLaunchKernelGGL((k_balance_items<In, VEC, GW, Q, true>), dim3(1), dim3(kWave * kItemWaves<Q, true>), lds,
+                                strm, a);
+    else hipLaunchKernelGGL((k_balance_items<In, VEC, GW, Q, false>), dim3((unsigned)a.slots),
+                            dim3(kWave * kItemWaves<Q, false>), lds, strm, a);
   }
 };
 struct LaunchBwd {
