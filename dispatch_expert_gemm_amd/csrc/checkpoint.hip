@@ -52,30 +52,62 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float& dg
   du = d * si;
 }
 
-// n of the eight bf16 at p (any address; zeros behind them), and their stores.  A
-// row's last eight columns may be fewer: 4, 2 and 1 of them at a time.
+// Eight values of a row of F that begin at column c.  WHOLE: aligned, and all there.
+// Otherwise the address may be any, and the row may end among the eight: they are
+// then read as the row's last eight, and moved down (zeros behind) when they are
+// used, so that every load goes out before the first wait.  A row of less than
+// eight is read value by value.
 template <bool WHOLE>
-__device__ __forceinline__ uint4 load8(const uint16_t* p, int n) {
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t F) {
+  if (WHOLE) return *reinterpret_cast<const uint4*>(row + c);
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (WHOLE) return *reinterpret_cast<const uint4*>(p);
-  if (n >= 8) {
-    __builtin_memcpy(&v, p, 16);
-    return v;
-  }
-  if (n & 4) __builtin_memcpy(&v, p, 8);
-  if (n & 2) {
-    uint32_t w;
-    __builtin_memcpy(&w, p + (n & 4), 4);
-    (n & 4 ? v.z : v.x) = w;
-  }
-  if (n & 1) {
-    const uint32_t w = p[n & 6];
-    (n & 4 ? (n & 2 ? v.w : v.z) : (n & 2 ? v.y : v.x)) = w;
+  if (F >= 8) {
+    __builtin_memcpy(&v, row + (c < F - 8 ? c : F - 8), 16);
+  } else if (c == 0) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < F) w[j / 2] |= (uint32_t)row[j] << (16 * (j & 1));
+    v = make_uint4(w[0], w[1], w[2], w[3]);
   }
   return v;
 }
 template <bool WHOLE>
-__device__ __forceinline__ void store8(uint16_t* p, const uint4& v, int n) {
+__device__ __forceinline__ uint2 load8(const int8_t* row, int64_t c, int64_t F) {
+  if (WHOLE) return *reinterpret_cast<const uint2*>(row + c);
+  uint2 v = make_uint2(0u, 0u);
+  if (F >= 8) {
+    __builtin_memcpy(&v, row + (c < F - 8 ? c : F - 8), 8);
+  } else if (c == 0) {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < F) w[j / 4] |= (uint32_t)(uint8_t)row[j] << (8 * (j & 3));
+    v = make_uint2(w[0], w[1]);
+  }
+  return v;
+}
+// n of the eight loaded: moved down by 8 - n (rows of less than eight came so).
+__device__ __forceinline__ void settle8(uint4& v, int n, int64_t F) {
+  if (n >= 8 || F < 8) return;
+  const int k = 16 * (8 - n);  // 16 to 128 bits
+  uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
+  lo = k >= 64 ? (k == 128 ? 0ull : hi >> (k & 63)) : lo >> k | hi << (64 - k);
+  hi = k >= 64 ? 0ull : hi >> k;
+  v = make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
+}
+__device__ __forceinline__ void settle8(uint2& v, int n, int64_t F) {
+  if (n >= 8 || F < 8) return;
+  const int k = 8 * (8 - n);  // 8 to 64 bits
+  uint64_t w = (uint64_t)v.y << 32 | v.x;
+  w = k == 64 ? 0ull : w >> k;
+  v = make_uint2((uint32_t)w, (uint32_t)(w >> 32));
+}
+// n of eight values to any address: 8, or 4, 2 and 1 of them.
+// (The words are picked by value: picked by reference they would be an array in LDS,
+// whose address takes the launch's packet in host memory, 14 us of a small call.)
+template <bool WHOLE>
+__device__ __forceinline__ void store8(uint16_t* p, uint4 v, int n) {
   if (WHOLE) {
     *reinterpret_cast<uint4*>(p) = v;
     return;
@@ -84,31 +116,15 @@ __device__ __forceinline__ void store8(uint16_t* p, const uint4& v, int n) {
     __builtin_memcpy(p, &v, 16);
     return;
   }
-  if (n & 4) __builtin_memcpy(p, &v, 8);
-  if (n & 2) {
-    const uint32_t w = n & 4 ? v.z : v.x;
-    __builtin_memcpy(p + (n & 4), &w, 4);
-  }
-  if (n & 1) p[n & 6] = (uint16_t)(n & 4 ? (n & 2 ? v.w : v.z) : (n & 2 ? v.y : v.x));
-}
-// The same of eight codes.
-template <bool WHOLE>
-__device__ __forceinline__ uint2 load8(const int8_t* p, int n) {
-  uint2 v = make_uint2(0u, 0u);
-  if (WHOLE) return *reinterpret_cast<const uint2*>(p);
-  if (n >= 8) {
-    __builtin_memcpy(&v, p, 8);
-    return v;
-  }
-  if (n & 4) __builtin_memcpy(&v, p, 4);
-  uint32_t w = 0;
-  if (n & 2) __builtin_memcpy(&w, p + (n & 4), 2);
-  if (n & 1) w |= (uint32_t)(uint8_t)p[n & 6] << (n & 2 ? 16 : 0);
-  if (n & 3) (n & 4 ? v.y : v.x) = w;
-  return v;
+  const uint32_t x = v.x, y = v.y, z = v.z, w = v.w;
+  const uint32_t two = n & 4 ? z : x, one = n & 4 ? (n & 2 ? w : z) : (n & 2 ? y : x);
+  const uint2 four = make_uint2(x, y);
+  if (n & 4) __builtin_memcpy(p, &four, 8);
+  if (n & 2) __builtin_memcpy(p + (n & 4), &two, 4);
+  if (n & 1) p[n & 6] = (uint16_t)one;
 }
 template <bool WHOLE>
-__device__ __forceinline__ void store8(int8_t* p, const uint2& v, int n) {
+__device__ __forceinline__ void store8(int8_t* p, uint2 v, int n) {
   if (WHOLE) {
     *reinterpret_cast<uint2*>(p) = v;
     return;
@@ -117,20 +133,21 @@ __device__ __forceinline__ void store8(int8_t* p, const uint2& v, int n) {
     __builtin_memcpy(p, &v, 8);
     return;
   }
-  if (n & 4) __builtin_memcpy(p, &v, 4);
-  const uint32_t w = n & 4 ? v.y : v.x;
-  if (n & 2) __builtin_memcpy(p + (n & 4), &w, 2);
-  if (n & 1) p[n & 6] = (int8_t)(n & 2 ? w >> 16 : w);
+  const uint32_t x = v.x, y = v.y, rest = n & 4 ? y : x;
+  if (n & 4) __builtin_memcpy(p, &x, 4);
+  const uint16_t two = (uint16_t)rest;
+  if (n & 2) __builtin_memcpy(p + (n & 4), &two, 2);
+  if (n & 1) p[n & 6] = (int8_t)(n & 2 ? rest >> 16 : rest);
 }
 
-// A lane takes eight columns of G and the same eight of U: a unit.  kUnits units a
-// thread, kThreads apart, loads first.  WHOLE: F is a multiple of 32 and every
-// matrix 16-byte aligned; otherwise a row is rounded up to whole blocks (units past
-// F hold zeros) and accesses may begin anywhere: 32768 rows of 1001 columns 69 us,
-// with a lane for each column 158.
-template <int PASS, bool WHOLE>
+// A lane takes eight columns of G and the same eight of U: a unit; U units a thread,
+// kThreads apart, loads first.  WHOLE: F is a multiple of 32 and every matrix 16-byte
+// aligned; otherwise a row is rounded up to whole blocks (units past F hold zeros) and
+// accesses may begin anywhere (32768 rows of 1001 columns 44 us; a lane for each
+// column 158).
+template <int PASS, bool WHOLE, int U>
 __global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
-  constexpr int kUnits = 2;
+  constexpr int kUnits = U;
   const int64_t rows = rows_of(a), F = a.F;
   const int64_t u0 = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
   int64_t row[kUnits];
@@ -159,15 +176,19 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
       if (row[i] < rows) {
-        g[i] = load8<WHOLE>(gu + gate(i), count(i));
-        u[i] = load8<WHOLE>(gu + gate(i) + F, count(i));
+        g[i] = load8<WHOLE>(gu + row[i] * 2 * F, 8 * (int64_t)col[i], F);
+        u[i] = load8<WHOLE>(gu + row[i] * 2 * F + F, 8 * (int64_t)col[i], F);
       }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       if (row[i] >= rows) continue;  // the four lanes of a block leave together
+      const int n = count(i);
+      if constexpr (!WHOLE) {
+        settle8(g[i], n, F);
+        settle8(u[i], n, F);
+      }
       float ig, iu;
       const uint32_t sg = kept_scale(block_amax(g[i]), ig), su = kept_scale(block_amax(u[i]), iu);
-      const int n = count(i);
       store8<WHOLE>(a.codes + gate(i), codes8(g[i], ig), n);
       store8<WHOLE>(a.codes + gate(i) + F, codes8(u[i], iu), n);
       if ((col[i] & 3) == 0) {
@@ -190,22 +211,27 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_rows(SwigluArgs a) {
     for (int i = 0; i < kUnits; ++i)
       if (row[i] < rows) {
         const uint16_t* sc = a.scales + row[i] * 2 * a.nb + col[i] / 4;
-        qg[i] = load8<WHOLE>(a.codes + gate(i), count(i));
-        qu[i] = load8<WHOLE>(a.codes + gate(i) + F, count(i));
+        qg[i] = load8<WHOLE>(a.codes + row[i] * 2 * F, 8 * (int64_t)col[i], F);
+        qu[i] = load8<WHOLE>(a.codes + row[i] * 2 * F + F, 8 * (int64_t)col[i], F);
         sg[i] = sc[0];
         su[i] = sc[a.nb];
-        dh[i] = load8<WHOLE>(static_cast<const uint16_t*>(a.grad_h) + hcol(i), count(i));
+        dh[i] = load8<WHOLE>(static_cast<const uint16_t*>(a.grad_h) + row[i] * F, 8 * (int64_t)col[i], F);
       }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       if (row[i] >= rows) continue;
+      const int n = count(i);
+      if constexpr (!WHOLE) {
+        settle8(qg[i], n, F);
+        settle8(qu[i], n, F);
+        settle8(dh[i], n, F);
+      }
       float g[8], u[8], d[8];
       kept8(qg[i], bf2f(sg[i]), g);
       kept8(qu[i], bf2f(su[i]), u);
       unpack8(dh[i], d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) swiglu_grad(g[j], u[j], d[j], g[j], u[j]);
-      const int n = count(i);
       uint16_t* out = static_cast<uint16_t*>(a.out) + gate(i);
       store8<WHOLE>(out, pack8h(g), n);
       store8<WHOLE>(out + F, pack8h(u), n);
@@ -408,9 +434,18 @@ moe_status launch_swiglu(SwigluArgs a, void* stream) {
   a.step_cols = kThreads % a.cols;
   const int64_t units = a.R * (int64_t)a.cols;
   if (units / 2 > kMaxThreads) return MOE_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)((units + 2 * kThreads - 1) / (2 * kThreads)));
-  if (whole) hipLaunchKernelGGL((k_swiglu_rows<PASS, true>), grid, dim3(kThreads), 0, as_stream(stream), a);
-  else hipLaunchKernelGGL((k_swiglu_rows<PASS, false>), grid, dim3(kThreads), 0, as_stream(stream), a);
+  auto go = [&](auto kernel, int per) {
+    const int64_t each = per * kThreads;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((units + each - 1) / each)), dim3(kThreads), 0, as_stream(stream), a);
+  };
+  // two units a thread once that still gives every SIMD eight waves
+  if (units < (int64_t)1 << 20) {
+    if (whole) go(k_swiglu_rows<PASS, true, 1>, 1);
+    else go(k_swiglu_rows<PASS, false, 1>, 1);
+  } else {
+    if (whole) go(k_swiglu_rows<PASS, true, 2>, 2);
+    else go(k_swiglu_rows<PASS, false, 2>, 2);
+  }
   return launch_status();
 }
 
