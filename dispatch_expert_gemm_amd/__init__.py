@@ -1871,24 +1871,12 @@ def swiglu_checkpoint(gate_up):
     return _node("swiglu_checkpoint", gate_up)
 
 
-def _kept_rows_at(shape, codes, scales, dev):
-    n = shape.capacity
-    return (_at(codes, I8T, n * shape.H, "y_codes", dev),
-            _at(scales, BF16, n * (-(-shape.H // 32)), "y_scales", dev))
-
-
-def _combine_args(shape, topk_idx, topk_weights, assist_info_for_combine, ep_send_counts, x_active_mask, dev):
-    TK = shape.T * shape.K
-    return (_at(topk_idx, I32, TK, "topk_idx", dev), _at(topk_weights, F32, TK, "topk_weights", dev),
-            _at(assist_info_for_combine, I32, TK + shape.capacity, "assist_info_for_combine", dev),
-            _at(ep_send_counts, I32, shape.num_experts, "ep_send_counts", dev),
-            _at(_u8(x_active_mask), torch.uint8, (0, shape.T, TK)[shape.mask_ndim], "x_active_mask", dev))
-
-
-def _special_at(shape, ori_x, const_alpha_1, const_alpha_2, const_v, dev):
-    QH = shape.const_expert_num * shape.H
-    return (_at(ori_x, BF16, shape.T * shape.H, "ori_x", dev), _at(const_alpha_1, BF16, QH, "const_alpha_1", dev),
-            _at(const_alpha_2, BF16, QH, "const_alpha_2", dev), _at(const_v, BF16, QH, "const_v", dev))
+def _raw_stream(stream, t):
+    """A stream argument for the calls of csrc/torch_nodes.cpp: -1 for the current one."""
+    if stream is None:
+        return -1
+    _same_device(stream, _device_of(t, "a tensor"))
+    return stream.cuda_stream
 
 
 def moe_combine_checkpoint(shape, y, topk_idx, topk_weights, assist_info_for_combine, ep_send_counts, x_active_mask,
@@ -1896,26 +1884,18 @@ def moe_combine_checkpoint(shape, y, topk_idx, topk_weights, assist_info_for_com
                            stream=None):
     """moe_combine that keeps y's routed rows in 8 bits: y_codes (capacity, H) int8, y_scales (capacity,
     ceil(H / 32)) bf16 (checkpoint_buffers)."""
-    dev = _device_of(y, "y")
-    _launch(lib().moe_combine_checkpoint, dev, stream, ctypes.byref(shape),
-            _at(y, BF16, shape.capacity * shape.H, "y", dev),
-            *_combine_args(shape, topk_idx, topk_weights, assist_info_for_combine, ep_send_counts, x_active_mask, dev),
-            _at(shared_expert_x, BF16, shape.T * shape.H, "shared_expert_x", dev),
-            *_special_at(shape, ori_x, const_alpha_1, const_alpha_2, const_v, dev),
-            _at(out, BF16, shape.T * shape.H, "out", dev), *_kept_rows_at(shape, y_codes, y_scales, dev))
+    _node("combine_checkpoint", ctypes.addressof(shape), _raw_stream(stream, y), y, topk_idx, topk_weights,
+          assist_info_for_combine, ep_send_counts, x_active_mask, shared_expert_x, ori_x, const_alpha_1, const_alpha_2,
+          const_v, out, y_codes, y_scales)
 
 
 def moe_combine_bwd_weights_checkpoint(shape, grad_out, y_codes, y_scales, topk_idx, topk_weights,
                                        assist_info_for_combine, ep_send_counts, x_active_mask, ori_x, const_alpha_1,
                                        const_alpha_2, const_v, grad_topk_weights, row_weights=None, stream=None):
     """moe_combine_bwd_weights on the kept rows of moe_combine_checkpoint."""
-    dev = _device_of(grad_out, "grad_out")
-    _launch(lib().moe_combine_bwd_weights_checkpoint, dev, stream, ctypes.byref(shape),
-            _at(grad_out, BF16, shape.T * shape.H, "grad_out", dev), *_kept_rows_at(shape, y_codes, y_scales, dev),
-            *_combine_args(shape, topk_idx, topk_weights, assist_info_for_combine, ep_send_counts, x_active_mask, dev),
-            *_special_at(shape, ori_x, const_alpha_1, const_alpha_2, const_v, dev),
-            _at(grad_topk_weights, F32, shape.T * shape.K, "grad_topk_weights", dev),
-            _at(row_weights, F32, shape.capacity, "row_weights", dev))
+    _node("combine_bwd_weights_checkpoint", ctypes.addressof(shape), _raw_stream(stream, grad_out), grad_out, y_codes,
+          y_scales, topk_idx, topk_weights, assist_info_for_combine, ep_send_counts, x_active_mask, ori_x,
+          const_alpha_1, const_alpha_2, const_v, grad_topk_weights, row_weights)
 
 
 def moe_layer(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, x_active_mask=None,

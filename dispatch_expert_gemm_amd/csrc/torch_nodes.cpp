@@ -1,10 +1,12 @@
-// Autograd nodes of balance_loss and swiglu_checkpoint.
+// Autograd nodes of balance_loss and swiglu_checkpoint, and the calls of the combine
+// that keeps its rows.
 //
-// Both are a few microseconds of GPU work for a small batch, where the host bounds a
+// The nodes are a few microseconds of GPU work for a small batch, where the host bounds a
 // step: a forward and backward through nodes written in Python took 110 us (balance
 // loss, 256 tokens) and 95 us (SwiGLU, 8 rows), through these 55 and 49, on a host
 // where torch's own x * 2 takes 44.  The nodes call the C entries themselves; the
-// arguments' checks and errors are the Python binding's.
+// arguments' checks and errors are the Python binding's.  The combine's two calls have
+// 15 tensors each to look at: a step of 64 tokens 20 us with them in Python, 13 here.
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
@@ -236,6 +238,77 @@ Tensor swiglu_checkpoint(const Tensor& gate_up) {
   return SwigluNode::apply(gate_up);
 }
 
+// ----------------------------------------------------------------------------- combine
+
+using Arg = const std::optional<Tensor>&;
+
+// The entries' tensor arguments: contiguous, on one device, of their type and size.
+struct Args {
+  c10::Device dev;
+  template <typename T = void>
+  T* at(Arg t, at::ScalarType type, int64_t n, const char* name) const {
+    if (!t) return nullptr;
+    goes_with(*t, dev, name);
+    typed(*t, type, name);
+    if (t->numel() < n) refuse(name, " holds ", t->numel(), " elements, needs at least ", n);
+    return static_cast<T*>(t->data_ptr());
+  }
+  const uint8_t* mask(Arg t, int64_t n) const {
+    if (!t) return nullptr;
+    return at<const uint8_t>(t, t->scalar_type() == at::kBool ? at::kBool : at::kByte, n, "x_active_mask");
+  }
+};
+
+int64_t slots(const moe_shape& s) { return s.T * s.K; }
+int64_t masked(const moe_shape& s) { return s.mask_ndim == 0 ? 0 : (s.mask_ndim == 1 ? s.T : slots(s)); }
+int64_t blocks(const moe_shape& s) { return s.capacity * ((s.H + 31) / 32); }
+
+// `stream`: a hipStream_t, or -1 for the current one of the tensors' device.
+void* stream_or_current(int64_t stream, c10::Device dev) {
+  return stream == -1 ? c10::hip::getCurrentHIPStream(dev.index()).stream() : reinterpret_cast<void*>(stream);
+}
+
+void combine_checkpoint(int64_t shape, int64_t stream, Arg y, Arg idx, Arg w, Arg assist, Arg counts, Arg mask,
+                        Arg shared, Arg ori, Arg a1, Arg a2, Arg v, Arg out, Arg codes, Arg scales) {
+  const moe_shape& s = *reinterpret_cast<const moe_shape*>(shape);
+  if (!y) refuse("y must be a GPU tensor");
+  on_gpu(*y, "y");
+  const Args a{y->device()};
+  const c10::DeviceGuard guard(a.dev);
+  const int64_t q = s.const_expert_num * s.H;
+  check(moe_combine_checkpoint(
+      &s, a.at(y, at::kBFloat16, s.capacity * s.H, "y"), a.at<int32_t>(idx, at::kInt, slots(s), "topk_idx"),
+      a.at<float>(w, at::kFloat, slots(s), "topk_weights"),
+      a.at<int32_t>(assist, at::kInt, slots(s) + s.capacity, "assist_info_for_combine"),
+      a.at<int32_t>(counts, at::kInt, s.num_experts, "ep_send_counts"), a.mask(mask, masked(s)),
+      a.at(shared, at::kBFloat16, s.T * s.H, "shared_expert_x"), a.at(ori, at::kBFloat16, s.T * s.H, "ori_x"),
+      a.at(a1, at::kBFloat16, q, "const_alpha_1"), a.at(a2, at::kBFloat16, q, "const_alpha_2"),
+      a.at(v, at::kBFloat16, q, "const_v"), a.at(out, at::kBFloat16, s.T * s.H, "out"),
+      a.at<int8_t>(codes, at::kChar, s.capacity * s.H, "y_codes"), a.at(scales, at::kBFloat16, blocks(s), "y_scales"),
+      stream_or_current(stream, a.dev)));
+}
+
+void combine_bwd_weights_checkpoint(int64_t shape, int64_t stream, Arg grad_out, Arg codes, Arg scales, Arg idx, Arg w,
+                                    Arg assist, Arg counts, Arg mask, Arg ori, Arg a1, Arg a2, Arg v, Arg grad_w,
+                                    Arg row_w) {
+  const moe_shape& s = *reinterpret_cast<const moe_shape*>(shape);
+  if (!grad_out) refuse("grad_out must be a GPU tensor");
+  on_gpu(*grad_out, "grad_out");
+  const Args a{grad_out->device()};
+  const c10::DeviceGuard guard(a.dev);
+  const int64_t q = s.const_expert_num * s.H;
+  check(moe_combine_bwd_weights_checkpoint(
+      &s, a.at(grad_out, at::kBFloat16, s.T * s.H, "grad_out"),
+      a.at<int8_t>(codes, at::kChar, s.capacity * s.H, "y_codes"), a.at(scales, at::kBFloat16, blocks(s), "y_scales"),
+      a.at<int32_t>(idx, at::kInt, slots(s), "topk_idx"), a.at<float>(w, at::kFloat, slots(s), "topk_weights"),
+      a.at<int32_t>(assist, at::kInt, slots(s) + s.capacity, "assist_info_for_combine"),
+      a.at<int32_t>(counts, at::kInt, s.num_experts, "ep_send_counts"), a.mask(mask, masked(s)),
+      a.at(ori, at::kBFloat16, s.T * s.H, "ori_x"), a.at(a1, at::kBFloat16, q, "const_alpha_1"),
+      a.at(a2, at::kBFloat16, q, "const_alpha_2"), a.at(v, at::kBFloat16, q, "const_v"),
+      a.at<float>(grad_w, at::kFloat, slots(s), "grad_topk_weights"),
+      a.at<float>(row_w, at::kFloat, s.capacity, "row_weights"), stream_or_current(stream, a.dev)));
+}
+
 py::handle g_error;
 
 }  // namespace
@@ -251,5 +324,7 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
   });
   m.def("balance_loss", &balance_loss);
   m.def("swiglu_checkpoint", &swiglu_checkpoint);
+  m.def("combine_checkpoint", &combine_checkpoint);
+  m.def("combine_bwd_weights_checkpoint", &combine_bwd_weights_checkpoint);
   m.def("refuse_foreign_leaves", &refuse_foreign_leaves);
 }

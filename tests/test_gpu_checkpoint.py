@@ -419,6 +419,73 @@ def test_combine_rows_that_are_not_finite():
     assert torch.equal(torch.isnan(gw), (slots == 3) | (slots == 5))
 
 
+def test_combine_refusals_streams_and_captured():
+    T, H, E, K = 20, 96, 4, 2
+    idx, w, mask, _ = (t if t is None or isinstance(t, tuple) else t.to(DEV) for t in routing(T, E, K, False, True, 1))
+    shape = dm.make_shape(T, H, K, E, mask_ndim=2)
+    y = torch.randn(T * K, H, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    route = dm.route(shape, idx, mask)
+    none = [None] * 5
+    codes, scales = (t.zero_() for t in dm.checkpoint_buffers(T * K, H, DEV))  # (rows of masked slots are not written)
+    out, gw = torch.empty(T, H, dtype=torch.bfloat16, device=DEV), torch.empty_like(w)
+
+    def fwd(stream=None, **kw):
+        a = dict(y=y, idx=idx, w=w, assist=route.assist_info_for_combine, counts=route.ep_recv_counts, mask=mask, out=out,
+                 codes=codes, scales=scales)
+        a.update(kw)
+        dm.moe_combine_checkpoint(shape, a["y"], a["idx"], a["w"], a["assist"], a["counts"], a["mask"], *none, a["out"],
+                                  a["codes"], a["scales"], stream=stream)
+
+    def bwd(stream=None, **kw):
+        a = dict(d=out, codes=codes, scales=scales, idx=idx, w=w, assist=route.assist_info_for_combine,
+                 counts=route.ep_recv_counts, mask=mask, gw=gw, rw=None)
+        a.update(kw)
+        dm.moe_combine_bwd_weights_checkpoint(shape, a["d"], a["codes"], a["scales"], a["idx"], a["w"], a["assist"],
+                                              a["counts"], a["mask"], None, None, None, None, a["gw"], a["rw"],
+                                              stream=stream)
+
+    fwd()
+    bwd()
+    want = out.clone(), codes.clone(), scales.clone(), gw.clone()
+    for f, names in ((fwd, ("y", "idx", "w", "assist", "counts", "out", "codes", "scales")),
+                     (bwd, ("d", "codes", "scales", "idx", "w", "assist", "counts", "gw"))):
+        for name in names:
+            t = dict(y=y, d=out, idx=idx, w=w, assist=route.assist_info_for_combine, counts=route.ep_recv_counts, out=out,
+                     codes=codes, scales=scales, gw=gw)[name]
+            for bad in (None, 3, t.cpu(), t.double(), t.flatten()[:-1], torch.stack([t, t], -1)[..., 0]):
+                with pytest.raises(dm.MoeError):
+                    f(**{name: bad})
+        with pytest.raises(dm.MoeError):
+            f(mask=mask.float())
+        f(mask=mask.bool())
+    with pytest.raises(dm.MoeError):
+        bwd(rw=gw.flatten()[:-1])
+    for a, b in zip((out, codes, scales, gw), want):
+        same(a, b)
+    side = torch.cuda.Stream()
+    for t in (out, codes, scales, gw):
+        t.zero_()
+    torch.cuda.synchronize()
+    fwd(side)
+    bwd(side)
+    side.synchronize()
+    for a, b in zip((out, codes, scales, gw), want):
+        same(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fwd()
+        bwd()
+    for seed in (2, 3, 4):
+        y.copy_(torch.randn(T * K, H, generator=torch.Generator().manual_seed(seed)).bfloat16())
+        graph.replay()
+        got = out.clone(), codes.clone(), scales.clone(), gw.clone()
+        fwd()
+        bwd()
+        torch.cuda.synchronize()
+        for a, b in zip(got, (out, codes, scales, gw)):
+            same(a, b)
+
+
 # ----------------------------------------------------------------------------- large
 
 
