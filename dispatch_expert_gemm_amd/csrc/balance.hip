@@ -222,9 +222,9 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
 }
 
 // Waves of a workgroup of items: a wave waits for its tokens' rows, so eight where the
-// registers of Q runs allow it (32768 tokens of 1024 columns, 512 items: 4 waves 67 us,
-// 8 waves and rows loaded ahead 43).
-// The only workgroup of a small batch takes 16.
+// registers of Q runs allow it (32768 tokens of 1024 columns, the gradient left in the
+// caches: 4 waves 67 us, 8 waves and rows loaded ahead 43).  The only workgroup of a
+// small batch takes 16.
 template <int Q, bool ALONE>
 constexpr int kItemWaves = Q <= 4 ? (ALONE ? 16 : 8) : 4;
 // Rows of column sums in LDS that the waves are added into.
@@ -618,10 +618,10 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
 inline int group_lanes(int64_t n) { return n <= 16 ? 4 : (n <= 64 ? 16 : (n <= 128 ? 32 : 64)); }
 inline int step_tokens(int64_t n, int waves) { return waves * kWave / group_lanes(n); }
 
-// Tokens of an item: whole steps, at most kItems items of a batch, so that with some
-// sequences' last items all of them (three workgroups of eight waves on a CU, 768)
-// are resident at once.
-constexpr int64_t kItems = 700;
+// Tokens of an item: whole steps, at most kItems items of a batch: two workgroups a CU,
+// and few rows of sums to join (32768 x 1024, forward and backward: 500 items 89.7 us,
+// 700 91.8, 1500 93.4).
+constexpr int64_t kItems = 500;
 inline int64_t item_tokens(int64_t T, int64_t n) {
   const int64_t step = step_tokens(n, n <= 1024 ? kItemWaves<4, false> : kItemWaves<8, false>);
   const int64_t per = (T + kItems - 1) / kItems;
