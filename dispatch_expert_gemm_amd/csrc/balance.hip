@@ -134,18 +134,14 @@ __device__ __forceinline__ void load4(const BalanceArgs& a, int64_t t, int c, Ra
   }
 }
 
-// A lane's part of row t (-inf where t >= t1): issued a step ahead of its use.
+// A lane's part of row t (-inf where t >= t1): issued a step ahead of its use.  Rows of
+// more than 1024 columns are held by a workgroup's 256 lanes (GW 256).
 template <typename In, bool VEC, int GW, int Q>
 __device__ __forceinline__ void load_row(const BalanceArgs& a, int64_t t, int64_t t1, Raw4<In> (&v)[Q]) {
   const int l = threadIdx.x & (GW - 1);
 #pragma unroll
   for (int q = 0; q < Q; ++q) load4<In, VEC>(a, t, t < t1 ? (q * GW + l) * 4 : a.n, v[q]);
 }
-
-// Rows of up to 1024 columns are loaded a step ahead; longer ones keep 32 or 64 values
-// in flight for each lane anyway, and a second row would leave one wave on a SIMD.
-template <int Q>
-constexpr bool kAhead = Q <= 4;
 
 // The values of a row, a NaN read as -inf (fmaxf drops it).
 template <typename In, int Q>
@@ -161,16 +157,16 @@ __device__ __forceinline__ void take_row(const Raw4<In> (&raw)[Q], float (&v)[Q]
     }
 }
 
-// exp(v - m) in place of the row's logits; m the row's largest, total the sum.  A
-// row that holds nothing above -inf gives zeros and total 0.
-template <int GW, int Q>
-__device__ __forceinline__ void row_exp(float (&v)[Q][4], float& m, float& total) {
+// exp(v - m) in place of the row's logits; m the row's largest (`top` over its lanes),
+// total the sum (`sum`).  A row that holds nothing above -inf gives zeros and total 0.
+template <int Q, typename Top, typename Sum>
+__device__ __forceinline__ void row_exp(float (&v)[Q][4], float& m, float& total, Top top, Sum sum) {
   m = -INFINITY;
 #pragma unroll
   for (int q = 0; q < Q; ++q)
 #pragma unroll
     for (int j = 0; j < 4; ++j) m = fmaxf(m, v[q][j]);
-  m = group_max<GW>(m);
+  m = top(m);
   const float base = m != -INFINITY ? m : 0.f;
   float s = 0.f;
 #pragma unroll
@@ -180,8 +176,34 @@ __device__ __forceinline__ void row_exp(float (&v)[Q][4], float& m, float& total
       v[q][j] = __expf(v[q][j] - base);
       s += v[q][j];
     }
-  total = group_sum<GW>(s);
+  total = sum(s);
 }
+
+// A value over a workgroup's 256 lanes: its waves meet in one of two rows of LDS in
+// turn, so one barrier a value is enough (a row is written again only behind the
+// barrier of the value between).
+struct Meet {
+  float (*rows)[kWaves];
+  int turn;
+  template <typename Op>
+  __device__ __forceinline__ float all(float v, Op op) {
+    v = group_all<kWave>(v, op);
+    float* r = rows[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = r[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v = op(v, r[w]);
+    return v;
+  }
+  __device__ __forceinline__ float max(float v) {
+    return all(v, [](float a, float b) { return fmaxf(a, b); });
+  }
+  __device__ __forceinline__ float sum(float v) {
+    return all(v, [](float a, float b) { return a + b; });
+  }
+};
 
 // A lane's part of token t's mask (0 where t is not in [lo, hi)), as it lies in
 // memory: loaded with the token's row, looked at with it.  Four lanes hold up to 16
@@ -221,20 +243,40 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return r;
 }
 
-// Waves of a workgroup of items: a wave waits for its tokens' rows, so eight where the
-// registers of Q runs allow it (32768 tokens of 1024 columns, the gradient left in the
-// caches: 4 waves 67 us, 8 waves and rows loaded ahead 43).  The only workgroup of a
-// small batch takes 16.
-template <int Q, bool ALONE>
-constexpr int kItemWaves = Q <= 4 ? (ALONE ? 16 : 8) : 4;
-// Rows of column sums in LDS that the waves are added into.
-template <int Q>
-constexpr int kSumRows = Q <= 8 ? 4 : 2;
+// Waves of a workgroup of items: a wave waits for its tokens' rows, so eight (32768
+// tokens of 1024 columns, the gradient left in the caches: 4 waves 67 us, 8 waves and
+// rows loaded ahead 43).  The only workgroup of a small batch takes 16.
+template <bool ALONE>
+constexpr int kItemWaves = ALONE ? 16 : 8;
+constexpr int kSumRows = 4;  // rows of column sums in LDS that the waves are added into
+
+// The tokens of an item, from the offsets; false where no sequence fills the slot.
+__device__ __forceinline__ bool tokens_of(const BalanceArgs& a, int64_t item, int64_t& t0, int64_t& t1) {
+  int s = 0;
+  if (a.off) s = find_last(a.S, item, [&](int i) { return off_at(a, i) / a.C + i; });
+  const int64_t lo = off_at(a, s), hi = off_at(a, s + 1);
+  t0 = lo + (item - (lo / a.C + s)) * a.C;
+  t1 = t0 + a.C < hi ? t0 + a.C : hi;
+  return t0 >= lo && t0 < t1;
+}
+
+// The choices of tokens t0 to t1 into the histogram, a thread each: with each token's
+// among its logits the wave would wait for them too.
+__device__ __forceinline__ void count_choices(const BalanceArgs& a, int64_t t0, int64_t t1, int* hist) {
+  const int slots = (int)(t1 - t0) * a.K;
+  for (int i = threadIdx.x; i < slots; i += blockDim.x) {
+    const int64_t at = t0 * a.K + i;
+    const int32_t e = a.idx[at];
+    bool on = (uint32_t)e < (uint32_t)a.n;
+    if (a.mask_ndim) on = on && a.mask[a.mask_ndim == 2 ? at : t0 + (uint32_t)i / (uint32_t)a.K];
+    if (on) atomicAdd(&hist[e], 1);
+  }
+}
 
 // ALONE: the batch is one item, so this workgroup finishes it.
 template <typename In, bool VEC, int GW, int Q, bool ALONE>
-__global__ __launch_bounds__((kWave * kItemWaves<Q, ALONE>), Q <= 4 && !ALONE ? 6 : 1) void k_balance_items(BalanceArgs a) {
-  constexpr int W = kItemWaves<Q, ALONE>, RW = kSumRows<Q>, G = kWave / GW;
+__global__ __launch_bounds__(kWave * kItemWaves<ALONE>, ALONE ? 1 : 6) void k_balance_items(BalanceArgs a) {
+  constexpr int W = kItemWaves<ALONE>, RW = kSumRows, G = kWave / GW;
   extern __shared__ float smem[];
   float* rows = smem;                                   // RW x n column sums
   int* hist = reinterpret_cast<int*>(smem + RW * a.n);  // n
@@ -245,33 +287,14 @@ __global__ __launch_bounds__((kWave * kItemWaves<Q, ALONE>), Q <= 4 && !ALONE ? 
   const int64_t item = blockIdx.x;
   if (!ALONE && item == 0 && tid == 0) *a.ticket = 0;
   int64_t t0 = 0, t1 = a.T;
-  if constexpr (!ALONE) {
-    int s = 0;
-    if (a.off) s = find_last(a.S, item, [&](int i) { return off_at(a, i) / a.C + i; });
-    const int64_t lo = off_at(a, s), hi = off_at(a, s + 1);
-    t0 = lo + (item - (lo / a.C + s)) * a.C;
-    t1 = t0 + a.C < hi ? t0 + a.C : hi;
-    if (t0 < lo || t0 >= t1) return;  // a slot that no sequence fills: never read
-  }
+  if (!ALONE && !tokens_of(a, item, t0, t1)) return;  // (never read)
   for (int i = tid; i < a.n; i += kWave * W) hist[i] = 0;
   float v[Q][4];
   Raw4<In> next[Q];
-  uint32_t mask_next = 0u;
-  if constexpr (kAhead<Q>) {
-    load_row<In, VEC, GW, Q>(a, t0 + wave * G + lane / GW, t1, next);
-    mask_next = load_mask<GW>(a, t0 + wave * G + lane / GW, t0, t1);
-  }
+  load_row<In, VEC, GW, Q>(a, t0 + wave * G + lane / GW, t1, next);
+  uint32_t mask_next = load_mask<GW>(a, t0 + wave * G + lane / GW, t0, t1);
   __syncthreads();
-  // the choices by themselves, a thread each: with each token's among its logits the
-  // wave would wait for them too
-  const int slots = (int)(t1 - t0) * a.K;
-  for (int i = tid; i < slots; i += kWave * W) {
-    const int64_t at = t0 * a.K + i;
-    const int32_t e = a.idx[at];
-    bool on = (uint32_t)e < (uint32_t)a.n;
-    if (a.mask_ndim) on = on && a.mask[a.mask_ndim == 2 ? at : t0 + (uint32_t)i / (uint32_t)a.K];
-    if (on) atomicAdd(&hist[e], 1);
-  }
+  count_choices(a, t0, t1, hist);
   float p[Q][4];
 #pragma unroll
   for (int q = 0; q < Q; ++q)
@@ -281,18 +304,12 @@ __global__ __launch_bounds__((kWave * kItemWaves<Q, ALONE>), Q <= 4 && !ALONE ? 
   int nt = 0;
   for (int64_t b = t0 + wave * G; b < t1; b += W * G) {
     const int64_t t = b + lane / GW;
-    if constexpr (!kAhead<Q>) {
-      load_row<In, VEC, GW, Q>(a, t, t1, next);
-      mask_next = load_mask<GW>(a, t, t0, t1);
-    }
     take_row<In, Q>(next, v);
     const bool on = token_on<GW>(mask_next);
-    if constexpr (kAhead<Q>) {
-      load_row<In, VEC, GW, Q>(a, t + W * G, t1, next);
-      mask_next = load_mask<GW>(a, t + W * G, t0, t1);
-    }
+    load_row<In, VEC, GW, Q>(a, t + W * G, t1, next);
+    mask_next = load_mask<GW>(a, t + W * G, t0, t1);
     float m, total;
-    row_exp<GW, Q>(v, m, total);
+    row_exp(v, m, total, group_max<GW>, group_sum<GW>);
     const float inv = on && total != 0.f ? 1.0f / total : 0.f;
     if (on) {  // (a token that is off adds nothing, not even a NaN)
 #pragma unroll
@@ -362,6 +379,66 @@ __global__ __launch_bounds__((kWave * kItemWaves<Q, ALONE>), Q <= 4 && !ALONE ? 
       a.zsum[item] = (float)v;
       a.ntok[item] = k;
     }
+  }
+}
+
+// Rows of more than 1024 columns: the workgroup's 256 lanes hold a token, Q runs each,
+// so a lane keeps the sums of its own columns and a CU holds eight tokens (a wave for
+// a token takes 200 to 256 registers: 8192 x 4096 89 us forward and 166 backward, 48 and
+// 53 so).
+template <typename In, bool VEC, int Q>
+__global__ __launch_bounds__(kThreads) void k_balance_items_wide(BalanceArgs a) {
+  extern __shared__ float smem[];
+  int* hist = reinterpret_cast<int*>(smem);  // n
+  __shared__ float rows[2][kWaves];
+  const int tid = threadIdx.x;
+  const int64_t item = blockIdx.x;
+  if (item == 0 && tid == 0) *a.ticket = 0;
+  int64_t t0, t1;
+  if (!tokens_of(a, item, t0, t1)) return;  // (never read)
+  for (int i = tid; i < a.n; i += kThreads) hist[i] = 0;
+  Meet meet{rows, 0};
+  float v[Q][4], p[Q][4];
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[q][j] = 0.f;
+  Raw4<In> next[Q];
+  load_row<In, VEC, kThreads, Q>(a, t0, t1, next);
+  uint32_t mask_next = load_mask<kWave>(a, t0, t0, t1);
+  __syncthreads();
+  count_choices(a, t0, t1, hist);
+  float z = 0.f;
+  int nt = 0;
+  for (int64_t t = t0; t < t1; ++t) {
+    take_row<In, Q>(next, v);
+    const bool on = token_on<kWave>(mask_next);
+    load_row<In, VEC, kThreads, Q>(a, t + 1, t1, next);
+    mask_next = load_mask<kWave>(a, t + 1, t0, t1);
+    float m, total;
+    row_exp(v, m, total, [&](float x) { return meet.max(x); }, [&](float x) { return meet.sum(x); });
+    if (on) {
+      const float inv = total != 0.f ? 1.0f / total : 0.f;
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[q][j] += v[q][j] * inv;
+      const float lse = total != 0.f ? m + __logf(total) : 0.f;
+      z += lse * lse;
+      ++nt;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int c = (q * kThreads + tid) * 4;
+    if (c < a.n)
+      *reinterpret_cast<float4*>(a.psum + item * a.pitch + c) = make_float4(p[q][0], p[q][1], p[q][2], p[q][3]);
+  }
+  for (int c = tid; c < a.n; c += kThreads) a.hist[item * a.pitch + c] = hist[c];
+  if (tid == 0) {
+    a.zsum[item] = z;
+    a.ntok[item] = nt;
   }
 }
 
@@ -532,21 +609,30 @@ __device__ __forceinline__ void store4(const BalanceArgs& a, int64_t t, int c, c
   }
 }
 
-// PAST: the gradient does not fit the caches and is written around them.
+// PAST: the gradient does not fit the caches and is written around them.  GW 256: the
+// workgroup holds one token.
 template <typename In, bool VEC, int GW, int Q, bool PAST>
 __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (GW - 1);
-  constexpr int G = kWave / GW;
+  constexpr bool kWide = GW > kWave;
+  constexpr int kMaskLanes = kWide ? kWave : GW, kStep = kThreads / GW;
+  __shared__ float rows[2][kWaves];
+  Meet meet{rows, 0};
+  const int tid = threadIdx.x, l = tid & (GW - 1);
+  auto sum = [&](float x) {
+    if constexpr (kWide) return meet.sum(x);
+    else return group_sum<GW>(x);
+  };
+  auto top = [&](float x) {
+    if constexpr (kWide) return meet.max(x);
+    else return group_max<GW>(x);
+  };
   const int64_t t0 = (int64_t)blockIdx.x * a.C;
   const int64_t t1 = t0 + a.C < a.T ? t0 + a.C : a.T;
   // (every load before the first use of one: a small batch waits for memory once)
   float v[Q][4];
   Raw4<In> next[Q];
-  uint32_t mask_next = 0u;
-  if constexpr (kAhead<Q>) {
-    load_row<In, VEC, GW, Q>(a, t0 + wave * G + lane / GW, t1, next);
-    mask_next = load_mask<GW>(a, t0 + wave * G + lane / GW, t0, t1);
-  }
+  load_row<In, VEC, GW, Q>(a, t0 + tid / GW, t1, next);
+  uint32_t mask_next = load_mask<kMaskLanes>(a, t0 + tid / GW, t0, t1);
   // the last sequence that begins at or before the run's first token
   int s = a.off ? find_last(a.S, t0, [&](int i) { return off_at(a, i); }) : 0;
   int64_t s0 = off_at(a, s), s1 = off_at(a, s + 1);
@@ -565,19 +651,13 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
   const int all = a.seq_tokens[a.S];
   const float g_loss = a.g_loss ? *a.g_loss : 0.f, g_z = a.g_z ? *a.g_z : 0.f;
   const float gb = (float)((double)g_loss * a.n / ((double)a.K * all)), gz = (float)(g_z * 2.0 / all);
-  for (int64_t b = t0 + wave * G; b < t1; b += kWaves * G) {
-    const int64_t t = b + lane / GW;
+  for (int64_t b = t0; b < t1; b += kStep) {  // (the whole workgroup)
+    const int64_t t = b + tid / GW;
     const bool in = t < t1;
-    if constexpr (!kAhead<Q>) {
-      load_row<In, VEC, GW, Q>(a, t, t1, next);
-      mask_next = load_mask<GW>(a, t, t0, t1);
-    }
     take_row<In, Q>(next, v);
-    const bool unmasked = token_on<GW>(mask_next);
-    if constexpr (kAhead<Q>) {
-      load_row<In, VEC, GW, Q>(a, t + kWaves * G, t1, next);
-      mask_next = load_mask<GW>(a, t + kWaves * G, t0, t1);
-    }
+    const bool unmasked = token_on<kMaskLanes>(mask_next);
+    load_row<In, VEC, GW, Q>(a, t + kStep, t1, next);
+    mask_next = load_mask<kMaskLanes>(a, t + kStep, t0, t1);
     while (t >= s1 && s + 1 < a.S) {
       ++s;
       s0 = off_at(a, s);
@@ -589,7 +669,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
       hold();
     }
     float m, total;
-    row_exp<GW, Q>(v, m, total);
+    row_exp(v, m, total, top, sum);
     const bool some = on && total != 0.f;
     const float inv = some ? 1.0f / total : 0.f;
     const float share = some ? gb / (float)tokens : 0.f;
@@ -602,7 +682,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
           v[q][j] *= inv;
           d += v[q][j] * (float)c[q][j];
         }
-    d = group_sum<GW>(d);
+    d = sum(d);
     const float zt = some ? gz * (m + __logf(total)) : 0.f;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -615,7 +695,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
 }
 
 // Tokens that a workgroup of `waves` takes at a time.
-inline int group_lanes(int64_t n) { return n <= 16 ? 4 : (n <= 64 ? 16 : (n <= 128 ? 32 : 64)); }
+inline int group_lanes(int64_t n) { return n <= 16 ? 4 : (n <= 64 ? 16 : (n <= 128 ? 32 : (n <= 1024 ? 64 : 256))); }
 inline int step_tokens(int64_t n, int waves) { return waves * kWave / group_lanes(n); }
 
 // Tokens of an item: whole steps, at most kItems items of a batch: two workgroups a CU,
@@ -623,13 +703,13 @@ inline int step_tokens(int64_t n, int waves) { return waves * kWave / group_lane
 // 700 91.8, 1500 93.4).
 constexpr int64_t kItems = 500;
 inline int64_t item_tokens(int64_t T, int64_t n) {
-  const int64_t step = step_tokens(n, n <= 1024 ? kItemWaves<4, false> : kItemWaves<8, false>);
+  const int64_t step = step_tokens(n, n <= 1024 ? kItemWaves<false> : kWaves);
   const int64_t per = (T + kItems - 1) / kItems;
   return per ? (per + step - 1) / step * step : step;
 }
 
 // One workgroup does a small batch without sequences in one launch.
-inline bool alone(int64_t T, int64_t n, int64_t num_seqs) { return num_seqs == 0 && T * n <= 32768; }
+inline bool alone(int64_t T, int64_t n, int64_t num_seqs) { return num_seqs == 0 && n <= 1024 && T * n <= 32768; }
 
 struct Layout {
   int64_t slots, psum, hist, zsum, ntok, dots, zseq, ticket, bytes;
@@ -673,8 +753,8 @@ void launch_gq(int64_t n, Fn f) {
   else if (n <= 256) f.template operator()<In, VEC, 64, 1>();
   else if (n <= 512) f.template operator()<In, VEC, 64, 2>();
   else if (n <= 1024) f.template operator()<In, VEC, 64, 4>();
-  else if (n <= 2048) f.template operator()<In, VEC, 64, 8>();
-  else f.template operator()<In, VEC, 64, 16>();
+  else if (n <= 2048) f.template operator()<In, VEC, 256, 2>();
+  else f.template operator()<In, VEC, 256, 4>();
 }
 
 struct LaunchItems {
@@ -683,11 +763,15 @@ struct LaunchItems {
   bool one;
   template <typename In, bool VEC, int GW, int Q>
   void operator()() const {
-    const unsigned lds = (kSumRows<Q> + 1) * a.n * 4;
-    if (one) hipLaunchKernelGGL((k_balance_items<In, VEC, GW, Q, true>), dim3(1), dim3(kWave * kItemWaves<Q, true>), lds,
-                                strm, a);
-    else hipLaunchKernelGGL((k_balance_items<In, VEC, GW, Q, false>), dim3((unsigned)a.slots),
-                            dim3(kWave * kItemWaves<Q, false>), lds, strm, a);
+    if constexpr (GW > kWave) {
+      hipLaunchKernelGGL((k_balance_items_wide<In, VEC, Q>), dim3((unsigned)a.slots), dim3(kThreads), a.n * 4, strm, a);
+    } else {
+      const unsigned lds = (kSumRows + 1) * a.n * 4;
+      if (one) hipLaunchKernelGGL((k_balance_items<In, VEC, GW, Q, true>), dim3(1), dim3(kWave * kItemWaves<true>), lds,
+                                  strm, a);
+      else hipLaunchKernelGGL((k_balance_items<In, VEC, GW, Q, false>), dim3((unsigned)a.slots),
+                              dim3(kWave * kItemWaves<false>), lds, strm, a);
+    }
   }
 };
 struct LaunchBwd {

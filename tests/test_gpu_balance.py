@@ -82,6 +82,15 @@ def test_sequences(T, n, K, S, lead, tail, mask):
     assert got[2].shape == (S, n)
 
 
+@pytest.mark.parametrize("mask", [0, 1, 2])
+@pytest.mark.parametrize("T,n,K,S,lead,tail", [(70, 1500, 8, 9, 0, 3), (4100, 1028, 8, 37, 5, 61), (2100, 4093, 3, 700, 0, 0)])
+def test_sequences_of_wide_rows(T, n, K, S, lead, tail, mask):
+    """Rows that a whole workgroup holds: items and runs of several tokens that sequences end inside."""
+    l, idx = _inputs(T, n, K, S)
+    for x in (l, l.bfloat16()):
+        _check(f"S={S} {x.dtype}", x, idx, _mask(mask, T, K, S), _offsets(S, T, S, lead, tail))
+
+
 def test_sequences_are_each_by_themselves():
     """Two sequences give the token-weighted mean of their own losses, and the gradient of a token does not see the
     other sequence's logits."""
