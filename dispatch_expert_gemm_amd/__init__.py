@@ -1871,6 +1871,13 @@ def swiglu_checkpoint(gate_up):
     return _node("swiglu_checkpoint", gate_up)
 
 
+def _shape_at(shape):
+    """A shape's address for the calls of csrc/torch_nodes.cpp."""
+    if not isinstance(shape, MoeShape):
+        raise MoeError(f"shape must be a MoeShape (make_shape), got {type(shape).__name__}")
+    return ctypes.addressof(shape)
+
+
 def _raw_stream(stream, t):
     """A stream argument for the calls of csrc/torch_nodes.cpp: -1 for the current one."""
     if stream is None:
@@ -1884,7 +1891,7 @@ def moe_combine_checkpoint(shape, y, topk_idx, topk_weights, assist_info_for_com
                            stream=None):
     """moe_combine that keeps y's routed rows in 8 bits: y_codes (capacity, H) int8, y_scales (capacity,
     ceil(H / 32)) bf16 (checkpoint_buffers)."""
-    _node("combine_checkpoint", ctypes.addressof(shape), _raw_stream(stream, y), y, topk_idx, topk_weights,
+    _node("combine_checkpoint", _shape_at(shape), _raw_stream(stream, y), y, topk_idx, topk_weights,
           assist_info_for_combine, ep_send_counts, x_active_mask, shared_expert_x, ori_x, const_alpha_1, const_alpha_2,
           const_v, out, y_codes, y_scales)
 
@@ -1893,7 +1900,7 @@ def moe_combine_bwd_weights_checkpoint(shape, grad_out, y_codes, y_scales, topk_
                                        assist_info_for_combine, ep_send_counts, x_active_mask, ori_x, const_alpha_1,
                                        const_alpha_2, const_v, grad_topk_weights, row_weights=None, stream=None):
     """moe_combine_bwd_weights on the kept rows of moe_combine_checkpoint."""
-    _node("combine_bwd_weights_checkpoint", ctypes.addressof(shape), _raw_stream(stream, grad_out), grad_out, y_codes,
+    _node("combine_bwd_weights_checkpoint", _shape_at(shape), _raw_stream(stream, grad_out), grad_out, y_codes,
           y_scales, topk_idx, topk_weights, assist_info_for_combine, ep_send_counts, x_active_mask, ori_x,
           const_alpha_1, const_alpha_2, const_v, grad_topk_weights, row_weights)
 

@@ -832,6 +832,7 @@ extern "C" moe_status moe_balance_fwd(int64_t T, int64_t n_ids, int32_t K, int64
   const int64_t S = num_seqs ? num_seqs : 1;
   const Layout w = layout_of(T, n_ids, S);
   if (!workspace || ws_bytes < (size_t)w.bytes) return MOE_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % 16) return MOE_ERR_BAD_SHAPE;
   const int64_t blocks = S * ((n_ids + 63) / 64);
   if (w.slots > 0x3fffff || blocks > 0x3fffff) return MOE_ERR_BAD_SHAPE;  // 2^32 threads of a launch
   const bool one = alone(T, n_ids, num_seqs);

@@ -884,8 +884,8 @@ moe_status moe_balance_workspace_size(int64_t T, int64_t n_ids, int64_t num_seqs
  *       NULL with mask_ndim 0; seq_offsets (num_seqs + 1) int32 or NULL with num_seqs 0
  *  out  loss, z_loss: one fp32 each; counts (max(num_seqs, 1), n_ids) int32: c;
  *       seq_tokens (max(num_seqs, 1) + 1) int32: n_s, then N (the backward's)
- *  workspace >= moe_balance_workspace_size bytes, else MOE_ERR_WORKSPACE.  Calls that
- *  share one must not overlap in time. */
+ *  workspace >= moe_balance_workspace_size bytes, else MOE_ERR_WORKSPACE, on a 16-byte
+ *  boundary, else MOE_ERR_BAD_SHAPE.  Calls that share one must not overlap in time. */
 moe_status moe_balance_fwd(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs, int32_t mask_ndim, int32_t dtype,
                            const void* logits, const int32_t* topk_idx, const uint8_t* x_active_mask,
                            const int32_t* seq_offsets, float* loss, float* z_loss, int32_t* counts,

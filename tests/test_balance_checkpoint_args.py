@@ -30,7 +30,8 @@ def L():
     (dict(mask=3), BAD_RANGE), (dict(mask=-1), BAD_RANGE), (dict(dtype=2), BAD_RANGE), (dict(dtype=-1), BAD_RANGE),
     (dict(logits=N), NULL_ARG), (dict(idx=N), NULL_ARG), (dict(mask=1, m=N), NULL_ARG), (dict(S=2, off=N), NULL_ARG),
     (dict(loss=N), NULL_ARG), (dict(z=N), NULL_ARG), (dict(counts=N), NULL_ARG), (dict(tokens=N), NULL_ARG),
-    (dict(ws=N), WORKSPACE), (dict(ws_bytes=255), WORKSPACE)])
+    (dict(ws=N), WORKSPACE), (dict(ws_bytes=255), WORKSPACE), (dict(ws=P(0x10008)), BAD_SHAPE),
+    (dict(ws=P(0x10001)), BAD_SHAPE)])
 def test_balance_forward_refuses(L, kw, expect):
     a = dict(T=64, n=32, K=4, S=0, mask=0, dtype=1, logits=P(), idx=P(), m=P(), off=P(), loss=P(), z=P(), counts=P(),
              tokens=P(), ws=P(), ws_bytes=1 << 40)
@@ -137,6 +138,14 @@ def test_python_calls_refuse_cpu_tensors():
             dm.swiglu_checkpoint(bad)
     with pytest.raises(dm.MoeError, match="GPU tensor"):
         dm.moe_swiglu_checkpoint_bwd(torch.zeros(4, 64, dtype=torch.int8), N, N, N)
+
+
+def test_combine_calls_refuse_other_shapes():
+    for bad in (None, (8, 64), ctypes.c_int64(8)):
+        with pytest.raises(dm.MoeError, match="MoeShape"):
+            dm.moe_combine_checkpoint(bad, *[N] * 14)
+        with pytest.raises(dm.MoeError, match="MoeShape"):
+            dm.moe_combine_bwd_weights_checkpoint(bad, *[N] * 13)
 
 
 def test_checkpoint_buffers():
