@@ -206,7 +206,7 @@ struct Meet {
 };
 
 // A lane's part of token t's mask (0 where t is not in [lo, hi)), as it lies in
-// memory: loaded with the token's row, looked at with it.  Four lanes hold up to 16
+// memory: loaded with the token's row, looked at with it.  Four or eight lanes hold up to 16
 // slots, more lanes one each.
 template <int GW>
 __device__ __forceinline__ uint32_t load_mask(const BalanceArgs& a, int64_t t, int64_t lo, int64_t hi) {
@@ -245,7 +245,7 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
 
 // Waves of a workgroup of items: a wave waits for its tokens' rows, so eight (32768
 // tokens of 1024 columns, the gradient left in the caches: 4 waves 67 us, 8 waves and
-// rows loaded ahead 43).  The only workgroup of a small batch takes 16.
+// rows loaded ahead 43; rows loaded two steps ahead gain nothing).  The only workgroup of a small batch takes 16.
 template <bool ALONE>
 constexpr int kItemWaves = ALONE ? 16 : 8;
 constexpr int kSumRows = 4;  // rows of column sums in LDS that the waves are added into
@@ -275,7 +275,7 @@ __device__ __forceinline__ void count_choices(const BalanceArgs& a, int64_t t0, 
 
 // ALONE: the batch is one item, so this workgroup finishes it.
 template <typename In, bool VEC, int GW, int Q, bool ALONE>
-__global__ __launch_bounds__(kWave * kItemWaves<ALONE>, ALONE ? 1 : 6) void k_balance_items(BalanceArgs a) {
+__global__ __launch_bounds__(kWave * kItemWaves<ALONE>, ALONE ? 1 : 4) void k_balance_items(BalanceArgs a) {
   constexpr int W = kItemWaves<ALONE>, RW = kSumRows, G = kWave / GW;
   extern __shared__ float smem[];
   float* rows = smem;                                   // RW x n column sums
@@ -694,17 +694,25 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
   }
 }
 
+// Lanes of a token.  The more runs of four a lane holds, the fewer steps the sum over
+// the lanes takes and the more tokens share a wave's instructions (65536 tokens,
+// forward + backward in us: 260 columns fp32 64 lanes 34 + 31, 32 lanes 28 + 26; 128
+// bf16 32 lanes 20 + 15, 16 lanes 18 + 14), until a small batch has too few items (8192
+// tokens of 64 columns 16 lanes 8.8, 8 lanes 9.6) or the registers end (32768 x 1024 by 32
+// lanes 159 + 55 for 40 + 52).
+inline int group_lanes(int64_t n) {
+  return n <= 16 ? 4 : (n <= 32 ? 8 : (n <= 128 ? 16 : (n <= 512 ? 32 : (n <= 1024 ? 64 : 256))));
+}
 // Tokens that a workgroup of `waves` takes at a time.
-inline int group_lanes(int64_t n) { return n <= 16 ? 4 : (n <= 64 ? 16 : (n <= 128 ? 32 : (n <= 1024 ? 64 : 256))); }
 inline int step_tokens(int64_t n, int waves) { return waves * kWave / group_lanes(n); }
 
-// Tokens of an item: whole steps, at most kItems items of a batch: two workgroups a CU,
-// and few rows of sums to join (32768 x 1024, forward and backward: 500 items 89.7 us,
-// 700 91.8, 1500 93.4).
-constexpr int64_t kItems = 500;
+// Tokens of an item: whole steps, about 500 items of a batch: two workgroups of eight
+// waves a CU, and few rows of sums to join (32768 x 1024, forward and backward: 500 items
+// 89.7 us, 700 91.8, 1500 93.4).  Workgroups of four waves (wide rows): four a CU (32768 x
+// 2048, the forward: 500 items 103 us, 1000 71, 2000 75), of four tokens or more.
 inline int64_t item_tokens(int64_t T, int64_t n) {
-  const int64_t step = step_tokens(n, n <= 1024 ? kItemWaves<false> : kWaves);
-  const int64_t per = (T + kItems - 1) / kItems;
+  const int64_t step = n <= 1024 ? step_tokens(n, kItemWaves<false>) : kWaves;
+  const int64_t items = n <= 1024 ? 500 : 1000, per = (T + items - 1) / items;
   return per ? (per + step - 1) / step * step : step;
 }
 
@@ -748,10 +756,12 @@ moe_status check_balance(int64_t T, int64_t n, int32_t K, int64_t S, int32_t mas
 template <typename In, bool VEC, typename Fn>
 void launch_gq(int64_t n, Fn f) {
   if (n <= 16) f.template operator()<In, VEC, 4, 1>();
+  else if (n <= 32) f.template operator()<In, VEC, 8, 1>();
   else if (n <= 64) f.template operator()<In, VEC, 16, 1>();
-  else if (n <= 128) f.template operator()<In, VEC, 32, 1>();
-  else if (n <= 256) f.template operator()<In, VEC, 64, 1>();
-  else if (n <= 512) f.template operator()<In, VEC, 64, 2>();
+  else if (n <= 128) f.template operator()<In, VEC, 16, 2>();
+  else if (n <= 256) f.template operator()<In, VEC, 32, 2>();
+  else if (n <= 384) f.template operator()<In, VEC, 32, 3>();
+  else if (n <= 512) f.template operator()<In, VEC, 32, 4>();
   else if (n <= 1024) f.template operator()<In, VEC, 64, 4>();
   else if (n <= 2048) f.template operator()<In, VEC, 256, 2>();
   else f.template operator()<In, VEC, 256, 4>();

@@ -52,7 +52,7 @@ def _check(name, l, idx, mask=None, offsets=None, g=0.7, gz=0.3):
 
 
 # every number of columns that changes the lanes or runs of a token, odd ones among them
-COLUMNS = [1, 2, 3, 4, 5, 16, 17, 63, 64, 65, 100, 128, 129, 256, 257, 260, 512, 513, 1024, 1025, 2048, 2051, 4096]
+COLUMNS = [1, 2, 3, 4, 5, 16, 17, 32, 33, 63, 64, 65, 100, 128, 129, 256, 257, 260, 384, 385, 512, 513, 1024, 1025, 2048, 2051, 4096]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
