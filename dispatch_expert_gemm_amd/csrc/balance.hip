@@ -384,7 +384,7 @@ __global__ __launch_bounds__(kWave * kItemWaves<ALONE>, ALONE ? 1 : 4) void k_ba
 
 // Rows of more than 1024 columns: the workgroup's 256 lanes hold a token, Q runs each,
 // so a lane keeps the sums of its own columns and a CU holds eight tokens (a wave for
-// a token takes 200 to 256 registers: 8192 x 4096 89 us forward and 166 backward, 48 and
+// a token takes 200 to 256 registers: 8192 x 4096 89 us forward and 166 backward, 45 and
 // 53 so).
 template <typename In, bool VEC, int Q>
 __global__ __launch_bounds__(kThreads) void k_balance_items_wide(BalanceArgs a) {

@@ -161,6 +161,23 @@ def test_impossible_and_extreme_logits(dtype):
     _check("extreme", l, idx)
 
 
+def test_wide_rows_with_anything_in_them():
+    l, idx = _inputs(90, 1500, 6, 4)
+    l[:, 7] = -float("inf")
+    l[3, :1499] = -float("inf")                   # one id left, in the last wave
+    l[4] = -float("inf")
+    l[5, 1300] = float("nan")
+    l[8] = l[8] * 30
+    mask = _mask(1, 90, 6, 2)
+    mask[:10] = True
+    mask[20:23] = False
+    l[20], l[21], l[22] = float("nan"), float("inf"), -float("inf")
+    got = _check("wide", l, idx, mask)
+    assert not got[3][4].any() and not got[3][20:23].any() and float(got[3][5, 1300]) == 0
+    for a, b in zip(got, _run(l, idx, mask)):
+        assert torch.equal(a, b)
+
+
 def test_plus_infinity_is_seen():
     l, idx = _inputs(33, 16, 2, 4)
     l[3, 5] = float("inf")
