@@ -658,10 +658,22 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
     const bool unmasked = token_on<kMaskLanes>(mask_next);
     load_row<In, VEC, GW, Q>(a, t + kStep, t1, next);
     mask_next = load_mask<kMaskLanes>(a, t + kStep, t0, t1);
-    while (t >= s1 && s + 1 < a.S) {
-      ++s;
-      s0 = off_at(a, s);
-      s1 = off_at(a, s + 1);
+    if (in && t >= s1 && s + 1 < a.S) {  // the next sequence, or behind it the last that begins at or before t
+      s0 = s1;
+      s1 = off_at(a, ++s + 1);
+      if (t >= s1 && s + 1 < a.S) {
+        // (halving: empty sequences, offsets padded to a number of sequences, may be any many;
+        // 70 tokens among 131072 sequences 14 ms one by one, 9 us so)
+        int lo = s + 1, end = a.S;
+        while (end - lo > 1) {
+          const int mid = lo + (end - lo) / 2;
+          if (off_at(a, mid) <= t) lo = mid;
+          else end = mid;
+        }
+        s = lo;
+        s0 = off_at(a, s);
+        s1 = off_at(a, s + 1);
+      }
     }
     const bool on = unmasked && in && t >= s0 && t < s1;
     if (on && held != s) {

@@ -363,3 +363,45 @@ def test_entry_refusals():
             dm.moe_balance_fwd(**a)
     with pytest.raises(dm.MoeError, match="grad_logits"):
         dm.moe_balance_bwd(l, 2, None, None, i, i, f, f, l[:10])
+
+
+def _backward_us(l, K, off, counts, tokens, grad, passes=5):
+    """The fastest of some passes of the backward, in us."""
+    one = torch.ones(1, device=DEV)
+    best = float("inf")
+    for _ in range(passes):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        dm.moe_balance_bwd(l, K, None, off, counts, tokens, one, one, grad)
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3)
+    return best
+
+
+@pytest.mark.parametrize("n", [64, 1500])
+@pytest.mark.parametrize("lead", [0, 5])
+def test_padded_offsets(n, lead):
+    """Offsets padded to a fixed number of sequences, before the first tokens, between them and behind the last, and
+    tokens behind them all: the gradient, and that a token's sequence is searched for, not walked to (131072 offsets
+    one by one took 14 ms)."""
+    T, K, S = 70, 4, 1 << 17
+    l, idx = _inputs(T, n, K, n)
+    off = torch.full((S + 1,), 40, dtype=torch.int32)
+    off[:1000] = lead
+    off[1000:50000] = 9
+    off[50000:60000] = 23
+    off = off.to(DEV)
+    loss, z = torch.empty(1, device=DEV), torch.empty(1, device=DEV)
+    counts, tokens = (torch.empty(k, dtype=torch.int32, device=DEV) for k in (S * n, S + 1))
+    ws = torch.empty(dm.moe_balance_workspace_size(T, n, S), dtype=torch.uint8, device=DEV)
+    dm.moe_balance_fwd(l, idx, None, off, loss, z, counts, tokens, ws)
+    grad = torch.empty_like(l)
+    us = _backward_us(l, K, off, counts, tokens, grad)
+    few = torch.tensor([lead, 9, 23, 40], dtype=torch.int32, device=DEV)
+    want = _run(l, idx, None, few, 1.0, 1.0)
+    compare("padded", (loss, z, want[2], grad), reference(l, idx, None, few, 1.0, 1.0))
+    assert torch.equal(grad, want[3])
+    # (the last sequences that are not empty hold the counts)
+    assert torch.equal(counts.view(S, n)[[999, 49999, 59999]], want[2])
+    assert us < 2000, us
