@@ -50,6 +50,10 @@ template <int GW>
 __device__ __forceinline__ float group_sum(float v) {
   return group_all<GW>(v, [](float a, float b) { return a + b; });
 }
+// The sum of two whole numbers held as a float's bits.
+__device__ __forceinline__ float add_bits(float a, float b) {
+  return __int_as_float(__float_as_int(a) + __float_as_int(b));
+}
 
 struct BalanceArgs {
   const void* logits;
@@ -636,8 +640,14 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
   // the last sequence that begins at or before the run's first token
   int s = a.off ? find_last(a.S, t0, [&](int i) { return off_at(a, i); }) : 0;
   int64_t s0 = off_at(a, s), s1 = off_at(a, s + 1);
+  // The counts are used less their mean (a whole number): as sum_j p_j = 1, that leaves
+  // c - sum_j p_j c_j as it is, but its rounding then goes by the counts' differences.  Near an
+  // even load the counts are large beside them (65536 x 64, top 8, two counts one off the mean:
+  // the gradient 0.8% off with the counts themselves, 1e-7 so).
   int held = s, tokens, c[Q][4];
+  bool centred = false;
   auto hold = [&]() {
+    centred = false;
     tokens = a.seq_tokens[s];
 #pragma unroll
     for (int q = 0; q < Q; ++q)
@@ -646,6 +656,22 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
         const int e = (q * GW + l) * 4 + j;
         c[q][j] = e < a.n ? a.counts[(int64_t)s * a.n + e] : 0;
       }
+  };
+  auto centre = [&]() {  // at the first use, so that a row's work covers the counts' loads
+    centred = true;
+    int part = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part += c[q][j];
+    float bits = __int_as_float(part);
+    if constexpr (kWide) bits = meet.all(bits, add_bits);
+    else bits = group_all<GW>(bits, add_bits);
+    const int mean = (int)rintf((float)__float_as_int(bits) / (float)a.n);
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[q][j] = (q * GW + l) * 4 + j < a.n ? c[q][j] - mean : 0;
   };
   hold();
   const int all = a.seq_tokens[a.S];
@@ -682,6 +708,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
     }
     float m, total;
     row_exp(v, m, total, top, sum);
+    if (!centred) centre();  // (the lanes of a token together)
     const bool some = on && total != 0.f;
     const float inv = some ? 1.0f / total : 0.f;
     const float share = some ? gb / (float)tokens : 0.f;

@@ -405,3 +405,47 @@ def test_padded_offsets(n, lead):
     # (the last sequences that are not empty hold the counts)
     assert torch.equal(counts.view(S, n)[[999, 49999, 59999]], want[2])
     assert us < 2000, us
+
+
+def _even(T, n, K):
+    """Choices that give every id the same count (T K a multiple of n)."""
+    return (torch.arange(T * K) % n).view(T, K).to(torch.int32)
+
+
+# (T, n, K): the lanes of a token from 4 to a whole workgroup
+EVEN = [(4096, 16, 4), (2048, 64, 8), (65536, 64, 8), (520, 260, 3), (4096, 1024, 8), (4096, 2048, 4), (8192, 4096, 16)]
+
+
+@pytest.mark.parametrize("T,n,K", EVEN)
+def test_an_even_load_has_no_gradient(T, n, K):
+    """sum_j p_j = 1, so equal counts give c - sum_j p_j c_j = 0 whatever the logits; masked tokens, whose counts are
+    not the tokens' share, do not change that."""
+    l, _ = _inputs(T, n, K, T + n, std=2.0)
+    idx = _even(T, n, K).to(DEV)
+    assert not _run(l, idx, gz=0.0)[3].any()
+    wide = torch.cat([l, l])
+    on = torch.arange(2 * T, device=DEV) < T
+    off = torch.tensor([0, T, 2 * T], dtype=torch.int32, device=DEV)
+    assert not _run(wide, torch.cat([idx, idx]), on, None, gz=0.0)[3].any()
+    assert not _run(wide, torch.cat([idx, idx]), None, off, gz=0.0)[3].any()
+
+
+@pytest.mark.parametrize("T,n,K", EVEN)
+def test_the_gradient_near_an_even_load(T, n, K):
+    """Two ids one choice off the mean: the error goes by the counts' distance from the mean, not by the counts.
+    With c' = c - mean (whole numbers) and p within e = (span + 16) 2^-23 of itself, d = sum_j p_j c'_j is within
+    (e + n 2^-24) sum_j p_j |c'_j|, and an element, p share (c' - d), within 2 e + 4 2^-24 of its parts and that."""
+    l, _ = _inputs(T, n, K, T + n)
+    idx = _even(T, n, K)
+    k = int((idx[0] == 0).nonzero()[0])
+    idx[0, k] = next(e for e in range(n) if not (idx[0] == e).any())
+    grad = _run(l, idx.to(DEV), g=1.0, gz=0.0)[3].cpu().double()
+    p = torch.softmax(l.cpu().double(), 1)
+    c = torch.bincount(idx.flatten().long(), minlength=n).double() - T * K // n
+    assert c.abs().max() == 1 and c.sum() == 0
+    share = n / (K * T * T)
+    want = share * p * (c - (p * c).sum(1, keepdim=True))
+    span = float((l.max(1)[0] - l.min(1)[0]).max())
+    bound = (3 * (span + 16) + n / 2 + 4) * 2.0 ** -23 * share * p * (c.abs() + (p * c.abs()).sum(1, keepdim=True))
+    err = (grad - want).abs()
+    assert (err <= bound + 2.0 ** -126 * 4).all(), float((err / bound).max())
