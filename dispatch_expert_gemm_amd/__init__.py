@@ -1051,6 +1051,11 @@ def shared_expert_shape(T, H, F) -> MoeShape:
     return make_shape(T, H, 1, 1, F=F, capacity=T)
 
 
+def _on_16_bytes(t):
+    """t, or a copy of it where it is a contiguous tensor off a 16-byte boundary."""
+    return t.clone() if isinstance(t, torch.Tensor) and t.data_ptr() % 16 and t.is_contiguous() else t
+
+
 class _MoELayerFn(torch.autograd.Function):
     """Forward: dispatch -> grouped SwiGLU FFN -> combine; backward: the reverse chain.
     In bf16 the dispatch permute is folded into the two GEMMs that read the
@@ -1078,6 +1083,9 @@ class _MoELayerFn(torch.autograd.Function):
                 shared_w_up, shared_w_down, topk_idx, x_active_mask, const_alpha_1, const_alpha_2,
                 const_v, zero_expert_num, copy_expert_num, const_expert_num, fp8, comm_quant_mode,
                 fp8_wgrad, mx, keep8):
+        if keep8:  # (what the combine that keeps its rows takes; the plain one takes any address)
+            x, shared_expert_x, const_alpha_1, const_alpha_2, const_v = map(
+                _on_16_bytes, (x, shared_expert_x, const_alpha_1, const_alpha_2, const_v))
         T, H = x.shape
         K = topk_idx.shape[1]
         E, F, _ = w_gate.shape
@@ -1203,6 +1211,8 @@ class _MoELayerFn(torch.autograd.Function):
         if ctx.keep8:
             gus, h = (gus, h), torch.empty((shape.capacity, shape.F), dtype=BF16, device=x.device)
         grad_out = grad_out.contiguous()
+        if ctx.keep8:
+            grad_out = _on_16_bytes(grad_out)
         cap, H, F, T, K = shape.capacity, shape.H, shape.F, shape.T, shape.K
         dev = x.device
         # grad_y rows exist on the 8-bit paths only (the bf16 down GEMMs read

@@ -290,3 +290,31 @@ def test_a_capture_refuses_leaves_of_a_living_eager_graph():
     graph.replay()
     for f, o in zip(calls, outs):
         same(f().detach(), o)
+
+
+def _offset(t, k):
+    """t's values in memory that begins k elements behind a boundary."""
+    return None if t is None else torch.empty(t.numel() + k, dtype=t.dtype, device=t.device)[k:].view(t.shape).copy_(t)
+
+
+@pytest.mark.parametrize("k", [1, 4])
+@pytest.mark.parametrize("F", [64, 1056])
+@pytest.mark.parametrize("special", [False, True])
+def test_tensors_off_a_16_byte_boundary(special, F, k):
+    """x, the shared term, the constants and the output's gradient may begin anywhere, as in the layer that keeps bf16:
+    the same bits as from aligned ones."""
+    T, H = 60, 128
+    d = _layer(T, H, F, 8, 2, 11, special, special)
+    g = torch.Generator().manual_seed(3)
+    term = None if special else torch.randn(T, H, generator=g).bfloat16().to(DEV)
+
+    def step(move):
+        leaves = [d[n].detach().clone().requires_grad_() for n in ("w", "wg", "wu", "wd")]
+        x = move(d["x"]).requires_grad_()
+        kw = {n: move(v) if n.startswith("const_") and isinstance(v, torch.Tensor) else v for n, v in d["kw"].items()}
+        out = dm.moe_layer(x, d["idx"], *leaves, shared_expert_x=None if term is None else move(term),
+                           checkpoint_8bit=True, **kw)
+        return [out.detach(), *torch.autograd.grad(out, [x, *leaves], move(d["dout"]))]
+
+    for a, b in zip(step(lambda t: t.detach().clone()), step(lambda t: _offset(t, k))):
+        same(a, b)
