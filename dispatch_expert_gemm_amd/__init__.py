@@ -1056,6 +1056,9 @@ def _on_16_bytes(t):
     return t.clone() if isinstance(t, torch.Tensor) and t.data_ptr() % 16 and t.is_contiguous() else t
 
 
+KEEP_Y = 2  # _MoELayerFn's keep8: also y's rows, which the routing weights' gradient reads
+
+
 class _MoELayerFn(torch.autograd.Function):
     """Forward: dispatch -> grouped SwiGLU FFN -> combine; backward: the reverse chain.
     In bf16 the dispatch permute is folded into the two GEMMs that read the
@@ -1075,8 +1078,8 @@ class _MoELayerFn(torch.autograd.Function):
 
     keep8 (bf16 path): [G | U] leave the gate/up GEMM in 8 bits (saved in the places of
     gate_up_save and h: their codes and scales), the down data gradient reads them so and
-    writes h again, and the combine keeps y's rows in 8 bits for the routing weights'
-    gradient."""
+    writes h again, and with KEEP_Y the combine keeps y's rows in 8 bits for the routing
+    weights' gradient."""
 
     @staticmethod
     def forward(ctx, x, topk_weights, w_gate, w_up, w_down, shared_expert_x, shared_w_gate,
@@ -1186,7 +1189,7 @@ class _MoELayerFn(torch.autograd.Function):
         y_scales = None
         if keep8:
             h = y = None
-            if ctx.needs_input_grad[1]:
+            if keep8 == KEEP_Y:
                 y, y_scales = checkpoint_buffers(cap, H, dev)
                 moe_combine_checkpoint(*combined, y, y_scales)
         if y_scales is None:
@@ -1946,7 +1949,11 @@ def moe_layer(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, x_active_mask=
     if checkpoint_8bit and torch.is_grad_enabled():
         _nodes().refuse_foreign_leaves([x, topk_weights, w_gate, w_up, w_down, shared_expert_x, shared_w_gate,
                                         shared_w_up, shared_w_down])
+    # (needs_input_grad inside the function is a leaf's own, also where nothing is recorded)
+    keep8 = bool(checkpoint_8bit)
+    if keep8 and torch.is_grad_enabled() and topk_weights.requires_grad:
+        keep8 = KEEP_Y
     return _MoELayerFn.apply(x, topk_weights, w_gate, w_up, w_down, shared_expert_x, shared_w_gate,
                              shared_w_up, shared_w_down, topk_idx, x_active_mask, const_alpha_1,
                              const_alpha_2, const_v, zero_expert_num, copy_expert_num,
-                             const_expert_num, fp8, comm_quant_mode, fp8_wgrad, mx, checkpoint_8bit)
+                             const_expert_num, fp8, comm_quant_mode, fp8_wgrad, mx, keep8)

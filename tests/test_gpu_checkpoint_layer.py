@@ -318,3 +318,25 @@ def test_tensors_off_a_16_byte_boundary(special, F, k):
 
     for a, b in zip(step(lambda t: t.detach().clone()), step(lambda t: _offset(t, k))):
         same(a, b)
+
+
+def test_rows_are_kept_only_for_a_backward(monkeypatch):
+    """y's codes are written where the routing weights' gradient will read them, so neither without gradients nor for
+    weights that need none."""
+    d = _layer(90, 128, 64, 8, 2, 7)
+    kept_calls = []
+    keep = dm.moe_combine_checkpoint
+    monkeypatch.setattr(dm, "moe_combine_checkpoint", lambda *a, **k: kept_calls.append(1) or keep(*a, **k))
+
+    def call(weights):
+        w = d["w"].detach().requires_grad_(weights)
+        x = d["x"].detach().requires_grad_()
+        return dm.moe_layer(x, d["idx"], w, d["wg"], d["wu"], d["wd"], checkpoint_8bit=True)
+
+    out = call(True)
+    assert len(kept_calls) == 1 and out.requires_grad
+    assert call(False).requires_grad and len(kept_calls) == 1
+    with torch.no_grad():
+        bare = call(True)
+    assert len(kept_calls) == 1 and not bare.requires_grad
+    same(bare, out.detach())
