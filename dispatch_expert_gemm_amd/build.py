@@ -3,11 +3,13 @@
     python -m dispatch_expert_gemm_amd.build
 
 compiles every csrc/*.hip with hipcc into lib/libmoe.so, and csrc/torch_nodes.cpp
-(autograd nodes that call it) into lib/moe_torch.so.  It always recompiles.
+(autograd nodes that call it; this part needs g++, torch's and Python's headers) into
+lib/moe_torch.so.  It always recompiles.
 """
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -38,6 +40,16 @@ def hipcc() -> str:
     return "hipcc"
 
 
+def rocm_include() -> str:
+    """The headers beside the chosen hipcc."""
+    found = shutil.which(hipcc())
+    for path in (found, os.path.realpath(found)) if found else (hipcc(),):
+        include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(path))), "include")
+        if os.path.exists(os.path.join(include, "hip", "hip_runtime.h")):
+            return include
+    return "/opt/rocm/include"
+
+
 def sources():
     return sorted(f for f in os.listdir(CSRC) if f.endswith(".hip"))
 
@@ -54,23 +66,32 @@ def _run(cmd):
 def nodes_command():
     """The compiler call of the autograd nodes' object file (host code only)."""
     from torch.utils import cpp_extension
-    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], "/opt/rocm/include"]
+    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], rocm_include()]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
             "-DTORCH_API_INCLUDE_EXTENSION_H", "-DTORCH_EXTENSION_NAME=moe_torch", "-I", INCLUDE,
             *[a for i in includes for a in ("-isystem", i)],
             "-c", os.path.join(CSRC, "torch_nodes.cpp"), "-o", os.path.join(LIBDIR, "obj", "torch_nodes.o")]
 
 
+def _must(what, cmd, verbose=False):
+    rc, out = _run(cmd)
+    if verbose and out.strip():
+        print(out)
+    if rc != 0:
+        raise RuntimeError(f"{what}:\n{' '.join(cmd)}\n{out}")
+
+
+def compile_nodes(verbose=False):
+    _must("the compiler failed on torch_nodes.cpp", nodes_command(), verbose)
+
+
 def link_nodes():
     from torch.utils import cpp_extension
     libs = cpp_extension.library_paths()
     tmp = TORCH_NODES + ".tmp"
-    cmd = ["g++", "-shared", os.path.join(LIBDIR, "obj", "torch_nodes.o"), "-L" + LIBDIR, "-l:libmoe.so",
-           "-Wl,-rpath,$ORIGIN", *["-L" + p for p in libs], "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch",
-           "-ltorch_python", "-o", tmp]
-    rc, out = _run(cmd)
-    if rc != 0:
-        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{out}")
+    _must("link failed", ["g++", "-shared", os.path.join(LIBDIR, "obj", "torch_nodes.o"), "-L" + LIBDIR, "-l:libmoe.so",
+                          "-Wl,-rpath,$ORIGIN", *["-L" + p for p in libs], "-lc10", "-lc10_hip", "-ltorch_cpu",
+                          "-ltorch", "-ltorch_python", "-o", tmp])
     os.replace(tmp, TORCH_NODES)
 
 
@@ -82,22 +103,22 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(LIBDIR, "obj", src.replace(".hip", ".o"))
         cmd = [cc, *COMMON, *EXTRA.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
         jobs.append((src, obj, cmd))
-    kernels = list(jobs)
-    jobs.append(("torch_nodes.cpp", None, nodes_command()))
-    with ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
-        results = list(ex.map(lambda j: (j, _run(j[2])), jobs))
-    for (src, _, cmd), (rc, out) in results:
-        if verbose and out.strip():
-            print(out)
-        if rc != 0:
-            raise RuntimeError(f"the compiler failed on {src}:\n{' '.join(cmd)}\n{out}")
-    tmp = LIB + ".tmp"
-    cmd = [cc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *[o for _, o, _ in kernels], "-o", tmp]
-    rc, out = _run(cmd)
-    if rc != 0:
-        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{out}")
-    os.replace(tmp, LIB)
-    link_nodes()
+    with ThreadPoolExecutor(max_workers=min(8, len(jobs) + 1)) as ex:
+        kernels = [ex.submit(_must, f"hipcc failed on {src}", cmd, verbose) for src, _, cmd in jobs]
+        nodes = ex.submit(compile_nodes, verbose)
+        for k in kernels:
+            k.result()
+        # libmoe.so needs nothing of the nodes: linked before their failure is raised
+        tmp = LIB + ".tmp"
+        _must("link failed", [cc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *[o for _, o, _ in jobs], "-o", tmp])
+        os.replace(tmp, LIB)
+    try:
+        nodes.result()
+        link_nodes()
+    except Exception:
+        if os.path.exists(TORCH_NODES):
+            os.remove(TORCH_NODES)  # (an older one may not go with this libmoe.so)
+        raise
     return LIB
 
 
