@@ -862,6 +862,13 @@ def moe_router_bwd(logits, K, renorm, topk_idx, topk_weights, grad_topk_weights,
                                 _ptr(grad_logits, F32, "grad_logits"), _stream(stream)))
 
 
+def _check_captured_backward():
+    """Refuses a captured backward that would reach what an eager forward left on the default stream: the engine would
+    make that stream wait inside the capture, which ends the process."""
+    if torch.cuda.is_current_stream_capturing():
+        _nodes().refuse_default_stream_ahead()
+
+
 class _RouterFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, K, renorm):
@@ -877,6 +884,7 @@ class _RouterFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, g_idx, g_w):
+        _check_captured_backward()
         logits, idx, w = ctx.saved_tensors
         gl = torch.empty_like(logits)
         if g_w is None:
@@ -1207,6 +1215,7 @@ class _MoELayerFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_out):
+        _check_captured_backward()
         saved = ctx.saved_tensors
         (x, topk_weights, w_gate, w_up, w_down, topk_idx, mask, a1, a2, cv, expand_x, assist,
          recv, gus, h, y, y_scales) = saved[:17]

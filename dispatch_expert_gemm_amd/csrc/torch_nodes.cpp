@@ -10,9 +10,13 @@
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/graph_task.h>
 #include <torch/csrc/autograd/variable.h>
 #include <torch/extension.h>
+
+#include <unordered_set>
 
 #include "moe.h"
 
@@ -90,6 +94,36 @@ void refuse_foreign_leaves(const std::vector<std::optional<Tensor>>& tensors) {
     if (t && t->is_cuda()) refuse_foreign_leaf(*t, "an input");
 }
 
+// In a captured backward: a node that it will still come to and that an eager forward on the
+// default stream made (a leaf's accumulator that a living graph holds, or a part of that graph
+// itself).  The engine would make the default stream wait inside the capture, which ends the
+// process.  Only nodes that this backward executes count, and any other stream may take part.
+void refuse_default_stream_ahead() {
+  if (!capturing()) return;
+  const auto here = torch::autograd::get_current_node();
+  if (!here) return;
+  const auto* executed = torch::autograd::get_current_graph_task_exec_info();
+  std::unordered_set<torch::autograd::Node*> seen;
+  std::vector<torch::autograd::Node*> open{here.get()};
+  while (!open.empty()) {
+    const auto* node = open.back();
+    open.pop_back();
+    for (const auto& edge : node->next_edges()) {
+      auto* next = edge.function.get();
+      if (!next || !seen.insert(next).second) continue;
+      if (executed && !executed->empty()) {
+        const auto it = executed->find(next);
+        if (it == executed->end() || !it->second.should_execute()) continue;
+      }
+      const auto home = next->stream();
+      if (home && home->id() == c10::hip::getDefaultHIPStream(home->device_index()).id())
+        refuse("a captured backward would reach ", next->name(), " of the default stream, of a graph that an eager "
+               "forward built and that still lives: free that graph, or capture with leaves of its own");
+      open.push_back(next);
+    }
+  }
+}
+
 // Gradients that cannot be differentiated again: a second derivative raises.
 variable_list once(variable_list grads) {
   if (!at::GradMode::is_enabled()) return grads;
@@ -137,6 +171,7 @@ struct BalanceNode : torch::autograd::Function<BalanceNode> {
 
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
     if (!grads[0].defined() && !grads[1].defined()) return {Tensor(), Tensor(), Tensor()};
+    refuse_default_stream_ahead();
     const auto saved = ctx->get_saved_variables();
     const Tensor &logits = saved[0], &mask = saved[1], &off = saved[2], &counts = saved[3], &tokens = saved[4];
     Tensor grad;
@@ -213,6 +248,7 @@ struct SwigluNode : torch::autograd::Function<SwigluNode> {
   }
 
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    refuse_default_stream_ahead();
     const auto saved = ctx->get_saved_variables();
     const Tensor &codes = saved[0], &scales = saved[1];
     Tensor grad;
@@ -327,4 +363,5 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
   m.def("combine_checkpoint", &combine_checkpoint);
   m.def("combine_bwd_weights_checkpoint", &combine_bwd_weights_checkpoint);
   m.def("refuse_foreign_leaves", &refuse_foreign_leaves);
+  m.def("refuse_default_stream_ahead", &refuse_default_stream_ahead);
 }

@@ -340,3 +340,51 @@ def test_rows_are_kept_only_for_a_backward(monkeypatch):
         bare = call(True)
     assert len(kept_calls) == 1 and not bare.requires_grad
     same(bare, out.detach())
+
+
+@pytest.mark.parametrize("op", ["balance", "swiglu", "router", "layer", "layer with checkpoints"])
+def test_a_captured_backward_refuses_what_an_eager_graph_left(op):
+    """A weight behind the operator's input whose eager graph still lives: the engine would end the process, so the
+    backward is refused before it gets there.  A forward alone, and a backward that stops before that weight, run."""
+    p = _train_inputs(64, 128, 64, 8, 2, [0, 64])
+    idx, w = dm.router(p["logits"], 2)
+    base = {"swiglu": torch.randn(8, 64, device=DEV).bfloat16(), "layer": p["x"], "layer with checkpoints": p["x"]}
+    base = base.get(op, p["logits"]).detach()
+    weight = torch.full((base.shape[1],), 0.5, dtype=base.dtype, device=DEV, requires_grad=True)
+    layer = lambda x, keep: dm.moe_layer(x, idx, w, p["wg"], p["wu"], p["wd"], checkpoint_8bit=keep)  # noqa: E731
+    call = {"balance": lambda x: dm.balance_loss(x, idx)[0], "swiglu": dm.swiglu_checkpoint,
+            "router": lambda x: dm.router(x, 2)[1], "layer": lambda x: layer(x, False),
+            "layer with checkpoints": lambda x: layer(x, True)}[op]
+
+    def step(wrt, at=base):
+        at = at * weight
+        out = call(at)
+        return out.detach(), *torch.autograd.grad(out, weight if wrt else at, torch.ones_like(out))
+
+    want = [t.clone() for t in step(False)]
+    alive = call(base * weight)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="leaves of its own"):
+            step(True)
+        forward = call(base * weight).detach()
+        part = step(False)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        same(forward, alive.detach())
+        for a, b in zip(want, part):
+            same(a, b)
+    del alive
+    # with that graph gone, or a leaf of its own, the whole backward is captured
+    whole = [t.clone() for t in step(True)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(True)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, whole):
+            same(a, b)
