@@ -421,8 +421,8 @@ moe_status check_swiglu(int64_t R, int64_t F) {
   return MOE_OK;
 }
 
-// HIP refuses a launch of 2^32 threads or more.
-constexpr int64_t kMaxThreads = 0xffffff00;
+// Threads of a launch: one of 2^32 or more runs only a part of them, without an error.
+constexpr int64_t kMaxThreads = 0xffffff00, kMaxWaves = kMaxThreads / kWave;
 
 template <int PASS>
 moe_status launch_swiglu(SwigluArgs a, void* stream) {
@@ -449,10 +449,12 @@ moe_status launch_swiglu(SwigluArgs a, void* stream) {
   return launch_status();
 }
 
-// Waves per token: one for each 64-vector column block, up to 16.
-inline int keep_split(int64_t Hv) {
-  const int64_t blocks = (Hv + kWave - 1) / kWave;
-  return (int)(blocks < 16 ? blocks : 16);
+// Waves per token: one for each 64-vector column block, up to 16 and what a launch holds.
+inline int keep_split(int64_t T, int64_t Hv) {
+  int64_t split = (Hv + kWave - 1) / kWave;
+  if (split > 16) split = 16;
+  if (split > kMaxWaves / T) split = kMaxWaves / T;
+  return (int)split;
 }
 
 }  // namespace
@@ -506,6 +508,7 @@ extern "C" moe_status moe_combine_checkpoint(const moe_shape* s, const void* y, 
   if (st != MOE_OK) return st;
   if (s->comm_quant_mode != 0) return MOE_ERR_UNSUPPORTED;
   if (s->T == 0) return MOE_OK;
+  if (s->T > kMaxWaves) return MOE_ERR_UNSUPPORTED;
   MOE_NEED(y, s->capacity * s->H);
   MOE_NEED(y_codes, s->capacity * s->H);
   MOE_NEED(y_scales, s->capacity * s->H);
@@ -531,7 +534,7 @@ extern "C" moe_status moe_combine_checkpoint(const moe_shape* s, const void* y, 
                       s->K,
                       s->H / 8,
                       0,
-                      keep_split(s->H / 8)};
+                      keep_split(s->T, s->H / 8)};
   const KeptArgs q{reinterpret_cast<uint2*>(y_codes), static_cast<uint16_t*>(y_scales), (s->H + kCols - 1) / kCols};
   const int64_t waves = s->T * a.split;
   launch_k(s->K, [&](auto km) {
@@ -554,6 +557,7 @@ extern "C" moe_status moe_combine_bwd_weights_checkpoint(
   if (st != MOE_OK) return st;
   if (s->comm_quant_mode != 0) return MOE_ERR_UNSUPPORTED;
   if (s->T == 0) return MOE_OK;
+  if (s->T > kMaxWaves) return MOE_ERR_UNSUPPORTED;
   MOE_NEED(y_codes, s->capacity * s->H);
   MOE_NEED(y_scales, s->capacity * s->H);
   if (!grad_out || !topk_idx || !topk_weights || !assist || !ep_send_counts || !grad_topk_weights)
@@ -588,7 +592,7 @@ extern "C" moe_status moe_combine_bwd_weights_checkpoint(
     };
     // four waves for a row of four 64-vector blocks or more: 4096 tokens of 7168
     // columns 69 us against 75 with two (and 92 with one)
-    if (a.Hv >= 256) {
+    if (a.Hv >= 256 && s->T <= kMaxWaves / 4) {
       if (special) go(k_combine_kept_bwd<KM, true, 4>, s->T);
       else go(k_combine_kept_bwd<KM, false, 4>, s->T);
     } else {

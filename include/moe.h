@@ -954,7 +954,8 @@ moe_status moe_ffn_down_bwd_data_checkpoint(const moe_shape* s, const void* grad
  * row of y in 8 bits on its way, so y need not outlive the call.
  *  out  y_codes (capacity, H) int8, y_scales (capacity, ceil(H / 32)) bf16: the rows
  *       that a slot refers to; others are not written
- *  other arguments as moe_combine.  comm_quant_mode must be 0 (MOE_ERR_UNSUPPORTED);
+ *  other arguments as moe_combine.  comm_quant_mode must be 0 and T below 2^26 - 4 (a
+ *  launch's threads), else MOE_ERR_UNSUPPORTED;
  *  bf16 matrices on 16-byte boundaries, codes on 8 (MOE_ERR_BAD_SHAPE). */
 moe_status moe_combine_checkpoint(const moe_shape* s, const void* y, const int32_t* topk_idx,
                                   const float* topk_weights, const int32_t* assist_info_for_combine,

@@ -153,3 +153,11 @@ def test_checkpoint_buffers():
     assert c.shape == (3, 100) and s.shape == (3, 4) and c.dtype == torch.int8 and s.dtype == torch.bfloat16
     c, s = dm.checkpoint_buffers(3, 33, "cpu", halves=2)
     assert c.shape == (3, 66) and s.shape == (3, 4)
+
+
+def test_combine_refuses_more_tokens_than_a_launch_has_waves(L):
+    """A wave for a token is 2^32 threads at 2^26 tokens."""
+    for T, expect in ((1 << 26, UNSUPPORTED), ((1 << 31) - 1, UNSUPPORTED)):
+        s = ctypes.byref(dm.make_shape(T, 8, 1, 1))
+        assert L.moe_combine_checkpoint(s, *[P()] * 5, *[N] * 6, *[P()] * 3, N) == expect
+        assert L.moe_combine_bwd_weights_checkpoint(s, *[P()] * 7, *[N] * 5, P(), N, N) == expect

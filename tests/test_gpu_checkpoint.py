@@ -530,3 +530,32 @@ def test_combine_past_32_bit_offsets():
     c = int(route.assist_info_for_combine[T * K - 1])
     p = kept(codes[c:c + 1].cpu(), scales[c:c + 1].cpu())[0] * out[T - 1].cpu().double()
     assert abs(float(gw[T - 1, K - 1]) - float(p.sum())) <= (H / 64 + 12) * 2.0 ** -23 * float(p.abs().sum())
+
+
+def test_combine_of_more_tokens_than_a_launch_has_waves_for():
+    """2^22 tokens of 16 column blocks and 2^24 of four are past the 2^32 threads of a launch at a wave for each block: fewer
+    waves a token.  Every slot is empty, so rows, codes and scales are not touched and out is 0."""
+    H, T, T2 = 8192, (1 << 22) + 5, (1 << 24) + 3
+    room = torch.empty(max(T * H, T2 * H // 4), dtype=torch.bfloat16, device=DEV).fill_(1)
+    some = torch.zeros(64, dtype=torch.int32, device=DEV)
+    P = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def inputs(t):
+        w = torch.full((t, 1), 2.0, device=DEV)
+        return some, w, torch.full((2 * t,), -1, dtype=torch.int32, device=DEV), some, None
+
+    args = inputs(T)
+    shape = dm.make_shape(T, H, 1, 1)
+    dm._check(dm.lib().moe_combine_checkpoint(dm.ctypes.byref(shape), P(some), *map(P, args), *[None] * 5, P(room), P(some),
+                                              P(some), stream))
+    out = room[:T * H].view(T, H)
+    for a in range(0, T, 1 << 20):
+        assert not out[a:a + (1 << 20)].any()
+    room.fill_(1)
+    args = inputs(T2)
+    grad = torch.full((T2, 1), 5.0, device=DEV)
+    shape = dm.make_shape(T2, H // 4, 1, 1)
+    dm._check(dm.lib().moe_combine_bwd_weights_checkpoint(dm.ctypes.byref(shape), P(room), P(some), P(some), *map(P, args),
+                                                          *[None] * 4, P(grad), None, stream))
+    assert not grad.any()
