@@ -421,8 +421,7 @@ moe_status check_swiglu(int64_t R, int64_t F) {
   return MOE_OK;
 }
 
-// Threads of a launch: one of 2^32 or more runs only a part of them, without an error.
-constexpr int64_t kMaxThreads = 0xffffff00, kMaxWaves = kMaxThreads / kWave;
+constexpr int64_t kMaxWaves = kMaxThreads / kWave;
 
 template <int PASS>
 moe_status launch_swiglu(SwigluArgs a, void* stream) {

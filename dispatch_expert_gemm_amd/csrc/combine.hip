@@ -287,6 +287,9 @@ inline int combine_split(int64_t Hv, int K) {
   return token_split(Hv, K);
 }
 
+// (waves: T times the waves of a token; fewer than 2^26 - 4 fit a launch)
+inline bool fits_waves(int64_t waves) { return fits_launch((waves + kWavesPerBlock - 1) / kWavesPerBlock, 256); }
+
 inline dim3 token_grid(int64_t T) {
   return dim3((unsigned)((T + kWavesPerBlock - 1) / kWavesPerBlock));
 }
@@ -320,6 +323,7 @@ extern "C" moe_status moe_combine(const moe_shape* s, const void* y, const int32
                 // the int8 payload needs every row's amax, which one wave per
                 // token computes once
                 s->comm_quant_mode == 2 ? 1 : combine_split(s->H / 8, s->K)};
+  if (!fits_waves(s->T * a.split)) return MOE_ERR_UNSUPPORTED;
   launch_k(s->K, [&](auto km) {
     constexpr int KM = decltype(km)::value;
     if (a.qpay && a.Hv <= (int64_t)kChunk<KM> * kWave)
@@ -372,6 +376,7 @@ moe_status combine_bwd_impl(const moe_shape* s, const void* grad_out, const void
                    grad_y_scales,
                    s->capacity,
                    row_weights};
+  if (!fits_waves(s->T)) return MOE_ERR_UNSUPPORTED;
   launch_k(s->K, [&](auto km) {
     constexpr int KM = decltype(km)::value;
     const bool one = a.qpay && a.Hv <= (int64_t)kChunk<KM> * kWave;
@@ -462,6 +467,7 @@ extern "C" moe_status moe_dispatch_bwd(const moe_shape* s, const void* grad_expa
                     s->K,
                     s->H / 8,
                     token_split(s->H / 8, s->K)};
+  if (!fits_waves(s->T * a.split)) return MOE_ERR_UNSUPPORTED;
   launch_k(s->K, [&](auto km) {
     hipLaunchKernelGGL(k_dispatch_bwd<decltype(km)::value>, token_grid(s->T * a.split), dim3(256), 0,
                        as_stream(stream), a);

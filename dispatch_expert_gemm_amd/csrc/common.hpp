@@ -222,6 +222,10 @@ inline int token_split(int64_t Hv, int K) {
   return Hv >= 512 ? 4 : (Hv >= 256 ? 2 : 1);
 }
 
+// Threads of a launch: HIP runs one of 2^32 or more in part only, without an error.
+constexpr int64_t kMaxThreads = 0xffffff00;
+inline bool fits_launch(int64_t blocks, int64_t threads) { return blocks <= kMaxThreads / threads; }
+
 inline moe_status launch_status() {
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

@@ -1694,6 +1694,7 @@ moe_status launch_cfg(GemmArgs g, const moe_shape* s, hipStream_t strm) {
   if (g.tiles == 0) return MOE_OK;
   const int64_t grid = (g.tiles + 7) / 8 * 8;  // weight gradients: already 8 * E * block
   if (grid > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
+  if (!fits_launch(grid, Cfg<MODE, BM, BN, FP8, BK, S, WM, WN>::kThreads)) return MOE_ERR_UNSUPPORTED;
   hipLaunchKernelGGL((k_gemm<MODE, BM, BN, FP8, BK, S, WM, WN, I8, MX, KEEP>), dim3((unsigned)grid),
                      dim3(Cfg<MODE, BM, BN, FP8, BK, S, WM, WN>::kThreads), 0, strm, g);
   return launch_status();

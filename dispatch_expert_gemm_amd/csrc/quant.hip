@@ -308,6 +308,7 @@ extern "C" moe_status moe_quant_rows_fp8(int64_t R, int64_t C, const void* src,
   if (!src || !codes || !scales) return MOE_ERR_NULL_ARG;
   const int64_t groups = (R + kRowsPerGroup - 1) / kRowsPerGroup * (C / 128);  // 16 lanes each
   const int64_t blocks = (groups * 16 + 255) / 256;
+  if (!fits_launch(blocks, 256)) return MOE_ERR_UNSUPPORTED;
   hipLaunchKernelGGL(k_quant_rows_fp8, dim3((unsigned)blocks), dim3(256), 0, as_stream(stream),
                      static_cast<const uint4*>(src), R, C, nrows, reinterpret_cast<uint2*>(codes),
                      scales);
@@ -324,6 +325,7 @@ extern "C" moe_status moe_quant_cols_fp8(int64_t capacity, int64_t D, int32_t nu
   if (!ep_recv_counts) return MOE_ERR_NULL_ARG;
   if (capacity == 0) return MOE_OK;
   if (!src || !codes_t || !scales) return MOE_ERR_NULL_ARG;
+  if (!fits_launch(blocks, 256)) return MOE_ERR_UNSUPPORTED;
   hipLaunchKernelGGL(k_quant_cols_fp8, dim3((unsigned)blocks), dim3(256), 0, as_stream(stream),
                      static_cast<const uint4*>(src), D, (int)num_experts, ep_recv_counts, slots * 128,
                      codes_t, scales);
@@ -338,6 +340,7 @@ extern "C" moe_status moe_quantize_weights_fp8(int64_t E, int64_t N, int64_t Kdi
   if (!w || !codes || !scales) return MOE_ERR_NULL_ARG;
   const int64_t blocks = E * (N / 128) * (Kdim / 128);
   if (blocks > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
+  if (!fits_launch(blocks, 256)) return MOE_ERR_UNSUPPORTED;
   hipLaunchKernelGGL(k_quant_weights_fp8, dim3((unsigned)blocks), dim3(256), 0, as_stream(stream),
                      static_cast<const uint4*>(w), N, Kdim, codes, codes_t, scales);
   return launch_status();
@@ -350,6 +353,7 @@ extern "C" moe_status moe_quant_rows_int8(int64_t R, int64_t C, const void* src,
   if (!src || !codes || !scales) return MOE_ERR_NULL_ARG;
   const int64_t blocks = (R + 3) / 4;
   if (blocks > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
+  if (!fits_launch(blocks, 256)) return MOE_ERR_UNSUPPORTED;
   hipLaunchKernelGGL(k_quant_rows_int8, dim3((unsigned)blocks), dim3(256), 0, as_stream(stream),
                      static_cast<const uint4*>(src), R, C, nrows, reinterpret_cast<uint2*>(codes), scales);
   return launch_status();
@@ -362,6 +366,7 @@ extern "C" moe_status moe_quant_rows_mx(int64_t R, int64_t C, const void* src, c
   if (!src || !codes || !scales) return MOE_ERR_NULL_ARG;
   const int64_t blocks = (R * (C / 8) + 255) / 256;
   if (blocks > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
+  if (!fits_launch(blocks, 256)) return MOE_ERR_UNSUPPORTED;
   hipLaunchKernelGGL(k_quant_rows_mx, dim3((unsigned)blocks), dim3(256), 0, as_stream(stream),
                      static_cast<const uint4*>(src), R, C, nrows, reinterpret_cast<uint2*>(codes), scales);
   return launch_status();
@@ -378,6 +383,7 @@ extern "C" moe_status moe_quantize_weights_mx(int64_t E, int64_t N, int64_t K, c
   if (st != MOE_OK || !codes_t) return st;
   const int64_t blocks = E * (N / 32) * (K / 128);
   if (blocks > 0x7fffffff) return MOE_ERR_BAD_SHAPE;
+  if (!fits_launch(blocks, 256)) return MOE_ERR_UNSUPPORTED;
   hipLaunchKernelGGL(k_quant_weights_mx_t, dim3((unsigned)blocks), dim3(256), 0, as_stream(stream),
                      static_cast<const uint4*>(w), E, N, K, codes_t, scales_t);
   return launch_status();

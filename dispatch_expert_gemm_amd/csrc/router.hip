@@ -181,6 +181,7 @@ moe_status check_router(int64_t T, int64_t n, int32_t K, int32_t renorm) {
   if (renorm != 0 && renorm != 1) return MOE_ERR_BAD_RANGE;
   if (T * n > ((int64_t)1 << 40) || (T + kWavesPerBlock - 1) / kWavesPerBlock > 0x7fffffff)
     return MOE_ERR_BAD_SHAPE;
+  if (!fits_launch((T + kWavesPerBlock - 1) / kWavesPerBlock, 64 * kWavesPerBlock)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 }  // namespace

@@ -49,7 +49,8 @@ typedef int32_t moe_status;
 #define MOE_ERR_BAD_SHAPE (-2)   /* a size is out of range or misaligned */
 #define MOE_ERR_BAD_RANGE (-3)   /* an enum-like field has an unknown value */
 #define MOE_ERR_CAPACITY (-4)    /* capacity < T * min(E, K) */
-#define MOE_ERR_UNSUPPORTED (-5) /* valid but not implemented combination */
+#define MOE_ERR_UNSUPPORTED (-5) /* valid but not implemented combination; sizes whose launch
+                                    would hold 2^32 threads (2^26 tokens at a wave each) */
 #define MOE_ERR_WORKSPACE (-6)   /* workspace missing or too small */
 #define MOE_ERR_HIP (-7)         /* a HIP launch failed */
 
