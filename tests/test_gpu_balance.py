@@ -449,3 +449,26 @@ def test_the_gradient_near_an_even_load(T, n, K):
     bound = (3 * (span + 16) + n / 2 + 4) * 2.0 ** -23 * share * p * (c.abs() + (p * c.abs()).sum(1, keepdim=True))
     err = (grad - want).abs()
     assert (err <= bound + 2.0 ** -126 * 4).all(), float((err / bound).max())
+
+
+@pytest.mark.parametrize("T,n,K,S", [(300, 64, 8, 0), (3000, 160, 8, 0), (3000, 160, 8, 11), (20000, 33, 3, 0), (513, 1001, 4, 40),
+                                     (4100, 1028, 8, 37), (2100, 4093, 3, 0), (0, 64, 4, 3), (0, 2000, 4, 0)])
+def test_whatever_the_workspace_holds(T, n, K, S):
+    """The same bits from workspaces of their exact size whose bytes are all 0, 0x7f or 0xff, and nothing written behind them."""
+    l, idx = _inputs(T, n, K, n)
+    off = _offsets(S, T, S, T // 50, T // 20) if S else None
+    size = dm.moe_balance_workspace_size(T, n, S)
+    got = []
+    for byte in (0, 0x7F, 0xFF):
+        room = torch.full((size + 4096,), byte, dtype=torch.uint8, device=DEV)
+        outs = [torch.full((k,), 7, dtype=t, device=DEV) for k, t in
+                ((1, torch.float32), (1, torch.float32), (max(S, 1) * n, torch.int32), (max(S, 1) + 1, torch.int32))]
+        dm.moe_balance_fwd(l, idx, None, off, *outs, room[:size])
+        assert (room[size:] == byte).all()
+        got.append(outs)
+    for outs in got[1:]:
+        for a, b in zip(got[0], outs):
+            assert torch.equal(a, b)
+    ref = reference(l, idx, None, off)
+    assert torch.equal(got[0][2].cpu().long().view(ref["counts"].shape), ref["counts"])
+    assert abs(float(got[0][0]) - ref["loss"]) <= ref["loss_bound"] and abs(float(got[0][1]) - ref["z"]) <= ref["z_bound"]

@@ -559,3 +559,55 @@ def test_combine_of_more_tokens_than_a_launch_has_waves_for():
     dm._check(dm.lib().moe_combine_bwd_weights_checkpoint(dm.ctypes.byref(shape), P(room), P(some), P(some), *map(P, args),
                                                           *[None] * 4, P(grad), None, stream))
     assert not grad.any()
+
+
+# 2^20 units of eight columns and more: two a thread, kThreads apart.  The second one's columns carry over (256 is no
+# multiple of a row's 60, 132, 1792 or 28 units), or stay (4 units of the narrow rows)
+@pytest.mark.parametrize("R,F", [(17500, 480), (17500, 479), (8000, 1050), (600, 14336), (600, 14329), (40000, 224),
+                                 (262200, 7), (262200, 31), (262144, 32)])
+def test_swiglu_two_units_a_thread(R, F):
+    assert R * (-(-F // 32) * 4) >= 1 << 20
+    check_swiglu(gate_up(R, F, R + F, 2.0), F)
+
+
+def test_swiglu_two_units_a_thread_rows_in_use():
+    """nrows that ends between a thread's two units' rows."""
+    R, F = 17500, 480
+    gu = gate_up(R, F, 1).to(DEV)
+    whole = [torch.empty(R, F, dtype=torch.bfloat16, device=DEV), *dm.checkpoint_buffers(R, F, DEV, halves=2)]
+    grad = torch.empty_like(gu)
+    dm.moe_swiglu_checkpoint_fwd(gu, *whole)
+    dm.moe_swiglu_checkpoint_bwd(whole[1], whole[2], whole[0], grad)
+    for n in (0, 1, 5, 8745, 17499):
+        nrows = torch.tensor([n], dtype=torch.int32, device=DEV)
+        part = [torch.full_like(t, 9) for t in whole]
+        g = torch.full_like(grad, 9)
+        dm.moe_swiglu_checkpoint_fwd(gu, *part, nrows=nrows)
+        dm.moe_swiglu_checkpoint_bwd(part[1], part[2], whole[0], g, nrows=nrows)
+        for a, b in zip([*whole, grad], [*part, g]):
+            same(a[:n], b[:n])
+            assert (b[n:] == 9).all()
+
+
+@pytest.mark.parametrize("F", [96, 480, 33])
+@pytest.mark.parametrize("R", [37, 17500])
+def test_misaligned_rows_by_element(R, F):
+    """Forward and backward from and to matrices that begin on 2 bytes (codes on 1), every element against the 64-bit form."""
+    gu = gate_up(R, F, 5, 2.0)
+
+    def odd(shape, dtype):
+        return torch.empty(shape[0] * shape[1] + 1, dtype=dtype, device=DEV)[1:].view(shape)
+
+    x = odd((R, 2 * F), torch.bfloat16).copy_(gu)
+    h = odd((R, F), torch.bfloat16)
+    codes, scales = (odd(t.shape, t.dtype) for t in dm.checkpoint_buffers(R, F, DEV, halves=2))
+    dm.moe_swiglu_checkpoint_fwd(x, h, codes, scales)
+    qc, qs = halves(gu)
+    same(codes, qc)
+    same(scales, qs)
+    near("h", h, *swiglu64(gu[:, :F].double(), gu[:, F:].double()))
+    d = gate_up(R, F, 6, 0.3)[:, :F]
+    grad = odd((R, 2 * F), torch.bfloat16)
+    dm.moe_swiglu_checkpoint_bwd(codes, scales, odd((R, F), torch.bfloat16).copy_(d), grad)
+    nb = qs.shape[1] // 2
+    near("grad", grad, *swiglu64(kept(qc[:, :F], qs[:, :nb]), kept(qc[:, F:], qs[:, nb:]), d.double()))
