@@ -68,7 +68,7 @@ def nodes_command():
     from torch.utils import cpp_extension
     includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], rocm_include()]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
-            "-DTORCH_API_INCLUDE_EXTENSION_H", "-DTORCH_EXTENSION_NAME=moe_torch", "-I", INCLUDE,
+            "-DTORCH_API_INCLUDE_EXTENSION_H", "-DTORCH_EXTENSION_NAME=moe_torch", "-I", INCLUDE, "-I", CSRC,
             *[a for i in includes for a in ("-isystem", i)],
             "-c", os.path.join(CSRC, "torch_nodes.cpp"), "-o", os.path.join(LIBDIR, "obj", "torch_nodes.o")]
 

@@ -17,6 +17,7 @@
 // Backward: a workgroup takes a run of tokens, recomputes the softmax from the
 // logits (read once) and writes each gradient once; the counts of a token's
 // sequence stay in registers while the sequence stays the same.
+#include "balance.hpp"
 #include "common.hpp"
 
 namespace moe {
@@ -74,6 +75,7 @@ struct BalanceArgs {
   float* loss;
   float* z_loss;
   int32_t* counts;      // S x n
+  int32_t* counts2;     // the same, or NULL
   int32_t* seq_tokens;  // S, then their sum
   // backward
   const float* g_loss;
@@ -360,6 +362,7 @@ __global__ __launch_bounds__(kWave * kItemWaves<ALONE>, ALONE ? 1 : 4) void k_ba
     for (int r = 1; r < RW; ++r) v += rows[r * a.n + c];
     if constexpr (ALONE) {
       a.counts[c] = hist[c];
+      if (a.counts2) a.counts2[c] = hist[c];
       dot += (double)v * hist[c];
     } else {
       a.psum[item * a.pitch + c] = v;
@@ -538,6 +541,7 @@ __global__ __launch_bounds__(kWave * kJoinWaves) void k_balance_join(BalanceArgs
         ks += csum[w][lane];
       }
       a.counts[(int64_t)s * a.n + c] = ks;
+      if (a.counts2) a.counts2[(int64_t)s * a.n + c] = ks;
       dot = ps * ks;
     }
 #pragma unroll
@@ -867,11 +871,11 @@ extern "C" moe_status moe_balance_workspace_size(int64_t T, int64_t n_ids, int64
   return MOE_OK;
 }
 
-extern "C" moe_status moe_balance_fwd(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs, int32_t mask_ndim,
-                                      int32_t dtype, const void* logits, const int32_t* topk_idx,
-                                      const uint8_t* x_active_mask, const int32_t* seq_offsets, float* loss,
-                                      float* z_loss, int32_t* counts, int32_t* seq_tokens, void* workspace,
-                                      size_t ws_bytes, void* stream) {
+moe_status moe::balance_forward(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs, int32_t mask_ndim, int32_t dtype,
+                                const void* logits, const int32_t* topk_idx, const uint8_t* x_active_mask,
+                                const int32_t* seq_offsets, float* loss, float* z_loss, int32_t* counts,
+                                int32_t* counts_again, int32_t* seq_tokens, void* workspace, size_t ws_bytes,
+                                void* stream) {
   const moe_status st = check_balance(T, n_ids, K, num_seqs, mask_ndim, dtype);
   if (st != MOE_OK) return st;
   MOE_NEED(logits, T);
@@ -909,12 +913,22 @@ extern "C" moe_status moe_balance_fwd(int64_t T, int64_t n_ids, int32_t K, int64
   a.loss = loss;
   a.z_loss = z_loss;
   a.counts = counts;
+  a.counts2 = counts_again;
   a.seq_tokens = seq_tokens;
   launch_any(a, dtype, rows_aligned(logits, n_ids, dtype), LaunchItems{a, as_stream(stream), one});
   const moe_status first = launch_status();
   if (first != MOE_OK || one) return first;
   hipLaunchKernelGGL(k_balance_join, dim3((unsigned)blocks), dim3(kWave * kJoinWaves), 0, as_stream(stream), a);
   return launch_status();
+}
+
+extern "C" moe_status moe_balance_fwd(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs, int32_t mask_ndim,
+                                      int32_t dtype, const void* logits, const int32_t* topk_idx,
+                                      const uint8_t* x_active_mask, const int32_t* seq_offsets, float* loss,
+                                      float* z_loss, int32_t* counts, int32_t* seq_tokens, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+  return balance_forward(T, n_ids, K, num_seqs, mask_ndim, dtype, logits, topk_idx, x_active_mask, seq_offsets, loss,
+                         z_loss, counts, nullptr, seq_tokens, workspace, ws_bytes, stream);
 }
 
 extern "C" moe_status moe_balance_bwd(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs, int32_t mask_ndim,

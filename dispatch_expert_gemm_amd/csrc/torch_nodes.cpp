@@ -18,6 +18,7 @@
 
 #include <unordered_set>
 
+#include "balance.hpp"
 #include "moe.h"
 
 namespace py = pybind11;
@@ -146,7 +147,14 @@ struct Choices {
 struct BalanceSizes {
   int64_t T, n, S;
   int32_t K, mask_ndim, dtype;
+  bool keep;  // a backward may come
 };
+
+// The node's own integers: the tokens of each sequence and their sum, then on a 16-byte
+// boundary the counts.  (The counts that it returns are the caller's, who may change them
+// before the backward: a sum over ranks in place is not seen by autograd.)
+int64_t counts_at(int64_t rows) { return (rows + 4) / 4 * 4; }
+int32_t* kept_counts(const Tensor& tokens, int64_t rows) { return tokens.data_ptr<int32_t>() + counts_at(rows); }
 
 struct BalanceNode : torch::autograd::Function<BalanceNode> {
   static variable_list forward(AutogradContext* ctx, const Tensor& given, const Choices& c, const BalanceSizes& z) {
@@ -157,12 +165,14 @@ struct BalanceNode : torch::autograd::Function<BalanceNode> {
     check(moe_balance_workspace_size(z.T, z.n, z.S, &bytes));
     Tensor loss = at::empty({}, f32), z_loss = at::empty({}, f32);
     Tensor counts = z.S ? at::empty({z.S, z.n}, i32) : at::empty({z.n}, i32);
-    Tensor tokens = at::empty({rows + 1}, i32), workspace = at::empty({(int64_t)bytes}, i32.dtype(at::kByte));
-    check(moe_balance_fwd(z.T, z.n, z.K, z.S, z.mask_ndim, z.dtype, logits.data_ptr(), c.idx.data_ptr<int32_t>(),
-                          at_or_null<const uint8_t>(c.mask), at_or_null<const int32_t>(c.off), loss.data_ptr<float>(),
-                          z_loss.data_ptr<float>(), counts.data_ptr<int32_t>(), tokens.data_ptr<int32_t>(),
-                          workspace.data_ptr(), bytes, stream_of(logits)));
-    ctx->save_for_backward({logits, c.mask, c.off, counts, tokens});
+    Tensor tokens = at::empty({z.keep ? counts_at(rows) + rows * z.n : rows + 1}, i32);
+    Tensor workspace = at::empty({(int64_t)bytes}, i32.dtype(at::kByte));
+    check(moe::balance_forward(z.T, z.n, z.K, z.S, z.mask_ndim, z.dtype, logits.data_ptr(), c.idx.data_ptr<int32_t>(),
+                               at_or_null<const uint8_t>(c.mask), at_or_null<const int32_t>(c.off),
+                               loss.data_ptr<float>(), z_loss.data_ptr<float>(), counts.data_ptr<int32_t>(),
+                               z.keep ? kept_counts(tokens, rows) : nullptr, tokens.data_ptr<int32_t>(),
+                               workspace.data_ptr(), bytes, stream_of(logits)));
+    ctx->save_for_backward({logits, c.mask, c.off, tokens});
     ctx->saved_data["K"] = (int64_t)z.K;
     ctx->mark_non_differentiable({counts});
     ctx->set_materialize_grads(false);
@@ -173,17 +183,18 @@ struct BalanceNode : torch::autograd::Function<BalanceNode> {
     if (!grads[0].defined() && !grads[1].defined()) return {Tensor(), Tensor(), Tensor()};
     refuse_default_stream_ahead();
     const auto saved = ctx->get_saved_variables();
-    const Tensor &logits = saved[0], &mask = saved[1], &off = saved[2], &counts = saved[3], &tokens = saved[4];
+    const Tensor &logits = saved[0], &mask = saved[1], &off = saved[2], &tokens = saved[3];
+    const int64_t seqs = off.defined() ? off.numel() - 1 : 0;
     Tensor grad;
     {
       at::NoGradGuard no_grad;
       const c10::DeviceGuard guard(logits.device());
       grad = at::empty_like(logits);
       check(moe_balance_bwd(logits.size(0), logits.size(1), (int32_t)ctx->saved_data["K"].toInt(),
-                            off.defined() ? off.numel() - 1 : 0, mask.defined() ? (int32_t)mask.dim() : 0,
+                            seqs, mask.defined() ? (int32_t)mask.dim() : 0,
                             logits.scalar_type() == at::kFloat ? MOE_DTYPE_FP32 : MOE_DTYPE_BF16, logits.data_ptr(),
                             at_or_null<const uint8_t>(mask), at_or_null<const int32_t>(off),
-                            counts.data_ptr<int32_t>(), tokens.data_ptr<int32_t>(),
+                            kept_counts(tokens, seqs ? seqs : 1), tokens.data_ptr<int32_t>(),
                             at_or_null<const float>(grads[0]), at_or_null<const float>(grads[1]), grad.data_ptr(),
                             stream_of(logits)));
     }
@@ -202,7 +213,8 @@ std::tuple<Tensor, Tensor, Tensor> balance_loss(const Tensor& logits, const Tens
   goes_with(idx, logits.device(), "topk_idx");
   typed(idx, at::kInt, "topk_idx");
   BalanceSizes z{logits.size(0), logits.size(1), 0, (int32_t)std::min<int64_t>(idx.size(1), 1 << 20), 0,
-                 logits.scalar_type() == at::kFloat ? MOE_DTYPE_FP32 : MOE_DTYPE_BF16};
+                 logits.scalar_type() == at::kFloat ? MOE_DTYPE_FP32 : MOE_DTYPE_BF16,
+                 at::GradMode::is_enabled() && logits.requires_grad()};
   Choices c{idx, {}, {}};
   if (mask) {
     const Tensor& m = *mask;

@@ -472,3 +472,19 @@ def test_whatever_the_workspace_holds(T, n, K, S):
     ref = reference(l, idx, None, off)
     assert torch.equal(got[0][2].cpu().long().view(ref["counts"].shape), ref["counts"])
     assert abs(float(got[0][0]) - ref["loss"]) <= ref["loss_bound"] and abs(float(got[0][1]) - ref["z"]) <= ref["z_bound"]
+
+
+@pytest.mark.parametrize("T,n,S", [(100, 64, 0), (5000, 64, 0), (5000, 260, 7), (3000, 1500, 0)])
+def test_the_counts_are_the_callers(T, n, S):
+    """What a step does to the counts before its backward (a sum over ranks in place, which leaves no trace on the tensor,
+    or a bias update) does not reach the gradient."""
+    l, idx = _inputs(T, n, 4, n)
+    off = _offsets(S, T, S) if S else None
+    want = _run(l, idx, None, off, 1.0, 1.0)
+    for change in (lambda c: c.data.mul_(8), lambda c: c.mul_(8), lambda c: c.zero_()):
+        x = l.clone().requires_grad_()
+        loss, z, counts = dm.balance_loss(x, idx, seq_offsets=off)
+        assert torch.equal(counts, want[2])
+        change(counts)
+        grad, = torch.autograd.grad(loss + z, x)
+        assert torch.equal(grad, want[3])
