@@ -1759,23 +1759,28 @@ def moe_balance_workspace_size(T: int, n_ids: int, num_seqs: int = 0) -> int:
     return n.value
 
 
+def _dims(t):
+    """The number of dimensions of a tensor argument, -1 for anything else."""
+    return t.dim() if isinstance(t, torch.Tensor) else -1
+
+
 def _balance_sizes(logits, K, x_active_mask, seq_offsets):
     """(T, n, K, num_seqs, mask_ndim, dtype) of a balance call, its tensors' shapes checked."""
-    if getattr(logits, "dim", lambda: 0)() != 2:
+    if _dims(logits) != 2:
         raise MoeError(f"logits must be a tensor of shape (T, n_ids), got {getattr(logits, 'shape', logits)}")
     T, n = logits.shape
     if logits.dtype not in DTYPE_CODE:
         raise MoeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     ndim = 0
     if x_active_mask is not None:
-        ndim = x_active_mask.dim()
+        ndim = 2 if _dims(x_active_mask) == 2 else 1
         _shaped(x_active_mask, (T, K) if ndim == 2 else (T,), "x_active_mask")
     S = 0
     if seq_offsets is not None:
-        S = seq_offsets.numel() - 1
-        if seq_offsets.dim() != 1 or S < 1:
+        if _dims(seq_offsets) != 1 or seq_offsets.numel() < 2:
             raise MoeError(f"seq_offsets must hold the num_seqs + 1 ends of at least one sequence, got "
-                           f"{tuple(seq_offsets.shape)}")
+                           f"{getattr(seq_offsets, 'shape', seq_offsets)}")
+        S = seq_offsets.numel() - 1
     return T, n, K, S, ndim, DTYPE_CODE[logits.dtype]
 
 
@@ -1788,7 +1793,9 @@ def moe_balance_fwd(logits, topk_idx, x_active_mask, seq_offsets, loss, z_loss, 
     """logits (T, n) fp32 or bf16, topk_idx (T, K) int32, x_active_mask (T,) or (T, K) or None, seq_offsets
     (S + 1) int32 or None -> loss, z_loss (fp32, one element), counts (S or 1, n), seq_tokens (S or 1, + 1) int32."""
     dev = _device_of(logits, "logits")
-    sizes = T, n, K, S, ndim, _ = _balance_sizes(logits, topk_idx.shape[-1], x_active_mask, seq_offsets)
+    if _dims(topk_idx) != 2:
+        raise MoeError(f"topk_idx must be a tensor of shape (T, K), got {getattr(topk_idx, 'shape', topk_idx)}")
+    sizes = T, n, K, S, ndim, _ = _balance_sizes(logits, topk_idx.shape[1], x_active_mask, seq_offsets)
     _shaped(topk_idx, (T, K), "topk_idx")
     rows = max(S, 1)
     _launch(lib().moe_balance_fwd, dev, stream, *sizes, _at(logits, logits.dtype, T * n, "logits", dev),

@@ -488,3 +488,22 @@ def test_the_counts_are_the_callers(T, n, S):
         change(counts)
         grad, = torch.autograd.grad(loss + z, x)
         assert torch.equal(grad, want[3])
+
+
+def test_entries_refuse_what_is_no_tensor():
+    l, idx = _inputs(20, 16, 2, 1)
+    f = torch.empty(1, device=DEV)
+    i = torch.empty(64, dtype=torch.int32, device=DEV)
+    ws = torch.empty(dm.moe_balance_workspace_size(20, 16), dtype=torch.uint8, device=DEV)
+    for bad in (None, 3, [1], torch.tensor(2, dtype=torch.int32, device=DEV)):
+        with pytest.raises(dm.MoeError, match="topk_idx"):
+            dm.moe_balance_fwd(l, bad, None, None, f, f, i, i, ws)
+        if bad is not None:
+            with pytest.raises(dm.MoeError, match="x_active_mask"):
+                dm.moe_balance_fwd(l, idx, bad, None, f, f, i, i, ws)
+            with pytest.raises(dm.MoeError, match="seq_offsets"):
+                dm.moe_balance_fwd(l, idx, None, bad, f, f, i, i, ws)
+            with pytest.raises(dm.MoeError, match="x_active_mask"):
+                dm.moe_balance_bwd(l, 2, bad, None, i, i, f, f, l)
+        with pytest.raises(dm.MoeError):
+            dm.balance_loss(l, bad)
