@@ -198,7 +198,10 @@ def _nodes():
 def _node(name, *args):
     try:
         return getattr(_nodes(), name)(*args)
-    except TypeError as e:  # not a tensor
+    except TypeError as e:
+        if "incompatible function arguments" not in str(e):
+            raise
+        # not a tensor
         raise MoeError(f"{name} takes GPU tensors") from e
 
 

@@ -611,3 +611,13 @@ def test_misaligned_rows_by_element(R, F):
     dm.moe_swiglu_checkpoint_bwd(codes, scales, odd((R, F), torch.bfloat16).copy_(d), grad)
     nb = qs.shape[1] // 2
     near("grad", grad, *swiglu64(kept(qc[:, :F], qs[:, :nb]), kept(qc[:, F:], qs[:, nb:]), d.double()))
+
+
+def test_an_error_of_a_callers_hook_is_its_own():
+    def pack(t):
+        raise TypeError("of the hook")
+
+    x = gate_up(6, 32, 1).to(DEV).requires_grad_()
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+        with pytest.raises(TypeError, match="of the hook"):
+            dm.swiglu_checkpoint(x)
