@@ -1828,9 +1828,12 @@ def balance_loss(logits, topk_idx, *, x_active_mask=None, seq_offsets=None):
     in the logits (once), the counts int32 (n_ids,).
 
     Over the active tokens (x_active_mask as moe_layer's, (T,) or (T, K)): loss = n_ids * sum_e f_e P_e with f_e the
-    share of the choices that go to e and P_e the mean of softmax(logits)_e, 1 for an even load; z_loss = mean of
-    logsumexp(logits)^2.  seq_offsets (num_seqs + 1) int32, ascending: the loss of each packed sequence by
-    itself, averaged over tokens, and counts (num_seqs, n_ids); tokens outside the sequences take no part."""
+    active choices that go to e over K times the active tokens, and P_e the mean of softmax(logits)_e, so 1 for an
+    even load of all their slots (masked slots of active tokens lower it); z_loss = mean of logsumexp(logits)^2.
+    seq_offsets (num_seqs + 1) int32, ascending: the loss of each packed sequence by itself, averaged over tokens, and
+    counts (num_seqs, n_ids); tokens outside the sequences take no part.
+
+    The counts are held fixed in the gradient and are the caller's: changing them before the backward does not reach it."""
     return _node("balance_loss", logits, topk_idx, x_active_mask, seq_offsets)
 
 
@@ -1962,7 +1965,7 @@ def moe_layer(x, topk_idx, topk_weights, w_gate, w_up, w_down, *, x_active_mask=
     checkpoint_8bit=True (bf16 only) keeps what the backward needs of every routed
     row in 8 bits, 2.125 F + 1.0625 H bytes in place of 6 F + 2 H (2.125 F where
     topk_weights need no gradient): the forward's results are the same bits, the
-    gradients those of the kept G, U and y."""
+    gradients those of the kept y and of the kept G and U rounded to bf16."""
     if checkpoint_8bit and (fp8 or comm_quant_mode):
         raise MoeError("checkpoint_8bit keeps the bf16 path's activations (not with fp8 or comm_quant_mode)")
     if checkpoint_8bit and torch.is_grad_enabled():

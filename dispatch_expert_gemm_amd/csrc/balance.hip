@@ -671,7 +671,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_bwd(BalanceArgs a) {
     float bits = __int_as_float(part);
     if constexpr (kWide) bits = meet.all(bits, add_bits);
     else bits = group_all<GW>(bits, add_bits);
-    const int mean = (int)rintf((float)__float_as_int(bits) / (float)a.n);
+    const int mean = __float_as_int(bits) / a.n;  // (exact for equal counts of any size)
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll

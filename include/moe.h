@@ -865,8 +865,10 @@ moe_status moe_linear_int8_dynamic(int64_t M, int64_t N, int64_t K, const void* 
  *   n_s     = the active tokens of s, N = their sum over s
  *   loss    = n_ids / (K N) * sum_s (1 / n_s) sum_e c[s, e] sum_{t active in s} p[t, e]
  *   z_loss  = (1 / N) sum_{t active} logsumexp(logits[t, :])^2
- * so loss is the mean over tokens of their sequence's n_ids sum_e f_e P_e, 1 for an
- * even load.  A slot is active when its mask (T, K) is set, or its token's (T,); a
+ * so loss is the mean over tokens of their sequence's n_ids sum_e f_e P_e with f_e = c[s, e] /
+ * (K n_s): 1 for an even load of every slot of the active tokens.  (Slots that a (T, K) mask takes out
+ * of an active token are not in c, but K n_s holds them: a tenth of them masked, and an even load is 0.9.)
+ * A slot is active when its mask (T, K) is set, or its token's (T,); a
  * token is when any of its slots is.  Ids outside [0, n_ids) are not counted.
  * Without an active token both losses are 0.  A NaN logit counts as -inf, as in the router; a row
  * that holds nothing above -inf adds nothing to either sum and has gradient 0; a
@@ -896,6 +898,7 @@ moe_status moe_balance_fwd(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs
  * logits (the counts are held fixed):
  *   g[t, e] = grad_loss n_ids / (K N n_s) p[t, e] (c[s, e] - sum_j p[t, j] c[s, j])
  *             + grad_z_loss (2 / N) logsumexp(logits[t, :]) p[t, e]
+ * its first line from the counts less their mean, so equal counts give 0 there.
  *  in   logits, x_active_mask, seq_offsets, counts, seq_tokens as in the forward;
  *       grad_loss, grad_z_loss: one fp32 each on the device, or NULL (0)
  *  out  grad_logits (T, n_ids) in the logits' type, every element written (0 for
@@ -914,7 +917,7 @@ moe_status moe_balance_bwd(int64_t T, int64_t n_ids, int32_t K, int64_t num_seqs
  * keeps NaN.  Rows of width W: codes (rows, W) int8, scales (rows, ceil(W / 32))
  * bf16; rows [G | U] of width 2F are cut into blocks as two rows of width F: scales
  * (rows, 2, ceil(F / 32)).  R >= 0 rows, 1 <= F <= 2^20 (else MOE_ERR_BAD_SHAPE), up to
- * 2^31 blocks of G (else MOE_ERR_UNSUPPORTED); any alignment (fastest with F a multiple of 32
+ * 2^31 - 128 blocks of G (else MOE_ERR_UNSUPPORTED); any alignment (fastest with F a multiple of 32
  * and matrices on 16-byte boundaries).  nrows: the rows in use,
  * one int32 on the device (e.g. the last of ep_recv_counts), or NULL: all R; rows past
  * them are neither read nor written.  One launch each.

@@ -507,3 +507,25 @@ def test_entries_refuse_what_is_no_tensor():
                 dm.moe_balance_bwd(l, 2, bad, None, i, i, f, f, l)
         with pytest.raises(dm.MoeError):
             dm.balance_loss(l, bad)
+
+
+def test_an_even_load_of_masked_slots():
+    """K n_s holds the masked slots of active tokens: a quarter of them masked, and an even load is 0.75."""
+    l = torch.zeros(64, 32, device=DEV)
+    idx = ((torch.arange(64)[:, None] * 3 + torch.arange(4)) % 32).to(torch.int32).to(DEV)
+    mask = torch.ones(64, 4, dtype=torch.bool, device=DEV)
+    mask[:, 3] = False
+    loss, _, counts, _ = _run(l, idx, mask)
+    assert (counts == 6).all() and float(loss) == 0.75
+
+
+def test_large_even_counts_have_no_gradient():
+    """Counts past 2^24 and their sum near 2^31, given to the backward."""
+    n, T, c = 127, 8, 16909319
+    l, _ = _inputs(T, n, 4, 1)
+    counts = torch.full((n,), c, dtype=torch.int32, device=DEV)
+    tokens = torch.full((2,), T, dtype=torch.int32, device=DEV)
+    one = torch.ones(1, device=DEV)
+    grad = torch.full_like(l, 7)
+    dm.moe_balance_bwd(l, 4, None, None, counts, tokens, one, None, grad)
+    assert not grad.any()
